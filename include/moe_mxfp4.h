@@ -380,6 +380,153 @@ int moe_forward_static_scratch(const moe_layer* L, const void* x_dev, int T, voi
                                float* logits_out, int32_t* idx_out, float* w_out,
                                int* dev_status, moe_stream_t stream);
 
+/* ---- attention beside the layer ----------------------------------------------
+ *
+ * The attention half of a decoder block that this layer is the other half of:
+ * attention over a prompt, a paged key/value cache held in 8 bits, attention
+ * of new tokens over that cache, and eviction from it. Source: none of the
+ * pages defines an attention operator or a cache format; the formulas are
+ * softmax(scale Q K^T) V and the formats OCP MX v1.0's E4M3 and E8M0.
+ *
+ * n_heads query heads share n_kv_heads key/value heads, query head i reading
+ * key/value head i / (n_heads / n_kv_heads). head_dim is 64 or 128.
+ *
+ * Masked places do not count, whatever they hold: a key or value that a query
+ * does not see does not change its result, not even if it is inf or NaN. A
+ * query that sees nothing gets a zero output and a log-sum-exp of -inf. */
+
+/* Rows of bf16 heads: element (token t, head h, channel c) is
+ * data[t * token_stride + h * head_stride + c] (strides in elements, multiples
+ * of 8; data 16-B aligned), so slices of a fused projection need no copy. */
+typedef struct moe_rows {
+  const void* data;
+  int64_t token_stride, head_stride;
+} moe_rows;
+
+/* Attention of every prompt token over its sequence, on packed sequences.
+ *   q            [total_q][n_heads][head_dim]; k, v [total_k][n_kv_heads][head_dim]
+ *   cu_q_dev     int32 [n_seq + 1]: sequence b's queries are rows cu_q[b] ..
+ *                cu_q[b + 1] - 1; cu_k_dev the same for its keys (may be the
+ *                same array). Lengths of 0 are fine. cu[0] = 0, ascending.
+ *   causal       1: the sequences' ends are aligned, query r of a sequence
+ *                with nq queries and nk keys sees keys 0 .. r + nk - nq;
+ *                0: every query sees every key of its sequence
+ *   scale        factor of the scores, usually 1 / sqrt(head_dim); finite
+ *   out_dev      bf16 [total_q][n_heads][head_dim] (contiguous, 16-B aligned)
+ *   lse_dev      fp32 [total_q][n_heads]: natural log of the sum of
+ *                exp(scores) (NULL: not returned)
+ *   dev_status   device int (may be NULL): MOE_DEV_INDEX_OOB if an entry of
+ *                cu_q or cu_k leaves [0, total] or falls (such a sequence's
+ *                length is taken as what fits); MOE_DEV_TIMEOUT
+ * Rows of q outside every sequence are not written. Probabilities enter the
+ * second product as bf16; sums and outputs are held in fp32.
+ * Errors: MOE_ERR_INVALID_ARG (null pointer, negative size, stride or address
+ * not aligned, scale not finite), MOE_ERR_UNSUPPORTED_SHAPE (head_dim,
+ * n_heads % n_kv_heads, n_seq > 65536), MOE_ERR_NO_DEVICE, MOE_ERR_CUDA. */
+int moe_attn_prefill(const moe_rows* q, const moe_rows* k, const moe_rows* v, int n_heads, int n_kv_heads,
+                     int head_dim, const int32_t* cu_q_dev, const int32_t* cu_k_dev, int n_seq, int total_q,
+                     int total_k, int causal, float scale, void* out_dev, float* lse_dev, int* dev_status,
+                     moe_stream_t stream);
+
+/* A paged key/value cache in 8 bits (device buffers owned by the caller).
+ * Codes are E4M3 [n_pages][n_kv_heads][page_size][head_dim]; a page and
+ * key/value head have one scale byte s for their keys and one for their
+ * values, [n_pages][n_kv_heads], a code c being worth e4m3(c) * 2^(s - 127).
+ * Position p of a sequence is slot p % page_size of the page
+ * page_table[sequence][p / page_size]. A page that is written belongs to one
+ * sequence only. */
+typedef struct moe_kv_cache {
+  int32_t n_pages;
+  int32_t page_size;    /* 16, 32, 64 or 128 */
+  int32_t n_kv_heads;
+  int32_t head_dim;     /* 64 or 128 */
+  void* k_codes;        /* 16-B aligned */
+  void* v_codes;        /* 16-B aligned */
+  uint8_t* k_scales;
+  uint8_t* v_scales;
+} moe_kv_cache;
+
+/* Append keys and values to the cache.
+ *   k, v            [total][n_kv_heads][head_dim], sequence b's new tokens
+ *                   being rows cu[b] .. cu[b + 1] - 1 (cu_dev int32 [n_seq + 1])
+ *   start_dev       int32 [n_seq]: positions that sequence b holds already;
+ *                   its new tokens go to positions start[b], start[b] + 1, ...
+ *   page_table_dev  int32 [n_seq][table_width]
+ *   dev_status      device int (may be NULL): MOE_DEV_NONFINITE_INPUT (a value
+ *                   is inf or NaN: it is stored as NaN), MOE_DEV_INDEX_OOB (a
+ *                   position past the table or a page outside the cache: not
+ *                   written; cu out of order: as moe_attn_prefill)
+ * Scale of a page: the smallest power of two with every |finite new value| <=
+ * 448 times it (2^-127 at least, and for zeros), but not below the one that
+ * the page has if a part of it is filled already. Codes round to nearest even.
+ * Where the scale of a part-filled page grows, its older codes are rounded
+ * once more, which changes only those that become E4M3 subnormals. Whether a
+ * page is part-filled is known from start alone, so its bytes need no
+ * initialisation before its first slot is written.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED_SHAPE (the cache's sizes,
+ * n_seq > 65536), MOE_ERR_NO_DEVICE, MOE_ERR_CUDA. */
+int moe_kv_append_fp8(const moe_kv_cache* cache, const moe_rows* k, const moe_rows* v, const int32_t* cu_dev,
+                      const int32_t* start_dev, int n_seq, int total, const int32_t* page_table_dev,
+                      int table_width, int* dev_status, moe_stream_t stream);
+
+/* Attention of the last n_new tokens of each sequence over the cache, which
+ * holds those tokens' own keys and values already (moe_kv_append_fp8): n_new =
+ * 1 for plain decoding, up to 8 for the verification of drafted tokens.
+ *   q            [n_seq * n_new][n_heads][head_dim]: row b * n_new + t is token
+ *                t of sequence b; it sees positions 0 .. lengths[b] - n_new + t
+ *   lengths_dev  int32 [n_seq]: positions in the cache, the new ones included
+ *   out_dev      bf16 [n_seq * n_new][n_heads][head_dim] (contiguous, 16-B aligned)
+ *   lse_dev      fp32 [n_seq * n_new][n_heads] (NULL: not returned)
+ *   weights_dev  fp32, NULL for none: to entry (b * n_kv_heads + h) *
+ *                weights_stride + j the probabilities that the tokens and
+ *                query heads of (b, h) give to position j are added, for j <
+ *                lengths[b] (in a fixed order: equal inputs give equal bits)
+ *   workspace    >= moe_attn_decode_workspace_bytes(...) bytes (256-B aligned),
+ *                zero-filled before its first use: its first bytes hold
+ *                counters that every call leaves at zero
+ *   dev_status   device int (may be NULL): MOE_DEV_INDEX_OOB (a length outside
+ *                [0, table_width * page_size] or above weights_stride is cut
+ *                to it; a page outside the cache counts as masked)
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED_SHAPE (the cache's sizes,
+ * n_heads % n_kv_heads, n_new > 8, n_new * n_heads / n_kv_heads > 64, n_seq >
+ * 4096), MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_NO_DEVICE, MOE_ERR_CUDA. The
+ * workspace size is 0 for an unsupported shape or without an sm_103 device. */
+size_t moe_attn_decode_workspace_bytes(const moe_kv_cache* cache, int n_seq, int n_new, int n_heads,
+                                       int table_width, int with_weights);
+int moe_attn_decode_fp8(const moe_kv_cache* cache, const moe_rows* q, int n_heads, int n_seq, int n_new,
+                        const int32_t* lengths_dev, const int32_t* page_table_dev, int table_width, float scale,
+                        void* out_dev, float* lse_dev, float* weights_dev, int64_t weights_stride,
+                        void* workspace_dev, size_t workspace_bytes, int* dev_status, moe_stream_t stream);
+
+/* Keep the positions with the most accumulated attention weight. For each
+ * sequence b and key/value head h with length L = lengths[b]: everything if L
+ * <= keep; else the last `recent` positions and, of the others, the keep -
+ * recent with the largest weight (equal weights: the lower position; -0 ranks
+ * as +0, NaN as -inf). The kept positions, in ascending order, become
+ * positions 0, 1, ... of pages dst_table[b][...], requantised as
+ * moe_kv_append_fp8 does for a new page. Heads keep different positions but
+ * equally many, so the cache stays one table for all heads.
+ *   weights_dev       fp32 as moe_attn_decode_fp8 writes them
+ *   dst_table_dev     int32 [n_seq][dst_width]: pages that hold none of the
+ *                     positions of lengths_dev, for any sequence
+ *   kept_dev          int32 [n_seq][n_kv_heads][keep]: positions kept, -1 past
+ *                     the last
+ *   kept_weights_dev  fp32 [n_seq][n_kv_heads][keep]: their weights, 0 past the
+ *                     last (NULL: not returned)
+ *   new_lengths_dev   int32 [n_seq]: min(L, keep)
+ *   dev_status        device int (may be NULL): MOE_DEV_INDEX_OOB as in
+ *                     moe_attn_decode_fp8; a position whose page is outside
+ *                     the cache is kept as zeros, a destination page outside
+ *                     it is not written
+ * Errors: MOE_ERR_INVALID_ARG (also recent outside [0, keep], keep < 1),
+ * MOE_ERR_UNSUPPORTED_SHAPE (the cache's sizes, n_seq > 65535),
+ * MOE_ERR_BUFFER_TOO_SMALL (dst_width * page_size below min(keep, table_width
+ * * page_size)), MOE_ERR_NO_DEVICE, MOE_ERR_CUDA. */
+int moe_kv_evict_fp8(const moe_kv_cache* cache, const int32_t* page_table_dev, int table_width,
+                     const int32_t* lengths_dev, int n_seq, const float* weights_dev, int64_t weights_stride,
+                     int keep, int recent, const int32_t* dst_table_dev, int dst_width, int32_t* kept_dev,
+                     float* kept_weights_dev, int32_t* new_lengths_dev, int* dev_status, moe_stream_t stream);
+
 /* Comma-separated names of the stages of `path` in launch order (the
  * boundaries moe_forward's stage_events mark); NULL for an unknown path. */
 const char* moe_stage_names(int path);

@@ -19,7 +19,9 @@ __all__ = [
     "moe_packed_desc", "moe_shape", "moe_layer", "Layer",
     "moe_packed_bytes", "moe_describe_packed", "moe_pack_mxfp4", "moe_unpack_mxfp4",
     "moe_route_topk", "moe_sort_workspace_bytes", "moe_sort_by_expert",
-    "moe_workspace_bytes", "moe_query_path", "moe_stage_names", "moe_forward", "moe_forward_profiled", "moe_forward_w4a8", "moe_quant_mxfp8", "moe_lmhead_pack_fp8", "moe_lmhead_fp8", "moe_forward_static_scratch", "STATIC_SCRATCH_BYTES", "moe_selftest_bounded_wait", "moe_status_string", "moe_version",
+    "moe_workspace_bytes", "moe_query_path", "moe_stage_names", "moe_forward", "moe_forward_profiled", "moe_forward_w4a8", "moe_quant_mxfp8", "moe_lmhead_pack_fp8", "moe_lmhead_fp8", "moe_forward_static_scratch", "STATIC_SCRATCH_BYTES",
+    "moe_rows", "moe_kv_cache", "KVCache", "moe_attn_prefill", "moe_kv_append_fp8", "moe_attn_decode_workspace_bytes",
+    "moe_attn_decode_fp8", "moe_kv_evict_fp8", "moe_selftest_bounded_wait", "moe_status_string", "moe_version",
 ]
 
 # The in-tree build, and only it: there is no way to point the binding at
@@ -62,13 +64,24 @@ class moe_layer(ctypes.Structure):
                 ("shared_down", ctypes.c_void_p)]
 
 
+class moe_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class moe_kv_cache(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
             f"{LIB_PATH} is missing. Build it with `python -c \"import __graft_entry__ as g; g.build()\"` "
             "(nvcc, sm_103a). This package has no CPU or PyTorch fallback.")
     L = ctypes.CDLL(LIB_PATH)
-    vp, i32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    vp, i32, i64, sz, f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+    rows, cache = ctypes.POINTER(moe_rows), ctypes.POINTER(moe_kv_cache)
     sig = {
         "moe_packed_bytes": (sz, [i32, i32, i32, i32]),
         "moe_describe_packed": (i32, [i32, i32, i32, i32, ctypes.POINTER(moe_packed_desc)]),
@@ -87,6 +100,11 @@ def _load():
         "moe_forward_profiled": (i32, [ctypes.POINTER(moe_layer), vp, i32, vp, vp, i32, vp, vp, vp, vp, sz, vp,
                                          ctypes.POINTER(ctypes.c_void_p), i32, vp]),
         "moe_forward_static_scratch": (i32, [ctypes.POINTER(moe_layer), vp, i32, vp, vp, i32, vp, vp, vp, vp, vp]),
+        "moe_attn_prefill": (i32, [rows, rows, rows, i32, i32, i32, vp, vp, i32, i32, i32, i32, f32, vp, vp, vp, vp]),
+        "moe_kv_append_fp8": (i32, [cache, rows, rows, vp, vp, i32, i32, vp, i32, vp, vp]),
+        "moe_attn_decode_workspace_bytes": (sz, [cache, i32, i32, i32, i32, i32]),
+        "moe_attn_decode_fp8": (i32, [cache, rows, i32, i32, i32, vp, vp, i32, f32, vp, vp, vp, i64, vp, sz, vp, vp]),
+        "moe_kv_evict_fp8": (i32, [cache, vp, i32, vp, i32, vp, i64, i32, i32, vp, i32, vp, vp, vp, vp, vp]),
         "moe_stage_names": (ctypes.c_char_p, [i32]),
         "moe_selftest_bounded_wait": (i32, [vp, ctypes.c_uint32, ctypes.c_longlong, vp, vp]),
         "moe_status_string": (ctypes.c_char_p, [i32]),
@@ -425,3 +443,242 @@ def moe_forward_static_scratch(layer: Layer, x: torch.Tensor, y: torch.Tensor, b
                                           _p(logits_out), _p(idx_out), _p(w_out), _p(dev_status), _s(stream)),
            "moe_forward_static_scratch")
     return y
+
+
+# ---- attention beside the layer ---------------------------------------------------
+
+
+class KVCache:
+    """A paged key/value cache in 8 bits: the device tensors and the struct the C ABI takes.
+
+    k_codes, v_codes: uint8 [n_pages, n_kv_heads, page_size, head_dim], E4M3 codes;
+    k_scales, v_scales: uint8 [n_pages, n_kv_heads], a code c of that page and
+    head being worth e4m3(c) * 2**(scale - 127).
+    """
+
+    def __init__(self, k_codes, v_codes, k_scales, v_scales):
+        for name, t in (("k_codes", k_codes), ("v_codes", v_codes), ("k_scales", k_scales), ("v_scales", v_scales)):
+            _cuda(t, torch.uint8, name)
+        if k_codes.dim() != 4 or v_codes.shape != k_codes.shape:
+            raise ValueError("k_codes and v_codes must be [n_pages, n_kv_heads, page_size, head_dim], of one shape")
+        if k_scales.shape != k_codes.shape[:2] or v_scales.shape != k_codes.shape[:2]:
+            raise ValueError(f"k_scales and v_scales must be {tuple(k_codes.shape[:2])}")
+        n_pages, H, P, D = k_codes.shape
+        if P not in (16, 32, 64, 128) or D not in (64, 128):
+            raise ValueError("page_size must be 16, 32, 64 or 128 and head_dim 64 or 128")
+        self.device = k_codes.device
+        if any(t.device != self.device for t in (v_codes, k_scales, v_scales)):
+            raise ValueError("the cache's tensors must be on one device")
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = n_pages, H, P, D
+        self.struct = moe_kv_cache(n_pages, P, H, D, k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),
+                                   v_scales.data_ptr())
+
+    @classmethod
+    def alloc(cls, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, device="cuda"):
+        """An empty cache; its bytes need no initialisation."""
+        codes = [torch.empty((n_pages, n_kv_heads, page_size, head_dim), dtype=torch.uint8, device=device) for _ in "kv"]
+        scales = [torch.empty((n_pages, n_kv_heads), dtype=torch.uint8, device=device) for _ in "kv"]
+        return cls(*codes, *scales)
+
+
+def _rows(t, name, heads=None, d=None):
+    """moe_rows of a bf16 [tokens, heads, d] tensor whose innermost dimension is contiguous."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != 3 or (heads is not None and shape[1] != heads) or (d is not None and shape[2] != d):
+        raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, "
+                         f"{'head_dim' if d is None else d}], got {tuple(shape)}")
+    ts, hs, es = t.stride()
+    if es != 1 and shape[2] > 1:
+        raise ValueError(f"{name}'s innermost dimension must be contiguous")
+    # the stride of a dimension of size 1 is arbitrary
+    return moe_rows(t.data_ptr(), ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0)
+
+
+def _on(dev, **tensors):
+    """Every given tensor lives on the current device, which is `dev`."""
+    cur = torch.cuda.current_device()
+    if dev.index != cur:
+        raise ValueError(f"the inputs are on cuda:{dev.index}, the current device is cuda:{cur}")
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the other inputs are on {dev}")
+
+
+def _status_arg(dev_status):
+    if dev_status is not None:
+        _cuda(dev_status, torch.int32, "dev_status")
+        if dev_status.numel() < 1:
+            raise ValueError("dev_status needs 1 element")
+    return dev_status
+
+
+def _ints(t, name, *shape):
+    """Contiguous int32 tensor of that shape."""
+    _cuda(t, torch.int32, name)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _table(t, name, n_seq):
+    _cuda(t, torch.int32, name)
+    if t.dim() != 2 or t.shape[0] != n_seq:
+        raise ValueError(f"{name} must be [{n_seq}, pages], got {tuple(t.shape)}")
+    return t
+
+
+def moe_attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
+                     cu_k: torch.Tensor | None = None, causal: bool = True, scale: float | None = None,
+                     out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                     dev_status: torch.Tensor | None = None, stream=None):
+    """Attention of packed prompts: bf16 q [total_q, n_heads, D], k and v [total_k, n_kv_heads, D] -> out like q.
+
+    cu_q, cu_k int32 [n_seq + 1]: first row of every sequence, and the total
+    (cu_k omitted: cu_q). causal aligns the sequences' ends. q, k and v may be
+    slices of one projection (strides that are multiples of 8 elements). scale
+    defaults to 1 / sqrt(D). lse fp32 [total_q, n_heads] is written if given.
+    """
+    qr = _rows(q, "q")
+    total_q, n_heads, d = q.shape
+    kr = _rows(k, "k", d=d)
+    total_k, n_kv = k.shape[0], k.shape[1]
+    vr = _rows(v, "v", heads=n_kv, d=d)
+    if v.shape[0] != total_k:
+        raise ValueError("k and v must have the same number of rows")
+    _cuda(cu_q, torch.int32, "cu_q")
+    if cu_q.dim() != 1 or cu_q.numel() < 1:
+        raise ValueError("cu_q must be [n_seq + 1]")
+    cu_k = cu_q if cu_k is None else _ints(cu_k, "cu_k", cu_q.numel())
+    if out is None:
+        out = torch.empty((total_q, n_heads, d), dtype=torch.bfloat16, device=q.device)
+    _cuda(out, torch.bfloat16, "out")
+    if out.shape != q.shape:
+        raise ValueError(f"out must have q's shape {tuple(q.shape)}, got {tuple(out.shape)}")
+    if lse is not None:
+        _cuda(lse, torch.float32, "lse")
+        if lse.shape != q.shape[:2]:
+            raise ValueError(f"lse must be {tuple(q.shape[:2])}, got {tuple(lse.shape)}")
+    _on(q.device, k=k, v=v, cu_q=cu_q, cu_k=cu_k, out=out, lse=lse, dev_status=_status_arg(dev_status))
+    _check(lib.moe_attn_prefill(ctypes.byref(qr), ctypes.byref(kr), ctypes.byref(vr), n_heads, n_kv, d, _p(cu_q),
+                                _p(cu_k), cu_q.numel() - 1, total_q, total_k, 1 if causal else 0,
+                                d ** -0.5 if scale is None else float(scale), _p(out), _p(lse), _p(dev_status),
+                                _s(stream)), "moe_attn_prefill")
+    return out
+
+
+def moe_kv_append_fp8(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                      start: torch.Tensor, page_table: torch.Tensor, dev_status: torch.Tensor | None = None,
+                      stream=None):
+    """Append bf16 k, v [total, n_kv_heads, D] to the cache: rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 go to
+    positions start[b], start[b] + 1, ... of sequence b, whose pages are page_table[b] (int32 [n_seq, width])."""
+    kr = _rows(k, "k", heads=cache.n_kv_heads, d=cache.head_dim)
+    vr = _rows(v, "v", heads=cache.n_kv_heads, d=cache.head_dim)
+    if v.shape[0] != k.shape[0]:
+        raise ValueError("k and v must have the same number of rows")
+    _cuda(start, torch.int32, "start")
+    n_seq = start.numel()
+    _ints(cu_seqlens, "cu_seqlens", n_seq + 1)
+    _table(page_table, "page_table", n_seq)
+    _on(cache.device, k=k, v=v, cu_seqlens=cu_seqlens, start=start, page_table=page_table,
+        dev_status=_status_arg(dev_status))
+    _check(lib.moe_kv_append_fp8(ctypes.byref(cache.struct), ctypes.byref(kr), ctypes.byref(vr), _p(cu_seqlens),
+                                 _p(start), n_seq, k.shape[0], _p(page_table), page_table.shape[1], _p(dev_status),
+                                 _s(stream)), "moe_kv_append_fp8")
+
+
+def moe_attn_decode_workspace_bytes(cache: KVCache, n_seq: int, n_new: int, n_heads: int, table_width: int,
+                                    with_weights: bool = False) -> int:
+    """Bytes of the workspace of moe_attn_decode_fp8; 0 for an unsupported shape."""
+    return int(lib.moe_attn_decode_workspace_bytes(ctypes.byref(cache.struct), n_seq, n_new, n_heads, table_width,
+                                                   1 if with_weights else 0))
+
+
+def moe_attn_decode_fp8(cache: KVCache, q: torch.Tensor, lengths: torch.Tensor, page_table: torch.Tensor,
+                        scale: float | None = None, out: torch.Tensor | None = None,
+                        lse: torch.Tensor | None = None, weights: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None, dev_status: torch.Tensor | None = None, stream=None):
+    """Attention of the last n_new tokens of every sequence over the cache: bf16 q [n_seq, n_new, n_heads, D] -> out
+    like q. lengths int32 [n_seq] counts the positions in the cache, the new tokens' own included.
+
+    weights fp32 [n_seq, n_kv_heads, positions]: the probabilities that every
+    position receives are added to it. lse fp32 [n_seq, n_new, n_heads] is
+    written if given. workspace: uint8 device tensor of
+    moe_attn_decode_workspace_bytes(...) bytes, zero-filled before its first
+    use (it carries counters between calls); allocated with zeros when omitted.
+    """
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be [n_seq, n_new, n_heads, head_dim]")
+    n_seq, n_new, n_heads, d = q.shape
+    if n_seq > 1 and n_new > 1 and q.stride(0) != n_new * q.stride(1):
+        raise ValueError("q's tokens must have one stride over all sequences")
+    rows = q[:, 0] if n_new == 1 else (q[0] if n_seq == 1 else q.flatten(0, 1))
+    qr = _rows(rows, "q", d=cache.head_dim)
+    _ints(lengths, "lengths", n_seq)
+    _table(page_table, "page_table", n_seq)
+    if out is None:
+        out = torch.empty((n_seq, n_new, n_heads, d), dtype=torch.bfloat16, device=q.device)
+    _cuda(out, torch.bfloat16, "out")
+    if out.shape != q.shape:
+        raise ValueError(f"out must have q's shape {tuple(q.shape)}, got {tuple(out.shape)}")
+    if lse is not None:
+        _cuda(lse, torch.float32, "lse")
+        if lse.shape != q.shape[:3]:
+            raise ValueError(f"lse must be {tuple(q.shape[:3])}, got {tuple(lse.shape)}")
+    if weights is not None:
+        _cuda(weights, torch.float32, "weights")
+        if weights.dim() != 3 or weights.shape[:2] != (n_seq, cache.n_kv_heads):
+            raise ValueError(f"weights must be [{n_seq}, {cache.n_kv_heads}, positions], got {tuple(weights.shape)}")
+    if workspace is None:
+        n = moe_attn_decode_workspace_bytes(cache, n_seq, n_new, n_heads, page_table.shape[1], weights is not None)
+        workspace = torch.zeros(max(n, 256), dtype=torch.uint8, device=q.device)
+    _cuda(workspace, torch.uint8, "workspace")
+    _on(cache.device, q=q, lengths=lengths, page_table=page_table, out=out, lse=lse, weights=weights,
+        workspace=workspace, dev_status=_status_arg(dev_status))
+    _check(lib.moe_attn_decode_fp8(ctypes.byref(cache.struct), ctypes.byref(qr), n_heads, n_seq, n_new, _p(lengths),
+                                   _p(page_table), page_table.shape[1], d ** -0.5 if scale is None else float(scale),
+                                   _p(out), _p(lse), _p(weights), weights.shape[2] if weights is not None else 0,
+                                   _p(workspace), workspace.numel(), _p(dev_status), _s(stream)),
+           "moe_attn_decode_fp8")
+    return out
+
+
+def moe_kv_evict_fp8(cache: KVCache, page_table: torch.Tensor, lengths: torch.Tensor, weights: torch.Tensor,
+                     keep: int, recent: int, dst_table: torch.Tensor, kept: torch.Tensor | None = None,
+                     kept_weights: torch.Tensor | None = None, new_lengths: torch.Tensor | None = None,
+                     dev_status: torch.Tensor | None = None, stream=None):
+    """Keep `keep` positions of every sequence and key/value head: the last `recent` and those of the others with the
+    most accumulated weight. They become positions 0, 1, ... of the pages dst_table (int32 [n_seq, width]), which
+    must hold none of the positions read. Returns (kept int32 [n_seq, n_kv_heads, keep], kept_weights fp32 like it,
+    new_lengths int32 [n_seq])."""
+    _cuda(lengths, torch.int32, "lengths")
+    n_seq, H = lengths.numel(), cache.n_kv_heads
+    _table(page_table, "page_table", n_seq)
+    _table(dst_table, "dst_table", n_seq)
+    _cuda(weights, torch.float32, "weights")
+    if weights.dim() != 3 or weights.shape[:2] != (n_seq, H):
+        raise ValueError(f"weights must be [{n_seq}, {H}, positions], got {tuple(weights.shape)}")
+    if keep < 1 or not 0 <= recent <= keep:
+        raise ValueError("keep must be at least 1 and recent in [0, keep]")
+    if kept is None:
+        kept = torch.empty((n_seq, H, keep), dtype=torch.int32, device=weights.device)
+    if kept_weights is None:
+        kept_weights = torch.empty((n_seq, H, keep), dtype=torch.float32, device=weights.device)
+    if new_lengths is None:
+        new_lengths = torch.empty(n_seq, dtype=torch.int32, device=weights.device)
+    _ints(kept, "kept", n_seq, H, keep)
+    _cuda(kept_weights, torch.float32, "kept_weights")
+    if kept_weights.shape != kept.shape:
+        raise ValueError(f"kept_weights must be {tuple(kept.shape)}, got {tuple(kept_weights.shape)}")
+    _ints(new_lengths, "new_lengths", n_seq)
+    _on(cache.device, page_table=page_table, lengths=lengths, weights=weights, dst_table=dst_table, kept=kept,
+        kept_weights=kept_weights, new_lengths=new_lengths, dev_status=_status_arg(dev_status))
+    _check(lib.moe_kv_evict_fp8(ctypes.byref(cache.struct), _p(page_table), page_table.shape[1], _p(lengths), n_seq,
+                                _p(weights), weights.shape[2], keep, recent, _p(dst_table), dst_table.shape[1],
+                                _p(kept), _p(kept_weights), _p(new_lengths), _p(dev_status), _s(stream)),
+           "moe_kv_evict_fp8")
+    return kept, kept_weights, new_lengths

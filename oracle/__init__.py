@@ -13,8 +13,9 @@ Contents
            shared expert, layer output, and the token->expert sort
   mxfp8  — E4M3 activation quantisation for the W4A8 mode
   lmhead — the FP8 (per-row scale) LM-head GEMV
+  attention — attention, the 8-bit key/value cache, eviction
 
 Pin status of every function is listed in the module docstrings; none is
 "parity unpinned".
 """
-from . import lmhead, mxfp4, moe, mxfp8  # noqa: F401
+from . import attention, lmhead, mxfp4, moe, mxfp8  # noqa: F401
