@@ -1,123 +1,800 @@
-// Attention over whole prompts (packed sequences, grouped heads).
+// Attention over whole prompts (packed sequences, grouped heads) on the
+// 5th-generation tensor cores.
 //
-// Simple form: four threads per query row, each holding a quarter of the
-// channels of q and of the output; 32 rows of one head per CTA, keys and
-// values in tiles of 32 through shared memory, softmax with a running maximum
-// and sum, everything in fp32. Keys that a row does not see are skipped.
+// out_i = sum_j softmax_j(scale q_i . k_j) v_j over the keys j that query i
+// sees. Work is 4 D flops per visible (query, key) pair and head; both
+// products run on tcgen05 (bf16 in, fp32 accumulators in tensor memory), the
+// exponentials between them on the special-function units.
+//
+// Work items. 128 consecutive queries of one head are a query tile. The tiles
+// of a sequence and key/value head, ordered by position and then by head of the
+// group, are taken two at a time: the pair shares every key and value tile that
+// is loaded, and (heads of one group) mostly the same causal range too. Items
+// differ in cost by their number of key tiles; a persistent CTA per SM takes
+// items c, 2N - 1 - c, 2N + c, ... of the list ordered by falling cost, which
+// is nowhere written down: a scheduler warp finds item r by bisection over the
+// cost (how many items cost at least x is a sum over sequences, in closed form).
+//
+// Tensor memory (512 columns): scores S0, S1 (128 fp32 columns each), outputs
+// O0, O1 (D each). Probabilities go back as bf16 over the scores they came
+// from, as the A operand of the second product.
+//
+// Warp roles, meeting only at mbarriers:
+//   producer (one thread)  Q tiles, then K0 V0 K1 V1 ... by TMA into a ring
+//   MMA (one thread)       S_t = Q_t K^T, then per key tile and query tile
+//                          O_t += P_t V and the next S_t: while the tensor
+//                          cores do one tile's pair of products, the other
+//                          tile's softmax runs
+//   scheduler (one warp)   the next item
+//   scan (one warp)        masked key tiles only, see below
+//   softmax 0, 1 (4 warps each, one thread per query): S to registers, maximum,
+//                          probabilities (fp32 sum, bf16 store), and at the end
+//                          O / sum. The reference maximum is raised only when
+//                          it is passed by 2^8 (bf16 has fp32's range, and the
+//                          sum is fp32), so O is rescaled rarely.
+//
+// Masked places must not count, whatever they hold, but 0 * inf is NaN in the
+// second product. For a tile that some query of the item does not see whole the
+// scan warp zeroes the value rows past the sequence's end and looks for
+// non-finite values in the others; only if it finds one (a broken model) the
+// softmax threads add that tile's visible products themselves.
+#include <cuda.h>
+
 #include "attn.h"
 #include "fp8kv.cuh"
+#include "tma.cuh"
+#include "umma.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kRowsPerCta = 32, kSplit = 4, kKeys = 32;
-constexpr int kThreads = kRowsPerCta * kSplit;
+constexpr int kQT = 128, kKT = 128;            // queries per tile, keys per tile
+constexpr int kWProd = 0, kWMma = 1, kWSched = 2, kWScan = 3, kWSoft = 4;
+constexpr int kPfWarps = 12;
+constexpr int kPfThreads = kPfWarps * 32;
+constexpr int kRegsCtl = 88, kRegsSoft = 208;  // registers after the split
+constexpr int kRegsLaunch = 168;
+static_assert(4 * kRegsCtl + 8 * kRegsSoft <= kPfWarps * kRegsLaunch, "register split exceeds the launch's total");
+constexpr float kPfRaise = 8.0f;
+constexpr uint32_t kBoxBytes = 128 * 128;      // 128 rows of 64 channels
+constexpr int kScanRing = 4;
+constexpr float kLn2f = 0.6931471805599453f, kLog2ef = 1.4426950408889634f;
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) prefill_simple_kernel(const PrefillArgs a) {
-  constexpr int DS = D / kSplit;
-  __shared__ __align__(16) __nv_bfloat16 ks[kKeys][D], vs[kKeys][D];
-  __shared__ int s_b, s_tile;
-  const int tid = threadIdx.x, lane = tid & 31;
-  if (tid < 32) {
-    bool bad = false;
-    int before = 0, fb = -1, ft = 0;
-    for (int b0 = 0; b0 < a.n_seq && fb < 0; b0 += 32) {
-      int c0 = 0, c1 = 0, k0, k1;
-      if (b0 + lane < a.n_seq) {
-        packed_range(a.cu_q, b0 + lane, a.total_q, &c0, &c1, &bad);
-        packed_range(a.cu_k, b0 + lane, a.total_k, &k0, &k1, &bad);
-      }
-      const int n = (c1 - c0 + kRowsPerCta - 1) / kRowsPerCta;
-      int incl = n;
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      const int lo = before + incl - n, x = blockIdx.x;
-      const unsigned hit = __ballot_sync(0xFFFFFFFFu, x >= lo && x < lo + n);
-      if (hit) {
-        fb = b0 + __ffs(hit) - 1;
-        ft = x - __shfl_sync(0xFFFFFFFFu, lo, __ffs(hit) - 1);
-      }
-      before += __shfl_sync(0xFFFFFFFFu, incl, 31);
-    }
-    bad = __any_sync(0xFFFFFFFFu, bad);
-    if (lane == 0) {
-      s_b = fb;
-      s_tile = ft;
-      if (bad && a.status) atomicOr(a.status, MOE_DEV_INDEX_OOB);
-    }
-  }
-  __syncthreads();
-  if (s_b < 0) return;
+struct PfPlan {
+  static constexpr int kBoxes = D / 64;
+  static constexpr uint32_t kTile = kBoxes * kBoxBytes;
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr uint32_t kQ = 0, kRing = 2 * kTile, kBars = kRing + kStages * kTile;
+  static constexpr int kNBars = 2 + 2 * kStages + 8 + 2 * kScanRing + 4;
+  static constexpr uint32_t kItems = kBars + kNBars * 8;
+  static constexpr uint32_t kTotal = kItems + 2 * 80 + kScanRing * 4 + 16 + 1024;   // + alignment slack
+};
+static_assert(PfPlan<128>::kTotal <= 232448 && PfPlan<64>::kTotal <= 232448, "shared memory");
+
+struct PfItem {
+  int n;               // key tiles, -1: no more items
+  int q0[2], head[2], rows[2], t0[2], nkt[2];   // per query tile: global row, head, rows (0: none), position, key tiles
+  int kv0, nk, off, vmin, hk;                   // keys: global row, count; nk - nq; fewest keys a query sees
+};
+static_assert(sizeof(PfItem) <= 80, "item");
+
+struct PfParams {
+  CUtensorMap map[3];    // q, k, v: 64-channel x 128-row boxes
+  int swapped[3];        // dimensions are (channel, token, head) instead of (channel, head, token)
+  int one_head[3];       // heads share their memory: head coordinate 0
+  PrefillArgs a;
+  float c;               // |scale| log2(e)
+  int negate;            // scale < 0
+};
+
+// ---- tensor-memory helpers -------------------------------------------------------
+__device__ __forceinline__ void umma_bf16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+                                             bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+// Descriptor of an operand whose rows (keys) are K and whose 64-channel boxes
+// are M or N ("MN-major"), 128-byte swizzle: lbo = bytes between boxes, 1024
+// bytes between groups of 8 keys.
+__device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t saddr, uint32_t lbo) {
+  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+#define MOE_R8(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), \
+                     "=r"(v[i + 6]), "=r"(v[i + 7])
+// 32 columns of the warp's lanes; no wait.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : MOE_R8(v, 0), MOE_R8(v, 8), MOE_R8(v, 16), MOE_R8(v, 24)
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+#define MOE_I8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), \
+                     "r"(v[i + 6]), "r"(v[i + 7])
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      MOE_I8(v, 0), MOE_I8(v, 8)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      MOE_I8(v, 0), MOE_I8(v, 8), MOE_I8(v, 16), MOE_I8(v, 24)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ float pf_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <int R>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+// ---- the list of items ---------------------------------------------------------------
+struct PfSeq {
+  int q0, nq, k0, nk, pairs;
+};
+__device__ __forceinline__ PfSeq pf_seq(const PrefillArgs& a, int G, int b, bool* bad) {
+  PfSeq s;
+  int q1, k1;
+  packed_range(a.cu_q, b, a.total_q, &s.q0, &q1, bad);
+  packed_range(a.cu_k, b, a.total_k, &s.k0, &k1, bad);
+  s.nq = q1 - s.q0;
+  s.nk = k1 - s.k0;
+  s.pairs = ((s.nq + kQT - 1) / kQT * G + 1) / 2;
+  return s;
+}
+// Keys that the tile which ends before query `end` sees.
+__device__ __forceinline__ int pf_kv_end(const PfSeq& s, int end, int causal) {
+  return causal ? min(max(end + s.nk - s.nq, 0), s.nk) : s.nk;
+}
+// Pairs with at least c key tiles (at least one counts as one): the last ones.
+__device__ __forceinline__ int pf_count_ge(const PfSeq& s, int G, int causal, int c) {
+  if (c <= 1) return s.pairs;
+  const int x = (c - 1) * kKT + 1;          // keys that such a pair sees at least
+  if (s.nk < x || s.pairs == 0) return 0;
+  if (!causal) return s.pairs;
+  const int y = x - (s.nk - s.nq);          // its last query's position + 1, at least
+  if (s.nq < y) return 0;
+  const int i0 = y <= 0 ? 0 : (y + kQT - 1) / kQT - 1;   // first tile position that reaches it
+  return s.pairs - int((int64_t)i0 * G / 2);
+}
+__device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xFFFFFFFFu, v); }
+
+// Whole warp: item number idx (< total), into *out by lane 0.
+__device__ void pf_find_item(const PfParams& P, int G, int idx, bool sorted, PfItem* out) {
+  const PrefillArgs& a = P.a;
+  const int lane = threadIdx.x & 31;
+  const int r = idx / a.n_kv, hk = idx % a.n_kv;
   bool ignore = false;
-  int q0, q1, k0, k1;
-  packed_range(a.cu_q, s_b, a.total_q, &q0, &q1, &ignore);
-  packed_range(a.cu_k, s_b, a.total_k, &k0, &k1, &ignore);
-  const int nq = q1 - q0, nk = k1 - k0;
-  const int r = s_tile * kRowsPerCta + tid / kSplit, part = tid % kSplit;
-  const int hq = blockIdx.y, hk = hq / (a.n_heads / a.n_kv);
-  const int vis = r < nq ? (a.causal ? min(max(r + nk - nq + 1, 0), nk) : nk) : 0;
-  const int last = min(s_tile * kRowsPerCta + kRowsPerCta, nq) - 1;   // last row of the tile
-  const int most = a.causal ? min(max(last + nk - nq + 1, 0), nk) : nk;
-  float q[DS], o[DS];
-#pragma unroll
-  for (int i = 0; i < DS; ++i) {
-    q[i] = r < nq ? __bfloat162float(a.q[(q0 + r) * a.q_ts + hq * a.q_hs + part * DS + i]) : 0.0f;
-    o[i] = 0.0f;
+  auto count = [&](int c) {
+    int n = 0;
+    for (int b = lane; b < a.n_seq; b += 32) n += pf_count_ge(pf_seq(a, G, b, &ignore), G, a.causal, c);
+    return warp_sum(n);
+  };
+  int c = 1, skip = 0;      // the item costs c; so many cost more
+  if (sorted) {
+    int lo = 1, hi = (a.total_k + kKT - 1) / kKT;
+    while (lo < hi) {       // largest c with count(c) > r
+      const int mid = (lo + hi + 1) >> 1;
+      if (count(mid) > r) lo = mid; else hi = mid - 1;
+    }
+    c = lo;
+    skip = count(c + 1);
   }
-  float m = -INFINITY, l = 0.0f;
-  for (int t0 = 0; t0 < most; t0 += kKeys) {
-    __syncthreads();
-    for (int v = tid; v < kKeys * D / 8; v += kThreads) {
-      const int row = v / (D / 8), ch = (v % (D / 8)) * 8;
-      if (t0 + row < nk) {
-        *reinterpret_cast<uint4*>(&ks[row][ch]) = *reinterpret_cast<const uint4*>(a.k + (k0 + t0 + row) * a.k_ts + hk * a.k_hs + ch);
-        *reinterpret_cast<uint4*>(&vs[row][ch]) = *reinterpret_cast<const uint4*>(a.v + (k0 + t0 + row) * a.v_ts + hk * a.v_hs + ch);
+  int before = skip;
+  for (int b0 = 0; b0 < a.n_seq; b0 += 32) {
+    const int b = b0 + lane;
+    PfSeq s{0, 0, 0, 0, 0};
+    int n = 0, first = 0;
+    if (b < a.n_seq) {
+      s = pf_seq(a, G, b, &ignore);
+      const int ge = pf_count_ge(s, G, a.causal, c);
+      n = sorted ? ge - pf_count_ge(s, G, a.causal, c + 1) : s.pairs;
+      first = s.pairs - ge;
+    }
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const int lo = before + incl - n;
+    const bool mine = r >= lo && r < lo + n;
+    if (mine) {
+      const int p = first + (r - lo);
+      const int tiles = (s.nq + kQT - 1) / kQT * G;
+      PfItem it;
+      it.kv0 = s.k0;
+      it.nk = s.nk;
+      it.off = s.nk - s.nq;
+      it.hk = hk;
+      it.vmin = s.nk;
+      it.n = 0;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int t = 2 * p + j, pos = t / G * kQT;
+        const bool have = t < tiles;
+        it.head[j] = hk * G + t % G;
+        it.t0[j] = pos;
+        it.q0[j] = s.q0 + pos;
+        it.rows[j] = have ? min(kQT, s.nq - pos) : 0;
+        const int end = have ? pf_kv_end(s, min(pos + kQT, s.nq), a.causal) : 0;
+        it.nkt[j] = (end + kKT - 1) / kKT;
+        it.n = max(it.n, it.nkt[j]);
+        if (have && a.causal) it.vmin = min(it.vmin, min(max(pos + 1 + it.off, 0), s.nk));
+      }
+      *out = it;
+    }
+    if (__any_sync(0xFFFFFFFFu, mine)) return;
+    before += __shfl_sync(0xFFFFFFFFu, incl, 31);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_constant__ PfParams P) {
+  using Plan = PfPlan<D>;
+  constexpr int NS = Plan::kStages;
+  constexpr int NB = Plan::kBoxes;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + Plan::kBars);
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* full = q_empty + 1;
+  uint64_t* empty = full + NS;
+  uint64_t* s_full = empty + NS;       // [2]
+  uint64_t* p_full = s_full + 2;       // [2]
+  uint64_t* o_full = p_full + 2;       // [2]
+  uint64_t* o_free = o_full + 2;       // [2]
+  uint64_t* scanned = o_free + 2;      // [kScanRing]
+  uint64_t* scan_go = scanned + kScanRing;   // [kScanRing]
+  uint64_t* it_full = scan_go + kScanRing;   // [2]
+  uint64_t* it_empty = it_full + 2;          // [2]
+  PfItem* items = reinterpret_cast<PfItem*>(smem + Plan::kItems);
+  volatile int* poison = reinterpret_cast<volatile int*>(smem + Plan::kItems + 2 * 80);   // [kScanRing]
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + Plan::kItems + 2 * 80 + kScanRing * 4);
+  volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
+
+  const PrefillArgs& a = P.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int G = a.n_heads / a.n_kv;
+  int* status = a.status;
+
+  if (tid == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&o_free[i], 4);
+      mbar_init(&it_full[i], 1);
+      mbar_init(&it_empty[i], 11);   // producer, MMA, scan, 8 softmax warps
+    }
+    for (int i = 0; i < kScanRing; ++i) {
+      mbar_init(&scanned[i], 1);
+      mbar_init(&scan_go[i], 1);
+    }
+    *abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == kWMma) tmem_alloc(tslot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  const uint32_t base = smem_addr(smem);
+  const uint32_t q_s = base + Plan::kQ, ring_s = base + Plan::kRing;
+
+  // The t-th item of this CTA, copied out of its slot (whole warp or one
+  // thread; one arrival per reader).
+  auto next_item = [&](int t, bool arrives, PfItem* it) {
+    if (!uwait(&it_full[t & 1], uint32_t(t >> 1) & 1u, abort, status)) return false;
+    *it = items[t & 1];
+    __syncwarp(__activemask());
+    if (arrives) mbar_arrive(&it_empty[t & 1]);
+    return it->n >= 0;
+  };
+
+  if (warp < kWSoft) {
+    regs_dec<kRegsCtl>();
+    if (warp == kWSched) {
+      // ---- scheduler --------------------------------------------------------------------
+      bool bad = false;
+      int total = 0;
+      for (int b = lane; b < a.n_seq; b += 32) total += pf_seq(a, G, b, &bad).pairs;
+      total = warp_sum(total) * a.n_kv;
+      bad = __any_sync(0xFFFFFFFFu, bad);
+      if (bad && blockIdx.x == 0 && lane == 0 && status) atomicOr(status, MOE_DEV_INDEX_OOB);
+      const int N = gridDim.x, c = blockIdx.x;
+      for (int t = 0;; ++t) {
+        if (t >= 2 && !uwait(&it_empty[t & 1], uint32_t((t >> 1) - 1) & 1u, abort, status)) break;
+        const int64_t idx = (int64_t)t * N + (t & 1 ? N - 1 - c : c);
+        const bool done = idx >= total;
+        if (done) {
+          if (lane == 0) items[t & 1].n = -1;
+        } else {
+          pf_find_item(P, G, int(idx), total > N, &items[t & 1]);
+        }
+        __threadfence_block();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&it_full[t & 1]);
+        if (done) break;   // this CTA's later indices are larger still
+      }
+    } else if (warp == kWProd) {
+      // ---- producer ---------------------------------------------------------------------
+      if (lane == 0) {
+        int p = 0, issued_q = 0;
+        bool ok = true;
+        PfItem it;
+        for (int t = 0; ok && next_item(t, true, &it); ++t) {
+          if (it.n == 0) continue;
+          // Q: after the last products with the previous item's
+          if (issued_q > 0 && !uwait(q_empty, uint32_t(issued_q - 1) & 1u, abort, status)) break;
+          const int have1 = it.rows[1] > 0;
+          mbar_arrive_expect_tx(q_full, (1 + have1) * Plan::kTile);
+          for (int j = 0; j <= have1; ++j)
+            for (int x = 0; x < NB; ++x) {
+              const int h = P.one_head[0] ? 0 : it.head[j], r = it.q0[j];
+              tma_load_3d(q_s + j * Plan::kTile + x * kBoxBytes, &P.map[0], x * 64, P.swapped[0] ? r : h,
+                          P.swapped[0] ? h : r, q_full);
+            }
+          ++issued_q;
+          for (int i = 0; i < 2 * it.n; ++i, ++p) {
+            const int s = p % NS, w = 1 + (i & 1);
+            if (p >= NS && !uwait(&empty[s], uint32_t(p / NS - 1) & 1u, abort, status)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&full[s], Plan::kTile);
+            const int h = P.one_head[w] ? 0 : it.hk, r = it.kv0 + (i >> 1) * kKT;
+            for (int x = 0; x < NB; ++x)
+              tma_load_3d(ring_s + s * Plan::kTile + x * kBoxBytes, &P.map[w], x * 64, P.swapped[w] ? r : h,
+                          P.swapped[w] ? h : r, &full[s]);
+          }
+        }
+        if (*abort) {   // copies in flight land before the CTA's shared memory goes away
+          for (int i = p > NS ? p - NS : 0; i < p; ++i) mbar_wait(&full[i % NS], uint32_t(i / NS) & 1u, status);
+          if (issued_q > 0) mbar_wait(q_full, uint32_t(issued_q - 1) & 1u, status);
+        }
+      }
+    } else if (warp == kWMma) {
+      // ---- MMA --------------------------------------------------------------------------
+      if (lane == 0) {
+        const uint32_t id_s = umma_idesc_bf16(kQT, kKT) | (P.negate ? 1u << 13 : 0u);   // bit 13: negate A
+        const uint32_t id_o = umma_idesc_bf16(kQT, D) | (1u << 16);                     // bit 16: B is MN-major
+        int p = 0, nq = 0, ns = 0;       // ring position; items with Q; masked tiles seen
+        int np[2] = {0, 0}, no[2] = {0, 0};   // probabilities awaited; items begun, per query tile
+        uint64_t* last = nullptr;
+        uint32_t last_par = 0;
+        bool ok = true;
+        PfItem it;
+        auto scores = [&](int j, int s) {
+          const uint32_t k0 = ring_s + s * Plan::kTile, q0 = q_s + j * Plan::kTile;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t o = (kk >> 2) * kBoxBytes + (kk & 3) * 32;
+            umma_bf16(tmem + j * kKT, umma_desc_sw128(q0 + o), umma_desc_sw128(k0 + o), id_s, kk > 0);
+          }
+          umma_commit(&s_full[j]);
+        };
+        for (int t = 0; ok && next_item(t, true, &it); ++t) {
+          if (it.n == 0) continue;
+          if (!uwait(q_full, uint32_t(nq++) & 1u, abort, status)) break;
+          const int s0 = p % NS;
+          if (!uwait(&full[s0], uint32_t(p / NS) & 1u, abort, status)) break;
+          tc_fence_after();
+          for (int j = 0; j < 2; ++j)
+            if (it.nkt[j] > 0) scores(j, s0);
+          umma_commit(&empty[s0]);
+          last = &empty[s0];
+          last_par = uint32_t(p / NS) & 1u;
+          if (it.n == 1) umma_commit(q_empty);
+          ++p;
+          for (int i = 0; i < it.n && ok; ++i) {
+            const int sv = p % NS, sk = (p + 1) % NS;
+            const bool more = i + 1 < it.n, masked = (i + 1) * kKT > it.vmin;
+            if (!uwait(&full[sv], uint32_t(p / NS) & 1u, abort, status)) {
+              ok = false;
+              break;
+            }
+            if (masked) mbar_arrive(&scan_go[ns & (kScanRing - 1)]);
+            bool have_k = false;
+            for (int j = 0; j < 2; ++j) {
+              if (i >= it.nkt[j]) continue;
+              if (i == 0 && no[j]++ > 0 && !uwait(&o_free[j], uint32_t(no[j] - 2) & 1u, abort, status)) {
+                ok = false;
+                break;
+              }
+              if (!uwait(&p_full[j], uint32_t(np[j]++) & 1u, abort, status)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              if (!(masked && poison[ns & (kScanRing - 1)])) {
+                const uint32_t v0 = ring_s + sv * Plan::kTile;
+#pragma unroll
+                for (int kk = 0; kk < kKT / 16; ++kk)
+                  umma_bf16_ts(tmem + 256 + j * D, tmem + j * kKT + kk * 8, umma_desc_mn_sw128(v0 + kk * 2048, kBoxBytes),
+                               id_o, i > 0 || kk > 0);
+              }
+              if (i + 1 < it.nkt[j]) {
+                if (!have_k) {
+                  if (!uwait(&full[sk], uint32_t((p + 1) / NS) & 1u, abort, status)) {
+                    ok = false;
+                    break;
+                  }
+                  tc_fence_after();
+                  have_k = true;
+                }
+                scores(j, sk);
+              } else {
+                umma_commit(&o_full[j]);
+              }
+            }
+            if (!ok) break;
+            umma_commit(&empty[sv]);
+            last = &empty[sv];
+            last_par = uint32_t(p / NS) & 1u;
+            ++p;
+            if (more) {
+              umma_commit(&empty[sk]);
+              last = &empty[sk];
+              last_par = uint32_t(p / NS) & 1u;
+              ++p;
+              if (i + 2 == it.n) umma_commit(q_empty);
+            }
+            if (masked) ++ns;
+          }
+        }
+        // every MMA has finished before tensor memory is freed
+        if (last) mbar_wait(last, last_par, status);
+      }
+    } else {
+      // ---- scan -------------------------------------------------------------------------
+      int p0 = 0, ns = 0;
+      PfItem it;
+      for (int t = 0; next_item(t, lane == 0, &it); ++t) {
+        bool ok = true;
+        for (int i = it.vmin / kKT; i < it.n && ok; ++i, ++ns) {
+          // the MMA thread says when the values are there: it alone has waited
+          // for every earlier phase of their stage
+          const int p = p0 + 2 * i + 1, s = p % NS;
+          if (!uwait(&scan_go[ns & (kScanRing - 1)], uint32_t(ns / kScanRing) & 1u, abort, status) ||
+              !uwait(&full[s], uint32_t(p / NS) & 1u, abort, status)) {
+            ok = false;
+            break;
+          }
+          uint8_t* v = smem + Plan::kRing + s * Plan::kTile;
+          const int rows = min(kKT, it.nk - i * kKT);
+          uint32_t found = 0;
+          for (int x = 0; x < NB; ++x) {
+            uint4* box = reinterpret_cast<uint4*>(v + x * kBoxBytes);
+            for (int e = lane; e < rows * 8; e += 32) {
+              const uint4 w = box[e];
+              // a half has exponent 255 iff adding one to its exponent field carries into its sign
+              found |= ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
+                       ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
+            }
+            for (int e = rows * 8 + lane; e < kKT * 8; e += 32) box[e] = make_uint4(0, 0, 0, 0);
+          }
+          const bool any = __any_sync(0xFFFFFFFFu, (found & 0x80008000u) != 0);
+          fence_async_smem();   // the zeros, before the tensor cores read them
+          __syncwarp();
+          if (lane == 0) {
+            poison[ns & (kScanRing - 1)] = any ? 1 : 0;
+            __threadfence_block();
+            mbar_arrive(&scanned[ns & (kScanRing - 1)]);
+          }
+        }
+        if (!ok) break;
+        p0 += 2 * it.n;
       }
     }
-    __syncthreads();
-    for (int j = 0; j < kKeys && t0 + j < most; ++j) {
-      float s = 0.0f;
+  } else {
+    regs_inc<kRegsSoft>();
+    // ---- softmax ------------------------------------------------------------------------
+    const int j = (warp - kWSoft) >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t lanes = uint32_t(quarter * 32) << 16;
+    const uint32_t ts = tmem + lanes + j * kKT, to = tmem + lanes + 256 + j * D;
+    int nsf = 0, nof = 0, ns = 0, p0 = 0;   // scores and outputs awaited; masked tiles; ring position
+    bool ok = true;
+    PfItem it;
+    const float c = P.c;
+    for (int t = 0; ok && next_item(t, lane == 0, &it); ++t) {
+      const int nkt = it.nkt[j];
+      const int vis = a.causal ? min(max(it.t0[j] + row + it.off + 1, 0), it.nk) : it.nk;
+      const int vis_w = __shfl_sync(0xFFFFFFFFu, vis, 0);   // the warp's fewest
+      float m = -INFINITY, l = 0.0f;
+      for (int i = 0; i < nkt; ++i) {
+        const int k0 = i * kKT;
+        const bool masked = k0 + kKT > it.vmin;
+        if (!uwait(&s_full[j], uint32_t(nsf++) & 1u, abort, status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t s[kKT];
 #pragma unroll
-      for (int i = 0; i < DS; ++i) s = fmaf(q[i], __bfloat162float(ks[j][part * DS + i]), s);
-      s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
-      s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
-      if (t0 + j >= vis) continue;
-      s *= a.scale;
-      if (s > m) {
-        const float f = expf(m - s);
-        m = s;
-        l *= f;
+        for (int x = 0; x < 4; ++x) tmem_ld32(ts + x * 32, s + x * 32);
+        tmem_wait_ld();
+        if (k0 + kKT > vis_w) {
+          const int n = vis - k0;
 #pragma unroll
-        for (int i = 0; i < DS; ++i) o[i] *= f;
+          for (int x = 0; x < kKT; ++x)
+            if (x >= n) s[x] = 0xFF800000u;
+        }
+        float mx[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) mx[x] = fmaxf(__uint_as_float(s[x]), __uint_as_float(s[x + 4]));
+#pragma unroll
+        for (int x = 8; x < kKT; x += 8)
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            mx[y] = fmaxf(mx[y], fmaxf(__uint_as_float(s[x + y]), __uint_as_float(s[x + y + 4])));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        const bool raise = top > m + kPfRaise;
+        if (__any_sync(0xFFFFFFFFu, raise)) {
+          const float f = raise ? pf_ex2(m - top) : 1.0f;
+          if (raise) m = top;
+          l *= f;
+          if (i > 0) {
+            // the previous product has finished: this tile's scores were issued after it
+#pragma unroll
+            for (int x = 0; x < D; x += 32) {
+              uint32_t o[32];
+              tmem_ld32(to + x, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+              tmem_st32(to + x, o);
+            }
+          }
+        }
+        const float ref = m == -INFINITY ? 0.0f : m;
+        const uint64_t c2 = pack2(c, c), r2 = pack2(-ref, -ref);
+        uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+        for (int x = 0; x < kKT; x += 32) {
+          uint32_t pb[16];
+#pragma unroll
+          for (int y = 0; y < 32; y += 4) {
+            float e0, e1, e2, e3;
+            unpack2(fma2(pack2(__uint_as_float(s[x + y]), __uint_as_float(s[x + y + 1])), c2, r2), e0, e1);
+            unpack2(fma2(pack2(__uint_as_float(s[x + y + 2]), __uint_as_float(s[x + y + 3])), c2, r2), e2, e3);
+            e0 = pf_ex2(e0);
+            e1 = pf_ex2(e1);
+            e2 = pf_ex2(e2);
+            e3 = pf_ex2(e3);
+            sum0 = add2(sum0, pack2(e0, e1));
+            sum1 = add2(sum1, pack2(e2, e3));
+            pb[y / 2] = bf16x2_bits(e0, e1);
+            pb[y / 2 + 1] = bf16x2_bits(e2, e3);
+          }
+          tmem_st16(ts + x / 2, pb);
+        }
+        {
+          float x0, x1;
+          unpack2(add2(sum0, sum1), x0, x1);
+          l += x0 + x1;
+        }
+        tmem_wait_st();
+        if (masked) {
+          const int slot = ns & (kScanRing - 1);
+          if (!uwait(&scanned[slot], uint32_t(ns / kScanRing) & 1u, abort, status)) {
+            ok = false;
+            break;
+          }
+          ++ns;
+          if (poison[slot]) {
+            // this tile's visible products, by the thread of the query itself
+            const int pv = p0 + 2 * i + 1;
+            if (!uwait(&full[pv % NS], uint32_t(pv / NS) & 1u, abort, status)) {
+              ok = false;
+              break;
+            }
+            const uint8_t* v = smem + Plan::kRing + (pv % NS) * Plan::kTile;
+            for (int d0 = 0; d0 < D; d0 += 8) {
+              uint32_t o[8];
+              if (i > 0) {
+                tmem_ld8(to + d0, o);
+              } else {
+#pragma unroll
+                for (int y = 0; y < 8; ++y) o[y] = 0;
+              }
+              const uint8_t* vb = v + (d0 / 64) * kBoxBytes;
+              for (int k1 = 0; k1 < kKT; k1 += 16) {
+                uint32_t pk[8];
+                tmem_ld8(ts + k1 / 2, pk);
+#pragma unroll
+                for (int y = 0; y < 16; ++y) {
+                  const int key = k1 + y;
+                  if (k0 + key < vis) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(vb + key * 128 + (((d0 % 64) / 8) ^ (key & 7)) * 16);
+                    const float pr = y & 1 ? bf16_hi(pk[y / 2]) : bf16_lo(pk[y / 2]);
+                    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                      o[2 * z] = __float_as_uint(fmaf(pr, bf16_lo(ww[z]), __uint_as_float(o[2 * z])));
+                      o[2 * z + 1] = __float_as_uint(fmaf(pr, bf16_hi(ww[z]), __uint_as_float(o[2 * z + 1])));
+                    }
+                  }
+                }
+                __syncwarp();
+              }
+              asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(to + d0),
+                           MOE_I8(o, 0)
+                           : "memory");
+            }
+            tmem_wait_st();
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[j]);
       }
-      const float p = s == -INFINITY ? 0.0f : expf(s - m);
-      l += p;
+      if (!ok) break;
+      p0 += 2 * it.n;
+      // masked tiles of the item that this query tile does not take part in
+      {
+        const int from = max(it.vmin / kKT, nkt);
+        if (it.n > from) ns += it.n - from;
+      }
+      if (it.rows[j] == 0) continue;
+      const bool mine = row < it.rows[j];
+      const int64_t orow = (int64_t)(it.q0[j] + row) * a.n_heads + it.head[j];
+      __nv_bfloat16* out = a.out + orow * D;
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      if (nkt > 0) {
+        if (!uwait(&o_full[j], uint32_t(nof++) & 1u, abort, status)) break;
+        tc_fence_after();
+      }
 #pragma unroll
-      for (int i = 0; i < DS; ++i) o[i] = fmaf(p, __bfloat162float(vs[j][part * DS + i]), o[i]);
+      for (int x = 0; x < D; x += 32) {
+        uint32_t o[32];
+        if (nkt > 0) {
+          tmem_ld32(to + x, o);
+          tmem_wait_ld();
+          if (x + 32 == D) {   // all of O is in registers: the next item may overwrite it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_free[j]);
+          }
+        } else {
+#pragma unroll
+          for (int y = 0; y < 32; ++y) o[y] = 0;
+        }
+        uint32_t b[16];
+#pragma unroll
+        for (int y = 0; y < 16; ++y)
+          b[y] = l == 0.0f ? 0u : bf16x2_bits(__uint_as_float(o[2 * y]) * inv, __uint_as_float(o[2 * y + 1]) * inv);
+        if (mine) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            *reinterpret_cast<uint4*>(out + x + y * 8) = make_uint4(b[4 * y], b[4 * y + 1], b[4 * y + 2], b[4 * y + 3]);
+        }
+      }
+      if (mine && a.lse) a.lse[orow] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2f;
     }
   }
-  if (r >= nq) return;
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-  for (int i = 0; i < DS; ++i)
-    a.out[((size_t)(q0 + r) * a.n_heads + hq) * D + part * DS + i] = __float2bfloat16_rn(o[i] * inv);
-  if (a.lse && part == 0) a.lse[(size_t)(q0 + r) * a.n_heads + hq] = l == 0.0f ? -INFINITY : m + logf(l);
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWMma) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Tensor map of bf16 rows [tokens][heads][D] with these strides (elements):
+// boxes of 64 channels of one head by 128 tokens, 128-byte swizzle. The outer
+// dimension is the one with the larger stride.
+int encode_rows(PfParams* p, int w, const __nv_bfloat16* base, int tokens, int heads, int D, int64_t ts, int64_t hs) {
+  if (tokens > 1 && ts == 0) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (heads > 1 && hs == 0) {
+    p->one_head[w] = 1;
+    heads = 1;
+  }
+  if (heads == 1) hs = D;
+  if (tokens == 1) ts = D;
+  const bool sw = hs > ts;
+  p->swapped[w] = sw;
+  const uint64_t dims[3] = {uint64_t(D), uint64_t(sw ? tokens : heads), uint64_t(sw ? heads : tokens)};
+  const uint64_t strides[2] = {uint64_t(sw ? ts : hs) * 2, uint64_t(sw ? hs : ts) * 2};
+  const uint32_t box[3] = {64, sw ? 128u : 1u, sw ? 1u : 128u};
+  return tma_encode(&p->map[w], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box,
+                    CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int D>
+int launch_pf(const PfParams& P, const DeviceInfo& di, cudaStream_t s) {
+  constexpr uint32_t smem = PfPlan<D>::kTotal;
+  if (smem > di.smem_optin) return MOE_ERR_UNSUPPORTED_SHAPE;
+  // the register split draws on what the launch gives: a build that launches
+  // with fewer registers would wait for ever
+  cudaFuncAttributes at;
+  MOE_CUDA_TRY(cudaFuncGetAttributes(&at, prefill_kernel<D>));
+  if (at.numRegs != kRegsLaunch) return MOE_ERR_CUDA;
+  MOE_CUDA_TRY(cudaFuncSetAttribute(prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
+  const int64_t G = P.a.n_heads / P.a.n_kv;
+  const int64_t most = P.a.n_kv * (((int64_t)P.a.total_q / kQT + P.a.n_seq) * G / 2 + P.a.n_seq);
+  const int grid = int(most < di.sm_count ? most : di.sm_count);
+  prefill_kernel<D><<<grid, kPfThreads, smem, s>>>(P);
+  return launch_status();
 }
 
 }  // namespace
 
 int launch_attn_prefill(const PrefillArgs& a, const DeviceInfo& di, cudaStream_t s) {
-  (void)di;
-  // tiles of all sequences, and one block more, which looks at every sequence
-  const dim3 grid(unsigned(a.total_q / kRowsPerCta + a.n_seq + 1), a.n_heads);
-  if (a.D == 128)
-    prefill_simple_kernel<128><<<grid, kThreads, 0, s>>>(a);
-  else
-    prefill_simple_kernel<64><<<grid, kThreads, 0, s>>>(a);
-  return launch_status();
+  PfParams P{};
+  int st;
+  if ((st = encode_rows(&P, 0, a.q, a.total_q, a.n_heads, a.D, a.q_ts, a.q_hs))) return st;
+  if (a.total_k > 0) {
+    if ((st = encode_rows(&P, 1, a.k, a.total_k, a.n_kv, a.D, a.k_ts, a.k_hs))) return st;
+    if ((st = encode_rows(&P, 2, a.v, a.total_k, a.n_kv, a.D, a.v_ts, a.v_hs))) return st;
+  }
+  P.a = a;
+  // a scale of 0 must still turn a masked score (-inf) into a probability of 0
+  const float c = fabsf(a.scale) * kLog2ef;
+  P.c = c > 1e-30f ? c : 1e-30f;
+  P.negate = a.scale < 0.0f;
+  return a.D == 128 ? launch_pf<128>(P, di, s) : launch_pf<64>(P, di, s);
 }
 
 }  // namespace moe
