@@ -12,28 +12,31 @@
 // the pair to finish (a counter) joins them in order, so results do not depend
 // on who finishes when.
 //
-// Inside a CTA the warps take groups of 16 positions (a group never leaves its
-// page, so it has one scale for keys and one for values). A warp's next groups
-// are on their way into shared memory by cp.async, every lane fetching what
-// itself will use: no barrier, no bank conflict. Both products run on the f16
-// warp MMA (m16n8k16) with positions or channels as its 16 rows and the query
-// rows (token, head of the group) as its 8 columns: E4M3 converts to f16
-// exactly, two codes an instruction, and up to 8 query rows cost one MMA
-// column block instead of a 16-row one.
-//   scores   S^T[pos][row] = K q^T: lane (g, c) holds 16-byte chunks of the
-//            positions g and g + 8 and takes 4 consecutive codes of a chunk as
-//            its k = 2c, 2c+1, 2c+8, 2c+9 of one MMA; q is loaded in the same
-//            order, as f16 scaled by a power of two per row
-//   softmax  running maximum that is raised only when a score passes it by
-//            2^6 (probabilities up to 2^6 are exact enough in f16), sums in
-//            fp32 kept per lane until the end
-//   output   O^T[d][row] = V^T P^T: lane (g, c) holds a chunk of the positions
-//            2c, 2c+1, 2c+8, 2c+9; a byte permute pairs the codes of two
-//            positions; movmatrix turns the probabilities from S's layout
-//            into the B operand
-// The page's key scale multiplies the scores; O is held in units of the
-// largest value scale so far, and a group of smaller scale is added with an
-// fp32 factor, so no page's values are rounded for the sake of another's.
+// Inside a CTA the warps take chunks of 32 positions. A warp's next chunks are on
+// their way into its own part of shared memory by cp.async: no CTA barrier. Both
+// products run on the e4m3 warp MMA (m16n8k32, exact products, fp32 sums), which
+// takes the cache's codes as they are: no conversion, 4096 multiplies a cycle and
+// SM (measured: one MMA per 1.07 cycles; f16's m16n8k16 takes 2.03, and its
+// conversions from E4M3 another 1.5 per 512 bytes).
+//   scores   S^T[pos][row] = K q^T. A bf16 query value is two e4m3 terms, t0 its
+//            first 4 significant bits, t1 the other 4 times 16, after a power
+//            of two per row that puts the row's largest in [2^7, 2^8): exact
+//            down to 2^-13 of that, then within 2^-22 of it. Lane (g, c) takes
+//            16-byte pieces of the positions 2g and 2g + 1 as consecutive
+//            words of its A fragment; q is laid out in the same order.
+//   output   O^T[d][row] = V^T P^T. ldmatrix transposes bytes on the way from
+//            shared memory, so lane (g, c) holds 4 consecutive positions of
+//            channel g. The probabilities of a chunk, relative to the chunk's
+//            largest times 2^8, are three e4m3 terms (12 significant bits, and
+//            2^-18 of the largest); since S's rows were dealt 2g, 2g + 1, a
+//            movmatrix on byte pairs turns them into the B operand.
+//   joining  a chunk's product goes into O with an fp32 factor per row that
+//            holds its reference and its page's value scale. A page of 16
+//            positions shares its chunk with another: the probabilities then
+//            carry the difference of the scales, and their reference is the
+//            largest product of both, so no page is rounded for another's sake.
+// The references of O and of the sum follow the maximum only when it passes them
+// by 2^30: fp32 has the range, and O is hardly ever rescaled.
 #include "attn.h"
 #include "fp8kv.cuh"
 
@@ -43,7 +46,8 @@ namespace {
 constexpr int kDecWarps = 8;
 constexpr int kDecThreads = kDecWarps * 32;
 constexpr int kMaxSeqs = 4096;
-constexpr float kRaise = 6.0f;     // log2 by which a score may pass the reference
+constexpr float kRaise = 30.0f;    // log2 by which a score may pass the reference
+constexpr int kChunk = 32;         // positions per warp step
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Workspace: counters [n_seq * n_kv], then partials, then (with weights) the
@@ -54,12 +58,16 @@ struct DecWs {
 };
 
 struct DecPlan {
-  int nt, rt;         // column blocks of 8 rows per warp; row tiles
+  int nt, rt;         // blocks of 8 query rows per warp; row tiles
 };
+// Up to 24 rows stay with one warp (its output takes 32 registers a block at
+// head_dim 128); more are cut into tiles whose warps read the same positions.
 inline DecPlan dec_plan(int rows) {
   if (rows <= 8) return {1, 1};
   if (rows <= 16) return {2, 1};
+  if (rows <= 24) return {3, 1};
   if (rows <= 32) return {2, 2};
+  if (rows <= 48) return {3, 2};
   return {2, 4};
 }
 
@@ -67,10 +75,11 @@ struct DecParams {
   DecodeArgs a;
   int G, rows;              // query heads per kv head; query rows n_new * G
   unsigned* counter;        // [n_seq * n_kv]
-  float* parts;             // [n_cta][2][rows padded][D + 2]
+  float* parts;             // [n_cta][2][rows padded][D + 4]: output, then the references and the sum
   float* lse2;              // [n_seq * n_kv][rows padded] (weights)
   float* scores;            // [n_seq * n_kv][cap][rows padded] (weights)
   int64_t cap;
+  int log2_page;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -86,33 +95,31 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// codes in the low or high half of a word -> f16 pair
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
-  uint32_t r;
-  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}\n" : "=r"(r) : "r"(w));
-  return r;
-}
-__device__ __forceinline__ uint32_t e4m3x2_f16x2_hi(uint32_t w) {
-  uint32_t r;
-  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}\n" : "=r"(r) : "r"(w));
-  return r;
-}
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
+__device__ __forceinline__ void mma_fp8(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t movm(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-__device__ __forceinline__ uint32_t f16x2_bits(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
+// Two 16 x 16 byte matrices, rows of 16 bytes at the lanes' addresses (lanes 0
+// .. 15 the first's), transposed: lane (g, c) gets bytes 4c .. 4c + 3 of the
+// columns g and g + 8 of the first, then of the second.
+__device__ __forceinline__ void ldm_trans8(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
 }
+// e4m3 pairs (a, b) and (c, d) -> one word, a in the lowest byte
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  return uint32_t(f32x2_to_e4m3x2(a, b)) | uint32_t(f32x2_to_e4m3x2(c, d)) << 16;
+}
+__device__ __forceinline__ float top4(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFF00000u); }
 // Does one of the word's four codes stand for NaN?
 __device__ __forceinline__ bool any_nan4(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
@@ -130,25 +137,29 @@ __device__ __forceinline__ int dec_length(const DecodeArgs& a, int b, bool* bad)
 // + 1, .. RT work on the same positions). WT: scores are kept for the weights.
 template <int D, int NT, int RT, bool WT>
 struct DecCfg {
-  static constexpr int kStages = 4;
-  static constexpr int kGroups = kDecWarps / RT;         // position groups in flight per CTA step
-  static constexpr int kUnit = 16 * kGroups;             // positions per unit
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kGroups = kDecWarps / RT;         // chunks in work per CTA step
+  static constexpr int kUnit = kChunk * kGroups;         // positions per unit
   static constexpr int kRows = 8 * NT * RT;              // padded query rows
-  static constexpr int kVec = D / 16;                    // 16-byte vectors per lane and group (keys + values)
-  static constexpr uint32_t kStageBytes = kVec * 32 * 16;
+  static constexpr uint32_t kKBytes = kChunk * D;
+  static constexpr uint32_t kVCol = kChunk * 16 + 64;    // 16 channels of a chunk; 64 bytes on, for the banks
+  static constexpr uint32_t kStageBytes = kKBytes + D / 16 * kVCol;
   static constexpr uint32_t kRing = kDecWarps * kStages * kStageBytes;
-  static constexpr uint32_t kMerge = kDecWarps * 8 * NT * (D + 2) * 4;   // reuses the ring
-  static constexpr uint32_t kSmem = (kRing > kMerge ? kRing : kMerge) + (kMaxSeqs + 1) * 4 + 64;
+  static constexpr int kLd = D + 4;                      // row stride of the merge, floats
+  static constexpr uint32_t kMerge = kDecWarps * 8 * NT * (kLd + 3) * 4;   // reuses the ring
+  static constexpr uint32_t kPrefix = kRing > kMerge ? kRing : kMerge;
+  static constexpr uint32_t kSmem = kPrefix + (kMaxSeqs + 1) * 4;
+  static constexpr int kPart = kRows * (D + 4);          // floats of a partial result
 };
 
 template <int D, int NT, int RT, bool WT>
 __global__ void __launch_bounds__(kDecThreads) decode_attn_kernel(const DecParams p) {
   using C = DecCfg<D, NT, RT, WT>;
-  constexpr int KS = D / 16;      // MMA steps over the channels
+  constexpr int KS = D / 32;      // MMA steps over the channels
   constexpr int MT = D / 16;      // 16-channel blocks of the output
-  constexpr int KC = D / 64;      // 16-byte key chunks per lane and position
+  constexpr int KC = D / 64;      // 16-byte pieces per lane and position
   extern __shared__ __align__(128) uint8_t smem[];
-  int* prefix = reinterpret_cast<int*>(smem + (C::kRing > C::kMerge ? C::kRing : C::kMerge));
+  int* prefix = reinterpret_cast<int*>(smem + C::kPrefix);
   __shared__ int s_scan[kDecWarps];
   __shared__ int s_last;
   const DecodeArgs& a = p.a;
@@ -195,7 +206,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_attn_kernel(const DecParam
 
   const int rt = warp % RT, tg = warp / RT;
   uint8_t* ring = smem + (size_t)warp * C::kStages * C::kStageBytes;
-  const uint32_t ring_s = smem_addr(ring) + lane * 16;
+  const uint32_t ring_s = smem_addr(ring);
 
   while (pos < end) {
     // sequence of unit pos: the last b with prefix[b] H <= pos
@@ -211,54 +222,92 @@ __global__ void __launch_bounds__(kDecThreads) decode_attn_kernel(const DecParam
     bool ignore = false;
     const int L = dec_length(a, b, &ignore);
     const int first = u0 * C::kUnit, last = min(L, u1 * C::kUnit);
-    const int n_my = last > first + tg * 16 ? (last - first - tg * 16 + C::kUnit - 1) / C::kUnit : 0;
+    const int n_my = last > first + tg * kChunk ? (last - first - tg * kChunk + C::kUnit - 1) / C::kUnit : 0;
     const int32_t* table = a.table + (size_t)b * a.width;
     const size_t head_bytes = (size_t)P * D, page_bytes = head_bytes * H;
     const uint8_t* kbase = static_cast<const uint8_t*>(a.c.k_codes) + h * head_bytes;
     const uint8_t* vbase = static_cast<const uint8_t*>(a.c.v_codes) + h * head_bytes;
 
-    // position of this warp's group i; its page (-1: outside the cache)
-    auto gpos = [&](int i) { return first + (i * C::kGroups + tg) * 16; };
-    auto page_of = [&](int i) {
-      if (i >= n_my) return -1;
-      const int pg = __ldg(table + gpos(i) / P);
-      return pg >= 0 && pg < a.c.n_pages ? pg : -1;
-    };
-    auto issue = [&](int i, int pg) {
-      if (i < n_my && pg >= 0) {
-        const size_t row = (size_t)pg * page_bytes + (size_t)(gpos(i) % P) * D;
-        const uint32_t dst = ring_s + (i % C::kStages) * C::kStageBytes;
-        const uint8_t* k0 = kbase + row + c * 16;
-#pragma unroll
-        for (int j = 0; j < KC; ++j) {
-          cp_async16(dst + (2 * j) * 512, k0 + (size_t)g * D + 64 * j);
-          cp_async16(dst + (2 * j + 1) * 512, k0 + (size_t)(g + 8) * D + 64 * j);
+    auto gpos = [&](int i) { return first + (i * C::kGroups + tg) * kChunk; };
+    // Pages and scales of 32 chunks at a time, lane l those of the l-th: halves
+    // (16 positions) A and B, -1 outside the table or the cache. Scales of the
+    // chunks in work and of those being fetched.
+    int pg_a = -1, pg_b = -1;
+    uint32_t sc_next = 0, sc = 0;                                   // scale bytes kA kB vA vB
+    uint32_t bad_na = 0, bad_nb = 0, bad_a = 0, bad_b = 0;          // chunks whose half has no page
+    auto lookup = [&](int i0) {
+      const int i = i0 + lane;
+      const int t = gpos(i);
+      pg_a = pg_b = -1;
+      uint32_t w = 0;
+      bool oob_a = false, oob_b = false;
+      if (i < n_my) {
+        pg_a = __ldg(table + (t >> p.log2_page));
+        oob_a = pg_a < 0 || pg_a >= a.c.n_pages;
+        if (oob_a) pg_a = -1;
+        if (t + 16 < last) {
+          pg_b = P == 16 ? __ldg(table + (t >> 4) + 1) : pg_a;
+          oob_b = pg_b < 0 || pg_b >= a.c.n_pages;
+          if (oob_b) pg_b = -1;
         }
-        // head_dim 128: chunk g of the positions 2c, 2c+1, 2c+8, 2c+9; head_dim
-        // 64: a position has 4 chunks, lanes g and g ^ 1 fetch two positions' each
-        const uint8_t* v0 = vbase + row;
-        if (D == 128) {
-          cp_async16(dst + (2 * KC) * 512, v0 + (size_t)(2 * c) * D + g * 16);
-          cp_async16(dst + (2 * KC + 1) * 512, v0 + (size_t)(2 * c + 1) * D + g * 16);
-          cp_async16(dst + (2 * KC + 2) * 512, v0 + (size_t)(2 * c + 8) * D + g * 16);
-          cp_async16(dst + (2 * KC + 3) * 512, v0 + (size_t)(2 * c + 9) * D + g * 16);
+        if (pg_a >= 0) {
+          const size_t o = (size_t)pg_a * H + h;
+          w = __ldg(a.c.k_scales + o) | uint32_t(__ldg(a.c.v_scales + o)) << 16;
+        }
+        if (pg_b >= 0) {
+          const size_t o = (size_t)pg_b * H + h;
+          w |= uint32_t(__ldg(a.c.k_scales + o)) << 8 | uint32_t(__ldg(a.c.v_scales + o)) << 24;
         } else {
-          const int o = g & 1;
-          cp_async16(dst + (2 * KC) * 512, v0 + (size_t)(2 * c + o) * D + (g >> 1) * 16);
-          cp_async16(dst + (2 * KC + 1) * 512, v0 + (size_t)(2 * c + 8 + o) * D + (g >> 1) * 16);
+          w |= (w & 0x00FF00FFu) << 8;
+        }
+      }
+      sc_next = w;
+      bad_na = __ballot_sync(0xFFFFFFFFu, oob_a);
+      bad_nb = __ballot_sync(0xFFFFFFFFu, oob_b);
+      if ((bad_na | bad_nb) && lane == 0 && a.status) atomicOr(a.status, MOE_DEV_INDEX_OOB);
+    };
+    auto issue = [&](int i) {
+      if ((i & 31) == 0) lookup(i);
+      const int pa = __shfl_sync(0xFFFFFFFFu, pg_a, i & 31), pb = __shfl_sync(0xFFFFFFFFu, pg_b, i & 31);
+      if (i < n_my) {
+        const int slot = gpos(i) & (P - 1);
+        const size_t ra = (size_t)max(pa, 0) * page_bytes + slot * D;
+        const size_t rb = P == 16 ? (size_t)max(pb, 0) * page_bytes : ra + 16 * D;
+        const uint32_t st = ring_s + (i % C::kStages) * C::kStageBytes;
+        // keys: lane (g, c) what it will use, at its own 16 bytes of each row of 512
+        const uint32_t ko = (2 * g) * D + c * 16;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          if ((mt ? pb : pa) < 0) continue;
+          const uint8_t* k0 = kbase + (mt ? rb : ra) + ko;
+#pragma unroll
+          for (int o = 0; o < 2; ++o)
+#pragma unroll
+            for (int j = 0; j < KC; ++j)
+              cp_async16(st + ((mt * 2 + o) * KC + j) * 512 + lane * 16, k0 + o * D + 64 * j);
+        }
+        // values: rows of D bytes, a lane 16 of them, to [16-channel block][position]
+        constexpr int LPR = D / 16, RPI = 32 / LPR;   // lanes per row, rows per instruction
+        const uint32_t vd = st + C::kKBytes + (lane % LPR) * C::kVCol + (lane / LPR) * 16;
+        const uint32_t vo = (lane / LPR) * D + (lane % LPR) * 16;
+#pragma unroll
+        for (int n = 0; n < kChunk / RPI; ++n) {
+          const bool second = n >= 16 / RPI;
+          if ((second ? pb : pa) < 0) continue;
+          cp_async16(vd + n * RPI * 16, vbase + (second ? rb + (n * RPI - 16) * D : ra + n * RPI * D) + vo);
         }
       }
       cp_async_commit();
     };
 
-    // query rows -> B fragments (f16, scaled by 2^-qe) and the factors that undo it
-    uint32_t qf[KS][NT][2];
-    float qs[NT][2];         // of rows 2c, 2c+1 of each block: 2^qe scale log2(e)
+    // query rows -> B fragments (two e4m3 terms) and the factors that undo their scale
+    uint32_t qf[2][KS][NT][2];
+    float qs[NT][2];         // of rows 2c, 2c+1 of each block: 2^e scale log2(e)
     int vis[NT][2];          // positions that those rows see
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int r = (rt * NT + n) * 8 + g;
-      float x[KS * 4];
+      float x[KC * 16];
       float top = 0.0f;
       if (r < p.rows) {
         const __nv_bfloat16* q = a.q + ((int64_t)b * T + r / p.G) * a.q_ts + (int64_t)(h * p.G + r % p.G) * a.q_hs;
@@ -274,22 +323,32 @@ __global__ void __launch_bounds__(kDecThreads) decode_attn_kernel(const DecParam
           }
         }
 #pragma unroll
-        for (int i = 0; i < KS * 4; ++i) top = fmaxf(top, fabsf(x[i]));
+        for (int i = 0; i < KC * 16; ++i) top = fmaxf(top, fabsf(x[i]));
       } else {
 #pragma unroll
-        for (int i = 0; i < KS * 4; ++i) x[i] = 0.0f;
+        for (int i = 0; i < KC * 16; ++i) x[i] = 0.0f;
       }
       top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
       int e = 0;
       if (top > 0.0f && top < INFINITY) {
         frexpf(top, &e);
-        e -= 12;             // the row's largest value in [2^11, 2^12)
+        e -= 8;              // the row's largest value in [2^7, 2^8)
       }
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        qf[k][n][0] = f16x2_bits(scale2(x[4 * k], -e), scale2(x[4 * k + 1], -e));
-        qf[k][n][1] = f16x2_bits(scale2(x[4 * k + 2], -e), scale2(x[4 * k + 3], -e));
+      for (int i = 0; i < KC * 16; i += 4) {
+        float t0[4], t1[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          // inf has no e4m3 code: the row is NaN, as softmax of infinite scores is
+          const float y = fabsf(x[i + k]) == INFINITY ? __int_as_float(0x7FC00000) : scale2(x[i + k], -e);
+          const uint32_t code = f32x2_to_e4m3x2(top4(y), 0.0f) & 0xFFu;
+          t0[k] = e4m3_is_nan(code) ? y : e4m3_to_f32(code);
+          t1[k] = (y - t0[k]) * 16.0f;
+        }
+        // 8 channels per MMA step: the first word is b0, the second b1
+        qf[0][i / 8][n][(i / 4) & 1] = e4m3x4(t0[0], t0[1], t0[2], t0[3]);
+        qf[1][i / 8][n][(i / 4) & 1] = e4m3x4(t1[0], t1[1], t1[2], t1[3]);
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -300,7 +359,8 @@ __global__ void __launch_bounds__(kDecThreads) decode_attn_kernel(const DecParam
       }
     }
 
-    float o[MT][NT][4], m[NT][2], l[NT][2];
+    // O (in units of 2^ro), the sum (of 2^m)
+    float o[MT][NT][4], m[NT][2], ro[NT][2], l[NT][2];
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -310,188 +370,214 @@ __global__ void __launch_bounds__(kDecThreads) decode_attn_kernel(const DecParam
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) m[n][j] = -INFINITY, l[n][j] = 0.0f;
-    int unit = 0;             // scale byte of o
+      for (int j = 0; j < 2; ++j) m[n][j] = ro[n][j] = -INFINITY, l[n][j] = 0.0f;
 
-    // pages and scales one step ahead of their use
-    int pgs[C::kStages];      // pages of groups i .. i + kStages - 1
-#pragma unroll
-    for (int j = 0; j < C::kStages; ++j) pgs[j] = page_of(j);
-#pragma unroll
-    for (int j = 0; j < C::kStages - 1; ++j) issue(j, pgs[j]);
-    auto scale_of = [&](const uint8_t* s, int pg) { return pg >= 0 ? int(__ldg(s + (size_t)pg * H + h)) : 0; };
-    int ks_n = scale_of(a.c.k_scales, pgs[0]), vs_n = scale_of(a.c.v_scales, pgs[0]);
+#pragma unroll 1
+    for (int j = 0; j < C::kStages - 1; ++j) {
+      issue(j);
+      if (j == 0) sc = sc_next, bad_a = bad_na, bad_b = bad_nb;
+    }
 
+#pragma unroll 1
     for (int i = 0; i < n_my; ++i) {
-      issue(i + C::kStages - 1, pgs[C::kStages - 1]);
-      const int pg = pgs[0], ks = ks_n, vs = vs_n;
-#pragma unroll
-      for (int j = 0; j + 1 < C::kStages; ++j) pgs[j] = pgs[j + 1];
-      pgs[C::kStages - 1] = page_of(i + C::kStages);
-      ks_n = scale_of(a.c.k_scales, pgs[0]);
-      vs_n = scale_of(a.c.v_scales, pgs[0]);
+      issue(i + C::kStages - 1);
+      if ((i & 31) == 0) sc = sc_next, bad_a = bad_na, bad_b = bad_nb;   // fetches are ahead by less than 32
       cp_async_wait<C::kStages - 1>();
+      __syncwarp();
+      const uint32_t w = __shfl_sync(0xFFFFFFFFu, sc, i & 31);
       const int t0 = gpos(i);
-      if (pg < 0) {
-        if (a.status && lane == 0) atomicOr(a.status, MOE_DEV_INDEX_OOB);
-      }
-      const uint4* st = reinterpret_cast<const uint4*>(ring + (i % C::kStages) * C::kStageBytes) + lane;
+      const int va = int(w >> 16 & 0xFFu), vb = int(w >> 24);
+      const bool no_a = bad_a >> (i & 31) & 1u, no_b = bad_b >> (i & 31) & 1u;
+      const uint32_t st = (i % C::kStages) * C::kStageBytes;
+      const uint4* kst = reinterpret_cast<const uint4*>(ring + st) + lane;
+      const bool full = !no_a && !no_b && t0 + kChunk <= L - T + 1;   // every row sees every position
 
-      // scores
-      float s[NT][4];
+      uint32_t pf[3][NT][2];      // probabilities: terms, row blocks, halves
+      float beta[NT][2];
+      {
+        uint4 kw[2][2][KC];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+        for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[n][j] = 0.0f;
+          for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int j = 0; j < KC; ++j) {
-        const uint4 ka = st[(2 * j) * 32], kb = st[(2 * j + 1) * 32];
-        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t a0 = e4m3x2_f16x2(wa[k]), a2 = e4m3x2_f16x2_hi(wa[k]);
-          const uint32_t a1 = e4m3x2_f16x2(wb[k]), a3 = e4m3x2_f16x2_hi(wb[k]);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) mma_f16(s[n], a0, a1, a2, a3, qf[4 * j + k][n][0], qf[4 * j + k][n][1]);
-        }
-      }
-      const bool full = pg >= 0 && t0 + 16 <= L - T + 1;   // every row sees every position
-      const float kf = exp2i(ks - 127);
-      bool raise = false;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s[n][j] *= qs[n][j & 1] * kf;
-          if (!full && (pg < 0 || t0 + g + (j >> 1) * 8 >= vis[n][j & 1])) s[n][j] = -INFINITY;
-          raise |= s[n][j] > m[n][j & 1] + kRaise;
-        }
-      if (WT) {
-        const int64_t pair = (int64_t)b * H + h;
-        float* sc = p.scores + (pair * p.cap + t0) * C::kRows + rt * NT * 8 + 2 * c;
+            for (int j = 0; j < KC; ++j) kw[mt][x][j] = kst[((mt * 2 + x) * KC + j) * 32];
+        const float kfa = exp2i(int(w & 0xFFu) - 127), kfb = exp2i(int(w >> 8 & 0xFFu) - 127);
+        const float vfa = float(va - 127), vfb = float(vb - 127);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          if (t0 + g < L) *reinterpret_cast<float2*>(sc + (size_t)g * C::kRows + n * 8) = make_float2(s[n][0], s[n][1]);
-          if (t0 + g + 8 < L)
-            *reinterpret_cast<float2*>(sc + (size_t)(g + 8) * C::kRows + n * 8) = make_float2(s[n][2], s[n][3]);
-        }
-      }
-      if (__any_sync(0xFFFFFFFFu, raise)) {
+          float s[2][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+          for (int mt = 0; mt < 2; ++mt) {
+            float s1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[mt][j] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < KC; ++j) {
+              const uint4 x = kw[mt][0][j], y = kw[mt][1][j];
+              const uint32_t a0[4] = {x.x, y.x, x.y, y.y}, a1[4] = {x.z, y.z, x.w, y.w};
+              mma_fp8(s[mt], a0, qf[0][2 * j][n][0], qf[0][2 * j][n][1]);
+              mma_fp8(s1, a0, qf[1][2 * j][n][0], qf[1][2 * j][n][1]);
+              mma_fp8(s[mt], a1, qf[0][2 * j + 1][n][0], qf[0][2 * j + 1][n][1]);
+              mma_fp8(s1, a1, qf[1][2 * j + 1][n][0], qf[1][2 * j + 1][n][1]);
+            }
+            // s[mt][x]: position t0 + 16 mt + 2g + x / 2, row 2c + x % 2
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              s[mt][x] = fmaf(s1[x], 0.0625f, s[mt][x]) * (qs[n][x & 1] * (mt ? kfb : kfa));
+              if (!full && ((mt ? no_b : no_a) || t0 + 16 * mt + 2 * g + (x >> 1) >= vis[n][x & 1])) s[mt][x] = -INFINITY;
+            }
+          }
+          if (WT) {
+            float* sp = p.scores + (((int64_t)b * H + h) * p.cap + t0 + 2 * g) * C::kRows + (rt * NT + n) * 8 + 2 * c;
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+              for (int x = 0; x < 2; ++x)
+                if (t0 + 16 * mt + 2 * g + x < L)
+                  *reinterpret_cast<float2*>(sp + (16 * mt + x) * C::kRows) = make_float2(s[mt][2 * x], s[mt][2 * x + 1]);
+          }
+          // the chunk's largest score, and largest score times value scale
+          float us[2], ms[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float x = fmaxf(s[n][j], s[n][j + 2]);
-            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
-            x = fmaxf(x, m[n][j]);
-            const float f = x == m[n][j] ? 1.0f : ex2(m[n][j] - x);   // equal also where both are -inf
-            m[n][j] = x;
-            l[n][j] *= f;
-#pragma unroll
-            for (int t = 0; t < MT; ++t) o[t][n][j] *= f, o[t][n][j + 2] *= f;
+            const float xa = fmaxf(s[0][j], s[0][j + 2]), xb = fmaxf(s[1][j], s[1][j + 2]);
+            us[j] = fmaxf(xa + vfa, xb + vfb);
+            us[j] = fmaxf(us[j], __shfl_xor_sync(0xFFFFFFFFu, us[j], 4));
+            us[j] = fmaxf(us[j], __shfl_xor_sync(0xFFFFFFFFu, us[j], 8));
+            us[j] = fmaxf(us[j], __shfl_xor_sync(0xFFFFFFFFu, us[j], 16));
+            ms[j] = fmaxf(xa, xb);
           }
-      }
-      uint32_t pb[NT][2];
+          if (va == vb) {
+            ms[0] = us[0] - vfa;
+            ms[1] = us[1] - vfa;
+          } else {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float e[4];
+            for (int j = 0; j < 2; ++j) {
+              ms[j] = fmaxf(ms[j], __shfl_xor_sync(0xFFFFFFFFu, ms[j], 4));
+              ms[j] = fmaxf(ms[j], __shfl_xor_sync(0xFFFFFFFFu, ms[j], 8));
+              ms[j] = fmaxf(ms[j], __shfl_xor_sync(0xFFFFFFFFu, ms[j], 16));
+            }
+          }
+          const bool raise = ms[0] > m[n][0] + kRaise || ms[1] > m[n][1] + kRaise || us[0] > ro[n][0] + kRaise ||
+                             us[1] > ro[n][1] + kRaise;
+          if (__any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          e[j] = s[n][j] == -INFINITY ? 0.0f : ex2(s[n][j] - m[n][j & 1]);
-          l[n][j & 1] += e[j];
+            for (int j = 0; j < 2; ++j) {
+              if (ms[j] > m[n][j] + kRaise) {
+                l[n][j] *= ex2(m[n][j] - ms[j]);
+                m[n][j] = ms[j];
+              }
+              if (us[j] > ro[n][j] + kRaise) {
+                const float f = ex2(ro[n][j] - us[j]);
+                ro[n][j] = us[j];
+#pragma unroll
+                for (int t = 0; t < MT; ++t) o[t][n][j] *= f, o[t][n][j + 2] *= f;
+              }
+            }
+          }
+          // probabilities times 2^8 over the chunk's largest, in three terms
+          float pr[2][4];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const bool none = us[j] == -INFINITY;
+            const float ref = none ? 0.0f : 8.0f - us[j];
+            beta[n][j] = none ? 0.0f : ex2(us[j] - 8.0f - ro[n][j]);
+#pragma unroll
+            for (int x = j; x < 4; x += 2) {
+              pr[0][x] = ex2(s[0][x] + (vfa + ref));
+              pr[1][x] = ex2(s[1][x] + (vfb + ref));
+            }
+            if (va == vb) {
+              const float sum = (pr[0][j] + pr[0][j + 2]) + (pr[1][j] + pr[1][j + 2]);
+              // a row of NaN scores has no largest one, but must not pass for empty
+              l[n][j] += none ? sum : sum * ex2(us[j] - 8.0f - vfa - m[n][j]);
+            } else {
+              const float mr = m[n][j] == -INFINITY ? 0.0f : m[n][j];
+              l[n][j] += (ex2(s[0][j] - mr) + ex2(s[0][j + 2] - mr)) + (ex2(s[1][j] - mr) + ex2(s[1][j + 2] - mr));
+            }
+          }
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            float t0v[4], t1v[4], t2v[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              t0v[x] = top4(pr[mt][x]);
+              const float r = pr[mt][x] - t0v[x];
+              t1v[x] = top4(r);
+              t2v[x] = r - t1v[x];
+            }
+            // row 2c's pair (positions 2g, 2g + 1), row 2c + 1's pair
+            pf[0][n][mt] = movm(e4m3x4(t0v[0], t0v[2], t0v[1], t0v[3]));
+            pf[1][n][mt] = movm(e4m3x4(t1v[0], t1v[2], t1v[1], t1v[3]));
+            pf[2][n][mt] = movm(e4m3x4(t2v[0], t2v[2], t2v[1], t2v[3]));
+          }
         }
-        pb[n][0] = movm(f16x2_bits(e[0], e[1]));
-        pb[n][1] = movm(f16x2_bits(e[2], e[3]));
       }
-      if (pg < 0) continue;
 
       // output
-      uint32_t vw[4][KC * 2];   // codes of the positions 2c, 2c+1, 2c+8, 2c+9
-      if (D == 128) {
+      const uint32_t va_s = ring_s + st + C::kKBytes + lane * 16;
+      if (full) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint4 v = st[(2 * KC + j) * 32];
-          vw[j][0] = v.x;
-          vw[j][1] = v.y;
-          vw[j][KC * 2 - 2] = v.z;
-          vw[j][KC * 2 - 1] = v.w;
-        }
-      } else {
-        // lanes g and g ^ 1 hold the two positions of a pair for the same 16
-        // channels: each keeps its half (8 channels) of both
-        const uint4 u = st[(2 * KC) * 32], v = st[(2 * KC + 1) * 32];
-        const bool odd = g & 1;
-        const uint32_t su0 = odd ? u.x : u.z, su1 = odd ? u.y : u.w, sv0 = odd ? v.x : v.z, sv1 = odd ? v.y : v.w;
-        const uint32_t ru0 = __shfl_xor_sync(0xFFFFFFFFu, su0, 4), ru1 = __shfl_xor_sync(0xFFFFFFFFu, su1, 4);
-        const uint32_t rv0 = __shfl_xor_sync(0xFFFFFFFFu, sv0, 4), rv1 = __shfl_xor_sync(0xFFFFFFFFu, sv1, 4);
-        vw[0][0] = odd ? ru0 : u.x;
-        vw[0][1] = odd ? ru1 : u.y;
-        vw[1][0] = odd ? u.z : ru0;
-        vw[1][1] = odd ? u.w : ru1;
-        vw[2][0] = odd ? rv0 : v.x;
-        vw[2][1] = odd ? rv1 : v.y;
-        vw[3][0] = odd ? v.z : rv0;
-        vw[3][1] = odd ? v.w : rv1;
-      }
-      bool poison = false;
-      if (!full) {
-        // positions past the end hold anything: zero codes
+        for (int t = 0; t < MT; ++t) {
+          uint32_t x[4];
+          ldm_trans8(x, va_s + t * C::kVCol);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bool out = t0 + 2 * c + (j & 1) + (j >> 1) * 8 >= L;
+          for (int n = 0; n < NT; ++n) {
+            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            mma_fp8(d, x, pf[2][n][0], pf[2][n][1]);
+            mma_fp8(d, x, pf[1][n][0], pf[1][n][1]);
+            mma_fp8(d, x, pf[0][n][0], pf[0][n][1]);
 #pragma unroll
-          for (int w = 0; w < KC * 2; ++w) {
-            if (out) vw[j][w] = 0;
-            poison |= any_nan4(vw[j][w]);
+            for (int j = 0; j < 4; ++j) o[t][n][j] = fmaf(d[j], beta[n][j & 1], o[t][n][j]);
           }
         }
-        poison = __any_sync(0xFFFFFFFFu, poison) && T > 1;
-      }
-      if (vs > unit) {
-        const float f = exp2i(unit - vs);
-        unit = vs;
+      } else {
+        // Positions past the end hold anything: their codes are zeroed. A half
+        // without a page too. Where a NaN is visible to some tokens only (0 * NaN is NaN) every token takes
+        // a pass over what it sees.
+        auto keep4 = [&](int first_pos, int seen) {   // bytes of 4 consecutive positions
+          const int k = seen - first_pos;
+          return k >= 4 ? 0xFFFFFFFFu : (k <= 0 ? 0u : (1u << (8 * k)) - 1u);
+        };
+        bool poison = false;
+        if (T > 1) {
+          const uint32_t ka = no_a ? 0u : keep4(t0 + 4 * c, L), kb = no_b ? 0u : keep4(t0 + 16 + 4 * c, L);
+#pragma unroll 1
+          for (int t = 0; t < MT; ++t) {
+            uint32_t x[4];
+            ldm_trans8(x, va_s + t * C::kVCol);
+            poison |= any_nan4(x[0] & ka) || any_nan4(x[1] & ka) || any_nan4(x[2] & kb) || any_nan4(x[3] & kb);
+          }
+          poison = __any_sync(0xFFFFFFFFu, poison);
+        }
+        const int n_pass = poison ? T : 1;
+#pragma unroll 1
+        for (int pass = 0; pass < n_pass; ++pass) {
+          const int seen = poison ? L - T + pass + 1 : L;
+          const uint32_t ka = no_a ? 0u : keep4(t0 + 4 * c, seen), kb = no_b ? 0u : keep4(t0 + 16 + 4 * c, seen);
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[t][n][j] *= f;
-      }
-      // one pass; or, where a NaN is visible to some tokens only (0 * NaN is
-      // NaN), a pass for each token over what it sees
-      for (int pass = 0; pass < (poison ? T : 1); ++pass) {
-        const float f = exp2i(vs - unit);
-        const bool direct = vs == unit && !poison;
-        const int seen = poison ? L - T + pass + 1 : 0x7FFFFFFF;
-#pragma unroll
-        for (int w = 0; w < KC * 2; ++w) {
-          uint32_t x[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) x[j] = t0 + 2 * c + (j & 1) + (j >> 1) * 8 >= seen ? 0u : vw[j][w];
-          const uint32_t p0 = __byte_perm(x[0], x[1], 0x5140), p1 = __byte_perm(x[0], x[1], 0x7362);
-          const uint32_t p2 = __byte_perm(x[2], x[3], 0x5140), p3 = __byte_perm(x[2], x[3], 0x7362);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t lo2 = k ? p1 : p0, hi2 = k ? p3 : p2;
-            const uint32_t a0 = e4m3x2_f16x2(lo2), a1 = e4m3x2_f16x2_hi(lo2);
-            const uint32_t a2 = e4m3x2_f16x2(hi2), a3 = e4m3x2_f16x2_hi(hi2);
+          for (int t = 0; t < MT; ++t) {
+            uint32_t x[4];
+            ldm_trans8(x, va_s + t * C::kVCol);
+            x[0] &= ka;
+            x[1] &= ka;
+            x[2] &= kb;
+            x[3] &= kb;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              if (direct) {
-                mma_f16(o[2 * w + k][n], a0, a1, a2, a3, pb[n][0], pb[n][1]);
-              } else {
-                float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                mma_f16(d, a0, a1, a2, a3, pb[n][0], pb[n][1]);
+              float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+              mma_fp8(d, x, pf[2][n][0], pf[2][n][1]);
+              mma_fp8(d, x, pf[1][n][0], pf[1][n][1]);
+              mma_fp8(d, x, pf[0][n][0], pf[0][n][1]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  if (!poison || vis[n][j & 1] == seen) o[2 * w + k][n][j] = fmaf(d[j], f, o[2 * w + k][n][j]);
-              }
+              for (int j = 0; j < 4; ++j)
+                if (!poison || vis[n][j & 1] == seen) o[t][n][j] = fmaf(d[j], beta[n][j & 1], o[t][n][j]);
             }
           }
         }
       }
+      __syncwarp();   // every lane has read the stage before it is filled again
     }
     cp_async_wait<0>();
 
@@ -505,44 +591,68 @@ __global__ void __launch_bounds__(kDecThreads) decode_attn_kernel(const DecParam
         l[n][j] += __shfl_xor_sync(0xFFFFFFFFu, l[n][j], 16);
       }
     __syncthreads();   // every warp has left the ring
-    float* mo = reinterpret_cast<float*>(smem);                    // [warp][8 NT][D]
-    float* mm = mo + kDecWarps * 8 * NT * D;                       // [warp][8 NT]
-    float* ml = mm + kDecWarps * 8 * NT;
-    {
-      const float f = exp2i(unit - 127);
+    constexpr int LD = C::kLd;
+    float* mo = reinterpret_cast<float*>(smem);                    // [warp][8 NT][LD]
+    float* mr = mo + kDecWarps * 8 * NT * LD;                      // [warp][8 NT]: reference of O
+    float* mm = mr + kDecWarps * 8 * NT;                           //   of the sum
+    float* ml = mm + kDecWarps * 8 * NT;                           //   the sum
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int r = n * 8 + 2 * c + j;
-          float* row = mo + ((size_t)warp * 8 * NT + r) * D + g * (D / 8);
+      for (int j = 0; j < 2; ++j) {
+        const int r = warp * 8 * NT + n * 8 + 2 * c + j;
+        float* row = mo + (size_t)r * LD + g;
 #pragma unroll
-          for (int t = 0; t < MT; ++t)
-            *reinterpret_cast<float2*>(row + 2 * t) = make_float2(o[t][n][j] * f, o[t][n][j + 2] * f);
-          if (g == 0) {
-            mm[warp * 8 * NT + r] = m[n][j];
-            ml[warp * 8 * NT + r] = l[n][j];
-          }
+        for (int t = 0; t < MT; ++t) {
+          row[16 * t] = o[t][n][j];
+          row[16 * t + 8] = o[t][n][j + 2];
         }
-    }
+        if (g == 0) {
+          mr[r] = ro[n][j];
+          mm[r] = m[n][j];
+          ml[r] = l[n][j];
+        }
+      }
     __syncthreads();
     const bool whole = u0 == 0 && u1 == nu;
     const int64_t pair = (int64_t)b * H + h;
     const int slot = u0 > 0 ? 0 : 1;   // continues an earlier CTA's part, or begins the pair
-    float* part = p.parts + ((size_t)blockIdx.x * 2 + slot) * C::kRows * (D + 2);
+    float* part = p.parts + ((size_t)blockIdx.x * 2 + slot) * C::kPart;
+    // running (O, its reference, sum, its reference) + another's
+    struct Acc {
+      float4 o;
+      float r, m, l;
+    };
+    auto join = [](Acc& x, float4 v, float r, float mw, float lw) {
+      if (mw == -INFINITY && lw == 0.0f) return;   // saw nothing
+      if (r > -INFINITY) {
+        const float R = fmaxf(x.r, r);
+        const float f0 = x.r == R ? 1.0f : ex2(x.r - R), f1 = r == R ? 1.0f : ex2(r - R);
+        x.r = R;
+        x.o.x = x.o.x * f0 + v.x * f1;
+        x.o.y = x.o.y * f0 + v.y * f1;
+        x.o.z = x.o.z * f0 + v.z * f1;
+        x.o.w = x.o.w * f0 + v.w * f1;
+      }
+      const float M = fmaxf(x.m, mw);
+      const float g0 = x.m == M ? 1.0f : ex2(x.m - M), g1 = mw == M ? 1.0f : ex2(mw - M);
+      x.m = M;
+      x.l = x.l * g0 + lw * g1;
+    };
     // 4 channels per thread
-    auto finish = [&](int r, int d4, float4 acc, float M, float Ls) {
+    auto finish = [&](int r, int d4, const Acc& x) {
       const int tok = r / p.G, hq = h * p.G + r % p.G;
-      const float inv = Ls > 0.0f ? 1.0f / Ls : (Ls == 0.0f ? 0.0f : Ls);   // NaN stays NaN
       const int64_t row = ((int64_t)b * T + tok) * a.n_heads + hq;
-      const __nv_bfloat162 y0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-      const __nv_bfloat162 y1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+      float f = 0.0f;                               // nothing seen: zeros
+      if (x.l != 0.0f) f = x.r == -INFINITY ? x.l : ex2(x.r - x.m) / x.l;   // a row of NaN scores: NaN
+      const __nv_bfloat162 y0 = __floats2bfloat162_rn(x.o.x * f, x.o.y * f);
+      const __nv_bfloat162 y1 = __floats2bfloat162_rn(x.o.z * f, x.o.w * f);
       uint2 y;
       y.x = *reinterpret_cast<const uint32_t*>(&y0);
       y.y = *reinterpret_cast<const uint32_t*>(&y1);
       *reinterpret_cast<uint2*>(a.out + row * D + d4) = y;
       if (d4 == 0) {
-        const float lse2 = Ls == 0.0f ? -INFINITY : M + log2f(Ls);
+        const float lse2 = x.l == 0.0f ? -INFINITY : (x.m == -INFINITY ? x.l : x.m + log2f(x.l));
         if (a.lse) a.lse[row] = lse2 * kLn2;
         if (WT) p.lse2[pair * C::kRows + r] = lse2;
       }
@@ -551,32 +661,17 @@ __global__ void __launch_bounds__(kDecThreads) decode_attn_kernel(const DecParam
       const int r = i / (D / 4), d4 = (i % (D / 4)) * 4;
       if (r >= p.rows) continue;
       const int w0 = r / (8 * NT), rr = r % (8 * NT);   // row tile; row inside it
-      float M = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < C::kGroups; ++k) M = fmaxf(M, mm[(k * RT + w0) * 8 * NT + rr]);
-      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      float Ls = 0.0f;
+      Acc x{make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY, -INFINITY, 0.0f};
 #pragma unroll
       for (int k = 0; k < C::kGroups; ++k) {
         const int wr = (k * RT + w0) * 8 * NT + rr;
-        const float mw = mm[wr];
-        if (mw == -INFINITY && ml[wr] == 0.0f) continue;
-        const float f = mw == M ? 1.0f : ex2(mw - M);
-        const float4 v = *reinterpret_cast<const float4*>(mo + (size_t)wr * D + d4);
-        acc.x = fmaf(v.x, f, acc.x);
-        acc.y = fmaf(v.y, f, acc.y);
-        acc.z = fmaf(v.z, f, acc.z);
-        acc.w = fmaf(v.w, f, acc.w);
-        Ls = fmaf(ml[wr], f, Ls);
+        join(x, *reinterpret_cast<const float4*>(mo + (size_t)wr * LD + d4), mr[wr], mm[wr], ml[wr]);
       }
       if (whole) {
-        finish(r, d4, acc, M, Ls);
+        finish(r, d4, x);
       } else {
-        *reinterpret_cast<float4*>(part + (size_t)r * D + d4) = acc;
-        if (d4 == 0) {
-          part[C::kRows * D + r] = M;
-          part[C::kRows * (D + 1) + r] = Ls;
-        }
+        *reinterpret_cast<float4*>(part + (size_t)r * D + d4) = x.o;
+        if (d4 == 0) *reinterpret_cast<float4*>(part + C::kRows * D + r * 4) = make_float4(x.r, x.m, x.l, 0.0f);
       }
     }
     if (!whole) {
@@ -596,24 +691,14 @@ __global__ void __launch_bounds__(kDecThreads) decode_attn_kernel(const DecParam
         for (int i = tid; i < C::kRows * (D / 4); i += kDecThreads) {
           const int r = i / (D / 4), d4 = (i % (D / 4)) * 4;
           if (r >= p.rows) continue;
-          float M = -INFINITY;
-          float Ls = 0.0f;
-          float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          Acc x{make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY, -INFINITY, 0.0f};
           for (int k = c0; k <= c1; ++k) {
-            const float* q = p.parts + ((size_t)k * 2 + (k == c0 ? 1 : 0)) * C::kRows * (D + 2);
-            const float mw = __ldcg(q + C::kRows * D + r), lw = __ldcg(q + C::kRows * (D + 1) + r);
+            const float* q = p.parts + ((size_t)k * 2 + (k == c0 ? 1 : 0)) * C::kPart;
             const float4 v = __ldcg(reinterpret_cast<const float4*>(q + (size_t)r * D + d4));
-            if (mw == -INFINITY && lw == 0.0f) continue;
-            const float Mn = fmaxf(M, mw);
-            const float f0 = M == Mn ? 1.0f : ex2(M - Mn), f1 = mw == Mn ? 1.0f : ex2(mw - Mn);
-            M = Mn;
-            acc.x = acc.x * f0 + v.x * f1;
-            acc.y = acc.y * f0 + v.y * f1;
-            acc.z = acc.z * f0 + v.z * f1;
-            acc.w = acc.w * f0 + v.w * f1;
-            Ls = Ls * f0 + lw * f1;
+            const float4 t = __ldcg(reinterpret_cast<const float4*>(q + C::kRows * D + r * 4));
+            join(x, v, t.x, t.y, t.z);
           }
-          finish(r, d4, acc, M, Ls);
+          finish(r, d4, x);
         }
       }
     }
@@ -657,7 +742,7 @@ size_t ws_layout(const moe_kv_cache& c, int n_seq, int n_new, int n_heads, int w
   w->n_cta = n_cta;
   const size_t pairs = (size_t)n_seq * c.n_kv_heads;
   w->parts = round_up(pairs * 4, 256);
-  w->lse2 = w->parts + round_up((size_t)n_cta * 2 * w->rows * (c.head_dim + 2) * 4, 256);
+  w->lse2 = w->parts + round_up((size_t)n_cta * 2 * w->rows * (c.head_dim + 4) * 4, 256);
   w->scores = w->lse2 + (weights ? round_up(pairs * w->rows * 4, 256) : 0);
   w->total = w->scores + (weights ? pairs * ((size_t)width * c.page_size) * w->rows * 4 : 0);
   if (w->total == 0) w->total = 256;
@@ -681,8 +766,8 @@ int launch_one(const DecParams& p, int n_cta, cudaStream_t s) {
 template <int D, bool WT>
 int launch_plan(const DecParams& p, const DecPlan& pl, int n_cta, cudaStream_t s) {
   if (pl.nt == 1) return launch_one<D, 1, 1, WT>(p, n_cta, s);
-  if (pl.rt == 1) return launch_one<D, 2, 1, WT>(p, n_cta, s);
-  if (pl.rt == 2) return launch_one<D, 2, 2, WT>(p, n_cta, s);
+  if (pl.rt == 1) return pl.nt == 2 ? launch_one<D, 2, 1, WT>(p, n_cta, s) : launch_one<D, 3, 1, WT>(p, n_cta, s);
+  if (pl.rt == 2) return pl.nt == 2 ? launch_one<D, 2, 2, WT>(p, n_cta, s) : launch_one<D, 3, 2, WT>(p, n_cta, s);
   return launch_one<D, 2, 4, WT>(p, n_cta, s);
 }
 
@@ -708,6 +793,7 @@ int launch_attn_decode(const DecodeArgs& a, const DeviceInfo& di, cudaStream_t s
   p.lse2 = reinterpret_cast<float*>(base + w.lse2);
   p.scores = reinterpret_cast<float*>(base + w.scores);
   p.cap = (int64_t)a.width * a.c.page_size;
+  p.log2_page = a.c.page_size == 16 ? 4 : a.c.page_size == 32 ? 5 : a.c.page_size == 64 ? 6 : 7;
   const DecPlan pl = dec_plan(p.rows);
   if (a.c.head_dim == 128) return wt ? launch_plan<128, true>(p, pl, w.n_cta, s) : launch_plan<128, false>(p, pl, w.n_cta, s);
   return wt ? launch_plan<64, true>(p, pl, w.n_cta, s) : launch_plan<64, false>(p, pl, w.n_cta, s);
