@@ -4,16 +4,18 @@
 // key/value head. What this asks of a kernel is many bytes in flight, few
 // instructions per byte, and work cut evenly whatever the lengths are.
 //
-// Work. All (sequence, key/value head) pairs are laid end to end in units of
-// kUnit positions; CTA c takes units [c W / N, (c + 1) W / N) of the W. Its
-// range is one or more segments, each a run of positions of one pair. A
-// segment that is a whole pair writes the output; any other writes its
-// unnormalised output, maximum and sum to the workspace, and the last CTA of
-// the pair to finish (a counter) joins them in order, so results do not depend
-// on who finishes when.
+// Work. All (sequence, key/value head) pairs are laid end to end in chunks of 32
+// positions; CTA c of N takes chunks [c W / N, (c + 1) W / N) of the W, its warps
+// equal parts of that, so work is even whatever the lengths are and a warp meets
+// no barrier on its way: one warp's change from pair to pair hides behind the
+// other warps' reads. A warp writes the output of a pair that lies in its part
+// whole; the (at most two) others' unnormalised output, references and sum go to
+// the workspace. When its warps are done the CTA joins theirs, and what still
+// reaches past the CTA is joined by the last CTA of the pair to finish (a
+// counter): always in order of position, so results do not depend on who is last.
 //
-// Inside a CTA the warps take chunks of 32 positions. A warp's next chunks are on
-// their way into its own part of shared memory by cp.async: no CTA barrier. Both
+// A warp's next chunks are on their way into its own part of shared memory by
+// cp.async. Both
 // products run on the e4m3 warp MMA (m16n8k32, exact products, fp32 sums), which
 // takes the cache's codes as they are: no conversion, 4096 multiplies a cycle and
 // SM (measured: one MMA per 1.07 cycles; f16's m16n8k16 takes 2.03, and its
@@ -38,13 +40,12 @@
 // The references of O and of the sum follow the maximum only when it passes them
 // by 2^30: fp32 has the range, and O is hardly ever rescaled.
 #include "attn.h"
+#include "f32x2.cuh"
 #include "fp8kv.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kDecWarps = 8;
-constexpr int kDecThreads = kDecWarps * 32;
 constexpr int kMaxSeqs = 4096;
 constexpr float kRaise = 30.0f;    // log2 by which a score may pass the reference
 constexpr int kChunk = 32;         // positions per warp step
@@ -75,7 +76,7 @@ struct DecParams {
   DecodeArgs a;
   int G, rows;              // query heads per kv head; query rows n_new * G
   unsigned* counter;        // [n_seq * n_kv]
-  float* parts;             // [n_cta][2][rows padded][D + 4]: output, then the references and the sum
+  float* parts;             // per CTA: 2 partial results, then 2 per warp: [rows][D] outputs, [rows][4] references and sum
   float* lse2;              // [n_seq * n_kv][rows padded] (weights)
   float* scores;            // [n_seq * n_kv][cap][rows padded] (weights)
   int64_t cap;
@@ -101,6 +102,13 @@ __device__ __forceinline__ void mma_fp8(float (&d)[4], const uint32_t (&a)[4], u
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// ... from 0
+__device__ __forceinline__ void mma_fp8_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ uint32_t movm(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -119,6 +127,13 @@ __device__ __forceinline__ void ldm_trans8(uint32_t (&r)[4], uint32_t addr) {
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return uint32_t(f32x2_to_e4m3x2(a, b)) | uint32_t(f32x2_to_e4m3x2(c, d)) << 16;
 }
+__device__ __forceinline__ float2 e4m3x2_f32x2(uint16_t c) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// 2^(s - 127) for a scale byte
+__device__ __forceinline__ float scale_value(uint32_t s) { return __uint_as_float(s ? s << 23 : 0x00400000u); }
 __device__ __forceinline__ float top4(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFF00000u); }
 // Does one of the word's four codes stand for NaN?
 __device__ __forceinline__ bool any_nan4(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
@@ -137,36 +152,39 @@ __device__ __forceinline__ int dec_length(const DecodeArgs& a, int b, bool* bad)
 // + 1, .. RT work on the same positions). WT: scores are kept for the weights.
 template <int D, int NT, int RT, bool WT>
 struct DecCfg {
-  static constexpr int kStages = D == 128 ? 3 : 6;
-  static constexpr int kGroups = kDecWarps / RT;         // chunks in work per CTA step
-  static constexpr int kUnit = kChunk * kGroups;         // positions per unit
+  // One block of rows takes 168 registers a thread, so 12 warps; more blocks
+  // take up to 255. The stages of all warps fill shared memory.
+  static constexpr int kWarps = NT == 1 ? 12 : 8;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kStages = 24 / kWarps * (D == 128 ? 1 : 2);
+  static constexpr int kGroups = kWarps / RT;            // warps with a part of their own
   static constexpr int kRows = 8 * NT * RT;              // padded query rows
   static constexpr uint32_t kKBytes = kChunk * D;
-  static constexpr uint32_t kVCol = kChunk * 16 + 64;    // 16 channels of a chunk; 64 bytes on, for the banks
-  static constexpr uint32_t kStageBytes = kKBytes + D / 16 * kVCol;
-  static constexpr uint32_t kRing = kDecWarps * kStages * kStageBytes;
-  static constexpr int kLd = D + 4;                      // row stride of the merge, floats
-  static constexpr uint32_t kMerge = kDecWarps * 8 * NT * (kLd + 3) * 4;   // reuses the ring
-  static constexpr uint32_t kPrefix = kRing > kMerge ? kRing : kMerge;
-  static constexpr uint32_t kSmem = kPrefix + (kMaxSeqs + 1) * 4;
-  static constexpr int kPart = kRows * (D + 4);          // floats of a partial result
+  static constexpr uint32_t kStageBytes = 2 * kKBytes;   // values as they come, 16-byte pieces exchanged within 128 bytes
+  static constexpr uint32_t kRing = kWarps * kStages * kStageBytes;
+  static constexpr uint32_t kSmem = kRing + (kMaxSeqs + 1) * 4;
+  static constexpr int kPartW = 8 * NT * (D + 4);        // floats of a warp's partial result
+  static constexpr int kPart = kRows * (D + 4);          // and of a CTA's
+  static constexpr int kPartsCta = 2 * kPart + 2 * kWarps * kPartW;
 };
 
 template <int D, int NT, int RT, bool WT>
-__global__ void __launch_bounds__(kDecThreads) decode_attn_kernel(const DecParams p) {
+__global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_attn_kernel(const DecParams p) {
   using C = DecCfg<D, NT, RT, WT>;
   constexpr int KS = D / 32;      // MMA steps over the channels
   constexpr int MT = D / 16;      // 16-channel blocks of the output
   constexpr int KC = D / 64;      // 16-byte pieces per lane and position
-  extern __shared__ __align__(128) uint8_t smem[];
-  int* prefix = reinterpret_cast<int*>(smem + C::kPrefix);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  int* prefix = reinterpret_cast<int*>(smem + C::kRing);
+  constexpr int kDecWarps = C::kWarps, kDecThreads = C::kThreads;
   __shared__ int s_scan[kDecWarps];
   __shared__ int s_last;
+  __shared__ int s_pair[2 * C::kGroups];   // pairs of the warps' partial results, -1: none
   const DecodeArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int H = a.c.n_kv_heads, P = a.c.page_size, B = a.n_seq, T = a.n_new;
 
-  // units of the sequences before each one (per kv head)
+  // chunks of the sequences before each one (per kv head)
   {
     bool bad = false;
     int before = 0;
@@ -175,7 +193,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_attn_kernel(const DecParam
       int n = 0;
       if (b < B) {
         const int L = dec_length(a, b, &bad);
-        n = L > 0 ? (L + C::kUnit - 1) / C::kUnit : 1;
+        n = L > 0 ? (L + kChunk - 1) / kChunk : 1;
       }
       int incl = n;
 #pragma unroll
@@ -199,106 +217,184 @@ __global__ void __launch_bounds__(kDecThreads) decode_attn_kernel(const DecParam
     if (bad && blockIdx.x == 0 && a.status) atomicOr(a.status, MOE_DEV_INDEX_OOB);
     __syncthreads();
   }
-  const int64_t W = (int64_t)prefix[B] * H, N = min((int64_t)gridDim.x, W);   // no CTA has an empty range
+  const int64_t W = (int64_t)prefix[B] * H;
+  const int64_t N = min((int64_t)gridDim.x, (W + C::kGroups - 1) / C::kGroups);   // no warp idles while others have two
   if (blockIdx.x >= N) return;
-  int64_t pos = blockIdx.x * W / N;
-  const int64_t end = (blockIdx.x + 1) * W / N;
+  const int64_t cta0 = blockIdx.x * W / N, cta1 = (blockIdx.x + 1) * W / N;
+  float* cta_parts = p.parts + (size_t)blockIdx.x * C::kPartsCta;
 
   const int rt = warp % RT, tg = warp / RT;
+  int64_t pos = cta0 + tg * (cta1 - cta0) / C::kGroups;
+  const int64_t end = cta0 + (tg + 1) * (cta1 - cta0) / C::kGroups;
   uint8_t* ring = smem + (size_t)warp * C::kStages * C::kStageBytes;
   const uint32_t ring_s = smem_addr(ring);
+  if (rt == 0 && lane < 2) s_pair[2 * tg + lane] = -1;
+  __syncwarp();
 
-  while (pos < end) {
-    // sequence of unit pos: the last b with prefix[b] H <= pos
+  // sequence of a chunk: the last b with prefix[b] H <= x
+  auto seq_of = [&](int64_t x) {
     int lo = 0, hi = B - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if ((int64_t)prefix[mid] * H <= pos) lo = mid; else hi = mid - 1;
+      if ((int64_t)prefix[mid] * H <= x) lo = mid; else hi = mid - 1;
     }
-    const int b = lo, nu = prefix[b + 1] - prefix[b];
-    const int64_t pair0 = (int64_t)prefix[b] * H;
-    const int h = int((pos - pair0) / nu), u0 = int((pos - pair0) % nu);
-    const int u1 = int(min((int64_t)nu, u0 + (end - pos)));
+    return lo;
+  };
+  // (O, its reference, sum, its reference) of 4 channels of a row, + another's
+  struct Acc {
+    float4 o;
+    float r, m, l;
+  };
+  auto join = [](Acc& x, float4 v, float r, float mw, float lw) {
+    if (mw == -INFINITY && lw == 0.0f) return;   // saw nothing
+    if (r > -INFINITY) {
+      const float R = fmaxf(x.r, r);
+      const float f0 = x.r == R ? 1.0f : ex2(x.r - R), f1 = r == R ? 1.0f : ex2(r - R);
+      x.r = R;
+      x.o.x = x.o.x * f0 + v.x * f1;
+      x.o.y = x.o.y * f0 + v.y * f1;
+      x.o.z = x.o.z * f0 + v.z * f1;
+      x.o.w = x.o.w * f0 + v.w * f1;
+    }
+    const float M = fmaxf(x.m, mw);
+    const float g0 = x.m == M ? 1.0f : ex2(x.m - M), g1 = mw == M ? 1.0f : ex2(mw - M);
+    x.m = M;
+    x.l = x.l * g0 + lw * g1;
+  };
+  // what O is multiplied with for the output
+  auto out_factor = [](float r, float m, float l) {
+    if (l == 0.0f) return 0.0f;                     // nothing seen: zeros
+    return r == -INFINITY ? l : ex2(r - m) / l;     // a row of NaN scores: NaN
+  };
+  auto write_lse = [&](int b, int h, int r, int64_t row, float m, float l) {
+    const float lse2 = l == 0.0f ? -INFINITY : (m == -INFINITY ? l : m + log2f(l));
+    if (a.lse) a.lse[row] = lse2 * kLn2;
+    if (WT) p.lse2[((int64_t)b * H + h) * C::kRows + r] = lse2;
+  };
+  auto finish = [&](int b, int h, int r, int d4, const Acc& x) {
+    const int64_t row = ((int64_t)b * T + r / p.G) * a.n_heads + h * p.G + r % p.G;
+    const float f = out_factor(x.r, x.m, x.l);
+    const __nv_bfloat162 y0 = __floats2bfloat162_rn(x.o.x * f, x.o.y * f);
+    const __nv_bfloat162 y1 = __floats2bfloat162_rn(x.o.z * f, x.o.w * f);
+    uint2 y;
+    y.x = *reinterpret_cast<const uint32_t*>(&y0);
+    y.y = *reinterpret_cast<const uint32_t*>(&y1);
+    *reinterpret_cast<uint2*>(a.out + row * D + d4) = y;
+    if (d4 == 0) write_lse(b, h, r, row, x.m, x.l);
+  };
+
+  // ---- this warp's chunks: fetched as one sequence, whatever pairs they belong to
+  const int n_my = int(end - pos);
+  // A chunk's halves A and B (16 positions each) are 16-row groups of the code
+  // arrays: group * 16 D bytes in; kNone past the sequence's end or where there
+  // is no page. Lane l looks up the l-th chunk of a block of 32, half a block
+  // ahead and in steps, so that no load is waited for.
+  constexpr uint32_t kNone = 0xFFFFFFFFu;
+  uint32_t grp_a = kNone, grp_b = kNone;                    // of the block being fetched
+  uint32_t sc = 0, no_a = 0, no_b = 0;                      // of the block in work: bytes kA kB vA vB; halves that are none
+  int nx_a = -1, nx_b = -1;                                 // next block: pages, then groups
+  uint32_t nx_h = 0, nx_slot = 0, nx_sc[4] = {0, 0, 0, 0};
+  const uint32_t gpp = P / 16;                              // groups per page and head
+  auto look_pages = [&](int i0) {
+    nx_a = nx_b = -2;                                       // nothing there, and nothing wrong
+    if (i0 + lane < n_my) {
+      const int64_t x = pos + i0 + lane;
+      const int b = seq_of(x), nu = prefix[b + 1] - prefix[b];
+      const int64_t rel = x - (int64_t)prefix[b] * H;
+      const int h = rel <= 0x7FFFFFFF ? int(rel) / nu : int(rel / nu);
+      const int t = int(rel - (int64_t)h * nu) * kChunk;
+      bool ignore = false;
+      const int L = dec_length(a, b, &ignore);
+      const int32_t* tab = a.table + (size_t)b * a.width + (t >> p.log2_page);
+      if (t < L) nx_a = max(__ldg(tab), -1);
+      if (t + 16 < L) nx_b = P == 16 ? max(__ldg(tab + 1), -1) : nx_a;
+      nx_h = h;
+      nx_slot = uint32_t(t & (P - 1)) >> 4;
+    }
+  };
+  auto look_scales = [&]() {
+    const bool bad = nx_a == -1 || nx_b == -1 || nx_a >= a.c.n_pages || nx_b >= a.c.n_pages;
+    if (bad && a.status) atomicOr(a.status, MOE_DEV_INDEX_OOB);
+    const uint32_t ra = uint32_t(nx_a) * H + nx_h, rb = uint32_t(nx_b) * H + nx_h;
+    const bool in_a = nx_a >= 0 && nx_a < a.c.n_pages, in_b = nx_b >= 0 && nx_b < a.c.n_pages;
+    if (in_a) {
+      nx_sc[0] = __ldg(a.c.k_scales + ra);
+      nx_sc[2] = __ldg(a.c.v_scales + ra);
+    }
+    if (in_b) {
+      nx_sc[1] = __ldg(a.c.k_scales + rb);
+      nx_sc[3] = __ldg(a.c.v_scales + rb);
+    }
+    nx_a = in_a ? int(ra * gpp + nx_slot) : -1;
+    nx_b = in_b ? int(rb * gpp + (P == 16 ? 0 : nx_slot + 1)) : -1;
+  };
+  auto issue = [&](int i) {
+    switch (i & 31) {
+      case 0:
+        grp_a = uint32_t(nx_a);
+        grp_b = uint32_t(nx_b);
+        break;
+      case 8: look_pages((i & ~31) + 32); break;
+      case 20: look_scales(); break;
+    }
+    const uint32_t ga = __shfl_sync(0xFFFFFFFFu, grp_a, i & 31), gb = __shfl_sync(0xFFFFFFFFu, grp_b, i & 31);
+    if (i < n_my) {
+      // Keys: lane (g, c) what it will use, at its own 16 bytes of each row of
+      // 512. Values: 512 consecutive bytes at a time, the 16-byte pieces of each
+      // 128 permuted so that 8 positions' pieces of the same channels lie in
+      // different banks (a permutation over more than 128 bytes would cut the
+      // L2 requests into 16-byte ones: measured, 1.5 times the traffic into the
+      // SM and 0.75 of the rate).
+      const uint32_t st = ring_s + (i % C::kStages) * C::kStageBytes;
+      const uint32_t kd = st + lane * 16;
+      const uint32_t vd = st + C::kKBytes + (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4);
+      const uint8_t* kl = static_cast<const uint8_t*>(a.c.k_codes) + (2 * g) * D + c * 16;
+      const uint8_t* vl = static_cast<const uint8_t*>(a.c.v_codes) + lane * 16;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t gr = half ? gb : ga;
+        if (gr == kNone) continue;
+        const uint8_t* ks = kl + (size_t)gr * (16 * D);
+        const uint8_t* vs = vl + (size_t)gr * (16 * D);
+#pragma unroll
+        for (int o = 0; o < 2; ++o)
+#pragma unroll
+          for (int j = 0; j < KC; ++j) cp_async16(kd + ((2 * half + o) * KC + j) * 512, ks + o * D + 64 * j);
+#pragma unroll
+        for (int n = 0; n < D / 32; ++n) {
+          const int k = half * (D / 32) + n;   // the odd ones: positions 4 .. 7 of 8
+          cp_async16((k & 1 ? vd ^ 64 : vd) + k * 512, vs + n * 512);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+  // The block in work follows the one being fetched by less than 32 chunks.
+  auto enter_block = [&]() {
+    no_a = __ballot_sync(0xFFFFFFFFu, grp_a == kNone);
+    no_b = __ballot_sync(0xFFFFFFFFu, grp_b == kNone);
+    const bool b_too = grp_b != kNone;   // else A's, so that the halves' scales are equal
+    sc = nx_sc[0] | nx_sc[b_too ? 1 : 0] << 8 | nx_sc[2] << 16 | nx_sc[b_too ? 3 : 2] << 24;
+  };
+
+  if (n_my > 0) {
+    look_pages(0);
+    look_scales();
+  }
+#pragma unroll 1
+  for (int j = 0; j < C::kStages - 1; ++j) issue(j);
+
+  int i = 0;
+  while (i < n_my) {
+    // ---- a pair, or the part of it that is this warp's
+    const int b = seq_of(pos + i), nu = prefix[b + 1] - prefix[b];
+    const int64_t rel = pos + i - (int64_t)prefix[b] * H;
+    const int h = rel <= 0x7FFFFFFF ? int(rel) / nu : int(rel / nu);
+    const int u0 = int(rel - (int64_t)h * nu), u1 = min(nu, u0 + (n_my - i));
+    const int i1 = i + (u1 - u0);
+    const int tbase = (u0 - i) * kChunk;     // chunk i's first position - 32 i
     bool ignore = false;
     const int L = dec_length(a, b, &ignore);
-    const int first = u0 * C::kUnit, last = min(L, u1 * C::kUnit);
-    const int n_my = last > first + tg * kChunk ? (last - first - tg * kChunk + C::kUnit - 1) / C::kUnit : 0;
-    const int32_t* table = a.table + (size_t)b * a.width;
-    const size_t head_bytes = (size_t)P * D, page_bytes = head_bytes * H;
-    const uint8_t* kbase = static_cast<const uint8_t*>(a.c.k_codes) + h * head_bytes;
-    const uint8_t* vbase = static_cast<const uint8_t*>(a.c.v_codes) + h * head_bytes;
-
-    auto gpos = [&](int i) { return first + (i * C::kGroups + tg) * kChunk; };
-    // Pages and scales of 32 chunks at a time, lane l those of the l-th: halves
-    // (16 positions) A and B, -1 outside the table or the cache. Scales of the
-    // chunks in work and of those being fetched.
-    int pg_a = -1, pg_b = -1;
-    uint32_t sc_next = 0, sc = 0;                                   // scale bytes kA kB vA vB
-    uint32_t bad_na = 0, bad_nb = 0, bad_a = 0, bad_b = 0;          // chunks whose half has no page
-    auto lookup = [&](int i0) {
-      const int i = i0 + lane;
-      const int t = gpos(i);
-      pg_a = pg_b = -1;
-      uint32_t w = 0;
-      bool oob_a = false, oob_b = false;
-      if (i < n_my) {
-        pg_a = __ldg(table + (t >> p.log2_page));
-        oob_a = pg_a < 0 || pg_a >= a.c.n_pages;
-        if (oob_a) pg_a = -1;
-        if (t + 16 < last) {
-          pg_b = P == 16 ? __ldg(table + (t >> 4) + 1) : pg_a;
-          oob_b = pg_b < 0 || pg_b >= a.c.n_pages;
-          if (oob_b) pg_b = -1;
-        }
-        if (pg_a >= 0) {
-          const size_t o = (size_t)pg_a * H + h;
-          w = __ldg(a.c.k_scales + o) | uint32_t(__ldg(a.c.v_scales + o)) << 16;
-        }
-        if (pg_b >= 0) {
-          const size_t o = (size_t)pg_b * H + h;
-          w |= uint32_t(__ldg(a.c.k_scales + o)) << 8 | uint32_t(__ldg(a.c.v_scales + o)) << 24;
-        } else {
-          w |= (w & 0x00FF00FFu) << 8;
-        }
-      }
-      sc_next = w;
-      bad_na = __ballot_sync(0xFFFFFFFFu, oob_a);
-      bad_nb = __ballot_sync(0xFFFFFFFFu, oob_b);
-      if ((bad_na | bad_nb) && lane == 0 && a.status) atomicOr(a.status, MOE_DEV_INDEX_OOB);
-    };
-    auto issue = [&](int i) {
-      if ((i & 31) == 0) lookup(i);
-      const int pa = __shfl_sync(0xFFFFFFFFu, pg_a, i & 31), pb = __shfl_sync(0xFFFFFFFFu, pg_b, i & 31);
-      if (i < n_my) {
-        const int slot = gpos(i) & (P - 1);
-        const size_t ra = (size_t)max(pa, 0) * page_bytes + slot * D;
-        const size_t rb = P == 16 ? (size_t)max(pb, 0) * page_bytes : ra + 16 * D;
-        const uint32_t st = ring_s + (i % C::kStages) * C::kStageBytes;
-        // keys: lane (g, c) what it will use, at its own 16 bytes of each row of 512
-        const uint32_t ko = (2 * g) * D + c * 16;
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          if ((mt ? pb : pa) < 0) continue;
-          const uint8_t* k0 = kbase + (mt ? rb : ra) + ko;
-#pragma unroll
-          for (int o = 0; o < 2; ++o)
-#pragma unroll
-            for (int j = 0; j < KC; ++j)
-              cp_async16(st + ((mt * 2 + o) * KC + j) * 512 + lane * 16, k0 + o * D + 64 * j);
-        }
-        // values: rows of D bytes, a lane 16 of them, to [16-channel block][position]
-        constexpr int LPR = D / 16, RPI = 32 / LPR;   // lanes per row, rows per instruction
-        const uint32_t vd = st + C::kKBytes + (lane % LPR) * C::kVCol + (lane / LPR) * 16;
-        const uint32_t vo = (lane / LPR) * D + (lane % LPR) * 16;
-#pragma unroll
-        for (int n = 0; n < kChunk / RPI; ++n) {
-          const bool second = n >= 16 / RPI;
-          if ((second ? pb : pa) < 0) continue;
-          cp_async16(vd + n * RPI * 16, vbase + (second ? rb + (n * RPI - 16) * D : ra + n * RPI * D) + vo);
-        }
-      }
-      cp_async_commit();
-    };
 
     // query rows -> B fragments (two e4m3 terms) and the factors that undo their scale
     uint32_t qf[2][KS][NT][2];
@@ -335,19 +431,23 @@ __global__ void __launch_bounds__(kDecThreads) decode_attn_kernel(const DecParam
         frexpf(top, &e);
         e -= 8;              // the row's largest value in [2^7, 2^8)
       }
+      // 2^-e in two factors; inf has no e4m3 code: the row is NaN, as a softmax of infinite scores is
+      const float f0 = top == INFINITY ? __int_as_float(0x7FC00000) : exp2i(-e / 2), f1 = exp2i(-e - (-e / 2));
 #pragma unroll
       for (int i = 0; i < KC * 16; i += 4) {
-        float t0[4], t1[4];
+        uint32_t w0 = 0;
+        float t1[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          // inf has no e4m3 code: the row is NaN, as softmax of infinite scores is
-          const float y = fabsf(x[i + k]) == INFINITY ? __int_as_float(0x7FC00000) : scale2(x[i + k], -e);
-          const uint32_t code = f32x2_to_e4m3x2(top4(y), 0.0f) & 0xFFu;
-          t0[k] = e4m3_is_nan(code) ? y : e4m3_to_f32(code);
-          t1[k] = (y - t0[k]) * 16.0f;
+        for (int k = 0; k < 4; k += 2) {
+          const float y0 = x[i + k] * f0 * f1, y1 = x[i + k + 1] * f0 * f1;
+          const uint16_t code = f32x2_to_e4m3x2(top4(y0), top4(y1));
+          const float2 t0 = e4m3x2_f32x2(code);   // not top4(y) where that is below the format's range
+          w0 |= uint32_t(code) << (8 * k);
+          t1[k] = (y0 - t0.x) * 16.0f;
+          t1[k + 1] = (y1 - t0.y) * 16.0f;
         }
         // 8 channels per MMA step: the first word is b0, the second b1
-        qf[0][i / 8][n][(i / 4) & 1] = e4m3x4(t0[0], t0[1], t0[2], t0[3]);
+        qf[0][i / 8][n][(i / 4) & 1] = w0;
         qf[1][i / 8][n][(i / 4) & 1] = e4m3x4(t1[0], t1[1], t1[2], t1[3]);
       }
 #pragma unroll
@@ -373,24 +473,18 @@ __global__ void __launch_bounds__(kDecThreads) decode_attn_kernel(const DecParam
       for (int j = 0; j < 2; ++j) m[n][j] = ro[n][j] = -INFINITY, l[n][j] = 0.0f;
 
 #pragma unroll 1
-    for (int j = 0; j < C::kStages - 1; ++j) {
-      issue(j);
-      if (j == 0) sc = sc_next, bad_a = bad_na, bad_b = bad_nb;
-    }
-
-#pragma unroll 1
-    for (int i = 0; i < n_my; ++i) {
+    for (; i < i1; ++i) {
       issue(i + C::kStages - 1);
-      if ((i & 31) == 0) sc = sc_next, bad_a = bad_na, bad_b = bad_nb;   // fetches are ahead by less than 32
+      if ((i & 31) == 0) enter_block();
       cp_async_wait<C::kStages - 1>();
       __syncwarp();
       const uint32_t w = __shfl_sync(0xFFFFFFFFu, sc, i & 31);
-      const int t0 = gpos(i);
+      const int t0 = tbase + i * kChunk;
       const int va = int(w >> 16 & 0xFFu), vb = int(w >> 24);
-      const bool no_a = bad_a >> (i & 31) & 1u, no_b = bad_b >> (i & 31) & 1u;
+      const bool none_a = no_a >> (i & 31) & 1u, none_b = no_b >> (i & 31) & 1u;
       const uint32_t st = (i % C::kStages) * C::kStageBytes;
       const uint4* kst = reinterpret_cast<const uint4*>(ring + st) + lane;
-      const bool full = !no_a && !no_b && t0 + kChunk <= L - T + 1;   // every row sees every position
+      const bool full = !none_a && !none_b && t0 + kChunk <= L - T + 1;   // every row sees every position
 
       uint32_t pf[3][NT][2];      // probabilities: terms, row blocks, halves
       float beta[NT][2];
@@ -402,31 +496,41 @@ __global__ void __launch_bounds__(kDecThreads) decode_attn_kernel(const DecParam
           for (int x = 0; x < 2; ++x)
 #pragma unroll
             for (int j = 0; j < KC; ++j) kw[mt][x][j] = kst[((mt * 2 + x) * KC + j) * 32];
-        const float kfa = exp2i(int(w & 0xFFu) - 127), kfb = exp2i(int(w >> 8 & 0xFFu) - 127);
+        const float kfa = scale_value(w & 0xFFu), kfb = scale_value(w >> 8 & 0xFFu);
         const float vfa = float(va - 127), vfb = float(vb - 127);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float s[2][4];
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt) {
-            float s1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[mt][j] = 0.0f;
+            float s1[4];
 #pragma unroll
             for (int j = 0; j < KC; ++j) {
               const uint4 x = kw[mt][0][j], y = kw[mt][1][j];
               const uint32_t a0[4] = {x.x, y.x, x.y, y.y}, a1[4] = {x.z, y.z, x.w, y.w};
-              mma_fp8(s[mt], a0, qf[0][2 * j][n][0], qf[0][2 * j][n][1]);
-              mma_fp8(s1, a0, qf[1][2 * j][n][0], qf[1][2 * j][n][1]);
+              if (j == 0) {
+                mma_fp8_zero(s[mt], a0, qf[0][0][n][0], qf[0][0][n][1]);
+                mma_fp8_zero(s1, a0, qf[1][0][n][0], qf[1][0][n][1]);
+              } else {
+                mma_fp8(s[mt], a0, qf[0][2 * j][n][0], qf[0][2 * j][n][1]);
+                mma_fp8(s1, a0, qf[1][2 * j][n][0], qf[1][2 * j][n][1]);
+              }
               mma_fp8(s[mt], a1, qf[0][2 * j + 1][n][0], qf[0][2 * j + 1][n][1]);
               mma_fp8(s1, a1, qf[1][2 * j + 1][n][0], qf[1][2 * j + 1][n][1]);
             }
             // s[mt][x]: position t0 + 16 mt + 2g + x / 2, row 2c + x % 2
+            const uint64_t f2 = mul2(pack2(qs[n][0], qs[n][1]), pack2(mt ? kfb : kfa, mt ? kfb : kfa));
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              s[mt][x] = fmaf(s1[x], 0.0625f, s[mt][x]) * (qs[n][x & 1] * (mt ? kfb : kfa));
-              if (!full && ((mt ? no_b : no_a) || t0 + 16 * mt + 2 * g + (x >> 1) >= vis[n][x & 1])) s[mt][x] = -INFINITY;
-            }
+            for (int x = 0; x < 4; x += 2)
+              unpack2(mul2(fma2(pack2(s1[x], s1[x + 1]), pack2(0.0625f, 0.0625f), pack2(s[mt][x], s[mt][x + 1])), f2),
+                      s[mt][x], s[mt][x + 1]);
+          }
+          if (!full) {
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                if ((mt ? none_b : none_a) || t0 + 16 * mt + 2 * g + (x >> 1) >= vis[n][x & 1]) s[mt][x] = -INFINITY;
           }
           if (WT) {
             float* sp = p.scores + (((int64_t)b * H + h) * p.cap + t0 + 2 * g) * C::kRows + (rt * NT + n) * 8 + 2 * c;
@@ -501,11 +605,15 @@ __global__ void __launch_bounds__(kDecThreads) decode_attn_kernel(const DecParam
           for (int mt = 0; mt < 2; ++mt) {
             float t0v[4], t1v[4], t2v[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
+            for (int x = 0; x < 4; x += 2) {
+              float r0, r1;
               t0v[x] = top4(pr[mt][x]);
-              const float r = pr[mt][x] - t0v[x];
-              t1v[x] = top4(r);
-              t2v[x] = r - t1v[x];
+              t0v[x + 1] = top4(pr[mt][x + 1]);
+              const uint64_t r = add2(pack2(pr[mt][x], pr[mt][x + 1]), pack2(-t0v[x], -t0v[x + 1]));
+              unpack2(r, r0, r1);
+              t1v[x] = top4(r0);
+              t1v[x + 1] = top4(r1);
+              unpack2(add2(r, pack2(-t1v[x], -t1v[x + 1])), t2v[x], t2v[x + 1]);
             }
             // row 2c's pair (positions 2g, 2g + 1), row 2c + 1's pair
             pf[0][n][mt] = movm(e4m3x4(t0v[0], t0v[2], t0v[1], t0v[3]));
@@ -516,37 +624,42 @@ __global__ void __launch_bounds__(kDecThreads) decode_attn_kernel(const DecParam
       }
 
       // output
-      const uint32_t va_s = ring_s + st + C::kKBytes + lane * 16;
+      // piece 0 of position `lane`; piece t is at this address ^ 16 t
+      const int line = D == 128 ? lane : lane >> 1;
+      const uint32_t va_s = ring_s + st + C::kKBytes + line * 128 +
+                            (((D == 128 ? 0 : (lane & 1) << 2) ^ (line & 7)) << 4);
       if (full) {
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
           uint32_t x[4];
-          ldm_trans8(x, va_s + t * C::kVCol);
+          ldm_trans8(x, va_s ^ (t << 4));
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            mma_fp8(d, x, pf[2][n][0], pf[2][n][1]);
+            float d[4];
+            mma_fp8_zero(d, x, pf[2][n][0], pf[2][n][1]);
             mma_fp8(d, x, pf[1][n][0], pf[1][n][1]);
             mma_fp8(d, x, pf[0][n][0], pf[0][n][1]);
+            const uint64_t b2 = pack2(beta[n][0], beta[n][1]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[t][n][j] = fmaf(d[j], beta[n][j & 1], o[t][n][j]);
+            for (int j = 0; j < 4; j += 2)
+              unpack2(fma2(pack2(d[j], d[j + 1]), b2, pack2(o[t][n][j], o[t][n][j + 1])), o[t][n][j], o[t][n][j + 1]);
           }
         }
       } else {
-        // Positions past the end hold anything: their codes are zeroed. A half
-        // without a page too. Where a NaN is visible to some tokens only (0 * NaN is NaN) every token takes
-        // a pass over what it sees.
+        // Positions past the end, and halves without a page, hold anything:
+        // their codes are zeroed. Where a NaN is visible to some tokens only (0
+        // * NaN is NaN) every token takes a pass over what it sees.
         auto keep4 = [&](int first_pos, int seen) {   // bytes of 4 consecutive positions
           const int k = seen - first_pos;
           return k >= 4 ? 0xFFFFFFFFu : (k <= 0 ? 0u : (1u << (8 * k)) - 1u);
         };
         bool poison = false;
         if (T > 1) {
-          const uint32_t ka = no_a ? 0u : keep4(t0 + 4 * c, L), kb = no_b ? 0u : keep4(t0 + 16 + 4 * c, L);
+          const uint32_t ka = none_a ? 0u : keep4(t0 + 4 * c, L), kb = none_b ? 0u : keep4(t0 + 16 + 4 * c, L);
 #pragma unroll 1
           for (int t = 0; t < MT; ++t) {
             uint32_t x[4];
-            ldm_trans8(x, va_s + t * C::kVCol);
+            ldm_trans8(x, va_s ^ (t << 4));
             poison |= any_nan4(x[0] & ka) || any_nan4(x[1] & ka) || any_nan4(x[2] & kb) || any_nan4(x[3] & kb);
           }
           poison = __any_sync(0xFFFFFFFFu, poison);
@@ -555,19 +668,19 @@ __global__ void __launch_bounds__(kDecThreads) decode_attn_kernel(const DecParam
 #pragma unroll 1
         for (int pass = 0; pass < n_pass; ++pass) {
           const int seen = poison ? L - T + pass + 1 : L;
-          const uint32_t ka = no_a ? 0u : keep4(t0 + 4 * c, seen), kb = no_b ? 0u : keep4(t0 + 16 + 4 * c, seen);
+          const uint32_t ka = none_a ? 0u : keep4(t0 + 4 * c, seen), kb = none_b ? 0u : keep4(t0 + 16 + 4 * c, seen);
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
             uint32_t x[4];
-            ldm_trans8(x, va_s + t * C::kVCol);
+            ldm_trans8(x, va_s ^ (t << 4));
             x[0] &= ka;
             x[1] &= ka;
             x[2] &= kb;
             x[3] &= kb;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-              mma_fp8(d, x, pf[2][n][0], pf[2][n][1]);
+              float d[4];
+              mma_fp8_zero(d, x, pf[2][n][0], pf[2][n][1]);
               mma_fp8(d, x, pf[1][n][0], pf[1][n][1]);
               mma_fp8(d, x, pf[0][n][0], pf[0][n][1]);
 #pragma unroll
@@ -579,131 +692,137 @@ __global__ void __launch_bounds__(kDecThreads) decode_attn_kernel(const DecParam
       }
       __syncwarp();   // every lane has read the stage before it is filled again
     }
-    cp_async_wait<0>();
-
-    // lanes' sums; the warp's partials to shared memory
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        l[n][j] += __shfl_xor_sync(0xFFFFFFFFu, l[n][j], 4);
-        l[n][j] += __shfl_xor_sync(0xFFFFFFFFu, l[n][j], 8);
-        l[n][j] += __shfl_xor_sync(0xFFFFFFFFu, l[n][j], 16);
-      }
-    __syncthreads();   // every warp has left the ring
-    constexpr int LD = C::kLd;
-    float* mo = reinterpret_cast<float*>(smem);                    // [warp][8 NT][LD]
-    float* mr = mo + kDecWarps * 8 * NT * LD;                      // [warp][8 NT]: reference of O
-    float* mm = mr + kDecWarps * 8 * NT;                           //   of the sum
-    float* ml = mm + kDecWarps * 8 * NT;                           //   the sum
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r = warp * 8 * NT + n * 8 + 2 * c + j;
-        float* row = mo + (size_t)r * LD + g;
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          row[16 * t] = o[t][n][j];
-          row[16 * t + 8] = o[t][n][j + 2];
-        }
-        if (g == 0) {
-          mr[r] = ro[n][j];
-          mm[r] = m[n][j];
-          ml[r] = l[n][j];
-        }
-      }
-    __syncthreads();
+    // ---- results
     const bool whole = u0 == 0 && u1 == nu;
-    const int64_t pair = (int64_t)b * H + h;
-    const int slot = u0 > 0 ? 0 : 1;   // continues an earlier CTA's part, or begins the pair
-    float* part = p.parts + ((size_t)blockIdx.x * 2 + slot) * C::kPart;
-    // running (O, its reference, sum, its reference) + another's
-    struct Acc {
-      float4 o;
-      float r, m, l;
-    };
-    auto join = [](Acc& x, float4 v, float r, float mw, float lw) {
-      if (mw == -INFINITY && lw == 0.0f) return;   // saw nothing
-      if (r > -INFINITY) {
-        const float R = fmaxf(x.r, r);
-        const float f0 = x.r == R ? 1.0f : ex2(x.r - R), f1 = r == R ? 1.0f : ex2(r - R);
-        x.r = R;
-        x.o.x = x.o.x * f0 + v.x * f1;
-        x.o.y = x.o.y * f0 + v.y * f1;
-        x.o.z = x.o.z * f0 + v.z * f1;
-        x.o.w = x.o.w * f0 + v.w * f1;
-      }
-      const float M = fmaxf(x.m, mw);
-      const float g0 = x.m == M ? 1.0f : ex2(x.m - M), g1 = mw == M ? 1.0f : ex2(mw - M);
-      x.m = M;
-      x.l = x.l * g0 + lw * g1;
-    };
-    // 4 channels per thread
-    auto finish = [&](int r, int d4, const Acc& x) {
-      const int tok = r / p.G, hq = h * p.G + r % p.G;
-      const int64_t row = ((int64_t)b * T + tok) * a.n_heads + hq;
-      float f = 0.0f;                               // nothing seen: zeros
-      if (x.l != 0.0f) f = x.r == -INFINITY ? x.l : ex2(x.r - x.m) / x.l;   // a row of NaN scores: NaN
-      const __nv_bfloat162 y0 = __floats2bfloat162_rn(x.o.x * f, x.o.y * f);
-      const __nv_bfloat162 y1 = __floats2bfloat162_rn(x.o.z * f, x.o.w * f);
-      uint2 y;
-      y.x = *reinterpret_cast<const uint32_t*>(&y0);
-      y.y = *reinterpret_cast<const uint32_t*>(&y1);
-      *reinterpret_cast<uint2*>(a.out + row * D + d4) = y;
-      if (d4 == 0) {
-        const float lse2 = x.l == 0.0f ? -INFINITY : (x.m == -INFINITY ? x.l : x.m + log2f(x.l));
-        if (a.lse) a.lse[row] = lse2 * kLn2;
-        if (WT) p.lse2[pair * C::kRows + r] = lse2;
-      }
-    };
-    for (int i = tid; i < C::kRows * (D / 4); i += kDecThreads) {
-      const int r = i / (D / 4), d4 = (i % (D / 4)) * 4;
-      if (r >= p.rows) continue;
-      const int w0 = r / (8 * NT), rr = r % (8 * NT);   // row tile; row inside it
-      Acc x{make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY, -INFINITY, 0.0f};
+    const int slot = u0 > 0 ? 0 : 1;   // continues an earlier warp's part, or begins the pair
+    float* part = cta_parts + 2 * C::kPart + (2 * warp + slot) * C::kPartW;
 #pragma unroll
-      for (int k = 0; k < C::kGroups; ++k) {
-        const int wr = (k * RT + w0) * 8 * NT + rr;
-        join(x, *reinterpret_cast<const float4*>(mo + (size_t)wr * LD + d4), mr[wr], mm[wr], ml[wr]);
-      }
-      if (whole) {
-        finish(r, d4, x);
-      } else {
-        *reinterpret_cast<float4*>(part + (size_t)r * D + d4) = x.o;
-        if (d4 == 0) *reinterpret_cast<float4*>(part + C::kRows * D + r * 4) = make_float4(x.r, x.m, x.l, 0.0f);
-      }
-    }
-    if (!whole) {
-      // CTAs of this pair: those whose ranges meet units [s0, s1)
-      const int64_t s0 = pair0 + (int64_t)h * nu, s1 = s0 + nu;
-      const int c0 = int(((s0 + 1) * N - 1) / W), c1 = int((s1 * N - 1) / W);
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const unsigned seen = atomicAdd(p.counter + pair, 1u);
-        s_last = seen == unsigned(c1 - c0);
-        if (s_last) p.counter[pair] = 0;
-      }
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        for (int i = tid; i < C::kRows * (D / 4); i += kDecThreads) {
-          const int r = i / (D / 4), d4 = (i % (D / 4)) * 4;
-          if (r >= p.rows) continue;
-          Acc x{make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY, -INFINITY, 0.0f};
-          for (int k = c0; k <= c1; ++k) {
-            const float* q = p.parts + ((size_t)k * 2 + (k == c0 ? 1 : 0)) * C::kPart;
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(q + (size_t)r * D + d4));
-            const float4 t = __ldcg(reinterpret_cast<const float4*>(q + C::kRows * D + r * 4));
-            join(x, v, t.x, t.y, t.z);
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float sum = l[n][j];
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 4);
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 8);
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
+        const int rr = n * 8 + 2 * c + j, r = rt * 8 * NT + rr;
+        if (!whole) {
+          // 8 lanes write 8 consecutive channels
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            part[rr * D + 16 * t + g] = o[t][n][j];
+            part[rr * D + 16 * t + g + 8] = o[t][n][j + 2];
           }
-          finish(r, d4, x);
+          if (g == 0)
+            *reinterpret_cast<float4*>(part + 8 * NT * D + rr * 4) = make_float4(ro[n][j], m[n][j], sum, 0.0f);
+        } else {
+          const bool have = r < p.rows;
+          const int64_t row = ((int64_t)b * T + r / p.G) * a.n_heads + h * p.G + r % p.G;
+          const float f = out_factor(ro[n][j], m[n][j], sum);
+          // lanes g and g ^ 1 swap, so that each holds two neighbouring channels
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            const float give = g & 1 ? o[t][n][j] : o[t][n][j + 2];
+            const float got = __shfl_xor_sync(0xFFFFFFFFu, give, 4);
+            const __nv_bfloat162 y = g & 1 ? __floats2bfloat162_rn(got * f, o[t][n][j + 2] * f)
+                                           : __floats2bfloat162_rn(o[t][n][j] * f, got * f);
+            if (have) *reinterpret_cast<__nv_bfloat162*>(a.out + row * D + 16 * t + (g & 1 ? g + 7 : g)) = y;
+          }
+          if (have && g == 0) write_lse(b, h, r, row, m[n][j], sum);
         }
       }
+    if (!whole && rt == 0 && lane == 0) s_pair[2 * tg + slot] = b * H + h;
+  }
+  cp_async_wait<0>();
+  __syncthreads();
+
+  // the warps' partial results, in order of position
+  for (int i = tid; i < C::kRows * (D / 4); i += kDecThreads) {
+    const int r = i / (D / 4), d4 = (i % (D / 4)) * 4;
+    if (r >= p.rows) continue;
+    const int w0 = r / (8 * NT), rr = r % (8 * NT);   // row tile; row inside it
+    int cur = -1;
+    Acc x;
+    auto flush = [&]() {
+      if (cur < 0) return;
+      const int b = cur / H, h = cur % H, nu = prefix[b + 1] - prefix[b];
+      const int64_t s0 = (int64_t)prefix[b] * H + (int64_t)h * nu;
+      if (s0 >= cta0 && s0 + nu <= cta1) {
+        finish(b, h, r, d4, x);
+      } else {
+        float* q = cta_parts + (s0 < cta0 ? 0 : C::kPart);
+        *reinterpret_cast<float4*>(q + r * D + d4) = x.o;
+        if (d4 == 0) *reinterpret_cast<float4*>(q + C::kRows * D + r * 4) = make_float4(x.r, x.m, x.l, 0.0f);
+      }
+    };
+    constexpr int KB = 8;   // loads in flight; slots without a result are read and passed over
+    for (int k0 = 0; k0 < 2 * C::kGroups; k0 += KB) {
+      float4 v[KB], t[KB];
+#pragma unroll
+      for (int k = 0; k < KB; ++k) {
+        const int ks = min(k0 + k, 2 * C::kGroups - 1);
+        const float* q = cta_parts + 2 * C::kPart + (2 * ((ks >> 1) * RT + w0) + (ks & 1)) * C::kPartW;
+        v[k] = *reinterpret_cast<const float4*>(q + rr * D + d4);
+        t[k] = *reinterpret_cast<const float4*>(q + 8 * NT * D + rr * 4);
+      }
+#pragma unroll
+      for (int k = 0; k < KB; ++k) {
+        const int pair = k0 + k < 2 * C::kGroups ? s_pair[k0 + k] : -1;
+        if (pair < 0) continue;
+        if (pair != cur) {
+          flush();
+          cur = pair;
+          x = Acc{make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY, -INFINITY, 0.0f};
+        }
+        join(x, v[k], t[k].x, t[k].y, t[k].z);
+      }
     }
-    __syncthreads();   // shared memory is used again
-    pos += u1 - u0;
+    flush();
+  }
+
+  // pairs that reach past this CTA: the one of its first chunk, the one of its last
+  for (int edge = 0; edge < 2; ++edge) {
+    const int64_t at = edge ? cta1 - 1 : cta0;
+    const int b = seq_of(at), nu = prefix[b + 1] - prefix[b];
+    const int64_t pair0 = (int64_t)prefix[b] * H;
+    const int h = int((at - pair0) / nu);
+    const int64_t s0 = pair0 + (int64_t)h * nu, s1 = s0 + nu;
+    if (s0 >= cta0 && s1 <= cta1) continue;
+    if (edge && s0 <= cta0) continue;     // the same pair again
+    // CTAs whose ranges meet chunks [s0, s1)
+    const int c0 = int(((s0 + 1) * N - 1) / W), c1 = int((s1 * N - 1) / W);
+    const int64_t pair = (int64_t)b * H + h;
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+      const unsigned seen = atomicAdd(p.counter + pair, 1u);
+      s_last = seen == unsigned(c1 - c0);
+      if (s_last) p.counter[pair] = 0;
+    }
+    __syncthreads();
+    if (s_last) {
+      __threadfence();
+      for (int i = tid; i < C::kRows * (D / 4); i += kDecThreads) {
+        const int r = i / (D / 4), d4 = (i % (D / 4)) * 4;
+        if (r >= p.rows) continue;
+        Acc x{make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY, -INFINITY, 0.0f};
+        constexpr int KB = 8;
+        for (int k0 = c0; k0 <= c1; k0 += KB) {
+          float4 v[KB], t[KB];
+#pragma unroll
+          for (int k = 0; k < KB; ++k) {
+            const int kc = min(k0 + k, c1);
+            const float* q = p.parts + (size_t)kc * C::kPartsCta + (kc == c0 ? C::kPart : 0);
+            v[k] = __ldcg(reinterpret_cast<const float4*>(q + r * D + d4));
+            t[k] = __ldcg(reinterpret_cast<const float4*>(q + C::kRows * D + r * 4));
+          }
+#pragma unroll
+          for (int k = 0; k < KB; ++k)
+            if (k0 + k <= c1) join(x, v[k], t[k].x, t[k].y, t[k].z);
+        }
+        finish(b, h, r, d4, x);
+      }
+    }
+    __syncthreads();
   }
 }
 
@@ -735,17 +854,22 @@ __global__ void __launch_bounds__(256) decode_weights_kernel(const DecParams p) 
   }
 }
 
-size_t ws_layout(const moe_kv_cache& c, int n_seq, int n_new, int n_heads, int width, bool weights, int n_cta, DecWs* w) {
+// CTAs that can have work, and the workspace's parts. Mirrors DecCfg.
+size_t ws_layout(const moe_kv_cache& c, int n_seq, int n_new, int n_heads, int width, bool weights, int sm_count, DecWs* w) {
   const int rows = n_new * (n_heads / c.n_kv_heads);
   const DecPlan pl = dec_plan(rows);
+  const int warps = pl.nt == 1 ? 12 : 8, groups = warps / pl.rt;
   w->rows = 8 * pl.nt * pl.rt;
-  w->n_cta = n_cta;
   const size_t pairs = (size_t)n_seq * c.n_kv_heads;
+  const size_t cap = (size_t)width * c.page_size;
+  const size_t chunks = pairs * (cap > 0 ? (cap + kChunk - 1) / kChunk : 1);
+  const size_t ctas = (chunks + groups - 1) / groups;
+  w->n_cta = int(ctas < (size_t)sm_count ? (ctas ? ctas : 1) : sm_count);
+  const size_t part = (size_t)(c.head_dim + 4) * 4 * (2 * w->rows + 2 * warps * 8 * pl.nt);
   w->parts = round_up(pairs * 4, 256);
-  w->lse2 = w->parts + round_up((size_t)n_cta * 2 * w->rows * (c.head_dim + 4) * 4, 256);
+  w->lse2 = w->parts + round_up(w->n_cta * part, 256);
   w->scores = w->lse2 + (weights ? round_up(pairs * w->rows * 4, 256) : 0);
-  w->total = w->scores + (weights ? pairs * ((size_t)width * c.page_size) * w->rows * 4 : 0);
-  if (w->total == 0) w->total = 256;
+  w->total = w->scores + (weights ? pairs * cap * w->rows * 4 : 0);
   return w->total;
 }
 
@@ -754,7 +878,7 @@ int launch_one(const DecParams& p, int n_cta, cudaStream_t s) {
   using C = DecCfg<D, NT, RT, WT>;
   MOE_CUDA_TRY(cudaFuncSetAttribute(decode_attn_kernel<D, NT, RT, WT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     int(C::kSmem)));
-  decode_attn_kernel<D, NT, RT, WT><<<n_cta, kDecThreads, C::kSmem, s>>>(p);
+  decode_attn_kernel<D, NT, RT, WT><<<n_cta, C::kThreads, C::kSmem, s>>>(p);
   int st = launch_status();
   if (st != MOE_OK || !WT) return st;
   if (p.cap == 0) return MOE_OK;
