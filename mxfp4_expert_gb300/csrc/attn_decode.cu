@@ -15,23 +15,24 @@
 // counter): always in order of position, so results do not depend on who is last.
 //
 // A warp's next chunks are on their way into its own part of shared memory by
-// cp.async. Both
-// products run on the e4m3 warp MMA (m16n8k32, exact products, fp32 sums), which
-// takes the cache's codes as they are: no conversion, 4096 multiplies a cycle and
-// SM (measured: one MMA per 1.07 cycles; f16's m16n8k16 takes 2.03, and its
-// conversions from E4M3 another 1.5 per 512 bytes).
-//   scores   S^T[pos][row] = K q^T. A bf16 query value is two e4m3 terms, t0 its
-//            first 4 significant bits, t1 the other 4 times 16, after a power
-//            of two per row that puts the row's largest in [2^7, 2^8): exact
-//            down to 2^-13 of that, then within 2^-22 of it. Lane (g, c) takes
-//            16-byte pieces of the positions 2g and 2g + 1 as consecutive
-//            words of its A fragment; q is laid out in the same order.
-//   output   O^T[d][row] = V^T P^T. ldmatrix transposes bytes on the way from
+// cp.async. Both products run on the f16 warp MMA (m16n8k16) with positions or
+// channels as its 16 rows and the query rows as its 8 columns, so up to 8 query
+// rows cost one column block. E4M3 converts to f16 exactly, two codes an
+// instruction (three instructions for four codes, with the move of the upper
+// pair). The e4m3 warp MMA was built too and is slower: on this architecture it
+// is expanded into the same conversions and f16 MMAs, and wants two terms of q
+// and three of the probabilities (520 instructions a chunk at head_dim 64).
+//   scores   S^T[pos][row] = K q^T: lane (g, c) takes 4 consecutive codes of a
+//            16-byte piece as its k = 2c, 2c+1, 2c+8, 2c+9 of one MMA; q is
+//            laid out in the same order, as f16 scaled by a power of two per
+//            row that puts the row's largest in [2^11, 2^12): exact down to
+//            2^-18 of that, then within 2^-37 of it.
+//   output   O^T[d][row] = V^T P^T: ldmatrix transposes bytes on the way from
 //            shared memory, so lane (g, c) holds 4 consecutive positions of
-//            channel g. The probabilities of a chunk, relative to the chunk's
-//            largest times 2^8, are three e4m3 terms (12 significant bits, and
-//            2^-18 of the largest); since S's rows were dealt 2g, 2g + 1, a
-//            movmatrix on byte pairs turns them into the B operand.
+//            channel g, and converts them to two k pairs. S's rows are dealt so
+//            that movmatrix turns its probabilities, as f16 pairs, into the B
+//            operand in the same order. They are relative to the chunk's
+//            largest times 2^12: 11 significant bits down to 2^-26 of it.
 //   joining  a chunk's product goes into O with an fp32 factor per row that
 //            holds its reference and its page's value scale. A page of 16
 //            positions shares its chunk with another: the probabilities then
@@ -96,18 +97,35 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ void mma_fp8(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// codes in the low or high half of a word -> f16 pair
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}\n" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_f16x2_hi(uint32_t w) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}\n" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // ... from 0
-__device__ __forceinline__ void mma_fp8_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ uint32_t f16x2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ uint32_t movm(uint32_t x) {
   uint32_t r;
@@ -123,18 +141,8 @@ __device__ __forceinline__ void ldm_trans8(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
-// e4m3 pairs (a, b) and (c, d) -> one word, a in the lowest byte
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  return uint32_t(f32x2_to_e4m3x2(a, b)) | uint32_t(f32x2_to_e4m3x2(c, d)) << 16;
-}
-__device__ __forceinline__ float2 e4m3x2_f32x2(uint16_t c) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
 // 2^(s - 127) for a scale byte
 __device__ __forceinline__ float scale_value(uint32_t s) { return __uint_as_float(s ? s << 23 : 0x00400000u); }
-__device__ __forceinline__ float top4(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFF00000u); }
 // Does one of the word's four codes stand for NaN?
 __device__ __forceinline__ bool any_nan4(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
@@ -171,7 +179,7 @@ struct DecCfg {
 template <int D, int NT, int RT, bool WT>
 __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_attn_kernel(const DecParams p) {
   using C = DecCfg<D, NT, RT, WT>;
-  constexpr int KS = D / 32;      // MMA steps over the channels
+  constexpr int KS = D / 16;      // MMA steps over the channels
   constexpr int MT = D / 16;      // 16-channel blocks of the output
   constexpr int KC = D / 64;      // 16-byte pieces per lane and position
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -348,7 +356,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
       const uint32_t st = ring_s + (i % C::kStages) * C::kStageBytes;
       const uint32_t kd = st + lane * 16;
       const uint32_t vd = st + C::kKBytes + (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4);
-      const uint8_t* kl = static_cast<const uint8_t*>(a.c.k_codes) + (2 * g) * D + c * 16;
+      const uint8_t* kl = static_cast<const uint8_t*>(a.c.k_codes) + (4 * (g >> 1) + (g & 1)) * D + c * 16;
       const uint8_t* vl = static_cast<const uint8_t*>(a.c.v_codes) + lane * 16;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -359,7 +367,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
 #pragma unroll
         for (int o = 0; o < 2; ++o)
 #pragma unroll
-          for (int j = 0; j < KC; ++j) cp_async16(kd + ((2 * half + o) * KC + j) * 512, ks + o * D + 64 * j);
+          for (int j = 0; j < KC; ++j) cp_async16(kd + ((2 * half + o) * KC + j) * 512, ks + 2 * o * D + 64 * j);
 #pragma unroll
         for (int n = 0; n < D / 32; ++n) {
           const int k = half * (D / 32) + n;   // the odd ones: positions 4 .. 7 of 8
@@ -396,8 +404,8 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
     bool ignore = false;
     const int L = dec_length(a, b, &ignore);
 
-    // query rows -> B fragments (two e4m3 terms) and the factors that undo their scale
-    uint32_t qf[2][KS][NT][2];
+    // query rows -> B fragments and the factors that undo their scale
+    uint32_t qf[KS][NT][2];
     float qs[NT][2];         // of rows 2c, 2c+1 of each block: 2^e scale log2(e)
     int vis[NT][2];          // positions that those rows see
 #pragma unroll
@@ -429,27 +437,12 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
       int e = 0;
       if (top > 0.0f && top < INFINITY) {
         frexpf(top, &e);
-        e -= 8;              // the row's largest value in [2^7, 2^8)
+        e -= 12;             // the row's largest value in [2^11, 2^12)
       }
-      // 2^-e in two factors; inf has no e4m3 code: the row is NaN, as a softmax of infinite scores is
-      const float f0 = top == INFINITY ? __int_as_float(0x7FC00000) : exp2i(-e / 2), f1 = exp2i(-e - (-e / 2));
+      const float f0 = exp2i(-e / 2), f1 = exp2i(-e - (-e / 2));   // 2^-e, which itself may leave fp32's range
 #pragma unroll
-      for (int i = 0; i < KC * 16; i += 4) {
-        uint32_t w0 = 0;
-        float t1[4];
-#pragma unroll
-        for (int k = 0; k < 4; k += 2) {
-          const float y0 = x[i + k] * f0 * f1, y1 = x[i + k + 1] * f0 * f1;
-          const uint16_t code = f32x2_to_e4m3x2(top4(y0), top4(y1));
-          const float2 t0 = e4m3x2_f32x2(code);   // not top4(y) where that is below the format's range
-          w0 |= uint32_t(code) << (8 * k);
-          t1[k] = (y0 - t0.x) * 16.0f;
-          t1[k + 1] = (y1 - t0.y) * 16.0f;
-        }
-        // 8 channels per MMA step: the first word is b0, the second b1
-        qf[0][i / 8][n][(i / 4) & 1] = w0;
-        qf[1][i / 8][n][(i / 4) & 1] = e4m3x4(t1[0], t1[1], t1[2], t1[3]);
-      }
+      for (int i = 0; i < KC * 16; i += 2)
+        qf[i / 4][n][(i / 2) & 1] = f16x2_bits(x[i] * f0 * f1, x[i + 1] * f0 * f1);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int er = __shfl_sync(0xFFFFFFFFu, e, (2 * c + j) * 4);
@@ -486,66 +479,66 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
       const uint4* kst = reinterpret_cast<const uint4*>(ring + st) + lane;
       const bool full = !none_a && !none_b && t0 + kChunk <= L - T + 1;   // every row sees every position
 
-      uint32_t pf[3][NT][2];      // probabilities: terms, row blocks, halves
+      // scores: s[mt][n][x] is position t0 + 16 mt + 4 (g / 2) + g % 2 + 2 (x / 2), row 2c + x % 2
+      float s[2][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int j = 0; j < KC; ++j) {
+          const uint4 x = kst[(mt * 2 * KC + j) * 32], y = kst[((mt * 2 + 1) * KC + j) * 32];
+          const uint32_t wx[4] = {x.x, x.y, x.z, x.w}, wy[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t a0 = e4m3x2_f16x2(wx[k]), a1 = e4m3x2_f16x2(wy[k]);
+            const uint32_t a2 = e4m3x2_f16x2_hi(wx[k]), a3 = e4m3x2_f16x2_hi(wy[k]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const uint32_t b0 = qf[4 * j + k][n][0], b1 = qf[4 * j + k][n][1];
+              if (j == 0 && k == 0)
+                mma_f16_zero(s[mt][n], a0, a1, a2, a3, b0, b1);
+              else
+                mma_f16(s[mt][n], a0, a1, a2, a3, b0, b1);
+            }
+          }
+        }
+
+      uint32_t pf[NT][4];         // probabilities: B fragments of the two halves
       float beta[NT][2];
-      {
-        uint4 kw[2][2][KC];
+      const float kfa = scale_value(w & 0xFFu), kfb = scale_value(w >> 8 & 0xFFu);
+      const float vfa = float(va - 127), vfb = float(vb - 127);
+      const int p0 = t0 + 4 * (g >> 1) + (g & 1);
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int j = 0; j < KC; ++j) kw[mt][x][j] = kst[((mt * 2 + x) * KC + j) * 32];
-        const float kfa = scale_value(w & 0xFFu), kfb = scale_value(w >> 8 & 0xFFu);
-        const float vfa = float(va - 127), vfb = float(vb - 127);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float s[2][4];
+      for (int n = 0; n < NT; ++n) {
+        {
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt) {
-            float s1[4];
-#pragma unroll
-            for (int j = 0; j < KC; ++j) {
-              const uint4 x = kw[mt][0][j], y = kw[mt][1][j];
-              const uint32_t a0[4] = {x.x, y.x, x.y, y.y}, a1[4] = {x.z, y.z, x.w, y.w};
-              if (j == 0) {
-                mma_fp8_zero(s[mt], a0, qf[0][0][n][0], qf[0][0][n][1]);
-                mma_fp8_zero(s1, a0, qf[1][0][n][0], qf[1][0][n][1]);
-              } else {
-                mma_fp8(s[mt], a0, qf[0][2 * j][n][0], qf[0][2 * j][n][1]);
-                mma_fp8(s1, a0, qf[1][2 * j][n][0], qf[1][2 * j][n][1]);
-              }
-              mma_fp8(s[mt], a1, qf[0][2 * j + 1][n][0], qf[0][2 * j + 1][n][1]);
-              mma_fp8(s1, a1, qf[1][2 * j + 1][n][0], qf[1][2 * j + 1][n][1]);
-            }
-            // s[mt][x]: position t0 + 16 mt + 2g + x / 2, row 2c + x % 2
             const uint64_t f2 = mul2(pack2(qs[n][0], qs[n][1]), pack2(mt ? kfb : kfa, mt ? kfb : kfa));
 #pragma unroll
             for (int x = 0; x < 4; x += 2)
-              unpack2(mul2(fma2(pack2(s1[x], s1[x + 1]), pack2(0.0625f, 0.0625f), pack2(s[mt][x], s[mt][x + 1])), f2),
-                      s[mt][x], s[mt][x + 1]);
+              unpack2(mul2(pack2(s[mt][n][x], s[mt][n][x + 1]), f2), s[mt][n][x], s[mt][n][x + 1]);
           }
           if (!full) {
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
               for (int x = 0; x < 4; ++x)
-                if ((mt ? none_b : none_a) || t0 + 16 * mt + 2 * g + (x >> 1) >= vis[n][x & 1]) s[mt][x] = -INFINITY;
+                if ((mt ? none_b : none_a) || p0 + 16 * mt + 2 * (x >> 1) >= vis[n][x & 1]) s[mt][n][x] = -INFINITY;
           }
           if (WT) {
-            float* sp = p.scores + (((int64_t)b * H + h) * p.cap + t0 + 2 * g) * C::kRows + (rt * NT + n) * 8 + 2 * c;
+            float* sp = p.scores + (((int64_t)b * H + h) * p.cap + p0) * C::kRows + (rt * NT + n) * 8 + 2 * c;
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
               for (int x = 0; x < 2; ++x)
-                if (t0 + 16 * mt + 2 * g + x < L)
-                  *reinterpret_cast<float2*>(sp + (16 * mt + x) * C::kRows) = make_float2(s[mt][2 * x], s[mt][2 * x + 1]);
+                if (p0 + 16 * mt + 2 * x < L)
+                  *reinterpret_cast<float2*>(sp + (16 * mt + 2 * x) * C::kRows) =
+                      make_float2(s[mt][n][2 * x], s[mt][n][2 * x + 1]);
           }
           // the chunk's largest score, and largest score times value scale
           float us[2], ms[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float xa = fmaxf(s[0][j], s[0][j + 2]), xb = fmaxf(s[1][j], s[1][j + 2]);
+            const float xa = fmaxf(s[0][n][j], s[0][n][j + 2]), xb = fmaxf(s[1][n][j], s[1][n][j + 2]);
             us[j] = fmaxf(xa + vfa, xb + vfb);
             us[j] = fmaxf(us[j], __shfl_xor_sync(0xFFFFFFFFu, us[j], 4));
             us[j] = fmaxf(us[j], __shfl_xor_sync(0xFFFFFFFFu, us[j], 8));
@@ -580,45 +573,31 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
               }
             }
           }
-          // probabilities times 2^8 over the chunk's largest, in three terms
+          // probabilities times 2^12 over the chunk's largest
           float pr[2][4];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const bool none = us[j] == -INFINITY;
-            const float ref = none ? 0.0f : 8.0f - us[j];
-            beta[n][j] = none ? 0.0f : ex2(us[j] - 8.0f - ro[n][j]);
+            const float ref = none ? 0.0f : 12.0f - us[j];
+            beta[n][j] = none ? 0.0f : ex2(us[j] - 12.0f - ro[n][j]);
 #pragma unroll
             for (int x = j; x < 4; x += 2) {
-              pr[0][x] = ex2(s[0][x] + (vfa + ref));
-              pr[1][x] = ex2(s[1][x] + (vfb + ref));
+              pr[0][x] = ex2(s[0][n][x] + (vfa + ref));
+              pr[1][x] = ex2(s[1][n][x] + (vfb + ref));
             }
             if (va == vb) {
               const float sum = (pr[0][j] + pr[0][j + 2]) + (pr[1][j] + pr[1][j + 2]);
               // a row of NaN scores has no largest one, but must not pass for empty
-              l[n][j] += none ? sum : sum * ex2(us[j] - 8.0f - vfa - m[n][j]);
+              l[n][j] += none ? sum : sum * ex2(us[j] - 12.0f - vfa - m[n][j]);
             } else {
               const float mr = m[n][j] == -INFINITY ? 0.0f : m[n][j];
-              l[n][j] += (ex2(s[0][j] - mr) + ex2(s[0][j + 2] - mr)) + (ex2(s[1][j] - mr) + ex2(s[1][j + 2] - mr));
+              l[n][j] += (ex2(s[0][n][j] - mr) + ex2(s[0][n][j + 2] - mr)) + (ex2(s[1][n][j] - mr) + ex2(s[1][n][j + 2] - mr));
             }
           }
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt) {
-            float t0v[4], t1v[4], t2v[4];
-#pragma unroll
-            for (int x = 0; x < 4; x += 2) {
-              float r0, r1;
-              t0v[x] = top4(pr[mt][x]);
-              t0v[x + 1] = top4(pr[mt][x + 1]);
-              const uint64_t r = add2(pack2(pr[mt][x], pr[mt][x + 1]), pack2(-t0v[x], -t0v[x + 1]));
-              unpack2(r, r0, r1);
-              t1v[x] = top4(r0);
-              t1v[x + 1] = top4(r1);
-              unpack2(add2(r, pack2(-t1v[x], -t1v[x + 1])), t2v[x], t2v[x + 1]);
-            }
-            // row 2c's pair (positions 2g, 2g + 1), row 2c + 1's pair
-            pf[0][n][mt] = movm(e4m3x4(t0v[0], t0v[2], t0v[1], t0v[3]));
-            pf[1][n][mt] = movm(e4m3x4(t1v[0], t1v[2], t1v[1], t1v[3]));
-            pf[2][n][mt] = movm(e4m3x4(t2v[0], t2v[2], t2v[1], t2v[3]));
+            pf[n][2 * mt] = movm(f16x2_bits(pr[mt][0], pr[mt][1]));
+            pf[n][2 * mt + 1] = movm(f16x2_bits(pr[mt][2], pr[mt][3]));
           }
         }
       }
@@ -633,12 +612,16 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
         for (int t = 0; t < MT; ++t) {
           uint32_t x[4];
           ldm_trans8(x, va_s ^ (t << 4));
+          // tokens 4c, 4c+1 and 4c+2, 4c+3 of each half: an MMA's two k pairs
+          const uint32_t a0 = e4m3x2_f16x2(x[0]), a1 = e4m3x2_f16x2(x[1]), a2 = e4m3x2_f16x2_hi(x[0]),
+                         a3 = e4m3x2_f16x2_hi(x[1]);
+          const uint32_t e0 = e4m3x2_f16x2(x[2]), e1 = e4m3x2_f16x2(x[3]), e2 = e4m3x2_f16x2_hi(x[2]),
+                         e3 = e4m3x2_f16x2_hi(x[3]);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             float d[4];
-            mma_fp8_zero(d, x, pf[2][n][0], pf[2][n][1]);
-            mma_fp8(d, x, pf[1][n][0], pf[1][n][1]);
-            mma_fp8(d, x, pf[0][n][0], pf[0][n][1]);
+            mma_f16_zero(d, a0, a1, a2, a3, pf[n][0], pf[n][1]);
+            mma_f16(d, e0, e1, e2, e3, pf[n][2], pf[n][3]);
             const uint64_t b2 = pack2(beta[n][0], beta[n][1]);
 #pragma unroll
             for (int j = 0; j < 4; j += 2)
@@ -677,12 +660,15 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
             x[1] &= ka;
             x[2] &= kb;
             x[3] &= kb;
+            const uint32_t a0 = e4m3x2_f16x2(x[0]), a1 = e4m3x2_f16x2(x[1]), a2 = e4m3x2_f16x2_hi(x[0]),
+                           a3 = e4m3x2_f16x2_hi(x[1]);
+            const uint32_t e0 = e4m3x2_f16x2(x[2]), e1 = e4m3x2_f16x2(x[3]), e2 = e4m3x2_f16x2_hi(x[2]),
+                           e3 = e4m3x2_f16x2_hi(x[3]);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               float d[4];
-              mma_fp8_zero(d, x, pf[2][n][0], pf[2][n][1]);
-              mma_fp8(d, x, pf[1][n][0], pf[1][n][1]);
-              mma_fp8(d, x, pf[0][n][0], pf[0][n][1]);
+              mma_f16_zero(d, a0, a1, a2, a3, pf[n][0], pf[n][1]);
+              mma_f16(d, e0, e1, e2, e3, pf[n][2], pf[n][3]);
 #pragma unroll
               for (int j = 0; j < 4; ++j)
                 if (!poison || vis[n][j & 1] == seen) o[t][n][j] = fmaf(d[j], beta[n][j & 1], o[t][n][j]);
