@@ -141,6 +141,8 @@ __device__ __forceinline__ void ldm_trans8(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
+// 2^e, -126 <= e <= 127
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
 // 2^(s - 127) for a scale byte
 __device__ __forceinline__ float scale_value(uint32_t s) { return __uint_as_float(s ? s << 23 : 0x00400000u); }
 // Does one of the word's four codes stand for NaN?
@@ -156,6 +158,11 @@ __device__ __forceinline__ int dec_length(const DecodeArgs& a, int b, bool* bad)
   return l;
 }
 
+// A pair that this CTA joins, and the CTAs that have parts of it.
+struct Edge {
+  int b, h, c0, c1;
+};
+
 // D: head_dim. NT: blocks of 8 query rows per warp. RT: row tiles (warps w, w
 // + 1, .. RT work on the same positions). WT: scores are kept for the weights.
 template <int D, int NT, int RT, bool WT>
@@ -170,7 +177,8 @@ struct DecCfg {
   static constexpr uint32_t kKBytes = kChunk * D;
   static constexpr uint32_t kStageBytes = 2 * kKBytes;   // values as they come, 16-byte pieces exchanged within 128 bytes
   static constexpr uint32_t kRing = kWarps * kStages * kStageBytes;
-  static constexpr uint32_t kSmem = kRing + (kMaxSeqs + 1) * 4;
+  static constexpr uint32_t kSmem = kRing + (2 * kMaxSeqs + 1) * 4;   // ring, prefix sums, lengths
+  static_assert(kSmem + 1024 <= 232448, "shared memory");
   static constexpr int kPartW = 8 * NT * (D + 4);        // floats of a warp's partial result
   static constexpr int kPart = kRows * (D + 4);          // and of a CTA's
   static constexpr int kPartsCta = 2 * kPart + 2 * kWarps * kPartW;
@@ -184,9 +192,10 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
   constexpr int KC = D / 64;      // 16-byte pieces per lane and position
   extern __shared__ __align__(1024) uint8_t smem[];
   int* prefix = reinterpret_cast<int*>(smem + C::kRing);
+  int* lens = prefix + kMaxSeqs + 1;
   constexpr int kDecWarps = C::kWarps, kDecThreads = C::kThreads;
   __shared__ int s_scan[kDecWarps];
-  __shared__ int s_last;
+  __shared__ Edge s_edge[2];
   __shared__ int s_pair[2 * C::kGroups];   // pairs of the warps' partial results, -1: none
   const DecodeArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
@@ -201,6 +210,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
       int n = 0;
       if (b < B) {
         const int L = dec_length(a, b, &bad);
+        lens[b] = L;
         n = L > 0 ? (L + kChunk - 1) / kChunk : 1;
       }
       int incl = n;
@@ -311,8 +321,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
       const int64_t rel = x - (int64_t)prefix[b] * H;
       const int h = rel <= 0x7FFFFFFF ? int(rel) / nu : int(rel / nu);
       const int t = int(rel - (int64_t)h * nu) * kChunk;
-      bool ignore = false;
-      const int L = dec_length(a, b, &ignore);
+      const int L = lens[b];
       const int32_t* tab = a.table + (size_t)b * a.width + (t >> p.log2_page);
       if (t < L) nx_a = max(__ldg(tab), -1);
       if (t + 16 < L) nx_b = P == 16 ? max(__ldg(tab + 1), -1) : nx_a;
@@ -385,8 +394,26 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
     sc = nx_sc[0] | nx_sc[b_too ? 1 : 0] << 8 | nx_sc[2] << 16 | nx_sc[b_too ? 3 : 2] << 24;
   };
 
+  // a pair's query rows: lane (g, c) the channels 64 j + 16 c + [0, 16) of row g of each block
+  uint4 qw[NT][2 * KC];
+  auto load_q = [&](int x) {
+    const int b = seq_of(pos + x), nu = prefix[b + 1] - prefix[b];
+    const int64_t rel = pos + x - (int64_t)prefix[b] * H;
+    const int h = rel <= 0x7FFFFFFF ? int(rel) / nu : int(rel / nu);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int r = (rt * NT + n) * 8 + g;
+      const __nv_bfloat16* q = a.q + ((int64_t)b * T + r / p.G) * a.q_ts + (int64_t)(h * p.G + r % p.G) * a.q_hs;
+#pragma unroll
+      for (int j = 0; j < 2 * KC; ++j)
+        qw[n][j] = r < p.rows ? *reinterpret_cast<const uint4*>(q + 64 * (j >> 1) + 16 * c + 8 * (j & 1))
+                              : make_uint4(0, 0, 0, 0);
+    }
+  };
+
   if (n_my > 0) {
     look_pages(0);
+    load_q(0);
     look_scales();
   }
 #pragma unroll 1
@@ -401,8 +428,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
     const int u0 = int(rel - (int64_t)h * nu), u1 = min(nu, u0 + (n_my - i));
     const int i1 = i + (u1 - u0);
     const int tbase = (u0 - i) * kChunk;     // chunk i's first position - 32 i
-    bool ignore = false;
-    const int L = dec_length(a, b, &ignore);
+    const int L = lens[b];
 
     // query rows -> B fragments and the factors that undo their scale
     uint32_t qf[KS][NT][2];
@@ -410,36 +436,24 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
     int vis[NT][2];          // positions that those rows see
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int r = (rt * NT + n) * 8 + g;
       float x[KC * 16];
-      float top = 0.0f;
-      if (r < p.rows) {
-        const __nv_bfloat16* q = a.q + ((int64_t)b * T + r / p.G) * a.q_ts + (int64_t)(h * p.G + r % p.G) * a.q_hs;
+      uint32_t top = 0;      // the row's largest magnitude, as bf16 bits
 #pragma unroll
-        for (int j = 0; j < KC; ++j) {
-          const uint4 v0 = *reinterpret_cast<const uint4*>(q + 64 * j + 16 * c);
-          const uint4 v1 = *reinterpret_cast<const uint4*>(q + 64 * j + 16 * c + 8);
-          const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+      for (int j = 0; j < 2 * KC; ++j) {
+        const uint32_t w[4] = {qw[n][j].x, qw[n][j].y, qw[n][j].z, qw[n][j].w};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x[16 * j + 2 * i] = bf16_lo(w[i]);
-            x[16 * j + 2 * i + 1] = bf16_hi(w[i]);
-          }
+        for (int i = 0; i < 4; ++i) {
+          top = max(top, max(w[i] & 0x7FFFu, w[i] >> 16 & 0x7FFFu));
+          x[8 * j + 2 * i] = bf16_lo(w[i]);
+          x[8 * j + 2 * i + 1] = bf16_hi(w[i]);
         }
-#pragma unroll
-        for (int i = 0; i < KC * 16; ++i) top = fmaxf(top, fabsf(x[i]));
-      } else {
-#pragma unroll
-        for (int i = 0; i < KC * 16; ++i) x[i] = 0.0f;
       }
-      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-      int e = 0;
-      if (top > 0.0f && top < INFINITY) {
-        frexpf(top, &e);
-        e -= 12;             // the row's largest value in [2^11, 2^12)
-      }
-      const float f0 = exp2i(-e / 2), f1 = exp2i(-e - (-e / 2));   // 2^-e, which itself may leave fp32's range
+      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+      // 2^-e puts the largest in [2^11, 2^12); in two factors, since it may leave fp32's range. A row with inf or NaN
+      // keeps them.
+      const int e = top >= 0x7F80u ? 0 : max(int(top >> 7), 1) - 138, eh = e / 2;
+      const float f0 = pow2(-eh), f1 = pow2(eh - e);
 #pragma unroll
       for (int i = 0; i < KC * 16; i += 2)
         qf[i / 4][n][(i / 2) & 1] = f16x2_bits(x[i] * f0 * f1, x[i + 1] * f0 * f1);
@@ -447,7 +461,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
       for (int j = 0; j < 2; ++j) {
         const int er = __shfl_sync(0xFFFFFFFFu, e, (2 * c + j) * 4);
         const int rr = (rt * NT + n) * 8 + 2 * c + j;
-        qs[n][j] = scale2(a.scale * kLog2e, er);
+        qs[n][j] = a.scale * kLog2e * pow2(er / 2) * pow2(er - er / 2);
         vis[n][j] = rr < p.rows ? L - T + rr / p.G + 1 : 0;
       }
     }
@@ -678,6 +692,8 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
       }
       __syncwarp();   // every lane has read the stage before it is filled again
     }
+    if (i1 < n_my) load_q(i1);
+
     // ---- results
     const bool whole = u0 == 0 && u1 == nu;
     const int slot = u0 > 0 ? 0 : 1;   // continues an earlier warp's part, or begins the pair
@@ -722,7 +738,8 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
   __syncthreads();
 
   // the warps' partial results, in order of position
-  for (int i = tid; i < C::kRows * (D / 4); i += kDecThreads) {
+  const unsigned have = __ballot_sync(0xFFFFFFFFu, lane < 2 * C::kGroups && s_pair[lane < 2 * C::kGroups ? lane : 0] >= 0);
+  for (int i = tid; i < C::kRows * (D / 4) && have; i += kDecThreads) {
     const int r = i / (D / 4), d4 = (i % (D / 4)) * 4;
     if (r >= p.rows) continue;
     const int w0 = r / (8 * NT), rr = r % (8 * NT);   // row tile; row inside it
@@ -740,20 +757,24 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
         if (d4 == 0) *reinterpret_cast<float4*>(q + C::kRows * D + r * 4) = make_float4(x.r, x.m, x.l, 0.0f);
       }
     };
-    constexpr int KB = 8;   // loads in flight; slots without a result are read and passed over
-    for (int k0 = 0; k0 < 2 * C::kGroups; k0 += KB) {
+    constexpr int KB = 12;   // loads in flight
+    for (unsigned left = have; left;) {
       float4 v[KB], t[KB];
+      int slot[KB];
 #pragma unroll
       for (int k = 0; k < KB; ++k) {
-        const int ks = min(k0 + k, 2 * C::kGroups - 1);
-        const float* q = cta_parts + 2 * C::kPart + (2 * ((ks >> 1) * RT + w0) + (ks & 1)) * C::kPartW;
-        v[k] = *reinterpret_cast<const float4*>(q + rr * D + d4);
-        t[k] = *reinterpret_cast<const float4*>(q + 8 * NT * D + rr * 4);
+        slot[k] = left ? __ffs(left) - 1 : -1;
+        left &= left - 1;
+        if (slot[k] >= 0) {
+          const float* q = cta_parts + 2 * C::kPart + (2 * ((slot[k] >> 1) * RT + w0) + (slot[k] & 1)) * C::kPartW;
+          v[k] = *reinterpret_cast<const float4*>(q + rr * D + d4);
+          t[k] = *reinterpret_cast<const float4*>(q + 8 * NT * D + rr * 4);
+        }
       }
 #pragma unroll
       for (int k = 0; k < KB; ++k) {
-        const int pair = k0 + k < 2 * C::kGroups ? s_pair[k0 + k] : -1;
-        if (pair < 0) continue;
+        if (slot[k] < 0) break;
+        const int pair = s_pair[slot[k]];
         if (pair != cur) {
           flush();
           cur = pair;
@@ -765,50 +786,52 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
     flush();
   }
 
-  // pairs that reach past this CTA: the one of its first chunk, the one of its last
-  for (int edge = 0; edge < 2; ++edge) {
-    const int64_t at = edge ? cta1 - 1 : cta0;
+  // Pairs that reach past this CTA: the one of its first chunk, and that of its
+  // last where it is another. CTAs c0 .. c1 have chunks of the pair.
+  __threadfence();
+  __syncthreads();
+  if (tid < 2) {
+    const int64_t at = tid ? cta1 - 1 : cta0;
     const int b = seq_of(at), nu = prefix[b + 1] - prefix[b];
     const int64_t pair0 = (int64_t)prefix[b] * H;
     const int h = int((at - pair0) / nu);
     const int64_t s0 = pair0 + (int64_t)h * nu, s1 = s0 + nu;
-    if (s0 >= cta0 && s1 <= cta1) continue;
-    if (edge && s0 <= cta0) continue;     // the same pair again
-    // CTAs whose ranges meet chunks [s0, s1)
-    const int c0 = int(((s0 + 1) * N - 1) / W), c1 = int((s1 * N - 1) / W);
-    const int64_t pair = (int64_t)b * H + h;
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) {
-      const unsigned seen = atomicAdd(p.counter + pair, 1u);
-      s_last = seen == unsigned(c1 - c0);
-      if (s_last) p.counter[pair] = 0;
-    }
-    __syncthreads();
-    if (s_last) {
-      __threadfence();
-      for (int i = tid; i < C::kRows * (D / 4); i += kDecThreads) {
-        const int r = i / (D / 4), d4 = (i % (D / 4)) * 4;
-        if (r >= p.rows) continue;
-        Acc x{make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY, -INFINITY, 0.0f};
-        constexpr int KB = 8;
-        for (int k0 = c0; k0 <= c1; k0 += KB) {
-          float4 v[KB], t[KB];
-#pragma unroll
-          for (int k = 0; k < KB; ++k) {
-            const int kc = min(k0 + k, c1);
-            const float* q = p.parts + (size_t)kc * C::kPartsCta + (kc == c0 ? C::kPart : 0);
-            v[k] = __ldcg(reinterpret_cast<const float4*>(q + r * D + d4));
-            t[k] = __ldcg(reinterpret_cast<const float4*>(q + C::kRows * D + r * 4));
-          }
-#pragma unroll
-          for (int k = 0; k < KB; ++k)
-            if (k0 + k <= c1) join(x, v[k], t[k].x, t[k].y, t[k].z);
-        }
-        finish(b, h, r, d4, x);
+    Edge e{-1, 0, 0, 0};
+    if ((s0 < cta0 || s1 > cta1) && !(tid && s0 <= cta0)) {
+      const int c0 = int(((s0 + 1) * N - 1) / W), c1 = int((s1 * N - 1) / W);
+      const int64_t pair = (int64_t)b * H + h;
+      if (atomicAdd(p.counter + pair, 1u) == unsigned(c1 - c0)) {   // the last of them
+        p.counter[pair] = 0;
+        e = Edge{b, h, c0, c1};
       }
     }
-    __syncthreads();
+    s_edge[tid] = e;
+  }
+  __syncthreads();
+  for (int k2 = 0; k2 < 2; ++k2) {
+    const Edge e = s_edge[k2];
+    if (e.b < 0) continue;
+    __threadfence();
+    for (int i = tid; i < C::kRows * (D / 4); i += kDecThreads) {
+      const int r = i / (D / 4), d4 = (i % (D / 4)) * 4;
+      if (r >= p.rows) continue;
+      Acc x{make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY, -INFINITY, 0.0f};
+      constexpr int KB = 8;   // loads in flight
+      for (int k0 = e.c0; k0 <= e.c1; k0 += KB) {
+        float4 v[KB], t[KB];
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+          const int kc = min(k0 + k, e.c1);
+          const float* q = p.parts + (size_t)kc * C::kPartsCta + (kc == e.c0 ? C::kPart : 0);
+          v[k] = __ldcg(reinterpret_cast<const float4*>(q + r * D + d4));
+          t[k] = __ldcg(reinterpret_cast<const float4*>(q + C::kRows * D + r * 4));
+        }
+#pragma unroll
+        for (int k = 0; k < KB; ++k)
+          if (k0 + k <= e.c1) join(x, v[k], t[k].x, t[k].y, t[k].z);
+      }
+      finish(e.b, e.h, r, d4, x);
+    }
   }
 }
 
