@@ -466,13 +466,14 @@ class KVCache:
         n_pages, H, P, D = k_codes.shape
         if P not in (16, 32, 64, 128) or D not in (64, 128):
             raise ValueError("page_size must be 16, 32, 64 or 128 and head_dim 64 or 128")
-        self.device = k_codes.device
+        self.device, self.device_index = k_codes.device, k_codes.get_device()
         if any(t.device != self.device for t in (v_codes, k_scales, v_scales)):
             raise ValueError("the cache's tensors must be on one device")
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = n_pages, H, P, D
         self.struct = moe_kv_cache(n_pages, P, H, D, k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),
                                    v_scales.data_ptr())
+        self._ref = ctypes.byref(self.struct)
 
     @classmethod
     def alloc(cls, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, device="cuda"):
@@ -482,54 +483,70 @@ class KVCache:
         return cls(*codes, *scales)
 
 
-def _rows(t, name, heads=None, d=None):
+_Tensor, _I32, _F32, _U8, _BF16 = torch.Tensor, torch.int32, torch.float32, torch.uint8, torch.bfloat16
+# the current stream's handle without a Stream object: a call here takes a few microseconds in all
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _stream(stream, dev):
+    return _current_raw_stream(dev) if stream is None else stream.cuda_stream
+
+
+def _ptr(t, dtype, name, dev, shape=None):
+    """Address of a contiguous tensor of that type and shape on device `dev` (the current one); raises otherwise."""
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return t.data_ptr()
+    _cuda(t, dtype, name)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _opt(t, dtype, name, dev, shape=None):
+    return None if t is None else _ptr(t, dtype, name, dev, shape)
+
+
+def _status_ptr(t, dev):
+    if t is None:
+        return None
+    if isinstance(t, _Tensor) and t.numel() < 1:
+        raise ValueError("dev_status needs 1 element")
+    return _ptr(t, _I32, "dev_status", dev)
+
+
+def _rows(t, name, dev, heads, d):
     """moe_rows of a bf16 [tokens, heads, d] tensor whose innermost dimension is contiguous."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+    if not (isinstance(t, _Tensor) and t.is_cuda):
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not _BF16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
     shape = t.shape
-    if len(shape) != 3 or (heads is not None and shape[1] != heads) or (d is not None and shape[2] != d):
-        raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, "
-                         f"{'head_dim' if d is None else d}], got {tuple(shape)}")
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d:
+        raise ValueError(f"{name} must be [tokens, {heads}, {d}], got {list(shape)}")
     ts, hs, es = t.stride()
-    if es != 1 and shape[2] > 1:
+    if es != 1:
         raise ValueError(f"{name}'s innermost dimension must be contiguous")
     # the stride of a dimension of size 1 is arbitrary
-    return moe_rows(t.data_ptr(), ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0)
+    return moe_rows(t.data_ptr(), ts if shape[0] > 1 else 0, hs if heads > 1 else 0)
 
 
-def _on(dev, **tensors):
-    """Every given tensor lives on the current device, which is `dev`."""
-    cur = torch.cuda.current_device()
-    if dev.index != cur:
-        raise ValueError(f"the inputs are on cuda:{dev.index}, the current device is cuda:{cur}")
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the other inputs are on {dev}")
-
-
-def _status_arg(dev_status):
-    if dev_status is not None:
-        _cuda(dev_status, torch.int32, "dev_status")
-        if dev_status.numel() < 1:
-            raise ValueError("dev_status needs 1 element")
-    return dev_status
-
-
-def _ints(t, name, *shape):
-    """Contiguous int32 tensor of that shape."""
-    _cuda(t, torch.int32, name)
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    return t
-
-
-def _table(t, name, n_seq):
-    _cuda(t, torch.int32, name)
+def _table(t, name, dev, n_seq):
+    """Address and width of a page table."""
+    p = _ptr(t, _I32, name, dev)
     if t.dim() != 2 or t.shape[0] != n_seq:
-        raise ValueError(f"{name} must be [{n_seq}, pages], got {tuple(t.shape)}")
-    return t
+        raise ValueError(f"{name} must be [{n_seq}, pages], got {list(t.shape)}")
+    return p, t.shape[1]
+
+
+def _cache_device(cache):
+    dev = torch.cuda.current_device()
+    if cache.device_index != dev:
+        raise ValueError(f"the cache is on cuda:{cache.device_index}, the current device is cuda:{dev}")
+    return dev
 
 
 def moe_attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
@@ -543,31 +560,29 @@ def moe_attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     slices of one projection (strides that are multiples of 8 elements). scale
     defaults to 1 / sqrt(D). lse fp32 [total_q, n_heads] is written if given.
     """
-    qr = _rows(q, "q")
-    total_q, n_heads, d = q.shape
-    kr = _rows(k, "k", d=d)
-    total_k, n_kv = k.shape[0], k.shape[1]
-    vr = _rows(v, "v", heads=n_kv, d=d)
+    for name, t in (("q", q), ("k", k)):
+        if not (isinstance(t, _Tensor) and t.is_cuda):
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.dim() != 3:
+            raise ValueError(f"{name} must be [tokens, heads, head_dim], got {list(t.shape)}")
+    dev = torch.cuda.current_device()
+    total_q, n_heads, d = q_shape = q.shape
+    total_k, n_kv, _ = k.shape
+    qr, kr, vr = _rows(q, "q", dev, n_heads, d), _rows(k, "k", dev, n_kv, d), _rows(v, "v", dev, n_kv, d)
     if v.shape[0] != total_k:
         raise ValueError("k and v must have the same number of rows")
-    _cuda(cu_q, torch.int32, "cu_q")
-    if cu_q.dim() != 1 or cu_q.numel() < 1:
+    cu_qp = _ptr(cu_q, _I32, "cu_q", dev)
+    n_cu = cu_q.numel()
+    if n_cu < 1 or cu_q.dim() != 1:
         raise ValueError("cu_q must be [n_seq + 1]")
-    cu_k = cu_q if cu_k is None else _ints(cu_k, "cu_k", cu_q.numel())
+    cu_kp = cu_qp if cu_k is None else _ptr(cu_k, _I32, "cu_k", dev, (n_cu,))
     if out is None:
-        out = torch.empty((total_q, n_heads, d), dtype=torch.bfloat16, device=q.device)
-    _cuda(out, torch.bfloat16, "out")
-    if out.shape != q.shape:
-        raise ValueError(f"out must have q's shape {tuple(q.shape)}, got {tuple(out.shape)}")
-    if lse is not None:
-        _cuda(lse, torch.float32, "lse")
-        if lse.shape != q.shape[:2]:
-            raise ValueError(f"lse must be {tuple(q.shape[:2])}, got {tuple(lse.shape)}")
-    _on(q.device, k=k, v=v, cu_q=cu_q, cu_k=cu_k, out=out, lse=lse, dev_status=_status_arg(dev_status))
-    _check(lib.moe_attn_prefill(ctypes.byref(qr), ctypes.byref(kr), ctypes.byref(vr), n_heads, n_kv, d, _p(cu_q),
-                                _p(cu_k), cu_q.numel() - 1, total_q, total_k, 1 if causal else 0,
-                                d ** -0.5 if scale is None else float(scale), _p(out), _p(lse), _p(dev_status),
-                                _s(stream)), "moe_attn_prefill")
+        out = torch.empty(q_shape, dtype=_BF16, device=q.device)
+    _check(lib.moe_attn_prefill(ctypes.byref(qr), ctypes.byref(kr), ctypes.byref(vr), n_heads, n_kv, d, cu_qp, cu_kp,
+                                n_cu - 1, total_q, total_k, 1 if causal else 0,
+                                d ** -0.5 if scale is None else float(scale), _ptr(out, _BF16, "out", dev, q_shape),
+                                _opt(lse, _F32, "lse", dev, (total_q, n_heads)), _status_ptr(dev_status, dev),
+                                _stream(stream, dev)), "moe_attn_prefill")
     return out
 
 
@@ -576,25 +591,23 @@ def moe_kv_append_fp8(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu_seqle
                       stream=None):
     """Append bf16 k, v [total, n_kv_heads, D] to the cache: rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 go to
     positions start[b], start[b] + 1, ... of sequence b, whose pages are page_table[b] (int32 [n_seq, width])."""
-    kr = _rows(k, "k", heads=cache.n_kv_heads, d=cache.head_dim)
-    vr = _rows(v, "v", heads=cache.n_kv_heads, d=cache.head_dim)
-    if v.shape[0] != k.shape[0]:
+    dev, H, D = _cache_device(cache), cache.n_kv_heads, cache.head_dim
+    kr, vr = _rows(k, "k", dev, H, D), _rows(v, "v", dev, H, D)
+    total = k.shape[0]
+    if v.shape[0] != total:
         raise ValueError("k and v must have the same number of rows")
-    _cuda(start, torch.int32, "start")
+    startp = _ptr(start, _I32, "start", dev)
     n_seq = start.numel()
-    _ints(cu_seqlens, "cu_seqlens", n_seq + 1)
-    _table(page_table, "page_table", n_seq)
-    _on(cache.device, k=k, v=v, cu_seqlens=cu_seqlens, start=start, page_table=page_table,
-        dev_status=_status_arg(dev_status))
-    _check(lib.moe_kv_append_fp8(ctypes.byref(cache.struct), ctypes.byref(kr), ctypes.byref(vr), _p(cu_seqlens),
-                                 _p(start), n_seq, k.shape[0], _p(page_table), page_table.shape[1], _p(dev_status),
-                                 _s(stream)), "moe_kv_append_fp8")
+    tablep, width = _table(page_table, "page_table", dev, n_seq)
+    _check(lib.moe_kv_append_fp8(cache._ref, ctypes.byref(kr), ctypes.byref(vr),
+                                 _ptr(cu_seqlens, _I32, "cu_seqlens", dev, (n_seq + 1,)), startp, n_seq, total, tablep,
+                                 width, _status_ptr(dev_status, dev), _stream(stream, dev)), "moe_kv_append_fp8")
 
 
 def moe_attn_decode_workspace_bytes(cache: KVCache, n_seq: int, n_new: int, n_heads: int, table_width: int,
                                     with_weights: bool = False) -> int:
     """Bytes of the workspace of moe_attn_decode_fp8; 0 for an unsupported shape."""
-    return int(lib.moe_attn_decode_workspace_bytes(ctypes.byref(cache.struct), n_seq, n_new, n_heads, table_width,
+    return int(lib.moe_attn_decode_workspace_bytes(cache._ref, n_seq, n_new, n_heads, table_width,
                                                    1 if with_weights else 0))
 
 
@@ -611,39 +624,37 @@ def moe_attn_decode_fp8(cache: KVCache, q: torch.Tensor, lengths: torch.Tensor, 
     moe_attn_decode_workspace_bytes(...) bytes, zero-filled before its first
     use (it carries counters between calls); allocated with zeros when omitted.
     """
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
-        raise ValueError("q must be [n_seq, n_new, n_heads, head_dim]")
-    n_seq, n_new, n_heads, d = q.shape
-    if n_seq > 1 and n_new > 1 and q.stride(0) != n_new * q.stride(1):
+    dev, H = _cache_device(cache), cache.n_kv_heads
+    if not isinstance(q, _Tensor) or q.dim() != 4:
+        raise ValueError("q must be a tensor [n_seq, n_new, n_heads, head_dim]")
+    n_seq, n_new, n_heads, d = shape = q.shape
+    if n_new == 1:
+        rows = q[:, 0]
+    elif n_seq == 1:
+        rows = q[0]
+    elif q.stride(0) != n_new * q.stride(1):
         raise ValueError("q's tokens must have one stride over all sequences")
-    rows = q[:, 0] if n_new == 1 else (q[0] if n_seq == 1 else q.flatten(0, 1))
-    qr = _rows(rows, "q", d=cache.head_dim)
-    _ints(lengths, "lengths", n_seq)
-    _table(page_table, "page_table", n_seq)
+    else:
+        rows = q.flatten(0, 1)
+    qr = _rows(rows, "q", dev, n_heads, cache.head_dim)
+    tablep, width = _table(page_table, "page_table", dev, n_seq)
     if out is None:
-        out = torch.empty((n_seq, n_new, n_heads, d), dtype=torch.bfloat16, device=q.device)
-    _cuda(out, torch.bfloat16, "out")
-    if out.shape != q.shape:
-        raise ValueError(f"out must have q's shape {tuple(q.shape)}, got {tuple(out.shape)}")
-    if lse is not None:
-        _cuda(lse, torch.float32, "lse")
-        if lse.shape != q.shape[:3]:
-            raise ValueError(f"lse must be {tuple(q.shape[:3])}, got {tuple(lse.shape)}")
+        out = torch.empty(shape, dtype=_BF16, device=q.device)
+    wp, wn = None, 0
     if weights is not None:
-        _cuda(weights, torch.float32, "weights")
-        if weights.dim() != 3 or weights.shape[:2] != (n_seq, cache.n_kv_heads):
-            raise ValueError(f"weights must be [{n_seq}, {cache.n_kv_heads}, positions], got {tuple(weights.shape)}")
+        wp = _ptr(weights, _F32, "weights", dev)
+        if weights.dim() != 3 or weights.shape[:2] != (n_seq, H):
+            raise ValueError(f"weights must be [{n_seq}, {H}, positions], got {list(weights.shape)}")
+        wn = weights.shape[2]
     if workspace is None:
-        n = moe_attn_decode_workspace_bytes(cache, n_seq, n_new, n_heads, page_table.shape[1], weights is not None)
-        workspace = torch.zeros(max(n, 256), dtype=torch.uint8, device=q.device)
-    _cuda(workspace, torch.uint8, "workspace")
-    _on(cache.device, q=q, lengths=lengths, page_table=page_table, out=out, lse=lse, weights=weights,
-        workspace=workspace, dev_status=_status_arg(dev_status))
-    _check(lib.moe_attn_decode_fp8(ctypes.byref(cache.struct), ctypes.byref(qr), n_heads, n_seq, n_new, _p(lengths),
-                                   _p(page_table), page_table.shape[1], d ** -0.5 if scale is None else float(scale),
-                                   _p(out), _p(lse), _p(weights), weights.shape[2] if weights is not None else 0,
-                                   _p(workspace), workspace.numel(), _p(dev_status), _s(stream)),
-           "moe_attn_decode_fp8")
+        n = moe_attn_decode_workspace_bytes(cache, n_seq, n_new, n_heads, width, weights is not None)
+        workspace = torch.zeros(max(n, 256), dtype=_U8, device=q.device)
+    _check(lib.moe_attn_decode_fp8(cache._ref, ctypes.byref(qr), n_heads, n_seq, n_new,
+                                   _ptr(lengths, _I32, "lengths", dev, (n_seq,)), tablep, width,
+                                   d ** -0.5 if scale is None else float(scale), _ptr(out, _BF16, "out", dev, shape),
+                                   _opt(lse, _F32, "lse", dev, (n_seq, n_new, n_heads)), wp, wn,
+                                   _ptr(workspace, _U8, "workspace", dev), workspace.numel(),
+                                   _status_ptr(dev_status, dev), _stream(stream, dev)), "moe_attn_decode_fp8")
     return out
 
 
@@ -655,30 +666,26 @@ def moe_kv_evict_fp8(cache: KVCache, page_table: torch.Tensor, lengths: torch.Te
     most accumulated weight. They become positions 0, 1, ... of the pages dst_table (int32 [n_seq, width]), which
     must hold none of the positions read. Returns (kept int32 [n_seq, n_kv_heads, keep], kept_weights fp32 like it,
     new_lengths int32 [n_seq])."""
-    _cuda(lengths, torch.int32, "lengths")
-    n_seq, H = lengths.numel(), cache.n_kv_heads
-    _table(page_table, "page_table", n_seq)
-    _table(dst_table, "dst_table", n_seq)
-    _cuda(weights, torch.float32, "weights")
+    dev, H = _cache_device(cache), cache.n_kv_heads
+    lengthsp = _ptr(lengths, _I32, "lengths", dev)
+    n_seq = lengths.numel()
+    tablep, width = _table(page_table, "page_table", dev, n_seq)
+    dstp, dst_width = _table(dst_table, "dst_table", dev, n_seq)
+    wp = _ptr(weights, _F32, "weights", dev)
     if weights.dim() != 3 or weights.shape[:2] != (n_seq, H):
-        raise ValueError(f"weights must be [{n_seq}, {H}, positions], got {tuple(weights.shape)}")
+        raise ValueError(f"weights must be [{n_seq}, {H}, positions], got {list(weights.shape)}")
     if keep < 1 or not 0 <= recent <= keep:
         raise ValueError("keep must be at least 1 and recent in [0, keep]")
+    shape = (n_seq, H, keep)
     if kept is None:
-        kept = torch.empty((n_seq, H, keep), dtype=torch.int32, device=weights.device)
+        kept = torch.empty(shape, dtype=_I32, device=weights.device)
     if kept_weights is None:
-        kept_weights = torch.empty((n_seq, H, keep), dtype=torch.float32, device=weights.device)
+        kept_weights = torch.empty(shape, dtype=_F32, device=weights.device)
     if new_lengths is None:
-        new_lengths = torch.empty(n_seq, dtype=torch.int32, device=weights.device)
-    _ints(kept, "kept", n_seq, H, keep)
-    _cuda(kept_weights, torch.float32, "kept_weights")
-    if kept_weights.shape != kept.shape:
-        raise ValueError(f"kept_weights must be {tuple(kept.shape)}, got {tuple(kept_weights.shape)}")
-    _ints(new_lengths, "new_lengths", n_seq)
-    _on(cache.device, page_table=page_table, lengths=lengths, weights=weights, dst_table=dst_table, kept=kept,
-        kept_weights=kept_weights, new_lengths=new_lengths, dev_status=_status_arg(dev_status))
-    _check(lib.moe_kv_evict_fp8(ctypes.byref(cache.struct), _p(page_table), page_table.shape[1], _p(lengths), n_seq,
-                                _p(weights), weights.shape[2], keep, recent, _p(dst_table), dst_table.shape[1],
-                                _p(kept), _p(kept_weights), _p(new_lengths), _p(dev_status), _s(stream)),
-           "moe_kv_evict_fp8")
+        new_lengths = torch.empty(n_seq, dtype=_I32, device=weights.device)
+    _check(lib.moe_kv_evict_fp8(cache._ref, tablep, width, lengthsp, n_seq, wp, weights.shape[2], keep, recent, dstp,
+                                dst_width, _ptr(kept, _I32, "kept", dev, shape),
+                                _ptr(kept_weights, _F32, "kept_weights", dev, shape),
+                                _ptr(new_lengths, _I32, "new_lengths", dev, (n_seq,)), _status_ptr(dev_status, dev),
+                                _stream(stream, dev)), "moe_kv_evict_fp8")
     return kept, kept_weights, new_lengths
