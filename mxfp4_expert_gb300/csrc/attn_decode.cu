@@ -141,13 +141,8 @@ __device__ __forceinline__ void ldm_trans8(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
-// 2^e, -126 <= e <= 127
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
 // 2^(s - 127) for a scale byte
 __device__ __forceinline__ float scale_value(uint32_t s) { return __uint_as_float(s ? s << 23 : 0x00400000u); }
-// Does one of the word's four codes stand for NaN?
-__device__ __forceinline__ bool any_nan4(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
-
 // Length of sequence b, cut to what table, weights and workspace hold.
 __device__ __forceinline__ int dec_length(const DecodeArgs& a, int b, bool* bad) {
   const int x = __ldg(a.lengths + b);

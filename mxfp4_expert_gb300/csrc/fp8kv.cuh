@@ -17,19 +17,25 @@ __device__ __forceinline__ int kv_scale_byte(float amax) {
 }
 __device__ __forceinline__ bool e4m3_is_nan(uint32_t c) { return (c & 0x7Fu) == 0x7Fu; }
 
-// Four codes in a word, worth 2^sh of what they were (sh < 0: rounded to
-// nearest even; NaN stays NaN).
-__device__ __forceinline__ uint32_t kv_rescale4(uint32_t w, int sh) {
-  uint32_t r = 0;
-#pragma unroll
-  for (int i = 0; i < 4; i += 2) {
-    const uint32_t c0 = (w >> (8 * i)) & 0xFFu, c1 = (w >> (8 * i + 8)) & 0xFFu;
-    const float v0 = e4m3_is_nan(c0) ? __int_as_float(0x7FC00000) : scale2(e4m3_to_f32(c0), sh);
-    const float v1 = e4m3_is_nan(c1) ? __int_as_float(0x7FC00000) : scale2(e4m3_to_f32(c1), sh);
-    r |= uint32_t(f32x2_to_e4m3x2(v0, v1)) << (8 * i);
-  }
-  return r;
+// 2^e, -126 <= e <= 127
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
+// Does one of the word's four codes stand for NaN?
+__device__ __forceinline__ bool any_nan4(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
+// Four codes in a word times f, a power of two: rounded to nearest even, NaN
+// stays NaN. |values| * f <= 448 is up to the caller.
+__device__ __forceinline__ uint32_t kv_rescale4(uint32_t w, float f) {
+  uint32_t h0, h1;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+      : "=r"(h0), "=r"(h1)
+      : "r"(w));
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+  return uint32_t(f32x2_to_e4m3x2(a.x * f, a.y * f)) | uint32_t(f32x2_to_e4m3x2(b.x * f, b.y * f)) << 16;
 }
+// The factor that turns codes of scale byte `from` into units of `to`; below
+// 2^-126 every code becomes zero.
+__device__ __forceinline__ float kv_factor(int from, int to) { return pow2(max(from - to, -126)); }
 
 // Sequence b's rows [c0, c1) of `total` packed rows, cut to what fits;
 // *bad if cu leaves [0, total] or falls.

@@ -8,6 +8,8 @@
 // 2 bytes in and 1 out per value.
 //
 // evict: see the two kernels below.
+#include <algorithm>
+
 #include "attn.h"
 #include "fp8kv.cuh"
 
@@ -92,77 +94,91 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const AppendArgs a)
   const Block f = sblk;
   if (f.b < 0) return;
   const int P = a.c.page_size, D = a.c.head_dim, H = a.c.n_kv_heads, h = blockIdx.y;
+  // the page, and meanwhile the values; then the page's scale, and meanwhile their maximum
   const int page = f.blk < a.width ? __ldg(a.table + (size_t)f.b * a.width + f.blk) : -1;
+  const bool is_v = blockIdx.z != 0;
+  const __nv_bfloat16* src = (is_v ? a.v : a.k) + h * (is_v ? a.v_hs : a.k_hs);
+  const int64_t ts = is_v ? a.v_ts : a.k_ts;
+  const int cpr = D / 8, n = (f.s1 - f.s0) * cpr;   // vectors per row; of the new rows
+  const int row = tid / cpr, col = (tid % cpr) * 8, rows = kAppThreads / cpr;   // a thread's first vector; rows to its next
+
+  uint4 x[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    x[i] = i * kAppThreads + tid < n ? *reinterpret_cast<const uint4*>(src + (f.t0 + row + i * rows) * ts + col)
+                                     : make_uint4(0, 0, 0, 0);
   if (page < 0 || page >= a.c.n_pages) {
     if (tid == 0 && a.status) atomicOr(a.status, MOE_DEV_INDEX_OOB);
     return;
   }
-  const bool is_v = blockIdx.z != 0;
-  const __nv_bfloat16* src = (is_v ? a.v : a.k) + h * (is_v ? a.v_hs : a.k_hs);
-  const int64_t ts = is_v ? a.v_ts : a.k_ts;
   uint8_t* codes = static_cast<uint8_t*>(is_v ? a.c.v_codes : a.c.k_codes) + ((size_t)page * H + h) * P * D;
   uint8_t* scale = (is_v ? a.c.v_scales : a.c.k_scales) + (size_t)page * H + h;
-  const int cpr = D / 8, n = (f.s1 - f.s0) * cpr;   // vectors per row; of the new rows
-
-  uint4 x[NV];
-  int top = 0, nonfinite = 0;   // largest finite magnitude, as bf16 bits
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = i * kAppThreads + tid;
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (v < n) x[i] = *reinterpret_cast<const uint4*>(src + (f.t0 + v / cpr) * ts + (v % cpr) * 8);
-  }
+  const int had = f.s0 > 0 ? int(*scale) : 0;
+  uint32_t top2 = 0;   // largest magnitudes, as bf16 bits, of the even and the odd values
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int lo = w[j] & 0x7FFF, hi = (w[j] >> 16) & 0x7FFF;
-      if (lo < 0x7F80) top = max(top, lo); else nonfinite = 1;
-      if (hi < 0x7F80) top = max(top, hi); else nonfinite = 1;
+    for (int j = 0; j < 4; ++j) top2 = __vmaxu2(top2, w[j] & 0x7FFF7FFFu);
+  }
+  int top = max(top2 & 0xFFFFu, top2 >> 16);
+  bool nonfinite = __any_sync(0xFFFFFFFFu, top >= 0x7F80);
+  if (nonfinite) {     // the largest finite one then
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int lo = w[j] & 0x7FFF, hi = (w[j] >> 16) & 0x7FFF;
+        if (lo < 0x7F80) top = max(top, lo);
+        if (hi < 0x7F80) top = max(top, hi);
+      }
     }
   }
   top = __reduce_max_sync(0xFFFFFFFFu, top);
-  nonfinite = __any_sync(0xFFFFFFFFu, nonfinite);
   if (lane == 0) {
     smax[warp] = top;
     sbad[warp] = nonfinite;
   }
-  const int had = f.s0 > 0 ? int(*scale) : 0;
   __syncthreads();   // also: everyone has read the old scale
 #pragma unroll
   for (int i = 0; i < kAppThreads / 32; ++i) {
     top = max(top, smax[i]);
-    nonfinite |= sbad[i];
+    nonfinite |= sbad[i] != 0;
   }
   const int byte = max(kv_scale_byte(__uint_as_float(uint32_t(top) << 16)), had);
   if (tid == 0) {
     *scale = uint8_t(byte);
     if (nonfinite && a.status) atomicOr(a.status, MOE_DEV_NONFINITE_INPUT);
   }
+  // 2^(127 - byte); 2^-127 and 2^-128 are subnormal (new values need 247 at most, but the page may hold more)
+  const float f1 = byte <= 253 ? pow2(127 - byte) : __uint_as_float(0x00800000u >> (byte - 253));
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int v = i * kAppThreads + tid;
-    if (v >= n) break;
+    if (i * kAppThreads + tid >= n) break;
     const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
     uint32_t q[2] = {0, 0};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      // inf takes the code of NaN: there is none for it
-      const float lo = (w[j] & 0x7F80u) == 0x7F80u ? __int_as_float(0x7FC00000) : scale2(bf16_lo(w[j]), 127 - byte);
-      const float hi = (w[j] & 0x7F800000u) == 0x7F800000u ? __int_as_float(0x7FC00000) : scale2(bf16_hi(w[j]), 127 - byte);
+      float lo = bf16_lo(w[j]) * f1, hi = bf16_hi(w[j]) * f1;
+      if (nonfinite) {   // inf takes the code of NaN: there is none for it
+        if ((w[j] & 0x7F80u) == 0x7F80u) lo = __int_as_float(0x7FC00000);
+        if ((w[j] & 0x7F800000u) == 0x7F800000u) hi = __int_as_float(0x7FC00000);
+      }
       q[j >> 1] |= uint32_t(f32x2_to_e4m3x2(lo, hi)) << (16 * (j & 1));
     }
-    *reinterpret_cast<uint2*>(codes + (size_t)(f.s0 + v / cpr) * D + (v % cpr) * 8) = make_uint2(q[0], q[1]);
+    *reinterpret_cast<uint2*>(codes + (f.s0 + row + i * rows) * D + col) = make_uint2(q[0], q[1]);
   }
   if (byte > had && f.s0 > 0) {   // older codes, in units of the new scale
+    const float fo = kv_factor(had, byte);
     for (int v = tid; v < f.s0 * D / 16; v += kAppThreads) {
       uint4* p = reinterpret_cast<uint4*>(codes) + v;
       uint4 c = *p;
-      c.x = kv_rescale4(c.x, had - byte);
-      c.y = kv_rescale4(c.y, had - byte);
-      c.z = kv_rescale4(c.z, had - byte);
-      c.w = kv_rescale4(c.w, had - byte);
+      c.x = kv_rescale4(c.x, fo);
+      c.y = kv_rescale4(c.y, fo);
+      c.z = kv_rescale4(c.z, fo);
+      c.w = kv_rescale4(c.w, fo);
       *p = c;
     }
   }
@@ -172,6 +188,9 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const AppendArgs a)
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelTile = 4 * kSelThreads;
+constexpr int kSelBits = 11, kSelBins = 1 << kSelBits, kSelPasses = 3;
+constexpr int kSelCluster = 8;          // CTAs per (sequence, head), at most
+constexpr int kSelEach = 4096;          // positions worth another CTA
 
 // Order-preserving key: larger weight, larger key; -0 as +0, NaN as -inf.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -190,110 +209,187 @@ __device__ __forceinline__ int cut_length(const int32_t* lengths, int b, int wid
   return l;
 }
 
-// Which positions of (sequence blockIdx.y, head blockIdx.x) stay: the threshold
-// weight by radix selection, 8 bits a pass, then one pass in order that takes
-// what is above it, the first of what equals it, and the recent ones.
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
-  __shared__ unsigned hist[256];
+// Which positions of (sequence, head) stay. A cluster of CTAs shares one pair,
+// each a run of positions. The threshold weight comes from a radix selection, 11
+// bits of the key a pass: every CTA counts its positions' digits in its own
+// shared memory, then reads the others' counts through the cluster and finds the
+// digit for itself, so a pass takes one cluster barrier. One more pass, in
+// order, takes what is above the threshold, the first of what equals it, and
+// the recent ones. Bound by latency: a few dependent passes over 4 bytes a
+// position that lie in L2. Three passes of 11 bits instead of four of 8, and 8
+// CTAs instead of one, took 16 x 4 pairs of 32768 positions from 36 us to 25 us (a read of the weights at
+// the copy rate takes 1.3).
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a, int csize) {
+  __shared__ unsigned hist[kSelPasses][kSelBins];
   __shared__ unsigned s_bin, s_left;
-  __shared__ unsigned long long s_warp[kSelThreads / 32];
-  __shared__ unsigned long long s_base;
+  __shared__ unsigned s_sum[kSelThreads / 32];
+  __shared__ unsigned s_cnt[2];                          // this CTA's positions above and at the threshold
+  __shared__ unsigned s_gt[kSelThreads / 32], s_eq[kSelThreads / 32];
+  __shared__ unsigned s_base[2];                         // positions above and at the threshold so far
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.x, b = blockIdx.y, H = a.c.n_kv_heads;
+  const int rank = blockIdx.x % csize, h = blockIdx.x / csize, b = blockIdx.y, H = a.c.n_kv_heads;
   bool bad = false;
   const int L = cut_length(a.lengths, b, a.width, a.c.page_size, a.w_stride, &bad);
   const float* w = a.weights + ((size_t)b * H + h) * a.w_stride;
   int32_t* kept = a.kept + ((size_t)b * H + h) * a.keep;
   float* kw = a.kept_w ? a.kept_w + ((size_t)b * H + h) * a.keep : nullptr;
   const int m = min(L, a.keep);
-  if (h == 0 && tid == 0) {
+  const int me = rank * kSelThreads + tid, all = csize * kSelThreads;
+  if (h == 0 && me == 0) {
     a.new_lengths[b] = m;
     if (bad && a.status) atomicOr(a.status, MOE_DEV_INDEX_OOB);
   }
-  for (int i = m + tid; i < a.keep; i += kSelThreads) {
+  for (int i = m + me; i < a.keep; i += all) {
     kept[i] = -1;
     if (kw) kw[i] = 0.0f;
   }
   if (L <= a.keep) {
-    for (int i = tid; i < m; i += kSelThreads) {
+    for (int i = me; i < m; i += all) {
       kept[i] = i;
       if (kw) kw[i] = w[i];
     }
     return;
   }
   const int n = L - a.recent;            // positions that compete
-  unsigned left = a.keep - a.recent;     // for so many places (fewer than n)
-  uint32_t thr = 0;
-  if (left > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      for (int i = tid; i < n; i += kSelThreads) {
-        const uint32_t k = weight_key(w[i]);
-        if (shift == 24 || (k >> (shift + 8)) == (thr >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1u);
-      }
-      __syncthreads();
-      if (warp == 0) {
-        // lane l: bins 255 - 8 l down to 248 - 8 l
-        unsigned c[8], sum = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum += (c[j] = hist[255 - 8 * lane - j]);
-        unsigned incl = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-          if (lane >= o) incl += v;
-        }
-        unsigned above = incl - sum;   // in the bins above this lane's
-        if (above < left && incl >= left) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (above < left && above + c[j] >= left) {
-              s_bin = 255 - 8 * lane - j;
-              s_left = left - above;
-              above = 0xFFFFFFFFu;   // found
-            } else if (above != 0xFFFFFFFFu) {
-              above += c[j];
-            }
-          }
-        }
-      }
-      __syncthreads();
-      thr |= s_bin << shift;
-      left = s_left;
-    }
+  const int room = a.keep - a.recent;    // for so many places (fewer than n)
+  for (int i = me; i < a.recent; i += all) {
+    kept[room + i] = n + i;
+    if (kw) kw[room + i] = w[n + i];
   }
-  // In order: (positions taken so far, ties seen so far) in one 64-bit sum.
-  const bool any = a.keep > a.recent;
-  if (tid == 0) s_base = 0;
+  if (room == 0) return;                 // the same for the whole cluster
+  // this CTA's run of positions
+  const int each = ((n + csize - 1) / csize + 3) & ~3;
+  const int i0 = min(n, rank * each), i1 = min(n, i0 + each);
+  for (int i = tid; i < kSelPasses * kSelBins; i += kSelThreads) (&hist[0][0])[i] = 0;
   __syncthreads();
-  for (int i0 = 0; i0 < n && any; i0 += kSelTile) {
+
+  uint32_t thr = 0;
+  unsigned left = room;
+  // one address per lane and warp of any CTA's hist / s_cnt
+  auto remote = [&](const void* p, int r) {
+    uint32_t x;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(x) : "r"(smem_addr(p)), "r"(r));
+    return x;
+  };
+  auto ld_remote = [&](uint32_t x) {
+    unsigned v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(x));
+    return v;
+  };
+  // a value per warp: the sum over the warps before this one
+  auto warps_before = [&](const unsigned* p) {
+    return __reduce_add_sync(0xFFFFFFFFu, lane < warp ? p[lane] : 0u);
+  };
+  auto cluster_sync = [&]() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  };
+  // digits, from the top: bits [21, 32), [10, 21), [0, 10)
+#pragma unroll
+  for (int pass = 0; pass < kSelPasses; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+    const uint32_t mask = (1u << bits) - 1;
+#pragma unroll 8
+    for (int i = i0 + tid; i < i1; i += kSelThreads) {
+      const uint32_t k = weight_key(w[i]);
+      if (pass == 0 || (k >> (shift + bits)) == (thr >> (shift + bits))) atomicAdd(&hist[pass][(k >> shift) & mask], 1u);
+    }
+    if (csize > 1) cluster_sync(); else __syncthreads();
+    // thread t: bins kSelBins - 1 - 2t and the one below
+    const int hi = kSelBins - 1 - 2 * tid;
+    unsigned c0 = 0, c1 = 0;
+    if (csize == 1) {
+      c0 = hist[pass][hi];
+      c1 = hist[pass][hi - 1];
+    } else {
+      unsigned v0[kSelCluster], v1[kSelCluster];   // all on their way at once
+#pragma unroll
+      for (int r = 0; r < kSelCluster; ++r) {
+        v0[r] = r < csize ? ld_remote(remote(&hist[pass][hi], r)) : 0;
+        v1[r] = r < csize ? ld_remote(remote(&hist[pass][hi - 1], r)) : 0;
+      }
+#pragma unroll
+      for (int r = 0; r < kSelCluster; ++r) c0 += v0[r], c1 += v1[r];
+    }
+    unsigned incl = c0 + c1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) s_sum[warp] = incl;
+    __syncthreads();
+    const unsigned above = incl - c0 - c1 + warps_before(s_sum);   // in the bins above this thread's
+    if (above < left && above + c0 + c1 >= left) {
+      const bool first = above + c0 >= left;
+      s_bin = first ? hi : hi - 1;
+      s_left = left - above - (first ? 0 : c0);
+    }
+    __syncthreads();
+    thr |= s_bin << shift;
+    left = s_left;
+  }
+
+  // positions above and at the threshold in the CTAs before this one
+  if (tid < 2) s_cnt[tid] = s_base[tid] = 0;
+  __syncthreads();
+  if (csize > 1) {
+    unsigned gt = 0, eq = 0;
+#pragma unroll 8
+    for (int i = i0 + tid; i < i1; i += kSelThreads) {
+      const uint32_t k = weight_key(w[i]);
+      gt += k > thr;
+      eq += k == thr;
+    }
+    gt = __reduce_add_sync(0xFFFFFFFFu, gt);
+    eq = __reduce_add_sync(0xFFFFFFFFu, eq);
+    if (lane == 0) {
+      atomicAdd(&s_cnt[0], gt);
+      atomicAdd(&s_cnt[1], eq);
+    }
+    cluster_sync();
+    if (warp == 0) {
+      const unsigned g = lane < rank ? ld_remote(remote(&s_cnt[0], lane)) : 0;
+      const unsigned e = lane < rank ? ld_remote(remote(&s_cnt[1], lane)) : 0;
+      const unsigned gs = __reduce_add_sync(0xFFFFFFFFu, g), es = __reduce_add_sync(0xFFFFFFFFu, e);
+      if (lane == 0) {
+        s_base[0] = gs;
+        s_base[1] = es;
+      }
+    }
+    __syncthreads();
+  }
+  for (int t0 = i0; t0 < i1; t0 += kSelTile) {
     uint32_t k[4];
     float x[4];
     unsigned gt = 0, eq = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int i = i0 + 4 * tid + j;
-      x[j] = i < n ? w[i] : 0.0f;
+      const int i = t0 + 4 * tid + j;
+      x[j] = i < i1 ? w[i] : 0.0f;
       k[j] = weight_key(x[j]);
-      gt += i < n && k[j] > thr;
-      eq += i < n && k[j] == thr;
+      gt += i < i1 && k[j] > thr;
+      eq += i < i1 && k[j] == thr;
     }
-    unsigned long long mine = (unsigned long long)gt << 32 | eq, incl = mine;
+    // (above, at) before this thread: at most 4 of each per thread, so both counts of a warp fit one word
+    unsigned incl = gt << 16 | eq;
+    const unsigned mine = incl;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      const unsigned v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
       if (lane >= o) incl += v;
     }
-    if (lane == 31) s_warp[warp] = incl;
+    if (lane == 31) {
+      s_gt[warp] = incl >> 16;
+      s_eq[warp] = incl & 0xFFFFu;
+    }
     __syncthreads();
-    unsigned long long before = s_base + incl - mine;
-    for (int j = 0; j < warp; ++j) before += s_warp[j];
-    unsigned g = unsigned(before >> 32), e = unsigned(before);
+    unsigned g = s_base[0] + warps_before(s_gt) + ((incl - mine) >> 16);
+    unsigned e = s_base[1] + warps_before(s_eq) + ((incl - mine) & 0xFFFFu);
+    const unsigned g1 = g + gt, e1 = e + eq;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int i = i0 + 4 * tid + j;
-      if (i >= n) break;
+      const int i = t0 + 4 * tid + j;
+      if (i >= i1) break;
       const bool tie = k[j] == thr;
       if (k[j] > thr || (tie && e < left)) {
         const unsigned at = g + min(e, left);
@@ -304,20 +400,23 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
       e += tie;
     }
     __syncthreads();
-    if (tid == kSelThreads - 1) s_base = before + mine;
+    if (tid == kSelThreads - 1) {
+      s_base[0] = g1;
+      s_base[1] = e1;
+    }
     __syncthreads();
   }
-  for (int i = tid; i < a.recent; i += kSelThreads) {
-    kept[a.keep - a.recent + i] = n + i;
-    if (kw) kw[a.keep - a.recent + i] = w[n + i];
-  }
+  if (csize > 1) cluster_sync();     // no CTA leaves while another reads its counts
 }
 
 constexpr int kGatThreads = 256;
 
 // One destination page of one head: threads 0..127 its keys, 128..255 its
 // values. The codes stay in registers between the maximum and the rounding.
-// NV = 16-code vectors per thread: page_size * head_dim / 16 / 128.
+// NV = 16-code vectors per thread: page_size * head_dim / 16 / 128. Bound by
+// HBM (a byte in and out per code); what costs is the chain of loads to the
+// source row (kept position, its page, scale and codes), so many small CTAs
+// per SM.
 template <int NV>
 __global__ void __launch_bounds__(kGatThreads) evict_gather_kernel(const EvictArgs a) {
   __shared__ int s_page[128];        // source page of each slot, -1: none
@@ -327,84 +426,87 @@ __global__ void __launch_bounds__(kGatThreads) evict_gather_kernel(const EvictAr
   const int blk = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   const int P = a.c.page_size, D = a.c.head_dim, H = a.c.n_kv_heads;
   bool bad = false;
+  const int page = __ldg(a.dst + (size_t)b * a.dst_width + blk);
+  const int i = tid < P && blk * P + tid < a.keep ? a.kept[((size_t)b * H + h) * a.keep + blk * P + tid] : -1;
   const int m = min(cut_length(a.lengths, b, a.width, P, a.w_stride, &bad), a.keep);
   if (blk * P >= m) return;
-  const int page = __ldg(a.dst + (size_t)b * a.dst_width + blk);
-  bool oob = page < 0 || page >= a.c.n_pages;
-  if (oob) {
+  if (page < 0 || page >= a.c.n_pages) {
     if (tid == 0 && a.status) atomicOr(a.status, MOE_DEV_INDEX_OOB);
     return;
   }
   const int slots = min(P, m - blk * P);
   if (tid < slots) {
-    const int i = a.kept[((size_t)b * H + h) * a.keep + blk * P + tid];
     const int sp = __ldg(a.table + (size_t)b * a.width + i / P);
-    uint8_t ks = 0, vs = 0;
     const bool in = sp >= 0 && sp < a.c.n_pages;
-    if (!in) {
-      if (a.status) atomicOr(a.status, MOE_DEV_INDEX_OOB);
-    } else {
-      ks = a.c.k_scales[(size_t)sp * H + h];
-      vs = a.c.v_scales[(size_t)sp * H + h];
-    }
+    if (!in && a.status) atomicOr(a.status, MOE_DEV_INDEX_OOB);
     s_page[tid] = in ? sp : -1;
     s_slot[tid] = uint8_t(i % P);
-    s_scale[0][tid] = ks;
-    s_scale[1][tid] = vs;
+    s_scale[0][tid] = in ? a.c.k_scales[(size_t)sp * H + h] : 0;
+    s_scale[1][tid] = in ? a.c.v_scales[(size_t)sp * H + h] : 0;
   }
   __syncthreads();
   const int part = tid >> 7, pt = tid & 127;
   uint8_t* codes = static_cast<uint8_t*>(part ? a.c.v_codes : a.c.k_codes);
-  const int cpr = D / 16, n = slots * cpr;
+  const int cpr = D / 16, row = pt / cpr, col = (pt % cpr) * 16, rows = 128 / cpr;   // first vector's slot; slots to the next
   uint4 x[NV];
   int sc[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = i * 128 + pt;
-    x[i] = make_uint4(0, 0, 0, 0);
-    sc[i] = 0;
-    if (v < n) {
-      const int sp = s_page[v / cpr];
+  for (int v = 0; v < NV; ++v) {
+    const int s = row + v * rows;
+    x[v] = make_uint4(0, 0, 0, 0);
+    sc[v] = 0;
+    if (s < slots) {
+      const int sp = s_page[s];
       if (sp >= 0) {
-        const size_t row = ((size_t)sp * H + h) * P + s_slot[v / cpr];
-        x[i] = *reinterpret_cast<const uint4*>(codes + row * D + (v % cpr) * 16);
-        sc[i] = s_scale[part][v / cpr];
+        x[v] = *reinterpret_cast<const uint4*>(codes + (((size_t)sp * H + h) * P + s_slot[s]) * D + col);
+        sc[v] = s_scale[part][s];
       }
     }
   }
   float top = 0.0f;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-    uint32_t mag = 0;   // E4M3 magnitudes order as their codes do
+  for (int v = 0; v < NV; ++v) {
+    // E4M3 magnitudes order as their codes do; NaN's is the largest
+    const uint32_t w[4] = {x[v].x, x[v].y, x[v].z, x[v].w};
+    uint32_t mag = 0;
+    const bool nan = any_nan4(w[0]) || any_nan4(w[1]) || any_nan4(w[2]) || any_nan4(w[3]);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const uint32_t c = (w[j >> 2] >> (8 * (j & 3))) & 0x7Fu;
-      if (c != 0x7Fu) mag = max(mag, c);
+    for (int j = 0; j < 4; ++j) mag = __vmaxu2(mag, __vmaxu2(w[j] & 0x007F007Fu, (w[j] >> 8) & 0x007F007Fu));
+    mag = max(mag & 0xFFFFu, mag >> 16);
+    if (nan) {
+      mag = 0;
+#pragma unroll 1
+      for (int j = 0; j < 16; ++j) {
+        const uint32_t c = (w[j >> 2] >> (8 * (j & 3))) & 0x7Fu;
+        if (c != 0x7Fu) mag = max(mag, c);
+      }
     }
-    if (mag) top = fmaxf(top, scale2(e4m3_to_f32(mag), sc[i] - 127));
+    // its value times 2^(sc - 127), which may leave fp32's normal range: in two factors
+    const int e = sc[v] - 127;
+    top = fmaxf(top, e4m3_to_f32(mag) * pow2(e / 2) * pow2(e - e / 2));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
   if (lane == 0) s_max[warp] = top;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) top = fmaxf(top, s_max[part * 4 + i]);
+  for (int k = 0; k < 4; ++k) top = fmaxf(top, s_max[part * 4 + k]);
   const int byte = kv_scale_byte(top);
   if (pt == 0) (part ? a.c.v_scales : a.c.k_scales)[(size_t)page * H + h] = uint8_t(byte);
   uint8_t* to = codes + ((size_t)page * H + h) * P * D;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = i * 128 + pt;
-    if (v >= n) break;
-    uint4 c = x[i];
-    if (sc[i] != byte) {
-      c.x = kv_rescale4(c.x, sc[i] - byte);
-      c.y = kv_rescale4(c.y, sc[i] - byte);
-      c.z = kv_rescale4(c.z, sc[i] - byte);
-      c.w = kv_rescale4(c.w, sc[i] - byte);
+  for (int v = 0; v < NV; ++v) {
+    const int s = row + v * rows;
+    if (s >= slots) break;
+    uint4 c = x[v];
+    if (sc[v] != byte) {
+      const float f = kv_factor(min(sc[v] - byte, 127), 0);   // a larger one than 2^127 meets zeros only
+      c.x = kv_rescale4(c.x, f);
+      c.y = kv_rescale4(c.y, f);
+      c.z = kv_rescale4(c.z, f);
+      c.w = kv_rescale4(c.w, f);
     }
-    *reinterpret_cast<uint4*>(to + (size_t)v * 16) = c;
+    *reinterpret_cast<uint4*>(to + s * D + col) = c;
   }
 }
 
@@ -427,12 +529,26 @@ int launch_kv_append(const AppendArgs& a, cudaStream_t s) {
 }
 
 int launch_kv_evict(const EvictArgs& a, const DeviceInfo& di, cudaStream_t s) {
-  (void)di;
   const int P = a.c.page_size;
-  evict_select_kernel<<<dim3(a.c.n_kv_heads, a.n_seq), kSelThreads, 0, s>>>(a);
-  int st = launch_status();
-  if (st != MOE_OK) return st;
-  const int64_t most = (int64_t)a.width * P < a.keep ? (int64_t)a.width * P : a.keep;
+  const int64_t cap = std::min((int64_t)a.width * P, a.w_stride);
+  // more CTAs per pair while each keeps enough positions and all run at once
+  int csize = 1;
+  while (csize < kSelCluster && (int64_t)csize * kSelEach < cap &&
+         2 * (int64_t)csize * a.c.n_kv_heads * a.n_seq <= di.sm_count)
+    csize *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(a.c.n_kv_heads * csize, a.n_seq);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = csize;
+  at.val.clusterDim.y = 1;
+  at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, evict_select_kernel, a, csize));
+  const int64_t most = std::min((int64_t)a.width * P, (int64_t)a.keep);
   if (most == 0) return MOE_OK;
   const dim3 grid(unsigned((most + P - 1) / P), a.c.n_kv_heads, a.n_seq);
   switch (P * a.c.head_dim / 16 / 128) {
