@@ -20,24 +20,37 @@
 // from, as the A operand of the second product.
 //
 // Warp roles, meeting only at mbarriers:
-//   producer (one thread)  Q tiles, then K0 V0 K1 V1 ... by TMA into a ring
-//   MMA (one thread)       S_t = Q_t K^T, then per key tile and query tile
-//                          O_t += P_t V and the next S_t: while the tensor
-//                          cores do one tile's pair of products, the other
-//                          tile's softmax runs
-//   scheduler (one warp)   the next item
+//   producer (one warp)    the next item; this one's Q tiles, then K0 V0 K1 V1
+//                          ... by TMA into a ring
+//   MMA 0, 1 (a warp each) of its query tile: S = Q K^T, then per key tile
+//                          O += P V in two halves and the next S. A warp is held
+//                          while it issues (the tensor cores take few MMAs
+//                          ahead), so one for both tiles would see late that the
+//                          other tile is ready: it took 0.45 of the time
 //   scan (one warp)        masked key tiles only, see below
-//   softmax 0, 1 (4 warps each, one thread per query): S to registers, maximum,
+//   softmax 0, 1 (4 warps each, one thread per query): S to registers,
 //                          probabilities (fp32 sum, bf16 store), and at the end
-//                          O / sum. The reference maximum is raised only when
-//                          it is passed by 2^8 (bf16 has fp32's range, and the
-//                          sum is fp32), so O is rescaled rarely.
+//                          O / sum
+//
+// What bounds it: a query tile's chain S -> softmax -> P V -> next S against the
+// other tile's products. 128 x 128 scores take the special-function units 512
+// cycles (32 a cycle, measured) and the tensor cores 1024 for both products, so
+// the chain must not be much longer than 2048. Therefore
+//   - a tile's scores are worked on in two halves of 64 keys, and a half's
+//     probabilities are taken against the reference that was there: bf16 and
+//     fp32 have range enough for what lies up to 2^64 above it. A reference that
+//     was passed by 2^8 is raised, and O rescaled, when the next tile's scores
+//     arrive; one passed by more than 2^64 is raised at once;
+//   - the first 64 keys' probabilities are handed over as soon as they are
+//     stored, and their product runs while the other 64 are computed.
+// Maximum first and one hand-over took 3560 cycles per pair of tiles.
 //
 // Masked places must not count, whatever they hold, but 0 * inf is NaN in the
 // second product. For a tile that some query of the item does not see whole the
-// scan warp zeroes the value rows past the sequence's end and looks for
-// non-finite values in the others; only if it finds one (a broken model) the
-// softmax threads add that tile's visible products themselves.
+// scan warp zeroes the value rows past the sequence's end, and non-finite
+// values in the others. Where it found one (a broken model) the queries that
+// see it get it back at the end: the thread of the query reads the tile's
+// values from global memory and adds the non-finite ones to its output.
 #include <cuda.h>
 
 #include "attn.h"
@@ -50,13 +63,10 @@ namespace moe {
 namespace {
 
 constexpr int kQT = 128, kKT = 128;            // queries per tile, keys per tile
-constexpr int kWProd = 0, kWMma = 1, kWSched = 2, kWScan = 3, kWSoft = 4;
-constexpr int kPfWarps = 12;
+constexpr int kWProd = 0, kWMma0 = 1, kWMma1 = 2, kWSoft = 4;   // and 3: scan
+constexpr int kPfWarps = 12;   // 168 registers a thread
 constexpr int kPfThreads = kPfWarps * 32;
-constexpr int kRegsCtl = 88, kRegsSoft = 208;  // registers after the split
-constexpr int kRegsLaunch = 168;
-static_assert(4 * kRegsCtl + 8 * kRegsSoft <= kPfWarps * kRegsLaunch, "register split exceeds the launch's total");
-constexpr float kPfRaise = 8.0f;
+constexpr float kPfRaise = 8.0f, kPfMost = 64.0f;   // log2 of what the reference may be passed by: for long, at all
 constexpr uint32_t kBoxBytes = 128 * 128;      // 128 rows of 64 channels
 constexpr int kScanRing = 4;
 constexpr float kLn2f = 0.6931471805599453f, kLog2ef = 1.4426950408889634f;
@@ -67,7 +77,7 @@ struct PfPlan {
   static constexpr uint32_t kTile = kBoxes * kBoxBytes;
   static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr uint32_t kQ = 0, kRing = 2 * kTile, kBars = kRing + kStages * kTile;
-  static constexpr int kNBars = 2 + 2 * kStages + 8 + 2 * kScanRing + 4;
+  static constexpr int kNBars = 2 + 2 * kStages + 14 + kScanRing + 4;
   static constexpr uint32_t kItems = kBars + kNBars * 8;
   static constexpr uint32_t kTotal = kItems + 2 * 80 + kScanRing * 4 + 16 + 1024;   // + alignment slack
 };
@@ -90,12 +100,30 @@ struct PfParams {
 };
 
 // ---- tensor-memory helpers -------------------------------------------------------
-__device__ __forceinline__ void umma_bf16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
-                                             bool accumulate) {
+// The MMA warp runs as a whole and lets one lane issue: its operands then are
+// uniform for the compiler and live in uniform registers, which the instructions
+// want; from within a branch of one lane each of them is moved there first.
+__device__ __forceinline__ void umma_ss_1(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          bool accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_d),
+      "{\n .reg .pred p, q;\n elect.sync _|q, 0xFFFFFFFF;\n setp.ne.b32 p, %4, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+// A in tensor memory.
+__device__ __forceinline__ void umma_ts_1(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+                                          bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n elect.sync _|q, 0xFFFFFFFF;\n setp.ne.b32 p, %4, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_d),
       "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_1(uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xFFFFFFFF;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
       : "memory");
 }
 // Descriptor of an operand whose rows (keys) are K and whose 64-channel boxes
@@ -109,6 +137,8 @@ __device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t saddr, uint32_t 
   d |= (uint64_t)2 << 61;
   return d;
 }
+#define MOE_RW8(v, i) "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]), "+r"(v[i + 5]), \
+                      "+r"(v[i + 6]), "+r"(v[i + 7])
 #define MOE_R8(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), \
                      "=r"(v[i + 6]), "=r"(v[i + 7])
 // 32 columns of the warp's lanes; no wait.
@@ -119,7 +149,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
       : MOE_R8(v, 0), MOE_R8(v, 8), MOE_R8(v, 16), MOE_R8(v, 24)
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// ... and the values of a load come after it, for the compiler too.
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : MOE_RW8(v, 0), MOE_RW8(v, 8), MOE_RW8(v, 16), MOE_RW8(v, 24)::"memory");
+}
+__device__ __forceinline__ void tie32(uint32_t (&v)[32]) {
+  asm volatile("" : MOE_RW8(v, 0), MOE_RW8(v, 8), MOE_RW8(v, 16), MOE_RW8(v, 24));
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 #define MOE_I8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), \
                      "r"(v[i + 6]), "r"(v[i + 7])
@@ -127,13 +164,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
       MOE_I8(v, 0), MOE_I8(v, 8)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      MOE_I8(v, 0), MOE_I8(v, 8), MOE_I8(v, 16), MOE_I8(v, 24)
       : "memory");
 }
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
@@ -148,18 +178,15 @@ __device__ __forceinline__ float pf_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
-}
-template <int R>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
-}
-template <int R>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
 // ---- the list of items ---------------------------------------------------------------
@@ -275,12 +302,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
   uint64_t* full = q_empty + 1;
   uint64_t* empty = full + NS;
   uint64_t* s_full = empty + NS;       // [2]
-  uint64_t* p_full = s_full + 2;       // [2]
-  uint64_t* o_full = p_full + 2;       // [2]
+  uint64_t* p_full = s_full + 2;       // [2][2]: query tile, half of the keys
+  uint64_t* h_done = p_full + 4;       // [2]: the first half's product
+  uint64_t* o_full = h_done + 2;       // [2]
   uint64_t* o_free = o_full + 2;       // [2]
   uint64_t* scanned = o_free + 2;      // [kScanRing]
-  uint64_t* scan_go = scanned + kScanRing;   // [kScanRing]
-  uint64_t* it_full = scan_go + kScanRing;   // [2]
+  uint64_t* fin = scanned + kScanRing;       // [2]: a warp's MMAs at the end
+  uint64_t* it_full = fin + 2;               // [2]
   uint64_t* it_empty = it_full + 2;          // [2]
   PfItem* items = reinterpret_cast<PfItem*>(smem + Plan::kItems);
   volatile int* poison = reinterpret_cast<volatile int*>(smem + Plan::kItems + 2 * 80);   // [kScanRing]
@@ -294,27 +322,27 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
 
   if (tid == 0) {
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    mbar_init(q_empty, 2);         // both MMA warps
     for (int i = 0; i < NS; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], 3);     // both MMA warps, scan
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[2 * i], 4);
+      mbar_init(&p_full[2 * i + 1], 4);
+      mbar_init(&h_done[i], 1);
       mbar_init(&o_full[i], 1);
       mbar_init(&o_free[i], 4);
       mbar_init(&it_full[i], 1);
-      mbar_init(&it_empty[i], 11);   // producer, MMA, scan, 8 softmax warps
+      mbar_init(&fin[i], 1);
+      mbar_init(&it_empty[i], 11);   // 2 MMA, scan, 8 softmax warps
     }
-    for (int i = 0; i < kScanRing; ++i) {
-      mbar_init(&scanned[i], 1);
-      mbar_init(&scan_go[i], 1);
-    }
+    for (int i = 0; i < kScanRing; ++i) mbar_init(&scanned[i], 1);
     *abort = 0;
     mbar_fence_init();
   }
-  if (warp == kWMma) tmem_alloc(tslot, 512);
+  if (warp == kWMma0) tmem_alloc(tslot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -333,52 +361,54 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
   };
 
   if (warp < kWSoft) {
-    regs_dec<kRegsCtl>();
-    if (warp == kWSched) {
-      // ---- scheduler --------------------------------------------------------------------
-      bool bad = false;
+    if (warp == kWProd) {
+      // ---- producer: items, and their loads -------------------------------------------------
+      bool bad = false, ok = true;
       int total = 0;
       for (int b = lane; b < a.n_seq; b += 32) total += pf_seq(a, G, b, &bad).pairs;
       total = warp_sum(total) * a.n_kv;
       bad = __any_sync(0xFFFFFFFFu, bad);
       if (bad && blockIdx.x == 0 && lane == 0 && status) atomicOr(status, MOE_DEV_INDEX_OOB);
       const int N = gridDim.x, c = blockIdx.x;
-      for (int t = 0;; ++t) {
-        if (t >= 2 && !uwait(&it_empty[t & 1], uint32_t((t >> 1) - 1) & 1u, abort, status)) break;
-        const int64_t idx = (int64_t)t * N + (t & 1 ? N - 1 - c : c);
-        const bool done = idx >= total;
-        if (done) {
-          if (lane == 0) items[t & 1].n = -1;
-        } else {
-          pf_find_item(P, G, int(idx), total > N, &items[t & 1]);
+      // item t of this CTA into its slot; false if there is none (nor any later)
+      auto publish = [&](int t) {
+        if (t >= 2 && !uwait(&it_empty[t & 1], uint32_t((t >> 1) - 1) & 1u, abort, status)) {
+          ok = false;
+          return false;
         }
+        const int64_t idx = (int64_t)t * N + (t & 1 ? N - 1 - c : c);
+        if (idx < total)
+          pf_find_item(P, G, int(idx), total > N, &items[t & 1]);
+        else if (lane == 0)
+          items[t & 1].n = -1;
         __threadfence_block();
         __syncwarp();
         if (lane == 0) mbar_arrive(&it_full[t & 1]);
-        if (done) break;   // this CTA's later indices are larger still
-      }
-    } else if (warp == kWProd) {
-      // ---- producer ---------------------------------------------------------------------
-      if (lane == 0) {
-        int p = 0, issued_q = 0;
-        bool ok = true;
-        PfItem it;
-        for (int t = 0; ok && next_item(t, true, &it); ++t) {
-          if (it.n == 0) continue;
+        return idx < total;
+      };
+      int s = 0, issued_q = 0, loads = 0;   // ring stage
+      uint32_t par = 1;                     // phase of its release: the first lap waits for none
+      bool more = publish(0);
+      for (int t = 0; ok && more; ++t) {
+        more = publish(t + 1);              // found while this item's tail of the ring is worked off
+        const PfItem& it = items[t & 1];
+        if (lane == 0 && it.n > 0) {
           // Q: after the last products with the previous item's
-          if (issued_q > 0 && !uwait(q_empty, uint32_t(issued_q - 1) & 1u, abort, status)) break;
-          const int have1 = it.rows[1] > 0;
-          mbar_arrive_expect_tx(q_full, (1 + have1) * Plan::kTile);
-          for (int j = 0; j <= have1; ++j)
-            for (int x = 0; x < NB; ++x) {
-              const int h = P.one_head[0] ? 0 : it.head[j], r = it.q0[j];
-              tma_load_3d(q_s + j * Plan::kTile + x * kBoxBytes, &P.map[0], x * 64, P.swapped[0] ? r : h,
-                          P.swapped[0] ? h : r, q_full);
-            }
-          ++issued_q;
-          for (int i = 0; i < 2 * it.n; ++i, ++p) {
-            const int s = p % NS, w = 1 + (i & 1);
-            if (p >= NS && !uwait(&empty[s], uint32_t(p / NS - 1) & 1u, abort, status)) {
+          if (issued_q > 0 && !uwait(q_empty, uint32_t(issued_q - 1) & 1u, abort, status)) ok = false;
+          if (ok) {
+            const int have1 = it.rows[1] > 0;
+            mbar_arrive_expect_tx(q_full, (1 + have1) * Plan::kTile);
+            for (int j = 0; j <= have1; ++j)
+              for (int x = 0; x < NB; ++x) {
+                const int h = P.one_head[0] ? 0 : it.head[j], r = it.q0[j];
+                tma_load_3d(q_s + j * Plan::kTile + x * kBoxBytes, &P.map[0], x * 64, P.swapped[0] ? r : h,
+                            P.swapped[0] ? h : r, q_full);
+              }
+            ++issued_q;
+          }
+          for (int i = 0; ok && i < 2 * it.n; ++i) {
+            const int w = 1 + (i & 1);
+            if (loads >= NS && !uwait(&empty[s], par, abort, status)) {
               ok = false;
               break;
             }
@@ -387,154 +417,150 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
             for (int x = 0; x < NB; ++x)
               tma_load_3d(ring_s + s * Plan::kTile + x * kBoxBytes, &P.map[w], x * 64, P.swapped[w] ? r : h,
                           P.swapped[w] ? h : r, &full[s]);
+            ++loads;
+            if (++s == NS) s = 0, par ^= 1;
           }
         }
-        if (*abort) {   // copies in flight land before the CTA's shared memory goes away
-          for (int i = p > NS ? p - NS : 0; i < p; ++i) mbar_wait(&full[i % NS], uint32_t(i / NS) & 1u, status);
-          if (issued_q > 0) mbar_wait(q_full, uint32_t(issued_q - 1) & 1u, status);
-        }
+        ok = __all_sync(0xFFFFFFFFu, ok);
       }
-    } else if (warp == kWMma) {
+      if (lane == 0 && *abort) {   // copies in flight land before the CTA's shared memory goes away
+        for (int i = loads > NS ? loads - NS : 0; i < loads; ++i) mbar_wait(&full[i % NS], uint32_t(i / NS) & 1u, status);
+        if (issued_q > 0) mbar_wait(q_full, uint32_t(issued_q - 1) & 1u, status);
+      }
+    } else if (warp == kWMma0 || warp == kWMma1) {
       // ---- MMA --------------------------------------------------------------------------
-      if (lane == 0) {
-        const uint32_t id_s = umma_idesc_bf16(kQT, kKT) | (P.negate ? 1u << 13 : 0u);   // bit 13: negate A
-        const uint32_t id_o = umma_idesc_bf16(kQT, D) | (1u << 16);                     // bit 16: B is MN-major
-        int p = 0, nq = 0, ns = 0;       // ring position; items with Q; masked tiles seen
-        int np[2] = {0, 0}, no[2] = {0, 0};   // probabilities awaited; items begun, per query tile
-        uint64_t* last = nullptr;
-        uint32_t last_par = 0;
-        bool ok = true;
-        PfItem it;
-        auto scores = [&](int j, int s) {
-          const uint32_t k0 = ring_s + s * Plan::kTile, q0 = q_s + j * Plan::kTile;
+      // The whole warp; what is needed per key tile is kept up to date by
+      // additions (no division by the ring's length, no descriptor built anew).
+      constexpr uint32_t kTile16 = Plan::kTile >> 4, kBox16 = kBoxBytes >> 4;
+      const int j = warp == kWMma1;
+      const uint32_t id_s = umma_idesc_bf16(kQT, kKT) | (P.negate ? 1u << 13 : 0u);   // bit 13: negate A
+      const uint32_t id_o = umma_idesc_bf16(kQT, D) | (1u << 16);                     // bit 16: B is MN-major
+      const uint64_t dq = umma_desc_sw128(q_s + j * Plan::kTile);
+      const uint64_t dk = umma_desc_sw128(ring_s), dv = umma_desc_mn_sw128(ring_s, kBoxBytes);
+      const uint32_t ts = tmem + j * kKT, to = tmem + 256 + j * D;
+      const uint32_t empty_s = smem_addr(empty), q_empty_s = smem_addr(q_empty);
+      uint32_t st = 0, par = 0;                      // ring stage and phase
+      uint32_t q_par = 0, p_par = 0, o_par = 1;      // phases of Q, of the probabilities, of O's release
+      bool ok = true, o_used = false;
+      auto wait = [&](uint64_t* bar, uint32_t ph) {
+        if (__any_sync(0xFFFFFFFFu, mbar_try_wait(bar, ph))) return true;
+        return bool(__all_sync(0xFFFFFFFFu, uwait(bar, ph, abort, status)));
+      };
+      auto scores = [&]() {
+        const uint64_t b0 = dk + st * kTile16;
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t o = (kk >> 2) * kBoxBytes + (kk & 3) * 32;
-            umma_bf16(tmem + j * kKT, umma_desc_sw128(q0 + o), umma_desc_sw128(k0 + o), id_s, kk > 0);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t o = (kk >> 2) * kBox16 + (kk & 3) * 2;
+          umma_ss_1(ts, dq + o, b0 + o, id_s, kk > 0);
+        }
+        umma_commit_1(smem_addr(&s_full[j]));
+      };
+      auto next_stage = [&]() {      // this warp is done with the stage
+        umma_commit_1(empty_s + 8 * st);
+        if (++st == NS) st = 0, par ^= 1;
+      };
+      PfItem it;
+      for (int t = 0; ok && __all_sync(0xFFFFFFFFu, next_item(t, lane == 0, &it)); ++t) {
+        const int n = __shfl_sync(0xFFFFFFFFu, it.n, 0);
+        const int nkt = __shfl_sync(0xFFFFFFFFu, j ? it.nkt[1] : it.nkt[0], 0);
+        if (n == 0) continue;
+        if (!(ok = wait(q_full, q_par)) || !(ok = wait(&full[st], par))) break;
+        q_par ^= 1;
+        tc_fence_after();
+        if (nkt > 0) scores();
+        next_stage();
+        if (n == 1) umma_commit_1(q_empty_s);
+        for (int i = 0; i < n; ++i) {
+          if (!(ok = wait(&full[st], par))) break;
+          if (i < nkt) {
+            if (i == 0) {              // the last item's output has been read
+              if (o_used && !(ok = wait(&o_free[j], o_par))) break;
+              o_used = true;
+              o_par ^= 1;
+            }
+            const uint64_t b0 = dv + st * kTile16;
+            if (!(ok = wait(&p_full[2 * j], p_par))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < kKT / 32; ++kk) umma_ts_1(to, ts + kk * 8, b0 + kk * 128, id_o, kk > 0 || i > 0);
+            umma_commit_1(smem_addr(&h_done[j]));
+            if (!(ok = wait(&p_full[2 * j + 1], p_par))) break;
+            p_par ^= 1;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = kKT / 32; kk < kKT / 16; ++kk) umma_ts_1(to, ts + kk * 8, b0 + kk * 128, id_o, true);
           }
-          umma_commit(&s_full[j]);
-        };
-        for (int t = 0; ok && next_item(t, true, &it); ++t) {
-          if (it.n == 0) continue;
-          if (!uwait(q_full, uint32_t(nq++) & 1u, abort, status)) break;
-          const int s0 = p % NS;
-          if (!uwait(&full[s0], uint32_t(p / NS) & 1u, abort, status)) break;
-          tc_fence_after();
-          for (int j = 0; j < 2; ++j)
-            if (it.nkt[j] > 0) scores(j, s0);
-          umma_commit(&empty[s0]);
-          last = &empty[s0];
-          last_par = uint32_t(p / NS) & 1u;
-          if (it.n == 1) umma_commit(q_empty);
-          ++p;
-          for (int i = 0; i < it.n && ok; ++i) {
-            const int sv = p % NS, sk = (p + 1) % NS;
-            const bool more = i + 1 < it.n, masked = (i + 1) * kKT > it.vmin;
-            if (!uwait(&full[sv], uint32_t(p / NS) & 1u, abort, status)) {
-              ok = false;
-              break;
-            }
-            if (masked) mbar_arrive(&scan_go[ns & (kScanRing - 1)]);
-            bool have_k = false;
-            for (int j = 0; j < 2; ++j) {
-              if (i >= it.nkt[j]) continue;
-              if (i == 0 && no[j]++ > 0 && !uwait(&o_free[j], uint32_t(no[j] - 2) & 1u, abort, status)) {
-                ok = false;
-                break;
-              }
-              if (!uwait(&p_full[j], uint32_t(np[j]++) & 1u, abort, status)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              if (!(masked && poison[ns & (kScanRing - 1)])) {
-                const uint32_t v0 = ring_s + sv * Plan::kTile;
-#pragma unroll
-                for (int kk = 0; kk < kKT / 16; ++kk)
-                  umma_bf16_ts(tmem + 256 + j * D, tmem + j * kKT + kk * 8, umma_desc_mn_sw128(v0 + kk * 2048, kBoxBytes),
-                               id_o, i > 0 || kk > 0);
-              }
-              if (i + 1 < it.nkt[j]) {
-                if (!have_k) {
-                  if (!uwait(&full[sk], uint32_t((p + 1) / NS) & 1u, abort, status)) {
-                    ok = false;
-                    break;
-                  }
-                  tc_fence_after();
-                  have_k = true;
-                }
-                scores(j, sk);
-              } else {
-                umma_commit(&o_full[j]);
-              }
-            }
-            if (!ok) break;
-            umma_commit(&empty[sv]);
-            last = &empty[sv];
-            last_par = uint32_t(p / NS) & 1u;
-            ++p;
-            if (more) {
-              umma_commit(&empty[sk]);
-              last = &empty[sk];
-              last_par = uint32_t(p / NS) & 1u;
-              ++p;
-              if (i + 2 == it.n) umma_commit(q_empty);
-            }
-            if (masked) ++ns;
+          next_stage();
+          if (i + 1 == nkt) umma_commit_1(smem_addr(&o_full[j]));
+          if (i + 1 < n) {
+            if (!(ok = wait(&full[st], par))) break;
+            tc_fence_after();
+            if (i + 1 < nkt) scores();
+            next_stage();
+            if (i + 2 == n) umma_commit_1(q_empty_s);
           }
         }
-        // every MMA has finished before tensor memory is freed
-        if (last) mbar_wait(last, last_par, status);
       }
+      // every MMA has finished before tensor memory is freed
+      umma_commit_1(smem_addr(&fin[j]));
+      mbar_wait(&fin[j], 0, status);
     } else {
       // ---- scan -------------------------------------------------------------------------
-      int p0 = 0, ns = 0;
+      int s = 0, ns = 0;             // ring stage; masked tiles
+      uint32_t par = 0;
       PfItem it;
-      for (int t = 0; next_item(t, lane == 0, &it); ++t) {
-        bool ok = true;
-        for (int i = it.vmin / kKT; i < it.n && ok; ++i, ++ns) {
-          // the MMA thread says when the values are there: it alone has waited
-          // for every earlier phase of their stage
-          const int p = p0 + 2 * i + 1, s = p % NS;
-          if (!uwait(&scan_go[ns & (kScanRing - 1)], uint32_t(ns / kScanRing) & 1u, abort, status) ||
-              !uwait(&full[s], uint32_t(p / NS) & 1u, abort, status)) {
+      bool ok = true;
+      for (int t = 0; ok && next_item(t, lane == 0, &it); ++t) {
+        for (int e = 0; e < 2 * it.n; ++e) {
+          const int i = e >> 1;
+          if (!uwait(&full[s], par, abort, status)) {
             ok = false;
             break;
           }
-          uint8_t* v = smem + Plan::kRing + s * Plan::kTile;
-          const int rows = min(kKT, it.nk - i * kKT);
-          uint32_t found = 0;
-          for (int x = 0; x < NB; ++x) {
-            uint4* box = reinterpret_cast<uint4*>(v + x * kBoxBytes);
-            for (int e = lane; e < rows * 8; e += 32) {
-              const uint4 w = box[e];
-              // a half has exponent 255 iff adding one to its exponent field carries into its sign
-              found |= ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
-                       ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
+          if ((e & 1) && (i + 1) * kKT > it.vmin) {
+            uint8_t* v = smem + Plan::kRing + s * Plan::kTile;
+            const int rows = min(kKT, it.nk - i * kKT);
+            uint32_t found = 0;
+            for (int x = 0; x < NB; ++x) {
+              uint4* box = reinterpret_cast<uint4*>(v + x * kBoxBytes);
+              for (int e = lane; e < rows * 8; e += 32) {
+                const uint4 w = box[e];
+                // a half has exponent 255 iff adding one to its exponent field carries into its sign
+                found |= ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
+                         ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
+              }
+              for (int e = rows * 8 + lane; e < kKT * 8; e += 32) box[e] = make_uint4(0, 0, 0, 0);
             }
-            for (int e = rows * 8 + lane; e < kKT * 8; e += 32) box[e] = make_uint4(0, 0, 0, 0);
+            const bool any = __any_sync(0xFFFFFFFFu, (found & 0x80008000u) != 0);
+            if (any) {
+              for (int e = lane; e < rows * 64 * NB / 2; e += 32) {   // two values at a time
+                uint32_t* p2 = reinterpret_cast<uint32_t*>(v + (e / (rows * 32)) * kBoxBytes) + e % (rows * 32);
+                const uint32_t w = *p2;
+                *p2 = ((w & 0x7F80u) == 0x7F80u ? 0u : w & 0xFFFFu) | ((w & 0x7F800000u) == 0x7F800000u ? 0u : w & 0xFFFF0000u);
+              }
+            }
+            fence_async_smem();   // the zeros, before the tensor cores read them
+            __syncwarp();
+            if (lane == 0) {
+              poison[ns & (kScanRing - 1)] = any ? 1 : 0;
+              __threadfence_block();
+              mbar_arrive(&scanned[ns & (kScanRing - 1)]);
+            }
+            ++ns;
           }
-          const bool any = __any_sync(0xFFFFFFFFu, (found & 0x80008000u) != 0);
-          fence_async_smem();   // the zeros, before the tensor cores read them
           __syncwarp();
-          if (lane == 0) {
-            poison[ns & (kScanRing - 1)] = any ? 1 : 0;
-            __threadfence_block();
-            mbar_arrive(&scanned[ns & (kScanRing - 1)]);
-          }
+          if (lane == 0) mbar_arrive(&empty[s]);
+          if (++s == NS) s = 0, par ^= 1;
         }
-        if (!ok) break;
-        p0 += 2 * it.n;
       }
     }
   } else {
-    regs_inc<kRegsSoft>();
     // ---- softmax ------------------------------------------------------------------------
     const int j = (warp - kWSoft) >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lanes = uint32_t(quarter * 32) << 16;
     const uint32_t ts = tmem + lanes + j * kKT, to = tmem + lanes + 256 + j * D;
-    int nsf = 0, nof = 0, ns = 0, p0 = 0;   // scores and outputs awaited; masked tiles; ring position
+    int nsf = 0, nof = 0, ns = 0;   // scores and outputs awaited; masked tiles
     bool ok = true;
     PfItem it;
     const float c = P.c;
@@ -542,7 +568,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
       const int nkt = it.nkt[j];
       const int vis = a.causal ? min(max(it.t0[j] + row + it.off + 1, 0), it.nk) : it.nk;
       const int vis_w = __shfl_sync(0xFFFFFFFFu, vis, 0);   // the warp's fewest
-      float m = -INFINITY, l = 0.0f;
+      float m = -INFINITY, l = 0.0f;   // reference, sum in units of 2^m
+      float m_next = -INFINITY;        // the reference to be
+      unsigned bad = 0;                // masked tiles with non-finite values (a pair's queries span at most 4)
       for (int i = 0; i < nkt; ++i) {
         const int k0 = i * kKT;
         const bool masked = k0 + kKT > it.vmin;
@@ -551,127 +579,109 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
           break;
         }
         tc_fence_after();
-        uint32_t s[kKT];
+        const int n_vis = vis - k0;
+        const bool cut = k0 + kKT > vis_w;   // some lane of the warp does not see the whole tile
+        float top = -INFINITY;               // the tile's maximum
+        uint32_t s[2][32];
+        tmem_ld32(ts, s[0]);
+        tmem_ld32(ts + 32, s[1]);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) tmem_ld32(ts + x * 32, s + x * 32);
-        tmem_wait_ld();
-        if (k0 + kKT > vis_w) {
-          const int n = vis - k0;
+        for (int half = 0; half < 2; ++half) {
+          tmem_wait_ld32(s[0]);
+          tie32(s[1]);
+          float mx[4];
 #pragma unroll
-          for (int x = 0; x < kKT; ++x)
-            if (x >= n) s[x] = 0xFF800000u;
-        }
-        float mx[4];
+          for (int b = 0; b < 2; ++b) {
+            uint32_t(&x)[32] = s[b];
+            if (cut) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) mx[x] = fmaxf(__uint_as_float(s[x]), __uint_as_float(s[x + 4]));
+              for (int y = 0; y < 32; ++y)
+                if (64 * half + 32 * b + y >= n_vis) x[y] = 0xFF800000u;
+            }
+            float a0 = __uint_as_float(x[0]), a1 = __uint_as_float(x[1]);
 #pragma unroll
-        for (int x = 8; x < kKT; x += 8)
+            for (int y = 2; y + 4 <= 30; y += 4) {
+              a0 = max3(a0, __uint_as_float(x[y]), __uint_as_float(x[y + 1]));
+              a1 = max3(a1, __uint_as_float(x[y + 2]), __uint_as_float(x[y + 3]));
+            }
+            mx[2 * b] = max3(a0, __uint_as_float(x[30]), __uint_as_float(x[31]));
+            mx[2 * b + 1] = a1;
+          }
+          const float mine = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
+          top = fmaxf(top, mine);
+          // the reference: raised for the last tile's sake, or for this half's
+          float r = half == 0 ? m_next : -INFINITY;
+          if ((i == 0 && half == 0) || mine > m + kPfMost) r = fmaxf(r, mine);
+          if (__any_sync(0xFFFFFFFFu, r > m)) {
+            const float f = r > m ? pf_ex2(m - r) : 1.0f;
+            if (r > m) m = r;
+            l *= f;
+            // what is in O: the earlier tiles' products, which have finished,
+            // since this tile's scores were issued after them, and in the second
+            // half this tile's first half's
+            if (half == 1) {
+              if (!uwait(&h_done[j], uint32_t(nsf - 1) & 1u, abort, status)) ok = false;
+              tc_fence_after();
+            }
+            if (i > 0 || half == 1) {
+#pragma unroll 1
+              for (int z = 0; z < D; z += 16) {
+                uint32_t o[16];
+                tmem_ld16(to + z, o);
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            mx[y] = fmaxf(mx[y], fmaxf(__uint_as_float(s[x + y]), __uint_as_float(s[x + y + 4])));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-        const bool raise = top > m + kPfRaise;
-        if (__any_sync(0xFFFFFFFFu, raise)) {
-          const float f = raise ? pf_ex2(m - top) : 1.0f;
-          if (raise) m = top;
-          l *= f;
-          if (i > 0) {
-            // the previous product has finished: this tile's scores were issued after it
-#pragma unroll
-            for (int x = 0; x < D; x += 32) {
-              uint32_t o[32];
-              tmem_ld32(to + x, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-              tmem_st32(to + x, o);
+                for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                tmem_st16(to + z, o);
+              }
             }
           }
-        }
-        const float ref = m == -INFINITY ? 0.0f : m;
-        const uint64_t c2 = pack2(c, c), r2 = pack2(-ref, -ref);
-        uint64_t sum0 = 0, sum1 = 0;
+          const float ref = m == -INFINITY ? 0.0f : m;
+          const uint64_t c2 = pack2(c, c), r2 = pack2(-ref, -ref);
 #pragma unroll
-        for (int x = 0; x < kKT; x += 32) {
-          uint32_t pb[16];
+          for (int b = 0; b < 2; ++b) {
+            uint32_t(&x)[32] = s[b];
+            float e[32];
 #pragma unroll
-          for (int y = 0; y < 32; y += 4) {
-            float e0, e1, e2, e3;
-            unpack2(fma2(pack2(__uint_as_float(s[x + y]), __uint_as_float(s[x + y + 1])), c2, r2), e0, e1);
-            unpack2(fma2(pack2(__uint_as_float(s[x + y + 2]), __uint_as_float(s[x + y + 3])), c2, r2), e2, e3);
-            e0 = pf_ex2(e0);
-            e1 = pf_ex2(e1);
-            e2 = pf_ex2(e2);
-            e3 = pf_ex2(e3);
-            sum0 = add2(sum0, pack2(e0, e1));
-            sum1 = add2(sum1, pack2(e2, e3));
-            pb[y / 2] = bf16x2_bits(e0, e1);
-            pb[y / 2 + 1] = bf16x2_bits(e2, e3);
+            for (int y = 0; y < 32; y += 2)
+              unpack2(fma2(pack2(__uint_as_float(x[y]), __uint_as_float(x[y + 1])), c2, r2), e[y], e[y + 1]);
+            if (half == 0) tmem_ld32(ts + 64 + 32 * b, x);   // the second half's scores
+#pragma unroll
+            for (int y = 0; y < 32; ++y) e[y] = pf_ex2(e[y]);
+            uint32_t pb[16];
+#pragma unroll
+            for (int y = 0; y < 16; ++y) pb[y] = bf16x2_bits(e[2 * y], e[2 * y + 1]);
+            tmem_st16(ts + 32 * half + 16 * b, pb);
+            uint64_t sum[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) sum[y] = add2(pack2(e[2 * y], e[2 * y + 1]), pack2(e[2 * y + 8], e[2 * y + 9]));
+#pragma unroll
+            for (int y = 16; y < 32; y += 8)
+#pragma unroll
+              for (int z = 0; z < 4; ++z) sum[z] = add2(sum[z], pack2(e[y + 2 * z], e[y + 2 * z + 1]));
+            float a0, a1;
+            unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a0, a1);
+            l += a0 + a1;
           }
-          tmem_st16(ts + x / 2, pb);
-        }
-        {
-          float x0, x1;
-          unpack2(add2(sum0, sum1), x0, x1);
-          l += x0 + x1;
-        }
-        tmem_wait_st();
-        if (masked) {
-          const int slot = ns & (kScanRing - 1);
-          if (!uwait(&scanned[slot], uint32_t(ns / kScanRing) & 1u, abort, status)) {
-            ok = false;
-            break;
-          }
-          ++ns;
-          if (poison[slot]) {
-            // this tile's visible products, by the thread of the query itself
-            const int pv = p0 + 2 * i + 1;
-            if (!uwait(&full[pv % NS], uint32_t(pv / NS) & 1u, abort, status)) {
-              ok = false;
-              break;
-            }
-            const uint8_t* v = smem + Plan::kRing + (pv % NS) * Plan::kTile;
-            for (int d0 = 0; d0 < D; d0 += 8) {
-              uint32_t o[8];
-              if (i > 0) {
-                tmem_ld8(to + d0, o);
-              } else {
-#pragma unroll
-                for (int y = 0; y < 8; ++y) o[y] = 0;
-              }
-              const uint8_t* vb = v + (d0 / 64) * kBoxBytes;
-              for (int k1 = 0; k1 < kKT; k1 += 16) {
-                uint32_t pk[8];
-                tmem_ld8(ts + k1 / 2, pk);
-#pragma unroll
-                for (int y = 0; y < 16; ++y) {
-                  const int key = k1 + y;
-                  if (k0 + key < vis) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(vb + key * 128 + (((d0 % 64) / 8) ^ (key & 7)) * 16);
-                    const float pr = y & 1 ? bf16_hi(pk[y / 2]) : bf16_lo(pk[y / 2]);
-                    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                      o[2 * z] = __float_as_uint(fmaf(pr, bf16_lo(ww[z]), __uint_as_float(o[2 * z])));
-                      o[2 * z + 1] = __float_as_uint(fmaf(pr, bf16_hi(ww[z]), __uint_as_float(o[2 * z + 1])));
-                    }
-                  }
-                }
-                __syncwarp();
-              }
-              asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(to + d0),
-                           MOE_I8(o, 0)
-                           : "memory");
+          if (half == 0) {
+            if (masked) {
+              const int slot = ns & (kScanRing - 1);
+              if (!uwait(&scanned[slot], uint32_t(ns / kScanRing) & 1u, abort, status)) ok = false;
+              ++ns;
+              if (poison[slot]) bad |= 1u << (i - it.vmin / kKT);
             }
             tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[2 * j]);
           }
         }
+        if (!ok) break;
+        if (top > m + kPfRaise) m_next = top;
+        tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[j]);
+        if (lane == 0) mbar_arrive(&p_full[2 * j + 1]);
       }
       if (!ok) break;
-      p0 += 2 * it.n;
       // masked tiles of the item that this query tile does not take part in
       {
         const int from = max(it.vmin / kKT, nkt);
@@ -691,7 +701,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
         uint32_t o[32];
         if (nkt > 0) {
           tmem_ld32(to + x, o);
-          tmem_wait_ld();
+          tmem_wait_ld32(o);
           if (x + 32 == D) {   // all of O is in registers: the next item may overwrite it
             tc_fence_before();
             __syncwarp();
@@ -700,6 +710,25 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
         } else {
 #pragma unroll
           for (int y = 0; y < 32; ++y) o[y] = 0;
+        }
+        for (unsigned left = bad; left; left &= left - 1) {
+          const int k0 = (it.vmin / kKT + __ffs(left) - 1) * kKT;
+          const __nv_bfloat16* v = a.v + (int64_t)(it.kv0 + k0) * a.v_ts + it.hk * a.v_hs + x;
+          const int keys = min(kKT, vis - k0);
+          for (int k = 0; k < keys; ++k) {
+            const uint4* w4 = reinterpret_cast<const uint4*>(v + k * a.v_ts);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const uint4 w = w4[y];
+              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                uint32_t &o0 = o[8 * y + 2 * z], &o1 = o[8 * y + 2 * z + 1];
+                if ((ww[z] & 0x7F80u) == 0x7F80u) o0 = __float_as_uint(__uint_as_float(o0) + bf16_lo(ww[z]));
+                if ((ww[z] & 0x7F800000u) == 0x7F800000u) o1 = __float_as_uint(__uint_as_float(o1) + bf16_hi(ww[z]));
+              }
+            }
+          }
         }
         uint32_t b[16];
 #pragma unroll
@@ -717,7 +746,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kWMma) {
+  if (warp == kWMma0) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -748,11 +777,6 @@ template <int D>
 int launch_pf(const PfParams& P, const DeviceInfo& di, cudaStream_t s) {
   constexpr uint32_t smem = PfPlan<D>::kTotal;
   if (smem > di.smem_optin) return MOE_ERR_UNSUPPORTED_SHAPE;
-  // the register split draws on what the launch gives: a build that launches
-  // with fewer registers would wait for ever
-  cudaFuncAttributes at;
-  MOE_CUDA_TRY(cudaFuncGetAttributes(&at, prefill_kernel<D>));
-  if (at.numRegs != kRegsLaunch) return MOE_ERR_CUDA;
   MOE_CUDA_TRY(cudaFuncSetAttribute(prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
   const int64_t G = P.a.n_heads / P.a.n_kv;
   const int64_t most = P.a.n_kv * (((int64_t)P.a.total_q / kQT + P.a.n_seq) * G / 2 + P.a.n_seq);
