@@ -77,7 +77,7 @@ struct PfPlan {
   static constexpr uint32_t kTile = kBoxes * kBoxBytes;
   static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr uint32_t kQ = 0, kRing = 2 * kTile, kBars = kRing + kStages * kTile;
-  static constexpr int kNBars = 2 + 2 * kStages + 14 + kScanRing + 4;
+  static constexpr int kNBars = 2 + 2 * kStages + 16 + kScanRing + 4;
   static constexpr uint32_t kItems = kBars + kNBars * 8;
   static constexpr uint32_t kTotal = kItems + 2 * 80 + kScanRing * 4 + 16 + 1024;   // + alignment slack
 };
@@ -124,6 +124,11 @@ __device__ __forceinline__ void umma_commit_1(uint32_t bar) {
   asm volatile(
       "{\n .reg .pred q;\n elect.sync _|q, 0xFFFFFFFF;\n"
       " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_1(uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xFFFFFFFF;\n @q mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(bar)
       : "memory");
 }
 // Descriptor of an operand whose rows (keys) are K and whose 64-channel boxes
@@ -308,7 +313,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
   uint64_t* o_free = o_full + 2;       // [2]
   uint64_t* scanned = o_free + 2;      // [kScanRing]
   uint64_t* fin = scanned + kScanRing;       // [2]: a warp's MMAs at the end
-  uint64_t* it_full = fin + 2;               // [2]
+  uint64_t* turn = fin + 2;                  // [2]: the other MMA warp has issued
+  uint64_t* it_full = turn + 2;              // [2]
   uint64_t* it_empty = it_full + 2;          // [2]
   PfItem* items = reinterpret_cast<PfItem*>(smem + Plan::kItems);
   volatile int* poison = reinterpret_cast<volatile int*>(smem + Plan::kItems + 2 * 80);   // [kScanRing]
@@ -336,6 +342,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
       mbar_init(&o_free[i], 4);
       mbar_init(&it_full[i], 1);
       mbar_init(&fin[i], 1);
+      mbar_init(&turn[i], 1);
       mbar_init(&it_empty[i], 11);   // 2 MMA, scan, 8 softmax warps
     }
     for (int i = 0; i < kScanRing; ++i) mbar_init(&scanned[i], 1);
@@ -441,6 +448,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
       const uint32_t empty_s = smem_addr(empty), q_empty_s = smem_addr(q_empty);
       uint32_t st = 0, par = 0;                      // ring stage and phase
       uint32_t q_par = 0, p_par = 0, o_par = 1;      // phases of Q, of the probabilities, of O's release
+      uint32_t turn_par = 1 - j;                     // tile 0 begins
       bool ok = true, o_used = false;
       auto wait = [&](uint64_t* bar, uint32_t ph) {
         if (__any_sync(0xFFFFFFFFu, mbar_try_wait(bar, ph))) return true;
@@ -472,13 +480,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
         if (n == 1) umma_commit_1(q_empty_s);
         for (int i = 0; i < n; ++i) {
           if (!(ok = wait(&full[st], par))) break;
+          const uint64_t b0 = dv + st * kTile16;
           if (i < nkt) {
             if (i == 0) {              // the last item's output has been read
               if (o_used && !(ok = wait(&o_free[j], o_par))) break;
               o_used = true;
               o_par ^= 1;
             }
-            const uint64_t b0 = dv + st * kTile16;
             if (!(ok = wait(&p_full[2 * j], p_par))) break;
             tc_fence_after();
 #pragma unroll
@@ -486,6 +494,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
             umma_commit_1(smem_addr(&h_done[j]));
             if (!(ok = wait(&p_full[2 * j + 1], p_par))) break;
             p_par ^= 1;
+          }
+          // the two tiles' second products and next scores strictly in turn
+          if (!(ok = wait(&turn[j], turn_par))) break;
+          turn_par ^= 1;
+          if (i < nkt) {
             tc_fence_after();
 #pragma unroll
             for (int kk = kKT / 32; kk < kKT / 16; ++kk) umma_ts_1(to, ts + kk * 8, b0 + kk * 128, id_o, true);
@@ -496,8 +509,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
             if (!(ok = wait(&full[st], par))) break;
             tc_fence_after();
             if (i + 1 < nkt) scores();
+            mbar_arrive_1(smem_addr(&turn[1 - j]));
             next_stage();
             if (i + 2 == n) umma_commit_1(q_empty_s);
+          } else {
+            mbar_arrive_1(smem_addr(&turn[1 - j]));
           }
         }
       }
