@@ -527,6 +527,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
               unpack2(mul2(pack2(s[mt][n][x], s[mt][n][x + 1]), f2), s[mt][n][x], s[mt][n][x + 1]);
           }
           if (!full) {
+            asm volatile("" ::: "memory");   // a branch, not selects in every chunk
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
