@@ -50,6 +50,7 @@ namespace {
 constexpr int kMaxSeqs = 4096;
 constexpr float kRaise = 30.0f;    // log2 by which a score may pass the reference
 constexpr int kChunk = 32;         // positions per warp step
+constexpr int kInRing = 1 << 30;   // flag of a partial result's pair: it lies in the ring
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Workspace: counters [n_seq * n_kv], then partials, then (with weights) the
@@ -82,6 +83,7 @@ struct DecParams {
   float* scores;            // [n_seq * n_kv][cap][rows padded] (weights)
   int64_t cap;
   int log2_page;
+  uint32_t g_magic;         // r / G = r g_magic >> 16 for r < 64
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -172,6 +174,7 @@ struct DecCfg {
   static constexpr uint32_t kKBytes = kChunk * D;
   static constexpr uint32_t kStageBytes = 2 * kKBytes;   // values as they come, 16-byte pieces exchanged within 128 bytes
   static constexpr uint32_t kRing = kWarps * kStages * kStageBytes;
+  static_assert(8 * NT * (D + 4) * 4 <= kStages * kStageBytes, "a warp's results fit its part of the ring");
   static constexpr uint32_t kSmem = kRing + (2 * kMaxSeqs + 1) * 4;   // ring, prefix sums, lengths
   static_assert(kSmem + 1024 <= 232448, "shared memory");
   static constexpr int kPartW = 8 * NT * (D + 4);        // floats of a warp's partial result
@@ -274,6 +277,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
     x.m = M;
     x.l = x.l * g0 + lw * g1;
   };
+  auto tok_of = [&](int r) { return int(uint32_t(r) * p.g_magic >> 16); };   // new token of a query row
   // what O is multiplied with for the output
   auto out_factor = [](float r, float m, float l) {
     if (l == 0.0f) return 0.0f;                     // nothing seen: zeros
@@ -285,7 +289,8 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
     if (WT) p.lse2[((int64_t)b * H + h) * C::kRows + r] = lse2;
   };
   auto finish = [&](int b, int h, int r, int d4, const Acc& x) {
-    const int64_t row = ((int64_t)b * T + r / p.G) * a.n_heads + h * p.G + r % p.G;
+    const int tok = tok_of(r);
+    const int64_t row = ((int64_t)b * T + tok) * a.n_heads + h * p.G + r - tok * p.G;
     const float f = out_factor(x.r, x.m, x.l);
     const __nv_bfloat162 y0 = __floats2bfloat162_rn(x.o.x * f, x.o.y * f);
     const __nv_bfloat162 y1 = __floats2bfloat162_rn(x.o.z * f, x.o.w * f);
@@ -398,7 +403,8 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int r = (rt * NT + n) * 8 + g;
-      const __nv_bfloat16* q = a.q + ((int64_t)b * T + r / p.G) * a.q_ts + (int64_t)(h * p.G + r % p.G) * a.q_hs;
+      const int tok = tok_of(r);
+      const __nv_bfloat16* q = a.q + ((int64_t)b * T + tok) * a.q_ts + (int64_t)(h * p.G + r - tok * p.G) * a.q_hs;
 #pragma unroll
       for (int j = 0; j < 2 * KC; ++j)
         qw[n][j] = r < p.rows ? *reinterpret_cast<const uint4*>(q + 64 * (j >> 1) + 16 * c + 8 * (j & 1))
@@ -457,7 +463,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
         const int er = __shfl_sync(0xFFFFFFFFu, e, (2 * c + j) * 4);
         const int rr = (rt * NT + n) * 8 + 2 * c + j;
         qs[n][j] = a.scale * kLog2e * pow2(er / 2) * pow2(er - er / 2);
-        vis[n][j] = rr < p.rows ? L - T + rr / p.G + 1 : 0;
+        vis[n][j] = rr < p.rows ? L - T + tok_of(rr) + 1 : 0;
       }
     }
 
@@ -693,7 +699,9 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
     // ---- results
     const bool whole = u0 == 0 && u1 == nu;
     const int slot = u0 > 0 ? 0 : 1;   // continues an earlier warp's part, or begins the pair
-    float* part = cta_parts + 2 * C::kPart + (2 * warp + slot) * C::kPartW;
+    // the warp's last ones through its part of the ring, which is done with
+    const bool last_one = i1 == n_my;
+    float* part = last_one ? reinterpret_cast<float*>(ring) : cta_parts + 2 * C::kPart + (2 * warp + slot) * C::kPartW;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -714,7 +722,8 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
             *reinterpret_cast<float4*>(part + 8 * NT * D + rr * 4) = make_float4(ro[n][j], m[n][j], sum, 0.0f);
         } else {
           const bool have = r < p.rows;
-          const int64_t row = ((int64_t)b * T + r / p.G) * a.n_heads + h * p.G + r % p.G;
+          const int tok = tok_of(r);
+          const int64_t row = ((int64_t)b * T + tok) * a.n_heads + h * p.G + r - tok * p.G;
           const float f = out_factor(ro[n][j], m[n][j], sum);
           // lanes g and g ^ 1 swap, so that each holds two neighbouring channels
 #pragma unroll
@@ -728,7 +737,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
           if (have && g == 0) write_lse(b, h, r, row, m[n][j], sum);
         }
       }
-    if (!whole && rt == 0 && lane == 0) s_pair[2 * tg + slot] = b * H + h;
+    if (!whole && rt == 0 && lane == 0) s_pair[2 * tg + slot] = (b * H + h) | (last_one ? kInRing : 0);
   }
   cp_async_wait<0>();
   __syncthreads();
@@ -753,31 +762,20 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
         if (d4 == 0) *reinterpret_cast<float4*>(q + C::kRows * D + r * 4) = make_float4(x.r, x.m, x.l, 0.0f);
       }
     };
-    constexpr int KB = 12;   // loads in flight
-    for (unsigned left = have; left;) {
-      float4 v[KB], t[KB];
-      int slot[KB];
-#pragma unroll
-      for (int k = 0; k < KB; ++k) {
-        slot[k] = left ? __ffs(left) - 1 : -1;
-        left &= left - 1;
-        if (slot[k] >= 0) {
-          const float* q = cta_parts + 2 * C::kPart + (2 * ((slot[k] >> 1) * RT + w0) + (slot[k] & 1)) * C::kPartW;
-          v[k] = *reinterpret_cast<const float4*>(q + rr * D + d4);
-          t[k] = *reinterpret_cast<const float4*>(q + 8 * NT * D + rr * 4);
-        }
+#pragma unroll 1
+    for (unsigned left = have; left; left &= left - 1) {
+      const int slot = __ffs(left) - 1, pair = s_pair[slot] & ~kInRing, from = (slot >> 1) * RT + w0;
+      const float* q = s_pair[slot] & kInRing
+                           ? reinterpret_cast<const float*>(smem + (size_t)from * C::kStages * C::kStageBytes)
+                           : cta_parts + 2 * C::kPart + (2 * from + (slot & 1)) * C::kPartW;
+      const float4 v = *reinterpret_cast<const float4*>(q + rr * D + d4);
+      const float4 t = *reinterpret_cast<const float4*>(q + 8 * NT * D + rr * 4);
+      if (pair != cur) {
+        flush();
+        cur = pair;
+        x = Acc{make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY, -INFINITY, 0.0f};
       }
-#pragma unroll
-      for (int k = 0; k < KB; ++k) {
-        if (slot[k] < 0) break;
-        const int pair = s_pair[slot[k]];
-        if (pair != cur) {
-          flush();
-          cur = pair;
-          x = Acc{make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY, -INFINITY, 0.0f};
-        }
-        join(x, v[k], t[k].x, t[k].y, t[k].z);
-      }
+      join(x, v, t.x, t.y, t.z);
     }
     flush();
   }
@@ -804,6 +802,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
     s_edge[tid] = e;
   }
   __syncthreads();
+#pragma unroll 1
   for (int k2 = 0; k2 < 2; ++k2) {
     const Edge e = s_edge[k2];
     if (e.b < 0) continue;
@@ -812,7 +811,8 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
       const int r = i / (D / 4), d4 = (i % (D / 4)) * 4;
       if (r >= p.rows) continue;
       Acc x{make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY, -INFINITY, 0.0f};
-      constexpr int KB = 8;   // loads in flight
+      constexpr int KB = 4;   // loads in flight
+#pragma unroll 1
       for (int k0 = e.c0; k0 <= e.c1; k0 += KB) {
         float4 v[KB], t[KB];
 #pragma unroll
@@ -916,6 +916,7 @@ int launch_attn_decode(const DecodeArgs& a, const DeviceInfo& di, cudaStream_t s
   p.a = a;
   p.G = a.n_heads / a.c.n_kv_heads;
   p.rows = a.n_new * p.G;
+  p.g_magic = (65536u + p.G - 1) / p.G;
   char* base = static_cast<char*>(a.ws);
   p.counter = reinterpret_cast<unsigned*>(base);
   p.parts = reinterpret_cast<float*>(base + w.parts);
