@@ -68,8 +68,8 @@ struct DecPlan {
 inline DecPlan dec_plan(int rows) {
   if (rows <= 8) return {1, 1};
   if (rows <= 16) return {2, 1};
-  if (rows <= 24) return {3, 1};
-  if (rows <= 32) return {2, 2};
+  if (rows <= 24) return {1, 3};
+  if (rows <= 32) return {1, 4};
   if (rows <= 48) return {3, 2};
   return {2, 4};
 }
@@ -894,9 +894,11 @@ int launch_one(const DecParams& p, int n_cta, cudaStream_t s) {
 }
 template <int D, bool WT>
 int launch_plan(const DecParams& p, const DecPlan& pl, int n_cta, cudaStream_t s) {
+  if (pl.nt == 1 && pl.rt == 3) return launch_one<D, 1, 3, WT>(p, n_cta, s);
+  if (pl.nt == 1 && pl.rt == 4) return launch_one<D, 1, 4, WT>(p, n_cta, s);
   if (pl.nt == 1) return launch_one<D, 1, 1, WT>(p, n_cta, s);
-  if (pl.rt == 1) return pl.nt == 2 ? launch_one<D, 2, 1, WT>(p, n_cta, s) : launch_one<D, 3, 1, WT>(p, n_cta, s);
-  if (pl.rt == 2) return pl.nt == 2 ? launch_one<D, 2, 2, WT>(p, n_cta, s) : launch_one<D, 3, 2, WT>(p, n_cta, s);
+  if (pl.rt == 1) return launch_one<D, 2, 1, WT>(p, n_cta, s);
+  if (pl.rt == 2) return launch_one<D, 3, 2, WT>(p, n_cta, s);
   return launch_one<D, 2, 4, WT>(p, n_cta, s);
 }
 
