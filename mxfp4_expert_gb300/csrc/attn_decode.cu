@@ -831,7 +831,8 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
   }
 }
 
-// weights[pair][j] += sum over the query rows of exp(score - log-sum-exp).
+// weights[pair][j] += sum over the query rows of exp(score - log-sum-exp). Bound
+// by reading the scores back, mostly from L2.
 template <int ROWS>
 __global__ void __launch_bounds__(256) decode_weights_kernel(const DecParams p) {
   const DecodeArgs& a = p.a;
@@ -840,22 +841,40 @@ __global__ void __launch_bounds__(256) decode_weights_kernel(const DecParams p) 
   bool ignore = false;
   const int L = dec_length(a, b, &ignore);
   __shared__ float s_lse[ROWS];
-  for (int r = threadIdx.x; r < ROWS; r += blockDim.x) s_lse[r] = r < p.rows ? p.lse2[pair * ROWS + r] : 0.0f;
+  for (int r = threadIdx.x; r < ROWS; r += blockDim.x) s_lse[r] = r < p.rows ? p.lse2[pair * ROWS + r] : INFINITY;
   __syncthreads();
-  for (int64_t j = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; j < L; j += (int64_t)gridDim.x * blockDim.x) {
-    const float4* s = reinterpret_cast<const float4*>(p.scores + (pair * p.cap + j) * ROWS);
-    float w = 0.0f;
+  // 4 positions per thread and turn, each 4 rows at a time: the loads of all at once
+  constexpr int PT = 4;
+  for (int64_t j0 = (int64_t)blockIdx.x * 256 * PT; j0 < L; j0 += (int64_t)gridDim.x * 256 * PT) {
+    float w[PT], old[PT];
+    float* out = a.weights + pair * a.w_stride + j0 + threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < PT; ++k) {
+      w[k] = 0.0f;
+      old[k] = j0 + threadIdx.x + 256 * k < L ? out[256 * k] : 0.0f;
+    }
 #pragma unroll
     for (int r4 = 0; r4 < ROWS / 4; ++r4) {
-      const float4 v = __ldcs(s + r4);
-      const float x[4] = {v.x, v.y, v.z, v.w};
+      float4 v[PT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 4 * r4 + i;
-        if (r < p.rows && x[i] != -INFINITY) w += ex2(x[i] - s_lse[r]);
+      for (int k = 0; k < PT; ++k) {
+        const int64_t j = j0 + threadIdx.x + 256 * k;
+        v[k] = j < L ? __ldcs(reinterpret_cast<const float4*>(p.scores + (pair * p.cap + j) * ROWS) + r4)
+                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+#pragma unroll
+      for (int k = 0; k < PT; ++k) {
+        const float x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // rows that are padding have s_lse = inf; rows that see nothing have scores of -inf
+          if (x[i] != -INFINITY) w[k] += ex2(x[i] - s_lse[4 * r4 + i]);
+        }
       }
     }
-    a.weights[pair * a.w_stride + j] += w;
+#pragma unroll
+    for (int k = 0; k < PT; ++k)
+      if (j0 + threadIdx.x + 256 * k < L) out[256 * k] = old[k] + w[k];
   }
 }
 
@@ -887,7 +906,7 @@ int launch_one(const DecParams& p, int n_cta, cudaStream_t s) {
   int st = launch_status();
   if (st != MOE_OK || !WT) return st;
   if (p.cap == 0) return MOE_OK;
-  const int64_t blocks = (p.cap + 255) / 256;
+  const int64_t blocks = (p.cap + 1023) / 1024;
   const dim3 grid(unsigned(blocks < 64 ? blocks : 64), p.a.c.n_kv_heads, p.a.n_seq);
   decode_weights_kernel<C::kRows><<<grid, 256, 0, s>>>(p);
   return launch_status();
