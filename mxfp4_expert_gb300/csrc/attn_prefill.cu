@@ -16,34 +16,40 @@
 // cost (how many items cost at least x is a sum over sequences, in closed form).
 //
 // Tensor memory (512 columns): scores S0, S1 (128 fp32 columns each), outputs
-// O0, O1 (D each). Probabilities go back as bf16 over the scores they came
-// from, as the A operand of the second product.
+// O0, O1 (D each). A key tile's scores come as two halves of 64 keys, each with
+// 64 of the 128 columns. Its probabilities, bf16, go over the first half's
+// scores, as the A operand of the second product; the next key tile's first
+// scores go where the second half's were, and so on by turns.
 //
 // Warp roles, meeting only at mbarriers:
 //   producer (one warp)    the next item; this one's Q tiles, then K0 V0 K1 V1
 //                          ... by TMA into a ring
-//   MMA 0, 1 (a warp each) of its query tile: S = Q K^T, then per key tile
-//                          O += P V in two halves and the next S. A warp is held
-//                          while it issues (the tensor cores take few MMAs
+//   MMA 0, 1 (a warp each) of its query tile: S = Q K^T and O += P V. A warp is
+//                          held while it issues (the tensor cores take few MMAs
 //                          ahead), so one for both tiles would see late that the
-//                          other tile is ready: it took 0.45 of the time
+//                          other tile is ready
 //   scan (one warp)        masked key tiles only, see below
 //   softmax 0, 1 (4 warps each, one thread per query): S to registers,
 //                          probabilities (fp32 sum, bf16 store), and at the end
-//                          O / sum
+//                          O / sum; releases what the products have read
 //
-// What bounds it: a query tile's chain S -> softmax -> P V -> next S against the
-// other tile's products. 128 x 128 scores take the special-function units 512
-// cycles (32 a cycle, measured) and the tensor cores 1024 for both products, so
-// the chain must not be much longer than 2048. Therefore
-//   - a tile's scores are worked on in two halves of 64 keys, and a half's
-//     probabilities are taken against the reference that was there: bf16 and
-//     fp32 have range enough for what lies up to 2^64 above it. A reference that
-//     was passed by 2^8 is raised, and O rescaled, when the next tile's scores
-//     arrive; one passed by more than 2^64 is raised at once;
-//   - the first 64 keys' probabilities are handed over as soon as they are
-//     stored, and their product runs while the other 64 are computed.
-// Maximum first and one hand-over took 3560 cycles per pair of tiles.
+// What bounds it: the chain of a query tile. 128 x 128 scores take the
+// special-function units 512 cycles (32 a cycle, measured) and the tensor cores
+// 557 + 514 for the two products, but a softmax thread is at them for 1900,
+// and each hand-over between warps costs 200 to 400. Therefore
+//   - scores in halves: as soon as the second half's are in registers the next
+//     tile's first half is computed, so that the softmax warps find it ready.
+//     Products with 64 keys take 860 cycles a tile instead of 557 (they read as
+//     much of Q), which is less than waiting;
+//   - a half's probabilities are taken against the reference that was there:
+//     bf16 and fp32 have range enough for what lies up to 2^64 above it. A
+//     reference that was passed by 2^8 is raised, and O rescaled, when the next
+//     tile's scores arrive; one passed by more than 2^64 is raised at once;
+//   - the first 64 keys' product runs while the other 64 are worked on;
+//   - little code: the two halves are one loop and waits call one function. With
+//     the halves unrolled the warps waited twice as long for instructions.
+// 16,384 tokens, 16 heads over 2 of 128, causal: 698 us, 1,574 TFLOP/s; whole
+// tiles of scores, halves unrolled: 749 us.
 //
 // Masked places must not count, whatever they hold, but 0 * inf is NaN in the
 // second product. For a tile that some query of the item does not see whole the
@@ -77,7 +83,7 @@ struct PfPlan {
   static constexpr uint32_t kTile = kBoxes * kBoxBytes;
   static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr uint32_t kQ = 0, kRing = 2 * kTile, kBars = kRing + kStages * kTile;
-  static constexpr int kNBars = 2 + 2 * kStages + 16 + kScanRing + 4;
+  static constexpr int kNBars = 2 + 2 * kStages + 18 + kScanRing + 4;
   static constexpr uint32_t kItems = kBars + kNBars * 8;
   static constexpr uint32_t kTotal = kItems + 2 * 80 + kScanRing * 4 + 16 + 1024;   // + alignment slack
 };
@@ -103,20 +109,36 @@ struct PfParams {
 // The MMA warp runs as a whole and lets one lane issue: its operands then are
 // uniform for the compiler and live in uniform registers, which the instructions
 // want; from within a branch of one lane each of them is moved there first.
-__device__ __forceinline__ void umma_ss_1(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+// Four products in a row: 64 of the contracted elements; the first adds to what
+// is there only if `accumulate`. A in shared memory (steps of 32 bytes), and B
+// too (steps of `db` * 16 bytes).
+__device__ __forceinline__ void umma_ss_4(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                           bool accumulate) {
   asm volatile(
-      "{\n .reg .pred p, q;\n elect.sync _|q, 0xFFFFFFFF;\n setp.ne.b32 p, %4, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
+      "{\n .reg .pred p, q, t;\n .reg .b64 a, b;\n elect.sync _|q, 0xFFFFFFFF;\n setp.ne.b32 p, %4, 0;\n"
+      " setp.eq.b32 t, 0, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+      " add.s64 a, %1, 2;\n add.s64 b, %2, 2;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.s64 a, %1, 4;\n add.s64 b, %2, 4;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.s64 a, %1, 6;\n add.s64 b, %2, 6;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n}\n" ::"r"(tmem_d),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u)
       : "memory");
 }
-// A in tensor memory.
-__device__ __forceinline__ void umma_ts_1(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+__device__ __forceinline__ void umma_ts_4(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
                                           bool accumulate) {
   asm volatile(
-      "{\n .reg .pred p, q;\n elect.sync _|q, 0xFFFFFFFF;\n setp.ne.b32 p, %4, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_d),
+      "{\n .reg .pred p, q, t;\n .reg .b32 a;\n .reg .b64 b;\n elect.sync _|q, 0xFFFFFFFF;\n setp.ne.b32 p, %4, 0;\n"
+      " setp.eq.b32 t, 0, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      " add.s32 a, %1, 8;\n add.s64 b, %2, 128;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+      " add.s32 a, %1, 16;\n add.s64 b, %2, 256;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+      " add.s32 a, %1, 24;\n add.s64 b, %2, 384;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n}\n" ::"r"(tmem_d),
       "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u)
       : "memory");
 }
@@ -207,6 +229,14 @@ __device__ __forceinline__ PfSeq pf_seq(const PrefillArgs& a, int G, int b, bool
   s.nk = k1 - s.k0;
   s.pairs = ((s.nq + kQT - 1) / kQT * G + 1) / 2;
   return s;
+}
+// Bounded wait. The long way is one function for all: the warps' loops together
+// are near what the instruction cache holds.
+__device__ __noinline__ bool pf_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
+  return uwait(bar, parity, abort, status);
+}
+__device__ __forceinline__ bool pf_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
+  return mbar_try_wait(bar, parity) || pf_wait_long(bar, parity, abort, status);
 }
 // Keys that the tile which ends before query `end` sees.
 __device__ __forceinline__ int pf_kv_end(const PfSeq& s, int end, int causal) {
@@ -306,9 +336,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
   uint64_t* q_empty = q_full + 1;
   uint64_t* full = q_empty + 1;
   uint64_t* empty = full + NS;
-  uint64_t* s_full = empty + NS;       // [2]
-  uint64_t* p_full = s_full + 2;       // [2][2]: query tile, half of the keys
-  uint64_t* h_done = p_full + 4;       // [2]: the first half's product
+  uint64_t* s_full = empty + NS;       // [2][2]: query tile, half of the keys
+  uint64_t* p_first = s_full + 4;      // [2]: the first half's probabilities are there, the second half's scores taken
+  uint64_t* p_second = p_first + 2;    // [2]: the second half's probabilities
+  uint64_t* h_done = p_second + 2;       // [2]: the first half's product
   uint64_t* o_full = h_done + 2;       // [2]
   uint64_t* o_free = o_full + 2;       // [2]
   uint64_t* scanned = o_free + 2;      // [kScanRing]
@@ -334,9 +365,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
       mbar_init(&empty[i], 3);     // both MMA warps, scan
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[2 * i], 4);
-      mbar_init(&p_full[2 * i + 1], 4);
+      mbar_init(&s_full[2 * i], 1);
+      mbar_init(&s_full[2 * i + 1], 1);
+      mbar_init(&p_first[i], 4);
+      mbar_init(&p_second[i], 4);
       mbar_init(&h_done[i], 1);
       mbar_init(&o_full[i], 1);
       mbar_init(&o_free[i], 4);
@@ -360,7 +392,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
   // The t-th item of this CTA, copied out of its slot (whole warp or one
   // thread; one arrival per reader).
   auto next_item = [&](int t, bool arrives, PfItem* it) {
-    if (!uwait(&it_full[t & 1], uint32_t(t >> 1) & 1u, abort, status)) return false;
+    if (!pf_wait(&it_full[t & 1], uint32_t(t >> 1) & 1u, abort, status)) return false;
     *it = items[t & 1];
     __syncwarp(__activemask());
     if (arrives) mbar_arrive(&it_empty[t & 1]);
@@ -379,7 +411,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
       const int N = gridDim.x, c = blockIdx.x;
       // item t of this CTA into its slot; false if there is none (nor any later)
       auto publish = [&](int t) {
-        if (t >= 2 && !uwait(&it_empty[t & 1], uint32_t((t >> 1) - 1) & 1u, abort, status)) {
+        if (t >= 2 && !pf_wait(&it_empty[t & 1], uint32_t((t >> 1) - 1) & 1u, abort, status)) {
           ok = false;
           return false;
         }
@@ -401,7 +433,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
         const PfItem& it = items[t & 1];
         if (lane == 0 && it.n > 0) {
           // Q: after the last products with the previous item's
-          if (issued_q > 0 && !uwait(q_empty, uint32_t(issued_q - 1) & 1u, abort, status)) ok = false;
+          if (issued_q > 0 && !pf_wait(q_empty, uint32_t(issued_q - 1) & 1u, abort, status)) ok = false;
           if (ok) {
             const int have1 = it.rows[1] > 0;
             mbar_arrive_expect_tx(q_full, (1 + have1) * Plan::kTile);
@@ -415,7 +447,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
           }
           for (int i = 0; ok && i < 2 * it.n; ++i) {
             const int w = 1 + (i & 1);
-            if (loads >= NS && !uwait(&empty[s], par, abort, status)) {
+            if (loads >= NS && !pf_wait(&empty[s], par, abort, status)) {
               ok = false;
               break;
             }
@@ -440,7 +472,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
       // additions (no division by the ring's length, no descriptor built anew).
       constexpr uint32_t kTile16 = Plan::kTile >> 4, kBox16 = kBoxBytes >> 4;
       const int j = warp == kWMma1;
-      const uint32_t id_s = umma_idesc_bf16(kQT, kKT) | (P.negate ? 1u << 13 : 0u);   // bit 13: negate A
+      const uint32_t id_s = umma_idesc_bf16(kQT, kKT / 2) | (P.negate ? 1u << 13 : 0u);   // bit 13: negate A
       const uint32_t id_o = umma_idesc_bf16(kQT, D) | (1u << 16);                     // bit 16: B is MN-major
       const uint64_t dq = umma_desc_sw128(q_s + j * Plan::kTile);
       const uint64_t dk = umma_desc_sw128(ring_s), dv = umma_desc_mn_sw128(ring_s, kBoxBytes);
@@ -449,22 +481,23 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
       uint32_t st = 0, par = 0;                      // ring stage and phase
       uint32_t q_par = 0, p_par = 0, o_par = 1;      // phases of Q, of the probabilities, of O's release
       uint32_t turn_par = 1 - j;                     // tile 0 begins
+      uint32_t g = 0;                                // columns of a key tile's first scores: g * 64
       bool ok = true, o_used = false;
       auto wait = [&](uint64_t* bar, uint32_t ph) {
         if (__any_sync(0xFFFFFFFFu, mbar_try_wait(bar, ph))) return true;
-        return bool(__all_sync(0xFFFFFFFFu, uwait(bar, ph, abort, status)));
+        return bool(__all_sync(0xFFFFFFFFu, pf_wait_long(bar, ph, abort, status)));
       };
-      auto scores = [&]() {
-        const uint64_t b0 = dk + st * kTile16;
+      auto scores = [&](uint32_t stage, int half, uint32_t col) {
+        const uint64_t b0 = dk + stage * kTile16 + half * (kBox16 / 2);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t o = (kk >> 2) * kBox16 + (kk & 3) * 2;
-          umma_ss_1(ts, dq + o, b0 + o, id_s, kk > 0);
-        }
-        umma_commit_1(smem_addr(&s_full[j]));
+        for (int x = 0; x < NB; ++x) umma_ss_4(ts + col, dq + x * kBox16, b0 + x * kBox16, id_s, x > 0);
+        umma_commit_1(smem_addr(&s_full[2 * j + half]));
       };
-      auto next_stage = [&]() {      // this warp is done with the stage
-        umma_commit_1(empty_s + 8 * st);
+      // On to the next stage. The softmax warps see from the scores that follow
+      // when a stage has been read; one of a tile that is not theirs is given
+      // up here.
+      auto next_stage = [&](bool unused) {
+        if (unused) mbar_arrive_1(empty_s + 8 * st);
         if (++st == NS) st = 0, par ^= 1;
       };
       PfItem it;
@@ -475,8 +508,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
         if (!(ok = wait(q_full, q_par)) || !(ok = wait(&full[st], par))) break;
         q_par ^= 1;
         tc_fence_after();
-        if (nkt > 0) scores();
-        next_stage();
+        if (nkt > 0) {
+          scores(st, 0, 64 * g);
+          scores(st, 1, 64 - 64 * g);
+        }
+        next_stage(nkt == 0);
         if (n == 1) umma_commit_1(q_empty_s);
         for (int i = 0; i < n; ++i) {
           if (!(ok = wait(&full[st], par))) break;
@@ -487,34 +523,41 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
               o_used = true;
               o_par ^= 1;
             }
-            if (!(ok = wait(&p_full[2 * j], p_par))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < kKT / 32; ++kk) umma_ts_1(to, ts + kk * 8, b0 + kk * 128, id_o, kk > 0 || i > 0);
+            if (i + 1 < nkt) {         // the next tile's first scores, where this one's second ones were
+              const uint32_t st1 = st + 1 == NS ? 0 : st + 1;
+              if (!(ok = wait(&full[st1], st1 ? par : par ^ 1)) || !(ok = wait(&p_first[j], p_par))) break;
+              tc_fence_after();
+              scores(st1, 0, 64 - 64 * g);
+            } else {
+              if (!(ok = wait(&p_first[j], p_par))) break;
+              tc_fence_after();
+            }
+            umma_ts_4(to, ts + 64 * g, b0, id_o, i > 0);
             umma_commit_1(smem_addr(&h_done[j]));
-            if (!(ok = wait(&p_full[2 * j + 1], p_par))) break;
+            if (!(ok = wait(&p_second[j], p_par))) break;
             p_par ^= 1;
+          }
+          if (i < nkt) {
+            tc_fence_after();
+            umma_ts_4(to, ts + 64 * g + 32, b0 + 4 * 128, id_o, true);
+            if (i + 1 == nkt) umma_commit_1(smem_addr(&o_full[j]));
           }
           // the two tiles' second products and next scores strictly in turn
           if (!(ok = wait(&turn[j], turn_par))) break;
           turn_par ^= 1;
-          if (i < nkt) {
-            tc_fence_after();
-#pragma unroll
-            for (int kk = kKT / 32; kk < kKT / 16; ++kk) umma_ts_1(to, ts + kk * 8, b0 + kk * 128, id_o, true);
-          }
-          next_stage();
-          if (i + 1 == nkt) umma_commit_1(smem_addr(&o_full[j]));
+          next_stage(i >= nkt);
           if (i + 1 < n) {
-            if (!(ok = wait(&full[st], par))) break;
-            tc_fence_after();
-            if (i + 1 < nkt) scores();
+            if (i + 1 < nkt)
+              scores(st, 1, 64 * g);
+            else if (!(ok = wait(&full[st], par)))
+              break;
             mbar_arrive_1(smem_addr(&turn[1 - j]));
-            next_stage();
+            next_stage(i + 1 >= nkt);
             if (i + 2 == n) umma_commit_1(q_empty_s);
           } else {
             mbar_arrive_1(smem_addr(&turn[1 - j]));
           }
+          if (i < nkt) g ^= 1;
         }
       }
       // every MMA has finished before tensor memory is freed
@@ -529,7 +572,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
       for (int t = 0; ok && next_item(t, lane == 0, &it); ++t) {
         for (int e = 0; e < 2 * it.n; ++e) {
           const int i = e >> 1;
-          if (!uwait(&full[s], par, abort, status)) {
+          if (!pf_wait(&full[s], par, abort, status)) {
             ok = false;
             break;
           }
@@ -576,6 +619,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
     const int row = quarter * 32 + lane;
     const uint32_t lanes = uint32_t(quarter * 32) << 16;
     const uint32_t ts = tmem + lanes + j * kKT, to = tmem + lanes + 256 + j * D;
+    int st = 0;                     // ring stage of the next key tile's keys
     int nsf = 0, nof = 0, ns = 0;   // scores and outputs awaited; masked tiles
     bool ok = true;
     PfItem it;
@@ -590,21 +634,32 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
       for (int i = 0; i < nkt; ++i) {
         const int k0 = i * kKT;
         const bool masked = k0 + kKT > it.vmin;
-        if (!uwait(&s_full[j], uint32_t(nsf++) & 1u, abort, status)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
+        const uint32_t ph = uint32_t(nsf) & 1u, ta = ts + 64 * ph, tb = ts + 64 - 64 * ph;
+        ++nsf;
         const int n_vis = vis - k0;
         const bool cut = k0 + kKT > vis_w;   // some lane of the warp does not see the whole tile
         float top = -INFINITY;               // the tile's maximum
         uint32_t s[2][32];
-        tmem_ld32(ts, s[0]);
-        tmem_ld32(ts + 32, s[1]);
-#pragma unroll
+#pragma unroll 1
         for (int half = 0; half < 2; ++half) {
+          if (!pf_wait(&s_full[2 * j + half], ph, abort, status)) ok = false;
+          if (half == 1) {   // the products before these scores are done, too: their values are released with the keys
+            if (warp == kWSoft + 4 * j && lane == 0) {
+              if (i > 0) mbar_arrive(&empty[st == 0 ? NS - 1 : st - 1]);
+              mbar_arrive(&empty[st]);
+            }
+            st = st + 2 >= NS ? st + 2 - NS : st + 2;
+          }
+          tc_fence_after();
+          tmem_ld32(half ? tb : ta, s[0]);
+          tmem_ld32((half ? tb : ta) + 32, s[1]);
           tmem_wait_ld32(s[0]);
           tie32(s[1]);
+          if (half == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_first[j]);
+          }
           float mx[4];
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
@@ -632,11 +687,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
             const float f = r > m ? pf_ex2(m - r) : 1.0f;
             if (r > m) m = r;
             l *= f;
-            // what is in O: the earlier tiles' products, which have finished,
-            // since this tile's scores were issued after them, and in the second
-            // half this tile's first half's
-            if (half == 1) {
-              if (!uwait(&h_done[j], uint32_t(nsf - 1) & 1u, abort, status)) ok = false;
+            // what is in O: the earlier tiles' products, which have finished
+            // when this tile's second scores have, since these were issued after
+            // them; in the second half this tile's first product too, after
+            // which the next tile's first scores are issued
+            if (half == 1 || i > 0) {
+              if (!pf_wait(half ? &h_done[j] : &s_full[2 * j + 1], ph, abort, status)) ok = false;
               tc_fence_after();
             }
             if (i > 0 || half == 1) {
@@ -659,13 +715,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
 #pragma unroll
             for (int y = 0; y < 32; y += 2)
               unpack2(fma2(pack2(__uint_as_float(x[y]), __uint_as_float(x[y + 1])), c2, r2), e[y], e[y + 1]);
-            if (half == 0) tmem_ld32(ts + 64 + 32 * b, x);   // the second half's scores
 #pragma unroll
             for (int y = 0; y < 32; ++y) e[y] = pf_ex2(e[y]);
             uint32_t pb[16];
 #pragma unroll
             for (int y = 0; y < 16; ++y) pb[y] = bf16x2_bits(e[2 * y], e[2 * y + 1]);
-            tmem_st16(ts + 32 * half + 16 * b, pb);
+            tmem_st16(ta + 32 * half + 16 * b, pb);
             uint64_t sum[4];
 #pragma unroll
             for (int y = 0; y < 4; ++y) sum[y] = add2(pack2(e[2 * y], e[2 * y + 1]), pack2(e[2 * y + 8], e[2 * y + 9]));
@@ -680,14 +735,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
           if (half == 0) {
             if (masked) {
               const int slot = ns & (kScanRing - 1);
-              if (!uwait(&scanned[slot], uint32_t(ns / kScanRing) & 1u, abort, status)) ok = false;
+              if (!pf_wait(&scanned[slot], uint32_t(ns / kScanRing) & 1u, abort, status)) ok = false;
               ++ns;
               if (poison[slot]) bad |= 1u << (i - it.vmin / kKT);
             }
             tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[2 * j]);
           }
         }
         if (!ok) break;
@@ -695,21 +747,26 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[2 * j + 1]);
+        if (lane == 0) mbar_arrive(&p_second[j]);
       }
       if (!ok) break;
+      const int st_end = (st + 2 * (it.n - nkt)) % NS;
       // masked tiles of the item that this query tile does not take part in
       {
         const int from = max(it.vmin / kKT, nkt);
         if (it.n > from) ns += it.n - from;
       }
-      if (it.rows[j] == 0) continue;
+      if (it.rows[j] == 0) {
+        st = st_end;
+        continue;
+      }
       const bool mine = row < it.rows[j];
       const int64_t orow = (int64_t)(it.q0[j] + row) * a.n_heads + it.head[j];
       __nv_bfloat16* out = a.out + orow * D;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       if (nkt > 0) {
-        if (!uwait(&o_full[j], uint32_t(nof++) & 1u, abort, status)) break;
+        if (!pf_wait(&o_full[j], uint32_t(nof++) & 1u, abort, status)) break;
+        if (warp == kWSoft + 4 * j && lane == 0) mbar_arrive(&empty[st == 0 ? NS - 1 : st - 1]);
         tc_fence_after();
       }
 #pragma unroll
@@ -756,6 +813,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
             *reinterpret_cast<uint4*>(out + x + y * 8) = make_uint4(b[4 * y], b[4 * y + 1], b[4 * y + 2], b[4 * y + 3]);
         }
       }
+      st = st_end;
       if (mine && a.lse) a.lse[orow] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2f;
     }
   }
