@@ -513,7 +513,8 @@ int moe_attn_decode_fp8(const moe_kv_cache* cache, const moe_rows* q, int n_head
  *                     the last
  *   kept_weights_dev  fp32 [n_seq][n_kv_heads][keep]: their weights, 0 past the
  *                     last (NULL: not returned)
- *   new_lengths_dev   int32 [n_seq]: min(L, keep)
+ *   new_lengths_dev   int32 [n_seq]: min(L, keep); not lengths_dev, nor
+ *                     kept_weights_dev weights_dev
  *   dev_status        device int (may be NULL): MOE_DEV_INDEX_OOB as in
  *                     moe_attn_decode_fp8; a position whose page is outside
  *                     the cache is kept as zeros, a destination page outside

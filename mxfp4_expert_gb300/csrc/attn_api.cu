@@ -181,6 +181,9 @@ extern "C" int moe_kv_evict_fp8(const moe_kv_cache* cache, const int32_t* page_t
   MOE_CHECK_ARG((int64_t)dst_width * page >= most, MOE_ERR_BUFFER_TOO_SMALL);
   if (n_seq == 0) return MOE_OK;
   MOE_CHECK_ARG(lengths_dev && kept_dev && new_lengths_dev, MOE_ERR_INVALID_ARG);
+  // other heads still read the old ones when the new are written
+  MOE_CHECK_ARG(new_lengths_dev != lengths_dev && (!kept_weights_dev || kept_weights_dev != weights_dev),
+                MOE_ERR_INVALID_ARG);
   MOE_CHECK_ARG(table_width == 0 || (page_table_dev && dst_table_dev && weights_dev), MOE_ERR_INVALID_ARG);
   DeviceInfo di;
   if ((st = current_device(&di))) return st;

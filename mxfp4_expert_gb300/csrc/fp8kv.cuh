@@ -15,7 +15,6 @@ __device__ __forceinline__ int kv_scale_byte(float amax) {
   e += (m > 0.875f ? 1 : 0) - 9 + 127;
   return e < 0 ? 0 : (e > 254 ? 254 : e);
 }
-__device__ __forceinline__ bool e4m3_is_nan(uint32_t c) { return (c & 0x7Fu) == 0x7Fu; }
 
 // 2^e, -126 <= e <= 127
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }

@@ -749,3 +749,22 @@ def test_decode_evict_decode(mx):
     after = mx.moe_attn_decode_fp8(c, q, ln, dst)
     lost = 1 - kw.sum(-1) / 2.0          # the share of the weight that was dropped
     assert float((after.float() - before.float()).abs().max()) <= 2 * float(lost.max()) * 4.0 * 2 + 0.05
+
+
+def test_evict_refuses_to_write_over_what_it_reads(mx):
+    c = _Cache(mx, 8, 16, 1, 64)
+    w, ln = _weights(1, 1, 1, 64), _i32([64])
+    with pytest.raises(mx.MoeError):
+        mx.moe_kv_evict_fp8(c.gpu, _i32([[0, 1, 2, 3]]), ln, w, 32, 8, _i32([[4, 5]]), new_lengths=ln)
+    with pytest.raises(mx.MoeError):
+        mx.moe_kv_evict_fp8(c.gpu, _i32([[0, 1, 2, 3]]), ln, w, 64, 8, _i32([[4, 5, 6, 7]]), kept_weights=w)
+
+
+@pytest.mark.parametrize("lens,keep,recent,H,ties", [([70001, 40000], 1500, 100, 2, False), ([70001], 1500, 0, 1, True),
+                                                     ([17003], 64, 5, 80, False), ([33000, 9], 700, 31, 3, True)])
+def test_evict_long(mx, lens, keep, recent, H, ties):
+    """More positions than a pair's CTAs keep in registers; several CTAs and one; ties across their borders."""
+    w = _weights(7, len(lens), H, -(-max(lens) // 128) * 128)
+    if ties:
+        w = (w * 4).round() / 4
+    _check_evict(mx, lens, keep, recent, H, 64, 128, 11, w)
