@@ -5,7 +5,10 @@
 // head, K or V) holds the page's new values in registers between the maximum
 // and the rounding, so each value is read once; a part-filled page whose scale
 // grows has its older codes rounded once more by the same CTA. Bound by HBM:
-// 2 bytes in and 1 out per value.
+// 2 bytes in and 1 out per value. 12,345 tokens of 8 heads of 128 for 5
+// sequences: 19.7 us, 3.8 TB/s: a CTA's chain (block, page, values, maximum,
+// codes) overlaps with the other CTAs' on its SM, of which 2.4 rounds run. 64
+// tokens for 64 sequences, 4 heads: 6.3 us, the launch and that chain.
 //
 // evict: see the two kernels below.
 #include <algorithm>
@@ -189,8 +192,8 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const AppendArgs a)
 constexpr int kSelThreads = 1024;
 constexpr int kSelTile = 4 * kSelThreads;
 constexpr int kSelBits = 11, kSelBins = 1 << kSelBits, kSelPasses = 3;
-constexpr int kSelCluster = 8;          // CTAs per (sequence, head), at most
-constexpr int kSelEach = 4096;          // positions worth another CTA
+constexpr int kSelCluster = 4;          // CTAs per (sequence, head), at most
+constexpr int kSelEach = 8192;          // positions that a CTA of several has at least
 constexpr int kSelRegs = 16;            // keys that a thread keeps
 
 // Order-preserving key: larger weight, larger key; -0 as +0, NaN as -inf.
@@ -216,10 +219,11 @@ __device__ __forceinline__ int cut_length(const int32_t* lengths, int b, int wid
 // shared memory, then reads the others' counts through the cluster and finds the
 // digit for itself, so a pass takes one cluster barrier. One more pass, in
 // order, takes what is above the threshold, the first of what equals it, and
-// the recent ones. Bound by latency: a few dependent passes over 4 bytes a
-// position that lie in L2. Three passes of 11 bits instead of four of 8, and 8
-// CTAs instead of one, took 16 x 4 pairs of 32768 positions from 36 us to 25 us (a read of the weights at
-// the copy rate takes 1.3).
+// the recent ones. Bound by latency: a few dependent passes over the keys, the
+// first kSelRegs x 1024 of a CTA in registers, each with a shared-memory atomic a
+// position, two barriers and a scan. 16 x 4 pairs of 32,768 positions, two CTAs
+// a pair: 24 us (36 with one CTA and four passes of 8 bits); a read of the
+// weights at the copy rate takes 1.3.
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a, int csize) {
   __shared__ unsigned hist[kSelPasses][kSelBins];
   __shared__ unsigned s_bin, s_left;
@@ -437,9 +441,11 @@ constexpr int kGatThreads = 256;
 // One destination page of one head: threads 0..127 its keys, 128..255 its
 // values. The codes stay in registers between the maximum and the rounding.
 // NV = 16-code vectors per thread: page_size * head_dim / 16 / 128. Bound by
-// HBM (a byte in and out per code); what costs is the chain of loads to the
-// source row (kept position, its page, scale and codes), so many small CTAs
-// per SM.
+// HBM (a byte in and out per code); what costs is that a kept row is 128 bytes at
+// a random place: 4.2 TB/s in all for such reads, 7.1 for long ones. Before it
+// lies a chain of loads (kept position, its page, scale and codes), so many small
+// CTAs per SM (with 4 instead of 8, 61.5 us instead of 56.2 for the call). 16 x
+// 32,768 positions of 4 heads to 4,096 each: 35 us, 134 MB.
 template <int NV>
 __global__ void __launch_bounds__(kGatThreads, NV <= 4 ? 8 : 4) evict_gather_kernel(const EvictArgs a) {
   __shared__ int s_page[128];        // source page of each slot, -1: none
@@ -555,9 +561,13 @@ int launch_kv_append(const AppendArgs& a, cudaStream_t s) {
 int launch_kv_evict(const EvictArgs& a, const DeviceInfo& di, cudaStream_t s) {
   const int P = a.c.page_size;
   const int64_t cap = std::min((int64_t)a.width * P, a.w_stride);
-  // more CTAs per pair while each keeps enough positions and all run at once
+  // More CTAs per pair while each keeps enough positions and all run at once. The
+  // whole call, us with 1, 2, 4 and 8 CTAs a pair: 4 pairs of 4,096 15.6, 18.7,
+  // 20.7, -; 16 of 9,000 23.9, 26.0, 28.0, -; 4 of 32,768 30.8, 24.6, 23.3, 32.6;
+  // 16 of 32,768 37.0, 31.1, 30.6, 61.7; 64 of 32,768 63.8, 56.1, 70.5, -; 8 of
+  // 100,000 78.4, 53.6, 37.1, 38.9.
   int csize = 1;
-  while (csize < kSelCluster && (int64_t)csize * kSelEach < cap &&
+  while (csize < kSelCluster && 2 * (int64_t)csize * kSelEach <= cap &&
          2 * (int64_t)csize * a.c.n_kv_heads * a.n_seq <= di.sm_count)
     csize *= 2;
   cudaLaunchConfig_t cfg{};
