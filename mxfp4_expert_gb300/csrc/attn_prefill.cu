@@ -255,20 +255,23 @@ __device__ __forceinline__ int pf_count_ge(const PfSeq& s, int G, int causal, in
 }
 __device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xFFFFFFFFu, v); }
 
-// Whole warp: item number idx (< total), into *out by lane 0.
-__device__ void pf_find_item(const PfParams& P, int G, int idx, bool sorted, PfItem* out) {
+// Whole warp: item number idx (< total), into *out by one lane. `own` is sequence
+// number `lane`, kept in registers: each count looks at every sequence. `most`:
+// no item has more key tiles.
+__device__ void pf_find_item(const PfParams& P, int G, const PfSeq& own, int most, int idx, bool sorted, PfItem* out) {
   const PrefillArgs& a = P.a;
   const int lane = threadIdx.x & 31;
   const int r = idx / a.n_kv, hk = idx % a.n_kv;
   bool ignore = false;
+  auto seq = [&](int b) { return b == lane ? own : pf_seq(a, G, b, &ignore); };
   auto count = [&](int c) {
     int n = 0;
-    for (int b = lane; b < a.n_seq; b += 32) n += pf_count_ge(pf_seq(a, G, b, &ignore), G, a.causal, c);
+    for (int b = lane; b < a.n_seq; b += 32) n += pf_count_ge(seq(b), G, a.causal, c);
     return warp_sum(n);
   };
   int c = 1, skip = 0;      // the item costs c; so many cost more
   if (sorted) {
-    int lo = 1, hi = (a.total_k + kKT - 1) / kKT;
+    int lo = 1, hi = most;
     while (lo < hi) {       // largest c with count(c) > r
       const int mid = (lo + hi + 1) >> 1;
       if (count(mid) > r) lo = mid; else hi = mid - 1;
@@ -282,7 +285,7 @@ __device__ void pf_find_item(const PfParams& P, int G, int idx, bool sorted, PfI
     PfSeq s{0, 0, 0, 0, 0};
     int n = 0, first = 0;
     if (b < a.n_seq) {
-      s = pf_seq(a, G, b, &ignore);
+      s = seq(b);
       const int ge = pf_count_ge(s, G, a.causal, c);
       n = sorted ? ge - pf_count_ge(s, G, a.causal, c + 1) : s.pairs;
       first = s.pairs - ge;
@@ -403,9 +406,16 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
     if (warp == kWProd) {
       // ---- producer: items, and their loads -------------------------------------------------
       bool bad = false, ok = true;
-      int total = 0;
-      for (int b = lane; b < a.n_seq; b += 32) total += pf_seq(a, G, b, &bad).pairs;
+      PfSeq own{0, 0, 0, 0, 0};
+      int total = 0, most = 1;
+      for (int b = lane; b < a.n_seq; b += 32) {
+        const PfSeq x = pf_seq(a, G, b, &bad);
+        if (b == lane) own = x;
+        total += x.pairs;
+        most = max(most, (x.nk + kKT - 1) / kKT);
+      }
       total = warp_sum(total) * a.n_kv;
+      most = __reduce_max_sync(0xFFFFFFFFu, most);
       bad = __any_sync(0xFFFFFFFFu, bad);
       if (bad && blockIdx.x == 0 && lane == 0 && status) atomicOr(status, MOE_DEV_INDEX_OOB);
       const int N = gridDim.x, c = blockIdx.x;
@@ -417,7 +427,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
         }
         const int64_t idx = (int64_t)t * N + (t & 1 ? N - 1 - c : c);
         if (idx < total)
-          pf_find_item(P, G, int(idx), total > N, &items[t & 1]);
+          pf_find_item(P, G, own, most, int(idx), total > N, &items[t & 1]);
         else if (lane == 0)
           items[t & 1].n = -1;
         __threadfence_block();
@@ -429,7 +439,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
       uint32_t par = 1;                     // phase of its release: the first lap waits for none
       bool more = publish(0);
       for (int t = 0; ok && more; ++t) {
-        more = publish(t + 1);              // found while this item's tail of the ring is worked off
+        more = publish(t + 1);
         const PfItem& it = items[t & 1];
         if (lane == 0 && it.n > 0) {
           // Q: after the last products with the previous item's
