@@ -768,3 +768,37 @@ def test_evict_long(mx, lens, keep, recent, H, ties):
     if ties:
         w = (w * 4).round() / 4
     _check_evict(mx, lens, keep, recent, H, 64, 128, 11, w)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_scores_that_leave_the_reference_behind(mx, d):
+    """Every 64 keys the scores rise by more than 2^64, for some queries only and in many items of a CTA."""
+    g = _gen(61)
+    n = 700
+    scale = 256.0 / d
+    ramp = torch.linspace(-3, 3, n, device="cuda")[:, None, None].expand(n, 1, d).to(torch.bfloat16).contiguous()
+    q = torch.ones((n, 2, d), dtype=torch.bfloat16, device="cuda")
+    q[::3] *= 0.25
+    q[1::7] *= -1
+    _check_prompt(mx, [n], [n], 2, 1, d, True, q=q, k=ramp, seed=62, scale=scale)
+    _check_prompt(mx, [n], [n], 2, 1, d, False, q=q, k=ramp, seed=63, scale=scale)
+    # a step at one key, in the first or the second half of a tile, the last key among them
+    for at in (1, 63, 64, 70, 127, 128, 200, 299):
+        k = torch.zeros((300, 1, d), dtype=torch.bfloat16, device="cuda")
+        k[at:] = 1.0
+        _check_prompt(mx, [300], [300], 2, 1, d, at % 2 == 0, q=q[:300], k=k, seed=at, scale=scale)
+    lens = [300, 129, 64, 257, 300, 31]
+    total = sum(lens)
+    k = (ramp[:1] * 0 + torch.randint(-3, 4, (total, 8, 1), generator=g, device="cuda")).to(torch.bfloat16).expand(
+        total, 8, d).contiguous()
+    q = torch.ones((total, 64, d), dtype=torch.bfloat16, device="cuda")
+    _check_prompt(mx, lens, lens, 64, 8, d, True, q=q, k=k, seed=64, scale=scale, heads=[0, 31, 63])
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_many_sequences_of_many_costs(mx, causal):
+    """More items than CTAs, of many costs, from more sequences than a warp has lanes."""
+    lens = [(i * 97) % 410 for i in range(50)]
+    _check_prompt(mx, lens, lens, 8, 4, 128, causal, seed=71, heads=[0, 5])
+    longer = [n + 300 * (i % 3) for i, n in enumerate(lens)]
+    _check_prompt(mx, lens, longer, 6, 2, 64, causal, seed=72, heads=[4])
