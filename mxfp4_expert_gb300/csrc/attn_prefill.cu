@@ -48,7 +48,7 @@
 //   - the first 64 keys' product runs while the other 64 are worked on;
 //   - little code: the two halves are one loop and waits call one function. With
 //     the halves unrolled the warps waited twice as long for instructions.
-// 16,384 tokens, 16 heads over 2 of 128, causal: 698 us, 1,574 TFLOP/s; whole
+// 16,384 tokens, 16 heads over 2 of 128, causal: 700 us, 1,571 TFLOP/s; whole
 // tiles of scores, halves unrolled: 749 us.
 //
 // Masked places must not count, whatever they hold, but 0 * inf is NaN in the
@@ -82,8 +82,12 @@ struct PfPlan {
   static constexpr int kBoxes = D / 64;
   static constexpr uint32_t kTile = kBoxes * kBoxBytes;
   static constexpr int kStages = D == 128 ? 5 : 8;
-  static constexpr uint32_t kQ = 0, kRing = 2 * kTile, kBars = kRing + kStages * kTile;
-  static constexpr int kNBars = 2 + 2 * kStages + 18 + kScanRing + 4;
+  // two items' Q where there is room: the next item's is loaded before this one's
+  // last scores are done (24 packed prompts of 6,001 tokens, heads of 64: 31.6 us
+  // with two, 32.9 with one)
+  static constexpr int kQBufs = D == 128 ? 1 : 2;
+  static constexpr uint32_t kQ = 0, kRing = kQBufs * 2 * kTile, kBars = kRing + kStages * kTile;
+  static constexpr int kNBars = 2 * kQBufs + 2 * kStages + 18 + kScanRing + 4;
   static constexpr uint32_t kItems = kBars + kNBars * 8;
   static constexpr uint32_t kTotal = kItems + 2 * 80 + kScanRing * 4 + 16 + 1024;   // + alignment slack
 };
@@ -332,12 +336,12 @@ template <int D>
 __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_constant__ PfParams P) {
   using Plan = PfPlan<D>;
   constexpr int NS = Plan::kStages;
-  constexpr int NB = Plan::kBoxes;
+  constexpr int NB = Plan::kBoxes, NQ = Plan::kQBufs;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + Plan::kBars);
-  uint64_t* q_empty = q_full + 1;
-  uint64_t* full = q_empty + 1;
+  uint64_t* q_empty = q_full + NQ;     // [NQ] each
+  uint64_t* full = q_empty + NQ;
   uint64_t* empty = full + NS;
   uint64_t* s_full = empty + NS;       // [2][2]: query tile, half of the keys
   uint64_t* p_first = s_full + 4;      // [2]: the first half's probabilities are there, the second half's scores taken
@@ -361,8 +365,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
   int* status = a.status;
 
   if (tid == 0) {
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 2);         // both MMA warps
+    for (int i = 0; i < NQ; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 2);   // both MMA warps
+    }
     for (int i = 0; i < NS; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 3);     // both MMA warps, scan
@@ -442,16 +448,17 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
         more = publish(t + 1);
         const PfItem& it = items[t & 1];
         if (lane == 0 && it.n > 0) {
-          // Q: after the last products with the previous item's
-          if (issued_q > 0 && !pf_wait(q_empty, uint32_t(issued_q - 1) & 1u, abort, status)) ok = false;
+          // Q: after the last products with what was there
+          const int qb = issued_q % NQ;
+          if (issued_q >= NQ && !pf_wait(&q_empty[qb], uint32_t(issued_q / NQ - 1) & 1u, abort, status)) ok = false;
           if (ok) {
             const int have1 = it.rows[1] > 0;
-            mbar_arrive_expect_tx(q_full, (1 + have1) * Plan::kTile);
+            mbar_arrive_expect_tx(&q_full[qb], (1 + have1) * Plan::kTile);
             for (int j = 0; j <= have1; ++j)
               for (int x = 0; x < NB; ++x) {
                 const int h = P.one_head[0] ? 0 : it.head[j], r = it.q0[j];
-                tma_load_3d(q_s + j * Plan::kTile + x * kBoxBytes, &P.map[0], x * 64, P.swapped[0] ? r : h,
-                            P.swapped[0] ? h : r, q_full);
+                tma_load_3d(q_s + (2 * qb + j) * Plan::kTile + x * kBoxBytes, &P.map[0], x * 64, P.swapped[0] ? r : h,
+                            P.swapped[0] ? h : r, &q_full[qb]);
               }
             ++issued_q;
           }
@@ -474,7 +481,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
       }
       if (lane == 0 && *abort) {   // copies in flight land before the CTA's shared memory goes away
         for (int i = loads > NS ? loads - NS : 0; i < loads; ++i) mbar_wait(&full[i % NS], uint32_t(i / NS) & 1u, status);
-        if (issued_q > 0) mbar_wait(q_full, uint32_t(issued_q - 1) & 1u, status);
+        for (int i = issued_q > NQ ? issued_q - NQ : 0; i < issued_q; ++i)
+          mbar_wait(&q_full[i % NQ], uint32_t(i / NQ) & 1u, status);
       }
     } else if (warp == kWMma0 || warp == kWMma1) {
       // ---- MMA --------------------------------------------------------------------------
@@ -484,12 +492,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
       const int j = warp == kWMma1;
       const uint32_t id_s = umma_idesc_bf16(kQT, kKT / 2) | (P.negate ? 1u << 13 : 0u);   // bit 13: negate A
       const uint32_t id_o = umma_idesc_bf16(kQT, D) | (1u << 16);                     // bit 16: B is MN-major
-      const uint64_t dq = umma_desc_sw128(q_s + j * Plan::kTile);
+      const uint64_t dq0 = umma_desc_sw128(q_s + j * Plan::kTile);
       const uint64_t dk = umma_desc_sw128(ring_s), dv = umma_desc_mn_sw128(ring_s, kBoxBytes);
       const uint32_t ts = tmem + j * kKT, to = tmem + 256 + j * D;
       const uint32_t empty_s = smem_addr(empty), q_empty_s = smem_addr(q_empty);
+      uint64_t dq = dq0;
       uint32_t st = 0, par = 0;                      // ring stage and phase
-      uint32_t q_par = 0, p_par = 0, o_par = 1;      // phases of Q, of the probabilities, of O's release
+      uint32_t q_buf = NQ - 1, q_par = 1, p_par = 0, o_par = 1;      // phases of Q, of the probabilities, of O's release
       uint32_t turn_par = 1 - j;                     // tile 0 begins
       uint32_t g = 0;                                // columns of a key tile's first scores: g * 64
       bool ok = true, o_used = false;
@@ -515,15 +524,16 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
         const int n = __shfl_sync(0xFFFFFFFFu, it.n, 0);
         const int nkt = __shfl_sync(0xFFFFFFFFu, j ? it.nkt[1] : it.nkt[0], 0);
         if (n == 0) continue;
-        if (!(ok = wait(q_full, q_par)) || !(ok = wait(&full[st], par))) break;
-        q_par ^= 1;
+        if (++q_buf == NQ) q_buf = 0, q_par ^= 1;
+        dq = dq0 + q_buf * (2 * kTile16);
+        if (!(ok = wait(&q_full[q_buf], q_par)) || !(ok = wait(&full[st], par))) break;
         tc_fence_after();
         if (nkt > 0) {
           scores(st, 0, 64 * g);
           scores(st, 1, 64 - 64 * g);
         }
         next_stage(nkt == 0);
-        if (n == 1) umma_commit_1(q_empty_s);
+        if (n == 1) umma_commit_1(q_empty_s + 8 * q_buf);
         for (int i = 0; i < n; ++i) {
           if (!(ok = wait(&full[st], par))) break;
           const uint64_t b0 = dv + st * kTile16;
@@ -563,7 +573,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
               break;
             mbar_arrive_1(smem_addr(&turn[1 - j]));
             next_stage(i + 1 >= nkt);
-            if (i + 2 == n) umma_commit_1(q_empty_s);
+            if (i + 2 == n) umma_commit_1(q_empty_s + 8 * q_buf);
           } else {
             mbar_arrive_1(smem_addr(&turn[1 - j]));
           }
