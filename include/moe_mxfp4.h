@@ -481,9 +481,12 @@ int moe_kv_append_fp8(const moe_kv_cache* cache, const moe_rows* k, const moe_ro
  *                weights_stride + j the probabilities that the tokens and
  *                query heads of (b, h) give to position j are added, for j <
  *                lengths[b] (in a fixed order: equal inputs give equal bits)
- *   workspace    >= moe_attn_decode_workspace_bytes(...) bytes (256-B aligned),
- *                zero-filled before its first use: its first bytes hold
- *                counters that every call leaves at zero
+ *   workspace    >= moe_attn_decode_workspace_bytes(...) bytes (256-B aligned).
+ *                Its first MOE_ATTN_DECODE_COUNTER_BYTES bytes hold counters:
+ *                zero them before its first use, every call leaves them at
+ *                zero. One workspace serves calls of any sizes for which it is
+ *                large enough, one after another; calls that may overlap in
+ *                time need one each.
  *   dev_status   device int (may be NULL): MOE_DEV_INDEX_OOB (a length outside
  *                [0, table_width * page_size] or above weights_stride is cut
  *                to it; a page outside the cache counts as masked)
@@ -491,6 +494,7 @@ int moe_kv_append_fp8(const moe_kv_cache* cache, const moe_rows* k, const moe_ro
  * n_heads % n_kv_heads, n_new > 8, n_new * n_heads / n_kv_heads > 64, n_seq >
  * 4096), MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_NO_DEVICE, MOE_ERR_CUDA. The
  * workspace size is 0 for an unsupported shape or without an sm_103 device. */
+#define MOE_ATTN_DECODE_COUNTER_BYTES 4096
 size_t moe_attn_decode_workspace_bytes(const moe_kv_cache* cache, int n_seq, int n_new, int n_heads,
                                        int table_width, int with_weights);
 int moe_attn_decode_fp8(const moe_kv_cache* cache, const moe_rows* q, int n_heads, int n_seq, int n_new,

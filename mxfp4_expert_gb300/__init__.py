@@ -622,7 +622,8 @@ def moe_attn_decode_fp8(cache: KVCache, q: torch.Tensor, lengths: torch.Tensor, 
     position receives are added to it. lse fp32 [n_seq, n_new, n_heads] is
     written if given. workspace: uint8 device tensor of
     moe_attn_decode_workspace_bytes(...) bytes, zero-filled before its first
-    use (it carries counters between calls); allocated with zeros when omitted.
+    use (it carries counters between calls, which may be of different sizes);
+    allocated with zeros when omitted.
     """
     dev, H = _cache_device(cache), cache.n_kv_heads
     if not isinstance(q, _Tensor) or q.dim() != 4:

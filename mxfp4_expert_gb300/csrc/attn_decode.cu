@@ -13,6 +13,9 @@
 // the workspace. When its warps are done the CTA joins theirs, and what still
 // reaches past the CTA is joined by the last CTA of the pair to finish (a
 // counter): always in order of position, so results do not depend on who is last.
+// At most one pair begins in a CTA and reaches past it, so a pair's counter is
+// that of the CTA it begins in, and the counters' place does not depend on the
+// sizes of a call: one workspace serves calls of all sizes in turn.
 //
 // A warp's next chunks are on their way into its own part of shared memory by
 // cp.async. Both products run on the f16 warp MMA (m16n8k16) with positions or
@@ -60,8 +63,10 @@ constexpr int kChunk = 32;         // positions per warp step
 constexpr int kInRing = 1 << 30;   // flag of a partial result's pair: it lies in the ring
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Workspace: counters [n_seq * n_kv], then partials, then (with weights) the
-// rows' log2-sum-exp and the scores.
+// Workspace: counters, always this many bytes, one for each CTA; then partials,
+// then (with weights) the rows' log2-sum-exp and the scores.
+constexpr size_t kCounterBytes = MOE_ATTN_DECODE_COUNTER_BYTES;
+constexpr int kMaxCtas = int(kCounterBytes / 4);
 struct DecWs {
   size_t parts, lse2, scores, total;
   int n_cta, rows;    // CTAs; query rows padded to the row tiles
@@ -89,7 +94,7 @@ inline DecPlan dec_plan(int rows) {
 struct DecParams {
   DecodeArgs a;
   int G, rows;              // query heads per kv head; query rows n_new * G
-  unsigned* counter;        // [n_seq * n_kv]
+  unsigned* counter;        // [CTAs]: of the pair that begins in the CTA and reaches past it
   float* parts;             // per CTA: 2 partial results, then 2 per warp: [rows][D] outputs, [rows][4] references and sum
   float* lse2;              // [n_seq * n_kv][rows padded] (weights)
   float* scores;            // [n_seq * n_kv][cap][rows padded] (weights)
@@ -805,9 +810,8 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
     Edge e{-1, 0, 0, 0};
     if ((s0 < cta0 || s1 > cta1) && !(tid && s0 <= cta0)) {
       const int c0 = int(((s0 + 1) * N - 1) / W), c1 = int((s1 * N - 1) / W);
-      const int64_t pair = (int64_t)b * H + h;
-      if (atomicAdd(p.counter + pair, 1u) == unsigned(c1 - c0)) {   // the last of them
-        p.counter[pair] = 0;
+      if (atomicAdd(p.counter + c0, 1u) == unsigned(c1 - c0)) {   // the last of them
+        p.counter[c0] = 0;
         e = Edge{b, h, c0, c1};
       }
     }
@@ -900,9 +904,10 @@ size_t ws_layout(const moe_kv_cache& c, int n_seq, int n_new, int n_heads, int w
   const size_t cap = (size_t)width * c.page_size;
   const size_t chunks = pairs * (cap > 0 ? (cap + kChunk - 1) / kChunk : 1);
   const size_t ctas = (chunks + groups - 1) / groups;
-  w->n_cta = int(ctas < (size_t)sm_count ? (ctas ? ctas : 1) : sm_count);
+  const size_t most = sm_count < kMaxCtas ? sm_count : kMaxCtas;
+  w->n_cta = int(ctas < most ? (ctas ? ctas : 1) : most);
   const size_t part = (size_t)(c.head_dim + 4) * 4 * (2 * w->rows + 2 * warps * 8 * pl.nt);
-  w->parts = round_up(pairs * 4, 256);
+  w->parts = kCounterBytes;
   w->lse2 = w->parts + round_up(w->n_cta * part, 256);
   w->scores = w->lse2 + (weights ? round_up(pairs * w->rows * 4, 256) : 0);
   w->total = w->scores + (weights ? pairs * cap * w->rows * 4 : 0);

@@ -802,3 +802,40 @@ def test_prompt_many_sequences_of_many_costs(mx, causal):
     _check_prompt(mx, lens, lens, 8, 4, 128, causal, seed=71, heads=[0, 5])
     longer = [n + 300 * (i % 3) for i, n in enumerate(lens)]
     _check_prompt(mx, lens, longer, 6, 2, 64, causal, seed=72, heads=[4])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_one_workspace_for_batches_of_any_size(mx, d):
+    """A workspace zeroed once, for calls whose sequences, heads and new tokens grow and shrink: as with a new one."""
+    P, big = 32, 200
+    g = _gen(d)
+    pools = {}
+    for H in (8, 2):
+        c, table = _filled(mx, [320] * big, P, H, d, 10, H)
+        pools[H] = c.gpu, table
+    ws = torch.zeros(max(mx.moe_attn_decode_workspace_bytes(pools[H][0], big, 4, 2 * H, 10, True) for H in pools),
+                     dtype=torch.uint8, device="cuda")
+    for H, n_seq, T, G in ((8, 4, 1, 2), (8, big, 1, 2), (2, 3, 4, 2), (8, big, 1, 1), (2, 1, 1, 1), (8, 150, 4, 2),
+                           (8, 8, 1, 2), (2, big, 2, 2), (8, big, 1, 2)):
+        cache, table = pools[H]
+        lens = _i32([1 + (i * 97) % 320 for i in range(n_seq)])
+        q = _bf16(g, n_seq, T, H * G, d)
+        got = []
+        for w in (ws, None):
+            out = torch.full_like(q, math.nan)
+            lse = torch.full(q.shape[:3], math.nan, device="cuda")
+            weights = torch.zeros((n_seq, H, 320), device="cuda")
+            mx.moe_attn_decode_fp8(cache, q, lens, table[:n_seq].contiguous(), out=out, lse=lse, weights=weights,
+                                   workspace=w)
+            got.append((out, lse, weights))
+        torch.cuda.synchronize()
+        assert torch.isfinite(got[1][0]).all()
+        for a, b in zip(*got):
+            assert torch.equal(a, b), (H, n_seq, T, G)
+
+
+@pytest.mark.parametrize("T,hq", [(1, 2), (3, 4), (5, 4)])
+def test_decode_many_sequences(mx, T, hq):
+    """More sequences than a CTA has threads, empty ones among them."""
+    lens = [(i * 37) % 70 if i % 5 else 0 for i in range(900)]
+    _check_decode(mx, lens, T, hq, 1, 64, 16, 5, seed=91, weights=True)
