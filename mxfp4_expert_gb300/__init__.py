@@ -5,6 +5,10 @@ marshal arguments: every step of the layer runs in the library's CUDA
 kernels. PyTorch supplies device memory and streams. There is no CPU or
 PyTorch fallback: importing this package fails if the library has not been
 built, and every call raises ``MoeError`` on a non-zero status.
+
+A call with ``stream=`` launches there, and what it allocates itself belongs to
+that stream; inputs that another stream writes have to be waited for by the
+caller, as have the results.
 """
 from __future__ import annotations
 
@@ -19,7 +23,7 @@ __all__ = [
     "moe_packed_desc", "moe_shape", "moe_layer", "Layer",
     "moe_packed_bytes", "moe_describe_packed", "moe_pack_mxfp4", "moe_unpack_mxfp4",
     "moe_route_topk", "moe_sort_workspace_bytes", "moe_sort_by_expert",
-    "moe_workspace_bytes", "moe_query_path", "moe_stage_names", "moe_forward", "moe_forward_profiled", "moe_forward_w4a8", "moe_quant_mxfp8", "moe_lmhead_pack_fp8", "moe_lmhead_fp8", "moe_forward_static_scratch", "STATIC_SCRATCH_BYTES",
+    "moe_workspace_bytes", "moe_query_path", "moe_stage_names", "moe_forward", "moe_forward_profiled", "moe_forward_w4a8", "moe_quant_mxfp8", "moe_lmhead_pack_fp8", "moe_lmhead_fp8", "moe_forward_static_scratch", "STATIC_SCRATCH_BYTES", "ATTN_DECODE_COUNTER_BYTES",
     "moe_rows", "moe_kv_cache", "KVCache", "moe_attn_prefill", "moe_kv_append_fp8", "moe_attn_decode_workspace_bytes",
     "moe_attn_decode_fp8", "moe_kv_evict_fp8", "moe_selftest_bounded_wait", "moe_status_string", "moe_version",
 ]
@@ -37,6 +41,7 @@ MOE_PATH_DECODE_FUSED = 2
 MOE_PATH_PREFILL_TC = 3
 DEV_NONFINITE_INPUT, DEV_SCALE_RANGE, DEV_INDEX_OOB, DEV_TIMEOUT = 1, 2, 4, 8
 STATIC_SCRATCH_BYTES = 4 * 1024 * 1024
+ATTN_DECODE_COUNTER_BYTES = 4096
 
 
 class MoeError(RuntimeError):
@@ -131,6 +136,18 @@ def _s(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream, zero_bytes=0):
+    """A new tensor that belongs to the stream a call launches on (None: the current one): the allocator then orders its
+    memory's earlier and later uses by that stream. zero_bytes: leading bytes (of a uint8 tensor) that are zeroed there."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _empty(shape, dtype, device, None, zero_bytes)
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if zero_bytes:
+        t[:zero_bytes].zero_()
+    return t
+
+
 def _check(status: int, what: str):
     if status != 0:
         raise MoeError(what, status)
@@ -180,7 +197,7 @@ def moe_pack_mxfp4(w: torch.Tensor, layout: int, out: torch.Tensor | None = None
     if nbytes == 0:
         raise MoeError("moe_pack_mxfp4", -2)
     if out is None:
-        out = torch.empty(nbytes, dtype=torch.uint8, device=w.device)
+        out = _empty(nbytes, torch.uint8, w.device, stream)
     desc = moe_packed_desc()
     _check(lib.moe_pack_mxfp4(_p(w), n_mat, N, K, layout, _p(out), out.numel(), ctypes.byref(desc),
                               _p(dev_status), _s(stream)), "moe_pack_mxfp4")
@@ -189,8 +206,8 @@ def moe_pack_mxfp4(w: torch.Tensor, layout: int, out: torch.Tensor | None = None
 
 def moe_unpack_mxfp4(packed: torch.Tensor, desc: moe_packed_desc, stream=None):
     """Packed buffer -> canonical (codes [n_mat, N, K/2], scales [n_mat, N, K/32]) uint8."""
-    codes = torch.empty((desc.n_mat, desc.N, desc.K // 2), dtype=torch.uint8, device=packed.device)
-    scales = torch.empty((desc.n_mat, desc.N, desc.K // 32), dtype=torch.uint8, device=packed.device)
+    codes = _empty((desc.n_mat, desc.N, desc.K // 2), torch.uint8, packed.device, stream)
+    scales = _empty((desc.n_mat, desc.N, desc.K // 32), torch.uint8, packed.device, stream)
     _check(lib.moe_unpack_mxfp4(_p(packed), ctypes.byref(desc), _p(codes), _p(scales), _s(stream)),
            "moe_unpack_mxfp4")
     return codes, scales
@@ -205,8 +222,8 @@ def moe_route_topk(logits: torch.Tensor, k: int, bias: torch.Tensor | None = Non
     if bias is not None:
         _cuda(bias, torch.float32, "bias")
         stride = 0 if bias.dim() == 1 else bias.shape[1]
-    idx = torch.empty((T, k), dtype=torch.int32, device=logits.device) if idx is None else idx
-    w = torch.empty((T, k), dtype=torch.float32, device=logits.device) if w is None else w
+    idx = _empty((T, k), torch.int32, logits.device, stream) if idx is None else idx
+    w = _empty((T, k), torch.float32, logits.device, stream) if w is None else w
     _check(lib.moe_route_topk(_p(logits), T, E, k, _p(bias), stride, _p(idx), _p(w), _s(stream)),
            "moe_route_topk")
     return idx, w
@@ -221,14 +238,14 @@ def moe_sort_by_expert(idx: torch.Tensor, E: int, dev_status: torch.Tensor | Non
     _cuda(idx, torch.int32, "idx")
     T, k = idx.shape
     dev = idx.device
-    out = {"counts": torch.empty(E, dtype=torch.int32, device=dev),
-           "offsets": torch.empty(E + 1, dtype=torch.int32, device=dev),
-           "perm": torch.empty(T * k, dtype=torch.int32, device=dev),
-           "inv": torch.empty(T * k, dtype=torch.int32, device=dev),
-           "active": torch.empty(E, dtype=torch.int32, device=dev),
-           "n_active": torch.empty(1, dtype=torch.int32, device=dev)}
+    out = {"counts": _empty(E, torch.int32, dev, stream),
+           "offsets": _empty(E + 1, torch.int32, dev, stream),
+           "perm": _empty(T * k, torch.int32, dev, stream),
+           "inv": _empty(T * k, torch.int32, dev, stream),
+           "active": _empty(E, torch.int32, dev, stream),
+           "n_active": _empty(1, torch.int32, dev, stream)}
     nws = moe_sort_workspace_bytes(T, k, E)
-    ws = torch.empty(max(nws, 256), dtype=torch.uint8, device=dev)
+    ws = _empty(max(nws, 256), torch.uint8, dev, stream)
     _check(lib.moe_sort_by_expert(_p(idx), T, k, E, _p(out["counts"]), _p(out["offsets"]), _p(out["perm"]),
                                   _p(out["inv"]), _p(out["active"]), _p(out["n_active"]), _p(ws), ws.numel(),
                                   _p(dev_status), _s(stream)), "moe_sort_by_expert")
@@ -359,8 +376,8 @@ def moe_quant_mxfp8(src: torch.Tensor, stream=None):
         raise TypeError("src must be bf16 or fp32")
     _cuda(src, src.dtype, "src")
     rows, K = src.shape
-    codes = torch.empty((rows, K), dtype=torch.uint8, device=src.device)
-    scales = torch.empty((rows, K // 32), dtype=torch.uint8, device=src.device)
+    codes = _empty((rows, K), torch.uint8, src.device, stream)
+    scales = _empty((rows, K // 32), torch.uint8, src.device, stream)
     _check(lib.moe_quant_mxfp8(_p(src), 1 if src.dtype == torch.bfloat16 else 0, rows, K, _p(codes), _p(scales),
                                _s(stream)), "moe_quant_mxfp8")
     return codes, scales
@@ -370,8 +387,8 @@ def moe_lmhead_pack_fp8(w: torch.Tensor, stream=None):
     """bf16 LM head [V, d] -> (E4M3 codes uint8 [V, d], fp32 row scales [V])."""
     _cuda(w, torch.bfloat16, "w")
     V, d = w.shape
-    codes = torch.empty((V, d), dtype=torch.uint8, device=w.device)
-    scales = torch.empty(V, dtype=torch.float32, device=w.device)
+    codes = _empty((V, d), torch.uint8, w.device, stream)
+    scales = _empty(V, torch.float32, w.device, stream)
     _check(lib.moe_lmhead_pack_fp8(_p(w), V, d, _p(codes), _p(scales), _s(stream)), "moe_lmhead_pack_fp8")
     return codes, scales
 
@@ -387,7 +404,7 @@ def moe_lmhead_fp8(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor, l
         raise ValueError("x must be [T, d] and scales [V] for codes [V, d]")
     T = x.shape[0]
     if logits is None:
-        logits = torch.empty((T, V), dtype=torch.float32, device=x.device)
+        logits = _empty((T, V), torch.float32, x.device, stream)
     _cuda(logits, torch.float32, "logits")
     if logits.numel() < T * V:
         raise ValueError("logits needs T * V elements")
@@ -410,10 +427,11 @@ def _forward(layer, x, bias, y, workspace, logits_out, idx_out, w_out, dev_statu
              entry="moe_forward"):
     if y is None:
         _cuda(x, torch.bfloat16, "x")
-        y = torch.empty_like(x)
+        y = _empty(x.shape, x.dtype, x.device, stream)
     T, stride = _forward_args(layer, x, bias, y, logits_out, idx_out, w_out, dev_status)
     if workspace is None:
-        workspace = torch.zeros(layer.workspace_bytes(T), dtype=torch.uint8, device=x.device)
+        n = layer.workspace_bytes(T)
+        workspace = _empty(n, torch.uint8, x.device, stream, n)
     _cuda(workspace, torch.uint8, "workspace")
     args = (ctypes.byref(layer.struct), _p(x), T, _p(y), _p(bias), stride, _p(logits_out), _p(idx_out), _p(w_out),
             _p(workspace), workspace.numel(), _p(dev_status))
@@ -577,7 +595,7 @@ def moe_attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
         raise ValueError("cu_q must be [n_seq + 1]")
     cu_kp = cu_qp if cu_k is None else _ptr(cu_k, _I32, "cu_k", dev, (n_cu,))
     if out is None:
-        out = torch.empty(q_shape, dtype=_BF16, device=q.device)
+        out = _empty(q_shape, _BF16, q.device, stream)
     _check(lib.moe_attn_prefill(ctypes.byref(qr), ctypes.byref(kr), ctypes.byref(vr), n_heads, n_kv, d, cu_qp, cu_kp,
                                 n_cu - 1, total_q, total_k, 1 if causal else 0,
                                 d ** -0.5 if scale is None else float(scale), _ptr(out, _BF16, "out", dev, q_shape),
@@ -621,9 +639,9 @@ def moe_attn_decode_fp8(cache: KVCache, q: torch.Tensor, lengths: torch.Tensor, 
     weights fp32 [n_seq, n_kv_heads, positions]: the probabilities that every
     position receives are added to it. lse fp32 [n_seq, n_new, n_heads] is
     written if given. workspace: uint8 device tensor of
-    moe_attn_decode_workspace_bytes(...) bytes, zero-filled before its first
-    use (it carries counters between calls, which may be of different sizes);
-    allocated with zeros when omitted.
+    moe_attn_decode_workspace_bytes(...) bytes whose first
+    ATTN_DECODE_COUNTER_BYTES are zero before its first use (they carry counters
+    between calls, which may be of different sizes); allocated when omitted.
     """
     dev, H = _cache_device(cache), cache.n_kv_heads
     if not isinstance(q, _Tensor) or q.dim() != 4:
@@ -640,7 +658,7 @@ def moe_attn_decode_fp8(cache: KVCache, q: torch.Tensor, lengths: torch.Tensor, 
     qr = _rows(rows, "q", dev, n_heads, cache.head_dim)
     tablep, width = _table(page_table, "page_table", dev, n_seq)
     if out is None:
-        out = torch.empty(shape, dtype=_BF16, device=q.device)
+        out = _empty(shape, _BF16, q.device, stream)
     wp, wn = None, 0
     if weights is not None:
         wp = _ptr(weights, _F32, "weights", dev)
@@ -649,7 +667,7 @@ def moe_attn_decode_fp8(cache: KVCache, q: torch.Tensor, lengths: torch.Tensor, 
         wn = weights.shape[2]
     if workspace is None:
         n = moe_attn_decode_workspace_bytes(cache, n_seq, n_new, n_heads, width, weights is not None)
-        workspace = torch.zeros(max(n, 256), dtype=_U8, device=q.device)
+        workspace = _empty(max(n, 256), _U8, q.device, stream, ATTN_DECODE_COUNTER_BYTES)
     _check(lib.moe_attn_decode_fp8(cache._ref, ctypes.byref(qr), n_heads, n_seq, n_new,
                                    _ptr(lengths, _I32, "lengths", dev, (n_seq,)), tablep, width,
                                    d ** -0.5 if scale is None else float(scale), _ptr(out, _BF16, "out", dev, shape),
@@ -679,11 +697,11 @@ def moe_kv_evict_fp8(cache: KVCache, page_table: torch.Tensor, lengths: torch.Te
         raise ValueError("keep must be at least 1 and recent in [0, keep]")
     shape = (n_seq, H, keep)
     if kept is None:
-        kept = torch.empty(shape, dtype=_I32, device=weights.device)
+        kept = _empty(shape, _I32, weights.device, stream)
     if kept_weights is None:
-        kept_weights = torch.empty(shape, dtype=_F32, device=weights.device)
+        kept_weights = _empty(shape, _F32, weights.device, stream)
     if new_lengths is None:
-        new_lengths = torch.empty(n_seq, dtype=_I32, device=weights.device)
+        new_lengths = _empty(n_seq, _I32, weights.device, stream)
     _check(lib.moe_kv_evict_fp8(cache._ref, tablep, width, lengthsp, n_seq, wp, weights.shape[2], keep, recent, dstp,
                                 dst_width, _ptr(kept, _I32, "kept", dev, shape),
                                 _ptr(kept_weights, _F32, "kept_weights", dev, shape),
