@@ -16,6 +16,16 @@ __device__ __forceinline__ int kv_scale_byte(float amax) {
   return e < 0 ? 0 : (e > 254 ? 254 : e);
 }
 
+// The same for a code of finite magnitude c (7 bits) and scale byte s, whose
+// value may be more than fp32 holds. A normal code is (8 + m) 2^(e - 10), of
+// which 448 = 14 * 2^5 goes to byte s at e = 15, m <= 6; m = 7 needs one more. A
+// subnormal one is m 2^-9 = m 2^-(floor log2 m) 2^(floor log2 m - 9).
+__device__ __forceinline__ int kv_code_byte(uint32_t c, int s) {
+  const int e = int(c >> 3), m = int(c & 7u);
+  const int b = e ? s + e - 15 + (m == 7) : (m ? s - 17 + (m >= 2) + (m >= 4) : 0);
+  return max(b, 0);
+}
+
 // 2^e, -126 <= e <= 127
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
 // Does one of the word's four codes stand for NaN?

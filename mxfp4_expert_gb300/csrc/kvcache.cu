@@ -450,7 +450,7 @@ template <int NV>
 __global__ void __launch_bounds__(kGatThreads, NV <= 4 ? 8 : 4) evict_gather_kernel(const EvictArgs a) {
   __shared__ int s_page[128];        // source page of each slot, -1: none
   __shared__ uint8_t s_slot[128], s_scale[2][128];
-  __shared__ float s_max[kGatThreads / 32];
+  __shared__ int s_top[kGatThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int blk = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   const int P = a.c.page_size, D = a.c.head_dim, H = a.c.n_kv_heads;
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(kGatThreads, NV <= 4 ? 8 : 4) evict_gather_ker
       }
     }
   }
-  float top = 0.0f;
+  int byte = 0;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     // E4M3 magnitudes order as their codes do; NaN's is the largest
@@ -511,17 +511,14 @@ __global__ void __launch_bounds__(kGatThreads, NV <= 4 ? 8 : 4) evict_gather_ker
         if (c != 0x7Fu) mag = max(mag, c);
       }
     }
-    // its value times 2^(sc - 127), which may leave fp32's normal range: in two factors
-    const int e = sc[v] - 127;
-    top = fmaxf(top, e4m3_to_f32(mag) * pow2(e / 2) * pow2(e - e / 2));
+    // the byte that the largest value needs is the largest of the bytes that the vectors need
+    byte = max(byte, kv_code_byte(mag, sc[v]));
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-  if (lane == 0) s_max[warp] = top;
+  byte = __reduce_max_sync(0xFFFFFFFFu, byte);
+  if (lane == 0) s_top[warp] = byte;
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < 4; ++k) top = fmaxf(top, s_max[part * 4 + k]);
-  const int byte = kv_scale_byte(top);
+  for (int k = 0; k < 4; ++k) byte = max(byte, s_top[part * 4 + k]);
   if (pt == 0) (part ? a.c.v_scales : a.c.k_scales)[(size_t)page * H + h] = uint8_t(byte);
   uint8_t* to = codes + ((size_t)page * H + h) * P * D;
 #pragma unroll

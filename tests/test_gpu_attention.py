@@ -839,3 +839,43 @@ def test_decode_many_sequences(mx, T, hq):
     """More sequences than a CTA has threads, empty ones among them."""
     lens = [(i * 37) % 70 if i % 5 else 0 for i in range(900)]
     _check_decode(mx, lens, T, hq, 1, 64, 16, 5, seed=91, weights=True)
+
+
+def test_evict_pages_with_the_largest_values(mx):
+    """A page whose largest value is bf16's largest (its code stands for 2^128), or near it; and codes of every magnitude."""
+    P, n = 16, 40
+    for top in (3.3895e38, 2.0 ** 127, 1e38):
+        c = _Cache(mx, 6, P, 1, 64)
+        k = _bf16(_gen(7), n, 1, 64, spread=1e36)
+        k[3, 0, 5], k[20, 0, 1], k[39, 0, 63] = top, -top, top
+        table, dst = _i32([[2, 0, 4]]), _i32([[1, 3, 5]])
+        c.append(mx, k, -k, [n], [0], table)
+        mx.moe_kv_evict_fp8(c.gpu, table, _i32([n]), torch.ones((1, 1, 48), device="cuda"), 48, 0, dst)
+        for name in "kv":
+            x = oa.sequence(c.codes[name], c.scales[name], [2, 0, 4], 0, n)
+            for i, (codes, byte) in enumerate(oa.repage(x, P)):
+                c.codes[name][[1, 3, 5][i], 0, :len(codes)] = codes
+                c.scales[name][[1, 3, 5][i], 0] = byte
+        c.check()
+
+
+def test_evict_page_scale_of_every_code(mx):
+    """The scale follows from the page's largest code and scale byte alone, whatever they are."""
+    P, srcs = 16, [0, 1, 17, 18, 130, 247, 254]
+    table = torch.arange(len(srcs), dtype=torch.int32, device="cuda")[:, None].contiguous()
+    for top in range(1, 127):
+        c = _Cache(mx, 2 * len(srcs), P, 1, 64)
+        for name in "kv":
+            c.codes[name][:] = np.random.default_rng(top).integers(0, top + 1, size=c.codes[name].shape)
+            c.codes[name][:, 0, 5, 9] = top | (0x80 if name == "v" else 0)
+            c.scales[name][:len(srcs), 0] = srcs
+        for name, codes, scales in (("k", c.gpu.k_codes, c.gpu.k_scales), ("v", c.gpu.v_codes, c.gpu.v_scales)):
+            codes.copy_(torch.tensor(c.codes[name]))
+            scales.copy_(torch.tensor(c.scales[name]))
+        mx.moe_kv_evict_fp8(c.gpu, table, _i32([P] * len(srcs)), torch.ones((len(srcs), 1, P), device="cuda"), P, 0,
+                            table + len(srcs))
+        for name in "kv":
+            for b, byte in enumerate(srcs):
+                [(codes, new)] = oa.repage(oa.decode(c.codes[name][b, 0], byte), P)
+                c.codes[name][len(srcs) + b, 0], c.scales[name][len(srcs) + b, 0] = codes, new
+        c.check()
