@@ -295,10 +295,14 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
     x.l = x.l * g0 + lw * g1;
   };
   auto tok_of = [&](int r) { return int(uint32_t(r) * p.g_magic >> 16); };   // new token of a query row
-  // what O is multiplied with for the output
+  // What O is multiplied with for the output, 2^(r - m) / l, as two factors, x
+  // first: r holds a value scale of 2^-127 to 2^127 and may lie 30 from the
+  // maximum as m may, so 2^(r - m) can leave fp32's range where the output does not.
   auto out_factor = [](float r, float m, float l) {
-    if (l == 0.0f) return 0.0f;                     // nothing seen: zeros
-    return r == -INFINITY ? l : ex2(r - m) / l;     // a row of NaN scores: NaN
+    if (l == 0.0f) return make_float2(0.0f, 0.0f);             // nothing seen: zeros
+    if (r == -INFINITY) return make_float2(l, 1.0f);           // a row of NaN scores: NaN
+    const float f = ex2(0.5f * (r - m));
+    return make_float2(f / l, f);
   };
   auto write_lse = [&](int b, int h, int r, int64_t row, float m, float l) {
     const float lse2 = l == 0.0f ? -INFINITY : (m == -INFINITY ? l : m + log2f(l));
@@ -308,9 +312,9 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
   auto finish = [&](int b, int h, int r, int d4, const Acc& x) {
     const int tok = tok_of(r);
     const int64_t row = ((int64_t)b * T + tok) * a.n_heads + h * p.G + r - tok * p.G;
-    const float f = out_factor(x.r, x.m, x.l);
-    const __nv_bfloat162 y0 = __floats2bfloat162_rn(x.o.x * f, x.o.y * f);
-    const __nv_bfloat162 y1 = __floats2bfloat162_rn(x.o.z * f, x.o.w * f);
+    const float2 f = out_factor(x.r, x.m, x.l);
+    const __nv_bfloat162 y0 = __floats2bfloat162_rn(x.o.x * f.x * f.y, x.o.y * f.x * f.y);
+    const __nv_bfloat162 y1 = __floats2bfloat162_rn(x.o.z * f.x * f.y, x.o.w * f.x * f.y);
     uint2 y;
     y.x = *reinterpret_cast<const uint32_t*>(&y0);
     y.y = *reinterpret_cast<const uint32_t*>(&y1);
@@ -741,14 +745,15 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
           const bool have = r < p.rows;
           const int tok = tok_of(r);
           const int64_t row = ((int64_t)b * T + tok) * a.n_heads + h * p.G + r - tok * p.G;
-          const float f = out_factor(ro[n][j], m[n][j], sum);
+          const float2 f = out_factor(ro[n][j], m[n][j], sum);
           // lanes g and g ^ 1 swap, so that each holds two neighbouring channels
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
             const float give = g & 1 ? o[t][n][j] : o[t][n][j + 2];
             const float got = __shfl_xor_sync(0xFFFFFFFFu, give, 4);
-            const __nv_bfloat162 y = g & 1 ? __floats2bfloat162_rn(got * f, o[t][n][j + 2] * f)
-                                           : __floats2bfloat162_rn(o[t][n][j] * f, got * f);
+            const float keep = g & 1 ? o[t][n][j + 2] : o[t][n][j];
+            const float y0 = (g & 1 ? got : keep) * f.x * f.y, y1 = (g & 1 ? keep : got) * f.x * f.y;
+            const __nv_bfloat162 y = __floats2bfloat162_rn(y0, y1);
             if (have) *reinterpret_cast<__nv_bfloat162*>(a.out + row * D + 16 * t + (g & 1 ? g + 7 : g)) = y;
           }
           if (have && g == 0) write_lse(b, h, r, row, m[n][j], sum);

@@ -879,3 +879,39 @@ def test_evict_page_scale_of_every_code(mx):
                 [(codes, new)] = oa.repage(oa.decode(c.codes[name][b, 0], byte), P)
                 c.codes[name][len(srcs) + b, 0], c.scales[name][len(srcs) + b, 0] = codes, new
         c.check()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_values_of_any_size(mx, d):
+    """Values near the ends of bf16's range, where scores and scales rise together in the middle of a warp's work."""
+    H, P, n = 8, 32, 20000
+    g = _gen(98)
+    c = mx.KVCache.alloc(n // P, P, H, d)
+    table = torch.arange(n // P, dtype=torch.int32, device="cuda")[None]
+    q = torch.ones((1, 1, H, d), dtype=torch.bfloat16, device="cuda")
+    for big in (2.0 ** 119, 2.0 ** 60):
+        k = torch.zeros((n, H, d), dtype=torch.bfloat16, device="cuda")
+        v = _bf16(g, n, H, d, spread=1e-3)
+        for h in range(H):
+            at = 32 * (40 + 61 * h)
+            k[at:at + 32, h] = 17.0 / d            # e^17 is 2^24.5
+            v[at:at + 32, h] = (_bf16(g, 32, d).clamp(-4, 4).float() * big).to(torch.bfloat16)
+        mx.moe_kv_append_fp8(c, k, v, _cu([n]), _i32([0]), table)
+        _range_check(mx, c, table, q, n, 1.0)
+    # and small ones: the results stay normal bf16 numbers
+    v = (_bf16(g, n, H, d).clamp(-4, 4).float() * 2.0 ** -122).to(torch.bfloat16)
+    v = torch.where(v == 0, torch.full_like(v, 2.0 ** -122), v).abs()
+    mx.moe_kv_append_fp8(c, k, v, _cu([n]), _i32([0]), table)
+    _range_check(mx, c, table, q, n, 1.0)
+
+
+def _range_check(mx, c, table, q, n, scale):
+    out = _np(mx.moe_attn_decode_fp8(c, q, _i32([n]), table, scale=scale))
+    codes = [t.cpu().numpy() for t in (c.k_codes, c.v_codes, c.k_scales, c.v_scales)]
+    tab = table[0].cpu().numpy()
+    for h in range(c.n_kv_heads):
+        k, v = oa.sequence(codes[0], codes[2], tab, h, n), oa.sequence(codes[1], codes[3], tab, h, n)
+        r = oa.attend(_np(q[0, :, h]), k, v, [n], scale)
+        err = np.abs(out[0, :, h] - r["out"])
+        bound = 2.0 ** -8 * np.abs(r["out"]) + (2.0 ** -10 + 2.0 ** -15 * (1 + r["size"][:, None])) * r["mass"]
+        assert np.all(err <= bound), (h, float(np.max(err / bound)))
