@@ -419,7 +419,9 @@ typedef struct moe_rows {
  *                cu_q or cu_k leaves [0, total] or falls (such a sequence's
  *                length is taken as what fits); MOE_DEV_TIMEOUT
  * Rows of q outside every sequence are not written. Probabilities enter the
- * second product as bf16; sums and outputs are held in fp32.
+ * second product as bf16; sums and outputs are held in fp32. Outputs are finite
+ * wherever the definition's are, for finite values of any size and up to 2^22
+ * keys; below 2^-80 they lose bits.
  * Errors: MOE_ERR_INVALID_ARG (null pointer, negative size, stride or address
  * not aligned, scale not finite), MOE_ERR_UNSUPPORTED_SHAPE (head_dim,
  * n_heads % n_kv_heads, n_seq > 65536), MOE_ERR_NO_DEVICE, MOE_ERR_CUDA. */

@@ -41,10 +41,10 @@
 //     tile's first half is computed, so that the softmax warps find it ready.
 //     Products with 64 keys take 860 cycles a tile instead of 557 (they read as
 //     much of Q), which is less than waiting;
-//   - a half's probabilities are taken against the reference that was there:
-//     bf16 and fp32 have range enough for what lies up to 2^64 above it. A
-//     reference that was passed by 2^8 is raised, and O rescaled, when the next
-//     tile's scores arrive; one passed by more than 2^64 is raised at once;
+//   - a half's probabilities are taken against the reference that was there,
+//     which is raised, and O rescaled, only where a half passes it by 2^16 (with
+//     scores of 128 keys that rise by 6, 12, 24 and 100 in log2 from tile to tile:
+//     209, 240, 261 and 332 us for 8,192 tokens, 193 where they do not);
 //   - the first 64 keys' product runs while the other 64 are worked on;
 //   - little code: the two halves are one loop and waits call one function. With
 //     the halves unrolled the warps waited twice as long for instructions.
@@ -72,7 +72,13 @@ constexpr int kQT = 128, kKT = 128;            // queries per tile, keys per til
 constexpr int kWProd = 0, kWMma0 = 1, kWMma1 = 2, kWSoft = 4;   // and 3: scan
 constexpr int kPfWarps = 12;   // 168 registers a thread
 constexpr int kPfThreads = kPfWarps * 32;
-constexpr float kPfRaise = 8.0f, kPfMost = 64.0f;   // log2 of what the reference may be passed by: for long, at all
+constexpr float kPfMost = 16.0f;   // log2 of what the reference may be passed by
+// Probabilities are taken 2^38 below their reference, so at most 2^-22 each: O, a
+// sum of products with values of any size, then stays finite for up to 2^22 keys
+// wherever the output is. In return what is below 2^-88 of the reference is 0,
+// and outputs lose bits below 2^-80 (bf16 and fp32 end at 2^-126). An exponent of
+// -38 has 2^-19 as its rounding: 2^-20 of a probability.
+constexpr float kPfBias = 38.0f;
 constexpr uint32_t kBoxBytes = 128 * 128;      // 128 rows of 64 channels
 constexpr int kScanRing = 4;
 constexpr float kLn2f = 0.6931471805599453f, kLog2ef = 1.4426950408889634f;
@@ -649,7 +655,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
       const int vis = a.causal ? min(max(it.t0[j] + row + it.off + 1, 0), it.nk) : it.nk;
       const int vis_w = __shfl_sync(0xFFFFFFFFu, vis, 0);   // the warp's fewest
       float m = -INFINITY, l = 0.0f;   // reference, sum in units of 2^m
-      float m_next = -INFINITY;        // the reference to be
       unsigned bad = 0;                // masked tiles with non-finite values (a pair's queries span at most 4)
       for (int i = 0; i < nkt; ++i) {
         const int k0 = i * kKT;
@@ -658,7 +663,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
         ++nsf;
         const int n_vis = vis - k0;
         const bool cut = k0 + kKT > vis_w;   // some lane of the warp does not see the whole tile
-        float top = -INFINITY;               // the tile's maximum
         uint32_t s[2][32];
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
@@ -699,10 +703,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
             mx[2 * b + 1] = a1;
           }
           const float mine = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
-          top = fmaxf(top, mine);
-          // the reference: raised for the last tile's sake, or for this half's
-          float r = half == 0 ? m_next : -INFINITY;
-          if ((i == 0 && half == 0) || mine > m + kPfMost) r = fmaxf(r, mine);
+          const float r = (i == 0 && half == 0) || mine > m + kPfMost ? mine : -INFINITY;
           if (__any_sync(0xFFFFFFFFu, r > m)) {
             const float f = r > m ? pf_ex2(m - r) : 1.0f;
             if (r > m) m = r;
@@ -726,7 +727,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
               }
             }
           }
-          const float ref = m == -INFINITY ? 0.0f : m;
+          const float ref = m == -INFINITY ? 0.0f : m + kPfBias;
           const uint64_t c2 = pack2(c, c), r2 = pack2(-ref, -ref);
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
@@ -763,7 +764,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
           }
         }
         if (!ok) break;
-        if (top > m + kPfRaise) m_next = top;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -834,7 +834,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
         }
       }
       st = st_end;
-      if (mine && a.lse) a.lse[orow] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2f;
+      if (mine && a.lse) a.lse[orow] = l == 0.0f ? -INFINITY : (m + log2f(l * pow2(int(kPfBias)))) * kLn2f;
     }
   }
 

@@ -915,3 +915,31 @@ def _range_check(mx, c, table, q, n, scale):
         err = np.abs(out[0, :, h] - r["out"])
         bound = 2.0 ** -8 * np.abs(r["out"]) + (2.0 ** -10 + 2.0 ** -15 * (1 + r["size"][:, None])) * r["mass"]
         assert np.all(err <= bound), (h, float(np.max(err / bound)))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_large_values(mx, d, causal):
+    """Values of any size, near the largest bf16 too, while the scores rise by up to 2^60 within a tile."""
+    g = _gen(97)
+    n = 400
+    q = torch.ones((n, 2, d), dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros((n, 1, d), dtype=torch.bfloat16, device="cuda")
+    for at, x in ((30, 0.25), (90, 0.5), (127, 0.75), (200, 1.0), (300, 1.25), (399, 1.4)):
+        k[at:] = x
+    scale = 40.0 / d    # a step of 0.25 is 14 in log2
+    for spread in (2.0 ** -77, 2.0 ** 60, 2.0 ** 100, 2.0 ** 123):
+        v = _bf16(g, n, 1, d, spread=1.0).clamp(-8, 8) * spread
+        _check_prompt(mx, [n], [n], 2, 1, d, causal, q=q, k=k, v=v, scale=scale)
+        _check_prompt(mx, [n], [n], 2, 1, d, causal, q=q, k=k, v=v, scale=4 * scale)
+        out, _ = _check_prompt(mx, [n], [n], 2, 1, d, causal, q=q, k=0 * k, v=v, scale=scale)
+        assert torch.isfinite(out).all()
+
+
+def test_prompt_equal_keys_and_the_largest_values(mx):
+    """A mean over many keys whose values' sum is beyond fp32."""
+    n, d = 5000, 64
+    q, k = _bf16(_gen(99), 3, 2, d), torch.zeros((n, 1, d), dtype=torch.bfloat16, device="cuda")
+    v = torch.full((n, 1, d), 2.0 ** 127, dtype=torch.bfloat16, device="cuda")
+    out = mx.moe_attn_prefill(q, k, v, _cu([3]), _cu([n]))
+    assert torch.all(out == 2.0 ** 127)
