@@ -424,7 +424,8 @@ typedef struct moe_rows {
  * keys; below 2^-80 they lose bits.
  * Errors: MOE_ERR_INVALID_ARG (null pointer, negative size, stride or address
  * not aligned, scale not finite), MOE_ERR_UNSUPPORTED_SHAPE (head_dim,
- * n_heads % n_kv_heads, n_seq > 65536), MOE_ERR_NO_DEVICE, MOE_ERR_CUDA. */
+ * n_heads % n_kv_heads, n_seq > 65536, more than 2^31 - 65536 rows),
+ * MOE_ERR_NO_DEVICE, MOE_ERR_CUDA. */
 int moe_attn_prefill(const moe_rows* q, const moe_rows* k, const moe_rows* v, int n_heads, int n_kv_heads,
                      int head_dim, const int32_t* cu_q_dev, const int32_t* cu_k_dev, int n_seq, int total_q,
                      int total_k, int causal, float scale, void* out_dev, float* lse_dev, int* dev_status,
@@ -436,7 +437,8 @@ int moe_attn_prefill(const moe_rows* q, const moe_rows* k, const moe_rows* v, in
  * values, [n_pages][n_kv_heads], a code c being worth e4m3(c) * 2^(s - 127).
  * Position p of a sequence is slot p % page_size of the page
  * page_table[sequence][p / page_size]. A page that is written belongs to one
- * sequence only. */
+ * sequence only. A table holds at most 2^31 - 65536 positions
+ * (MOE_ERR_INVALID_ARG). */
 typedef struct moe_kv_cache {
   int32_t n_pages;
   int32_t page_size;    /* 16, 32, 64 or 128 */
@@ -466,7 +468,7 @@ typedef struct moe_kv_cache {
  * page is part-filled is known from start alone, so its bytes need no
  * initialisation before its first slot is written.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED_SHAPE (the cache's sizes,
- * n_seq > 65536), MOE_ERR_NO_DEVICE, MOE_ERR_CUDA. */
+ * n_seq > 65536, total > 2^31 - 65536), MOE_ERR_NO_DEVICE, MOE_ERR_CUDA. */
 int moe_kv_append_fp8(const moe_kv_cache* cache, const moe_rows* k, const moe_rows* v, const int32_t* cu_dev,
                       const int32_t* start_dev, int n_seq, int total, const int32_t* page_table_dev,
                       int table_width, int* dev_status, moe_stream_t stream);
@@ -494,7 +496,8 @@ int moe_kv_append_fp8(const moe_kv_cache* cache, const moe_rows* k, const moe_ro
  *                to it; a page outside the cache counts as masked)
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED_SHAPE (the cache's sizes,
  * n_heads % n_kv_heads, n_new > 8, n_new * n_heads / n_kv_heads > 64, n_seq >
- * 4096), MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_NO_DEVICE, MOE_ERR_CUDA. The
+ * 4096, tables that hold about 2^36 positions or more for all sequences together),
+ * MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_NO_DEVICE, MOE_ERR_CUDA. The
  * workspace size is 0 for an unsupported shape or without an sm_103 device. */
 #define MOE_ATTN_DECODE_COUNTER_BYTES 4096
 size_t moe_attn_decode_workspace_bytes(const moe_kv_cache* cache, int n_seq, int n_new, int n_heads,

@@ -27,8 +27,10 @@ int check_cache(const moe_kv_cache* c, bool buffers) {
   return aligned(c->k_codes, 16) && aligned(c->v_codes, 16) ? MOE_OK : MOE_ERR_INVALID_ARG;
 }
 
-// A table's positions fit an int.
-bool table_ok(int width, int page) { return width >= 0 && (int64_t)width * page <= INT32_MAX; }
+// The kernels count rows and positions in an int and step past the last one by
+// tiles (of 16,384 positions at most, in the eviction).
+constexpr int64_t kMaxRows = INT32_MAX - 65535;
+bool table_ok(int width, int page) { return width >= 0 && (int64_t)width * page <= kMaxRows; }
 
 int check_decode_shape(const moe_kv_cache* c, int n_seq, int n_new, int n_heads, int width) {
   int st = check_cache(c, false);
@@ -36,7 +38,8 @@ int check_decode_shape(const moe_kv_cache* c, int n_seq, int n_new, int n_heads,
   if (n_seq < 0 || n_new < 1 || n_heads < 1 || !table_ok(width, c->page_size)) return MOE_ERR_INVALID_ARG;
   if (n_heads % c->n_kv_heads || n_new > 8 || n_new * (n_heads / c->n_kv_heads) > 64 || n_seq > 4096)
     return MOE_ERR_UNSUPPORTED_SHAPE;
-  return MOE_OK;
+  // and the chunks of 32 positions of all sequences in one, at the longest that the tables hold
+  return ((int64_t)width * c->page_size / 32 + 1) * n_seq <= INT32_MAX ? MOE_OK : MOE_ERR_UNSUPPORTED_SHAPE;
 }
 
 }  // namespace
@@ -50,7 +53,8 @@ extern "C" int moe_attn_prefill(const moe_rows* q, const moe_rows* k, const moe_
                                 float* lse_dev, int* dev_status, moe_stream_t stream) {
   MOE_CHECK_ARG(n_seq >= 0 && total_q >= 0 && total_k >= 0 && n_heads >= 1 && n_kv_heads >= 1, MOE_ERR_INVALID_ARG);
   MOE_CHECK_ARG((causal == 0 || causal == 1) && isfinite(scale), MOE_ERR_INVALID_ARG);
-  MOE_CHECK_ARG((head_dim == 64 || head_dim == 128) && n_heads % n_kv_heads == 0 && n_heads <= 65535 && n_seq <= 65536,
+  MOE_CHECK_ARG((head_dim == 64 || head_dim == 128) && n_heads % n_kv_heads == 0 && n_heads <= 65535 && n_seq <= 65536 &&
+                    total_q <= kMaxRows && total_k <= kMaxRows,
                 MOE_ERR_UNSUPPORTED_SHAPE);
   if (n_seq == 0 || total_q == 0) return MOE_OK;
   int st;
@@ -95,7 +99,7 @@ extern "C" int moe_kv_append_fp8(const moe_kv_cache* cache, const moe_rows* k, c
   int st;
   if ((st = check_cache(cache, true))) return st;
   MOE_CHECK_ARG(n_seq >= 0 && total >= 0 && table_ok(table_width, cache->page_size), MOE_ERR_INVALID_ARG);
-  MOE_CHECK_ARG(n_seq <= 65536, MOE_ERR_UNSUPPORTED_SHAPE);
+  MOE_CHECK_ARG(n_seq <= 65536 && total <= kMaxRows, MOE_ERR_UNSUPPORTED_SHAPE);
   if (n_seq == 0 || total == 0) return MOE_OK;
   if ((st = check_rows(k)) || (st = check_rows(v))) return st;
   MOE_CHECK_ARG(cu_dev && start_dev && page_table_dev, MOE_ERR_INVALID_ARG);

@@ -258,7 +258,7 @@ __device__ __forceinline__ bool pf_wait_warp(uint64_t* bar, uint32_t parity, vol
 }
 // Keys that the tile which ends before query `end` sees.
 __device__ __forceinline__ int pf_kv_end(const PfSeq& s, int end, int causal) {
-  return causal ? min(max(end + s.nk - s.nq, 0), s.nk) : s.nk;
+  return causal ? min(max(end - s.nq + s.nk, 0), s.nk) : s.nk;   // end <= nq: no step leaves an int
 }
 // Pairs with at least c key tiles (at least one counts as one): the last ones.
 __device__ __forceinline__ int pf_count_ge(const PfSeq& s, int G, int causal, int c) {

@@ -150,3 +150,22 @@ def test_binding_refuses_wrong_tensors(mx):
         mx.moe_attn_prefill(q, q, q, cu)
     with pytest.raises(TypeError, match="k_codes must be a CUDA tensor"):
         mx.KVCache.alloc(1, 64, 1, 64, device="cpu")
+
+
+def test_more_rows_than_32_bits_can_step_over_are_refused(mx):
+    """The kernels count positions in 32 bits and look a tile past the last one."""
+    L, p, most = mx.lib, ctypes.c_void_p(256), 2 ** 31 - 65536
+    r = ctypes.byref(mx.moe_rows(256, 128, 128))
+    for page in (16, 128):
+        cache = mx.moe_kv_cache(4, page, 2, 128, 256, 256, 256, 256)
+        c, w = ctypes.byref(cache), most // page + 1
+        assert L.moe_kv_append_fp8(c, r, r, p, p, 1, 8, p, w, None, None) == -1
+        assert L.moe_attn_decode_fp8(c, r, 8, 1, 1, p, p, w, 1.0, p, None, None, 0, p, 1 << 62, None, None) == -1
+        assert L.moe_attn_decode_workspace_bytes(c, 1, 1, 8, w, 0) == 0
+        assert L.moe_kv_evict_fp8(c, p, w, p, 1, p, 1 << 40, 64, 8, p, 8, p, None, p, None, None) == -1
+        # every table fits, but not the chunks of all sequences in one count
+        w = 2 ** 30 // page
+        assert L.moe_attn_decode_fp8(c, r, 8, 64, 1, p, p, w, 1.0, p, None, None, 0, p, 1 << 62, None, None) == -2
+    assert L.moe_kv_append_fp8(c, r, r, p, p, 1, most + 1, p, 8, None, None) == -2
+    for tq, tk in ((8, most + 1), (most + 1, 8)):
+        assert L.moe_attn_prefill(r, r, r, 4, 2, 128, p, p, 1, tq, tk, 1, 1.0, p, None, None, None) == -2
