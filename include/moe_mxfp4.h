@@ -393,7 +393,9 @@ int moe_forward_static_scratch(const moe_layer* L, const void* x_dev, int T, voi
  *
  * Masked places do not count, whatever they hold: a key or value that a query
  * does not see does not change its result, not even if it is inf or NaN. A
- * query that sees nothing gets a zero output and a log-sum-exp of -inf. */
+ * query that sees nothing gets a zero output and a log-sum-exp of -inf.
+ *
+ * Outputs overlap neither inputs nor one another. */
 
 /* Rows of bf16 heads: element (token t, head h, channel c) is
  * data[t * token_stride + h * head_stride + c] (strides in elements, multiples
@@ -522,13 +524,13 @@ int moe_attn_decode_fp8(const moe_kv_cache* cache, const moe_rows* q, int n_head
  *                     the last
  *   kept_weights_dev  fp32 [n_seq][n_kv_heads][keep]: their weights, 0 past the
  *                     last (NULL: not returned)
- *   new_lengths_dev   int32 [n_seq]: min(L, keep); not lengths_dev, nor
- *                     kept_weights_dev weights_dev
+ *   new_lengths_dev   int32 [n_seq]: min(L, keep)
  *   dev_status        device int (may be NULL): MOE_DEV_INDEX_OOB as in
  *                     moe_attn_decode_fp8; a position whose page is outside
  *                     the cache is kept as zeros, a destination page outside
  *                     it is not written
- * Errors: MOE_ERR_INVALID_ARG (also recent outside [0, keep], keep < 1),
+ * Errors: MOE_ERR_INVALID_ARG (also recent outside [0, keep], keep < 1; an
+ * output that overlaps an input or another output),
  * MOE_ERR_UNSUPPORTED_SHAPE (the cache's sizes, n_seq > 65535),
  * MOE_ERR_BUFFER_TOO_SMALL (dst_width * page_size below min(keep, table_width
  * * page_size)), MOE_ERR_NO_DEVICE, MOE_ERR_CUDA. */

@@ -32,6 +32,11 @@ int check_cache(const moe_kv_cache* c, bool buffers) {
 constexpr int64_t kMaxRows = INT32_MAX - 65535;
 bool table_ok(int width, int page) { return width >= 0 && (int64_t)width * page <= kMaxRows; }
 
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+
 int check_decode_shape(const moe_kv_cache* c, int n_seq, int n_new, int n_heads, int width) {
   int st = check_cache(c, false);
   if (st != MOE_OK) return st;
@@ -185,9 +190,16 @@ extern "C" int moe_kv_evict_fp8(const moe_kv_cache* cache, const int32_t* page_t
   MOE_CHECK_ARG((int64_t)dst_width * page >= most, MOE_ERR_BUFFER_TOO_SMALL);
   if (n_seq == 0) return MOE_OK;
   MOE_CHECK_ARG(lengths_dev && kept_dev && new_lengths_dev, MOE_ERR_INVALID_ARG);
-  // other heads still read the old ones when the new are written
-  MOE_CHECK_ARG(new_lengths_dev != lengths_dev && (!kept_weights_dev || kept_weights_dev != weights_dev),
-                MOE_ERR_INVALID_ARG);
+  // other heads still read the inputs when one writes its outputs
+  const size_t pairs = (size_t)n_seq * cache->n_kv_heads, n_kept = pairs * keep * 4, n_len = (size_t)n_seq * 4;
+  const struct { const void* p; size_t bytes; }
+      outs[3] = {{kept_dev, n_kept}, {kept_weights_dev, n_kept}, {new_lengths_dev, n_len}},
+      ins[4] = {{lengths_dev, n_len}, {weights_dev, pairs * weights_stride * 4},
+                {page_table_dev, (size_t)n_seq * table_width * 4}, {dst_table_dev, (size_t)n_seq * dst_width * 4}};
+  for (const auto& o : outs) {
+    for (const auto& i : ins) MOE_CHECK_ARG(!overlap(o.p, o.bytes, i.p, i.bytes), MOE_ERR_INVALID_ARG);
+    for (const auto& q : outs) MOE_CHECK_ARG(&o == &q || !overlap(o.p, o.bytes, q.p, q.bytes), MOE_ERR_INVALID_ARG);
+  }
   MOE_CHECK_ARG(table_width == 0 || (page_table_dev && dst_table_dev && weights_dev), MOE_ERR_INVALID_ARG);
   DeviceInfo di;
   if ((st = current_device(&di))) return st;

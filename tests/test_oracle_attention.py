@@ -169,3 +169,22 @@ def test_more_rows_than_32_bits_can_step_over_are_refused(mx):
     assert L.moe_kv_append_fp8(c, r, r, p, p, 1, most + 1, p, 8, None, None) == -2
     for tq, tk in ((8, most + 1), (most + 1, 8)):
         assert L.moe_attn_prefill(r, r, r, 4, 2, 128, p, p, 1, tq, tk, 1, 1.0, p, None, None, None) == -2
+
+
+def test_eviction_refuses_outputs_that_overlap(mx):
+    """Any overlap, not only equal addresses: 2 sequences, 2 heads, keep 8, weights of 64 positions each."""
+    c = ctypes.byref(mx.moe_kv_cache(4, 64, 2, 128, 256, 256, 256, 256))
+    names = ["table", "lengths", "weights", "dst", "kept", "kept_weights", "new_lengths"]
+    size = dict(table=8, lengths=8, weights=2 * 2 * 64 * 4, dst=8, kept=2 * 2 * 8 * 4, kept_weights=2 * 2 * 8 * 4, new_lengths=8)
+
+    def call(**at):
+        a = {n: ctypes.c_void_p(at.get(n, 4096 * (i + 1))) for i, n in enumerate(names)}
+        return mx.lib.moe_kv_evict_fp8(c, a["table"], 1, a["lengths"], 2, a["weights"], 64, 8, 2, a["dst"], 1, a["kept"],
+                                       a["kept_weights"], a["new_lengths"], None, None)
+
+    for out in names[4:]:
+        for other in names:
+            if other != out:
+                base = 1 << 16
+                for shift in (0, size[other] - 4, 4 - size[out]):
+                    assert call(**{other: base, out: base + shift}) == -1, (out, other, shift)
