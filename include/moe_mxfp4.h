@@ -426,8 +426,9 @@ typedef struct moe_rows {
  * keys; below 2^-80 they lose bits.
  * Errors: MOE_ERR_INVALID_ARG (null pointer, negative size, stride or address
  * not aligned, scale not finite), MOE_ERR_UNSUPPORTED_SHAPE (head_dim,
- * n_heads % n_kv_heads, n_seq > 65536, more than 2^31 - 65536 rows),
- * MOE_ERR_NO_DEVICE, MOE_ERR_CUDA. */
+ * n_heads % n_kv_heads, n_heads > 65535, n_seq > 65536, more than 2^31 - 65536
+ * rows, a token_stride of 0 with more than one row, which the calls over the
+ * cache take), MOE_ERR_NO_DEVICE, MOE_ERR_CUDA. */
 int moe_attn_prefill(const moe_rows* q, const moe_rows* k, const moe_rows* v, int n_heads, int n_kv_heads,
                      int head_dim, const int32_t* cu_q_dev, const int32_t* cu_k_dev, int n_seq, int total_q,
                      int total_k, int causal, float scale, void* out_dev, float* lse_dev, int* dev_status,

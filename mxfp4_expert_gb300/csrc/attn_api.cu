@@ -66,6 +66,9 @@ extern "C" int moe_attn_prefill(const moe_rows* q, const moe_rows* k, const moe_
   if ((st = check_rows(q))) return st;
   // keys may be absent altogether: every query then sees nothing
   if (total_k > 0 && ((st = check_rows(k)) || (st = check_rows(v)))) return st;
+  // a tensor map has no rows that lie on one another
+  MOE_CHECK_ARG((total_q <= 1 || q->token_stride) && (total_k <= 1 || (k->token_stride && v->token_stride)),
+                MOE_ERR_UNSUPPORTED_SHAPE);
   MOE_CHECK_ARG(cu_q_dev && cu_k_dev && out_dev && aligned(out_dev, 16), MOE_ERR_INVALID_ARG);
   DeviceInfo di;
   if ((st = current_device(&di))) return st;

@@ -859,7 +859,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
 // boxes of 64 channels of one head by 128 tokens, 128-byte swizzle. The outer
 // dimension is the one with the larger stride.
 int encode_rows(PfParams* p, int w, const __nv_bfloat16* base, int tokens, int heads, int D, int64_t ts, int64_t hs) {
-  if (tokens > 1 && ts == 0) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (heads > 1 && hs == 0) {
     p->one_head[w] = 1;
     heads = 1;

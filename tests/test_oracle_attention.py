@@ -188,3 +188,11 @@ def test_eviction_refuses_outputs_that_overlap(mx):
                 base = 1 << 16
                 for shift in (0, size[other] - 4, 4 - size[out]):
                     assert call(**{other: base, out: base + shift}) == -1, (out, other, shift)
+
+
+def test_prompt_refuses_what_its_header_says(mx):
+    """Limits of moe_attn_prefill alone: a broadcast token stride, many heads."""
+    p, r, one = ctypes.c_void_p(256), ctypes.byref(mx.moe_rows(256, 128, 128)), ctypes.byref(mx.moe_rows(256, 0, 128))
+    pre = lambda q=r, k=r, v=r, h=4, tq=8, tk=8: mx.lib.moe_attn_prefill(  # noqa: E731
+        q, k, v, h, 1, 128, p, p, 1, tq, tk, 1, 1.0, p, None, None, None)
+    assert pre(q=one) == pre(k=one) == pre(v=one) == pre(h=65536) == -2
