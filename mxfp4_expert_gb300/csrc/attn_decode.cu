@@ -76,15 +76,21 @@ struct DecPlan {
   int nt, rt;         // blocks of 8 query rows per warp; row tiles
 };
 // A block of 8 query rows takes a warp 32 registers for the output and 16 for q at
-// head_dim 128; one-block warps fit twelve to a CTA, others eight. More than 16
-// rows are cut into tiles of one block whose warps read the same positions: 20
-// rows (16 sequences of 20,011, page 16) took 109 us as one tile of three blocks
-// with eight warps, 94 as three tiles with twelve. At 32 rows two tiles of two
-// blocks and four of one are equal (114.5 and 116.4 us). Beyond, twelve warps do
-// not divide into tiles of one block any more, so blocks are put together.
+// head_dim 128; one-block warps fit twelve to a CTA, others eight. Up to 32 rows
+// are tiles of one block whose warps read the same positions; beyond, tiles of two
+// or three blocks.
+// us for 16 sequences of 20,011, page 16, head_dim 128 and 64:
+//   12 rows  two tiles of one block 65.3 and 49.3, one of two 66.1 and 51.4 (1,000
+//            positions: 20.6 and 18.5, 26.0 and 19.6)
+//   16 rows  the same 69.8 and 49.3, 67.7 and 51.4 (24.6 and 18.5, 26.8 and 19.7)
+//   20 rows  three tiles of one block 94, one of three 109 (head_dim 128)
+//   32 rows  four of one 116.4, two of two 114.5 (head_dim 128)
+//   48 rows  two of three 177.5 and 107.4, four of two 201 and 149, six of one 165
+//            and 117
+//   64 rows  four of two 209 and 152, two of four 325 and 151 (spills)
 inline DecPlan dec_plan(int rows) {
   if (rows <= 8) return {1, 1};
-  if (rows <= 16) return {2, 1};
+  if (rows <= 16) return {1, 2};
   if (rows <= 24) return {1, 3};
   if (rows <= 32) return {1, 4};
   if (rows <= 48) return {3, 2};
@@ -937,9 +943,9 @@ template <int D, bool WT>
 int launch_plan(const DecParams& p, const DecPlan& pl, int n_cta, cudaStream_t s) {
   if (pl.nt == 1 && pl.rt == 3) return launch_one<D, 1, 3, WT>(p, n_cta, s);
   if (pl.nt == 1 && pl.rt == 4) return launch_one<D, 1, 4, WT>(p, n_cta, s);
+  if (pl.nt == 1 && pl.rt == 2) return launch_one<D, 1, 2, WT>(p, n_cta, s);
   if (pl.nt == 1) return launch_one<D, 1, 1, WT>(p, n_cta, s);
-  if (pl.rt == 1) return launch_one<D, 2, 1, WT>(p, n_cta, s);
-  if (pl.rt == 2) return launch_one<D, 3, 2, WT>(p, n_cta, s);
+  if (pl.nt == 3) return launch_one<D, 3, 2, WT>(p, n_cta, s);
   return launch_one<D, 2, 4, WT>(p, n_cta, s);
 }
 

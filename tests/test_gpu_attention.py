@@ -943,3 +943,11 @@ def test_prompt_equal_keys_and_the_largest_values(mx):
     v = torch.full((n, 1, d), 2.0 ** 127, dtype=torch.bfloat16, device="cuda")
     out = mx.moe_attn_prefill(q, k, v, _cu([3]), _cu([n]))
     assert torch.all(out == 2.0 ** 127)
+
+
+@pytest.mark.parametrize("T,hq,H", [(5, 7, 1), (5, 16, 2), (6, 8, 1), (7, 14, 2), (7, 8, 1), (8, 24, 4), (7, 27, 3), (1, 49, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("weights", [False, True])
+def test_decode_more_than_32_rows(mx, T, hq, H, d, weights):
+    """Every number of row tiles and blocks above 32 query rows, work split over CTAs or not."""
+    _check_decode(mx, [200, 9, 77, 1500], T, hq, H, d, 32, seed=T + hq, weights=weights)
