@@ -530,8 +530,8 @@ int moe_attn_decode_fp8(const moe_kv_cache* cache, const moe_rows* q, int n_head
  *                     moe_attn_decode_fp8; a position whose page is outside
  *                     the cache is kept as zeros, a destination page outside
  *                     it is not written
- * Errors: MOE_ERR_INVALID_ARG (also recent outside [0, keep], keep < 1; an
- * output that overlaps an input or another output),
+ * Errors: MOE_ERR_INVALID_ARG (also recent outside [0, keep], keep outside
+ * [1, 2^31 - 65536]; an output that overlaps an input or another output),
  * MOE_ERR_UNSUPPORTED_SHAPE (the cache's sizes, n_seq > 65535),
  * MOE_ERR_BUFFER_TOO_SMALL (dst_width * page_size below min(keep, table_width
  * * page_size)), MOE_ERR_NO_DEVICE, MOE_ERR_CUDA. */

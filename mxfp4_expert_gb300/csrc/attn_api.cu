@@ -187,7 +187,7 @@ extern "C" int moe_kv_evict_fp8(const moe_kv_cache* cache, const int32_t* page_t
   if ((st = check_cache(cache, true))) return st;
   const int page = cache->page_size;
   MOE_CHECK_ARG(n_seq >= 0 && table_ok(table_width, page) && table_ok(dst_width, page), MOE_ERR_INVALID_ARG);
-  MOE_CHECK_ARG(keep >= 1 && recent >= 0 && recent <= keep && weights_stride >= 0, MOE_ERR_INVALID_ARG);
+  MOE_CHECK_ARG(keep >= 1 && keep <= kMaxRows && recent >= 0 && recent <= keep && weights_stride >= 0, MOE_ERR_INVALID_ARG);
   MOE_CHECK_ARG(n_seq <= 65535, MOE_ERR_UNSUPPORTED_SHAPE);
   const int64_t most = (int64_t)table_width * page < keep ? (int64_t)table_width * page : keep;
   MOE_CHECK_ARG((int64_t)dst_width * page >= most, MOE_ERR_BUFFER_TOO_SMALL);

@@ -196,3 +196,10 @@ def test_prompt_refuses_what_its_header_says(mx):
     pre = lambda q=r, k=r, v=r, h=4, tq=8, tk=8: mx.lib.moe_attn_prefill(  # noqa: E731
         q, k, v, h, 1, 128, p, p, 1, tq, tk, 1, 1.0, p, None, None, None)
     assert pre(q=one) == pre(k=one) == pre(v=one) == pre(h=65536) == -2
+
+
+def test_eviction_refuses_more_places_than_32_bits_can_step_over(mx):
+    c = ctypes.byref(mx.moe_kv_cache(4, 64, 2, 128, 256, 256, 256, 256))
+    at = [ctypes.c_void_p((i + 1) << 40) for i in range(6)]
+    assert mx.lib.moe_kv_evict_fp8(c, at[0], 1, at[1], 1, at[2], 64, 2 ** 31 - 65535, 8, at[3], 1, at[4], None, at[5], None,
+                                   None) == -1
