@@ -493,7 +493,11 @@ int moe_kv_append_fp8(const moe_kv_cache* cache, const moe_rows* k, const moe_ro
  *                zero them before its first use, every call leaves them at
  *                zero. One workspace serves calls of any sizes for which it is
  *                large enough, one after another; calls that may overlap in
- *                time need one each.
+ *                time need one each. With weights it holds the scores: 4 bytes
+ *                for each sequence, position that its table holds, key/value
+ *                head and query row (n_new * n_heads / n_kv_heads, rounded up
+ *                to 8 and from 33 to 48 or 64), so a table no wider than the
+ *                longest sequence needs saves memory.
  *   dev_status   device int (may be NULL): MOE_DEV_INDEX_OOB (a length outside
  *                [0, table_width * page_size] or above weights_stride is cut
  *                to it; a page outside the cache counts as masked)

@@ -48,8 +48,9 @@
 //   - the first 64 keys' product runs while the other 64 are worked on;
 //   - little code: the two halves are one loop and waits call one function. With
 //     the halves unrolled the warps waited twice as long for instructions.
-// 16,384 tokens, 16 heads over 2 of 128, causal: 700 us, 1,571 TFLOP/s; whole
-// tiles of scores, halves unrolled: 749 us.
+// 16,384 tokens, 16 heads over 2 of 128, causal: 690 us, 1,590 TFLOP/s (call
+// after call the card's power limit makes it 730); whole tiles of scores, halves
+// unrolled, were 749.
 //
 // Masked places must not count, whatever they hold, but 0 * inf is NaN in the
 // second product. For a tile that some query of the item does not see whole the

@@ -445,7 +445,7 @@ constexpr int kGatThreads = 256;
 // a random place: 4.2 TB/s in all for such reads, 7.1 for long ones. Before it
 // lies a chain of loads (kept position, its page, scale and codes), so many small
 // CTAs per SM (with 4 instead of 8, 61.5 us instead of 56.2 for the call). 16 x
-// 32,768 positions of 4 heads to 4,096 each: 35 us, 134 MB.
+// 32,768 positions of 4 heads to 4,096 each: 32 us, 134 MB.
 template <int NV>
 __global__ void __launch_bounds__(kGatThreads, NV <= 4 ? 8 : 4) evict_gather_kernel(const EvictArgs a) {
   __shared__ int s_page[128];        // source page of each slot, -1: none
@@ -559,10 +559,10 @@ int launch_kv_evict(const EvictArgs& a, const DeviceInfo& di, cudaStream_t s) {
   const int P = a.c.page_size;
   const int64_t cap = std::min((int64_t)a.width * P, a.w_stride);
   // More CTAs per pair while each keeps enough positions and all run at once. The
-  // whole call, us with 1, 2, 4 and 8 CTAs a pair: 4 pairs of 4,096 15.6, 18.7,
-  // 20.7, -; 16 of 9,000 23.9, 26.0, 28.0, -; 4 of 32,768 30.8, 24.6, 23.3, 32.6;
-  // 16 of 32,768 37.0, 31.1, 30.6, 61.7; 64 of 32,768 63.8, 56.1, 70.5, -; 8 of
-  // 100,000 78.4, 53.6, 37.1, 38.9.
+  // whole call, us with 1, 2, 4 and 8 CTAs a pair: 4 pairs of 4,096 14.5, 18.5,
+  // 20.6, 30.8; 16 of 9,000 18.6, 22.6, 24.6, 55.5; 4 of 32,768 29.6, 24.6, 22.7,
+  // 30.9; 16 of 32,768 32.9, 28.7, 26.9, 59.5; 64 of 32,768 59.4, 51.5, 67.7, 163;
+  // 8 of 100,000 77.3, 53.3, 36.6, 37.1.
   int csize = 1;
   while (csize < kSelCluster && 2 * (int64_t)csize * kSelEach <= cap &&
          2 * (int64_t)csize * a.c.n_kv_heads * a.n_seq <= di.sm_count)
