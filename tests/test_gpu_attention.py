@@ -834,7 +834,7 @@ def test_decode_one_workspace_for_batches_of_any_size(mx, d):
             assert torch.equal(a, b), (H, n_seq, T, G)
 
 
-@pytest.mark.parametrize("T,hq", [(1, 2), (3, 4), (5, 4)])
+@pytest.mark.parametrize("T,hq", [(1, 2), (3, 4), (5, 4), (8, 5), (8, 8)])
 def test_decode_many_sequences(mx, T, hq):
     """More sequences than a CTA has threads, empty ones among them."""
     lens = [(i * 37) % 70 if i % 5 else 0 for i in range(900)]
