@@ -42,7 +42,8 @@
 //            carry the difference of the scales, and their reference is the
 //            largest product of both, so no page is rounded for another's sake.
 // The references of O and of the sum follow the maximum only when it passes them
-// by 2^30: fp32 has the range, and O is hardly ever rescaled.
+// by 2^30: fp32 has the range, and O is hardly ever rescaled. Scores may be of any
+// size (kFar); partial results carry O's reference relative to the sum's.
 //
 // Measured: 32 sequences of up to 65,536, 8 heads of 64: 265 us, 6.3 TB/s. 16 of
 // up to 20,011, 4 heads of 128, 20 query rows, page 16: 92 us, 2.6 TB/s: three
@@ -59,16 +60,20 @@ namespace {
 
 constexpr int kMaxSeqs = 4096;
 constexpr float kRaise = 30.0f;    // log2 by which a score may pass the reference
+// Beyond this a score and a value scale's exponent, or 12, do not add up exactly in
+// fp32. Where a row's largest score is, the warp takes its rows' scores relative to
+// a base of their own, a score that the row has, and starts the chunk anew.
+constexpr float kFar = 4194304.0f;
 constexpr int kChunk = 32;         // positions per warp step
 constexpr int kInRing = 1 << 30;   // flag of a partial result's pair: it lies in the ring
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Workspace: counters, always this many bytes, one for each CTA; then partials,
-// then (with weights) the rows' log2-sum-exp and the scores.
+// then (with weights) the rows' references and sums, and the scores.
 constexpr size_t kCounterBytes = MOE_ATTN_DECODE_COUNTER_BYTES;
 constexpr int kMaxCtas = int(kCounterBytes / 4);
 struct DecWs {
-  size_t parts, lse2, scores, total;
+  size_t parts, norm, scores, total;
   int n_cta, rows;    // CTAs; query rows padded to the row tiles
 };
 
@@ -102,7 +107,7 @@ struct DecParams {
   int G, rows;              // query heads per kv head; query rows n_new * G
   unsigned* counter;        // [CTAs]: of the pair that begins in the CTA and reaches past it
   float* parts;             // per CTA: 2 partial results, then 2 per warp: [rows][D] outputs, [rows][4] references and sum
-  float* lse2;              // [n_seq * n_kv][rows padded] (weights)
+  float2* norm;             // [n_seq * n_kv][rows padded]: reference and 1 / sum (weights)
   float* scores;            // [n_seq * n_kv][cap][rows padded] (weights)
   int64_t cap;
   int log2_page;
@@ -217,6 +222,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
   constexpr int kDecWarps = C::kWarps, kDecThreads = C::kThreads;
   __shared__ int s_scan[kDecWarps];
   __shared__ Edge s_edge[2];
+  __shared__ float s_base[kDecWarps][8 * NT];   // see kFar
   __shared__ int s_pair[2 * C::kGroups];   // pairs of the warps' partial results, -1: none
   const DecodeArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
@@ -279,13 +285,19 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
     }
     return lo;
   };
-  // (O, its reference, sum, its reference) of 4 channels of a row, + another's
+  // (O, its reference relative to m, m, sum) of 4 channels of a row, + another's
   struct Acc {
     float4 o;
     float r, m, l;
   };
   auto join = [](Acc& x, float4 v, float r, float mw, float lw) {
     if (mw == -INFINITY && lw == 0.0f) return;   // saw nothing
+    const float M = fmaxf(x.m, mw);
+    const float dx = x.m == M ? 0.0f : x.m - M, dw = mw == M ? 0.0f : mw - M;
+    x.m = M;
+    x.l = x.l * ex2(dx) + lw * ex2(dw);
+    x.r += dx;
+    r += dw;
     if (r > -INFINITY) {
       const float R = fmaxf(x.r, r);
       const float f0 = x.r == R ? 1.0f : ex2(x.r - R), f1 = r == R ? 1.0f : ex2(r - R);
@@ -295,30 +307,26 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
       x.o.z = x.o.z * f0 + v.z * f1;
       x.o.w = x.o.w * f0 + v.w * f1;
     }
-    const float M = fmaxf(x.m, mw);
-    const float g0 = x.m == M ? 1.0f : ex2(x.m - M), g1 = mw == M ? 1.0f : ex2(mw - M);
-    x.m = M;
-    x.l = x.l * g0 + lw * g1;
   };
   auto tok_of = [&](int r) { return int(uint32_t(r) * p.g_magic >> 16); };   // new token of a query row
-  // What O is multiplied with for the output, 2^(r - m) / l, as two factors, x
-  // first: r holds a value scale of 2^-127 to 2^127 and may lie 30 from the
-  // maximum as m may, so 2^(r - m) can leave fp32's range where the output does not.
-  auto out_factor = [](float r, float m, float l) {
+  // What O is multiplied with for the output, 2^r / l, as two factors, x first: r
+  // holds a value scale of 2^-127 to 2^127 and may lie 30 from the maximum as m
+  // may, so 2^r can leave fp32's range where the output does not.
+  auto out_factor = [](float r, float l) {
     if (l == 0.0f) return make_float2(0.0f, 0.0f);             // nothing seen: zeros
     if (r == -INFINITY) return make_float2(l, 1.0f);           // a row of NaN scores: NaN
-    const float f = ex2(0.5f * (r - m));
+    const float f = ex2(0.5f * r);
     return make_float2(f / l, f);
   };
   auto write_lse = [&](int b, int h, int r, int64_t row, float m, float l) {
-    const float lse2 = l == 0.0f ? -INFINITY : (m == -INFINITY ? l : m + log2f(l));
-    if (a.lse) a.lse[row] = lse2 * kLn2;
-    if (WT) p.lse2[((int64_t)b * H + h) * C::kRows + r] = lse2;
+    const float m0 = m == -INFINITY ? 0.0f : m;   // nothing seen, or NaN scores
+    if (a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (m0 + log2f(l)) * kLn2;
+    if (WT) p.norm[((int64_t)b * H + h) * C::kRows + r] = make_float2(m0, l == 0.0f ? 0.0f : 1.0f / l);
   };
   auto finish = [&](int b, int h, int r, int d4, const Acc& x) {
     const int tok = tok_of(r);
     const int64_t row = ((int64_t)b * T + tok) * a.n_heads + h * p.G + r - tok * p.G;
-    const float2 f = out_factor(x.r, x.m, x.l);
+    const float2 f = out_factor(x.r, x.l);
     const __nv_bfloat162 y0 = __floats2bfloat162_rn(x.o.x * f.x * f.y, x.o.y * f.x * f.y);
     const __nv_bfloat162 y1 = __floats2bfloat162_rn(x.o.z * f.x * f.y, x.o.w * f.x * f.y);
     uint2 y;
@@ -494,7 +502,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
       }
     }
 
-    // O (in units of 2^ro), the sum (of 2^m)
+    // O (in units of 2^ro), the sum (of 2^m). `far`: relative to the row's s_base
     float o[MT][NT][4], m[NT][2], ro[NT][2], l[NT][2];
 #pragma unroll
     for (int t = 0; t < MT; ++t)
@@ -506,6 +514,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int j = 0; j < 2; ++j) m[n][j] = ro[n][j] = -INFINITY, l[n][j] = 0.0f;
+    bool far = false;
 
 #pragma unroll 1
     for (; i < i1; ++i) {
@@ -579,49 +588,88 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
           }
           // the chunk's largest score, and largest score times value scale
           float us[2], ms[2];
+#pragma unroll 1
+          while (true) {
+            if (far) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float xa = fmaxf(s[0][n][j], s[0][n][j + 2]), xb = fmaxf(s[1][n][j], s[1][n][j + 2]);
-            us[j] = fmaxf(xa + vfa, xb + vfb);
-            us[j] = fmaxf(us[j], __shfl_xor_sync(0xFFFFFFFFu, us[j], 4));
-            us[j] = fmaxf(us[j], __shfl_xor_sync(0xFFFFFFFFu, us[j], 8));
-            us[j] = fmaxf(us[j], __shfl_xor_sync(0xFFFFFFFFu, us[j], 16));
-            ms[j] = fmaxf(xa, xb);
-          }
-          if (va == vb) {
-            ms[0] = us[0] - vfa;
-            ms[1] = us[1] - vfa;
-          } else {
+              for (int j = 0; j < 2; ++j) {
+                float x = fmaxf(fmaxf(s[0][n][j], s[0][n][j + 2]), fmaxf(s[1][n][j], s[1][n][j + 2]));
+#pragma unroll
+                for (int k = 4; k < 32; k <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, k));
+                float base = s_base[warp][n * 8 + 2 * c + j];
+                __syncwarp();
+                if (x > base + kRaise || (m[n][j] == -INFINITY && x > -INFINITY)) {
+                  m[n][j] += base - x;
+                  ro[n][j] += base - x;
+                  s_base[warp][n * 8 + 2 * c + j] = base = x;
+                }
+#pragma unroll
+                for (int k = j; k < 4; k += 2) s[0][n][k] -= base, s[1][n][k] -= base;
+              }
+              __syncwarp();
+            }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              ms[j] = fmaxf(ms[j], __shfl_xor_sync(0xFFFFFFFFu, ms[j], 4));
-              ms[j] = fmaxf(ms[j], __shfl_xor_sync(0xFFFFFFFFu, ms[j], 8));
-              ms[j] = fmaxf(ms[j], __shfl_xor_sync(0xFFFFFFFFu, ms[j], 16));
+              const float xa = fmaxf(s[0][n][j], s[0][n][j + 2]), xb = fmaxf(s[1][n][j], s[1][n][j + 2]);
+              us[j] = fmaxf(xa + vfa, xb + vfb);
+              us[j] = fmaxf(us[j], __shfl_xor_sync(0xFFFFFFFFu, us[j], 4));
+              us[j] = fmaxf(us[j], __shfl_xor_sync(0xFFFFFFFFu, us[j], 8));
+              us[j] = fmaxf(us[j], __shfl_xor_sync(0xFFFFFFFFu, us[j], 16));
+              ms[j] = fmaxf(xa, xb);
             }
-          }
-          const bool raise = ms[0] > m[n][0] + kRaise || ms[1] > m[n][1] + kRaise || us[0] > ro[n][0] + kRaise ||
-                             us[1] > ro[n][1] + kRaise;
-          if (__any_sync(0xFFFFFFFFu, raise)) {
+            if (va == vb) {
+              ms[0] = us[0] - vfa;
+              ms[1] = us[1] - vfa;
+            } else {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              if (ms[j] > m[n][j] + kRaise) {
-                l[n][j] *= ex2(m[n][j] - ms[j]);
-                m[n][j] = ms[j];
-              }
-              if (us[j] > ro[n][j] + kRaise) {
-                const float f = ex2(ro[n][j] - us[j]);
-                ro[n][j] = us[j];
-#pragma unroll
-                for (int t = 0; t < MT; ++t) o[t][n][j] *= f, o[t][n][j + 2] *= f;
+              for (int j = 0; j < 2; ++j) {
+                ms[j] = fmaxf(ms[j], __shfl_xor_sync(0xFFFFFFFFu, ms[j], 4));
+                ms[j] = fmaxf(ms[j], __shfl_xor_sync(0xFFFFFFFFu, ms[j], 8));
+                ms[j] = fmaxf(ms[j], __shfl_xor_sync(0xFFFFFFFFu, ms[j], 16));
               }
             }
+            const bool raise = ms[0] > m[n][0] + kRaise || ms[1] > m[n][1] + kRaise || us[0] > ro[n][0] + kRaise ||
+                               us[1] > ro[n][1] + kRaise;
+            if (__any_sync(0xFFFFFFFFu, raise)) {
+              const bool out_there = (fabsf(ms[0]) > kFar && ms[0] > -INFINITY) || (fabsf(ms[1]) > kFar && ms[1] > -INFINITY);
+              if (!far && __any_sync(0xFFFFFFFFu, out_there)) {   // once more, relative to bases
+                far = true;
+#pragma unroll
+                for (int k = 0; k < NT; ++k)
+#pragma unroll
+                  for (int j = 0; j < 2; ++j) {
+                    const float base = m[k][j] == -INFINITY ? 0.0f : m[k][j];
+                    s_base[warp][k * 8 + 2 * c + j] = base;
+                    m[k][j] -= base;
+                    ro[k][j] -= base;
+                  }
+                __syncwarp();
+                continue;
+              }
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                if (ms[j] > m[n][j] + kRaise) {
+                  l[n][j] *= ex2(m[n][j] - ms[j]);
+                  m[n][j] = ms[j];
+                }
+                if (us[j] > ro[n][j] + kRaise) {
+                  const float f = ex2(ro[n][j] - us[j]);
+                  ro[n][j] = us[j];
+#pragma unroll
+                  for (int t = 0; t < MT; ++t) o[t][n][j] *= f, o[t][n][j + 2] *= f;
+                }
+              }
+            }
+            break;
           }
           // probabilities times 2^12 over the chunk's largest
           float pr[2][4];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const bool none = us[j] == -INFINITY;
-            const float ref = none ? 0.0f : 12.0f - us[j];
+            // nothing seen, NaN scores only, or all so far below the reference (which is above
+            // -kFar) that they count for nothing and would not add up with the 12
+            const bool none = !(us[j] > -2.0f * kFar);
+            const float ref = none ? -INFINITY : 12.0f - us[j];
             beta[n][j] = none ? 0.0f : ex2(us[j] - 12.0f - ro[n][j]);
 #pragma unroll
             for (int x = j; x < 4; x += 2) {
@@ -737,21 +785,31 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
         sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 4);
         sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 8);
         sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
-        const int rr = n * 8 + 2 * c + j, r = rt * 8 * NT + rr;
+        const int lr = n * 8 + 2 * c + j, r = rt * 8 * NT + lr;
+        // the sum's reference as a number of its own, O's relative to that
+        float mm = m[n][j], rr = ro[n][j];
+        if (mm > -INFINITY) {
+          if (far) {
+            sum *= ex2(mm);
+            mm = s_base[warp][lr];
+          } else {
+            rr -= mm;
+          }
+        }
         if (!whole) {
           // 8 lanes write 8 consecutive channels
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
-            part[rr * D + 16 * t + g] = o[t][n][j];
-            part[rr * D + 16 * t + g + 8] = o[t][n][j + 2];
+            part[lr * D + 16 * t + g] = o[t][n][j];
+            part[lr * D + 16 * t + g + 8] = o[t][n][j + 2];
           }
           if (g == 0)
-            *reinterpret_cast<float4*>(part + 8 * NT * D + rr * 4) = make_float4(ro[n][j], m[n][j], sum, 0.0f);
+            *reinterpret_cast<float4*>(part + 8 * NT * D + lr * 4) = make_float4(rr, mm, sum, 0.0f);
         } else {
           const bool have = r < p.rows;
           const int tok = tok_of(r);
           const int64_t row = ((int64_t)b * T + tok) * a.n_heads + h * p.G + r - tok * p.G;
-          const float2 f = out_factor(ro[n][j], m[n][j], sum);
+          const float2 f = out_factor(rr, sum);
           // lanes g and g ^ 1 swap, so that each holds two neighbouring channels
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
@@ -762,7 +820,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
             const __nv_bfloat162 y = __floats2bfloat162_rn(y0, y1);
             if (have) *reinterpret_cast<__nv_bfloat162*>(a.out + row * D + 16 * t + (g & 1 ? g + 7 : g)) = y;
           }
-          if (have && g == 0) write_lse(b, h, r, row, m[n][j], sum);
+          if (have && g == 0) write_lse(b, h, r, row, mm, sum);
         }
       }
     if (!whole && rt == 0 && lane == 0) s_pair[2 * tg + slot] = (b * H + h) | (last_one ? kInRing : 0);
@@ -858,8 +916,9 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
   }
 }
 
-// weights[pair][j] += sum over the query rows of exp(score - log-sum-exp). Bound
-// by reading the scores back, mostly from L2.
+// weights[pair][j] += sum over the query rows of 2^(score - reference) / sum (not
+// of 2^(score - log-sum-exp): in a large one the sum's logarithm is rounded away).
+// Bound by reading the scores back, mostly from L2.
 template <int ROWS>
 __global__ void __launch_bounds__(256) decode_weights_kernel(const DecParams p) {
   const DecodeArgs& a = p.a;
@@ -867,8 +926,9 @@ __global__ void __launch_bounds__(256) decode_weights_kernel(const DecParams p) 
   const int64_t pair = (int64_t)b * a.c.n_kv_heads + h;
   bool ignore = false;
   const int L = dec_length(a, b, &ignore);
-  __shared__ float s_lse[ROWS];
-  for (int r = threadIdx.x; r < ROWS; r += blockDim.x) s_lse[r] = r < p.rows ? p.lse2[pair * ROWS + r] : INFINITY;
+  __shared__ float2 s_norm[ROWS];
+  for (int r = threadIdx.x; r < ROWS; r += blockDim.x)
+    s_norm[r] = r < p.rows ? p.norm[pair * ROWS + r] : make_float2(0.0f, 0.0f);
   __syncthreads();
   // 4 positions per thread and turn, each 4 rows at a time: the loads of all at once
   constexpr int PT = 4;
@@ -894,8 +954,9 @@ __global__ void __launch_bounds__(256) decode_weights_kernel(const DecParams p) 
         const float x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          // rows that are padding have s_lse = inf; rows that see nothing have scores of -inf
-          if (x[i] != -INFINITY) w[k] += ex2(x[i] - s_lse[4 * r4 + i]);
+          // rows that are padding have a factor of 0; rows that see nothing have scores of -inf
+          const float2 f = s_norm[4 * r4 + i];
+          if (x[i] != -INFINITY) w[k] = fmaf(ex2(x[i] - f.x), f.y, w[k]);
         }
       }
     }
@@ -919,8 +980,8 @@ size_t ws_layout(const moe_kv_cache& c, int n_seq, int n_new, int n_heads, int w
   w->n_cta = int(ctas < most ? (ctas ? ctas : 1) : most);
   const size_t part = (size_t)(c.head_dim + 4) * 4 * (2 * w->rows + 2 * warps * 8 * pl.nt);
   w->parts = kCounterBytes;
-  w->lse2 = w->parts + round_up(w->n_cta * part, 256);
-  w->scores = w->lse2 + (weights ? round_up(pairs * w->rows * 4, 256) : 0);
+  w->norm = w->parts + round_up(w->n_cta * part, 256);
+  w->scores = w->norm + (weights ? round_up(pairs * w->rows * 8, 256) : 0);
   w->total = w->scores + (weights ? pairs * cap * w->rows * 4 : 0);
   return w->total;
 }
@@ -969,7 +1030,7 @@ int launch_attn_decode(const DecodeArgs& a, const DeviceInfo& di, cudaStream_t s
   char* base = static_cast<char*>(a.ws);
   p.counter = reinterpret_cast<unsigned*>(base);
   p.parts = reinterpret_cast<float*>(base + w.parts);
-  p.lse2 = reinterpret_cast<float*>(base + w.lse2);
+  p.norm = reinterpret_cast<float2*>(base + w.norm);
   p.scores = reinterpret_cast<float*>(base + w.scores);
   p.cap = (int64_t)a.width * a.c.page_size;
   p.log2_page = a.c.page_size == 16 ? 4 : a.c.page_size == 32 ? 5 : a.c.page_size == 64 ? 6 : 7;

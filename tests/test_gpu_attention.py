@@ -951,3 +951,75 @@ def test_prompt_equal_keys_and_the_largest_values(mx):
 def test_decode_more_than_32_rows(mx, T, hq, H, d, weights):
     """Every number of row tiles and blocks above 32 query rows, work split over CTAs or not."""
     _check_decode(mx, [200, 9, 77, 1500], T, hq, H, d, 32, seed=T + hq, weights=weights)
+
+
+@pytest.mark.parametrize("mag", [1e3, 1e4, 1e5, 1e9, 1e15])
+@pytest.mark.parametrize("mixed", [False, True])
+@pytest.mark.parametrize("hq", [4, 48])
+def test_decode_scores_beyond_24_bits(mx, mag, mixed, hq):
+    """Equal values give that value whatever the scores are, and every query's weights sum to 1; the leading key is there
+    twice. Value scales alike, and different ones for the same values."""
+    n, d, P, H = 3000, 64, 16, 2
+    g = _gen(101)
+    pages = -(-n // P)
+    c = mx.KVCache.alloc(pages, P, H, d)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    q, k = (_bf16(g, 1, 1, hq, d).float() * mag).to(torch.bfloat16), (_bf16(g, n, H, d).float() * mag).to(torch.bfloat16)
+    k[1] = k[2900] = (2 * q[0, 0, ::hq // H].float()).to(torch.bfloat16)   # leads for the first query of each group
+    v = torch.full((n, H, d), 1.5, dtype=torch.bfloat16, device="cuda")
+    mx.moe_kv_append_fp8(c, k, v, _cu([n]), _i32([0]), table)
+    # key pages of one scale, so that the two leading keys are equal
+    c.k_scales.fill_(int(c.k_scales.max()))
+    if mixed:
+        c.v_codes.fill_(0x3C), c.v_scales.fill_(127)          # 1.5
+        c.v_codes[::3], c.v_scales[::3] = 0x74, 120           # 192 * 2^-7
+    for codes in (c.k_codes.view(pages, H, P, d),):
+        codes[2900 // P, :, 2900 % P] = codes[0, :, 1]
+    w = torch.zeros((1, H, n), device="cuda")
+    lse = torch.empty((1, 1, hq), device="cuda")
+    out = mx.moe_attn_decode_fp8(c, q, _i32([n]), table, weights=w, lse=lse)
+    assert torch.all(out == 1.5)
+    assert torch.all((w.double().sum(-1) - hq // H).abs() <= 1e-4 * hq)
+    # the leading pair of the first query shares its weight evenly
+    one = torch.zeros_like(w)
+    for h in range(H):
+        alone = q[:, :, [h * (hq // H)] * H].contiguous()
+        mx.moe_attn_decode_fp8(c, alone, _i32([n]), table, weights=one.zero_())
+        assert abs(float(one[0, h, 1]) - 0.5) < 1e-6 and abs(float(one[0, h, 2900]) - 0.5) < 1e-6
+    assert torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,rise", [(16, False), (16, True), (80, True)])
+def test_decode_small_and_huge_scores_side_by_side(mx, d, hq, rise):
+    """Queries of very different sizes in one warp, several chunks each: the small ones keep their accuracy, the huge ones
+    give the value of the key that leads, wherever it lies."""
+    n, P, H = 20000, 16, 8
+    g = _gen(102)
+    pages, G = n // P, hq // H
+    c = mx.KVCache.alloc(pages, P, H, d)
+    table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)[None]
+    k, v = _bf16(g, n, H, d), _bf16(g, n, H, d)
+    v *= torch.exp2(torch.randint(-3, 4, (n, 1, 1), generator=g, device="cuda")).to(torch.bfloat16)   # scales differ
+    if rise:
+        k = (k.float() * torch.linspace(0.01, 8, n, device="cuda")[:, None, None]).to(torch.bfloat16)
+    mx.moe_kv_append_fp8(c, k, v, _cu([n]), _i32([0]), table)
+    size = torch.tensor([0.05, 3e4, 1.0, 1e9, 1e6], device="cuda").repeat(-(-G // 2))[:G].repeat(H)
+    q = (_bf16(g, 1, 1, hq, d).float() * size[None, None, :, None]).to(torch.bfloat16)
+    lse = torch.empty((1, 1, hq), device="cuda")
+    out = mx.moe_attn_decode_fp8(c, q, _i32([n]), table, lse=lse)
+    codes = {x: t.cpu().numpy() for x, t in (("k", c.k_codes), ("v", c.v_codes))}
+    scales = {x: t.cpu().numpy() for x, t in (("k", c.k_scales), ("v", c.v_scales))}
+    tab, huge = table[0].cpu().numpy(), 0
+    for h in (0, 3, 7):
+        kk, vv = (oa.sequence(codes[x], scales[x], tab, h, n) for x in "kv")
+        for i in range(h * G, (h + 1) * G):
+            r = oa.attend(_np(q[0, 0, i:i + 1]), kk, vv, [n], d ** -0.5)
+            s = np.sort(kk @ _np(q[0, 0, i]) * d ** -0.5)
+            if s[-1] - s[-2] > 100 + 2.0 ** -17 * r["size"][0]:     # one key leads, whatever fp32 rounds
+                err = np.abs(_np(out[0, 0, i]) - r["out"][0])
+                assert np.all(err <= (2.0 ** -8 + 2.0 ** -10) * np.abs(r["out"][0]) + 1e-30), (h, i, float(err.max()))
+                huge += 1
+            else:
+                _near(out[0, 0, i:i + 1], lse[0, 0, i:i + 1], r, 2.0 ** -10)
+    assert huge >= 3
