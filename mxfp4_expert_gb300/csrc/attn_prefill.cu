@@ -44,7 +44,7 @@
 //   - a half's probabilities are taken against the reference that was there,
 //     which is raised, and O rescaled, only where a half passes it by 2^16 (with
 //     scores of 128 keys that rise by 6, 12, 24 and 100 in log2 from tile to tile:
-//     209, 240, 261 and 332 us for 8,192 tokens, 193 where they do not);
+//     211, 242, 260 and 329 us for 8,192 tokens, 189 where they do not);
 //   - the first 64 keys' product runs while the other 64 are worked on;
 //   - little code: the two halves are one loop and waits call one function. With
 //     the halves unrolled the warps waited twice as long for instructions.
@@ -80,6 +80,11 @@ constexpr float kPfMost = 16.0f;   // log2 of what the reference may be passed b
 // and outputs lose bits below 2^-80 (bf16 and fp32 end at 2^-126). An exponent of
 // -38 has 2^-19 as its rounding: 2^-20 of a probability.
 constexpr float kPfBias = 38.0f;
+// A score times c is rounded for the reference and not for the probabilities. Up to
+// 2^31 they differ by 2^64 at most, which the bias leaves room for. Beyond, scores
+// that are not equal differ by 128 at least: only the largest counts, and with the
+// power of two below c in its place both products are exact.
+constexpr float kPfFar = 2147483648.0f;
 constexpr uint32_t kBoxBytes = 128 * 128;      // 128 rows of 64 channels
 constexpr int kScanRing = 4;
 constexpr float kLn2f = 0.6931471805599453f, kLog2ef = 1.4426950408889634f;
@@ -113,6 +118,7 @@ struct PfParams {
   int one_head[3];       // heads share their memory: head coordinate 0
   PrefillArgs a;
   float c;               // |scale| log2(e)
+  float c_pow2;          // the power of two not above c
   int negate;            // scale < 0
 };
 
@@ -661,6 +667,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
       const int vis = a.causal ? min(max(it.t0[j] + row + it.off + 1, 0), it.nk) : it.nk;
       const int vis_w = __shfl_sync(0xFFFFFFFFu, vis, 0);   // the warp's fewest
       float m = -INFINITY, l = 0.0f;   // reference, sum in units of 2^m
+      float cc = c, ref = 0.0f;        // exponent of a probability: score * cc - ref
       unsigned bad = 0;                // masked tiles with non-finite values (a pair's queries span at most 4)
       for (int i = 0; i < nkt; ++i) {
         const int k0 = i * kKT;
@@ -708,11 +715,16 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
             mx[2 * b] = max3(a0, __uint_as_float(x[30]), __uint_as_float(x[31]));
             mx[2 * b + 1] = a1;
           }
-          const float mine = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
+          const float raw = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]), mine = raw * c;
           const float r = (i == 0 && half == 0) || mine > m + kPfMost ? mine : -INFINITY;
           if (__any_sync(0xFFFFFFFFu, r > m)) {
             const float f = r > m ? pf_ex2(m - r) : 1.0f;
-            if (r > m) m = r;
+            if (r > m) {
+              m = r;
+              const bool far = fabsf(m) > kPfFar;
+              cc = far ? P.c_pow2 : c;
+              ref = far ? raw * P.c_pow2 : m + kPfBias;
+            }
             l *= f;
             // what is in O: the earlier tiles' products, which have finished
             // when this tile's second scores have, since these were issued after
@@ -733,8 +745,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
               }
             }
           }
-          const float ref = m == -INFINITY ? 0.0f : m + kPfBias;
-          const uint64_t c2 = pack2(c, c), r2 = pack2(-ref, -ref);
+          const uint64_t c2 = pack2(cc, cc), r2 = pack2(-ref, -ref);
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             uint32_t(&x)[32] = s[b];
@@ -901,6 +912,7 @@ int launch_attn_prefill(const PrefillArgs& a, const DeviceInfo& di, cudaStream_t
   // a scale of 0 must still turn a masked score (-inf) into a probability of 0
   const float c = fabsf(a.scale) * kLog2ef;
   P.c = c > 1e-30f ? c : 1e-30f;
+  P.c_pow2 = exp2f(floorf(log2f(P.c)));
   P.negate = a.scale < 0.0f;
   return a.D == 128 ? launch_pf<128>(P, di, s) : launch_pf<64>(P, di, s);
 }

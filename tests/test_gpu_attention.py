@@ -1023,3 +1023,49 @@ def test_decode_small_and_huge_scores_side_by_side(mx, d, hq, rise):
             else:
                 _near(out[0, 0, i:i + 1], lse[0, 0, i:i + 1], r, 2.0 ** -10)
     assert huge >= 3
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("mag", [1e3, 1e4, 3e4, 1e5, 1e9, 1e15])
+def test_prompt_scores_beyond_31_bits(mx, d, mag):
+    """Equal values give that value whatever the scores are; where one key leads by far, or two equal ones, the result is
+    its value, or their mean, in every tile."""
+    g = _gen(103)
+    n = 700
+    q, k = (_bf16(g, n, 2, d).float() * mag).to(torch.bfloat16), (_bf16(g, n, 1, d).float() * mag).to(torch.bfloat16)
+    lse = torch.empty((n, 2), device="cuda")
+    same = torch.full((n, 1, d), 1.5, dtype=torch.bfloat16, device="cuda")
+    for scale in (None, -d ** -0.5, 3.0):
+        out = mx.moe_attn_prefill(q, k, same, _cu([n]), lse=lse, scale=scale)
+        assert torch.all((out.float() - 1.5).abs() <= 2.0 ** -7) and torch.isfinite(lse).all(), scale
+    # keys of falling, then rising size, the first 64 of them twice in the last tile
+    k = (k.float() * (torch.arange(n, device="cuda") % 200 - 100).abs()[:, None, None] / 50).to(torch.bfloat16)
+    k[-64:] = k[:64]
+    v = _bf16(g, n, 1, d)
+    out = mx.moe_attn_prefill(q, k, v, _cu([n]), causal=False)
+    for h in range(2):
+        s = (q[:, h].double() @ k[:, 0].double().T) * d ** -0.5
+        top = s.amax(-1, keepdim=True)
+        leads = s == top
+        rest = s.masked_fill(leads, -math.inf).amax(-1)
+        clear = top[:, 0] - rest > 100 + 2.0 ** -17 * mag * mag * d ** 0.5 * 50
+        w = (leads / leads.sum(-1, keepdim=True)).double()
+        want, mass = w @ v[:, 0].double(), w @ v[:, 0].double().abs()
+        err = (out[:, h].double() - want).abs()
+        assert int(clear.sum()) > n // 4 and int((leads.sum(-1) == 2)[clear].sum()) > 3
+        assert torch.all(err[clear] <= 2.0 ** -8 * want[clear].abs() + 2.0 ** -8 * mass[clear] + 1e-30)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_small_and_huge_scores_side_by_side(mx, d):
+    """Queries of very different sizes in one tile: the small ones keep their accuracy."""
+    g = _gen(104)
+    n = 600
+    size = torch.tensor([0.05, 3e5, 1.0, 1e9, 2.0, 1e14], device="cuda").repeat(n // 6)
+    q = (_bf16(g, n, 2, d).float() * size[:, None, None]).to(torch.bfloat16)
+    k, v = _bf16(g, n, 1, d), _bf16(g, n, 1, d)
+    lse = torch.empty((n, 2), device="cuda")
+    out = mx.moe_attn_prefill(q, k, v, _cu([n]), lse=lse)
+    ref = oa.attend(_np(q[:, 1]), _np(k[:, 0]), _np(v[:, 0]), np.arange(n) + 1, d ** -0.5)
+    _near(out[:, 1], lse[:, 1], ref, 2.0 ** -8)
+    assert torch.isfinite(out).all()
