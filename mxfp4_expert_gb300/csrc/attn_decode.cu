@@ -81,24 +81,25 @@ struct DecPlan {
   int nt, rt;         // blocks of 8 query rows per warp; row tiles
 };
 // A block of 8 query rows takes a warp 32 registers for the output and 16 for q at
-// head_dim 128; one-block warps fit twelve to a CTA, others eight. Up to 32 rows
-// are tiles of one block whose warps read the same positions; beyond, tiles of two
-// or three blocks.
-// us for 16 sequences of 20,011, page 16, head_dim 128 and 64:
-//   12 rows  two tiles of one block 65.3 and 49.3, one of two 66.1 and 51.4 (1,000
-//            positions: 20.6 and 18.5, 26.0 and 19.6)
-//   16 rows  the same 69.8 and 49.3, 67.7 and 51.4 (24.6 and 18.5, 26.8 and 19.7)
-//   20 rows  three tiles of one block 94, one of three 109 (head_dim 128)
-//   32 rows  four of one 116.4, two of two 114.5 (head_dim 128)
-//   48 rows  two of three 177.5 and 107.4, four of two 201 and 149, six of one 165
-//            and 117
-//   64 rows  four of two 209 and 152, two of four 325 and 151 (spills)
-inline DecPlan dec_plan(int rows) {
+// head_dim 128; one-block warps fit twelve to a CTA, others eight. So row tiles of
+// one block, whose warps read the same positions, while they divide the twelve; at
+// head_dim 64 from 33 rows on, and from 49 always, two or three blocks a warp. us
+// for 16 sequences of 20,011 and of 1,000, page 16, 4 key/value heads (tiles x
+// blocks):
+//         head_dim 128                        head_dim 64
+//   rows  chosen          other               chosen          other
+//   12    2x1  65   20.7  1x2  70   26.8      2x1  50   18.5  1x2  53   20.5
+//   16    2x1  68   24.7  1x2  70   26.8      2x1  49   18.6  1x2  53   20.6
+//   20    3x1  91   26.8  1x3  109  39.1      3x1  66   18.6  1x3  70   26.7
+//   32    4x1  117  30.9  2x2  120  37.0      4x1  85   22.7  2x2  87   24.8
+//   48    6x1  165  37.2  2x3  187  53.4      2x3  111  32.9  6x1  119  26.4
+//   64    4x2  213  53.4  2x4  337  73.4      4x2  154  34.8  2x4  165  43.3
+inline DecPlan dec_plan(int rows, int d) {
   if (rows <= 8) return {1, 1};
   if (rows <= 16) return {1, 2};
   if (rows <= 24) return {1, 3};
   if (rows <= 32) return {1, 4};
-  if (rows <= 48) return {3, 2};
+  if (rows <= 48) return d == 128 ? DecPlan{1, 6} : DecPlan{3, 2};
   return {2, 4};
 }
 
@@ -558,6 +559,48 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
       const float kfa = scale_value(w & 0xFFu), kfb = scale_value(w >> 8 & 0xFFu);
       const float vfa = float(va - 127), vfb = float(vb - 127);
       const int p0 = t0 + 4 * (g >> 1) + (g & 1);
+      // the chunk's largest score, and largest score times value scale
+      auto largest = [&](int n, float (&us)[2], float (&ms)[2]) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float xa = fmaxf(s[0][n][j], s[0][n][j + 2]), xb = fmaxf(s[1][n][j], s[1][n][j + 2]);
+          us[j] = fmaxf(xa + vfa, xb + vfb);
+          us[j] = fmaxf(us[j], __shfl_xor_sync(0xFFFFFFFFu, us[j], 4));
+          us[j] = fmaxf(us[j], __shfl_xor_sync(0xFFFFFFFFu, us[j], 8));
+          us[j] = fmaxf(us[j], __shfl_xor_sync(0xFFFFFFFFu, us[j], 16));
+          ms[j] = fmaxf(xa, xb);
+        }
+        if (va == vb) {
+          ms[0] = us[0] - vfa;
+          ms[1] = us[1] - vfa;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            ms[j] = fmaxf(ms[j], __shfl_xor_sync(0xFFFFFFFFu, ms[j], 4));
+            ms[j] = fmaxf(ms[j], __shfl_xor_sync(0xFFFFFFFFu, ms[j], 8));
+            ms[j] = fmaxf(ms[j], __shfl_xor_sync(0xFFFFFFFFu, ms[j], 16));
+          }
+        }
+      };
+      // `far`: a row's scores relative to its base, which follows the largest
+      auto rebase = [&](int n) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float x = fmaxf(fmaxf(s[0][n][j], s[0][n][j + 2]), fmaxf(s[1][n][j], s[1][n][j + 2]));
+#pragma unroll
+          for (int k = 4; k < 32; k <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, k));
+          float base = s_base[warp][n * 8 + 2 * c + j];
+          __syncwarp();
+          if (x > base + kRaise || (m[n][j] == -INFINITY && x > -INFINITY)) {
+            m[n][j] += base - x;
+            ro[n][j] += base - x;
+            s_base[warp][n * 8 + 2 * c + j] = base = x;
+          }
+#pragma unroll
+          for (int k = j; k < 4; k += 2) s[0][n][k] -= base, s[1][n][k] -= base;
+        }
+        __syncwarp();
+      };
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         {
@@ -586,81 +629,41 @@ __global__ void __launch_bounds__(DecCfg<D, NT, RT, WT>::kThreads, 1) decode_att
                   *reinterpret_cast<float2*>(sp + (16 * mt + 2 * x) * C::kRows) =
                       make_float2(s[mt][n][2 * x], s[mt][n][2 * x + 1]);
           }
-          // the chunk's largest score, and largest score times value scale
+          if (far) rebase(n);
           float us[2], ms[2];
-#pragma unroll 1
-          while (true) {
-            if (far) {
+          largest(n, us, ms);
+          const bool raise = ms[0] > m[n][0] + kRaise || ms[1] > m[n][1] + kRaise || us[0] > ro[n][0] + kRaise ||
+                             us[1] > ro[n][1] + kRaise;
+          if (__any_sync(0xFFFFFFFFu, raise)) {
+            const bool out_there = (fabsf(ms[0]) > kFar && ms[0] > -INFINITY) || (fabsf(ms[1]) > kFar && ms[1] > -INFINITY);
+            if (!far && __any_sync(0xFFFFFFFFu, out_there)) {
+              far = true;
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                float x = fmaxf(fmaxf(s[0][n][j], s[0][n][j + 2]), fmaxf(s[1][n][j], s[1][n][j + 2]));
+              for (int k = 0; k < NT; ++k)
 #pragma unroll
-                for (int k = 4; k < 32; k <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, k));
-                float base = s_base[warp][n * 8 + 2 * c + j];
-                __syncwarp();
-                if (x > base + kRaise || (m[n][j] == -INFINITY && x > -INFINITY)) {
-                  m[n][j] += base - x;
-                  ro[n][j] += base - x;
-                  s_base[warp][n * 8 + 2 * c + j] = base = x;
+                for (int j = 0; j < 2; ++j) {
+                  const float base = m[k][j] == -INFINITY ? 0.0f : m[k][j];
+                  s_base[warp][k * 8 + 2 * c + j] = base;
+                  m[k][j] -= base;
+                  ro[k][j] -= base;
                 }
-#pragma unroll
-                for (int k = j; k < 4; k += 2) s[0][n][k] -= base, s[1][n][k] -= base;
-              }
               __syncwarp();
+              rebase(n);   // the blocks after this one come to it in their turn
+              largest(n, us, ms);
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const float xa = fmaxf(s[0][n][j], s[0][n][j + 2]), xb = fmaxf(s[1][n][j], s[1][n][j + 2]);
-              us[j] = fmaxf(xa + vfa, xb + vfb);
-              us[j] = fmaxf(us[j], __shfl_xor_sync(0xFFFFFFFFu, us[j], 4));
-              us[j] = fmaxf(us[j], __shfl_xor_sync(0xFFFFFFFFu, us[j], 8));
-              us[j] = fmaxf(us[j], __shfl_xor_sync(0xFFFFFFFFu, us[j], 16));
-              ms[j] = fmaxf(xa, xb);
-            }
-            if (va == vb) {
-              ms[0] = us[0] - vfa;
-              ms[1] = us[1] - vfa;
-            } else {
+              if (ms[j] > m[n][j] + kRaise) {
+                l[n][j] *= ex2(m[n][j] - ms[j]);
+                m[n][j] = ms[j];
+              }
+              if (us[j] > ro[n][j] + kRaise) {
+                const float f = ex2(ro[n][j] - us[j]);
+                ro[n][j] = us[j];
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                ms[j] = fmaxf(ms[j], __shfl_xor_sync(0xFFFFFFFFu, ms[j], 4));
-                ms[j] = fmaxf(ms[j], __shfl_xor_sync(0xFFFFFFFFu, ms[j], 8));
-                ms[j] = fmaxf(ms[j], __shfl_xor_sync(0xFFFFFFFFu, ms[j], 16));
+                for (int t = 0; t < MT; ++t) o[t][n][j] *= f, o[t][n][j + 2] *= f;
               }
             }
-            const bool raise = ms[0] > m[n][0] + kRaise || ms[1] > m[n][1] + kRaise || us[0] > ro[n][0] + kRaise ||
-                               us[1] > ro[n][1] + kRaise;
-            if (__any_sync(0xFFFFFFFFu, raise)) {
-              const bool out_there = (fabsf(ms[0]) > kFar && ms[0] > -INFINITY) || (fabsf(ms[1]) > kFar && ms[1] > -INFINITY);
-              if (!far && __any_sync(0xFFFFFFFFu, out_there)) {   // once more, relative to bases
-                far = true;
-#pragma unroll
-                for (int k = 0; k < NT; ++k)
-#pragma unroll
-                  for (int j = 0; j < 2; ++j) {
-                    const float base = m[k][j] == -INFINITY ? 0.0f : m[k][j];
-                    s_base[warp][k * 8 + 2 * c + j] = base;
-                    m[k][j] -= base;
-                    ro[k][j] -= base;
-                  }
-                __syncwarp();
-                continue;
-              }
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                if (ms[j] > m[n][j] + kRaise) {
-                  l[n][j] *= ex2(m[n][j] - ms[j]);
-                  m[n][j] = ms[j];
-                }
-                if (us[j] > ro[n][j] + kRaise) {
-                  const float f = ex2(ro[n][j] - us[j]);
-                  ro[n][j] = us[j];
-#pragma unroll
-                  for (int t = 0; t < MT; ++t) o[t][n][j] *= f, o[t][n][j + 2] *= f;
-                }
-              }
-            }
-            break;
           }
           // probabilities times 2^12 over the chunk's largest
           float pr[2][4];
@@ -969,7 +972,7 @@ __global__ void __launch_bounds__(256) decode_weights_kernel(const DecParams p) 
 // CTAs that can have work, and the workspace's parts. Mirrors DecCfg.
 size_t ws_layout(const moe_kv_cache& c, int n_seq, int n_new, int n_heads, int width, bool weights, int sm_count, DecWs* w) {
   const int rows = n_new * (n_heads / c.n_kv_heads);
-  const DecPlan pl = dec_plan(rows);
+  const DecPlan pl = dec_plan(rows, c.head_dim);
   const int warps = pl.nt == 1 ? 12 : 8, groups = warps / pl.rt;
   w->rows = 8 * pl.nt * pl.rt;
   const size_t pairs = (size_t)n_seq * c.n_kv_heads;
@@ -1005,8 +1008,8 @@ int launch_plan(const DecParams& p, const DecPlan& pl, int n_cta, cudaStream_t s
   if (pl.nt == 1 && pl.rt == 3) return launch_one<D, 1, 3, WT>(p, n_cta, s);
   if (pl.nt == 1 && pl.rt == 4) return launch_one<D, 1, 4, WT>(p, n_cta, s);
   if (pl.nt == 1 && pl.rt == 2) return launch_one<D, 1, 2, WT>(p, n_cta, s);
-  if (pl.nt == 1) return launch_one<D, 1, 1, WT>(p, n_cta, s);
-  if (pl.nt == 3) return launch_one<D, 3, 2, WT>(p, n_cta, s);
+  if (pl.nt == 1 && pl.rt == 1) return launch_one<D, 1, 1, WT>(p, n_cta, s);
+  if (pl.rt != 4) return launch_one<D, D == 128 ? 1 : 3, D == 128 ? 6 : 2, WT>(p, n_cta, s);   // 33 to 48 rows
   return launch_one<D, 2, 4, WT>(p, n_cta, s);
 }
 
@@ -1034,7 +1037,7 @@ int launch_attn_decode(const DecodeArgs& a, const DeviceInfo& di, cudaStream_t s
   p.scores = reinterpret_cast<float*>(base + w.scores);
   p.cap = (int64_t)a.width * a.c.page_size;
   p.log2_page = a.c.page_size == 16 ? 4 : a.c.page_size == 32 ? 5 : a.c.page_size == 64 ? 6 : 7;
-  const DecPlan pl = dec_plan(p.rows);
+  const DecPlan pl = dec_plan(p.rows, a.c.head_dim);
   if (a.c.head_dim == 128) return wt ? launch_plan<128, true>(p, pl, w.n_cta, s) : launch_plan<128, false>(p, pl, w.n_cta, s);
   return wt ? launch_plan<64, true>(p, pl, w.n_cta, s) : launch_plan<64, false>(p, pl, w.n_cta, s);
 }
