@@ -395,6 +395,10 @@ int moe_forward_static_scratch(const moe_layer* L, const void* x_dev, int T, voi
  * does not see does not change its result, not even if it is inf or NaN. A
  * query that sees nothing gets a zero output and a log-sum-exp of -inf.
  *
+ * Finite queries, keys and values may be of any size as long as their products
+ * q . k, with and without the scale, are finite in fp32; outputs are finite
+ * wherever the definition's are.
+ *
  * Outputs overlap neither inputs nor one another. */
 
 /* Rows of bf16 heads: element (token t, head h, channel c) is
@@ -421,9 +425,8 @@ typedef struct moe_rows {
  *                cu_q or cu_k leaves [0, total] or falls (such a sequence's
  *                length is taken as what fits); MOE_DEV_TIMEOUT
  * Rows of q outside every sequence are not written. Probabilities enter the
- * second product as bf16; sums and outputs are held in fp32. Outputs are finite
- * wherever the definition's are, for finite values of any size and up to 2^22
- * keys; below 2^-80 they lose bits.
+ * second product as bf16; sums and outputs are held in fp32. (Values near the
+ * largest bf16: up to 2^22 keys. Outputs below 2^-80 lose bits.)
  * Errors: MOE_ERR_INVALID_ARG (null pointer, negative size, stride or address
  * not aligned, scale not finite), MOE_ERR_UNSUPPORTED_SHAPE (head_dim,
  * n_heads % n_kv_heads, n_heads > 65535, n_seq > 65536, more than 2^31 - 65536
