@@ -208,6 +208,32 @@ int moe_route_topk(const float* logits_dev, int T, int E, int k,
                    const float* bias_dev, int bias_row_stride,
                    int32_t* idx_dev, float* w_dev, moe_stream_t stream);
 
+/* Routing by groups of experts, as models with many experts use it. Source:
+ * none of the pages defines it (page "3 ways to speed up MoE inference on NVIDIA
+ * DGX Spark", §2, gives 512 experts and top-8); the formulas, for the logits l of
+ * one token over E experts in n_groups groups of E / n_groups consecutive ones:
+ *   s[e]   = 1 / (1 + exp(-l[e])), or the softmax of l over all E experts
+ *   key[e] = s[e] + bias[e]                 the bias only selects
+ *   group  = its largest key, or (group_best 2) the sum of its two largest
+ *   S      = the k largest keys in the top_groups best groups
+ *   w[j]   = scale * s[S_j] / (sum_i s[S_i] + 1e-20), or scale * s[S_j]
+ * Equal keys go to the lower expert, equal groups to the lower group. Keys are
+ * compared as sums of two fp32 numbers, to about 2^-40 of a score, so that rounding
+ * decides no selection (scores below 2^-100 lose bits); without a bias the logits
+ * rank. A NaN logit has score 0 and ranks behind all others; an infinite one
+ * counts as the largest finite number of its sign.
+ *   logits_dev   fp32 [T][E]
+ *   bias_dev     fp32 [E], NULL for none
+ *   score        moe_score;  renormalise 0 or 1;  scale: finite
+ *   idx_dev      int32 [T][k], slots in descending key order;  w_dev fp32 [T][k]
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED_SHAPE (E > 1024, k > 32, E %
+ * n_groups, n_groups > 32, k > top_groups * E / n_groups, group_best > E /
+ * n_groups, or E / n_groups times the power of two not below n_groups > 1024). */
+typedef enum moe_score { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 } moe_score;
+int moe_route_groups(const float* logits_dev, int T, int E, int k, const float* bias_dev, int score, int n_groups,
+                     int top_groups, int group_best, int renormalise, float scale, int32_t* idx_dev, float* w_dev,
+                     moe_stream_t stream);
+
 /* Group (token, slot) pairs by expert, stable in p = t*k + j (page "MoE-SpeQ
  * ...", §4.2: sort the verify tokens' expert assignments by expert id so each
  * expert runs once over all its tokens).
@@ -479,6 +505,28 @@ int moe_kv_append_fp8(const moe_kv_cache* cache, const moe_rows* k, const moe_ro
                       const int32_t* start_dev, int n_seq, int total, const int32_t* page_table_dev,
                       int table_width, int* dev_status, moe_stream_t stream);
 
+/* moe_kv_append_fp8 with the position rotation on the way. Each of the first
+ * rot_dim channels of a key is turned before it is quantised, from fp32; queries
+ * are turned beside it. The pair j (channels j and j + rot_dim / 2, or interleaved
+ * 2j and 2j + 1) of a token at position p becomes
+ *   (a cos t - b sin t, b cos t + a sin t),  t = p * inv_freq[j]
+ * The angle is reduced exactly, so positions may be as far as an int reaches.
+ *   inv_freq_dev    fp32 [rot_dim / 2]
+ *   rot_dim         16, 32, .. head_dim (a multiple of 16)
+ *   rope_start_dev  int32 [n_seq]: position that a sequence's first new token is
+ *                   turned by, where it is not start (after an eviction the cache
+ *                   holds fewer positions than the sequence had); NULL: start_dev
+ *   q               [total][n_heads][head_dim], NULL for none
+ *   q_out_dev       bf16 [total][n_heads][head_dim] (contiguous, 16-B aligned);
+ *                   rows outside every sequence are not written
+ * Other arguments, status and errors as moe_kv_append_fp8 (a turned key beyond
+ * fp32 counts as infinite); MOE_ERR_UNSUPPORTED_SHAPE also for rot_dim. */
+int moe_kv_append_rope_fp8(const moe_kv_cache* cache, const moe_rows* k, const moe_rows* v, const int32_t* cu_dev,
+                           const int32_t* start_dev, int n_seq, int total, const int32_t* page_table_dev,
+                           int table_width, const float* inv_freq_dev, int rot_dim, int interleaved,
+                           const int32_t* rope_start_dev, const moe_rows* q, int n_heads, void* q_out_dev,
+                           int* dev_status, moe_stream_t stream);
+
 /* Attention of the last n_new tokens of each sequence over the cache, which
  * holds those tokens' own keys and values already (moe_kv_append_fp8): n_new =
  * 1 for plain decoding, up to 8 for the verification of drafted tokens.
@@ -517,6 +565,35 @@ int moe_attn_decode_fp8(const moe_kv_cache* cache, const moe_rows* q, int n_head
                         void* out_dev, float* lse_dev, float* weights_dev, int64_t weights_stride,
                         void* workspace_dev, size_t workspace_bytes, int* dev_status, moe_stream_t stream);
 
+/* Attention of a chunk of new tokens of each sequence over the cache, which
+ * holds those tokens' own keys and values already: prompts taken in chunks,
+ * prompts behind a cached prefix, follow-ups. Chunks may have any length, 0 and 1
+ * too (up to 8 equal ones are moe_attn_decode_fp8's).
+ *   q            [total_q][n_heads][head_dim]: sequence b's new tokens are rows
+ *                cu_q[b] .. cu_q[b + 1] - 1 (cu_q_dev int32 [n_seq + 1], as in
+ *                moe_attn_prefill); row r of a sequence with nq of them sees
+ *                positions 0 .. lengths[b] - nq + r
+ *   lengths_dev  int32 [n_seq]: positions in the cache, the new ones included
+ *   out_dev      bf16 [total_q][n_heads][head_dim] (contiguous, 16-B aligned)
+ *   lse_dev      fp32 [total_q][n_heads] (NULL: not returned)
+ *   workspace    >= moe_attn_chunk_workspace_bytes(...) bytes (256-B aligned); its
+ *                contents need no initialisation and carry nothing between calls;
+ *                calls that may overlap in time need one each
+ *   dev_status   device int (may be NULL): MOE_DEV_INDEX_OOB (cu_q as in
+ *                moe_attn_prefill; a length outside [0, table_width * page_size] is
+ *                cut to it; a page outside the cache counts as masked), MOE_DEV_TIMEOUT
+ * Rows of q outside every sequence are not written.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED_SHAPE (the cache's sizes,
+ * n_heads % n_kv_heads, n_heads > 65535, n_seq > 65536, total_q times the heads of
+ * a group > 2^31 - 65536), MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_NO_DEVICE,
+ * MOE_ERR_CUDA. The workspace size is 0 for an unsupported shape or without an
+ * sm_103 device. */
+size_t moe_attn_chunk_workspace_bytes(const moe_kv_cache* cache, int n_heads, int total_q, int n_seq);
+int moe_attn_chunk_fp8(const moe_kv_cache* cache, const moe_rows* q, int n_heads, const int32_t* cu_q_dev, int n_seq,
+                       int total_q, const int32_t* lengths_dev, const int32_t* page_table_dev, int table_width,
+                       float scale, void* out_dev, float* lse_dev, void* workspace_dev, size_t workspace_bytes,
+                       int* dev_status, moe_stream_t stream);
+
 /* Keep the positions with the most accumulated attention weight. For each
  * sequence b and key/value head h with length L = lengths[b]: everything if L
  * <= keep; else the last `recent` positions and, of the others, the keep -
@@ -547,6 +624,34 @@ int moe_kv_evict_fp8(const moe_kv_cache* cache, const int32_t* page_table_dev, i
                      int keep, int recent, const int32_t* dst_table_dev, int dst_width, int32_t* kept_dev,
                      float* kept_weights_dev, int32_t* new_lengths_dev, int* dev_status, moe_stream_t stream);
 
+/* ---- the norms around a block's halves -------------------------------------------
+ *
+ * Source: none of the pages defines them; root-mean-square norms of the output of
+ * one half of a block and of the input of the next, with the gate and the scaled
+ * residual sum between them, in one pass:
+ *   n = a * rsqrt(mean a^2 + eps) * (weight_offset + post_weight)   (n = a without)
+ *   y = x + residual_scale * gate * n
+ *   h = y * rsqrt(mean y^2 + eps) * (weight_offset + pre_weight)
+ * Means over the d channels of a row; h is taken from y before y is rounded.
+ * Sums are fp32 and do not overflow for finite inputs.
+ *   x_dev            [T][d] bf16, or fp32 if x_is_fp32: the residual stream
+ *   a_dev            bf16 [T][d]: the half's output; NULL: only h = norm of x
+ *                    (y_dev, post_weight_dev and gate_dev are NULL then too)
+ *   post_weight_dev  bf16 [d]; NULL: a is not normalised
+ *   gate_dev         bf16, NULL for none; gate_stride 0: one row [d] for all
+ *                    tokens, else [T][d]
+ *   pre_weight_dev   bf16 [d]; NULL: weights of 1, without the offset
+ *   y_dev            [T][d] of x's type; may be x itself (same stride)
+ *   h_dev            bf16 [T][d], NULL: not returned; may be a itself (same stride)
+ * Strides are those of rows, in elements, multiples of 8 and at least d; pointers
+ * 16-B aligned. d is a multiple of 8, at most 32768. T may be 0.
+ * Errors: MOE_ERR_INVALID_ARG (also scales or eps that are not finite, eps < 0),
+ * MOE_ERR_UNSUPPORTED_SHAPE (d), MOE_ERR_NO_DEVICE, MOE_ERR_CUDA. */
+int moe_block_norm(const void* x_dev, int64_t x_stride, int x_is_fp32, const void* a_dev, int64_t a_stride, int T,
+                   int d, const void* post_weight_dev, const void* gate_dev, int64_t gate_stride,
+                   float residual_scale, const void* pre_weight_dev, float eps, float weight_offset, void* y_dev,
+                   int64_t y_stride, void* h_dev, int64_t h_stride, moe_stream_t stream);
+
 /* Comma-separated names of the stages of `path` in launch order (the
  * boundaries moe_forward's stage_events mark); NULL for an unknown path. */
 const char* moe_stage_names(int path);
@@ -562,7 +667,7 @@ int moe_selftest_bounded_wait(const uint32_t* flag_dev, uint32_t want, long long
 /* Static text for a moe_status value. */
 const char* moe_status_string(int status);
 
-/* Library version, e.g. "moe_mxfp4 1.2 sm_103a". */
+/* Library version, e.g. "moe_mxfp4 1.3 sm_103a". */
 const char* moe_version(void);
 
 #ifdef __cplusplus

@@ -25,14 +25,15 @@ __all__ = [
     "moe_route_topk", "moe_sort_workspace_bytes", "moe_sort_by_expert",
     "moe_workspace_bytes", "moe_query_path", "moe_stage_names", "moe_forward", "moe_forward_profiled", "moe_forward_w4a8", "moe_quant_mxfp8", "moe_lmhead_pack_fp8", "moe_lmhead_fp8", "moe_forward_static_scratch", "STATIC_SCRATCH_BYTES", "ATTN_DECODE_COUNTER_BYTES",
     "moe_rows", "moe_kv_cache", "KVCache", "moe_attn_prefill", "moe_kv_append_fp8", "moe_attn_decode_workspace_bytes",
-    "moe_attn_decode_fp8", "moe_kv_evict_fp8", "moe_selftest_bounded_wait", "moe_status_string", "moe_version",
+    "moe_attn_decode_fp8", "moe_kv_evict_fp8", "moe_kv_append_rope_fp8", "moe_attn_chunk_workspace_bytes", "moe_attn_chunk_fp8",
+    "moe_block_norm", "moe_route_groups", "moe_selftest_bounded_wait", "moe_status_string", "moe_version",
 ]
 
 # The in-tree build, and only it: there is no way to point the binding at
 # another library.
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_mxfp4.so")
 # Version string the library must report (moe_version); anything else is refused.
-EXPECTED_VERSION = "moe_mxfp4 1.2 sm_103a"
+EXPECTED_VERSION = "moe_mxfp4 1.3 sm_103a"
 
 MOE_LAYOUT_TILE16 = 1
 MOE_LAYOUT_TILE16_GATEUP = 2
@@ -110,6 +111,12 @@ def _load():
         "moe_attn_decode_workspace_bytes": (sz, [cache, i32, i32, i32, i32, i32]),
         "moe_attn_decode_fp8": (i32, [cache, rows, i32, i32, i32, vp, vp, i32, f32, vp, vp, vp, i64, vp, sz, vp, vp]),
         "moe_kv_evict_fp8": (i32, [cache, vp, i32, vp, i32, vp, i64, i32, i32, vp, i32, vp, vp, vp, vp, vp]),
+        "moe_kv_append_rope_fp8": (i32, [cache, rows, rows, vp, vp, i32, i32, vp, i32, vp, i32, i32, vp, rows, i32, vp, vp,
+                                         vp]),
+        "moe_attn_chunk_workspace_bytes": (sz, [cache, i32, i32, i32]),
+        "moe_attn_chunk_fp8": (i32, [cache, rows, i32, vp, i32, i32, vp, vp, i32, f32, vp, vp, vp, sz, vp, vp]),
+        "moe_block_norm": (i32, [vp, i64, i32, vp, i64, i32, i32, vp, vp, i64, f32, vp, f32, f32, vp, i64, vp, i64, vp]),
+        "moe_route_groups": (i32, [vp, i32, i32, i32, vp, i32, i32, i32, i32, i32, f32, vp, vp, vp]),
         "moe_stage_names": (ctypes.c_char_p, [i32]),
         "moe_selftest_bounded_wait": (i32, [vp, ctypes.c_uint32, ctypes.c_longlong, vp, vp]),
         "moe_status_string": (ctypes.c_char_p, [i32]),
@@ -226,6 +233,38 @@ def moe_route_topk(logits: torch.Tensor, k: int, bias: torch.Tensor | None = Non
     w = _empty((T, k), torch.float32, logits.device, stream) if w is None else w
     _check(lib.moe_route_topk(_p(logits), T, E, k, _p(bias), stride, _p(idx), _p(w), _s(stream)),
            "moe_route_topk")
+    return idx, w
+
+
+_SCORES = {"sigmoid": 0, "softmax": 1}
+
+
+def moe_route_groups(logits: torch.Tensor, k: int, bias: torch.Tensor | None = None, score: str = "sigmoid",
+                     n_groups: int = 1, top_groups: int = 1, group_best: int = 2, renormalise: bool = True,
+                     scale: float = 1.0, idx: torch.Tensor | None = None, w: torch.Tensor | None = None, stream=None):
+    """fp32 logits [T, E] -> (idx int32 [T, k], w fp32 [T, k]): the k best experts in the top_groups best of n_groups
+    groups of consecutive experts.
+
+    score "sigmoid" or "softmax" (over all experts); bias fp32 [E] is added for
+    the selection only. A group counts by its best key, or (group_best 2) by the
+    sum of its two best. The scores of the selected are the weights,
+    renormalised to a sum of 1 unless told otherwise, times scale.
+    """
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    dev = torch.cuda.current_device()
+    lp = _ptr(logits, _F32, "logits", dev)
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [T, E], got {list(logits.shape)}")
+    T, E = logits.shape
+    shape = (T, k)
+    if idx is None:
+        idx = _empty(shape, _I32, logits.device, stream)
+    if w is None:
+        w = _empty(shape, _F32, logits.device, stream)
+    _check(lib.moe_route_groups(lp, T, E, k, _opt(bias, _F32, "bias", dev, (E,)), _SCORES[score], n_groups, top_groups,
+                                group_best, 1 if renormalise else 0, float(scale), _ptr(idx, _I32, "idx", dev, shape),
+                                _ptr(w, _F32, "w", dev, shape), _stream(stream, dev)), "moe_route_groups")
     return idx, w
 
 
@@ -622,6 +661,90 @@ def moe_kv_append_fp8(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu_seqle
                                  width, _status_ptr(dev_status, dev), _stream(stream, dev)), "moe_kv_append_fp8")
 
 
+def moe_kv_append_rope_fp8(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                           start: torch.Tensor, page_table: torch.Tensor, inv_freq: torch.Tensor,
+                           q: torch.Tensor | None = None, interleaved: bool = False,
+                           rope_start: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+                           dev_status: torch.Tensor | None = None, stream=None):
+    """moe_kv_append_fp8 with the keys' first 2 * len(inv_freq) channels turned by their positions, and q's, if given.
+
+    inv_freq fp32 [r / 2], r a multiple of 16 up to D: pair j of a token at
+    position p is turned by p * inv_freq[j]. Pairs are channels j and j + r / 2, or
+    neighbours if interleaved. rope_start int32 [n_seq]: position of each
+    sequence's first new token, where it is not `start`. q bf16 [total, n_heads, D]
+    -> returns q_out like q (contiguous; rows outside every sequence are not
+    written), else None.
+    """
+    dev, H, D = _cache_device(cache), cache.n_kv_heads, cache.head_dim
+    kr, vr = _rows(k, "k", dev, H, D), _rows(v, "v", dev, H, D)
+    total = k.shape[0]
+    if v.shape[0] != total:
+        raise ValueError("k and v must have the same number of rows")
+    startp = _ptr(start, _I32, "start", dev)
+    n_seq = start.numel()
+    tablep, width = _table(page_table, "page_table", dev, n_seq)
+    freqp = _ptr(inv_freq, _F32, "inv_freq", dev)
+    if inv_freq.dim() != 1:
+        raise ValueError(f"inv_freq must be [r / 2], got {list(inv_freq.shape)}")
+    qr, n_heads, qp = None, 0, None
+    if q is not None:
+        if not isinstance(q, _Tensor) or q.dim() != 3:
+            raise ValueError("q must be a tensor [total, n_heads, head_dim]")
+        n_heads = q.shape[1]
+        if q.shape[0] != total:
+            raise ValueError("q and k must have the same number of rows")
+        qr = ctypes.byref(_rows(q, "q", dev, n_heads, D))
+        if q_out is None:
+            q_out = _empty(q.shape, _BF16, q.device, stream)
+        qp = _ptr(q_out, _BF16, "q_out", dev, q.shape)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    _check(lib.moe_kv_append_rope_fp8(cache._ref, ctypes.byref(kr), ctypes.byref(vr),
+                                      _ptr(cu_seqlens, _I32, "cu_seqlens", dev, (n_seq + 1,)), startp, n_seq, total,
+                                      tablep, width, freqp, 2 * inv_freq.numel(), 1 if interleaved else 0,
+                                      _opt(rope_start, _I32, "rope_start", dev, (n_seq,)), qr, n_heads, qp,
+                                      _status_ptr(dev_status, dev), _stream(stream, dev)), "moe_kv_append_rope_fp8")
+    return q_out
+
+
+def moe_attn_chunk_workspace_bytes(cache: KVCache, n_heads: int, total_q: int, n_seq: int) -> int:
+    """Bytes of the workspace of moe_attn_chunk_fp8; 0 for an unsupported shape."""
+    return int(lib.moe_attn_chunk_workspace_bytes(cache._ref, n_heads, total_q, n_seq))
+
+
+def moe_attn_chunk_fp8(cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor, lengths: torch.Tensor,
+                       page_table: torch.Tensor, scale: float | None = None, out: torch.Tensor | None = None,
+                       lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                       dev_status: torch.Tensor | None = None, stream=None):
+    """Attention of a chunk of new tokens of every sequence over the cache: bf16 q [total, n_heads, D] -> out like q.
+
+    cu_q int32 [n_seq + 1]: first row of every sequence's chunk, and the total.
+    lengths int32 [n_seq] counts the positions in the cache, the chunk's own
+    included; its last token sees all of them. lse fp32 [total, n_heads] is written
+    if given. workspace: uint8 device tensor of moe_attn_chunk_workspace_bytes(...)
+    bytes, allocated when omitted.
+    """
+    dev = _cache_device(cache)
+    if not isinstance(q, _Tensor) or q.dim() != 3:
+        raise ValueError("q must be a tensor [tokens, n_heads, head_dim]")
+    total, n_heads, d = shape = q.shape
+    qr = _rows(q, "q", dev, n_heads, cache.head_dim)
+    lengthsp = _ptr(lengths, _I32, "lengths", dev)
+    n_seq = lengths.numel()
+    tablep, width = _table(page_table, "page_table", dev, n_seq)
+    if out is None:
+        out = _empty(shape, _BF16, q.device, stream)
+    if workspace is None:
+        n = moe_attn_chunk_workspace_bytes(cache, n_heads, total, n_seq)
+        workspace = _empty(max(n, 256), _U8, q.device, stream)
+    _check(lib.moe_attn_chunk_fp8(cache._ref, ctypes.byref(qr), n_heads, _ptr(cu_q, _I32, "cu_q", dev, (n_seq + 1,)),
+                                  n_seq, total, lengthsp, tablep, width, d ** -0.5 if scale is None else float(scale),
+                                  _ptr(out, _BF16, "out", dev, shape), _opt(lse, _F32, "lse", dev, (total, n_heads)),
+                                  _ptr(workspace, _U8, "workspace", dev), workspace.numel(),
+                                  _status_ptr(dev_status, dev), _stream(stream, dev)), "moe_attn_chunk_fp8")
+    return out
+
+
 def moe_attn_decode_workspace_bytes(cache: KVCache, n_seq: int, n_new: int, n_heads: int, table_width: int,
                                     with_weights: bool = False) -> int:
     """Bytes of the workspace of moe_attn_decode_fp8; 0 for an unsupported shape."""
@@ -708,3 +831,71 @@ def moe_kv_evict_fp8(cache: KVCache, page_table: torch.Tensor, lengths: torch.Te
                                 _ptr(new_lengths, _I32, "new_lengths", dev, (n_seq,)), _status_ptr(dev_status, dev),
                                 _stream(stream, dev)), "moe_kv_evict_fp8")
     return kept, kept_weights, new_lengths
+
+
+# ---- the norms around a block's halves -----------------------------------------------
+
+
+def _mat(t, dtype, name, dev, shape):
+    """Address and row stride of a [T, d] tensor of that type whose rows are contiguous."""
+    if not (isinstance(t, _Tensor) and t.is_cuda):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    rs, es = t.stride()
+    if es != 1 and shape[1] > 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return t.data_ptr(), rs if shape[0] > 1 else shape[1]
+
+
+def moe_block_norm(x: torch.Tensor, a: torch.Tensor | None = None, post_weight: torch.Tensor | None = None,
+                   gate: torch.Tensor | None = None, residual_scale: float = 1.0,
+                   pre_weight: torch.Tensor | None = None, eps: float = 1e-6, weight_offset: float = 0.0,
+                   y: torch.Tensor | None = None, h: torch.Tensor | None = None, stream=None):
+    """The residual step between two halves of a block and the norms on both sides of it; returns (y, h).
+
+        y = x + residual_scale * gate * norm(a) * (weight_offset + post_weight)
+        h = norm(y) * (weight_offset + pre_weight)
+
+    x [T, d] is the residual stream, bf16 or fp32; a bf16 [T, d] the half's output;
+    norm(z) = z / sqrt(mean z^2 + eps) over a row. Without post_weight a is not
+    normalised, without pre_weight h has weights of 1; weights are bf16 [d]. gate:
+    bf16 [d] or [T, d]. Without a there is only h = norm of x (y is None). y has x's
+    type and may be x itself; h is bf16 and may be a itself. With a but neither
+    pre_weight nor h there is only y (h is None). Rows may have strides that are
+    multiples of 8 elements.
+    """
+    if not isinstance(x, _Tensor) or x.dim() != 2:
+        raise ValueError("x must be a tensor [T, d]")
+    dev = torch.cuda.current_device()
+    if x.dtype not in (_BF16, _F32):
+        raise TypeError(f"x must be {_BF16} or {_F32}, got {x.dtype}")
+    T, d = shape = x.shape
+    xp, xs = _mat(x, x.dtype, "x", dev, shape)
+    ap = gp = yp = hp = None
+    as_ = gs = ys = hs = 0
+    if a is not None:
+        ap, as_ = _mat(a, _BF16, "a", dev, shape)
+        if y is None:
+            y = _empty(shape, x.dtype, x.device, stream)
+        yp, ys = _mat(y, x.dtype, "y", dev, shape)
+    elif y is not None:
+        raise ValueError("y needs a")
+    if gate is not None:
+        if isinstance(gate, _Tensor) and gate.dim() == 1:
+            gp = _ptr(gate, _BF16, "gate", dev, (d,))
+        else:
+            gp, gs = _mat(gate, _BF16, "gate", dev, shape)
+    if h is None and (a is None or pre_weight is not None):
+        h = _empty(shape, _BF16, x.device, stream)
+    if h is not None:
+        hp, hs = _mat(h, _BF16, "h", dev, shape)
+    _check(lib.moe_block_norm(xp, xs, 1 if x.dtype is _F32 else 0, ap, as_, T, d,
+                              _opt(post_weight, _BF16, "post_weight", dev, (d,)), gp, gs, float(residual_scale),
+                              _opt(pre_weight, _BF16, "pre_weight", dev, (d,)), float(eps), float(weight_offset), yp, ys,
+                              hp, hs, _stream(stream, dev)), "moe_block_norm")
+    return y, h

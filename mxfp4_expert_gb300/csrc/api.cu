@@ -572,7 +572,7 @@ extern "C" const char* moe_status_string(int status) {
   }
 }
 
-extern "C" const char* moe_version(void) { return "moe_mxfp4 1.2 sm_103a"; }
+extern "C" const char* moe_version(void) { return "moe_mxfp4 1.3 sm_103a"; }
 
 namespace moe {
 namespace {

@@ -35,6 +35,33 @@ struct AppendArgs {
 };
 int launch_kv_append(const AppendArgs& a, cudaStream_t s);
 
+struct RopeArgs {
+  AppendArgs ap;
+  const float* inv_freq;         // [rot / 2]
+  const int32_t* rope_start;     // [n_seq]: position that a sequence's first new token is rotated by
+  const __nv_bfloat16* q;        // or null
+  int64_t q_ts, q_hs;
+  __nv_bfloat16* q_out;          // [total][n_heads][D]
+  int n_heads, rot, interleaved;
+};
+int launch_kv_append_rope(const RopeArgs& a, cudaStream_t s);
+
+struct ChunkArgs {
+  moe_kv_cache c;
+  const __nv_bfloat16* q;
+  int64_t q_ts, q_hs;
+  int n_heads, n_seq, total_q;
+  const int32_t *cu_q, *lengths, *table;
+  int width;
+  float scale;
+  __nv_bfloat16* out;            // [total_q][n_heads][D]
+  float* lse;                    // [total_q][n_heads] or null
+  void* ws;
+  int* status;
+};
+size_t attn_chunk_ws_bytes(const moe_kv_cache& c, int n_heads, int total_q, int n_seq, const DeviceInfo& di);
+int launch_attn_chunk(const ChunkArgs& a, const DeviceInfo& di, cudaStream_t s);
+
 struct DecodeArgs {
   moe_kv_cache c;
   const __nv_bfloat16* q;

@@ -100,35 +100,133 @@ extern "C" int moe_attn_prefill(const moe_rows* q, const moe_rows* k, const moe_
   return launch_attn_prefill(a, di, (cudaStream_t)stream);
 }
 
-extern "C" int moe_kv_append_fp8(const moe_kv_cache* cache, const moe_rows* k, const moe_rows* v,
-                                 const int32_t* cu_dev, const int32_t* start_dev, int n_seq, int total,
-                                 const int32_t* page_table_dev, int table_width, int* dev_status,
-                                 moe_stream_t stream) {
+// Checks that both append calls share; fills *a. *empty: nothing to do.
+static int append_args(const moe_kv_cache* cache, const moe_rows* k, const moe_rows* v, const int32_t* cu_dev,
+                       const int32_t* start_dev, int n_seq, int total, const int32_t* page_table_dev, int table_width,
+                       int* dev_status, AppendArgs* a, bool* empty) {
   int st;
   if ((st = check_cache(cache, true))) return st;
   MOE_CHECK_ARG(n_seq >= 0 && total >= 0 && table_ok(table_width, cache->page_size), MOE_ERR_INVALID_ARG);
   MOE_CHECK_ARG(n_seq <= 65536 && total <= kMaxRows, MOE_ERR_UNSUPPORTED_SHAPE);
-  if (n_seq == 0 || total == 0) return MOE_OK;
+  if ((*empty = n_seq == 0 || total == 0)) return MOE_OK;
   if ((st = check_rows(k)) || (st = check_rows(v))) return st;
   MOE_CHECK_ARG(cu_dev && start_dev && page_table_dev, MOE_ERR_INVALID_ARG);
+  a->c = *cache;
+  a->k = static_cast<const __nv_bfloat16*>(k->data);
+  a->v = static_cast<const __nv_bfloat16*>(v->data);
+  a->k_ts = k->token_stride;
+  a->k_hs = k->head_stride;
+  a->v_ts = v->token_stride;
+  a->v_hs = v->head_stride;
+  a->cu = cu_dev;
+  a->start = start_dev;
+  a->table = page_table_dev;
+  a->n_seq = n_seq;
+  a->total = total;
+  a->width = table_width;
+  a->status = dev_status;
+  return MOE_OK;
+}
+
+extern "C" int moe_kv_append_fp8(const moe_kv_cache* cache, const moe_rows* k, const moe_rows* v,
+                                 const int32_t* cu_dev, const int32_t* start_dev, int n_seq, int total,
+                                 const int32_t* page_table_dev, int table_width, int* dev_status,
+                                 moe_stream_t stream) {
+  AppendArgs a{};
+  bool empty = false;
+  int st = append_args(cache, k, v, cu_dev, start_dev, n_seq, total, page_table_dev, table_width, dev_status, &a, &empty);
+  if (st != MOE_OK || empty) return st;
   DeviceInfo di;
   if ((st = current_device(&di))) return st;
-  AppendArgs a{};
-  a.c = *cache;
-  a.k = static_cast<const __nv_bfloat16*>(k->data);
-  a.v = static_cast<const __nv_bfloat16*>(v->data);
-  a.k_ts = k->token_stride;
-  a.k_hs = k->head_stride;
-  a.v_ts = v->token_stride;
-  a.v_hs = v->head_stride;
-  a.cu = cu_dev;
-  a.start = start_dev;
-  a.table = page_table_dev;
-  a.n_seq = n_seq;
-  a.total = total;
-  a.width = table_width;
-  a.status = dev_status;
   return launch_kv_append(a, (cudaStream_t)stream);
+}
+
+extern "C" int moe_kv_append_rope_fp8(const moe_kv_cache* cache, const moe_rows* k, const moe_rows* v,
+                                      const int32_t* cu_dev, const int32_t* start_dev, int n_seq, int total,
+                                      const int32_t* page_table_dev, int table_width, const float* inv_freq_dev,
+                                      int rot_dim, int interleaved, const int32_t* rope_start_dev, const moe_rows* q,
+                                      int n_heads, void* q_out_dev, int* dev_status, moe_stream_t stream) {
+  MOE_CHECK_ARG(interleaved == 0 || interleaved == 1, MOE_ERR_INVALID_ARG);
+  RopeArgs a{};
+  bool empty = false;
+  int st = append_args(cache, k, v, cu_dev, start_dev, n_seq, total, page_table_dev, table_width, dev_status, &a.ap,
+                       &empty);
+  if (st != MOE_OK) return st;
+  MOE_CHECK_ARG(rot_dim >= 16 && rot_dim % 16 == 0 && rot_dim <= cache->head_dim, MOE_ERR_UNSUPPORTED_SHAPE);
+  MOE_CHECK_ARG(!q || (n_heads >= 1 && n_heads <= 65535), MOE_ERR_UNSUPPORTED_SHAPE);
+  if (empty) return MOE_OK;
+  MOE_CHECK_ARG(inv_freq_dev, MOE_ERR_INVALID_ARG);
+  if (q) {
+    if ((st = check_rows(q))) return st;
+    MOE_CHECK_ARG(q_out_dev && aligned(q_out_dev, 16), MOE_ERR_INVALID_ARG);
+    a.q = static_cast<const __nv_bfloat16*>(q->data);
+    a.q_ts = q->token_stride;
+    a.q_hs = q->head_stride;
+    a.q_out = static_cast<__nv_bfloat16*>(q_out_dev);
+    a.n_heads = n_heads;
+  }
+  DeviceInfo di;
+  if ((st = current_device(&di))) return st;
+  a.inv_freq = inv_freq_dev;
+  a.rope_start = rope_start_dev ? rope_start_dev : start_dev;
+  a.rot = rot_dim;
+  a.interleaved = interleaved;
+  return launch_kv_append_rope(a, (cudaStream_t)stream);
+}
+
+static int check_chunk_shape(const moe_kv_cache* c, int n_heads, int n_seq, int total_q) {
+  const int st = check_cache(c, false);
+  if (st != MOE_OK) return st;
+  MOE_CHECK_ARG(n_heads >= 1 && n_seq >= 0 && total_q >= 0, MOE_ERR_INVALID_ARG);
+  // the rows of a sequence and key/value head, tokens times heads of a group, are counted in an int too
+  MOE_CHECK_ARG(n_heads % c->n_kv_heads == 0 && n_heads <= 65535 && n_seq <= 65536 && total_q <= kMaxRows &&
+                    (int64_t)total_q * (n_heads / c->n_kv_heads) <= kMaxRows,
+                MOE_ERR_UNSUPPORTED_SHAPE);
+  return MOE_OK;
+}
+
+extern "C" size_t moe_attn_chunk_workspace_bytes(const moe_kv_cache* cache, int n_heads, int total_q, int n_seq) {
+  if (check_chunk_shape(cache, n_heads, n_seq, total_q) != MOE_OK) return 0;
+  DeviceInfo di;
+  if (current_device(&di) != MOE_OK) return 0;
+  return attn_chunk_ws_bytes(*cache, n_heads, total_q, n_seq, di);
+}
+
+extern "C" int moe_attn_chunk_fp8(const moe_kv_cache* cache, const moe_rows* q, int n_heads, const int32_t* cu_q_dev,
+                                  int n_seq, int total_q, const int32_t* lengths_dev, const int32_t* page_table_dev,
+                                  int table_width, float scale, void* out_dev, float* lse_dev, void* workspace_dev,
+                                  size_t workspace_bytes, int* dev_status, moe_stream_t stream) {
+  int st;
+  if ((st = check_chunk_shape(cache, n_heads, n_seq, total_q))) return st;
+  if ((st = check_cache(cache, true))) return st;
+  MOE_CHECK_ARG(table_ok(table_width, cache->page_size) && isfinite(scale), MOE_ERR_INVALID_ARG);
+  if (n_seq == 0 || total_q == 0) return MOE_OK;
+  if ((st = check_rows(q))) return st;
+  MOE_CHECK_ARG(cu_q_dev && lengths_dev && (page_table_dev || table_width == 0) && out_dev && aligned(out_dev, 16),
+                MOE_ERR_INVALID_ARG);
+  MOE_CHECK_ARG(workspace_dev && aligned(workspace_dev, 256), MOE_ERR_INVALID_ARG);
+  DeviceInfo di;
+  if ((st = current_device(&di))) return st;
+  MOE_CHECK_ARG(workspace_bytes >= attn_chunk_ws_bytes(*cache, n_heads, total_q, n_seq, di),
+                MOE_ERR_WORKSPACE_TOO_SMALL);
+  ChunkArgs a{};
+  a.c = *cache;
+  a.q = static_cast<const __nv_bfloat16*>(q->data);
+  a.q_ts = q->token_stride;
+  a.q_hs = q->head_stride;
+  a.n_heads = n_heads;
+  a.n_seq = n_seq;
+  a.total_q = total_q;
+  a.cu_q = cu_q_dev;
+  a.lengths = lengths_dev;
+  a.table = page_table_dev;
+  a.width = table_width;
+  a.scale = scale;
+  a.out = static_cast<__nv_bfloat16*>(out_dev);
+  a.lse = lse_dev;
+  a.ws = workspace_dev;
+  a.status = dev_status;
+  return launch_attn_chunk(a, di, (cudaStream_t)stream);
 }
 
 extern "C" size_t moe_attn_decode_workspace_bytes(const moe_kv_cache* cache, int n_seq, int n_new, int n_heads,
