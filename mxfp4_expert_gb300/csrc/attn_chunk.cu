@@ -1,73 +1,1051 @@
-// Attention of chunks of new tokens over the 8-bit paged cache: one warp per
-// (token, head), one pass over the positions with the running maximum and sum.
+// Attention of chunks of new tokens over the 8-bit paged cache, on the
+// 5th-generation tensor cores.
+//
+// out_i = sum_j softmax_j(scale q_i . k_j) v_j over the positions j that token i
+// sees, 4 head_dim flops a visible pair and head. Keys and values come as E4M3 codes
+// with a power of two per page and head; both products run on tcgen05 in f16, of
+// which every code is a number. The scales stay outside: a key page's is a factor
+// of its scores, a value page's of its probabilities.
+//
+// Work items. The rows of a sequence and key/value head are its new tokens times
+// the heads of the group (row r: token r / G, head r % G); 256 of them, two query
+// tiles of 128, are an item and share every key and value tile that is converted.
+// Costs, in closed form, lay all items end to end; CTA c of N takes the stretch from
+// c / N to (c + 1) / N of the whole, cut at key tiles: work is even whatever the
+// lengths are, and few rows over many positions are shared out. An item that is cut
+// leaves partial results in the workspace, which a second kernel joins.
+//
+// Tensor memory and the order of the products are the prompt kernel's: scores S0,
+// S1 (128 fp32 columns each, two halves of 64 keys), outputs O0, O1; probabilities go
+// over scores as the A operand of the second product.
+//
+// Warp roles (16 warps, four of each kind, registers dealt by setmaxnreg):
+//   producer (one warp)    items; page-table entries, scale bytes; raw pages by
+//                          1-D bulk copies into a ring
+//   MMA 0, 1 (a warp each) of its query tile: S = Q K^T and O += P V
+//   converters (4 warps)   codes to f16, two an instruction, into the operand
+//                          ring; values that nobody sees to zero
+//   softmax 0, 1 (4 warps each, one thread per row): Q to f16 (a power of two per
+//                          row puts its largest in [2^14, 2^15)), then scores to
+//                          probabilities, and O / sum at the end
+//
+// Numerics. A row has two references: its scores' (a score it has had, raised when
+// passed by 2^16), which the sum is relative to, and its products' p 2^(value scale)
+// (an integer power of two above the scores', raised when passed by 2^7), which O is
+// relative to: probabilities are f16, 2^8 above that reference, so at most 2^15, of
+// 11 bits down to 2^-22 and none below 2^-33 of it. Differences of scores beyond
+// 2^17 are taken before they are scaled. Sums and outputs are fp32.
+//
+// Masked places must not count, whatever they hold, but 0 * NaN is NaN in the
+// second product: in a tile that some row of the item does not see whole the
+// converters put 0 for NaN; the rows that see it get it back at the end.
+#include <math.h>
+
 #include "attn.h"
+#include "attn_tc.cuh"
+#include "f32x2.cuh"
 #include "fp8kv.cuh"
+#include "umma.cuh"
 
 namespace moe {
 namespace {
 
-constexpr float kLn2f = 0.6931471805599453f, kLog2ef = 1.4426950408889634f;
+constexpr int kQT = 128, kKT = 128;        // rows per query tile, keys per tile
+constexpr int kThreads = 512;
+constexpr int kWProd = 0, kWMma0 = 1, kWMma1 = 2, kWConv = 4, kWSoft = 8;
+// registers: 128 a thread at launch; 64 + 96 + 2 * 176 = 4 * 128
+constexpr int kRegsCtl = 64, kRegsConv = 96, kRegsSoft = 176;
+constexpr uint32_t kBoxBytes = 128 * 128;  // 128 rows of 64 f16 channels
+constexpr int kSlots = 16;                 // key tiles whose scale bytes are kept
+constexpr float kRaiseSum = 16.0f, kRaiseOut = 7.0f, kPBias = 8.0f;   // log2; see above
+constexpr float kFar = 131072.0f;
+constexpr float kLn2f = 0.6931471805599453f;
+// Work of an item beside its keys, in keys, and the least work of a CTA, in keys of
+// a whole group: cuts of one item are then more than a tile apart (an item of n >= 2
+// tiles costs at most G (128 n + 128 + 1) + 256, so a tile at most 193 G + 128).
+constexpr int kItemKeys = 128, kCtaKeys = 448;
 
 template <int D>
-__global__ void __launch_bounds__(128) chunk_simple_kernel(const ChunkArgs a) {
-  constexpr int C = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int h = blockIdx.y, G = a.n_heads / a.c.n_kv_heads, hk = h / G, P = a.c.page_size;
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (t >= a.total_q) return;
-  // the token's sequence
-  int b = -1, c0 = 0, c1 = 0;
-  bool bad = false;
-  if (t == 0 && h == 0)
-    for (int i = lane; i < a.n_seq; i += 32) packed_range(a.cu_q, i, a.total_q, &c0, &c1, &bad);
-  if (bad && a.status) atomicOr(a.status, MOE_DEV_INDEX_OOB);
-  bad = false;
-  for (int i = 0; i < a.n_seq && b < 0; ++i) {
-    packed_range(a.cu_q, i, a.total_q, &c0, &c1, &bad);
-    if (t >= c0 && t < c1) b = i;
-  }
-  if (b < 0) return;
-  const int cap = a.width * P, L0 = __ldg(a.lengths + b), L = min(max(L0, 0), cap);
-  if (a.status && lane == 0 && (bad || L != L0)) atomicOr(a.status, MOE_DEV_INDEX_OOB);
-  const int vis = min(max(L - (c1 - c0) + (t - c0) + 1, 0), L);
-  float q[C], o[C], m = -INFINITY, l = 0.0f;
-  for (int i = 0; i < C; ++i) {
-    q[i] = __bfloat162float(a.q[(int64_t)t * a.q_ts + (int64_t)h * a.q_hs + lane * C + i]);
-    o[i] = 0.0f;
-  }
-  for (int p = 0; p < vis; ++p) {
-    const int page = __ldg(a.table + (size_t)b * a.width + p / P);
-    if (page < 0 || page >= a.c.n_pages) {
-      if (a.status && lane == 0) atomicOr(a.status, MOE_DEV_INDEX_OOB);
-      continue;
-    }
-    const size_t ph = (size_t)page * a.c.n_kv_heads + hk;
-    const size_t at = (ph * P + p % P) * D + lane * C;
-    const uint8_t *k = static_cast<const uint8_t*>(a.c.k_codes) + at, *v = static_cast<const uint8_t*>(a.c.v_codes) + at;
-    float s = 0.0f;
-    for (int i = 0; i < C; ++i) s += q[i] * e4m3_to_f32_hw(k[i]);
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-    s = s * exp2i(int(a.c.k_scales[ph]) - 127) * (a.scale * kLog2ef);
-    const float mn = fmaxf(m, s), f = exp2f(m - mn), e = exp2f(s - mn);
-    const float vs = exp2i(int(a.c.v_scales[ph]) - 127);
-    l = l * f + e;
-    for (int i = 0; i < C; ++i) o[i] = o[i] * f + e * (e4m3_to_f32_hw(v[i]) * vs);
-    m = mn;
-  }
-  const int64_t r = (int64_t)t * a.n_heads + h;
-  for (int i = 0; i < C; ++i) a.out[r * D + lane * C + i] = __float2bfloat16(l == 0.0f ? 0.0f : o[i] / l);
-  if (a.lse && lane == 0) a.lse[r] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2f;
+struct Plan {
+  static constexpr int kBoxes = D / 64;
+  static constexpr uint32_t kTile = kBoxes * kBoxBytes;      // f16 operand tile
+  static constexpr uint32_t kRaw = 128 * D;                  // codes of a tile
+  static constexpr int kStages = D == 128 ? 4 : 8, kRaws = D == 128 ? 2 : 6;
+  static constexpr uint32_t kQ = 0, kRing = 2 * kTile, kRawRing = kRing + kStages * kTile;
+  static constexpr uint32_t kInfo = kRawRing + kRaws * kRaw;
+  static constexpr uint32_t kBars = kInfo + kSlots * 32;
+  static constexpr int kNBars = 2 * kRaws + 2 * kStages + 2 + 4 + 2 * 6 + 2 + 4 + 2 * kSlots;
+  static constexpr uint32_t kItems = kBars + kNBars * 8;
+  static constexpr uint32_t kTotal = kItems + 2 * 96 + 16 + 1024;   // + alignment slack
+};
+static_assert(Plan<128>::kTotal <= 232448 && Plan<64>::kTotal <= 232448, "shared memory");
+
+struct Item {
+  int n;                 // key tiles of this part, -1: no more items
+  int t0;                // its first key tile
+  int nkt[2];            // of them, those that each query tile sees
+  int rows[2];           // rows of each query tile, 0: none
+  int r0;                // first row
+  int b, hk, q0;         // sequence, key/value head, sequence's first token
+  int off, nk, vmin;     // nk - nq, positions, fewest positions a row sees
+  int slot;              // partial result's place, -1: the item is whole
+};
+static_assert(sizeof(Item) <= 96, "item");
+
+// Scale bytes of a key tile's eight groups of 16 positions, groups without a page;
+// NaN found by each converter warp in a tile of values.
+struct __align__(32) Info {
+  uint32_t k[2], v[2], bad;
+  uint8_t poison[4];
+};
+
+// What a CTA leaves for the join.
+struct __align__(32) Desc {
+  int last;              // 1: the CTA's last item is cut, its part is in slot 2 c + 1
+  int first;             // bit 0: the first item continues an earlier CTA's (slot 2 c), bit 1: and a later CTA's it
+  int q0, r0, rows, hk;  // of the last item
+};
+
+struct Params {
+  ChunkArgs a;
+  int G, log2_page;
+  float cm;              // |scale| log2(e) = cm 2^ce, cm in [1, 2)
+  int ce, negate;        // negate: scale < 0
+  Desc* desc;            // [CTAs]
+  float4* parts;         // per slot: [D / 4][256] outputs, then [256] references and sums
+};
+
+// ---- the list of items -----------------------------------------------------------
+struct Seq {
+  int q0, nq, nk, items;
+  double off, work;      // G (nk - nq); work of one key/value head's items
+};
+// work of the items before number p (p <= items)
+__device__ __forceinline__ double work_before(double off, double G, int p) {
+  const double p0 = off >= 0.0 ? 0.0 : fmin(floor(-off / 256.0), double(p)), n = double(p) - p0;
+  return 128.0 * (double(p) * (double(p) + 1.0) - p0 * (p0 + 1.0)) + n * off + double(p) * G * kItemKeys;
 }
+__device__ __forceinline__ Seq load_seq(const Params& P, int b, bool* bad) {
+  const ChunkArgs& a = P.a;
+  Seq s;
+  int q1;
+  packed_range(a.cu_q, b, a.total_q, &s.q0, &q1, bad);
+  s.nq = q1 - s.q0;
+  const int x = __ldg(a.lengths + b);
+  s.nk = min(max(x, 0), a.width << P.log2_page);
+  if (s.nk != x) *bad = true;
+  s.items = int(((int64_t)s.nq * P.G + 255) / 256);
+  s.off = double(P.G) * (s.nk - s.nq);
+  s.work = work_before(s.off, P.G, s.items);
+  return s;
+}
+// key tiles that rows [0, end) of the sequence see
+__device__ __forceinline__ int tiles_to(const Seq& s, int G, int64_t end) {
+  const int64_t rows = (int64_t)s.nq * G;
+  const int t = int(((end < rows ? end : rows) - 1) / G);
+  return (min(max(s.nk - s.nq + (t + 1), 0), s.nk) + kKT - 1) / kKT;   // no step leaves an int
+}
+// A place in the list: item (sequence, head, number) and a key tile inside it,
+// which is 0 or cuts the item.
+struct Pos {
+  int b, hk, p, t;
+};
+__device__ __forceinline__ bool same_item(const Pos& x, const Pos& y) { return x.b == y.b && x.hk == y.hk && x.p == y.p; }
+
+// Whole warp: first sequence from b on that has items, n_seq if none.
+__device__ __forceinline__ int seq_from(const Params& P, int b) {
+  const int lane = threadIdx.x & 31;
+  bool bad;
+  for (; b < P.a.n_seq; b += 32) {
+    int q0, q1 = 0;
+    q0 = q1;
+    if (b + lane < P.a.n_seq) packed_range(P.a.cu_q, b + lane, P.a.total_q, &q0, &q1, &bad);
+    const unsigned any = __ballot_sync(0xFFFFFFFFu, q1 > q0);
+    if (any) return b + __ffs(any) - 1;
+  }
+  return P.a.n_seq;
+}
+__device__ __forceinline__ Pos next_item(const Params& P, const Seq& s, Pos x) {
+  x.t = 0;
+  if (++x.p == s.items) {
+    x.p = 0;
+    if (++x.hk == P.a.c.n_kv_heads) {
+      x.hk = 0;
+      x.b = seq_from(P, x.b + 1);
+    }
+  }
+  return x;
+}
+// Whole warp: the place at `at` of the whole work.
+__device__ Pos find_place(const Params& P, double at) {
+  const int lane = threadIdx.x & 31, H = P.a.c.n_kv_heads;
+  bool bad;
+  double before = 0.0;
+  Seq s{};
+  int b = -1;
+  for (int b0 = 0; b0 < P.a.n_seq && b < 0; b0 += 32) {
+    double w = 0.0;
+    if (b0 + lane < P.a.n_seq) w = load_seq(P, b0 + lane, &bad).work * H;
+    double incl = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    incl += before;
+    const unsigned hit = __ballot_sync(0xFFFFFFFFu, w > 0.0 && at < incl);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      b = b0 + src;
+      before = __shfl_sync(0xFFFFFFFFu, incl - w, src);
+      s = load_seq(P, b, &bad);
+    } else {
+      before = __shfl_sync(0xFFFFFFFFu, incl, 31);
+    }
+  }
+  if (b < 0) return Pos{P.a.n_seq, 0, 0, 0};
+  double rem = fmax(at - before, 0.0);
+  const int hk = min(int(rem / s.work), H - 1);
+  rem = fmax(rem - hk * s.work, 0.0);
+  // the last item that begins at or before rem: 32 candidates a round
+  int lo = 0, hi = s.items;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, p = lo + lane * step;
+    const unsigned ok = __ballot_sync(0xFFFFFFFFu, p < hi && work_before(s.off, P.G, p) <= rem);
+    const int k = ok ? 31 - __clz(ok) : 0;      // lane 0's begins before rem
+    hi = min(hi, lo + (k + 1) * step);
+    lo += k * step;
+  }
+  const double w0 = work_before(s.off, P.G, lo), w1 = work_before(s.off, P.G, lo + 1);
+  const int n = tiles_to(s, P.G, 256 * ((int64_t)lo + 1));
+  Pos x{b, hk, lo, int((rem - w0) / (w1 - w0) * n + 0.5)};
+  if (x.t >= n && n > 0) x = next_item(P, s, x);
+  else if (n == 0) x.t = 0;
+  return x;
+}
+
+__device__ __forceinline__ uint32_t f16x2_of(uint32_t w) {      // codes in the low half of a word
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}\n" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2_of_hi(uint32_t w) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}\n" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2_bits(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float pow2c(int e) { return pow2(min(max(e, -126), 127)); }
+// How far, in log2, the score s of a page with scale byte k and factor c lies above
+// the score sr of one with kr and cr: taken in units of the larger scale.
+__device__ __forceinline__ float above(float s, int k, float c, float sr, int kr, float cr) {
+  const int d = kr - k;
+  return fmaf(-sr, pow2c(min(d, 0)), s * pow2c(min(-d, 0))) * (d > 0 ? cr : c);
+}
+// Codes that are NaN, to zero.
+__device__ __forceinline__ uint32_t drop_nan4(uint32_t w) {
+  const uint32_t m = __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  return w & ~m;
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+// Bounded wait of a lane (inlined: setmaxnreg and calls do not go together) ...
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
+  return uwait(bar, parity, abort, status);
+}
+// ... and of a whole warp, whose lanes all get the same answer.
+__device__ __forceinline__ bool bar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
+  return __all_sync(0xFFFFFFFFu, uwait(bar, parity, abort, status));
+}
+// f16 operands, fp32 accumulator, both K-major.
+constexpr uint32_t idesc_f16(int M, int N) { return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24); }
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ Params P) {
+  using Pl = Plan<D>;
+  constexpr int NS = Pl::kStages, NR = Pl::kRaws, NB = Pl::kBoxes;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  Info* info = reinterpret_cast<Info*>(smem + Pl::kInfo);
+  uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + Pl::kBars);
+  uint64_t* raw_empty = raw_full + NR;
+  uint64_t* full = raw_empty + NR;
+  uint64_t* empty = full + NS;
+  uint64_t* q_full = empty + NS;       // [2]
+  uint64_t* s_full = q_full + 2;       // [2][2]: query tile, half of the keys
+  uint64_t* p_first = s_full + 4;      // [2]: the first half's probabilities are there, the second half's scores taken
+  uint64_t* p_second = p_first + 2;    // [2]: the second half's probabilities
+  uint64_t* h_done = p_second + 2;     // [2]: the first half's product
+  uint64_t* o_full = h_done + 2;       // [2]
+  uint64_t* o_free = o_full + 2;       // [2]
+  uint64_t* fin = o_free + 2;          // [2]: a warp's MMAs at the end
+  uint64_t* turn = fin + 2;            // [2]: the other MMA warp has issued
+  uint64_t* it_full = turn + 2;        // [2]
+  uint64_t* it_empty = it_full + 2;    // [2]
+  uint64_t* info_full = it_empty + 2;  // [kSlots]
+  uint64_t* v_done = info_full + kSlots;   // [kSlots]: the tile's values are converted
+  Item* items = reinterpret_cast<Item*>(smem + Pl::kItems);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + Pl::kItems + 2 * 96);
+  volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
+
+  const ChunkArgs& a = P.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int G = P.G, page = 1 << P.log2_page, H = a.c.n_kv_heads;
+  int* status = a.status;
+
+  if (tid == 0) {
+    for (int i = 0; i < NR; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], 4);
+    }
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], 4);
+      mbar_init(&empty[i], 2);     // both query tiles
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 4);
+      mbar_init(&s_full[2 * i], 1);
+      mbar_init(&s_full[2 * i + 1], 1);
+      mbar_init(&p_first[i], 4);
+      mbar_init(&p_second[i], 4);
+      mbar_init(&h_done[i], 1);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&o_free[i], 4);
+      mbar_init(&fin[i], 1);
+      mbar_init(&turn[i], 1);
+      mbar_init(&it_full[i], 1);
+      mbar_init(&it_empty[i], 14);   // 2 MMA, 4 converter, 8 softmax warps
+    }
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&info_full[i], 1);
+      mbar_init(&v_done[i], 4);
+    }
+    *abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == kWMma0) tmem_alloc(tslot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  const uint32_t base = smem_addr(smem);
+  const uint32_t q_s = base + Pl::kQ, ring_s = base + Pl::kRing, raw_s = base + Pl::kRawRing;
+
+  // The t-th item of this CTA, copied out of its slot (whole warp; one lane
+  // arrives when all have it).
+  auto take_item = [&](int t, Item* it) {
+    if (!bar_wait_warp(&it_full[t & 1], uint32_t(t >> 1) & 1u, abort, status)) return false;
+    *it = items[t & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&it_empty[t & 1]);
+    return it->n >= 0;
+  };
+
+  if (warp < 4) {
+    regs_down<kRegsCtl>();
+    if (warp == kWProd) {
+      // ---- producer: items, and their pages -------------------------------------------------
+      bool bad = false, ok = true;
+      double total = 0.0;
+      for (int b = lane; b < a.n_seq; b += 32) total += load_seq(P, b, &bad).work * H;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+      bad = __any_sync(0xFFFFFFFFu, bad);
+      if (bad && blockIdx.x == 0 && lane == 0 && status) atomicOr(status, MOE_DEV_INDEX_OOB);
+      const int N = int(fmin(fmax(total / (double(G) * kCtaKeys), 1.0), double(gridDim.x))), c = blockIdx.x;
+      Pos at{a.n_seq, 0, 0, 0}, end = at;
+      if (c < N && total > 0.0) {
+        at = c == 0 ? Pos{seq_from(P, 0), 0, 0, 0} : find_place(P, total * c / N);
+        if (c + 1 < N) end = find_place(P, total * (c + 1) / N);
+      }
+      bool ignore;
+      if (lane == 0) {
+        Desc d{};
+        if (at.t > 0) d.first = 1 | (same_item(at, end) ? 2 : 0);
+        if (end.t > 0 && !(at.t > 0 && same_item(at, end))) {
+          const Seq s = load_seq(P, end.b, &ignore);
+          d.last = 1;
+          d.q0 = s.q0;
+          d.r0 = 256 * end.p;
+          d.rows = int(min((int64_t)256, (int64_t)s.nq * G - d.r0));
+          d.hk = end.hk;
+        }
+        P.desc[c] = d;
+      }
+      // item t of this CTA into its slot; false if there is none (nor any later)
+      auto publish = [&](int t) {
+        if (t >= 2 && !bar_wait_warp(&it_empty[t & 1], uint32_t((t >> 1) - 1) & 1u, abort, status)) {
+          ok = false;
+          return false;
+        }
+        const bool last = same_item(at, end);
+        const bool have = at.b < a.n_seq && !(last && end.t <= at.t);
+        if (have) {
+          const Seq s = load_seq(P, at.b, &ignore);
+          Item it;
+          const int64_t rows = (int64_t)s.nq * G, r0 = 256 * (int64_t)at.p;
+          const int n = tiles_to(s, G, r0 + 256), t1 = last ? end.t : n;
+          it.n = t1 - at.t;
+          it.t0 = at.t;
+          it.r0 = int(r0);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int64_t f = r0 + j * kQT;
+            it.rows[j] = int(min(max(rows - f, (int64_t)0), (int64_t)kQT));
+            it.nkt[j] = it.rows[j] ? min(max(tiles_to(s, G, f + kQT) - at.t, 0), it.n) : 0;
+          }
+          it.b = at.b;
+          it.hk = at.hk;
+          it.q0 = s.q0;
+          it.off = s.nk - s.nq;
+          it.nk = s.nk;
+          it.vmin = min(max(int(r0 / G) + 1 + it.off, 0), s.nk);
+          it.slot = at.t > 0 ? 2 * c : t1 < n ? 2 * c + 1 : -1;
+          if (lane == 0) items[t & 1] = it;
+          at = last ? end : next_item(P, s, at);
+          if (last) at.b = a.n_seq;
+        } else if (lane == 0) {
+          items[t & 1].n = -1;
+        }
+        __threadfence_block();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&it_full[t & 1]);
+        return have;
+      };
+      const int per = page / 16;            // groups of a page
+      const uint32_t bytes = uint32_t(page) * D;
+      int r = 0, loads = 0, tiles = 0;      // raw slot, loads and key tiles so far
+      bool more = publish(0);
+      bool outside = false;
+      for (int t = 0; ok && more; ++t) {
+        more = publish(t + 1);
+        const Item it = items[t & 1];
+        // lane g < 8: group g's page (-1: none); scale bytes of a page
+        auto load_page = [&](int i) {
+          const int pos = (it.t0 + i) * kKT + 16 * lane;
+          if (lane >= 8 || i >= it.n || pos >= it.nk) return -2;
+          const int x = __ldg(a.table + (size_t)it.b * a.width + (pos >> P.log2_page));
+          return x >= 0 && x < a.c.n_pages ? x : -1;
+        };
+        auto load_scales = [&](int pg) {
+          if (pg < 0) return 0u;
+          const size_t x = (size_t)pg * H + it.hk;
+          return uint32_t(__ldg(a.c.k_scales + x)) | uint32_t(__ldg(a.c.v_scales + x)) << 8;
+        };
+        int pg = load_page(0), pg1 = load_page(1);
+        uint32_t sc = load_scales(pg);
+        for (int i = 0; i < it.n; ++i) {
+          const int pg2 = load_page(i + 2);
+          const uint32_t sc1 = load_scales(pg1);
+          outside |= pg == -1;
+          const int slot = tiles % kSlots;
+          if (lane < 8) {
+            reinterpret_cast<uint8_t*>(info[slot].k)[lane] = uint8_t(sc);
+            reinterpret_cast<uint8_t*>(info[slot].v)[lane] = uint8_t(sc >> 8);
+          }
+          const unsigned none = __ballot_sync(0xFFFFFFFFu, pg == -1) & 0xFFu;
+          if (lane == 0) info[slot].bad = none;
+          __threadfence_block();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&info_full[slot]);
+          const bool leads = lane < 8 && lane % per == 0 && pg >= 0;
+          const uint32_t sum = bytes * __popc(__ballot_sync(0xFFFFFFFFu, leads));
+          const size_t from = leads ? ((size_t)pg * H + it.hk) * bytes : 0;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (loads >= NR && !bar_wait_warp(&raw_empty[r], uint32_t(loads / NR - 1) & 1u, abort, status)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&raw_full[r], sum);
+            __syncwarp();
+            if (leads)
+              bulk_g2s(smem + Pl::kRawRing + r * Pl::kRaw + lane * (16 * D),
+                       static_cast<const uint8_t*>(e ? a.c.v_codes : a.c.k_codes) + from, bytes, &raw_full[r]);
+            ++loads;
+            if (++r == NR) r = 0;
+          }
+          if (!ok) break;
+          ++tiles;
+          pg = pg1, pg1 = pg2, sc = sc1;
+        }
+      }
+      if (__any_sync(0xFFFFFFFFu, outside) && lane == 0 && status) atomicOr(status, MOE_DEV_INDEX_OOB);
+      if (*abort) {   // copies in flight land before the CTA's shared memory goes away
+        for (int i = loads > NR ? loads - NR : 0; i < loads; ++i) mbar_wait(&raw_full[i % NR], uint32_t(i / NR) & 1u, status);
+      }
+    } else if (warp == kWMma0 || warp == kWMma1) {
+      // ---- MMA --------------------------------------------------------------------------
+      constexpr uint32_t kTile16 = Pl::kTile >> 4, kBox16 = kBoxBytes >> 4;
+      const int j = warp == kWMma1;
+      const uint32_t id_s = idesc_f16(kQT, kKT / 2), id_o = idesc_f16(kQT, D) | (1u << 16);   // bit 16: B is MN-major
+      const uint64_t dq = umma_desc_sw128(q_s + j * Pl::kTile);
+      const uint64_t dk = umma_desc_sw128(ring_s), dv = umma_desc_mn_sw128(ring_s, kBoxBytes);
+      const uint32_t ts = tmem + j * kKT, to = tmem + 256 + j * D;
+      const uint32_t empty_s = smem_addr(empty);
+      uint32_t st = 0, par = 0;                      // ring stage and phase
+      uint32_t q_par = 0, p_par = 0, o_par = 1;      // phases of Q, of the probabilities, of O's release
+      uint32_t turn_par = 1 - j;                     // tile 0 begins
+      uint32_t g = 0;                                // columns of a key tile's first scores: g * 64
+      bool ok = true, o_used = false;
+      auto wait = [&](uint64_t* bar, uint32_t ph) { return bar_wait_warp(bar, ph, abort, status); };
+      auto scores = [&](uint32_t stage, int half, uint32_t col) {
+        const uint64_t b0 = dk + stage * kTile16 + half * (kBox16 / 2);
+#pragma unroll
+        for (int x = 0; x < NB; ++x) umma_ss_4(ts + col, dq + x * kBox16, b0 + x * kBox16, id_s, x > 0);
+        umma_commit_1(smem_addr(&s_full[2 * j + half]));
+      };
+      // On to the next stage. The softmax warps see from the scores that follow
+      // when a stage has been read; one of a tile that is not theirs is given
+      // up here.
+      auto next_stage = [&](bool unused) {
+        if (unused) mbar_arrive_1(empty_s + 8 * st);
+        if (++st == NS) st = 0, par ^= 1;
+      };
+      Item it;
+      for (int t = 0; ok && take_item(t, &it); ++t) {
+        const int n = __shfl_sync(0xFFFFFFFFu, it.n, 0);
+        const int nkt = __shfl_sync(0xFFFFFFFFu, j ? it.nkt[1] : it.nkt[0], 0);
+        if (n == 0) continue;
+        if (!(ok = wait(&full[st], par))) break;
+        if (nkt > 0) {
+          if (!(ok = wait(&q_full[j], q_par))) break;
+          q_par ^= 1;
+          tc_fence_after();
+          scores(st, 0, 64 * g);
+          scores(st, 1, 64 - 64 * g);
+        }
+        next_stage(nkt == 0);
+        for (int i = 0; i < n; ++i) {
+          if (!(ok = wait(&full[st], par))) break;
+          const uint64_t b0 = dv + st * kTile16;
+          if (i < nkt) {
+            if (i == 0) {              // the last item's output has been read
+              if (o_used && !(ok = wait(&o_free[j], o_par))) break;
+              o_used = true;
+              o_par ^= 1;
+            }
+            if (i + 1 < nkt) {         // the next tile's first scores, where this one's second ones were
+              const uint32_t st1 = st + 1 == NS ? 0 : st + 1;
+              if (!(ok = wait(&full[st1], st1 ? par : par ^ 1)) || !(ok = wait(&p_first[j], p_par))) break;
+              tc_fence_after();
+              scores(st1, 0, 64 - 64 * g);
+            } else {
+              if (!(ok = wait(&p_first[j], p_par))) break;
+              tc_fence_after();
+            }
+            umma_ts_4(to, ts + 64 * g, b0, id_o, i > 0);
+            umma_commit_1(smem_addr(&h_done[j]));
+            if (!(ok = wait(&p_second[j], p_par))) break;
+            p_par ^= 1;
+            tc_fence_after();
+            umma_ts_4(to, ts + 64 * g + 32, b0 + 4 * 128, id_o, true);
+            if (i + 1 == nkt) umma_commit_1(smem_addr(&o_full[j]));
+          }
+          // the two tiles' second products and next scores strictly in turn
+          if (!(ok = wait(&turn[j], turn_par))) break;
+          turn_par ^= 1;
+          next_stage(i >= nkt);
+          if (i + 1 < n) {
+            if (i + 1 < nkt)
+              scores(st, 1, 64 * g);
+            else if (!(ok = wait(&full[st], par)))
+              break;
+            mbar_arrive_1(smem_addr(&turn[1 - j]));
+            next_stage(i + 1 >= nkt);
+          } else {
+            mbar_arrive_1(smem_addr(&turn[1 - j]));
+          }
+          if (i < nkt) g ^= 1;
+        }
+      }
+      // every MMA has finished before tensor memory is freed
+      umma_commit_1(smem_addr(&fin[j]));
+      mbar_wait(&fin[j], 0, status);
+    }
+  } else if (warp < kWSoft) {
+    // ---- converters -----------------------------------------------------------------------
+    regs_down<kRegsConv>();
+    constexpr int VPR = D / 16, NV = 128 * VPR / 128, RPI = 128 / VPR;   // 16-code vectors a row, a thread; rows a step
+    const int ct = tid - kWConv * 32, row0 = ct / VPR, c16 = ct % VPR;
+    const int box = c16 / 4, chunk = (c16 % 4) * 2, odd = box & 1;
+    // the two 16-byte pieces, in an order that spreads a quarter warp's over all banks
+    const uint32_t o0 = box * kBoxBytes + row0 * 128 + (((chunk + odd) ^ (row0 & 7)) << 4);
+    const uint32_t o1 = box * kBoxBytes + row0 * 128 + (((chunk + 1 - odd) ^ (row0 & 7)) << 4);
+    int s = 0, r = 0, loads = 0, tiles = 0;
+    bool ok = true;
+    Item it;
+    for (int t = 0; ok && take_item(t, &it); ++t) {
+      for (int e = 0; e < 2 * it.n; ++e) {
+        const int i = e >> 1;
+        if (!bar_wait_warp(&raw_full[r], uint32_t(loads / NR) & 1u, abort, status) ||
+            (loads >= NS && !bar_wait_warp(&empty[s], uint32_t(loads / NS - 1) & 1u, abort, status))) {
+          ok = false;
+          break;
+        }
+        const uint4* src = reinterpret_cast<const uint4*>(smem + Pl::kRawRing + r * Pl::kRaw) + ct;
+        uint8_t* dst = smem + Pl::kRing + s * Pl::kTile;
+        uint4 w[NV];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) w[v] = src[v * 128];
+        if (e & 1) {
+          const int k0 = (it.t0 + i) * kKT, slot = tiles % kSlots;
+          const unsigned none = *reinterpret_cast<volatile uint32_t*>(&info[slot].bad);
+          const bool masked = k0 + kKT > it.vmin;
+          bool found = false;
+          if (masked || none) {
+            const int keys = it.nk - k0;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+              const int row = row0 + v * RPI;
+              if (row >= keys || (none >> (row / 16)) & 1) w[v] = make_uint4(0, 0, 0, 0);
+              if (masked && (any_nan4(w[v].x) || any_nan4(w[v].y) || any_nan4(w[v].z) || any_nan4(w[v].w))) {
+                found = true;
+                w[v].x = drop_nan4(w[v].x);
+                w[v].y = drop_nan4(w[v].y);
+                w[v].z = drop_nan4(w[v].z);
+                w[v].w = drop_nan4(w[v].w);
+              }
+            }
+          }
+          found = __any_sync(0xFFFFFFFFu, found);
+          if (lane == 0) info[slot].poison[warp - kWConv] = found;
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const uint4 lo = make_uint4(f16x2_of(w[v].x), f16x2_of_hi(w[v].x), f16x2_of(w[v].y), f16x2_of_hi(w[v].y));
+          const uint4 hi = make_uint4(f16x2_of(w[v].z), f16x2_of_hi(w[v].z), f16x2_of(w[v].w), f16x2_of_hi(w[v].w));
+          *reinterpret_cast<uint4*>(dst + v * RPI * 128 + o0) = odd ? hi : lo;
+          *reinterpret_cast<uint4*>(dst + v * RPI * 128 + o1) = odd ? lo : hi;
+        }
+        fence_async_smem();
+        __threadfence_block();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&full[s]);
+          mbar_arrive(&raw_empty[r]);
+          if (e & 1) mbar_arrive(&v_done[tiles % kSlots]);
+        }
+        tiles += e & 1;
+        ++loads;
+        if (++s == NS) s = 0;
+        if (++r == NR) r = 0;
+      }
+    }
+  } else {
+    // ---- softmax ------------------------------------------------------------------------
+    regs_up<kRegsSoft>();
+    const int j = (warp - kWSoft) >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t lanes = uint32_t(quarter * 32) << 16;
+    const uint32_t ts = tmem + lanes + j * kKT, to = tmem + lanes + 256 + j * D;
+    int st = 0;                        // ring stage of the next key tile's keys
+    int nsf = 0, nof = 0, tiles = 0;   // scores and outputs awaited; key tiles of all items
+    bool ok = true;
+    Item it;
+    for (int t = 0; ok && take_item(t, &it); ++t) {
+      const int nkt = it.nkt[j], rows = it.rows[j];
+      const int64_t grow = (int64_t)it.r0 + j * kQT + row;       // row of the sequence and head
+      const int tok = int(grow / G), head = it.hk * G + int(grow % G);
+      const int vis = min(max(tok + it.off + 1, 0), it.nk);
+      const int vis_w = __shfl_sync(0xFFFFFFFFu, vis, 0);        // the warp's fewest
+      int ce = P.ce;
+      if (nkt > 0) {
+        // this row of Q to f16; its tile's products of the last item have been read
+        uint4 w[D / 8];
+        const __nv_bfloat16* q = a.q + (int64_t)(it.q0 + tok) * a.q_ts + (int64_t)head * a.q_hs;
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x) w[x] = row < rows ? *reinterpret_cast<const uint4*>(q + x * 8) : make_uint4(0, 0, 0, 0);
+        uint32_t m2 = 0;
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x)
+          m2 = __vmaxu2(__vmaxu2(m2, __vmaxu2(w[x].x & 0x7FFF7FFFu, w[x].y & 0x7FFF7FFFu)),
+                        __vmaxu2(w[x].z & 0x7FFF7FFFu, w[x].w & 0x7FFF7FFFu));
+        const int ex = min(max(int(max(m2 & 0xFFFFu, m2 >> 16) >> 7) - 127, -112), 127);
+        ce += ex - 14;
+        const float f = P.negate ? -pow2(14 - ex) : pow2(14 - ex);
+        const uint32_t dst = row * 128;
+        uint8_t* qs = smem + Pl::kQ + j * Pl::kTile;
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x) {
+          const uint32_t u[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+          uint32_t h[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) h[y] = f16x2_bits(bf16_lo(u[y]) * f, bf16_hi(u[y]) * f);
+          *reinterpret_cast<uint4*>(qs + (x / 8) * kBoxBytes + dst + (((x % 8) ^ (row & 7)) << 4)) =
+              make_uint4(h[0], h[1], h[2], h[3]);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[j]);
+      }
+      // references: score sr of a page with scale byte kr (none yet: have = false), its factor cr, so the score m in
+      // log2; value reference rv above m; sum l in units of 2^m, O in units of 2^(m + rv - 8)
+      bool have = false;
+      float sr = 0.0f, cr = 0.0f, m = 0.0f, l = 0.0f;
+      int kr = 0, rv = 0;              // of a scale byte below all, so that above() takes scores as they are
+      unsigned bad = 0;                // masked tiles with NaN (an item's rows span at most 256 tokens)
+      for (int i = 0; i < nkt; ++i) {
+        const int k0 = (it.t0 + i) * kKT, slot = (tiles + i) % kSlots;
+        const uint32_t slot_ph = uint32_t((tiles + i) / kSlots) & 1u;
+        const bool masked = k0 + kKT > it.vmin;
+        const uint32_t ph = uint32_t(nsf) & 1u, ta = ts + 64 * ph, tb = ts + 64 - 64 * ph;
+        ++nsf;
+        const int n_vis = vis - k0;
+        const bool cut = k0 + kKT > vis_w;   // some lane of the warp does not see the whole tile
+        uint32_t s[2][32];
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          if (!bar_wait(&s_full[2 * j + half], ph, abort, status)) ok = false;
+          // complete by now, and for this tile: a warp that had nothing to do for an item is far ahead of its ring
+          if (!bar_wait(&info_full[slot], slot_ph, abort, status)) ok = false;
+          const uint32_t kb4 = info[slot].k[half], vb4 = info[slot].v[half];
+          const unsigned none = info[slot].bad;
+          if (half == 1) {   // the products before these scores are done, too: their values are released with the keys
+            if (warp == kWSoft + 4 * j && lane == 0) {
+              if (i > 0) mbar_arrive(&empty[st == 0 ? NS - 1 : st - 1]);
+              mbar_arrive(&empty[st]);
+            }
+            st = st + 2 >= NS ? st + 2 - NS : st + 2;
+          }
+          tc_fence_after();
+          tmem_ld32(half ? tb : ta, s[0]);
+          tmem_ld32((half ? tb : ta) + 32, s[1]);
+          tmem_wait_ld32(s[0]);
+          tie32(s[1]);
+          if (half == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_first[j]);
+          }
+          // a group of 16 keys: factor of its scores, its largest score, how far that is above the reference
+          float ck[4], mx[4], d[4];
+          int ve[4];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            uint32_t* x = &s[g >> 1][(g & 1) * 16];
+            if (cut) {
+#pragma unroll
+              for (int y = 0; y < 16; ++y)
+                if (64 * half + 16 * g + y >= n_vis) x[y] = 0xFF800000u;
+            }
+            if (none) {
+              if ((none >> (4 * half + g)) & 1) {
+#pragma unroll
+                for (int y = 0; y < 16; ++y) x[y] = 0xFF800000u;
+              }
+            }
+            float a0 = max3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
+            float a1 = max3(__uint_as_float(x[3]), __uint_as_float(x[4]), __uint_as_float(x[5]));
+            a0 = max3(a0, __uint_as_float(x[6]), __uint_as_float(x[7]));
+            a1 = max3(a1, __uint_as_float(x[8]), __uint_as_float(x[9]));
+            a0 = max3(a0, __uint_as_float(x[10]), __uint_as_float(x[11]));
+            a1 = max3(a1, __uint_as_float(x[12]), __uint_as_float(x[13]));
+            a0 = max3(a0, __uint_as_float(x[14]), __uint_as_float(x[15]));
+            mx[g] = fmaxf(a0, a1);
+            const int kb = int(kb4 >> (8 * g)) & 255;
+            ve[g] = (int(vb4 >> (8 * g)) & 255) - 127;
+            ck[g] = __uint_as_float(__float_as_uint(P.cm) + (uint32_t(min(max(ce + kb - 127, -100), 126)) << 23));
+            d[g] = above(mx[g], kb, ck[g], sr, kr, cr);
+          }
+          const float dm = fmaxf(fmaxf(d[0], d[1]), fmaxf(d[2], d[3]));
+          const float dy = fmaxf(fmaxf(d[0] + float(ve[0]), d[1] + float(ve[1])), fmaxf(d[2] + float(ve[2]), d[3] + float(ve[3])));
+          const bool raise = have ? dm > kRaiseSum || dy > float(rv) + kRaiseOut : dm > -INFINITY;
+          if (__any_sync(0xFFFFFFFFu, raise)) {
+            float fl = 1.0f, fo = 1.0f;
+            if (raise) {
+              float top = have ? 0.0f : -INFINITY;     // of the new reference above the old one
+              float nsr = sr, ncr = cr;
+              int nkr = kr;
+#pragma unroll
+              for (int g = 0; g < 4; ++g)
+                if (d[g] > top) top = d[g], nsr = mx[g], ncr = ck[g], nkr = int(kb4 >> (8 * g)) & 255;
+              sr = nsr, cr = ncr, kr = nkr;
+              m = sr * cr;
+              float y = have ? float(rv) - top : -INFINITY;
+#pragma unroll
+              for (int g = 0; g < 4; ++g)
+                y = fmaxf(y, above(mx[g], int(kb4 >> (8 * g)) & 255, ck[g], sr, kr, cr) + float(ve[g]));
+              const int nrv = int(ceilf(fminf(fmaxf(y, -1000.0f), 1000.0f)));
+              fl = have ? pf_ex2(-top) : 0.0f;
+              fo = have ? pf_ex2(float(rv - nrv) - top) : 0.0f;
+              rv = nrv;
+              have = true;
+            }
+            l *= fl;
+            // what is in O: the earlier tiles' products, which have finished
+            // when this tile's second scores have, since these were issued after
+            // them; in the second half this tile's first product too, after
+            // which the next tile's first scores are issued
+            if (half == 1 || i > 0) {
+              if (!bar_wait(half ? &h_done[j] : &s_full[2 * j + 1], ph, abort, status)) ok = false;
+              tc_fence_after();
+#pragma unroll 1
+              for (int z = 0; z < D; z += 16) {
+                uint32_t o[16];
+                tmem_ld16(to + z, o);
+#pragma unroll
+                for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * fo);
+                tmem_st16(to + z, o);
+              }
+            }
+          }
+          const bool far = fabsf(m) > kFar;
+          const float ref = far ? 0.0f : m;
+          if (__any_sync(0xFFFFFFFFu, far)) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const int dk = kr - (int(kb4 >> (8 * g)) & 255);     // as above()
+              const float fs = far ? -sr * pow2c(min(dk, 0)) : 0.0f, fx = far ? pow2c(min(-dk, 0)) : 1.0f;
+              if (far && dk > 0) ck[g] = cr;
+              uint32_t* x = &s[g >> 1][(g & 1) * 16];
+#pragma unroll
+              for (int y = 0; y < 16; ++y) x[y] = __float_as_uint(fmaf(__uint_as_float(x[y]), fx, fs));
+            }
+          }
+          const uint64_t r2 = pack2(-ref, -ref);
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            uint32_t pb[16];
+            uint64_t sum[4];
+#pragma unroll
+            for (int hg = 0; hg < 2; ++hg) {
+              const int g = 2 * b + hg;
+              uint32_t* x = &s[b][hg * 16];
+              const uint64_t c2 = pack2(ck[g], ck[g]);
+              const float fv = pow2c(ve[g] - rv + int(kPBias));
+              const uint64_t f2 = pack2(fv, fv);
+              float e[16];
+#pragma unroll
+              for (int y = 0; y < 16; y += 2)
+                unpack2(fma2(pack2(__uint_as_float(x[y]), __uint_as_float(x[y + 1])), c2, r2), e[y], e[y + 1]);
+#pragma unroll
+              for (int y = 0; y < 16; ++y) e[y] = pf_ex2(e[y]);
+#pragma unroll
+              for (int y = 0; y < 16; y += 2) {
+                float p0, p1;
+                unpack2(mul2(pack2(e[y], e[y + 1]), f2), p0, p1);
+                pb[hg * 8 + y / 2] = f16x2_bits(p0, p1);
+              }
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                const uint64_t v = add2(pack2(e[2 * z], e[2 * z + 1]), pack2(e[2 * z + 8], e[2 * z + 9]));
+                sum[z] = hg ? add2(sum[z], v) : v;
+              }
+            }
+            tmem_st16(ta + 32 * half + 16 * b, pb);
+            float a0, a1;
+            unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a0, a1);
+            l += a0 + a1;
+          }
+          if (half == 0) tmem_wait_st();
+        }
+        if (masked) {
+          if (!bar_wait(&v_done[slot], slot_ph, abort, status)) ok = false;
+          if (*reinterpret_cast<volatile uint32_t*>(info[slot].poison)) bad |= 1u << (it.t0 + i - it.vmin / kKT);
+        }
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+          ok = false;
+          break;
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_second[j]);
+      }
+      if (!ok) break;
+      tiles += it.n;
+      const int st_end = (st + 2 * (it.n - nkt)) % NS;
+      if (rows == 0) {
+        st = st_end;
+        continue;
+      }
+      const bool mine = row < rows;
+      if (nkt > 0) {
+        if (!bar_wait_warp(&o_full[j], uint32_t(nof++) & 1u, abort, status)) break;
+        if (warp == kWSoft + 4 * j && lane == 0) mbar_arrive(&empty[st == 0 ? NS - 1 : st - 1]);
+        tc_fence_after();
+      }
+      const int64_t orow = (int64_t)(it.q0 + tok) * a.n_heads + head;
+      __nv_bfloat16* out = a.out + orow * D;
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const float f0 = pow2c((rv - int(kPBias)) >> 1), f1 = pow2c((rv - int(kPBias)) - ((rv - int(kPBias)) >> 1));
+      float4* part = P.parts + (size_t)(it.slot < 0 ? 0 : it.slot) * (256 * (D / 4 + 1)) + j * kQT + row;
+#pragma unroll 1
+      for (int x = 0; x < D; x += 32) {
+        uint32_t o[32];
+        if (nkt > 0) {
+          tmem_ld32(to + x, o);
+          tmem_wait_ld32(o);
+          if (x + 32 == D) {   // all of O is in registers: the next item may overwrite it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_free[j]);
+          }
+        } else {
+#pragma unroll
+          for (int y = 0; y < 32; ++y) o[y] = 0;
+        }
+        for (unsigned left = bad; left; left &= left - 1) {
+          const int k0 = (it.vmin / kKT + __ffs(left) - 1) * kKT;
+          for (int k = k0; k < min(k0 + kKT, vis); ++k) {
+            const int pg = __ldg(a.table + (size_t)it.b * a.width + (k >> P.log2_page));
+            if (pg < 0 || pg >= a.c.n_pages) continue;
+            const uint4* v = reinterpret_cast<const uint4*>(
+                static_cast<const uint8_t*>(a.c.v_codes) + ((((size_t)pg * H + it.hk) << P.log2_page) + (k & (page - 1))) * D + x);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint4 c4 = v[y];
+              const uint32_t c[4] = {c4.x, c4.y, c4.z, c4.w};
+#pragma unroll
+              for (int z = 0; z < 16; ++z)
+                if (((c[z >> 2] >> (8 * (z & 3))) & 0x7Fu) == 0x7Fu) o[16 * y + z] = 0x7FC00000u;
+            }
+          }
+        }
+        if (it.slot >= 0) {
+          if (mine) {
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+              part[(size_t)(x / 4 + y) * 256] = make_float4(__uint_as_float(o[4 * y]), __uint_as_float(o[4 * y + 1]),
+                                                            __uint_as_float(o[4 * y + 2]), __uint_as_float(o[4 * y + 3]));
+          }
+        } else if (mine) {
+          uint32_t b[16];
+#pragma unroll
+          for (int y = 0; y < 16; ++y)
+            b[y] = l == 0.0f ? 0u : bf16x2_bits(__uint_as_float(o[2 * y]) * inv * f0 * f1, __uint_as_float(o[2 * y + 1]) * inv * f0 * f1);
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            *reinterpret_cast<uint4*>(out + x + y * 8) = make_uint4(b[4 * y], b[4 * y + 1], b[4 * y + 2], b[4 * y + 3]);
+        }
+      }
+      st = st_end;
+      if (mine) {
+        if (it.slot >= 0)
+          part[(size_t)(D / 4) * 256] = make_float4(sr, cr, l, __int_as_float((rv << 8) | kr));
+        else if (a.lse)
+          a.lse[orow] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2f;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWMma0) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of an item that was cut, in order of position: block (c, x)
+// channels 4 x .. 4 x + 3 of the item that begins in CTA c and ends in a later one,
+// thread = row. References are those of the part with the largest; parts are read
+// coalesced over the rows.
+template <int D>
+__global__ void __launch_bounds__(256) chunk_join_kernel(const Params P) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x, x = blockIdx.y, row = threadIdx.x;
+  const Desc d = P.desc[c];
+  if (!d.last || row >= d.rows) return;
+  constexpr size_t kSlot = 256 * (D / 4 + 1);
+  int last = c + 1;                // the last CTA with a part
+  while (P.desc[last].first & 2) ++last;
+  auto slot = [&](int k) { return P.parts + (size_t)(k == c ? 2 * c + 1 : 2 * k) * kSlot + row; };
+  // the part with the largest reference
+  float m = -INFINITY, sr = 0.0f, cr = 0.0f;
+  int kr = 0;
+  for (int k = c; k <= last; ++k) {
+    const float4 h = slot(k)[(size_t)(D / 4) * 256];
+    if (h.z != 0.0f && !(h.x * h.y <= m)) m = h.x * h.y, sr = h.x, cr = h.y, kr = __float_as_int(h.w) & 255;
+  }
+  float l = 0.0f, rm = -INFINITY;
+  for (int k = c; k <= last; ++k) {
+    const float4 h = slot(k)[(size_t)(D / 4) * 256];
+    const int kb = __float_as_int(h.w) & 255, rv = __float_as_int(h.w) >> 8;
+    const float up = above(h.x, kb, h.y, sr, kr, cr);
+    if (h.z != 0.0f) {
+      l += h.z * pf_ex2(up);
+      rm = fmaxf(rm, up + float(rv));
+    }
+  }
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int k = c; k <= last; ++k) {
+    const float4 h = slot(k)[(size_t)(D / 4) * 256], v = slot(k)[(size_t)x * 256];
+    const int kb = __float_as_int(h.w) & 255, rv = __float_as_int(h.w) >> 8;
+    const float up = above(h.x, kb, h.y, sr, kr, cr);
+    if (h.z != 0.0f) {
+      const float f = pf_ex2(up + float(rv) - rm);
+      o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+    }
+  }
+  const int G = P.G, r = d.r0 + row;
+  const int64_t orow = (int64_t)(d.q0 + r / G) * P.a.n_heads + d.hk * G + r % G;
+  const float inv = 1.0f / l, f = pf_ex2(0.5f * (rm - kPBias));
+  uint2 w = make_uint2(0, 0);
+  if (l != 0.0f) w = make_uint2(bf16x2_bits(o.x * inv * f * f, o.y * inv * f * f), bf16x2_bits(o.z * inv * f * f, o.w * inv * f * f));
+  *reinterpret_cast<uint2*>(P.a.out + orow * D + 4 * x) = w;
+  if (x == 0 && P.a.lse) P.a.lse[orow] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2f;
+}
+
+template <int D>
+int launch_chunk(const Params& P, int grid, const DeviceInfo& di, cudaStream_t s) {
+  constexpr uint32_t smem = Plan<D>::kTotal;
+  if (smem > di.smem_optin) return MOE_ERR_UNSUPPORTED_SHAPE;
+  MOE_CUDA_TRY(cudaFuncSetAttribute(chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
+  chunk_kernel<D><<<grid, kThreads, smem, s>>>(P);
+  if (grid > 1) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid - 1, D / 4);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute pdl;
+    pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &pdl;
+    cfg.numAttrs = 1;
+    MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, chunk_join_kernel<D>, P));
+  }
+  return launch_status();
+}
+
+size_t desc_bytes(const DeviceInfo& di) { return round_up(size_t(di.sm_count) * sizeof(Desc), 256); }
 
 }  // namespace
 
-size_t attn_chunk_ws_bytes(const moe_kv_cache&, int, int, int, const DeviceInfo&) { return 256; }
+size_t attn_chunk_ws_bytes(const moe_kv_cache& c, int, int, int, const DeviceInfo& di) {
+  return desc_bytes(di) + size_t(2 * di.sm_count) * 256 * (c.head_dim + 4) * 4;
+}
 
-int launch_attn_chunk(const ChunkArgs& a, const DeviceInfo&, cudaStream_t s) {
-  const dim3 grid((a.total_q + 3) / 4, a.n_heads);
-  if (a.c.head_dim == 128) chunk_simple_kernel<128><<<grid, 128, 0, s>>>(a);
-  else chunk_simple_kernel<64><<<grid, 128, 0, s>>>(a);
-  return launch_status();
+int launch_attn_chunk(const ChunkArgs& a, const DeviceInfo& di, cudaStream_t s) {
+  Params P{};
+  P.a = a;
+  P.G = a.n_heads / a.c.n_kv_heads;
+  while ((1 << P.log2_page) < a.c.page_size) ++P.log2_page;
+  const float c = fabsf(a.scale) * 1.4426950408889634f;
+  if (c > 0.0f) {
+    int e;
+    P.cm = 2.0f * frexpf(c, &e);
+    P.ce = e - 1;
+  } else {   // every score counts the same
+    P.cm = 1.0f;
+    P.ce = -1000;
+  }
+  P.negate = a.scale < 0.0f;
+  P.desc = static_cast<Desc*>(a.ws);
+  P.parts = reinterpret_cast<float4*>(static_cast<char*>(a.ws) + desc_bytes(di));
+  return a.c.head_dim == 128 ? launch_chunk<128>(P, di.sm_count, di, s) : launch_chunk<64>(P, di.sm_count, di, s);
 }
 
 }  // namespace moe

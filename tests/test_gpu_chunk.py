@@ -306,6 +306,15 @@ def test_chunk_long_caches(mx, n, lens, hq, hkv, d, P):
     _check_chunk(mx, c, table, n, lens, hq, seed=6, rows={0, 1, 13, -2, -1})
 
 
+@pytest.mark.parametrize("d,P", [(64, 16), (128, 128)])
+def test_chunk_items_without_a_second_tile_between_others(mx, d, P):
+    """Sequences of more and of fewer rows than a query tile by turns, each long enough for a CTA's stretch to end in it."""
+    new = [150, 3, 90, 20, 130, 1, 64, 100]
+    lens = [4000, 6442, 3797, 5000, 3708, 4500, 2900, 7099]
+    c, table = _filled(mx, lens, P, 1, d, -(-max(lens) // P), 3)
+    _check_chunk(mx, c, table, new, lens, 4, seed=8, heads=[0, 3], rows={0, 1, 30, 33, 50, 63, -30, -2, -1})
+
+
 def test_chunk_many_sequences(mx):
     new = [(i * 37) % 23 for i in range(200)]
     lens = [n + (i * 53) % 90 for i, n in enumerate(new)]
