@@ -19,7 +19,7 @@
 // S1 (128 fp32 columns each, two halves of 64 keys), outputs O0, O1; probabilities go
 // over scores as the A operand of the second product.
 //
-// Warp roles (16 warps, four of each kind, registers dealt by setmaxnreg):
+// Warp roles:
 //   producer (one warp)    items; page-table entries, scale bytes; raw pages by
 //                          1-D bulk copies into a ring
 //   MMA 0, 1 (a warp each) of its query tile: S = Q K^T and O += P V
@@ -53,8 +53,6 @@ namespace {
 constexpr int kQT = 128, kKT = 128;        // rows per query tile, keys per tile
 constexpr int kThreads = 512;
 constexpr int kWProd = 0, kWMma0 = 1, kWMma1 = 2, kWConv = 4, kWSoft = 8;
-// registers: 128 a thread at launch; 64 + 96 + 2 * 176 = 4 * 128
-constexpr int kRegsCtl = 64, kRegsConv = 96, kRegsSoft = 176;
 constexpr uint32_t kBoxBytes = 128 * 128;  // 128 rows of 64 f16 channels
 constexpr int kSlots = 16;                 // key tiles whose scale bytes are kept
 constexpr float kRaiseSum = 16.0f, kRaiseOut = 7.0f, kPBias = 8.0f;   // log2; see above
@@ -63,7 +61,7 @@ constexpr float kLn2f = 0.6931471805599453f;
 // Work of an item beside its keys, in keys, and the least work of a CTA, in keys of
 // a whole group: cuts of one item are then more than a tile apart (an item of n >= 2
 // tiles costs at most G (128 n + 128 + 1) + 256, so a tile at most 193 G + 128).
-constexpr int kItemKeys = 128, kCtaKeys = 448;
+constexpr int kItemKeys = 256, kCtaKeys = 512;
 
 template <int D>
 struct Plan {
@@ -118,31 +116,31 @@ struct Params {
 // ---- the list of items -----------------------------------------------------------
 struct Seq {
   int q0, nq, nk, items;
-  double off, work;      // G (nk - nq); work of one key/value head's items
+  int64_t off, work;     // G (nk - nq); work of one key/value head's items
 };
-// work of the items before number p (p <= items)
-__device__ __forceinline__ double work_before(double off, double G, int p) {
-  const double p0 = off >= 0.0 ? 0.0 : fmin(floor(-off / 256.0), double(p)), n = double(p) - p0;
-  return 128.0 * (double(p) * (double(p) + 1.0) - p0 * (p0 + 1.0)) + n * off + double(p) * G * kItemKeys;
+// work of the items before number p: G times kItemKeys and, about, the positions each one's last row sees
+__device__ __forceinline__ int64_t work_before(int64_t off, int G, int64_t p) {
+  const int64_t p0 = off >= 0 ? 0 : min(-off >> 8, p);
+  return 128 * (p * (p + 1) - p0 * (p0 + 1)) + (p - p0) * off + p * (G * kItemKeys);
 }
 __device__ __forceinline__ Seq load_seq(const Params& P, int b, bool* bad) {
   const ChunkArgs& a = P.a;
   Seq s;
   int q1;
+  const int x = __ldg(a.lengths + b);
   packed_range(a.cu_q, b, a.total_q, &s.q0, &q1, bad);
   s.nq = q1 - s.q0;
-  const int x = __ldg(a.lengths + b);
   s.nk = min(max(x, 0), a.width << P.log2_page);
   if (s.nk != x) *bad = true;
-  s.items = int(((int64_t)s.nq * P.G + 255) / 256);
-  s.off = double(P.G) * (s.nk - s.nq);
+  s.items = int(((int64_t)s.nq * P.G + 255) >> 8);
+  s.off = (int64_t)P.G * (s.nk - s.nq);
   s.work = work_before(s.off, P.G, s.items);
   return s;
 }
 // key tiles that rows [0, end) of the sequence see
 __device__ __forceinline__ int tiles_to(const Seq& s, int G, int64_t end) {
   const int64_t rows = (int64_t)s.nq * G;
-  const int t = int(((end < rows ? end : rows) - 1) / G);
+  const int t = int(uint32_t((end < rows ? end : rows) - 1) / uint32_t(G));       // rows fit an int
   return (min(max(s.nk - s.nq + (t + 1), 0), s.nk) + kKT - 1) / kKT;   // no step leaves an int
 }
 // A place in the list: item (sequence, head, number) and a key tile inside it,
@@ -157,8 +155,7 @@ __device__ __forceinline__ int seq_from(const Params& P, int b) {
   const int lane = threadIdx.x & 31;
   bool bad;
   for (; b < P.a.n_seq; b += 32) {
-    int q0, q1 = 0;
-    q0 = q1;
+    int q0 = 0, q1 = 0;
     if (b + lane < P.a.n_seq) packed_range(P.a.cu_q, b + lane, P.a.total_q, &q0, &q1, &bad);
     const unsigned any = __ballot_sync(0xFFFFFFFFu, q1 > q0);
     if (any) return b + __ffs(any) - 1;
@@ -176,52 +173,74 @@ __device__ __forceinline__ Pos next_item(const Params& P, const Seq& s, Pos x) {
   }
   return x;
 }
-// Whole warp: the place at `at` of the whole work.
-__device__ Pos find_place(const Params& P, double at) {
-  const int lane = threadIdx.x & 31, H = P.a.c.n_kv_heads;
-  bool bad;
-  double before = 0.0;
-  Seq s{};
-  int b = -1;
-  for (int b0 = 0; b0 < P.a.n_seq && b < 0; b0 += 32) {
-    double w = 0.0;
-    if (b0 + lane < P.a.n_seq) w = load_seq(P, b0 + lane, &bad).work * H;
-    double incl = w;
+// Whole warp: the places at at[0], at[1] of the whole work (n_seq where there is
+// none), and the whole work into *total. Two rounds over the sequences: the places
+// depend on the total.
+__device__ void find_places(const Params& P, int c, int* n_cta, Pos (&x)[2], bool* bad) {
+  const int lane = threadIdx.x & 31, H = P.a.c.n_kv_heads, n_seq = P.a.n_seq;
+  Seq own{};
+  if (lane < n_seq) own = load_seq(P, lane, bad);
+  int64_t total = own.work * H;
+  for (int b = lane + 32; b < n_seq; b += 32) total += load_seq(P, b, bad).work * H;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+  const int64_t least = (int64_t)P.G * kCtaKeys;
+  const int N = total >= least * gridDim.x ? int(gridDim.x) : max(int(total / least), 1);
+  *n_cta = N;
+  int64_t at[2], before[2];
+  int b[2], hk[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = c + k;
+    at[k] = total / N * i + total % N * i / N;
+    b[k] = -1;
+    if (c >= N || i >= N || total == 0) b[k] = n_seq;
+  }
+  int64_t sum = 0;
+  bool ignore;
+  for (int b0 = 0; b0 < n_seq && (b[0] < 0 || b[1] < 0); b0 += 32) {
+    const int64_t w = b0 == 0 ? own.work * H : b0 + lane < n_seq ? load_seq(P, b0 + lane, &ignore).work * H : 0;
+    int64_t incl = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const double v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
       if (lane >= o) incl += v;
     }
-    incl += before;
-    const unsigned hit = __ballot_sync(0xFFFFFFFFu, w > 0.0 && at < incl);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      b = b0 + src;
-      before = __shfl_sync(0xFFFFFFFFu, incl - w, src);
-      s = load_seq(P, b, &bad);
-    } else {
-      before = __shfl_sync(0xFFFFFFFFu, incl, 31);
+    incl += sum;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const unsigned hit = __ballot_sync(0xFFFFFFFFu, w > 0 && at[k] < incl);
+      if (b[k] < 0 && hit) {
+        b[k] = b0 + __ffs(hit) - 1;
+        before[k] = __shfl_sync(0xFFFFFFFFu, incl - w, __ffs(hit) - 1);
+      }
     }
+    sum = __shfl_sync(0xFFFFFFFFu, incl, 31);
   }
-  if (b < 0) return Pos{P.a.n_seq, 0, 0, 0};
-  double rem = fmax(at - before, 0.0);
-  const int hk = min(int(rem / s.work), H - 1);
-  rem = fmax(rem - hk * s.work, 0.0);
-  // the last item that begins at or before rem: 32 candidates a round
-  int lo = 0, hi = s.items;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32, p = lo + lane * step;
-    const unsigned ok = __ballot_sync(0xFFFFFFFFu, p < hi && work_before(s.off, P.G, p) <= rem);
-    const int k = ok ? 31 - __clz(ok) : 0;      // lane 0's begins before rem
-    hi = min(hi, lo + (k + 1) * step);
-    lo += k * step;
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    x[k] = Pos{n_seq, 0, 0, 0};
+    if (b[k] < 0 || b[k] >= n_seq) continue;
+    const Seq s = load_seq(P, b[k], &ignore);
+    int64_t rem = at[k] - before[k];
+    int h = 0;
+    while (h + 1 < H && rem >= s.work) rem -= s.work, ++h;
+    hk[k] = h;
+    // the last item that begins at or before rem: 32 candidates a round
+    int lo = 0, hi = s.items;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, p = lo + lane * step;
+      const unsigned ok = __ballot_sync(0xFFFFFFFFu, p < hi && work_before(s.off, P.G, p) <= rem);
+      const int i = 31 - __clz(ok);              // lane 0's begins before rem
+      hi = min(hi, lo + (i + 1) * step);
+      lo += i * step;
+    }
+    const int64_t w0 = work_before(s.off, P.G, lo), w1 = work_before(s.off, P.G, lo + 1);
+    const int n = tiles_to(s, P.G, 256 * ((int64_t)lo + 1));
+    // the two CTAs on both sides of a cut come here with the same numbers
+    x[k] = Pos{b[k], hk[k], lo, n > 0 ? int(float(rem - w0) / float(w1 - w0) * n + 0.5f) : 0};
+    if (x[k].t >= n && n > 0) x[k] = next_item(P, s, x[k]);
   }
-  const double w0 = work_before(s.off, P.G, lo), w1 = work_before(s.off, P.G, lo + 1);
-  const int n = tiles_to(s, P.G, 256 * ((int64_t)lo + 1));
-  Pos x{b, hk, lo, int((rem - w0) / (w1 - w0) * n + 0.5)};
-  if (x.t >= n && n > 0) x = next_item(P, s, x);
-  else if (n == 0) x.t = 0;
-  return x;
 }
 
 __device__ __forceinline__ uint32_t f16x2_of(uint32_t w) {      // codes in the low half of a word
@@ -251,26 +270,25 @@ __device__ __forceinline__ uint32_t drop_nan4(uint32_t w) {
   const uint32_t m = __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
   return w & ~m;
 }
-template <int kRegs>
-__device__ __forceinline__ void regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-template <int kRegs>
-__device__ __forceinline__ void regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-// Bounded wait of a lane (inlined: setmaxnreg and calls do not go together) ...
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
+// Bounded wait of a lane, the long way of which is one function for all (little code:
+// inlined, the warps waited for instructions; 256 us instead of 197 for 1,024 tokens
+// behind 7,168) ...
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
   return uwait(bar, parity, abort, status);
+}
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
+  return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort, status);
 }
 // ... and of a whole warp, whose lanes all get the same answer.
 __device__ __forceinline__ bool bar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
-  return __all_sync(0xFFFFFFFFu, uwait(bar, parity, abort, status));
+  return __all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)) || __all_sync(0xFFFFFFFFu, wait_long(bar, parity, abort, status));
 }
 // f16 operands, fp32 accumulator, both K-major.
 constexpr uint32_t idesc_f16(int M, int N) { return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24); }
 
-template <int D>
+// NG: groups of keys with a scale of their own in half a tile, 4, 2 or 1 for pages of
+// 16, 32 or more.
+template <int D, int NG>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ Params P) {
   using Pl = Plan<D>;
   constexpr int NS = Pl::kStages, NR = Pl::kRaws, NB = Pl::kBoxes;
@@ -352,22 +370,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   };
 
   if (warp < 4) {
-    regs_down<kRegsCtl>();
     if (warp == kWProd) {
       // ---- producer: items, and their pages -------------------------------------------------
       bool bad = false, ok = true;
-      double total = 0.0;
-      for (int b = lane; b < a.n_seq; b += 32) total += load_seq(P, b, &bad).work * H;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
-      bad = __any_sync(0xFFFFFFFFu, bad);
-      if (bad && blockIdx.x == 0 && lane == 0 && status) atomicOr(status, MOE_DEV_INDEX_OOB);
-      const int N = int(fmin(fmax(total / (double(G) * kCtaKeys), 1.0), double(gridDim.x))), c = blockIdx.x;
-      Pos at{a.n_seq, 0, 0, 0}, end = at;
-      if (c < N && total > 0.0) {
-        at = c == 0 ? Pos{seq_from(P, 0), 0, 0, 0} : find_place(P, total * c / N);
-        if (c + 1 < N) end = find_place(P, total * (c + 1) / N);
-      }
+      const int c = blockIdx.x;
+      int n_cta;
+      Pos place[2];
+      find_places(P, c, &n_cta, place, &bad);
+      Pos at = place[0];
+      const Pos end = place[1];
+      if (__any_sync(0xFFFFFFFFu, bad) && c == 0 && lane == 0 && status) atomicOr(status, MOE_DEV_INDEX_OOB);
       bool ignore;
       if (lane == 0) {
         Desc d{};
@@ -449,15 +461,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           const uint32_t sc1 = load_scales(pg1);
           outside |= pg == -1;
           const int slot = tiles % kSlots;
-          if (lane < 8) {
-            reinterpret_cast<uint8_t*>(info[slot].k)[lane] = uint8_t(sc);
-            reinterpret_cast<uint8_t*>(info[slot].v)[lane] = uint8_t(sc >> 8);
-          }
           const unsigned none = __ballot_sync(0xFFFFFFFFu, pg == -1) & 0xFFu;
-          if (lane == 0) info[slot].bad = none;
+          if (lane == 0) info[slot].bad = none;     // the converters read it after the copies' barrier
           __threadfence_block();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&info_full[slot]);
           const bool leads = lane < 8 && lane % per == 0 && pg >= 0;
           const uint32_t sum = bytes * __popc(__ballot_sync(0xFFFFFFFFu, leads));
           const size_t from = leads ? ((size_t)pg * H + it.hk) * bytes : 0;
@@ -476,6 +483,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             if (++r == NR) r = 0;
           }
           if (!ok) break;
+          if (lane < 8) {
+            reinterpret_cast<uint8_t*>(info[slot].k)[lane] = uint8_t(sc);
+            reinterpret_cast<uint8_t*>(info[slot].v)[lane] = uint8_t(sc >> 8);
+          }
+          __threadfence_block();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&info_full[slot]);
           ++tiles;
           pg = pg1, pg1 = pg2, sc = sc1;
         }
@@ -575,13 +589,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     }
   } else if (warp < kWSoft) {
     // ---- converters -----------------------------------------------------------------------
-    regs_down<kRegsConv>();
-    constexpr int VPR = D / 16, NV = 128 * VPR / 128, RPI = 128 / VPR;   // 16-code vectors a row, a thread; rows a step
-    const int ct = tid - kWConv * 32, row0 = ct / VPR, c16 = ct % VPR;
-    const int box = c16 / 4, chunk = (c16 % 4) * 2, odd = box & 1;
-    // the two 16-byte pieces, in an order that spreads a quarter warp's over all banks
-    const uint32_t o0 = box * kBoxBytes + row0 * 128 + (((chunk + odd) ^ (row0 & 7)) << 4);
-    const uint32_t o1 = box * kBoxBytes + row0 * 128 + (((chunk + 1 - odd) ^ (row0 & 7)) << 4);
+    // A thread's vectors of 16 codes: a row's 64-channel box has four, 8 lanes take those of two rows, for heads of 128
+    // of one box of the first and the other of the second, so that neither their loads nor their stores meet in a bank.
+    constexpr int RPI = 32;             // rows between a thread's
+    const int ct = tid - kWConv * 32, c4 = ct & 3, pair = (ct >> 2) & 1, row0 = ct >> 2;
+    const uint32_t out0 = row0 * 128 + (((2 * c4) ^ (row0 & 7)) << 4), out1 = row0 * 128 + (((2 * c4 + 1) ^ (row0 & 7)) << 4);
+    const uint32_t in0 = row0 * D + c4 * 16;
     int s = 0, r = 0, loads = 0, tiles = 0;
     bool ok = true;
     Item it;
@@ -593,22 +606,23 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           ok = false;
           break;
         }
-        const uint4* src = reinterpret_cast<const uint4*>(smem + Pl::kRawRing + r * Pl::kRaw) + ct;
+        const uint8_t* src = smem + Pl::kRawRing + r * Pl::kRaw + in0;
         uint8_t* dst = smem + Pl::kRing + s * Pl::kTile;
-        uint4 w[NV];
+        const int k0 = (it.t0 + i) * kKT, slot = tiles % kSlots;
+        const unsigned none = *reinterpret_cast<volatile uint32_t*>(&info[slot].bad);
+        const bool masked = k0 + kKT > it.vmin, look = (e & 1) && (masked || none);
+        bool found = false;
+#pragma unroll 1
+        for (int k = 0; k < 128 / RPI; ++k) {
+          uint4 w[NB];
 #pragma unroll
-        for (int v = 0; v < NV; ++v) w[v] = src[v * 128];
-        if (e & 1) {
-          const int k0 = (it.t0 + i) * kKT, slot = tiles % kSlots;
-          const unsigned none = *reinterpret_cast<volatile uint32_t*>(&info[slot].bad);
-          const bool masked = k0 + kKT > it.vmin;
-          bool found = false;
-          if (masked || none) {
-            const int keys = it.nk - k0;
+          for (int v = 0; v < NB; ++v) w[v] = *reinterpret_cast<const uint4*>(src + k * (RPI * D) + (NB == 2 ? (v ^ pair) * 64 : 0));
+          if (look) {     // values that some row does not see: NaN to 0, all of what lies past the end or outside the cache
+            const int row = row0 + k * RPI;
+            const bool gone = row >= it.nk - k0 || (none >> (row / 16)) & 1;
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-              const int row = row0 + v * RPI;
-              if (row >= keys || (none >> (row / 16)) & 1) w[v] = make_uint4(0, 0, 0, 0);
+            for (int v = 0; v < NB; ++v) {
+              if (gone) w[v] = make_uint4(0, 0, 0, 0);
               if (masked && (any_nan4(w[v].x) || any_nan4(w[v].y) || any_nan4(w[v].z) || any_nan4(w[v].w))) {
                 found = true;
                 w[v].x = drop_nan4(w[v].x);
@@ -618,16 +632,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               }
             }
           }
-          found = __any_sync(0xFFFFFFFFu, found);
-          if (lane == 0) info[slot].poison[warp - kWConv] = found;
-        }
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          const uint4 lo = make_uint4(f16x2_of(w[v].x), f16x2_of_hi(w[v].x), f16x2_of(w[v].y), f16x2_of_hi(w[v].y));
-          const uint4 hi = make_uint4(f16x2_of(w[v].z), f16x2_of_hi(w[v].z), f16x2_of(w[v].w), f16x2_of_hi(w[v].w));
-          *reinterpret_cast<uint4*>(dst + v * RPI * 128 + o0) = odd ? hi : lo;
-          *reinterpret_cast<uint4*>(dst + v * RPI * 128 + o1) = odd ? lo : hi;
+          for (int v = 0; v < NB; ++v) {
+            uint8_t* o = dst + k * (RPI * 128) + (NB == 2 ? (v ^ pair) * kBoxBytes : 0);
+            *reinterpret_cast<uint4*>(o + out0) =
+                make_uint4(f16x2_of(w[v].x), f16x2_of_hi(w[v].x), f16x2_of(w[v].y), f16x2_of_hi(w[v].y));
+            *reinterpret_cast<uint4*>(o + out1) =
+                make_uint4(f16x2_of(w[v].z), f16x2_of_hi(w[v].z), f16x2_of(w[v].w), f16x2_of_hi(w[v].w));
+          }
         }
+        if (look) found = __any_sync(0xFFFFFFFFu, found);
+        if ((e & 1) && lane == 0) info[slot].poison[warp - kWConv] = found;
         fence_async_smem();
         __threadfence_block();
         __syncwarp();
@@ -644,7 +659,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     }
   } else {
     // ---- softmax ------------------------------------------------------------------------
-    regs_up<kRegsSoft>();
     const int j = (warp - kWSoft) >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lanes = uint32_t(quarter * 32) << 16;
@@ -728,38 +742,41 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_first[j]);
           }
-          // a group of 16 keys: factor of its scores, its largest score, how far that is above the reference
-          float ck[4], mx[4], d[4];
-          int ve[4];
+          if (cut || none) {   // places that this row does not see
+            uint64_t seen = n_vis - 64 * half >= 64 ? ~0ull : n_vis > 64 * half ? (1ull << (n_vis - 64 * half)) - 1 : 0ull;
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            uint32_t* x = &s[g >> 1][(g & 1) * 16];
-            if (cut) {
+            for (int g = 0; g < 4; ++g)
+              if ((none >> (4 * half + g)) & 1) seen &= ~(0xFFFFull << (16 * g));
+            const uint32_t seen2[2] = {uint32_t(seen), uint32_t(seen >> 32)};
 #pragma unroll
-              for (int y = 0; y < 16; ++y)
-                if (64 * half + 16 * g + y >= n_vis) x[y] = 0xFF800000u;
-            }
-            if (none) {
-              if ((none >> (4 * half + g)) & 1) {
+            for (int y = 0; y < 64; ++y)
+              if (!((seen2[y / 32] >> (y % 32)) & 1)) s[y / 32][y % 32] = 0xFF800000u;
+          }
+          // a group of keys: factor of its scores, its largest score, how far that is above the reference
+          constexpr int GK = 64 / NG, GB = 4 / NG;      // keys, scale bytes of a group
+          float ck[NG], mx[NG], d[NG];
+          int kb[NG], ve[NG];
+          float dm = -INFINITY, dy = -INFINITY;
 #pragma unroll
-                for (int y = 0; y < 16; ++y) x[y] = 0xFF800000u;
+          for (int g = 0; g < NG; ++g) {
+            kb[g] = int(kb4 >> (8 * GB * g)) & 255;
+            ve[g] = (int(vb4 >> (8 * GB * g)) & 255) - 127;
+            float a0 = -INFINITY, a1 = -INFINITY;
+#pragma unroll
+            for (int z = g * GK; z < (g + 1) * GK; z += 16) {
+              uint32_t* x = &s[z / 32][z % 32];
+#pragma unroll
+              for (int y = 0; y < 16; y += 4) {
+                a0 = max3(a0, __uint_as_float(x[y]), __uint_as_float(x[y + 1]));
+                a1 = max3(a1, __uint_as_float(x[y + 2]), __uint_as_float(x[y + 3]));
               }
             }
-            float a0 = max3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
-            float a1 = max3(__uint_as_float(x[3]), __uint_as_float(x[4]), __uint_as_float(x[5]));
-            a0 = max3(a0, __uint_as_float(x[6]), __uint_as_float(x[7]));
-            a1 = max3(a1, __uint_as_float(x[8]), __uint_as_float(x[9]));
-            a0 = max3(a0, __uint_as_float(x[10]), __uint_as_float(x[11]));
-            a1 = max3(a1, __uint_as_float(x[12]), __uint_as_float(x[13]));
-            a0 = max3(a0, __uint_as_float(x[14]), __uint_as_float(x[15]));
             mx[g] = fmaxf(a0, a1);
-            const int kb = int(kb4 >> (8 * g)) & 255;
-            ve[g] = (int(vb4 >> (8 * g)) & 255) - 127;
-            ck[g] = __uint_as_float(__float_as_uint(P.cm) + (uint32_t(min(max(ce + kb - 127, -100), 126)) << 23));
-            d[g] = above(mx[g], kb, ck[g], sr, kr, cr);
+            ck[g] = __uint_as_float(__float_as_uint(P.cm) + (uint32_t(min(max(ce + kb[g] - 127, -100), 126)) << 23));
+            d[g] = above(mx[g], kb[g], ck[g], sr, kr, cr);
+            dm = fmaxf(dm, d[g]);
+            dy = fmaxf(dy, d[g] + float(ve[g]));
           }
-          const float dm = fmaxf(fmaxf(d[0], d[1]), fmaxf(d[2], d[3]));
-          const float dy = fmaxf(fmaxf(d[0] + float(ve[0]), d[1] + float(ve[1])), fmaxf(d[2] + float(ve[2]), d[3] + float(ve[3])));
           const bool raise = have ? dm > kRaiseSum || dy > float(rv) + kRaiseOut : dm > -INFINITY;
           if (__any_sync(0xFFFFFFFFu, raise)) {
             float fl = 1.0f, fo = 1.0f;
@@ -768,14 +785,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               float nsr = sr, ncr = cr;
               int nkr = kr;
 #pragma unroll
-              for (int g = 0; g < 4; ++g)
-                if (d[g] > top) top = d[g], nsr = mx[g], ncr = ck[g], nkr = int(kb4 >> (8 * g)) & 255;
+              for (int g = 0; g < NG; ++g)
+                if (d[g] > top) top = d[g], nsr = mx[g], ncr = ck[g], nkr = kb[g];
               sr = nsr, cr = ncr, kr = nkr;
               m = sr * cr;
               float y = have ? float(rv) - top : -INFINITY;
 #pragma unroll
-              for (int g = 0; g < 4; ++g)
-                y = fmaxf(y, above(mx[g], int(kb4 >> (8 * g)) & 255, ck[g], sr, kr, cr) + float(ve[g]));
+              for (int g = 0; g < NG; ++g) y = fmaxf(y, above(mx[g], kb[g], ck[g], sr, kr, cr) + float(ve[g]));
               const int nrv = int(ceilf(fminf(fmaxf(y, -1000.0f), 1000.0f)));
               fl = have ? pf_ex2(-top) : 0.0f;
               fo = have ? pf_ex2(float(rv - nrv) - top) : 0.0f;
@@ -804,49 +820,47 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           const float ref = far ? 0.0f : m;
           if (__any_sync(0xFFFFFFFFu, far)) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              const int dk = kr - (int(kb4 >> (8 * g)) & 255);     // as above()
+            for (int g = 0; g < NG; ++g) {
+              const int dk = kr - kb[g];     // as above()
               const float fs = far ? -sr * pow2c(min(dk, 0)) : 0.0f, fx = far ? pow2c(min(-dk, 0)) : 1.0f;
               if (far && dk > 0) ck[g] = cr;
-              uint32_t* x = &s[g >> 1][(g & 1) * 16];
 #pragma unroll
-              for (int y = 0; y < 16; ++y) x[y] = __float_as_uint(fmaf(__uint_as_float(x[y]), fx, fs));
+              for (int y = g * GK; y < (g + 1) * GK; ++y)
+                s[y / 32][y % 32] = __float_as_uint(fmaf(__uint_as_float(s[y / 32][y % 32]), fx, fs));
             }
           }
-          const uint64_t r2 = pack2(-ref, -ref);
+          // A probability comes out in the units of O, 2^t times itself; what that makes of 16 at most is 2^15 at most,
+          // and below t = -60 it is 0 in f16 either way. The sum takes the 2^t back.
+          constexpr int SB = GK < 32 ? GK : 32;         // keys of one group in a row
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             uint32_t pb[16];
-            uint64_t sum[4];
 #pragma unroll
-            for (int hg = 0; hg < 2; ++hg) {
-              const int g = 2 * b + hg;
-              uint32_t* x = &s[b][hg * 16];
-              const uint64_t c2 = pack2(ck[g], ck[g]);
-              const float fv = pow2c(ve[g] - rv + int(kPBias));
-              const uint64_t f2 = pack2(fv, fv);
-              float e[16];
+            for (int u = 0; u < 32; u += SB) {
+              const int g = (32 * b + u) / GK;
+              const int t = min(max(ve[g] - rv + int(kPBias), -60), 126);
+              const uint64_t c2 = pack2(ck[g], ck[g]), r2 = pack2(float(t) - ref, float(t) - ref);
+              uint32_t* x = &s[b][u];
+              float e[SB];
 #pragma unroll
-              for (int y = 0; y < 16; y += 2)
+              for (int y = 0; y < SB; y += 2)
                 unpack2(fma2(pack2(__uint_as_float(x[y]), __uint_as_float(x[y + 1])), c2, r2), e[y], e[y + 1]);
 #pragma unroll
-              for (int y = 0; y < 16; ++y) e[y] = pf_ex2(e[y]);
+              for (int y = 0; y < SB; ++y) e[y] = pf_ex2(e[y]);
 #pragma unroll
-              for (int y = 0; y < 16; y += 2) {
-                float p0, p1;
-                unpack2(mul2(pack2(e[y], e[y + 1]), f2), p0, p1);
-                pb[hg * 8 + y / 2] = f16x2_bits(p0, p1);
-              }
+              for (int y = 0; y < SB; y += 2) pb[(u + y) / 2] = f16x2_bits(e[y], e[y + 1]);
+              uint64_t sum[4];
 #pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                const uint64_t v = add2(pack2(e[2 * z], e[2 * z + 1]), pack2(e[2 * z + 8], e[2 * z + 9]));
-                sum[z] = hg ? add2(sum[z], v) : v;
-              }
+              for (int z = 0; z < 4; ++z) sum[z] = add2(pack2(e[2 * z], e[2 * z + 1]), pack2(e[2 * z + 8], e[2 * z + 9]));
+#pragma unroll
+              for (int y = 16; y < SB; y += 8)
+#pragma unroll
+                for (int z = 0; z < 4; ++z) sum[z] = add2(sum[z], pack2(e[y + 2 * z], e[y + 2 * z + 1]));
+              float a0, a1;
+              unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a0, a1);
+              l = fmaf(a0 + a1, pow2c(-t), l);
             }
             tmem_st16(ta + 32 * half + 16 * b, pb);
-            float a0, a1;
-            unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a0, a1);
-            l += a0 + a1;
           }
           if (half == 0) tmem_wait_st();
         }
@@ -951,8 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 
 // Joins the parts of an item that was cut, in order of position: block (c, x)
 // channels 4 x .. 4 x + 3 of the item that begins in CTA c and ends in a later one,
-// thread = row. References are those of the part with the largest; parts are read
-// coalesced over the rows.
+// thread = row, so parts are read coalesced over the rows.
 template <int D>
 __global__ void __launch_bounds__(256) chunk_join_kernel(const Params P) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -963,33 +976,38 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const Params P) {
   int last = c + 1;                // the last CTA with a part
   while (P.desc[last].first & 2) ++last;
   auto slot = [&](int k) { return P.parts + (size_t)(k == c ? 2 * c + 1 : 2 * k) * kSlot + row; };
-  // the part with the largest reference
-  float m = -INFINITY, sr = 0.0f, cr = 0.0f;
+  // the parts one after another, four on their way at once; so far: reference sr, kr, cr, sum l in its units, outputs o
+  // and their reference rm above it
+  float sr = 0.0f, cr = 0.0f, l = 0.0f, rm = -INFINITY;
   int kr = 0;
-  for (int k = c; k <= last; ++k) {
-    const float4 h = slot(k)[(size_t)(D / 4) * 256];
-    if (h.z != 0.0f && !(h.x * h.y <= m)) m = h.x * h.y, sr = h.x, cr = h.y, kr = __float_as_int(h.w) & 255;
-  }
-  float l = 0.0f, rm = -INFINITY;
-  for (int k = c; k <= last; ++k) {
-    const float4 h = slot(k)[(size_t)(D / 4) * 256];
-    const int kb = __float_as_int(h.w) & 255, rv = __float_as_int(h.w) >> 8;
-    const float up = above(h.x, kb, h.y, sr, kr, cr);
-    if (h.z != 0.0f) {
-      l += h.z * pf_ex2(up);
-      rm = fmaxf(rm, up + float(rv));
-    }
-  }
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int k = c; k <= last; ++k) {
-    const float4 h = slot(k)[(size_t)(D / 4) * 256], v = slot(k)[(size_t)x * 256];
-    const int kb = __float_as_int(h.w) & 255, rv = __float_as_int(h.w) >> 8;
-    const float up = above(h.x, kb, h.y, sr, kr, cr);
-    if (h.z != 0.0f) {
-      const float f = pf_ex2(up + float(rv) - rm);
-      o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+  for (int k0 = c; k0 <= last; k0 += 4) {
+    float4 h[4], v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      h[i] = k0 + i <= last ? slot(k0 + i)[(size_t)(D / 4) * 256] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      v[i] = k0 + i <= last ? slot(k0 + i)[(size_t)x * 256] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (h[i].z == 0.0f) continue;            // nothing seen there
+      const int kb = __float_as_int(h[i].w) & 255, rv = __float_as_int(h[i].w) >> 8;
+      float up = l == 0.0f ? 0.0f : above(h[i].x, kb, h[i].y, sr, kr, cr);
+      float f = 1.0f;                          // of what is there
+      if (l == 0.0f || up > 0.0f) {
+        f = l == 0.0f ? 0.0f : pf_ex2(-up);
+        rm -= up;
+        sr = h[i].x, kr = kb, cr = h[i].y;
+        up = 0.0f;
+      }
+      l = fmaf(h[i].z, pf_ex2(up), l * f);
+      const float r = up + float(rv), rn = fmaxf(rm, r), fo = rm == -INFINITY ? 0.0f : pf_ex2(rm - rn), fv = pf_ex2(r - rn);
+      o.x = fmaf(v[i].x, fv, o.x * fo), o.y = fmaf(v[i].y, fv, o.y * fo);
+      o.z = fmaf(v[i].z, fv, o.z * fo), o.w = fmaf(v[i].w, fv, o.w * fo);
+      rm = rn;
     }
   }
+  const float m = sr * cr;
   const int G = P.G, r = d.r0 + row;
   const int64_t orow = (int64_t)(d.q0 + r / G) * P.a.n_heads + d.hk * G + r % G;
   const float inv = 1.0f / l, f = pf_ex2(0.5f * (rm - kPBias));
@@ -999,12 +1017,12 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const Params P) {
   if (x == 0 && P.a.lse) P.a.lse[orow] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2f;
 }
 
-template <int D>
+template <int D, int NG>
 int launch_chunk(const Params& P, int grid, const DeviceInfo& di, cudaStream_t s) {
   constexpr uint32_t smem = Plan<D>::kTotal;
   if (smem > di.smem_optin) return MOE_ERR_UNSUPPORTED_SHAPE;
-  MOE_CUDA_TRY(cudaFuncSetAttribute(chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
-  chunk_kernel<D><<<grid, kThreads, smem, s>>>(P);
+  MOE_CUDA_TRY(cudaFuncSetAttribute(chunk_kernel<D, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
+  chunk_kernel<D, NG><<<grid, kThreads, smem, s>>>(P);
   if (grid > 1) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid - 1, D / 4);
@@ -1043,9 +1061,17 @@ int launch_attn_chunk(const ChunkArgs& a, const DeviceInfo& di, cudaStream_t s) 
     P.ce = -1000;
   }
   P.negate = a.scale < 0.0f;
+  // work is counted in 64 bits: items times positions and heads of a group
+  const double items = double(a.total_q) * P.G / 256 + a.n_seq;
+  if (items * a.c.n_kv_heads * P.G * (double(a.width) * a.c.page_size + 1024) > 4e18) return MOE_ERR_UNSUPPORTED_SHAPE;
   P.desc = static_cast<Desc*>(a.ws);
   P.parts = reinterpret_cast<float4*>(static_cast<char*>(a.ws) + desc_bytes(di));
-  return a.c.head_dim == 128 ? launch_chunk<128>(P, di.sm_count, di, s) : launch_chunk<64>(P, di.sm_count, di, s);
+  const int ng = a.c.page_size == 16 ? 4 : a.c.page_size == 32 ? 2 : 1;
+  if (a.c.head_dim == 128)
+    return ng == 4 ? launch_chunk<128, 4>(P, di.sm_count, di, s)
+                   : ng == 2 ? launch_chunk<128, 2>(P, di.sm_count, di, s) : launch_chunk<128, 1>(P, di.sm_count, di, s);
+  return ng == 4 ? launch_chunk<64, 4>(P, di.sm_count, di, s)
+                 : ng == 2 ? launch_chunk<64, 2>(P, di.sm_count, di, s) : launch_chunk<64, 1>(P, di.sm_count, di, s);
 }
 
 }  // namespace moe
