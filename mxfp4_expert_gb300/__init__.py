@@ -838,6 +838,9 @@ def moe_kv_evict_fp8(cache: KVCache, page_table: torch.Tensor, lengths: torch.Te
 
 def _mat(t, dtype, name, dev, shape):
     """Address and row stride of a [T, d] tensor of that type whose rows are contiguous."""
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == shape
+            and t.is_contiguous()):
+        return t.data_ptr(), shape[1]
     if not (isinstance(t, _Tensor) and t.is_cuda):
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype is not dtype:

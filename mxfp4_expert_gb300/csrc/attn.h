@@ -44,7 +44,7 @@ struct RopeArgs {
   __nv_bfloat16* q_out;          // [total][n_heads][D]
   int n_heads, rot, interleaved;
 };
-int launch_kv_append_rope(const RopeArgs& a, cudaStream_t s);
+int launch_kv_append_rope(const RopeArgs& a, const DeviceInfo& di, cudaStream_t s);
 
 struct ChunkArgs {
   moe_kv_cache c;

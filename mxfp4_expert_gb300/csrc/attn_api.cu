@@ -171,7 +171,7 @@ extern "C" int moe_kv_append_rope_fp8(const moe_kv_cache* cache, const moe_rows*
   a.rope_start = rope_start_dev ? rope_start_dev : start_dev;
   a.rot = rot_dim;
   a.interleaved = interleaved;
-  return launch_kv_append_rope(a, (cudaStream_t)stream);
+  return launch_kv_append_rope(a, di, (cudaStream_t)stream);
 }
 
 static int check_chunk_shape(const moe_kv_cache* c, int n_heads, int n_seq, int total_q) {

@@ -7,11 +7,12 @@
 // p 2^-64 whatever p is. Its top 32 bits give quadrant and remainder, cosine and
 // sine of the remainder are their Taylor series.
 //
-// A CTA takes one page's new tokens: the cosines and sines of all of them into
-// shared memory, then of one key or value head the values into registers, their
-// maximum, the page's scale and the codes (as append_kernel, which has no
-// rotation), or several query heads one after another. Bound by HBM: 3 bytes a
-// key or value, 4 a query's channel.
+// A CTA takes one page's new tokens and a few heads, of keys, values or queries: the
+// cosines and sines of all the tokens into shared memory once, then head after head,
+// the next one's channels on their way meanwhile. A thread holds both halves of its
+// pairs. Of a key or value head the maximum, the page's scale and the codes as
+// append_kernel makes them, which has no rotation. Bound by HBM: 3 bytes a key or
+// value, 4 a query's channel.
 #include <algorithm>
 
 #include "attn.h"
@@ -22,7 +23,7 @@ namespace moe {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeQHeads = 4;      // query heads a CTA rotates
+constexpr int kRopeCtas = 6;        // CTAs an SM before heads share one
 
 // cos and sin of s 2^-32 turns.
 __device__ __forceinline__ float2 turn(uint32_t s) {
@@ -35,206 +36,364 @@ __device__ __forceinline__ float2 turn(uint32_t s) {
   return make_float2(((quad + 1) & 2) ? -a : a, (quad & 2) ? -b : b);
 }
 
-// Eight rotated channels at column col of a row: w, and where pairs lie r / 2
-// apart the other halves' channels o; cs: the row's cosines and sines.
-__device__ __forceinline__ void rotate8(const uint4& w, const uint4& o, const float2* cs, int col, int rot,
-                                        bool interleaved, float (&y)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w}, p[4] = {o.x, o.y, o.z, o.w};
-  if (col >= rot) {
+// Sixteen channels of a row, of eight pairs that t turns; kind 0: not turned, 1:
+// pair i is channel i of both vectors, 2: neighbours.
+__device__ __forceinline__ void turn16(const uint4& w0, const uint4& w1, const float2* t, int kind, float (&y)[16]) {
+  const uint32_t u[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+  if (kind == 0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       y[2 * i] = bf16_lo(u[i]);
       y[2 * i + 1] = bf16_hi(u[i]);
     }
-  } else if (interleaved) {
+    return;
+  }
+  const float4* t4 = reinterpret_cast<const float4*>(t);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 t = cs[col / 2 + i];
-      const float a = bf16_lo(u[i]), b = bf16_hi(u[i]);
-      y[2 * i] = a * t.x - b * t.y;
-      y[2 * i + 1] = b * t.x + a * t.y;
-    }
-  } else {
-    const bool second = col >= rot / 2;
-    const float2* c = cs + (second ? col - rot / 2 : col);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 t = c[2 * i], t2 = c[2 * i + 1];
-      y[2 * i] = bf16_lo(u[i]) * t.x + (second ? bf16_lo(p[i]) : -bf16_lo(p[i])) * t.y;
-      y[2 * i + 1] = bf16_hi(u[i]) * t2.x + (second ? bf16_hi(p[i]) : -bf16_hi(p[i])) * t2.y;
+  for (int i = 0; i < 4; ++i) {
+    const float4 c = t4[i];          // pairs 2 i and 2 i + 1
+    if (kind == 1) {
+      const float a0 = bf16_lo(u[i]), a1 = bf16_hi(u[i]), b0 = bf16_lo(u[4 + i]), b1 = bf16_hi(u[4 + i]);
+      y[2 * i] = a0 * c.x - b0 * c.y;
+      y[2 * i + 1] = a1 * c.z - b1 * c.w;
+      y[8 + 2 * i] = b0 * c.x + a0 * c.y;
+      y[8 + 2 * i + 1] = b1 * c.z + a1 * c.w;
+    } else {
+      const float a0 = bf16_lo(u[2 * i]), b0 = bf16_hi(u[2 * i]), a1 = bf16_lo(u[2 * i + 1]), b1 = bf16_hi(u[2 * i + 1]);
+      y[4 * i] = a0 * c.x - b0 * c.y;
+      y[4 * i + 1] = b0 * c.x + a0 * c.y;
+      y[4 * i + 2] = a1 * c.z - b1 * c.w;
+      y[4 * i + 3] = b1 * c.z + a1 * c.w;
     }
   }
 }
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 
-// NV = vectors of 8 channels a thread holds: page_size * head_dim / 8 / kRopeThreads, at least 1.
-template <int NV>
-__global__ void __launch_bounds__(kRopeThreads) append_rope_kernel(const RopeArgs a) {
+// find_block by the whole CTA: a sequence a thread, so one round of loads for up to
+// kRopeThreads of them. Ends with a barrier.
+__device__ __forceinline__ Block find_block_cta(const AppendArgs& a, int x, bool* bad) {
+  __shared__ int s_warp[kRopeThreads / 32];
+  __shared__ Block s_blk;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, P = a.c.page_size;
+  if (tid == 0) s_blk.b = -1;
+  int before = 0;
+  for (int b0 = 0; b0 < a.n_seq; b0 += kRopeThreads) {
+    const int b = b0 + tid;
+    int c0 = 0, c1 = 0, start = 0, n = 0;
+    if (b < a.n_seq) {
+      start = __ldg(a.start + b);
+      packed_range(a.cu, b, a.total, &c0, &c1, bad);
+      if (start < 0 || start > 0x7FFFFFFF - (c1 - c0)) {
+        *bad = true;
+        c1 = c0;
+      }
+      if (c1 > c0) n = (start + (c1 - c0) - 1) / P - start / P + 1;
+    }
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    int lo = before + incl - n, all = before;
+#pragma unroll
+    for (int i = 0; i < kRopeThreads / 32; ++i) {
+      lo += i < warp ? s_warp[i] : 0;
+      all += s_warp[i];
+    }
+    if (x >= lo && x < lo + n) {
+      const int blk = start / P + (x - lo);
+      const int64_t p0 = (int64_t)blk * P, end = (int64_t)start + (c1 - c0);
+      const int s0 = start > p0 ? int(start - p0) : 0;
+      s_blk = Block{b, blk, s0, end < p0 + P ? int(end - p0) : P, c0 + int(p0 + s0 - start)};
+    }
+    before = all;
+    __syncthreads();
+    if (x < before) break;       // found; the last CTA looks at every sequence
+  }
+  return s_blk;
+}
+// Phase of a frequency per position, in 2^-64 turns.
+__device__ __forceinline__ uint64_t turns_of(float inv_freq) {
+  double turns = double(inv_freq) * 0.15915494309189533577;
+  turns -= floor(turns);
+  return uint64_t(turns * 18446744073709551616.0);
+}
+// Cosines and sines of a page's new tokens, for the caller's barrier.
+__device__ __forceinline__ void fill_angles(const RopeArgs& a, const Block& f, uint64_t F, float2* cs) {
+  const int half = a.rot / 2, j = threadIdx.x % half, first = threadIdx.x / half, step = kRopeThreads / half;
+  if (first >= step) return;
+  const int64_t p0 = (int64_t)__ldg(a.rope_start + f.b) + ((int64_t)f.blk * a.ap.c.page_size + f.s0 - __ldg(a.ap.start + f.b));
+  uint64_t at = uint64_t(p0 + first) * F;
+  const uint64_t by = uint64_t(step) * F;
+  for (int t = first; t < f.s1 - f.s0; t += step, at += by) cs[t * half + j] = turn(uint32_t(at >> 32));
+}
+__device__ __forceinline__ void store_bf16(__nv_bfloat16* o, int c0, int c1, const float (&y)[16]) {
+  *reinterpret_cast<uint4*>(o + c0) = make_uint4(bf16x2(y[0], y[1]), bf16x2(y[2], y[3]), bf16x2(y[4], y[5]), bf16x2(y[6], y[7]));
+  *reinterpret_cast<uint4*>(o + c1) =
+      make_uint4(bf16x2(y[8], y[9]), bf16x2(y[10], y[11]), bf16x2(y[12], y[13]), bf16x2(y[14], y[15]));
+}
+// Largest finite magnitude's bits; *nonfinite if some are not.
+__device__ __forceinline__ uint32_t largest(const float (&y)[16], bool* nonfinite) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(y[e]) & 0x7FFFFFFFu);
+  if (top >= 0x7F800000u) {
+    *nonfinite = true;
+    top = 0;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const uint32_t m = __float_as_uint(y[e]) & 0x7FFFFFFFu;
+      if (m < 0x7F800000u) top = max(top, m);
+    }
+  }
+  return top;
+}
+// 2^(127 - byte); 2^-127 and 2^-128 are subnormal
+__device__ __forceinline__ float code_factor(int byte) {
+  return byte <= 253 ? pow2(127 - byte) : __uint_as_float(0x00800000u >> (byte - 253));
+}
+__device__ __forceinline__ void store_codes(uint8_t* o, int c0, int c1, const float (&y)[16], float f, bool nonfinite) {
+  uint32_t q[4];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float lo = y[2 * j] * f, hi = y[2 * j + 1] * f;
+    if (nonfinite) {   // inf takes the code of NaN: there is none for it
+      if (!(fabsf(y[2 * j]) <= 3.4028235e38f)) lo = __int_as_float(0x7FC00000);
+      if (!(fabsf(y[2 * j + 1]) <= 3.4028235e38f)) hi = __int_as_float(0x7FC00000);
+    }
+    const uint32_t c = f32x2_to_e4m3x2(lo, hi);
+    q[j >> 1] = j & 1 ? q[j >> 1] | c << 16 : c;
+  }
+  *reinterpret_cast<uint2*>(o + c0) = make_uint2(q[0], q[1]);
+  *reinterpret_cast<uint2*>(o + c1) = make_uint2(q[2], q[3]);
+}
+// The CTA: a part-filled page's older codes, in units of the new scale.
+__device__ __forceinline__ void rescale_codes(uint8_t* codes, int n, float f) {
+  for (int v = threadIdx.x; v < n / 16; v += kRopeThreads) {
+    uint4* p = reinterpret_cast<uint4*>(codes) + v;
+    uint4 c = *p;
+    c.x = kv_rescale4(c.x, f);
+    c.y = kv_rescale4(c.y, f);
+    c.z = kv_rescale4(c.z, f);
+    c.w = kv_rescale4(c.w, f);
+    *p = c;
+  }
+}
+
+// Few new tokens a page, one mostly (a decode step): a CTA takes all heads of a
+// page's tokens, D / 16 neighbouring lanes a head. Right for any number of tokens,
+// which are read once more where there are several.
+__global__ void __launch_bounds__(kRopeThreads) append_rope_few_kernel(const RopeArgs a) {
   extern __shared__ __align__(16) float2 s_cs[];        // [tokens][rot / 2]
-  __shared__ Block sblk;
-  __shared__ int smax[kRopeThreads / 32], sbad[kRopeThreads / 32];
+  __shared__ uint8_t s_grown[2][1024];                  // of a key or value head whose scale has grown: the bytes before
+  __shared__ int s_any;
   const AppendArgs& ap = a.ap;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (warp == 0) {
-    bool bad = false;
-    const Block f = find_block(ap, int(blockIdx.x), &bad);
-    bad = __any_sync(0xFFFFFFFFu, bad);
-    if (lane == 0) {
-      sblk = f;
-      if (bad && ap.status) atomicOr(ap.status, MOE_DEV_INDEX_OOB);
+  const int tid = threadIdx.x;
+  const int P = ap.c.page_size, D = ap.c.head_dim, H = ap.c.n_kv_heads, half = a.rot / 2;
+  if (tid == 0) s_any = 0;
+  const uint64_t F = tid / half < kRopeThreads / half ? turns_of(__ldg(a.inv_freq + tid % half)) : 0;
+  bool bad = false;
+  const Block f = find_block_cta(ap, int(blockIdx.x), &bad);
+  if (bad && ap.status) atomicOr(ap.status, MOE_DEV_INDEX_OOB);
+  if (f.b < 0) return;
+  const int tokens = f.s1 - f.s0, upr = D / 16, u = tid % upr, step = kRopeThreads / upr, all = 2 * H + (a.q ? a.n_heads : 0);
+  int page = f.blk < ap.width ? __ldg(ap.table + (size_t)f.b * ap.width + f.blk) : -1;
+  fill_angles(a, f, F, s_cs);
+  __syncthreads();
+  if (page < 0 || page >= ap.c.n_pages) {
+    if (tid == 0 && ap.status) atomicOr(ap.status, MOE_DEV_INDEX_OOB);
+    page = -1;
+  }
+  for (int g0 = 0; g0 < all; g0 += step) {
+    const int g = g0 + tid / upr, role = g < H ? 0 : g < 2 * H ? 1 : 2, h = g - role * H;
+    const bool in = g < all && (role == 2 || page >= 0);
+    const int rot = role == 1 ? 0 : a.rot, kind = 16 * u >= rot ? 0 : a.interleaved ? 2 : 1;
+    const int c0 = kind == 1 ? 8 * u : 16 * u, c1 = c0 + (kind == 1 ? half : 8);
+    const __nv_bfloat16* src = role == 0 ? ap.k + h * ap.k_hs : role == 1 ? ap.v + h * ap.v_hs : a.q + h * a.q_hs;
+    const int64_t ts = role == 0 ? ap.k_ts : role == 1 ? ap.v_ts : a.q_ts;
+    float y[16];
+    auto load = [&](int t) {
+      const __nv_bfloat16* p = src + (int64_t)(f.t0 + t) * ts;
+      turn16(*reinterpret_cast<const uint4*>(p + c0), *reinterpret_cast<const uint4*>(p + c1), s_cs + t * half + 8 * u, kind, y);
+    };
+    uint32_t top = 0;
+    bool nonfinite = false;
+    if (in)
+      for (int t = 0; t < tokens; ++t) {
+        load(t);
+        if (role == 2) store_bf16(a.q_out + ((int64_t)(f.t0 + t) * a.n_heads + h) * D, c0, c1, y);
+        else top = max(top, largest(y, &nonfinite));
+      }
+    for (int o = 1; o < upr; o <<= 1) {
+      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      nonfinite |= __shfl_xor_sync(0xFFFFFFFFu, int(nonfinite), o) != 0;
+    }
+    if (!in || role == 2) continue;
+    uint8_t* codes = static_cast<uint8_t*>(role ? ap.c.v_codes : ap.c.k_codes) + ((size_t)page * H + h) * P * D;
+    uint8_t* scale = (role ? ap.c.v_scales : ap.c.k_scales) + (size_t)page * H + h;
+    const int had = f.s0 > 0 ? int(*scale) : 0, byte = max(kv_scale_byte(__uint_as_float(top)), had);
+    for (int t = 0; t < tokens; ++t) {
+      if (tokens > 1) load(t);
+      store_codes(codes + (f.s0 + t) * D, c0, c1, y, code_factor(byte), nonfinite);
+    }
+    __syncwarp(((1u << upr) - 1) << ((tid & 31) & ~(upr - 1)));     // the head's lanes have read the old scale
+    if (u == 0) {
+      *scale = uint8_t(byte);
+      if (nonfinite && ap.status) atomicOr(ap.status, MOE_DEV_NONFINITE_INPUT);
+      if (f.s0 > 0) s_grown[role][h] = uint8_t(had);
+      if (f.s0 > 0 && byte > had) s_any = 1;
     }
   }
   __syncthreads();
-  const Block f = sblk;
-  if (f.b < 0) return;
-  const int P = ap.c.page_size, D = ap.c.head_dim, H = ap.c.n_kv_heads, role = blockIdx.y;
-  const bool is_q = role >= 2 * H, is_v = !is_q && role >= H;
-  const int rot = is_v ? 0 : a.rot, half = rot / 2, tokens = f.s1 - f.s0;
-  const int cpr = D / 8, n = tokens * cpr;              // vectors per row; of the new rows
-  const int row = tid / cpr, col = (tid % cpr) * 8, rows = kRopeThreads / cpr;
-  // where the other halves of the pairs are
-  const int other = a.interleaved || col >= rot ? 0 : col >= half ? -half : half;
-  const __nv_bfloat16* src;
-  int64_t ts;
-  int h = is_q ? (role - 2 * H) * kRopeQHeads : is_v ? role - H : role;
-  if (is_q) src = a.q, ts = a.q_ts;
-  else if (is_v) src = ap.v + h * ap.v_hs, ts = ap.v_ts;
-  else src = ap.k + h * ap.k_hs, ts = ap.k_ts;
-
-  if (rot) {   // cosines and sines of the page's new tokens; a thread keeps its frequency
-    const int j = tid % half, first = tid / half, step = kRopeThreads / half;
-    if (first < step) {
-      const int64_t p0 = (int64_t)__ldg(a.rope_start + f.b) + ((int64_t)f.blk * P + f.s0 - __ldg(ap.start + f.b));
-      double turns = double(__ldg(a.inv_freq + j)) * 0.15915494309189533577;
-      turns -= floor(turns);
-      const uint64_t F = uint64_t(turns * 18446744073709551616.0);
-      for (int t = first; t < tokens; t += step) s_cs[t * half + j] = turn(uint32_t((uint64_t(p0 + t) * F) >> 32));
-    }
-    __syncthreads();
+  if (f.s0 == 0 || page < 0 || !s_any) return;
+  for (int g = 0; g < 2 * H; ++g) {
+    const int role = g >= H, h = g - role * H, had = s_grown[role][h];
+    const int byte = (role ? ap.c.v_scales : ap.c.k_scales)[(size_t)page * H + h];
+    if (byte > had)
+      rescale_codes(static_cast<uint8_t*>(role ? ap.c.v_codes : ap.c.k_codes) + ((size_t)page * H + h) * P * D, f.s0 * D,
+                    kv_factor(had, byte));
   }
+}
 
-  if (is_q) {
-    const int h1 = min(h + kRopeQHeads, a.n_heads);
-    for (; h < h1; ++h) {
-      const __nv_bfloat16* s = src + h * a.q_hs;
+// NU = units of 16 channels a thread holds: page_size * head_dim / 16 / kRopeThreads,
+// at least 1. kRole: 0 keys, 1 values, 2 queries; gridDim.y counts groups of `heads`.
+template <int NU>
+__global__ void __launch_bounds__(kRopeThreads, NU == 4 ? 2 : NU == 2 ? 3 : 4) append_rope_kernel(const RopeArgs a, int heads, int k_groups) {
+  extern __shared__ __align__(16) float2 s_cs[];        // [tokens][rot / 2]
+  __shared__ int smax[2][kRopeThreads / 32], sbad[2][kRopeThreads / 32];
+  const AppendArgs& ap = a.ap;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int P = ap.c.page_size, D = ap.c.head_dim, H = ap.c.n_kv_heads;
+  const int group = blockIdx.y, role = group < k_groups ? 0 : group < 2 * k_groups ? 1 : 2;
+  const int rot = role == 1 ? 0 : a.rot, half = rot / 2;
+  const uint64_t F = rot && tid / half < kRopeThreads / half ? turns_of(__ldg(a.inv_freq + tid % half)) : 0;
+  bool bad = false;
+  const Block f = find_block_cta(ap, int(blockIdx.x), &bad);
+  if (bad && ap.status) atomicOr(ap.status, MOE_DEV_INDEX_OOB);
+  if (f.b < 0) return;
+  const int tokens = f.s1 - f.s0, upr = D / 16, n = tokens * upr;   // units per row; of the new rows
+  const int row0 = tid / upr, u = tid % upr, rows = kRopeThreads / upr;
+  const int kind = 16 * u >= rot ? 0 : a.interleaved ? 2 : 1;
+  const int c0 = kind == 1 ? 8 * u : 16 * u, c1 = c0 + (kind == 1 ? half : 8);
+  int h = (group - role * k_groups) * heads;
+  const int h1 = min(h + heads, role == 2 ? a.n_heads : H);
+  const __nv_bfloat16* src = role == 0 ? ap.k : role == 1 ? ap.v : a.q;
+  const int64_t ts = role == 0 ? ap.k_ts : role == 1 ? ap.v_ts : a.q_ts, hs = role == 0 ? ap.k_hs : role == 1 ? ap.v_hs : a.q_hs;
+
+  uint4 x[NU][2];
+  auto fetch = [&](int head) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int r = row + i * rows;
-        if (i * kRopeThreads + tid >= n) break;
-        const __nv_bfloat16* p = s + (int64_t)(f.t0 + r) * ts + col;
-        const uint4 w = *reinterpret_cast<const uint4*>(p), o = *reinterpret_cast<const uint4*>(p + other);
-        float y[8];
-        rotate8(w, o, s_cs + r * half, col, rot, a.interleaved, y);
-        uint32_t b[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b[e]) : "f"(y[2 * e + 1]), "f"(y[2 * e]));
-        *reinterpret_cast<uint4*>(a.q_out + ((int64_t)(f.t0 + r) * a.n_heads + h) * D + col) =
-            make_uint4(b[0], b[1], b[2], b[3]);
+    for (int i = 0; i < NU; ++i) {
+      x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
+      if (i * kRopeThreads + tid < n) {
+        const __nv_bfloat16* p = src + (int64_t)(f.t0 + row0 + i * rows) * ts + head * hs;
+        x[i][0] = *reinterpret_cast<const uint4*>(p + c0);
+        x[i][1] = *reinterpret_cast<const uint4*>(p + c1);
       }
     }
-    return;
+  };
+  fetch(h);
+  const int page = role < 2 && f.blk < ap.width ? __ldg(ap.table + (size_t)f.b * ap.width + f.blk) : -1;
+  if (rot) {
+    fill_angles(a, f, F, s_cs);
+    __syncthreads();
   }
-
-  const int page = f.blk < ap.width ? __ldg(ap.table + (size_t)f.b * ap.width + f.blk) : -1;
-  float y[NV][8];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int r = row + i * rows;
-    if (i * kRopeThreads + tid < n) {
-      const __nv_bfloat16* p = src + (int64_t)(f.t0 + r) * ts + col;
-      const uint4 w = *reinterpret_cast<const uint4*>(p), o = *reinterpret_cast<const uint4*>(p + other);
-      rotate8(w, o, s_cs + r * half, col, rot, a.interleaved, y[i]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[i][e] = 0.0f;
-    }
-  }
-  if (page < 0 || page >= ap.c.n_pages) {
+  if (role < 2 && (page < 0 || page >= ap.c.n_pages)) {
     if (tid == 0 && ap.status) atomicOr(ap.status, MOE_DEV_INDEX_OOB);
     return;
   }
-  uint8_t* codes = static_cast<uint8_t*>(is_v ? ap.c.v_codes : ap.c.k_codes) + ((size_t)page * H + h) * P * D;
-  uint8_t* scale = (is_v ? ap.c.v_scales : ap.c.k_scales) + (size_t)page * H + h;
-  const int had = f.s0 > 0 ? int(*scale) : 0;
-  uint32_t top = 0;            // the largest finite magnitude's bits
-  bool nonfinite = false;
+
+  for (int k = 0; h < h1; ++h, k ^= 1) {
+    float y[NU][16];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NU; ++i)     // a thread without a unit has zeros, and no angles of its own
+      turn16(x[i][0], x[i][1], s_cs + (row0 + i * rows) * half + 8 * u, i * kRopeThreads + tid < n ? kind : 0, y[i]);
+    if (h + 1 < h1) fetch(h + 1);
+    if (role == 2) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t m = __float_as_uint(y[i][e]) & 0x7FFFFFFFu;
-      const bool inf = m >= 0x7F800000u;
-      nonfinite |= inf;
-      top = max(top, inf ? 0u : m);
-    }
-  nonfinite = __any_sync(0xFFFFFFFFu, nonfinite);
-  top = __reduce_max_sync(0xFFFFFFFFu, top);
-  if (lane == 0) {
-    smax[warp] = int(top);
-    sbad[warp] = nonfinite;
-  }
-  __syncthreads();   // also: everyone has read the old scale
-#pragma unroll
-  for (int i = 0; i < kRopeThreads / 32; ++i) {
-    top = max(top, uint32_t(smax[i]));
-    nonfinite |= sbad[i] != 0;
-  }
-  const int byte = max(kv_scale_byte(__uint_as_float(top)), had);
-  if (tid == 0) {
-    *scale = uint8_t(byte);
-    if (nonfinite && ap.status) atomicOr(ap.status, MOE_DEV_NONFINITE_INPUT);
-  }
-  // 2^(127 - byte); 2^-127 and 2^-128 are subnormal
-  const float f1 = byte <= 253 ? pow2(127 - byte) : __uint_as_float(0x00800000u >> (byte - 253));
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if (i * kRopeThreads + tid >= n) break;
-    uint32_t q[2] = {0, 0};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float lo = y[i][2 * j] * f1, hi = y[i][2 * j + 1] * f1;
-      if (nonfinite) {   // inf takes the code of NaN: there is none for it
-        if (!(fabsf(y[i][2 * j]) <= 3.4028235e38f)) lo = __int_as_float(0x7FC00000);
-        if (!(fabsf(y[i][2 * j + 1]) <= 3.4028235e38f)) hi = __int_as_float(0x7FC00000);
+      for (int i = 0; i < NU; ++i) {
+        if (i * kRopeThreads + tid >= n) break;
+        store_bf16(a.q_out + ((int64_t)(f.t0 + row0 + i * rows) * a.n_heads + h) * D, c0, c1, y[i]);
       }
-      q[j >> 1] |= uint32_t(f32x2_to_e4m3x2(lo, hi)) << (16 * (j & 1));
+      continue;
     }
-    *reinterpret_cast<uint2*>(codes + (f.s0 + row + i * rows) * D + col) = make_uint2(q[0], q[1]);
-  }
-  if (byte > had && f.s0 > 0) {   // older codes, in units of the new scale
-    const float fo = kv_factor(had, byte);
-    for (int v = tid; v < f.s0 * D / 16; v += kRopeThreads) {
-      uint4* p = reinterpret_cast<uint4*>(codes) + v;
-      uint4 c = *p;
-      c.x = kv_rescale4(c.x, fo);
-      c.y = kv_rescale4(c.y, fo);
-      c.z = kv_rescale4(c.z, fo);
-      c.w = kv_rescale4(c.w, fo);
-      *p = c;
+    uint8_t* codes = static_cast<uint8_t*>(role ? ap.c.v_codes : ap.c.k_codes) + ((size_t)page * H + h) * P * D;
+    uint8_t* scale = (role ? ap.c.v_scales : ap.c.k_scales) + (size_t)page * H + h;
+    const int had = f.s0 > 0 ? int(*scale) : 0;
+    uint32_t top = 0;
+    bool nonfinite = false;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) top = max(top, largest(y[i], &nonfinite));
+    nonfinite = __any_sync(0xFFFFFFFFu, nonfinite);
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if (lane == 0) {
+      smax[k][warp] = int(top);
+      sbad[k][warp] = nonfinite;
     }
+    __syncthreads();   // also: everyone has read the old scale
+#pragma unroll
+    for (int i = 0; i < kRopeThreads / 32; ++i) {
+      top = max(top, uint32_t(smax[k][i]));
+      nonfinite |= sbad[k][i] != 0;
+    }
+    const int byte = max(kv_scale_byte(__uint_as_float(top)), had);
+    if (tid == 0) {
+      *scale = uint8_t(byte);
+      if (nonfinite && ap.status) atomicOr(ap.status, MOE_DEV_NONFINITE_INPUT);
+    }
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      if (i * kRopeThreads + tid >= n) break;
+      store_codes(codes + (f.s0 + row0 + i * rows) * D, c0, c1, y[i], code_factor(byte), nonfinite);
+    }
+    if (byte > had && f.s0 > 0) rescale_codes(codes, f.s0 * D, kv_factor(had, byte));
   }
 }
 
 }  // namespace
 
-int launch_kv_append_rope(const RopeArgs& a, cudaStream_t s) {
+int launch_kv_append_rope(const RopeArgs& a, const DeviceInfo& di, cudaStream_t s) {
   const int P = a.ap.c.page_size, D = a.ap.c.head_dim;
   // every sequence touches at most len / P + 2 pages, and no more than its tokens
   const int64_t most = (int64_t)a.ap.total / P + 2 * (int64_t)a.ap.n_seq;
   const int nb = int(std::min(most, (int64_t)a.ap.total)) + 1;   // the last one looks at every sequence
-  const dim3 grid(nb, 2 * a.ap.c.n_kv_heads + (a.q ? (a.n_heads + kRopeQHeads - 1) / kRopeQHeads : 0));
+  // Heads a CTA: more share one table of angles, while there are CTAs for every SM several times over.
+  const int H = a.ap.c.n_kv_heads, n_q = a.q ? a.n_heads : 0;
+  int heads = 1;
+  while (heads < 4 && (int64_t)nb * (2 * H + n_q) >= (int64_t)kRopeCtas * di.sm_count * 2 * heads) heads *= 2;
+  const int k_groups = (H + heads - 1) / heads;
+  const dim3 grid(nb, 2 * k_groups + (n_q + heads - 1) / heads);
   const uint32_t smem = uint32_t(P) * (a.rot / 2) * sizeof(float2);
-  auto go = [&](auto kernel) -> int {
+  auto room = [&](auto kernel) -> int {
+    if (smem <= 48 * 1024 - 4096) return MOE_OK;         // what a kernel may have without asking
     MOE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
-    kernel<<<grid, kRopeThreads, smem, s>>>(a);
+    return MOE_OK;
+  };
+  auto go = [&](auto kernel) -> int {
+    const int st = room(kernel);
+    if (st != MOE_OK) return st;
+    kernel<<<grid, kRopeThreads, smem, s>>>(a, heads, k_groups);
     return launch_status();
   };
-  switch (P * D / 8 / kRopeThreads) {
+  // a token or two a sequence: a CTA for all their heads
+  if (a.ap.total <= 2 * (int64_t)a.ap.n_seq) {
+    const int st = room(append_rope_few_kernel);
+    if (st != MOE_OK) return st;
+    append_rope_few_kernel<<<nb, kRopeThreads, smem, s>>>(a);
+    return launch_status();
+  }
+  switch (P * D / 16 / kRopeThreads) {
     case 0:
     case 1: return go(append_rope_kernel<1>);
     case 2: return go(append_rope_kernel<2>);
-    case 4: return go(append_rope_kernel<4>);
-    default: return go(append_rope_kernel<8>);
+    default: return go(append_rope_kernel<4>);
   }
 }
 

@@ -4,12 +4,14 @@
 //   y = x + scale * gate * n
 //   h = y * rsqrt(mean y^2 + eps) * (offset + wn)
 //
-// One CTA per row: the row stays in registers from the read of a and x to the
-// writes of y and h, so every element crosses memory once. Bound by HBM (8 bytes
-// an element with a bf16 stream); a single row by the launch and its chain of a
-// read and two sums over the CTA. h comes from y before its rounding.
+// A CTA takes a row at a time, which stays in registers from the read of a and x to
+// the writes of y and h, so every element crosses memory once; the next row's reads
+// are on their way meanwhile, and the weights stay for all rows. Bound by HBM (8
+// bytes an element with a bf16 stream); a single row by the launch and its chain of
+// a read and two sums over the CTA. h comes from y before its rounding.
 #include "block.h"
 #include "common.cuh"
+#include "f32x2.cuh"
 
 namespace moe {
 namespace {
@@ -23,6 +25,11 @@ __device__ __forceinline__ float cta_sum(float v, float* s) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   if (lane == 0) s[warp] = v;
   __syncthreads();
+  if (n <= 8) {                       // fewer instructions than five more shuffles
+    v = 0.0f;
+    for (int i = 0; i < n; ++i) v += s[i];
+    return v;
+  }
   v = lane < n ? s[lane] : 0.0f;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
@@ -37,149 +44,236 @@ __device__ __forceinline__ float cta_max(float v, float* s) {
   return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, lane < n ? __float_as_uint(s[lane]) : 0u));
 }
 
+// Eight elements, two to a 64-bit register: an instruction takes both.
+struct Eight {
+  uint64_t p[4];
+};
+__device__ __forceinline__ Eight widen(const uint4& w) {          // bf16
+  return {{pack2(bf16_lo(w.x), bf16_hi(w.x)), pack2(bf16_lo(w.y), bf16_hi(w.y)), pack2(bf16_lo(w.z), bf16_hi(w.z)),
+           pack2(bf16_lo(w.w), bf16_hi(w.w))}};
+}
+__device__ __forceinline__ uint32_t narrow(uint64_t v) {
+  float lo, hi;
+  unpack2(v, lo, hi);
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint4 narrow(const Eight& v) {
+  return make_uint4(narrow(v.p[0]), narrow(v.p[1]), narrow(v.p[2]), narrow(v.p[3]));
+}
+// Eight elements as they lie in memory.
+template <bool kF32>
+struct Raw {
+  uint4 w[kF32 ? 2 : 1];
+};
+template <bool kF32>
+__device__ __forceinline__ Raw<kF32> load_raw(const void* row, int c) {
+  const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(row) + c * (kF32 ? 4 : 2));
+  Raw<kF32> r;
+  r.w[0] = p[0];
+  if constexpr (kF32) r.w[1] = p[1];
+  return r;
+}
+template <bool kF32>
+__device__ __forceinline__ Eight widen(const Raw<kF32>& r) {
+  if constexpr (kF32)
+    return {{uint64_t(r.w[0].x) | uint64_t(r.w[0].y) << 32, uint64_t(r.w[0].z) | uint64_t(r.w[0].w) << 32,
+             uint64_t(r.w[1].x) | uint64_t(r.w[1].y) << 32, uint64_t(r.w[1].z) | uint64_t(r.w[1].w) << 32}};
+  else
+    return widen(r.w[0]);
+}
+template <bool kF32>
+__device__ __forceinline__ void store8(void* row, int c, const Eight& v) {
+  if constexpr (kF32) {
+    ulonglong2* p = reinterpret_cast<ulonglong2*>(static_cast<float*>(row) + c);
+    p[0] = make_ulonglong2(v.p[0], v.p[1]);
+    p[1] = make_ulonglong2(v.p[2], v.p[3]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(row) + c) = narrow(v);
+  }
+}
+
 // 1 / sqrt(mean v^2 + eps) of the row. Where the squares' sum leaves what fp32
 // holds well, they are summed once more in units of the row's largest value.
 template <int V>
-__device__ __forceinline__ float row_rstd(const float (&v)[V][8], float d, float eps, float* s) {
-  float q = 0.0f;
+__device__ __forceinline__ float row_rstd(const Eight (&v)[V], float d, float eps, float* s) {
+  auto squares = [&](float f) {
+    uint64_t q[2] = {0, 0};            // two zeros each
+    const uint64_t f2 = pack2(f, f);
 #pragma unroll
-  for (int i = 0; i < V; ++i)
+    for (int i = 0; i < V; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) q = fmaf(v[i][e], v[i][e], q);
-  q = cta_sum(q, s);
+      for (int e = 0; e < 4; ++e) {
+        const uint64_t z = f == 1.0f ? v[i].p[e] : mul2(v[i].p[e], f2);
+        q[e & 1] = fma2(z, z, q[e & 1]);
+      }
+    float lo, hi;
+    unpack2(add2(q[0], q[1]), lo, hi);
+    return lo + hi;
+  };
+  float q = cta_sum(squares(1.0f), s);
   if (q >= 1e-30f && q <= 1e37f) return rsqrtf(q / d + eps);
   float m = 0.0f;
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[i][e]));
+    for (int e = 0; e < 4; ++e) {
+      float lo, hi;
+      unpack2(v[i].p[e], lo, hi);
+      m = fmaxf(m, fmaxf(fabsf(lo), fabsf(hi)));
+    }
   m = cta_max(m, s);
   if (!(m > 0.0f && m <= 3.4028235e38f) || q != q) return rsqrtf(q / d + eps);
   const int ex = min(max(int(__float_as_uint(m) >> 23) - 127, -125), 126);
   const float f = __uint_as_float(uint32_t(127 - ex) << 23);   // 2^-ex
-  q = 0.0f;
-#pragma unroll
-  for (int i = 0; i < V; ++i)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) q = fmaf(v[i][e] * f, v[i][e] * f, q);
   __syncthreads();
-  q = cta_sum(q, s);
+  q = cta_sum(squares(f), s);
   const float e2 = eps * f * f;
   return e2 <= 3.4028235e38f ? f * rsqrtf(q / d + e2) : rsqrtf(eps);
 }
 
-__device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = bf16_lo(u[i]);
-    v[2 * i + 1] = bf16_hi(u[i]);
-  }
+// What n (of the half's output) and y are multiplied with, beside their norms:
+// scale (offset + wp) gate, the gate where all rows share it, and offset + wn.
+template <int V>
+struct Weights {
+  Eight a[V], h[V];
+};
+__device__ __forceinline__ Eight constant(float v) {
+  const uint64_t p = pack2(v, v);
+  return {{p, p, p, p}};
 }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
+__device__ __forceinline__ Eight product(const Eight& a, const Eight& b) {
+  return {{mul2(a.p[0], b.p[0]), mul2(a.p[1], b.p[1]), mul2(a.p[2], b.p[2]), mul2(a.p[3], b.p[3])}};
 }
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-  return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+__device__ __forceinline__ Eight plus(const Eight& a, const Eight& b) {
+  return {{add2(a.p[0], b.p[0]), add2(a.p[1], b.p[1]), add2(a.p[2], b.p[2]), add2(a.p[3], b.p[3])}};
 }
-// Eight elements at column c of a row; kF32: of fp32.
-template <bool kF32>
-__device__ __forceinline__ void load8(const void* row, int c, float (&v)[8]) {
-  if constexpr (kF32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(row) + c);
-    const float4 a = p[0], b = p[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-    unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(row) + c), v);
-  }
+__device__ __forceinline__ Eight weight_a(const NormArgs& a, int c) {
+  Eight w = constant(a.scale);
+  if (a.wp) w = product(w, plus(constant(a.offset), widen(*reinterpret_cast<const uint4*>(a.wp + c))));
+  if (a.gate && a.g_rs == 0) w = product(w, widen(*reinterpret_cast<const uint4*>(a.gate + c)));
+  return w;
 }
-template <bool kF32>
-__device__ __forceinline__ void store8(void* row, int c, const float (&v)[8]) {
-  if constexpr (kF32) {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(row) + c);
-    p[0] = make_float4(v[0], v[1], v[2], v[3]);
-    p[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(row) + c) = pack8(v);
-  }
+__device__ __forceinline__ Eight weight_h(const NormArgs& a, int c) {
+  return a.wn ? plus(constant(a.offset), widen(*reinterpret_cast<const uint4*>(a.wn + c))) : constant(1.0f);
 }
 
-// V: 8-element vectors a thread holds.
-template <int V, bool kF32>
-__global__ void __launch_bounds__(kNormMaxThreads) block_norm_kernel(const NormArgs a) {
-  __shared__ float s[2][32];
-  const int64_t t = blockIdx.x;
+// One row: y and h from x, the half's output n and the gate gt (if gate_row); weights
+// w where KEEP, else read. `next` runs once the row is out of x, n and gt. s0, s1:
+// room for both sums, not used for the row before.
+template <int V, bool kF32, bool HAS_A, bool KEEP, class Next>
+__device__ __forceinline__ void norm_row(const NormArgs& a, int64_t t, const Raw<kF32> (&x)[V], const uint4 (&n)[V],
+                                         const uint4 (&gt)[V], bool gate_row, const Weights<V>& w, float* s0, float* s1,
+                                         Next next) {
   const int tid = threadIdx.x, nt = blockDim.x;
-  constexpr int kBytes = kF32 ? 4 : 2;
-  const void* xr = static_cast<const char*>(a.x) + t * a.x_rs * kBytes;
-  float y[V][8], n[V][8];
+  Eight y[V], z[V];
+  uint4 g[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int c = (tid + i * nt) * 8;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[i][e] = n[i][e] = 0.0f;
-    if (c < a.d) {
-      load8<kF32>(xr, c, y[i]);
-      if (a.a) load8<false>(a.a + t * a.a_rs, c, n[i]);
-    }
+    y[i] = widen<kF32>(x[i]);
+    if (HAS_A) z[i] = widen(n[i]);
+    g[i] = gt[i];
   }
-  if (a.a) {
-    const float r = a.wp ? row_rstd<V>(n, float(a.d), a.eps, s[0]) : 1.0f;
-    void* yr = static_cast<char*>(a.y) + t * a.y_rs * kBytes;
+  next();
+  if (HAS_A) {
+    const float r = a.wp ? row_rstd<V>(z, float(a.d), a.eps, s0) : 1.0f;
+    void* yr = static_cast<char*>(a.y) + t * a.y_rs * (kF32 ? 4 : 2);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = (tid + i * nt) * 8;
       if (c >= a.d) break;
-      float w[8];
-      if (a.wp) {
-        load8<false>(a.wp, c, w);
+      z[i] = product(z[i], constant(r));
+      if (gate_row) z[i] = product(z[i], widen(g[i]));
+      const Eight f = KEEP ? w.a[i] : weight_a(a, c);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) n[i][e] = n[i][e] * r * (a.offset + w[e]);
-      }
-      if (a.gate) {
-        load8<false>(a.gate + t * a.g_rs, c, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) n[i][e] *= w[e];
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[i][e] = fmaf(a.scale, n[i][e], y[i][e]);
+      for (int e = 0; e < 4; ++e) y[i].p[e] = fma2(z[i].p[e], f.p[e], y[i].p[e]);
       store8<kF32>(yr, c, y[i]);
     }
   }
   if (a.h) {
-    const float r = row_rstd<V>(y, float(a.d), a.eps, s[1]);
+    const float r = row_rstd<V>(y, float(a.d), a.eps, s1);
     __nv_bfloat16* hr = a.h + t * a.h_rs;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = (tid + i * nt) * 8;
       if (c >= a.d) break;
-      float w[8];
-      if (a.wn) load8<false>(a.wn, c, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[i][e] = y[i][e] * r * (a.wn ? a.offset + w[e] : 1.0f);
-      store8<false>(hr, c, y[i]);
+      store8<false>(hr, c, product(product(y[i], constant(r)), KEEP ? w.h[i] : weight_h(a, c)));
     }
   }
 }
 
+// V: 8-element vectors a thread holds. HAS_A: not only a norm of x. AHEAD: weights
+// stay in registers for all rows of the CTA, and the next row is read while one is
+// worked on; for that rows must not be too long.
+template <int V, bool kF32, bool HAS_A, bool AHEAD>
+__global__ void __launch_bounds__(V <= 2 ? 512 : kNormMaxThreads) block_norm_kernel(const NormArgs a) {
+  __shared__ float s[4][32];
+  const int tid = threadIdx.x, nt = blockDim.x;
+  const bool gate_row = HAS_A && a.gate && a.g_rs != 0;
+  Raw<kF32> x[V];
+  uint4 n[V], gt[V];
+  auto fetch = [&](int64_t t) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = (tid + i * nt) * 8;
+      if (c < a.d) {
+        x[i] = load_raw<kF32>(static_cast<const char*>(a.x) + t * a.x_rs * (kF32 ? 4 : 2), c);
+        if (HAS_A) n[i] = *reinterpret_cast<const uint4*>(a.a + t * a.a_rs + c);
+        if (gate_row) gt[i] = *reinterpret_cast<const uint4*>(a.gate + t * a.g_rs + c);
+      }
+    }
+  };
+  Weights<V> w;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    x[i] = Raw<kF32>{};
+    n[i] = gt[i] = make_uint4(0, 0, 0, 0);
+    w.a[i] = w.h[i] = constant(0.0f);
+  }
+  fetch(blockIdx.x);
+  if (AHEAD) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = (tid + i * nt) * 8;
+      if (c < a.d) {
+        if (HAS_A) w.a[i] = weight_a(a, c);
+        w.h[i] = weight_h(a, c);
+      }
+    }
+  }
+  int k = 0;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, k ^= 2) {
+    if (!AHEAD && t != blockIdx.x) fetch(t);
+    norm_row<V, kF32, HAS_A, AHEAD>(a, t, x, n, gt, gate_row, w, s[k], s[k + 1], [&] {
+      if (AHEAD && t + gridDim.x < a.T) fetch(t + gridDim.x);
+    });
+  }
+}
+
+template <int V, bool kF32, bool HAS_A>
+int launch_norm(const NormArgs& a, int threads, const DeviceInfo& di, cudaStream_t s) {
+  constexpr bool kAhead = V <= 2;
+  int per_sm = 8;
+  if (kAhead && a.T > di.sm_count)
+    MOE_CUDA_TRY(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, block_norm_kernel<V, kF32, HAS_A, kAhead>, threads, 0));
+  const int64_t most = (int64_t)di.sm_count * (per_sm > 0 ? per_sm : 1);
+  block_norm_kernel<V, kF32, HAS_A, kAhead><<<int(a.T < most ? a.T : most), threads, 0, s>>>(a);
+  return launch_status();
+}
 template <int V>
-void launch_v(const NormArgs& a, int threads, cudaStream_t s) {
-  if (a.fp32) block_norm_kernel<V, true><<<a.T, threads, 0, s>>>(a);
-  else block_norm_kernel<V, false><<<a.T, threads, 0, s>>>(a);
+int launch_v(const NormArgs& a, int threads, const DeviceInfo& di, cudaStream_t s) {
+  if (a.fp32) return a.a ? launch_norm<V, true, true>(a, threads, di, s) : launch_norm<V, true, false>(a, threads, di, s);
+  return a.a ? launch_norm<V, false, true>(a, threads, di, s) : launch_norm<V, false, false>(a, threads, di, s);
 }
 
 }  // namespace
 
-int launch_block_norm(const NormArgs& a, const DeviceInfo&, cudaStream_t s) {
+int launch_block_norm(const NormArgs& a, const DeviceInfo& di, cudaStream_t s) {
   const int vecs = a.d / 8;
-  const int v = vecs <= 256 ? 1 : vecs <= 2048 ? 2 : 4;
+  const int v = vecs <= (a.T <= di.sm_count ? 512 : 256) ? 1 : vecs <= 1024 ? 2 : 4;
   const int threads = int(round_up((vecs + v - 1) / v, 32));
-  if (v == 1) launch_v<1>(a, threads, s);
-  else if (v == 2) launch_v<2>(a, threads, s);
-  else launch_v<4>(a, threads, s);
-  return launch_status();
+  return v == 1 ? launch_v<1>(a, threads, di, s) : v == 2 ? launch_v<2>(a, threads, di, s) : launch_v<4>(a, threads, di, s);
 }
 
 }  // namespace moe

@@ -104,87 +104,79 @@ __device__ __forceinline__ F2 exp_pair(const F2& x, const F2& tab) {
   return {v.hi * f1 * f2, v.lo * f1 * f2};
 }
 
-// PL: experts a lane holds.
-template <int PL>
-__global__ void __launch_bounds__(kGrpWarps * 32) route_groups_kernel(const GroupArgs a, int L) {
-  const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * kGrpWarps + (threadIdx.x >> 5);
-  if (t >= a.T) return;
-  const int size = a.E / a.n_groups, g = lane / L, u = lane % L;
-  const F2 tab{kExpTable.hi[lane], kExpTable.lo[lane]};
-  const float* row = a.logits + (size_t)t * a.E;
-  auto expert = [&](int j) { return g * size + u + j * L; };
-  auto held = [&](int j) { return g < a.n_groups && u + j * L < size; };
+// Distance up to which two fp32 keys may stand in the wrong order. The exponential
+// errs by 2^-22 (ex2.approx) and 2^-23, the quotient by 2^-22, the sum with one by
+// 2^-24: a sigmoid by less than 7e-7 of itself, a key by a rounding more; a softmax's
+// sum of up to 1,024 terms adds 2^-21, which all scores share.
+__device__ __forceinline__ float doubt(bool softmax, float s_max, float key) {
+  return s_max * (softmax ? 2.4e-6f : 1.4e-6f) + 2.4e-7f * fabsf(key);
+}
+__device__ __forceinline__ F2 pair_sigmoid(float x, const F2& tab) {
+  const F2 e = exp_pair({-fabsf(x), 0.0f}, tab), d = add({1.0f, 0.0f}, e);
+  return x >= 0.0f ? div({1.0f, 0.0f}, d) : div(e, d);
+}
+// Finite logit; *nan.
+__device__ __forceinline__ float logit(float x, bool* nan) {
+  *nan = isnan(x);
+  return *nan ? -kFmax : fminf(fmaxf(x, -kFmax), kFmax);
+}
+// A key as a pair, by the definition.
+__device__ __forceinline__ F2 pair_key(const F2& s, float b, bool nan) {
+  if (nan) return {-INFINITY, 0.0f};
+  return fabsf(b) <= kFmax ? add({b, 0.0f}, s) : F2{isnan(b) ? -INFINITY : b, 0.0f};
+}
 
-  float l[PL];
-  bool nan[PL];
-#pragma unroll
-  for (int j = 0; j < PL; ++j) {
-    l[j] = held(j) ? row[expert(j)] : -kFmax;
-    nan[j] = isnan(l[j]);
-    l[j] = nan[j] ? -kFmax : fminf(fmaxf(l[j], -kFmax), kFmax);
-  }
-  const bool scores = a.bias || a.best > 1 || a.softmax;   // else only those of the selected
-  F2 s[PL];
-  float top_l = 0.0f;
+// One token with every score as a pair (whole warp): keys to shared memory [n][32]
+// twice, high and low parts; lane r < k gets its expert. Taken where fp32 cannot tell
+// groups apart, or too many experts.
+__device__ __noinline__ int route_in_pairs(const GroupArgs& a, const float* row, int L, uint32_t* kh, uint32_t* kl) {
+  const int lane = threadIdx.x & 31, size = a.E / a.n_groups, g = lane / L, u = lane % L;
+  const int n = g < a.n_groups ? (size - u + L - 1) / L : 0;         // experts of this lane
+  const F2 tab{kExpTable.hi[lane], kExpTable.lo[lane]};
+  const int all = (size + L - 1) / L;
+  float top_l = -kFmax;
   F2 sum{0.0f, 0.0f};
   if (a.softmax) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < PL; ++j) m = max(m, held(j) && !nan[j] ? rank_key(l[j]) : 0u);
-    m = __reduce_max_sync(0xFFFFFFFFu, m);
-    top_l = m ? rank_value(m) : 0.0f;
-#pragma unroll
-    for (int j = 0; j < PL; ++j) {
-      s[j] = exp_pair(two_sum(l[j], -top_l), tab);
-      if (nan[j] || !held(j)) s[j] = {0.0f, 0.0f};
-      sum = add(sum, s[j]);
+    for (int j = 0; j < n; ++j) {
+      bool nan;
+      const float l = logit(row[g * size + u + j * L], &nan);
+      if (!nan) top_l = fmaxf(top_l, l);
     }
-#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top_l = fmaxf(top_l, __shfl_xor_sync(0xFFFFFFFFu, top_l, o));
+#pragma unroll 1
+    for (int j = 0; j < all; ++j) {
+      bool nan = true;
+      const float l = j < n ? logit(row[g * size + u + j * L], &nan) : 0.0f;
+      const F2 e = exp_pair(two_sum(l, -top_l), tab);
+      if (!nan) sum = add(sum, e);
+    }
     for (int o = 1; o < 32; o <<= 1) {
       const F2 other{__shfl_xor_sync(0xFFFFFFFFu, sum.hi, o), __shfl_xor_sync(0xFFFFFFFFu, sum.lo, o)};
-      // the same two numbers in the same order in both lanes
-      sum = (lane & o) ? add(other, sum) : add(sum, other);
+      sum = (lane & o) ? add(other, sum) : add(sum, other);   // the same in both lanes
     }
     if (sum.hi == 0.0f) sum = {1.0f, 0.0f};
   }
-  auto sigmoid = [&](float x) {
-    const F2 e = exp_pair({-fabsf(x), 0.0f}, tab);
-    const F2 d = add({1.0f, 0.0f}, e);
-    return x >= 0.0f ? div({1.0f, 0.0f}, d) : div(e, d);
+  F2 b0{-INFINITY, 0.0f}, b1{-INFINITY, 0.0f};                 // the two best of this lane's, for its group
+  auto take = [&](const F2& v) {
+    if (less(b0, v)) b1 = b0, b0 = v;
+    else if (less(b1, v)) b1 = v;
   };
-  if (scores) {
-#pragma unroll
-    for (int j = 0; j < PL; ++j) {
-      s[j] = a.softmax ? div(s[j], sum) : sigmoid(l[j]);
-      if (nan[j]) s[j] = {0.0f, 0.0f};
+#pragma unroll 1
+  for (int j = 0; j < all; ++j) {
+    bool nan = true;
+    const int e = g * size + u + j * L;
+    const float l = j < n ? logit(row[e], &nan) : 0.0f;
+    F2 s = a.softmax ? div(exp_pair(two_sum(l, -top_l), tab), sum) : pair_sigmoid(l, tab);
+    if (nan) s = {0.0f, 0.0f};
+    const F2 key = a.bias ? pair_key(s, j < n ? a.bias[e] : 0.0f, nan) : F2{nan ? -INFINITY : l, 0.0f};
+    if (j < n) {
+      kh[j * 32 + lane] = rank_key(key.hi);
+      kl[j * 32 + lane] = rank_key(key.lo);
+      take(a.bias || a.best == 1 || nan ? key : s);
     }
   }
-  // keys: high part 0 stands for "no candidate"
-  uint32_t kh[PL], kl[PL];
-#pragma unroll
-  for (int j = 0; j < PL; ++j) {
-    F2 key{l[j], 0.0f};
-    if (a.bias) {
-      const float b = held(j) ? a.bias[expert(j)] : 0.0f;
-      key = add({b, 0.0f}, s[j]);
-      if (!(fabsf(b) <= kFmax)) key = {b, 0.0f};
-      if (nan[j]) key = {-INFINITY, 0.0f};
-    }
-    kh[j] = held(j) ? rank_key(nan[j] ? -INFINITY : key.hi) : 0u;
-    kl[j] = kh[j] ? rank_key(key.lo) : 0u;
-  }
-
+  bool in = g < a.n_groups;
   if (a.top < a.n_groups) {
-    // a group's score: its best key, or the sum of its two best (without a bias, of their scores)
-    F2 b0{-INFINITY, 0.0f}, b1{-INFINITY, 0.0f};
-    auto take = [&](const F2& v) {
-      if (less(b0, v)) b1 = b0, b0 = v;
-      else if (less(b1, v)) b1 = v;
-    };
-#pragma unroll
-    for (int j = 0; j < PL; ++j)
-      if (kh[j]) take(a.best > 1 && !a.bias ? (nan[j] ? F2{-INFINITY, 0.0f} : s[j]) : F2{rank_value(kh[j]), rank_value(kl[j])});
     for (int o = 1; o < L; o <<= 1) {
       const F2 o0{__shfl_xor_sync(0xFFFFFFFFu, b0.hi, o), __shfl_xor_sync(0xFFFFFFFFu, b0.lo, o)};
       const F2 o1{__shfl_xor_sync(0xFFFFFFFFu, b1.hi, o), __shfl_xor_sync(0xFFFFFFFFu, b1.lo, o)};
@@ -198,57 +190,266 @@ __global__ void __launch_bounds__(kGrpWarps * 32) route_groups_kernel(const Grou
       const F2 v{__shfl_sync(0xFFFFFFFFu, score.hi, i * L), __shfl_sync(0xFFFFFFFFu, score.lo, i * L)};
       better += less(score, v) || (!less(v, score) && i < g);
     }
-    if (better >= a.top) {
-#pragma unroll
-      for (int j = 0; j < PL; ++j) kh[j] = 0u;
-    }
+    in = in && better < a.top;
   }
-
-  // the k best keys, equal ones by the lower expert
-  uint32_t bh, bl;
-  int bj;
-  auto local_best = [&]() {
-    bh = bl = 0u;
-    bj = 0;
-#pragma unroll
-    for (int j = 0; j < PL; ++j)
-      if (kh[j] > bh || (kh[j] == bh && kh[j] && kl[j] > bl)) bh = kh[j], bl = kl[j], bj = j;
-  };
-  local_best();
   int my_e = 0;
-  float my_s = 0.0f, my_l = 0.0f;
   for (int r = 0; r < a.k; ++r) {
+    uint32_t bh = 0u, bl = 0u;
+    int bj = 0;
+    if (in)
+      for (int j = 0; j < n; ++j) {
+        const uint32_t h = kh[j * 32 + lane], w = kl[j * 32 + lane];
+        if (h > bh || (h == bh && h && w > bl)) bh = h, bl = w, bj = j;
+      }
     const uint32_t h = __reduce_max_sync(0xFFFFFFFFu, bh);
-    const uint32_t lo = __reduce_max_sync(0xFFFFFFFFu, bh == h ? bl : 0u);
-    const int mine = bh == h && bl == lo ? expert(bj) : 0x7FFFFFFF;
+    const uint32_t w = __reduce_max_sync(0xFFFFFFFFu, bh == h ? bl : 0u);
+    const int mine = bh == h && bl == w ? g * size + u + bj * L : 0x7FFFFFFF;
     const int e = __reduce_min_sync(0xFFFFFFFFu, mine);
-    const int src = __ffs(__ballot_sync(0xFFFFFFFFu, mine == e)) - 1;
-    float sv = 0.0f, lv = 0.0f;
-    if (lane == src) {
+    if (mine == e) kh[bj * 32 + lane] = 0u;
+    if (lane == r) my_e = e;
+  }
+  return my_e;
+}
+
+// PL: experts a lane holds.
+template <int PL>
+__global__ void __launch_bounds__(kGrpWarps * 32, PL <= 8 ? 8 : PL <= 16 ? 7 : 3) route_groups_kernel(const GroupArgs a, int L) {
+  extern __shared__ uint32_t s_keys[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = blockIdx.x * kGrpWarps + warp;
+  if (t >= a.T) return;
+  const int size = a.E / a.n_groups, g = lane / L, u = lane % L;
+  const float* row = a.logits + (size_t)t * a.E;
+  auto expert = [&](int j) { return g * size + u + j * L; };
+  auto held = [&](int j) { return g < a.n_groups && u + j * L < size; };
+
+  // ---- keys in fp32 --------------------------------------------------------------
+  float l[PL], s[PL], b[PL];
+  float l_max = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < PL; ++j) {
+    l[j] = held(j) ? row[expert(j)] : -INFINITY;
+    b[j] = a.bias && held(j) ? a.bias[expert(j)] : 0.0f;
+  }
+  bool odd = false;              // a logit or a bias that is not finite
+#pragma unroll
+  for (int j = 0; j < PL; ++j) {
+    l_max = fmaxf(l_max, l[j]);
+    odd |= held(j) && !(fabsf(l[j]) <= kFmax && fabsf(b[j]) <= kFmax);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l_max = fmaxf(l_max, __shfl_xor_sync(0xFFFFFFFFu, l_max, o));
+  const bool scores = a.bias || a.best > 1;      // else the logits rank
+  float s_max = 1.0f;
+  bool unsure = __any_sync(0xFFFFFFFFu, odd);
+  int my_e = 0;
+  if (!unsure) {
+    if (scores) {
+      const float from = a.softmax ? l_max : 0.0f;
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < PL; ++j) {
+        // 2^(x log2 e), with what the product's rounding leaves out
+        const float x = a.softmax ? l[j] - from : -l[j], y = x * 1.4426950408889634f;
+        float e;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y));
+        if (fabsf(x) < 100.0f) e = fmaf(e, fmaf(x, 1.4426950408889634f, -y) * 0.6931472f, e);
+        s[j] = a.softmax ? e : __fdividef(1.0f, 1.0f + e);
+        if (!a.softmax && l[j] < -80.0f) s[j] = 0.0f;
+        sum += s[j];
+      }
+      if (a.softmax) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        s_max = 1.0f / sum;
+#pragma unroll
+        for (int j = 0; j < PL; ++j) s[j] *= s_max;
+      } else {
+        s_max = 1.0f / (1.0f + expf(-l_max));
+        unsure = l_max < -80.0f;                 // scores that fp32 hardly holds
+      }
+    }
+    uint32_t key[PL];
+#pragma unroll
+    for (int j = 0; j < PL; ++j) key[j] = held(j) ? rank_key(a.bias ? s[j] + b[j] : l[j]) : 0u;
+
+    if (a.top < a.n_groups) {
+      // a group's score: its best key, or the sum of its two best (without a bias, of their scores)
+      float b0 = -INFINITY, b1 = -INFINITY;
+      auto take = [&](float v) {
+        b1 = fmaxf(b1, fminf(b0, v));
+        b0 = fmaxf(b0, v);
+      };
 #pragma unroll
       for (int j = 0; j < PL; ++j)
-        if (j == bj) {
-          if (scores) sv = s[j].hi;
-          lv = nan[j] ? -INFINITY : l[j];
-          kh[j] = 0u;
+        if (held(j)) take(a.bias ? s[j] + b[j] : a.best > 1 ? s[j] : l[j]);
+      for (int o = 1; o < L; o <<= 1) {
+        const float o0 = __shfl_xor_sync(0xFFFFFFFFu, b0, o), o1 = __shfl_xor_sync(0xFFFFFFFFu, b1, o);
+        take(o0);
+        take(o1);
+      }
+      const float score = a.best > 1 ? b0 + b1 : b0;
+      int better = 0;
+      for (int i = 0; i < a.n_groups; ++i) {
+        const float v = __shfl_sync(0xFFFFFFFFu, score, i * L);
+        better += v > score || (v == score && i < g);
+      }
+      if (scores) {        // the last group that is in and the first that is not: does their order stand?
+        const int in = __ffs(__ballot_sync(0xFFFFFFFFu, g < a.n_groups && better == a.top - 1)) - 1;
+        const int out = __ffs(__ballot_sync(0xFFFFFFFFu, g < a.n_groups && better == a.top)) - 1;
+        const float v = __shfl_sync(0xFFFFFFFFu, score, in), w = __shfl_sync(0xFFFFFFFFu, score, out);
+        if (v - w <= 2.0f * doubt(a.softmax, s_max, fabsf(v) + fabsf(w))) {
+          // Rank the groups by sums of pairs, where it is clear of which experts. (A softmax wants its sum as a pair.)
+          const float from_key = (a.best > 1 ? b1 : b0) - doubt(a.softmax, s_max, fabsf(b0) + fabsf(b1));
+          int n = 0, e0 = -1, e1 = -1;           // this lane's experts that may count
+#pragma unroll
+          for (int j = 0; j < PL; ++j)
+            if (held(j) && (a.bias ? s[j] + b[j] : a.best > 1 ? s[j] : l[j]) >= from_key) {
+              e1 = n ? expert(j) : -1;
+              if (!n) e0 = expert(j);
+              ++n;
+            }
+          int of_group = n;
+          for (int o = 1; o < L; o <<= 1) of_group += __shfl_xor_sync(0xFFFFFFFFu, of_group, o);
+          unsure = a.softmax || __any_sync(0xFFFFFFFFu, g < a.n_groups && of_group != a.best);
+          if (!unsure) {
+            const F2 tab{kExpTable.hi[lane], kExpTable.lo[lane]};
+            F2 sum{0.0f, 0.0f};
+            for (int i = 0; i < a.best; ++i) {
+              const int e = i ? e1 : e0;
+              const F2 x = pair_sigmoid(e >= 0 ? row[e] : 0.0f, tab);
+              if (e >= 0) sum = add(sum, a.bias ? add({a.bias[e], 0.0f}, x) : x);
+            }
+            for (int o = 1; o < L; o <<= 1) {
+              const F2 other{__shfl_xor_sync(0xFFFFFFFFu, sum.hi, o), __shfl_xor_sync(0xFFFFFFFFu, sum.lo, o)};
+              sum = (lane & o) ? add(other, sum) : add(sum, other);   // the same in both lanes
+            }
+            better = 0;
+            for (int i = 0; i < a.n_groups; ++i) {
+              const F2 x{__shfl_sync(0xFFFFFFFFu, sum.hi, i * L), __shfl_sync(0xFFFFFFFFu, sum.lo, i * L)};
+              better += less(sum, x) || (!less(x, sum) && i < g);
+            }
+          }
         }
-      local_best();
+      }
+      if (better >= a.top) {
+#pragma unroll
+        for (int j = 0; j < PL; ++j) key[j] = 0u;
+      }
     }
-    sv = __shfl_sync(0xFFFFFFFFu, sv, src);
-    lv = __shfl_sync(0xFFFFFFFFu, lv, src);
-    if (lane == r) my_e = e, my_s = sv, my_l = lv;
+
+    // ---- the best keys, equal ones by the lower expert -------------------------------
+    uint32_t bk;
+    int bj;
+    auto local_best = [&]() {
+      bk = 0u;
+      bj = 0;
+#pragma unroll
+      for (int j = 0; j < PL; ++j)
+        if (key[j] > bk) bk = key[j], bj = j;
+    };
+    local_best();
+    uint32_t my_key = 0u;
+    auto next_best = [&](int r) {      // to lane r; false: there is none
+      const uint32_t h = __reduce_max_sync(0xFFFFFFFFu, bk);
+      const int e = __reduce_min_sync(0xFFFFFFFFu, bk == h ? expert(bj) : 0x7FFFFFFF);
+      if (bk == h && expert(bj) == e) {
+#pragma unroll
+        for (int j = 0; j < PL; ++j)
+          if (j == bj) key[j] = 0u;
+        local_best();
+      }
+      if (lane == r) my_e = e, my_key = h;
+      return h != 0u;
+    };
+    int n = 0;
+    while (n < a.k && next_best(n)) ++n;
+    if (a.bias && n == 32) unsure = true;      // there is no lane for one more
+    if (a.bias && !unsure) {
+      // Does the order stand? One more key than are wanted, and more while they may belong before the last.
+      float ml = 0.0f, mb = 0.0f;
+      bool close = false;
+      for (bool more = true; more && n < 32;) {
+        more = next_best(n);
+        if (more) ++n;
+        const float v = rank_value(my_key), w = __shfl_down_sync(0xFFFFFFFFu, v, 1);
+        if (lane < n) ml = row[my_e], mb = a.bias[my_e];
+        const float wl = __shfl_down_sync(0xFFFFFFFFu, ml, 1), wb = __shfl_down_sync(0xFFFFFFFFu, mb, 1);
+        // keys of one logit and bias are equal, whatever their rounding
+        const bool near = lane + 1 < n && v - w <= doubt(a.softmax, s_max, fabsf(v)) && !(ml == wl && mb == wb);
+        const unsigned nears = __ballot_sync(0xFFFFFFFFu, near);
+        close = nears != 0u;
+        more = more && (nears >> (n - 2)) & 1;       // the last two
+        if (more && n == 32) unsure = true;
+      }
+      if (close && !unsure) {       // rank the candidates by their keys as pairs
+        const F2 tab{kExpTable.hi[lane], kExpTable.lo[lane]};
+        F2 e{0.0f, 0.0f};
+        if (a.softmax) {
+          unsure = true;            // the sum over all experts is wanted as a pair, too
+        } else {
+          e = add({mb, 0.0f}, pair_sigmoid(ml, tab));
+          int before = 0;
+          for (int i = 0; i < n; ++i) {
+            const F2 v{__shfl_sync(0xFFFFFFFFu, e.hi, i), __shfl_sync(0xFFFFFFFFu, e.lo, i)};
+            const int id = __shfl_sync(0xFFFFFFFFu, my_e, i);
+            before += less(e, v) || (!less(v, e) && id < my_e);
+          }
+          int mine = 0;
+          for (int i = 0; i < n; ++i) {
+            const int at = __shfl_sync(0xFFFFFFFFu, before, i), id = __shfl_sync(0xFFFFFFFFu, my_e, i);
+            if (at == lane) mine = id;
+          }
+          my_e = mine;
+        }
+      }
+    }
   }
-  if (!scores) {
-    const F2 v = sigmoid(fmaxf(my_l, -kFmax));
-    my_s = v.hi;
+  if (unsure) my_e = route_in_pairs(a, row, L, s_keys + warp * (PL * 64), s_keys + warp * (PL * 64) + PL * 32);
+
+  // ---- weights ------------------------------------------------------------------------
+  if (a.softmax && __any_sync(0xFFFFFFFFu, odd)) {     // the largest finite logit, or what an infinite one counts as
+    l_max = -kFmax;
+#pragma unroll
+    for (int j = 0; j < PL; ++j) {
+      bool nan;
+      const float x = logit(l[j], &nan);
+      if (!nan && held(j)) l_max = fmaxf(l_max, x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l_max = fmaxf(l_max, __shfl_xor_sync(0xFFFFFFFFu, l_max, o));
   }
-  if (lane >= a.k || my_l == -INFINITY) my_s = 0.0f;
-  float all = my_s;
+  float my_s = 0.0f;
+  if (lane < a.k) {
+    bool nan;
+    const float x = logit(row[my_e], &nan);
+    if (a.softmax) {
+      my_s = expf(x - l_max);        // times the sum of all, as yet
+    } else {
+      const float e = expf(-fabsf(x));
+      my_s = (x >= 0.0f ? 1.0f : e) / (1.0f + e);
+    }
+    if (nan) my_s = 0.0f;
+  }
+  float all = my_s, sum = 1.0f;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+  // in a quotient of scores the sum of all drops out, but for the 1e-20, which is less than 2^-26 of more than 1e-9
+  if (a.softmax && !(a.renorm && all > 1e-9f)) {
+    sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < PL; ++j) {
+      bool nan;
+      const float x = logit(l[j], &nan);
+      if (!nan && held(j)) sum += expf(x - l_max);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (sum == 0.0f) sum = 1.0f;
+  }
   if (lane < a.k) {
     a.idx[(size_t)t * a.k + lane] = my_e;
-    a.w[(size_t)t * a.k + lane] = (a.renorm ? my_s / (all + 1e-20f) : my_s) * a.scale;
+    a.w[(size_t)t * a.k + lane] = (a.renorm ? my_s / fmaf(1e-20f, sum, all) : my_s / sum) * a.scale;
   }
 }
 
@@ -269,14 +470,16 @@ bool groups_ok(int E, int k, int n_groups, int top, int best) {
 int launch_route_groups(const GroupArgs& a, cudaStream_t s) {
   const int L = lanes_of(a.n_groups), pl = (a.E / a.n_groups + L - 1) / L;
   const int grid = (a.T + kGrpWarps - 1) / kGrpWarps;
-#define MOE_GRP_CASE(P)                                                 \
-  route_groups_kernel<P><<<grid, kGrpWarps * 32, 0, s>>>(a, L);         \
+#define MOE_GRP_CASE(P)                                                                               \
+  route_groups_kernel<P><<<grid, kGrpWarps * 32, kGrpWarps * P * 64 * sizeof(uint32_t), s>>>(a, L); \
   break;
-  switch (pl <= 1 ? 1 : pl <= 2 ? 2 : pl <= 4 ? 4 : pl <= 8 ? 8 : pl <= 16 ? 16 : 32) {
+  switch (pl <= 1 ? 1 : pl <= 2 ? 2 : pl <= 4 ? 4 : pl <= 6 ? 6 : pl <= 8 ? 8 : pl <= 12 ? 12 : pl <= 16 ? 16 : 32) {
     case 1: MOE_GRP_CASE(1)
     case 2: MOE_GRP_CASE(2)
     case 4: MOE_GRP_CASE(4)
+    case 6: MOE_GRP_CASE(6)
     case 8: MOE_GRP_CASE(8)
+    case 12: MOE_GRP_CASE(12)
     case 16: MOE_GRP_CASE(16)
     default: MOE_GRP_CASE(32)
   }
