@@ -224,15 +224,22 @@ int moe_route_topk(const float* logits_dev, int T, int E, int k,
  * counts as the largest finite number of its sign.
  *   logits_dev   fp32 [T][E]
  *   bias_dev     fp32 [E], NULL for none
- *   score        moe_score;  renormalise 0 or 1;  scale: finite
+ *   rule         host
  *   idx_dev      int32 [T][k], slots in descending key order;  w_dev fp32 [T][k]
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED_SHAPE (E > 1024, k > 32, E %
  * n_groups, n_groups > 32, k > top_groups * E / n_groups, group_best > E /
  * n_groups, or E / n_groups times the power of two not below n_groups > 1024). */
 typedef enum moe_score { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 } moe_score;
-int moe_route_groups(const float* logits_dev, int T, int E, int k, const float* bias_dev, int score, int n_groups,
-                     int top_groups, int group_best, int renormalise, float scale, int32_t* idx_dev, float* w_dev,
-                     moe_stream_t stream);
+typedef struct moe_group_rule {
+  int32_t score;        /* moe_score */
+  int32_t n_groups;     /* 1: no groups */
+  int32_t top_groups;   /* groups that experts are taken from */
+  int32_t group_best;   /* 1 or 2: keys that a group's score adds up */
+  int32_t renormalise;  /* 1: the weights of a token sum to scale, 0: not */
+  float scale;          /* finite */
+} moe_group_rule;
+int moe_route_groups(const float* logits_dev, int T, int E, int k, const float* bias_dev, const moe_group_rule* rule,
+                     int32_t* idx_dev, float* w_dev, moe_stream_t stream);
 
 /* Group (token, slot) pairs by expert, stable in p = t*k + j (page "MoE-SpeQ
  * ...", §4.2: sort the verify tokens' expert assignments by expert id so each
@@ -325,6 +332,14 @@ int moe_forward_w4a8(const moe_layer* L, const void* x_dev, int T, void* y_dev,
                      float* logits_out, int32_t* idx_out, float* w_out,
                      void* workspace_dev, size_t workspace_bytes, int* dev_status,
                      moe_stream_t stream);
+
+/* The layer with routing by groups (moe_route_groups) of its router's logits in
+ * place of moe_route_topk; bias_dev fp32 [E] or NULL. The per-stage kernels run for
+ * any T. Other arguments, workspace and errors as moe_forward, and those of
+ * moe_route_groups for the rule. */
+int moe_forward_groups(const moe_layer* L, const moe_group_rule* rule, const void* x_dev, int T, void* y_dev,
+                       const float* bias_dev, float* logits_out, int32_t* idx_out, float* w_out, void* workspace_dev,
+                       size_t workspace_bytes, int* dev_status, moe_stream_t stream);
 
 /* Quantise activation rows to MXFP8, the operation moe_forward_w4a8 applies
  * to x and to h: per row and 32-element block, s = clamp(floor(log2 amax) - 8

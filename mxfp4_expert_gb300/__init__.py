@@ -13,6 +13,7 @@ caller, as have the results.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -26,7 +27,7 @@ __all__ = [
     "moe_workspace_bytes", "moe_query_path", "moe_stage_names", "moe_forward", "moe_forward_profiled", "moe_forward_w4a8", "moe_quant_mxfp8", "moe_lmhead_pack_fp8", "moe_lmhead_fp8", "moe_forward_static_scratch", "STATIC_SCRATCH_BYTES", "ATTN_DECODE_COUNTER_BYTES",
     "moe_rows", "moe_kv_cache", "KVCache", "moe_attn_prefill", "moe_kv_append_fp8", "moe_attn_decode_workspace_bytes",
     "moe_attn_decode_fp8", "moe_kv_evict_fp8", "moe_kv_append_rope_fp8", "moe_attn_chunk_workspace_bytes", "moe_attn_chunk_fp8",
-    "moe_block_norm", "moe_route_groups", "moe_selftest_bounded_wait", "moe_status_string", "moe_version",
+    "moe_block_norm", "moe_group_rule", "moe_route_groups", "moe_forward_groups", "moe_selftest_bounded_wait", "moe_status_string", "moe_version",
 ]
 
 # The in-tree build, and only it: there is no way to point the binding at
@@ -68,6 +69,11 @@ class moe_layer(ctypes.Structure):
                 ("down", ctypes.c_void_p), ("down_desc", moe_packed_desc),
                 ("shared_gate", ctypes.c_void_p), ("shared_up", ctypes.c_void_p),
                 ("shared_down", ctypes.c_void_p)]
+
+
+class moe_group_rule(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("n_groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_best", ctypes.c_int32), ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 class moe_rows(ctypes.Structure):
@@ -116,7 +122,9 @@ def _load():
         "moe_attn_chunk_workspace_bytes": (sz, [cache, i32, i32, i32]),
         "moe_attn_chunk_fp8": (i32, [cache, rows, i32, vp, i32, i32, vp, vp, i32, f32, vp, vp, vp, sz, vp, vp]),
         "moe_block_norm": (i32, [vp, i64, i32, vp, i64, i32, i32, vp, vp, i64, f32, vp, f32, f32, vp, i64, vp, i64, vp]),
-        "moe_route_groups": (i32, [vp, i32, i32, i32, vp, i32, i32, i32, i32, i32, f32, vp, vp, vp]),
+        "moe_route_groups": (i32, [vp, i32, i32, i32, vp, ctypes.POINTER(moe_group_rule), vp, vp, vp]),
+        "moe_forward_groups": (i32, [ctypes.POINTER(moe_layer), ctypes.POINTER(moe_group_rule), vp, i32, vp, vp, vp, vp, vp, vp,
+                                     sz, vp, vp]),
         "moe_stage_names": (ctypes.c_char_p, [i32]),
         "moe_selftest_bounded_wait": (i32, [vp, ctypes.c_uint32, ctypes.c_longlong, vp, vp]),
         "moe_status_string": (ctypes.c_char_p, [i32]),
@@ -239,6 +247,15 @@ def moe_route_topk(logits: torch.Tensor, k: int, bias: torch.Tensor | None = Non
 _SCORES = {"sigmoid": 0, "softmax": 1}
 
 
+@functools.lru_cache(maxsize=64)
+def _rule(score, n_groups, top_groups, group_best, renormalise, scale):
+    """Reference to the struct of a rule; never written to."""
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    return ctypes.byref(moe_group_rule(_SCORES[score], n_groups, top_groups, group_best, 1 if renormalise else 0,
+                                       float(scale)))
+
+
 def moe_route_groups(logits: torch.Tensor, k: int, bias: torch.Tensor | None = None, score: str = "sigmoid",
                      n_groups: int = 1, top_groups: int = 1, group_best: int = 2, renormalise: bool = True,
                      scale: float = 1.0, idx: torch.Tensor | None = None, w: torch.Tensor | None = None, stream=None):
@@ -250,8 +267,7 @@ def moe_route_groups(logits: torch.Tensor, k: int, bias: torch.Tensor | None = N
     sum of its two best. The scores of the selected are the weights,
     renormalised to a sum of 1 unless told otherwise, times scale.
     """
-    if score not in _SCORES:
-        raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    rule = _rule(score, n_groups, top_groups, group_best, renormalise, scale)
     dev = torch.cuda.current_device()
     lp = _ptr(logits, _F32, "logits", dev)
     if logits.dim() != 2:
@@ -262,8 +278,7 @@ def moe_route_groups(logits: torch.Tensor, k: int, bias: torch.Tensor | None = N
         idx = _empty(shape, _I32, logits.device, stream)
     if w is None:
         w = _empty(shape, _F32, logits.device, stream)
-    _check(lib.moe_route_groups(lp, T, E, k, _opt(bias, _F32, "bias", dev, (E,)), _SCORES[score], n_groups, top_groups,
-                                group_best, 1 if renormalise else 0, float(scale), _ptr(idx, _I32, "idx", dev, shape),
+    _check(lib.moe_route_groups(lp, T, E, k, _opt(bias, _F32, "bias", dev, (E,)), rule, _ptr(idx, _I32, "idx", dev, shape),
                                 _ptr(w, _F32, "w", dev, shape), _stream(stream, dev)), "moe_route_groups")
     return idx, w
 
@@ -407,6 +422,29 @@ def moe_forward_w4a8(layer: Layer, x: torch.Tensor, bias: torch.Tensor | None = 
     on the block-scaled tcgen05 path for any T; otherwise as moe_forward."""
     return _forward(layer, x, bias, y, workspace, logits_out, idx_out, w_out, dev_status, None, stream,
                     entry="moe_forward_w4a8")
+
+
+def moe_forward_groups(layer: Layer, x: torch.Tensor, bias: torch.Tensor | None = None, score: str = "sigmoid",
+                       n_groups: int = 1, top_groups: int = 1, group_best: int = 2, renormalise: bool = True,
+                       scale: float = 1.0, y: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                       logits_out: torch.Tensor | None = None, idx_out: torch.Tensor | None = None,
+                       w_out: torch.Tensor | None = None, dev_status: torch.Tensor | None = None, stream=None):
+    """The layer with its router's logits routed as moe_route_groups does (bias fp32 [E]); otherwise as moe_forward."""
+    rule = _rule(score, n_groups, top_groups, group_best, renormalise, scale)
+    if bias is not None and (not isinstance(bias, _Tensor) or bias.dim() != 1):
+        raise ValueError(f"bias must be [{layer.shape.n_experts}]")
+    if y is None:
+        _cuda(x, torch.bfloat16, "x")
+        y = _empty(x.shape, x.dtype, x.device, stream)
+    T, _ = _forward_args(layer, x, bias, y, logits_out, idx_out, w_out, dev_status)
+    if workspace is None:
+        n = layer.workspace_bytes(T)
+        workspace = _empty(n, torch.uint8, x.device, stream, n)
+    _cuda(workspace, torch.uint8, "workspace")
+    _check(lib.moe_forward_groups(ctypes.byref(layer.struct), rule, _p(x), T, _p(y), _p(bias), _p(logits_out), _p(idx_out),
+                                  _p(w_out), _p(workspace), workspace.numel(), _p(dev_status), _s(stream)),
+           "moe_forward_groups")
+    return y
 
 
 def moe_quant_mxfp8(src: torch.Tensor, stream=None):

@@ -4,6 +4,7 @@
 
 #include <mutex>
 
+#include "block.h"
 #include "common.cuh"
 #include "decode.h"
 #include "host_util.h"
@@ -183,11 +184,13 @@ int validate_forward(const moe_layer* L, const void* x_dev, int T, const void* y
 }
 
 // The kernel sequence of one validated forward call on `stream`; stage_events
-// as in moe_forward_profiled (n_stage_events 0: none).
+// as in moe_forward_profiled (n_stage_events 0: none). rule: routing by groups,
+// by the per-stage kernels for any T (its logits, idx and w are set here).
 int enqueue_forward(const moe_layer* L, const void* x_dev, int T, void* y_dev, const float* bias_dev,
                     int bias_row_stride, float* logits_out, int32_t* idx_out, float* w_out, void* workspace_dev,
                     int* dev_status, void* const* stage_events, int n_stage_events, moe_stream_t stream,
-                    const Workspace& ws, const DeviceInfo& di, bool act_mxfp8 = false) {
+                    const Workspace& ws, const DeviceInfo& di, bool act_mxfp8 = false,
+                    const GroupArgs* rule = nullptr) {
   int st = MOE_OK;
   const moe_shape& sh = L->shape;
   const int d = sh.d_model, I = sh.d_ff, E = sh.n_experts, k = sh.top_k;
@@ -216,7 +219,9 @@ int enqueue_forward(const moe_layer* L, const void* x_dev, int T, void* y_dev, c
   };
   if ((st = mark())) return st;
 
-  const int path = act_mxfp8 ? MOE_PATH_PREFILL_TC : select_path(sh, T, di);
+  const int path = act_mxfp8 ? MOE_PATH_PREFILL_TC
+                   : rule    ? (T >= kPrefillMinT ? MOE_PATH_PREFILL_TC : MOE_PATH_DECODE_MMA)
+                             : select_path(sh, T, di);
   if (path == MOE_PATH_DECODE_FUSED) {
     DecodeArgs da{};
     da.T = T;
@@ -277,14 +282,22 @@ int enqueue_forward(const moe_layer* L, const void* x_dev, int T, void* y_dev, c
   int32_t* inv = at<int32_t>(B, ws.inv);
   int32_t* active = at<int32_t>(B, ws.active);
   int32_t* n_active = at<int32_t>(B, ws.n_active);
-  if (route_fused_ok(T, E, k)) {
+  if (!rule && route_fused_ok(T, E, k)) {
     if ((st = launch_route_fused(logits, T, E, k, bias_dev, bias_row_stride, idx, w, at<int32_t>(B, ws.counts),
                                  offsets, perm, inv, active, n_active, status, s)))
       return st;
     if ((st = mark())) return st;
   } else {
-    if ((st = launch_topk(logits, T, E, k, bias_dev, bias_row_stride, idx, w, s))) return st;
-    if ((st = mark())) return st;
+    if (rule) {
+      GroupArgs ga = *rule;
+      ga.logits = logits;
+      ga.idx = idx;
+      ga.w = w;
+      st = launch_route_groups(ga, s);
+    } else {
+      st = launch_topk(logits, T, E, k, bias_dev, bias_row_stride, idx, w, s);
+    }
+    if (st != MOE_OK || (st = mark())) return st;
     if ((st = launch_sort(idx, T, k, E, at<int32_t>(B, ws.counts), offsets, perm, inv, active, n_active,
                           at<void>(B, ws.sort_ws), status, s)))
       return st;
@@ -430,6 +443,21 @@ extern "C" int moe_forward_w4a8(const moe_layer* L, const void* x_dev, int T, vo
   if (st != MOE_OK) return st;
   return enqueue_forward(L, x_dev, T, y_dev, bias_dev, bias_row_stride, logits_out, idx_out, w_out, workspace_dev,
                          dev_status, nullptr, 0, stream, ws, di, true);
+}
+
+extern "C" int moe_forward_groups(const moe_layer* L, const moe_group_rule* rule, const void* x_dev, int T, void* y_dev,
+                                  const float* bias_dev, float* logits_out, int32_t* idx_out, float* w_out,
+                                  void* workspace_dev, size_t workspace_bytes, int* dev_status, moe_stream_t stream) {
+  Workspace ws;
+  DeviceInfo di;
+  MOE_CHECK_ARG(L && rule, MOE_ERR_INVALID_ARG);
+  GroupArgs g{};
+  int st = group_args(rule, T, L->shape.n_experts, L->shape.top_k, bias_dev, &g);
+  if (st != MOE_OK) return st;
+  st = validate_forward(L, x_dev, T, y_dev, 0, workspace_dev, workspace_bytes, &ws, &di);
+  if (st != MOE_OK) return st;
+  return enqueue_forward(L, x_dev, T, y_dev, bias_dev, 0, logits_out, idx_out, w_out, workspace_dev, dev_status, nullptr, 0,
+                         stream, ws, di, false, &g);
 }
 
 namespace moe {

@@ -35,6 +35,8 @@ struct GroupArgs {
   int32_t* idx;                  // [T][k]
   float* w;                      // [T][k]
 };
+// Checks a rule and fills all of *g but logits, idx and w.
+int group_args(const moe_group_rule* r, int T, int E, int k, const float* bias, GroupArgs* g);
 bool groups_ok(int E, int k, int n_groups, int top, int best);
 int launch_route_groups(const GroupArgs& a, cudaStream_t s);
 

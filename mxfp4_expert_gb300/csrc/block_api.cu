@@ -51,21 +51,35 @@ extern "C" int moe_block_norm(const void* x_dev, int64_t x_stride, int x_is_fp32
   return launch_block_norm(n, di, (cudaStream_t)stream);
 }
 
-extern "C" int moe_route_groups(const float* logits_dev, int T, int E, int k, const float* bias_dev, int score,
-                                int n_groups, int top_groups, int group_best, int renormalise, float scale,
-                                int32_t* idx_dev, float* w_dev, moe_stream_t stream) {
-  MOE_CHECK_ARG(T >= 0 && E >= 1 && k >= 1 && n_groups >= 1 && top_groups >= 1 && top_groups <= n_groups,
+namespace moe {
+
+int group_args(const moe_group_rule* r, int T, int E, int k, const float* bias, GroupArgs* g) {
+  MOE_CHECK_ARG(T >= 0 && E >= 1 && k >= 1 && r->n_groups >= 1 && r->top_groups >= 1 && r->top_groups <= r->n_groups,
                 MOE_ERR_INVALID_ARG);
-  MOE_CHECK_ARG(score == MOE_SCORE_SIGMOID || score == MOE_SCORE_SOFTMAX, MOE_ERR_INVALID_ARG);
-  MOE_CHECK_ARG((group_best == 1 || group_best == 2) && (renormalise == 0 || renormalise == 1) && isfinite(scale),
+  MOE_CHECK_ARG(r->score == MOE_SCORE_SIGMOID || r->score == MOE_SCORE_SOFTMAX, MOE_ERR_INVALID_ARG);
+  MOE_CHECK_ARG((r->group_best == 1 || r->group_best == 2) && (r->renormalise == 0 || r->renormalise == 1) &&
+                    isfinite(r->scale),
                 MOE_ERR_INVALID_ARG);
-  MOE_CHECK_ARG(groups_ok(E, k, n_groups, top_groups, group_best), MOE_ERR_UNSUPPORTED_SHAPE);
+  MOE_CHECK_ARG(groups_ok(E, k, r->n_groups, r->top_groups, r->group_best), MOE_ERR_UNSUPPORTED_SHAPE);
+  *g = GroupArgs{nullptr, bias, T, E, k, r->score == MOE_SCORE_SOFTMAX, r->n_groups, r->top_groups, r->group_best,
+                 r->renormalise, r->scale, nullptr, nullptr};
+  return MOE_OK;
+}
+
+}  // namespace moe
+
+extern "C" int moe_route_groups(const float* logits_dev, int T, int E, int k, const float* bias_dev,
+                                const moe_group_rule* rule, int32_t* idx_dev, float* w_dev, moe_stream_t stream) {
+  MOE_CHECK_ARG(rule, MOE_ERR_INVALID_ARG);
+  GroupArgs g{};
+  int st = group_args(rule, T, E, k, bias_dev, &g);
+  if (st != MOE_OK) return st;
   if (T == 0) return MOE_OK;
   MOE_CHECK_ARG(logits_dev && idx_dev && w_dev, MOE_ERR_INVALID_ARG);
   DeviceInfo di;
-  const int st = current_device(&di);
-  if (st != MOE_OK) return st;
-  const GroupArgs a{logits_dev, bias_dev, T, E, k, score == MOE_SCORE_SOFTMAX, n_groups, top_groups, group_best,
-                    renormalise, scale, idx_dev, w_dev};
-  return launch_route_groups(a, (cudaStream_t)stream);
+  if ((st = current_device(&di))) return st;
+  g.logits = logits_dev;
+  g.idx = idx_dev;
+  g.w = w_dev;
+  return launch_route_groups(g, (cudaStream_t)stream);
 }

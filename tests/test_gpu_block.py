@@ -326,3 +326,62 @@ def test_route_refusals(mx):
     for bad in (dict(k=0), dict(k=40), dict(n_groups=3), dict(n_groups=4, top_groups=5), dict(group_best=3), dict(scale=math.nan)):
         with pytest.raises(mx.MoeError):
             mx.moe_route_groups(**{"logits": l, "k": 2, **bad})
+
+
+# ---- the layer with it ------------------------------------------------------------------------------------------------
+
+@pytest.fixture(scope="module")
+def tiny(mx):
+    import workloads as wl
+    from mxfp4_expert_gb300 import synthetic
+    w = wl.get("tiny")
+    return w, synthetic.build_layer(w, 0)
+
+
+@pytest.mark.parametrize("T", [1, 4, 5, 40, 200])
+@pytest.mark.parametrize("score,n,top,best", [("sigmoid", 8, 3, 2), ("softmax", 4, 2, 1), ("sigmoid", 1, 1, 1)])
+def test_layer_routed_by_groups(mx, tiny, T, score, n, top, best):
+    """Against the oracle's experts, with the routing that the oracle finds for the layer's own logits. Tolerances as for
+    moe_forward: relative L2 5e-3, 2e-2 of the rms an element (or the nearest bf16)."""
+    import oracle_par
+    import workloads as wl
+    from oracle import moe as omoe
+    w, layer = tiny
+    g = _gen(T)
+    x, bias = _bf16(g, T, w.d), torch.randn(w.E, generator=g, device="cuda") * 0.1
+    logits = torch.empty((T, w.E), device="cuda")
+    idx, wts = torch.empty((T, w.k), dtype=torch.int32, device="cuda"), torch.empty((T, w.k), device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kw = dict(score=score, n_groups=n, top_groups=top, group_best=best, scale=2.5)
+    y = mx.moe_forward_groups(layer, x, bias, logits_out=logits, idx_out=idx, w_out=wts, dev_status=status, **kw)
+    assert int(status) == 0
+    alone = mx.moe_route_groups(logits, w.k, bias, **kw)
+    assert torch.equal(alone[0], idx) and torch.equal(alone[1], wts)
+    ri, rw = ob.route_groups(_np(logits), w.k, _np(bias), score, n, top, best, True, 2.5)
+    assert np.array_equal(idx.cpu().numpy(), ri)
+    xs = x.cpu()
+    sg, su, sd = (omoe.as_f64(t) for t in wl.gen_shared(w, 0, "cuda"))
+    ref = omoe.swiglu_ffn(omoe.as_f64(xs), sg, su, sd)
+    for e in np.unique(ri):
+        gu, dn = wl.gen_experts(w, 0, int(e), 1, "cuda")
+        t, j = np.nonzero(ri == e)
+        ref[t] += rw[t, j][:, None] * omoe.expert_outputs(xs[t], gu[0].cpu(), dn[0].cpu())
+    got = _np(y)
+    assert np.linalg.norm(got - ref) <= 5e-3 * np.linalg.norm(ref)
+    rms = np.sqrt(np.mean(ref ** 2))
+    assert np.all((np.abs(got - ref) <= 2e-2 * rms) | (got == oracle_par.bf16_rne(ref)))
+
+
+def test_layer_routed_by_groups_refusals(mx, tiny):
+    w, layer = tiny
+    x = torch.zeros((2, w.d), dtype=BF16, device="cuda")
+    with pytest.raises(ValueError):
+        mx.moe_forward_groups(layer, x, score="tanh")
+    with pytest.raises(ValueError):
+        mx.moe_forward_groups(layer, x, torch.zeros((2, w.E), device="cuda"))
+    with pytest.raises(ValueError):
+        mx.moe_forward_groups(layer, x[:, :64])
+    for bad in (dict(n_groups=5), dict(n_groups=8, top_groups=9), dict(group_best=0), dict(scale=math.nan),
+                dict(workspace=torch.zeros(256, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(mx.MoeError):
+            mx.moe_forward_groups(layer, x, **bad)

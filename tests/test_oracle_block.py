@@ -112,11 +112,15 @@ def test_norm_refusals(mx):
 
 def test_routing_refusals(mx):
     L, p = mx.lib, ctypes.c_void_p(64)
-    ok = dict(l=p, T=2, E=64, k=4, b=None, score=0, n=8, top=4, best=2, renorm=1, scale=1.0, idx=p, w=p)
+    rule = dict(score=0, n=8, top=4, best=2, renorm=1, scale=1.0)
+    ok = dict(l=p, T=2, E=64, k=4, b=None, idx=p, w=p)
 
     def call(**kw):
+        r = mx.moe_group_rule(*({**rule, **{n: v for n, v in kw.items() if n in rule}}[n] for n in rule))
         v = {**ok, **kw}
-        return L.moe_route_groups(*(v[n] for n in ok), None)
+        return L.moe_route_groups(v["l"], v["T"], v["E"], v["k"], v["b"], ctypes.byref(r), v["idx"], v["w"], None)
+    assert L.moe_route_groups(p, 2, 64, 4, None, None, p, p, None) == -1
+    assert L.moe_forward_groups(None, None, p, 2, p, None, None, None, None, p, 0, None, None) == -1
     assert call(T=0) == 0
     for kw in (dict(T=-1), dict(E=0), dict(k=0), dict(n=0), dict(top=0), dict(top=9), dict(score=2), dict(best=0),
                dict(best=3), dict(renorm=2), dict(scale=math.nan), dict(l=None), dict(idx=None), dict(w=None)):
