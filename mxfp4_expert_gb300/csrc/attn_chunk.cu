@@ -71,7 +71,7 @@ struct Plan {
   static constexpr int kStages = D == 128 ? 4 : 8, kRaws = D == 128 ? 2 : 6;
   static constexpr uint32_t kQ = 0, kRing = 2 * kTile, kRawRing = kRing + kStages * kTile;
   static constexpr uint32_t kInfo = kRawRing + kRaws * kRaw;
-  static constexpr uint32_t kBars = kInfo + kSlots * 32;
+  static constexpr uint32_t kBars = kInfo + kSlots * 64;
   static constexpr int kNBars = 2 * kRaws + 2 * kStages + 2 + 4 + 2 * 6 + 2 + 4 + 2 * kSlots;
   static constexpr uint32_t kItems = kBars + kNBars * 8;
   static constexpr uint32_t kTotal = kItems + 2 * 96 + 16 + 1024;   // + alignment slack
@@ -92,9 +92,10 @@ static_assert(sizeof(Item) <= 96, "item");
 
 // Scale bytes of a key tile's eight groups of 16 positions, groups without a page;
 // NaN found by each converter warp in a tile of values.
-struct __align__(32) Info {
-  uint32_t k[2], v[2], bad;
+struct __align__(64) Info {
+  uint32_t k[2], bad;
   uint8_t poison[4];
+  float v[8];
 };
 
 // What a CTA leaves for the join.
@@ -485,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           if (!ok) break;
           if (lane < 8) {
             reinterpret_cast<uint8_t*>(info[slot].k)[lane] = uint8_t(sc);
-            reinterpret_cast<uint8_t*>(info[slot].v)[lane] = uint8_t(sc >> 8);
+            info[slot].v[lane] = float(int(sc >> 8) - 127);
           }
           __threadfence_block();
           __syncwarp();
@@ -706,8 +707,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       // references: score sr of a page with scale byte kr (none yet: have = false), its factor cr, so the score m in
       // log2; value reference rv above m; sum l in units of 2^m, O in units of 2^(m + rv - 8)
       bool have = false;
-      float sr = 0.0f, cr = 0.0f, m = 0.0f, l = 0.0f;
-      int kr = 0, rv = 0;              // of a scale byte below all, so that above() takes scores as they are
+      float sr = 0.0f, cr = 0.0f, m = 0.0f, l = 0.0f, rv = 0.0f;
+      int kr = 0;              // of a scale byte below all, so that above() takes scores as they are
       unsigned bad = 0;                // masked tiles with NaN (an item's rows span at most 256 tokens)
       for (int i = 0; i < nkt; ++i) {
         const int k0 = (it.t0 + i) * kKT, slot = (tiles + i) % kSlots;
@@ -723,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           if (!bar_wait(&s_full[2 * j + half], ph, abort, status)) ok = false;
           // complete by now, and for this tile: a warp that had nothing to do for an item is far ahead of its ring
           if (!bar_wait(&info_full[slot], slot_ph, abort, status)) ok = false;
-          const uint32_t kb4 = info[slot].k[half], vb4 = info[slot].v[half];
+          const uint32_t kb4 = info[slot].k[half];
           const unsigned none = info[slot].bad;
           if (half == 1) {   // the products before these scores are done, too: their values are released with the keys
             if (warp == kWSoft + 4 * j && lane == 0) {
@@ -755,12 +756,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           // a group of keys: factor of its scores, its largest score, how far that is above the reference
           constexpr int GK = 64 / NG, GB = 4 / NG;      // keys, scale bytes of a group
           float ck[NG], mx[NG], d[NG];
-          int kb[NG], ve[NG];
+          int kb[NG];
+          float ve[NG];
           float dm = -INFINITY, dy = -INFINITY;
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
             kb[g] = int(kb4 >> (8 * GB * g)) & 255;
-            ve[g] = (int(vb4 >> (8 * GB * g)) & 255) - 127;
+            ve[g] = info[slot].v[4 * half + GB * g];
             float a0 = -INFINITY, a1 = -INFINITY;
 #pragma unroll
             for (int z = g * GK; z < (g + 1) * GK; z += 16) {
@@ -773,12 +775,31 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             }
             mx[g] = fmaxf(a0, a1);
             ck[g] = __uint_as_float(__float_as_uint(P.cm) + (uint32_t(min(max(ce + kb[g] - 127, -100), 126)) << 23));
-            d[g] = above(mx[g], kb[g], ck[g], sr, kr, cr);
-            dm = fmaxf(dm, d[g]);
-            dy = fmaxf(dy, d[g] + float(ve[g]));
           }
-          const bool raise = have ? dm > kRaiseSum || dy > float(rv) + kRaiseOut : dm > -INFINITY;
-          if (__any_sync(0xFFFFFFFFu, raise)) {
+          // Short pages: whether one's largest lies too far above the references is seen from fp32 differences first,
+          // which tell it to 2^-6 while a reference is not far.
+          bool look = true;
+          if (NG > 1) {
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+              d[g] = fmaf(mx[g], ck[g], -m);
+              dm = fmaxf(dm, d[g]);
+              dy = fmaxf(dy, d[g] + ve[g]);
+            }
+            look = __any_sync(0xFFFFFFFFu, !have || fabsf(m) > kFar || dm > kRaiseSum || dy > rv + kRaiseOut);
+            dm = dy = -INFINITY;
+          }
+          bool raise = false;
+          if (look) {
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+              d[g] = above(mx[g], kb[g], ck[g], sr, kr, cr);
+              dm = fmaxf(dm, d[g]);
+              dy = fmaxf(dy, d[g] + ve[g]);
+            }
+            raise = have ? dm > kRaiseSum || dy > rv + kRaiseOut : dm > -INFINITY;
+          }
+          if (look && __any_sync(0xFFFFFFFFu, raise)) {
             float fl = 1.0f, fo = 1.0f;
             if (raise) {
               float top = have ? 0.0f : -INFINITY;     // of the new reference above the old one
@@ -789,12 +810,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 if (d[g] > top) top = d[g], nsr = mx[g], ncr = ck[g], nkr = kb[g];
               sr = nsr, cr = ncr, kr = nkr;
               m = sr * cr;
-              float y = have ? float(rv) - top : -INFINITY;
+              float y = have ? rv - top : -INFINITY;
 #pragma unroll
-              for (int g = 0; g < NG; ++g) y = fmaxf(y, above(mx[g], kb[g], ck[g], sr, kr, cr) + float(ve[g]));
-              const int nrv = int(ceilf(fminf(fmaxf(y, -1000.0f), 1000.0f)));
+              for (int g = 0; g < NG; ++g) y = fmaxf(y, above(mx[g], kb[g], ck[g], sr, kr, cr) + ve[g]);
+              const float nrv = ceilf(fminf(fmaxf(y, -1000.0f), 1000.0f));
               fl = have ? pf_ex2(-top) : 0.0f;
-              fo = have ? pf_ex2(float(rv - nrv) - top) : 0.0f;
+              fo = have ? pf_ex2(rv - nrv - top) : 0.0f;
               rv = nrv;
               have = true;
             }
@@ -838,8 +859,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 #pragma unroll
             for (int u = 0; u < 32; u += SB) {
               const int g = (32 * b + u) / GK;
-              const int t = min(max(ve[g] - rv + int(kPBias), -60), 126);
-              const uint64_t c2 = pack2(ck[g], ck[g]), r2 = pack2(float(t) - ref, float(t) - ref);
+              const float t = fminf(fmaxf(ve[g] - rv + kPBias, -60.0f), 126.0f);
+              const uint64_t c2 = pack2(ck[g], ck[g]), r2 = pack2(t - ref, t - ref);
               uint32_t* x = &s[b][u];
               float e[SB];
 #pragma unroll
@@ -858,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 for (int z = 0; z < 4; ++z) sum[z] = add2(sum[z], pack2(e[y + 2 * z], e[y + 2 * z + 1]));
               float a0, a1;
               unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a0, a1);
-              l = fmaf(a0 + a1, pow2c(-t), l);
+              l = fmaf(a0 + a1, pf_ex2(-t), l);
             }
             tmem_st16(ta + 32 * half + 16 * b, pb);
           }
@@ -893,7 +914,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       const int64_t orow = (int64_t)(it.q0 + tok) * a.n_heads + head;
       __nv_bfloat16* out = a.out + orow * D;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      const float f0 = pow2c((rv - int(kPBias)) >> 1), f1 = pow2c((rv - int(kPBias)) - ((rv - int(kPBias)) >> 1));
+      const int ov = int(rv) - int(kPBias);
+      const float f0 = pow2c(ov >> 1), f1 = pow2c(ov - (ov >> 1));
       float4* part = P.parts + (size_t)(it.slot < 0 ? 0 : it.slot) * (256 * (D / 4 + 1)) + j * kQT + row;
 #pragma unroll 1
       for (int x = 0; x < D; x += 32) {
@@ -947,7 +969,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       st = st_end;
       if (mine) {
         if (it.slot >= 0)
-          part[(size_t)(D / 4) * 256] = make_float4(sr, cr, l, __int_as_float((rv << 8) | kr));
+          part[(size_t)(D / 4) * 256] = make_float4(sr, cr, l, __int_as_float((int(rv) << 8) | kr));
         else if (a.lse)
           a.lse[orow] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2f;
       }
