@@ -6,9 +6,14 @@
 //
 // A CTA takes a row at a time, which stays in registers from the read of a and x to
 // the writes of y and h, so every element crosses memory once; the next row's reads
-// are on their way meanwhile, and the weights stay for all rows. Bound by HBM (8
-// bytes an element with a bf16 stream); a single row by the launch and its chain of
-// a read and two sums over the CTA. h comes from y before its rounding.
+// are on their way meanwhile, and the weights stay for all rows. h comes from y
+// before its rounding.
+//
+// Bound by HBM, 8 bytes an element with a bf16 stream: 4,096 rows of 2,560 in 18.0 us
+// (4.7 TB/s; a fill alone writes 4.1), 1,001 of 7,168 with an fp32 stream and a gate
+// per token in 20.8 (4.8 TB/s). A ring of bulk copies in place of the reads into
+// registers took 21.2 to 23.8 and 21.9 us. One row of 2,560: 3.4 us, the launch and a
+// chain of a read and two sums over the CTA.
 #include "block.h"
 #include "common.cuh"
 #include "f32x2.cuh"
@@ -16,7 +21,7 @@
 namespace moe {
 namespace {
 
-constexpr int kNormMaxThreads = 1024;
+constexpr int kNormThreads = 512;    // at most: a thread may then have 128 registers
 
 // Sum over the CTA; s: one float a warp, not used by the sum before.
 __device__ __forceinline__ float cta_sum(float v, float* s) {
@@ -207,7 +212,7 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, int64_t t, const Raw
 // stay in registers for all rows of the CTA, and the next row is read while one is
 // worked on; for that rows must not be too long.
 template <int V, bool kF32, bool HAS_A, bool AHEAD>
-__global__ void __launch_bounds__(V <= 2 ? 512 : kNormMaxThreads) block_norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kNormThreads) block_norm_kernel(const NormArgs a) {
   __shared__ float s[4][32];
   const int tid = threadIdx.x, nt = blockDim.x;
   const bool gate_row = HAS_A && a.gate && a.g_rs != 0;
@@ -253,7 +258,7 @@ __global__ void __launch_bounds__(V <= 2 ? 512 : kNormMaxThreads) block_norm_ker
 
 template <int V, bool kF32, bool HAS_A>
 int launch_norm(const NormArgs& a, int threads, const DeviceInfo& di, cudaStream_t s) {
-  constexpr bool kAhead = V <= 2;
+  constexpr bool kAhead = V <= 3;
   int per_sm = 8;
   if (kAhead && a.T > di.sm_count)
     MOE_CUDA_TRY(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, block_norm_kernel<V, kF32, HAS_A, kAhead>, threads, 0));
@@ -262,18 +267,26 @@ int launch_norm(const NormArgs& a, int threads, const DeviceInfo& di, cudaStream
   return launch_status();
 }
 template <int V>
-int launch_v(const NormArgs& a, int threads, const DeviceInfo& di, cudaStream_t s) {
+int launch_v(const NormArgs& a, const DeviceInfo& di, cudaStream_t s) {
+  const int threads = int(round_up((a.d / 8 + V - 1) / V, 32));
   if (a.fp32) return a.a ? launch_norm<V, true, true>(a, threads, di, s) : launch_norm<V, true, false>(a, threads, di, s);
   return a.a ? launch_norm<V, false, true>(a, threads, di, s) : launch_norm<V, false, false>(a, threads, di, s);
 }
 
 }  // namespace
 
+// Vectors a thread. One up to 256 threads; with more of them a row's sums cost more than its channels, and two are
+// better (4,096 rows of 2,560: 320 threads with one 20.5 us, 160 with two 18.0), as many as registers hold where 512
+// threads need more. Three with the next row ahead against four without, 1,000 rows of 12,288: 28.8 to 47.8 us; a row
+// shared by a cluster of two CTAs 47.2. Rows beyond 16,384 channels leave registers (1,000 of 16,384: 42 us, 500 of
+// 32,768 with an fp32 stream 139).
 int launch_block_norm(const NormArgs& a, const DeviceInfo& di, cudaStream_t s) {
   const int vecs = a.d / 8;
-  const int v = vecs <= (a.T <= di.sm_count ? 512 : 256) ? 1 : vecs <= 1024 ? 2 : 4;
-  const int threads = int(round_up((vecs + v - 1) / v, 32));
-  return v == 1 ? launch_v<1>(a, threads, di, s) : v == 2 ? launch_v<2>(a, threads, di, s) : launch_v<4>(a, threads, di, s);
+  if (vecs <= 256) return launch_v<1>(a, di, s);
+  if (vecs <= 2 * kNormThreads) return launch_v<2>(a, di, s);
+  if (vecs <= 3 * kNormThreads) return launch_v<3>(a, di, s);
+  if (vecs <= 4 * kNormThreads) return launch_v<4>(a, di, s);
+  return launch_v<8>(a, di, s);
 }
 
 }  // namespace moe
