@@ -535,7 +535,8 @@ int moe_kv_append_fp8(const moe_kv_cache* cache, const moe_rows* k, const moe_ro
  *   q_out_dev       bf16 [total][n_heads][head_dim] (contiguous, 16-B aligned);
  *                   rows outside every sequence are not written
  * Other arguments, status and errors as moe_kv_append_fp8 (a turned key beyond
- * fp32 counts as infinite); MOE_ERR_UNSUPPORTED_SHAPE also for rot_dim. */
+ * fp32 counts as infinite); MOE_ERR_UNSUPPORTED_SHAPE also for rot_dim and for
+ * n_heads + 2 n_kv_heads > 65535. */
 int moe_kv_append_rope_fp8(const moe_kv_cache* cache, const moe_rows* k, const moe_rows* v, const int32_t* cu_dev,
                            const int32_t* start_dev, int n_seq, int total, const int32_t* page_table_dev,
                            int table_width, const float* inv_freq_dev, int rot_dim, int interleaved,

@@ -153,7 +153,8 @@ extern "C" int moe_kv_append_rope_fp8(const moe_kv_cache* cache, const moe_rows*
                        &empty);
   if (st != MOE_OK) return st;
   MOE_CHECK_ARG(rot_dim >= 16 && rot_dim % 16 == 0 && rot_dim <= cache->head_dim, MOE_ERR_UNSUPPORTED_SHAPE);
-  MOE_CHECK_ARG(!q || (n_heads >= 1 && n_heads <= 65535), MOE_ERR_UNSUPPORTED_SHAPE);
+  // a launch may count every head of keys, values and queries in its grid's second size
+  MOE_CHECK_ARG(!q || (n_heads >= 1 && n_heads + 2 * cache->n_kv_heads <= 65535), MOE_ERR_UNSUPPORTED_SHAPE);
   if (empty) return MOE_OK;
   MOE_CHECK_ARG(inv_freq_dev, MOE_ERR_INVALID_ARG);
   if (q) {

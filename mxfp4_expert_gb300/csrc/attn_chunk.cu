@@ -39,6 +39,21 @@
 // Masked places must not count, whatever they hold, but 0 * NaN is NaN in the
 // second product: in a tile that some row of the item does not see whole the
 // converters put 0 for NaN; the rows that see it get it back at the end.
+//
+// Measured: the last 4,096 tokens of 32,768, 32 heads over 4 of 128, in 1,653 us (1,250
+// TFLOP/s, 0.65 of the GEMM rate), 4 x 256 behind 65,536 each in 862. What bounds it
+// for heads of 128 is shared memory: a key tile costs 256 rows 2,066 wavefronts of
+// tensor operands (Q is read once for each half), about 1,120 of the converters and
+// 256 of the copies, of 3,950 cycles. Heads of 64 in short pages are bound by the
+// softmax threads (24 follow-ups of 62 tokens on average: 130 us, 4,600 cycles a tile),
+// items of few rows by the converters (2,200 cycles a tile), a single short call by its
+// chain (37 tokens behind 5,000: 34 us).
+// - Instructions have to be few as well: with long waits in line, the converters' loop
+//   unrolled and every mask in its own pass, the same took 1,122 instead of 888 us.
+// - Scores of 128 keys in one product read Q once, but a tile's chain of products then
+//   stands between two softmax passes: 1,098 instead of 868 us for 4 x 256.
+// - Moving registers between the roles (setmaxnreg) 905 instead of 870, the next half's
+//   scores fetched early 954 to 983 instead of 888, no turns between the MMA warps 880.
 #include <math.h>
 
 #include "attn.h"
@@ -60,7 +75,7 @@ constexpr float kFar = 131072.0f;
 constexpr float kLn2f = 0.6931471805599453f;
 // Work of an item beside its keys, in keys, and the least work of a CTA, in keys of
 // a whole group: cuts of one item are then more than a tile apart (an item of n >= 2
-// tiles costs at most G (128 n + 128 + 1) + 256, so a tile at most 193 G + 128).
+// tiles costs at most G (128 n + 256 + 1) + 256, so a tile at most 257 G + 128).
 constexpr int kItemKeys = 256, kCtaKeys = 512;
 
 template <int D>
@@ -90,8 +105,9 @@ struct Item {
 };
 static_assert(sizeof(Item) <= 96, "item");
 
-// Scale bytes of a key tile's eight groups of 16 positions, groups without a page;
-// NaN found by each converter warp in a tile of values.
+// A key tile's eight groups of 16 positions: scale bytes of the keys, exponents of the
+// values' scales, groups without a page; NaN that each converter warp found in the
+// values.
 struct __align__(64) Info {
   uint32_t k[2], bad;
   uint8_t poison[4];

@@ -8,13 +8,20 @@
 // merged by log2 L shuffles and a group is dropped by its own lanes.
 //
 // Selection must not hang on the rounding of an exponential: with a bias two
-// keys may lie closer than fp32 tells. A score therefore is a pair of fp32
-// numbers (high, low; about 2^-42 of it), keys are compared by both, and without
-// a bias the logits themselves are, of which the scores are monotone. The
-// exponential: exp(x) = 2^n exp(j/32) exp(r), |r| <= 1/64, exp(j/32) from a table
-// of pairs that the lanes hold (P. T. P. Tang, "Table-driven implementation of the
-// exponential function", 1989), exp(r) its Taylor series, of which the terms up
+// keys may lie closer than fp32 tells. Keys are taken in fp32 first; what lies so
+// close to a neighbour in rank, or to the cut, that their errors could turn it
+// (doubt()) is ranked once more by pairs of fp32 numbers (high, low; about 2^-42 of a
+// score): the few candidates of a sigmoid's, all of a token where its groups are in
+// doubt or its scores are a softmax, whose sum is wanted as a pair, too.
+// Without a bias the logits themselves rank, of which the scores are monotone. The
+// exponential of a pair: exp(x) = 2^n exp(j/32) exp(r), |r| <= 1/64, exp(j/32) from a
+// table of pairs that the lanes hold (P. T. P. Tang, "Table-driven implementation of
+// the exponential function", 1989), exp(r) its Taylor series, of which the terms up
 // to r^2 are pairs.
+//
+// Bound by instructions: 4,096 tokens over 512 experts in 8 groups, the 8 best of 4,
+// in 19.8 us (0.42 TB/s of logits; pairs for every key 49), 16,384 over 160 in 19.8. A
+// batch of 64 tokens takes 8.2, one token's chain of k + groups reductions.
 #include <math.h>
 
 #include "block.h"

@@ -180,3 +180,10 @@ def test_binding_checks_before_the_gpu(mx):
         mx.moe_block_norm(x)
     with pytest.raises(ValueError):
         mx.moe_route_groups(x, 2, score="tanh")
+
+
+def test_rope_refuses_more_heads_than_a_grid_has(mx):
+    p, r = ctypes.c_void_p(64), mx.moe_rows(64, 128, 64)
+    c = _cache(mx)
+    n = 65536 - 2 * c.n_kv_heads
+    assert mx.lib.moe_kv_append_rope_fp8(c, r, r, p, p, 2, 5, p, 2, p, 64, 0, None, r, n, p, None, None) == -2
