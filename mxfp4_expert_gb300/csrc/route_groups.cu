@@ -11,8 +11,8 @@
 // keys may lie closer than fp32 tells. Keys are taken in fp32 first; what lies so
 // close to a neighbour in rank, or to the cut, that their errors could turn it
 // (doubt()) is ranked once more by pairs of fp32 numbers (high, low; about 2^-42 of a
-// score): the few candidates of a sigmoid's, all of a token where its groups are in
-// doubt or its scores are a softmax, whose sum is wanted as a pair, too.
+// score): the few candidates mostly (and a softmax's sum), all of a token where it is
+// not clear which experts make a group's score.
 // Without a bias the logits themselves rank, of which the scores are monotone. The
 // exponential of a pair: exp(x) = 2^n exp(j/32) exp(r), |r| <= 1/64, exp(j/32) from a
 // table of pairs that the lanes hold (P. T. P. Tang, "Table-driven implementation of
@@ -20,8 +20,8 @@
 // to r^2 are pairs.
 //
 // Bound by instructions: 4,096 tokens over 512 experts in 8 groups, the 8 best of 4,
-// in 19.8 us (0.42 TB/s of logits; pairs for every key 49), 16,384 over 160 in 19.8. A
-// batch of 64 tokens takes 8.2, one token's chain of k + groups reductions.
+// in 17.8 us (0.47 TB/s of logits; pairs for every key 49), 16,384 over 160 in 19.8. A
+// batch of 64 tokens takes 7.5, one token's chain of k + groups reductions.
 #include <math.h>
 
 #include "block.h"
@@ -122,6 +122,9 @@ __device__ __forceinline__ F2 pair_sigmoid(float x, const F2& tab) {
   const F2 e = exp_pair({-fabsf(x), 0.0f}, tab), d = add({1.0f, 0.0f}, e);
   return x >= 0.0f ? div({1.0f, 0.0f}, d) : div(e, d);
 }
+__device__ __forceinline__ F2 pair_score(bool softmax, float x, float top, const F2& sum, const F2& tab) {
+  return softmax ? div(exp_pair(two_sum(x, -top), tab), sum) : pair_sigmoid(x, tab);
+}
 // Finite logit; *nan.
 __device__ __forceinline__ float logit(float x, bool* nan) {
   *nan = isnan(x);
@@ -131,6 +134,29 @@ __device__ __forceinline__ float logit(float x, bool* nan) {
 __device__ __forceinline__ F2 pair_key(const F2& s, float b, bool nan) {
   if (nan) return {-INFINITY, 0.0f};
   return fabsf(b) <= kFmax ? add({b, 0.0f}, s) : F2{isnan(b) ? -INFINITY : b, 0.0f};
+}
+
+// Sum of exp(l - top) over a token's experts (whole warp, all lanes the same); top is the largest logit. Two terms at a
+// time, since one is a long chain.
+__device__ __noinline__ F2 pair_sum(const float* row, int E, float top) {
+  const int lane = threadIdx.x & 31;
+  const F2 tab{kExpTable.hi[lane], kExpTable.lo[lane]};
+  F2 s0{0.0f, 0.0f}, s1{0.0f, 0.0f};
+#pragma unroll 1
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    bool nan0 = true, nan1 = true;
+    const int e = e0 + lane;
+    const float l0 = e < E ? logit(row[e], &nan0) : 0.0f, l1 = e + 32 < E ? logit(row[e + 32], &nan1) : 0.0f;
+    const F2 v0 = exp_pair(two_sum(l0, -top), tab), v1 = exp_pair(two_sum(l1, -top), tab);
+    if (!nan0) s0 = add(s0, v0);
+    if (!nan1) s1 = add(s1, v1);
+  }
+  F2 sum = add(s0, s1);
+  for (int o = 1; o < 32; o <<= 1) {
+    const F2 other{__shfl_xor_sync(0xFFFFFFFFu, sum.hi, o), __shfl_xor_sync(0xFFFFFFFFu, sum.lo, o)};
+    sum = (lane & o) ? add(other, sum) : add(sum, other);   // the same in both lanes
+  }
+  return sum.hi == 0.0f ? F2{1.0f, 0.0f} : sum;
 }
 
 // One token with every score as a pair (whole warp): keys to shared memory [n][32]
@@ -150,18 +176,7 @@ __device__ __noinline__ int route_in_pairs(const GroupArgs& a, const float* row,
       if (!nan) top_l = fmaxf(top_l, l);
     }
     for (int o = 16; o > 0; o >>= 1) top_l = fmaxf(top_l, __shfl_xor_sync(0xFFFFFFFFu, top_l, o));
-#pragma unroll 1
-    for (int j = 0; j < all; ++j) {
-      bool nan = true;
-      const float l = j < n ? logit(row[g * size + u + j * L], &nan) : 0.0f;
-      const F2 e = exp_pair(two_sum(l, -top_l), tab);
-      if (!nan) sum = add(sum, e);
-    }
-    for (int o = 1; o < 32; o <<= 1) {
-      const F2 other{__shfl_xor_sync(0xFFFFFFFFu, sum.hi, o), __shfl_xor_sync(0xFFFFFFFFu, sum.lo, o)};
-      sum = (lane & o) ? add(other, sum) : add(sum, other);   // the same in both lanes
-    }
-    if (sum.hi == 0.0f) sum = {1.0f, 0.0f};
+    sum = pair_sum(row, a.E, top_l);
   }
   F2 b0{-INFINITY, 0.0f}, b1{-INFINITY, 0.0f};                 // the two best of this lane's, for its group
   auto take = [&](const F2& v) {
@@ -220,7 +235,7 @@ __device__ __noinline__ int route_in_pairs(const GroupArgs& a, const float* row,
 
 // PL: experts a lane holds.
 template <int PL>
-__global__ void __launch_bounds__(kGrpWarps * 32, PL <= 8 ? 8 : PL <= 16 ? 7 : 3) route_groups_kernel(const GroupArgs a, int L) {
+__global__ void __launch_bounds__(kGrpWarps * 32, PL <= 8 ? 8 : PL <= 16 ? 7 : 4) route_groups_kernel(const GroupArgs a, int L) {
   extern __shared__ uint32_t s_keys[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x * kGrpWarps + warp;
@@ -278,7 +293,11 @@ __global__ void __launch_bounds__(kGrpWarps * 32, PL <= 8 ? 8 : PL <= 16 ? 7 : 3
     }
     uint32_t key[PL];
 #pragma unroll
-    for (int j = 0; j < PL; ++j) key[j] = held(j) ? rank_key(a.bias ? s[j] + b[j] : l[j]) : 0u;
+    for (int j = 0; j < PL; ++j) {
+      const float v = a.bias ? s[j] + b[j] : l[j];
+      key[j] = held(j) ? rank_key(v) : 0u;
+      s[j] = a.bias || a.best == 1 ? v : s[j];       // from here on: what counts for the group
+    }
 
     if (a.top < a.n_groups) {
       // a group's score: its best key, or the sum of its two best (without a bias, of their scores)
@@ -289,7 +308,7 @@ __global__ void __launch_bounds__(kGrpWarps * 32, PL <= 8 ? 8 : PL <= 16 ? 7 : 3
       };
 #pragma unroll
       for (int j = 0; j < PL; ++j)
-        if (held(j)) take(a.bias ? s[j] + b[j] : a.best > 1 ? s[j] : l[j]);
+        if (held(j)) take(s[j]);
       for (int o = 1; o < L; o <<= 1) {
         const float o0 = __shfl_xor_sync(0xFFFFFFFFu, b0, o), o1 = __shfl_xor_sync(0xFFFFFFFFu, b1, o);
         take(o0);
@@ -306,25 +325,26 @@ __global__ void __launch_bounds__(kGrpWarps * 32, PL <= 8 ? 8 : PL <= 16 ? 7 : 3
         const int out = __ffs(__ballot_sync(0xFFFFFFFFu, g < a.n_groups && better == a.top)) - 1;
         const float v = __shfl_sync(0xFFFFFFFFu, score, in), w = __shfl_sync(0xFFFFFFFFu, score, out);
         if (v - w <= 2.0f * doubt(a.softmax, s_max, fabsf(v) + fabsf(w))) {
-          // Rank the groups by sums of pairs, where it is clear of which experts. (A softmax wants its sum as a pair.)
+          // Rank the groups by sums of pairs, where it is clear of which experts.
           const float from_key = (a.best > 1 ? b1 : b0) - doubt(a.softmax, s_max, fabsf(b0) + fabsf(b1));
           int n = 0, e0 = -1, e1 = -1;           // this lane's experts that may count
 #pragma unroll
           for (int j = 0; j < PL; ++j)
-            if (held(j) && (a.bias ? s[j] + b[j] : a.best > 1 ? s[j] : l[j]) >= from_key) {
+            if (held(j) && s[j] >= from_key) {
               e1 = n ? expert(j) : -1;
               if (!n) e0 = expert(j);
               ++n;
             }
           int of_group = n;
           for (int o = 1; o < L; o <<= 1) of_group += __shfl_xor_sync(0xFFFFFFFFu, of_group, o);
-          unsure = a.softmax || __any_sync(0xFFFFFFFFu, g < a.n_groups && of_group != a.best);
+          unsure = __any_sync(0xFFFFFFFFu, g < a.n_groups && of_group != a.best);
           if (!unsure) {
             const F2 tab{kExpTable.hi[lane], kExpTable.lo[lane]};
+            const F2 of_all = a.softmax ? pair_sum(row, a.E, l_max) : F2{1.0f, 0.0f};
             F2 sum{0.0f, 0.0f};
             for (int i = 0; i < a.best; ++i) {
               const int e = i ? e1 : e0;
-              const F2 x = pair_sigmoid(e >= 0 ? row[e] : 0.0f, tab);
+              const F2 x = pair_score(a.softmax, e >= 0 ? row[e] : l_max, l_max, of_all, tab);
               if (e >= 0) sum = add(sum, a.bias ? add({a.bias[e], 0.0f}, x) : x);
             }
             for (int o = 1; o < L; o <<= 1) {
@@ -346,25 +366,33 @@ __global__ void __launch_bounds__(kGrpWarps * 32, PL <= 8 ? 8 : PL <= 16 ? 7 : 3
     }
 
     // ---- the best keys, equal ones by the lower expert -------------------------------
-    uint32_t bk;
-    int bj;
+    // a lane's two best, for it is seldom asked for a third
+    uint32_t bk, ck, gone = 0u;
+    int bj, cj;
     auto local_best = [&]() {
-      bk = 0u;
-      bj = 0;
+      bk = ck = 0u;
+      bj = cj = 0;
 #pragma unroll
-      for (int j = 0; j < PL; ++j)
-        if (key[j] > bk) bk = key[j], bj = j;
+      for (int j = 0; j < PL; ++j) {
+        const uint32_t v = (gone >> j) & 1u ? 0u : key[j];
+        const bool first = v > bk, second = v > ck;
+        ck = first ? bk : second ? v : ck;
+        cj = first ? bj : second ? j : cj;
+        bk = first ? v : bk;
+        bj = first ? j : bj;
+      }
     };
     local_best();
+    bool two = true;
     uint32_t my_key = 0u;
     auto next_best = [&](int r) {      // to lane r; false: there is none
       const uint32_t h = __reduce_max_sync(0xFFFFFFFFu, bk);
       const int e = __reduce_min_sync(0xFFFFFFFFu, bk == h ? expert(bj) : 0x7FFFFFFF);
       if (bk == h && expert(bj) == e) {
-#pragma unroll
-        for (int j = 0; j < PL; ++j)
-          if (j == bj) key[j] = 0u;
-        local_best();
+        gone |= 1u << bj;
+        bk = ck, bj = cj;
+        if (!two) local_best();
+        two = !two;
       }
       if (lane == r) my_e = e, my_key = h;
       return h != 0u;
@@ -391,24 +419,20 @@ __global__ void __launch_bounds__(kGrpWarps * 32, PL <= 8 ? 8 : PL <= 16 ? 7 : 3
       }
       if (close && !unsure) {       // rank the candidates by their keys as pairs
         const F2 tab{kExpTable.hi[lane], kExpTable.lo[lane]};
-        F2 e{0.0f, 0.0f};
-        if (a.softmax) {
-          unsure = true;            // the sum over all experts is wanted as a pair, too
-        } else {
-          e = add({mb, 0.0f}, pair_sigmoid(ml, tab));
-          int before = 0;
-          for (int i = 0; i < n; ++i) {
-            const F2 v{__shfl_sync(0xFFFFFFFFu, e.hi, i), __shfl_sync(0xFFFFFFFFu, e.lo, i)};
-            const int id = __shfl_sync(0xFFFFFFFFu, my_e, i);
-            before += less(e, v) || (!less(v, e) && id < my_e);
-          }
-          int mine = 0;
-          for (int i = 0; i < n; ++i) {
-            const int at = __shfl_sync(0xFFFFFFFFu, before, i), id = __shfl_sync(0xFFFFFFFFu, my_e, i);
-            if (at == lane) mine = id;
-          }
-          my_e = mine;
+        const F2 of_all = a.softmax ? pair_sum(row, a.E, l_max) : F2{1.0f, 0.0f};
+        const F2 e = add({mb, 0.0f}, pair_score(a.softmax, lane < n ? ml : l_max, l_max, of_all, tab));
+        int before = 0;
+        for (int i = 0; i < n; ++i) {
+          const F2 v{__shfl_sync(0xFFFFFFFFu, e.hi, i), __shfl_sync(0xFFFFFFFFu, e.lo, i)};
+          const int id = __shfl_sync(0xFFFFFFFFu, my_e, i);
+          before += less(e, v) || (!less(v, e) && id < my_e);
         }
+        int mine = 0;
+        for (int i = 0; i < n; ++i) {
+          const int at = __shfl_sync(0xFFFFFFFFu, before, i), id = __shfl_sync(0xFFFFFFFFu, my_e, i);
+          if (at == lane) mine = id;
+        }
+        my_e = mine;
       }
     }
   }
@@ -417,11 +441,10 @@ __global__ void __launch_bounds__(kGrpWarps * 32, PL <= 8 ? 8 : PL <= 16 ? 7 : 3
   // ---- weights ------------------------------------------------------------------------
   if (a.softmax && __any_sync(0xFFFFFFFFu, odd)) {     // the largest finite logit, or what an infinite one counts as
     l_max = -kFmax;
-#pragma unroll
-    for (int j = 0; j < PL; ++j) {
+    for (int e = lane; e < a.E; e += 32) {
       bool nan;
-      const float x = logit(l[j], &nan);
-      if (!nan && held(j)) l_max = fmaxf(l_max, x);
+      const float x = logit(row[e], &nan);
+      if (!nan) l_max = fmaxf(l_max, x);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l_max = fmaxf(l_max, __shfl_xor_sync(0xFFFFFFFFu, l_max, o));
@@ -444,11 +467,11 @@ __global__ void __launch_bounds__(kGrpWarps * 32, PL <= 8 ? 8 : PL <= 16 ? 7 : 3
   // in a quotient of scores the sum of all drops out, but for the 1e-20, which is less than 2^-26 of more than 1e-9
   if (a.softmax && !(a.renorm && all > 1e-9f)) {
     sum = 0.0f;
-#pragma unroll
-    for (int j = 0; j < PL; ++j) {
+#pragma unroll 4
+    for (int e = lane; e < a.E; e += 32) {
       bool nan;
-      const float x = logit(l[j], &nan);
-      if (!nan && held(j)) sum += expf(x - l_max);
+      const float x = logit(row[e], &nan);
+      if (!nan) sum += expf(x - l_max);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
