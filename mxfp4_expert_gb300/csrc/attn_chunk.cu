@@ -40,14 +40,14 @@
 // second product: in a tile that some row of the item does not see whole the
 // converters put 0 for NaN; the rows that see it get it back at the end.
 //
-// Measured: the last 4,096 tokens of 32,768, 32 heads over 4 of 128, in 1,653 us (1,250
-// TFLOP/s, 0.65 of the GEMM rate), 4 x 256 behind 65,536 each in 862. What bounds it
+// Measured: the last 4,096 tokens of 32,768, 32 heads over 4 of 128, in 1,650 us (1,250
+// TFLOP/s, 0.65 of the GEMM rate), 4 x 256 behind 65,536 each in 860. What bounds it
 // for heads of 128 is shared memory: a key tile costs 256 rows 2,066 wavefronts of
 // tensor operands (Q is read once for each half), about 1,120 of the converters and
 // 256 of the copies, of 3,950 cycles. Heads of 64 in short pages are bound by the
 // softmax threads (24 follow-ups of 62 tokens on average: 130 us, 4,600 cycles a tile),
 // items of few rows by the converters (2,200 cycles a tile), a single short call by its
-// chain (37 tokens behind 5,000: 34 us).
+// chain (37 tokens behind 5,000: 33 us).
 // - Instructions have to be few as well: with long waits in line, the converters' loop
 //   unrolled and every mask in its own pass, the same took 1,122 instead of 888 us.
 // - Scores of 128 keys in one product read Q once, but a tile's chain of products then
@@ -1009,25 +1009,30 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const Params P) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x, x = blockIdx.y, row = threadIdx.x;
   const Desc d = P.desc[c];
-  if (!d.last || row >= d.rows) return;
+  if (!d.last) return;
   constexpr size_t kSlot = 256 * (D / 4 + 1);
   int last = c + 1;                // the last CTA with a part
-  while (P.desc[last].first & 2) ++last;
+  for (unsigned ends = 0; !ends; last += ends ? __ffs(ends) - 1 : 32) {
+    const int i = last + (threadIdx.x & 31);
+    ends = __ballot_sync(0xFFFFFFFFu, i > int(gridDim.x) || !(P.desc[i].first & 2));
+  }
+  if (row >= d.rows) return;
   auto slot = [&](int k) { return P.parts + (size_t)(k == c ? 2 * c + 1 : 2 * k) * kSlot + row; };
-  // the parts one after another, four on their way at once; so far: reference sr, kr, cr, sum l in its units, outputs o
+  // the parts one after another, two on their way at once (with eight the code is longer, and 37 tokens took 3 us
+  // more); so far: reference sr, kr, cr, sum l in its units, outputs o
   // and their reference rm above it
   float sr = 0.0f, cr = 0.0f, l = 0.0f, rm = -INFINITY;
   int kr = 0;
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int k0 = c; k0 <= last; k0 += 4) {
-    float4 h[4], v[4];
+  for (int k0 = c; k0 <= last; k0 += 2) {
+    float4 h[2], v[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       h[i] = k0 + i <= last ? slot(k0 + i)[(size_t)(D / 4) * 256] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       v[i] = k0 + i <= last ? slot(k0 + i)[(size_t)x * 256] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       if (h[i].z == 0.0f) continue;            // nothing seen there
       const int kb = __float_as_int(h[i].w) & 255, rv = __float_as_int(h[i].w) >> 8;
       float up = l == 0.0f ? 0.0f : above(h[i].x, kb, h[i].y, sr, kr, cr);

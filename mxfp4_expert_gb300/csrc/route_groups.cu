@@ -499,7 +499,7 @@ bool groups_ok(int E, int k, int n_groups, int top, int best) {
 
 int launch_route_groups(const GroupArgs& a, cudaStream_t s) {
   const int L = lanes_of(a.n_groups), pl = (a.E / a.n_groups + L - 1) / L;
-  const int grid = (a.T + kGrpWarps - 1) / kGrpWarps;
+  const int grid = (a.T - 1) / kGrpWarps + 1;
 #define MOE_GRP_CASE(P)                                                                               \
   route_groups_kernel<P><<<grid, kGrpWarps * 32, kGrpWarps * P * 64 * sizeof(uint32_t), s>>>(a, L); \
   break;
