@@ -457,8 +457,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       bool more = publish(0);
       bool outside = false;
       for (int t = 0; ok && more; ++t) {
-        more = publish(t + 1);
         const Item it = items[t & 1];
+        more = it.n == 0 && publish(t + 1);    // else once its first tile is on its way
         // lane g < 8: group g's page (-1: none); scale bytes of a page
         auto load_page = [&](int i) {
           const int pos = (it.t0 + i) * kKT + 16 * lane;
@@ -509,6 +509,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           if (lane == 0) mbar_arrive(&info_full[slot]);
           ++tiles;
           pg = pg1, pg1 = pg2, sc = sc1;
+          if (i == 0) more = publish(t + 1);
+          if (!ok) break;
         }
       }
       if (__any_sync(0xFFFFFFFFu, outside) && lane == 0 && status) atomicOr(status, MOE_DEV_INDEX_OOB);
