@@ -184,8 +184,8 @@ int validate_forward(const moe_layer* L, const void* x_dev, int T, const void* y
 }
 
 // The kernel sequence of one validated forward call on `stream`; stage_events
-// as in moe_forward_profiled (n_stage_events 0: none). rule: routing by groups,
-// by the per-stage kernels for any T (its logits, idx and w are set here).
+// as in moe_forward_profiled (n_stage_events 0: none). rule: routing by groups
+// (its logits, idx and w are set here).
 int enqueue_forward(const moe_layer* L, const void* x_dev, int T, void* y_dev, const float* bias_dev,
                     int bias_row_stride, float* logits_out, int32_t* idx_out, float* w_out, void* workspace_dev,
                     int* dev_status, void* const* stage_events, int n_stage_events, moe_stream_t stream,
@@ -219,9 +219,8 @@ int enqueue_forward(const moe_layer* L, const void* x_dev, int T, void* y_dev, c
   };
   if ((st = mark())) return st;
 
-  const int path = act_mxfp8 ? MOE_PATH_PREFILL_TC
-                   : rule    ? (T >= kPrefillMinT ? MOE_PATH_PREFILL_TC : MOE_PATH_DECODE_MMA)
-                             : select_path(sh, T, di);
+  int path = act_mxfp8 ? MOE_PATH_PREFILL_TC : select_path(sh, T, di);
+  if (rule && path == MOE_PATH_DECODE_FUSED && !decode_takes_groups(T, E, rule->n_groups)) path = MOE_PATH_DECODE_MMA;
   if (path == MOE_PATH_DECODE_FUSED) {
     DecodeArgs da{};
     da.T = T;
@@ -249,7 +248,7 @@ int enqueue_forward(const moe_layer* L, const void* x_dev, int T, void* y_dev, c
     da.h = at<uint8_t>(B, ws.h);   // decode_h_bytes(T, k, I) <= slots * I * 4
     da.h_sh = at<float>(B, ws.h_sh);
     da.status = status;
-    if ((st = launch_decode(da, di, s))) return st;
+    if ((st = rule ? launch_decode_groups(da, *rule, di, s) : launch_decode(da, di, s))) return st;
     return mark();
   }
 

@@ -35,6 +35,13 @@ struct GroupArgs {
   int32_t* idx;                  // [T][k]
   float* w;                      // [T][k]
 };
+// Lanes of a warp that hold a group's experts, and how many of them each holds.
+inline int group_lanes(int n_groups) {
+  int p = 1;
+  while (p < n_groups) p *= 2;
+  return 32 / p;
+}
+inline int group_keys(int E, int n_groups) { return (E / n_groups + group_lanes(n_groups) - 1) / group_lanes(n_groups); }
 // Checks a rule and fills all of *g but logits, idx and w.
 int group_args(const moe_group_rule* r, int T, int E, int k, const float* bias, GroupArgs* g);
 bool groups_ok(int E, int k, int n_groups, int top, int best);

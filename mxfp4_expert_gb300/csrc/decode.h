@@ -54,5 +54,9 @@ size_t decode_h_bytes(int T, int k, int I);
 // dynamic shared memory of the launch.
 int decode_plan(const DecodeArgs& a, const DeviceInfo& di, uint32_t* smem_bytes);
 int launch_decode(const DecodeArgs& a, const DeviceInfo& di, cudaStream_t s);
+// The same with routing by groups (a.bias is not used), where its selection fits the kernel.
+struct GroupArgs;
+bool decode_takes_groups(int T, int E, int n_groups);
+int launch_decode_groups(const DecodeArgs& a, const GroupArgs& rule, const DeviceInfo& di, cudaStream_t s);
 
 }  // namespace moe
