@@ -527,7 +527,8 @@ int moe_kv_append_fp8(const moe_kv_cache* cache, const moe_rows* k, const moe_ro
  * are turned beside it. The pair j (channels j and j + rot_dim / 2, or interleaved
  * 2j and 2j + 1) of a token at position p becomes
  *   (a cos t - b sin t, b cos t + a sin t),  t = p * inv_freq[j]
- * The angle is reduced exactly, so positions may be as far as an int reaches.
+ * The angle is reduced exactly, so positions may be as far as an int reaches, and
+ * codes and scales are those of the exact turned keys (queries are turned in fp32).
  *   inv_freq_dev    fp32 [rot_dim / 2]
  *   rot_dim         16, 32, .. head_dim (a multiple of 16)
  *   rope_start_dev  int32 [n_seq]: position that a sequence's first new token is
@@ -600,7 +601,8 @@ int moe_attn_decode_fp8(const moe_kv_cache* cache, const moe_rows* q, int n_head
  *   dev_status   device int (may be NULL): MOE_DEV_INDEX_OOB (cu_q as in
  *                moe_attn_prefill; a length outside [0, table_width * page_size] is
  *                cut to it; a page outside the cache counts as masked), MOE_DEV_TIMEOUT
- * Rows of q outside every sequence are not written.
+ * Rows of q outside every sequence are not written. A query that is not finite
+ * gives outputs that are not, in its own row.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED_SHAPE (the cache's sizes,
  * n_heads % n_kv_heads, n_heads > 65535, n_seq > 65536, total_q times the heads of
  * a group > 2^31 - 65536), MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_NO_DEVICE,

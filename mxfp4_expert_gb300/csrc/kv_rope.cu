@@ -12,8 +12,8 @@
 // the next one's channels on their way meanwhile. A thread holds both halves of its
 // pairs. Of a key or value head the maximum, the page's scale and the codes as
 // append_kernel makes them, which has no rotation. Bound by HBM: 3 bytes a key or
-// value, 4 a query's channel; 12,345 tokens of 16 heads over 8 of 128 take 42.9 us (4.1
-// TB/s), a token of each of 64 sequences 6.1.
+// value, 4 a query's channel; 12,345 tokens of 16 heads over 8 of 128 take 47 us (3.8
+// TB/s), a token of each of 64 sequences 6.5 to 9 (a key in doubt costs 2).
 #include <algorithm>
 
 #include "attn.h"
@@ -120,17 +120,20 @@ __device__ __forceinline__ Block find_block_cta(const AppendArgs& a, int x, bool
   }
   return s_blk;
 }
-// Phase of a frequency per position, in 2^-64 turns.
+// Phase of a frequency per position, in 2^-64 turns: 1 / 2 pi in two parts.
 __device__ __forceinline__ uint64_t turns_of(float inv_freq) {
-  double turns = double(inv_freq) * 0.15915494309189533577;
-  turns -= floor(turns);
-  return uint64_t(turns * 18446744073709551616.0);
+  const double f = inv_freq, t = f * 0.15915494309189535, rest = fma(f, 0.15915494309189535, -t) + f * -9.839338337591243e-18;
+  return uint64_t((t - floor(t)) * 18446744073709551616.0) + uint64_t(int64_t(rest * 18446744073709551616.0));
+}
+// Position of a page's first new token.
+__device__ __forceinline__ int64_t first_position(const RopeArgs& a, const Block& f) {
+  return (int64_t)__ldg(a.rope_start + f.b) + ((int64_t)f.blk * a.ap.c.page_size + f.s0 - __ldg(a.ap.start + f.b));
 }
 // Cosines and sines of a page's new tokens, for the caller's barrier.
 __device__ __forceinline__ void fill_angles(const RopeArgs& a, const Block& f, uint64_t F, float2* cs) {
   const int half = a.rot / 2, j = threadIdx.x % half, first = threadIdx.x / half, step = kRopeThreads / half;
   if (first >= step) return;
-  const int64_t p0 = (int64_t)__ldg(a.rope_start + f.b) + ((int64_t)f.blk * a.ap.c.page_size + f.s0 - __ldg(a.ap.start + f.b));
+  const int64_t p0 = first_position(a, f);
   uint64_t at = uint64_t(p0 + first) * F;
   const uint64_t by = uint64_t(step) * F;
   for (int t = first; t < f.s1 - f.s0; t += step, at += by) cs[t * half + j] = turn(uint32_t(at >> 32));
@@ -175,6 +178,28 @@ __device__ __forceinline__ void store_codes(uint8_t* o, int c0, int c1, const fl
   *reinterpret_cast<uint2*>(o + c0) = make_uint2(q[0], q[1]);
   *reinterpret_cast<uint2*>(o + c1) = make_uint2(q[2], q[3]);
 }
+// A turned channel errs by less than kKeyError times the sizes of its pair: cosine and
+// sine by 2^-23 each (an angle of 24 bits, its factor, a series), two products and
+// their sum by 2^-24 each, so 2^-22 (|a| + |b|), and |a| + |b| is at most 1.4143 times
+// that of the turned pair. Where that could change a code, which is a step of 2^-3, or
+// a scale, the pair is turned once more in fp64, so that codes and scales are those of
+// the exact values: one value in 2^16, and 10 % of the time for 12,345 tokens.
+constexpr float kKeyError = 3.4e-7f;    // 1.4143 * 2^-22 = 3.372e-7
+
+// A key's pair turned in fp64, times f; rounded to fp32 by truncation with the last bit set where
+// that leaves something out, so that a further rounding is right.
+__device__ __noinline__ float2 turn_exact(float a0, float b0, const float* freq, int64_t pos, float f) {
+  const double a = a0, b = b0;
+  const int64_t at = int64_t(uint64_t(pos) * turns_of(__ldg(freq)));
+  double sn, cs;
+  sincospi(double(at) * 1.0842021724855044e-19, &sn, &cs);      // half turns: 2^-63
+  auto odd = [f](double v) {
+    v *= f;
+    const uint32_t r = __float_as_uint(__double2float_rz(v));
+    return __uint_as_float(double(__uint_as_float(r)) != v ? r | 1u : r);
+  };
+  return make_float2(odd(a * cs - b * sn), odd(b * cs + a * sn));
+}
 // The CTA: a part-filled page's older codes, in units of the new scale.
 __device__ __forceinline__ void rescale_codes(uint8_t* codes, int n, float f) {
   for (int v = threadIdx.x; v < n / 16; v += kRopeThreads) {
@@ -188,18 +213,125 @@ __device__ __forceinline__ void rescale_codes(uint8_t* codes, int n, float f) {
   }
 }
 
+// Could codes of y, times f, be others within the error of y?
+__device__ __forceinline__ bool in_doubt(const float (&y)[16], float f, int kind) {
+  uint32_t differ = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float a = (kind == 1 ? y[i] : y[2 * i]) * f, b = (kind == 1 ? y[8 + i] : y[2 * i + 1]) * f;
+    const float e = (fabsf(a) + fabsf(b)) * kKeyError;
+    differ |= uint32_t(f32x2_to_e4m3x2(a - e, b - e)) ^ uint32_t(f32x2_to_e4m3x2(a + e, b + e));
+  }
+  return (differ & 0x7F7Fu) != 0;        // the sign of a zero does not count
+}
+// Bounds of a largest magnitude: of turned channels on both sides of it, others are exact.
+__device__ __forceinline__ float largest_most(float top, int kind) {
+  return kind ? fminf(fmaf(top, 2.0f * kKeyError, top), 3.4028235e38f) : top;
+}
+__device__ __forceinline__ float largest_least(float top, int kind) { return kind ? fmaf(top, -2.0f * kKeyError, top) : top; }
+
+// What a CTA turns exactly when it has stored everything else: groups of eight pairs (head, row of the page's new tokens,
+// group; beyond the list's room all groups), and heads whose scale is in doubt, of which nothing is stored yet.
+constexpr int kDoubts = 256;
+struct Doubts {
+  int n, any_head;
+  uint32_t at[kDoubts], heads[32];
+};
+__device__ __forceinline__ void clear_doubts(Doubts* d) {
+  if (threadIdx.x < 32) d->heads[threadIdx.x] = 0;
+  if (threadIdx.x == 0) d->n = d->any_head = 0;
+}
+__device__ __forceinline__ void note_doubt(Doubts* d, int h, int row, int u) {
+  const int i = atomicAdd(&d->n, 1);
+  if (i < kDoubts) d->at[i] = uint32_t(h) << 16 | uint32_t(row) << 3 | uint32_t(u);
+}
+__device__ __forceinline__ void note_head(Doubts* d, int h) {
+  atomicOr(&d->heads[h >> 5], 1u << (h & 31));
+  d->any_head = 1;
+}
+// Whole CTA, behind a barrier: heads h0 .. h1 of its keys.
+__device__ __noinline__ void settle_doubts(const RopeArgs& a, const Block& f, int page, int h0, int h1, const Doubts* d) {
+  __shared__ uint32_t s_top;
+  const AppendArgs& ap = a.ap;
+  const int P = ap.c.page_size, D = ap.c.head_dim, H = ap.c.n_kv_heads, half = a.rot / 2, tokens = f.s1 - f.s0;
+  const int64_t p0 = first_position(a, f);
+  uint8_t* scales = static_cast<uint8_t*>(ap.c.k_scales) + (size_t)page * H;
+  // pair `pair` of the head in row `row`, turned exactly and times 2^(127 - byte)
+  auto exact = [&](int h, int row, int pair, int byte, int* c0, int* c1) {
+    *c0 = a.interleaved ? 2 * pair : pair;
+    *c1 = a.interleaved ? 2 * pair + 1 : pair + half;
+    const __nv_bfloat16* src = ap.k + (int64_t)(f.t0 + row) * ap.k_ts + h * ap.k_hs;
+    return turn_exact(__bfloat162float(src[*c0]), __bfloat162float(src[*c1]), a.inv_freq + pair, p0 + row, code_factor(byte));
+  };
+  auto codes = [&](int h) { return static_cast<uint8_t*>(ap.c.k_codes) + ((size_t)page * H + h) * P * D; };
+  auto in_heads = [&](int h) { return (d->heads[h >> 5] >> (h & 31)) & 1u; };
+
+  const bool all = d->n > kDoubts;
+  const int n = (all ? (h1 - h0) * tokens * (half / 8) : d->n) * 8;
+  for (int i = threadIdx.x; i < n; i += kRopeThreads) {
+    const int x = i >> 3;
+    const int h = all ? h0 + x / (tokens * (half / 8)) : int(d->at[x] >> 16);
+    const int row = all ? x / (half / 8) % tokens : int(d->at[x] >> 3) & 0x1FFF, u = all ? x % (half / 8) : int(d->at[x]) & 7;
+    if (in_heads(h)) continue;
+    int c0, c1;
+    const float2 v = exact(h, row, 8 * u + (i & 7), scales[h], &c0, &c1);
+    if (!(fabsf(v.x) <= 448.0f && fabsf(v.y) <= 448.0f)) continue;      // not finite in fp32: stored as NaN
+    uint8_t* o = codes(h) + (f.s0 + row) * D;
+    const uint32_t c = f32x2_to_e4m3x2(v.x, v.y);
+    o[c0] = uint8_t(c);
+    o[c1] = uint8_t(c >> 8);
+  }
+  for (int h = h0; d->any_head && h < h1; ++h) {
+    if (!in_heads(h)) continue;
+    // the exact largest value decides between a byte and the next
+    const int had = f.s0 > 0 ? int(scales[h]) : 0;
+    auto value = [&](int i, int byte, int* c0, int* c1) {       // pair i of the rows' D / 2, those of the rest as they are
+      const int row = i / (D / 2), pair = i % (D / 2);
+      if (pair < half) return exact(h, row, pair, byte, c0, c1);
+      *c0 = 2 * pair;
+      *c1 = 2 * pair + 1;
+      const __nv_bfloat16* src = ap.k + (int64_t)(f.t0 + row) * ap.k_ts + h * ap.k_hs;
+      return make_float2(__bfloat162float(src[*c0]) * code_factor(byte), __bfloat162float(src[*c1]) * code_factor(byte));
+    };
+    int c0, c1;
+    float top = 0.0f;                 // of values that are truncated, but not to what a scale holds exactly
+    for (int i = threadIdx.x; i < tokens * (D / 2); i += kRopeThreads) {
+      const float2 v = value(i, 127, &c0, &c1);
+      top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) s_top = 0;
+    __syncthreads();
+    atomicMax(&s_top, __float_as_uint(top));
+    __syncthreads();
+    const int byte = max(kv_scale_byte(__uint_as_float(s_top)), had);
+    for (int i = threadIdx.x; i < tokens * (D / 2); i += kRopeThreads) {
+      const float2 v = value(i, byte, &c0, &c1);
+      uint8_t* o = codes(h) + (f.s0 + i / (D / 2)) * D;
+      const uint32_t c = f32x2_to_e4m3x2(v.x, v.y);
+      o[c0] = uint8_t(c);
+      o[c1] = uint8_t(c >> 8);
+    }
+    __syncthreads();                  // everyone has read the old scale
+    if (threadIdx.x == 0) scales[h] = uint8_t(byte);
+    if (byte > had && f.s0 > 0) rescale_codes(codes(h), f.s0 * D, kv_factor(had, byte));
+  }
+}
 // Few new tokens a page, one mostly (a decode step): a CTA takes all heads of a
 // page's tokens, D / 16 neighbouring lanes a head. Right for any number of tokens,
 // which are read once more where there are several. A token of each of 64 sequences:
-// 6.1 us, by the other kernel, which gives a page's every head a CTA, 13.0.
+// 6.1 us, by the other kernel, which gives a page's every head a CTA, 13.0 (both before
+// keys in doubt were turned again).
 __global__ void __launch_bounds__(kRopeThreads) append_rope_few_kernel(const RopeArgs a) {
   extern __shared__ __align__(16) float2 s_cs[];        // [tokens][rot / 2]
   __shared__ uint8_t s_grown[2][1024];                  // of a key or value head whose scale has grown: the bytes before
   __shared__ int s_any;
+  __shared__ Doubts s_doubts;
   const AppendArgs& ap = a.ap;
   const int tid = threadIdx.x;
   const int P = ap.c.page_size, D = ap.c.head_dim, H = ap.c.n_kv_heads, half = a.rot / 2;
   if (tid == 0) s_any = 0;
+  clear_doubts(&s_doubts);             // find_block_cta has barriers
   const uint64_t F = tid / half < kRopeThreads / half ? turns_of(__ldg(a.inv_freq + tid % half)) : 0;
   bool bad = false;
   const Block f = find_block_cta(ap, int(blockIdx.x), &bad);
@@ -233,17 +365,30 @@ __global__ void __launch_bounds__(kRopeThreads) append_rope_few_kernel(const Rop
         if (role == 2) store_bf16(a.q_out + ((int64_t)(f.t0 + t) * a.n_heads + h) * D, c0, c1, y);
         else top = max(top, largest(y, &nonfinite));
       }
+    float most = largest_most(__uint_as_float(top), kind), least = largest_least(__uint_as_float(top), kind);
     for (int o = 1; o < upr; o <<= 1) {
-      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+      least = fmaxf(least, __shfl_xor_sync(0xFFFFFFFFu, least, o));
       nonfinite |= __shfl_xor_sync(0xFFFFFFFFu, int(nonfinite), o) != 0;
     }
     if (!in || role == 2) continue;
     uint8_t* codes = static_cast<uint8_t*>(role ? ap.c.v_codes : ap.c.k_codes) + ((size_t)page * H + h) * P * D;
     uint8_t* scale = (role ? ap.c.v_scales : ap.c.k_scales) + (size_t)page * H + h;
-    const int had = f.s0 > 0 ? int(*scale) : 0, byte = max(kv_scale_byte(__uint_as_float(top)), had);
+    const int had = f.s0 > 0 ? int(*scale) : 0;
+    int byte = kv_scale_byte(most);
+    const bool turned = role == 0 && !nonfinite;
+    if (byte > had && turned && kv_scale_byte(least) != byte) {
+      if (u == 0) {
+        note_head(&s_doubts, h);
+        s_grown[0][h] = 255;          // nothing below has to be done for it
+      }
+      continue;
+    }
+    byte = max(byte, had);
     for (int t = 0; t < tokens; ++t) {
       if (tokens > 1) load(t);
       store_codes(codes + (f.s0 + t) * D, c0, c1, y, code_factor(byte), nonfinite);
+      if (turned && kind && in_doubt(y, code_factor(byte), kind)) note_doubt(&s_doubts, h, t, u);
     }
     __syncwarp(((1u << upr) - 1) << ((tid & 31) & ~(upr - 1)));     // the head's lanes have read the old scale
     if (u == 0) {
@@ -254,6 +399,7 @@ __global__ void __launch_bounds__(kRopeThreads) append_rope_few_kernel(const Rop
     }
   }
   __syncthreads();
+  if (s_doubts.n || s_doubts.any_head) settle_doubts(a, f, page, 0, H, &s_doubts);
   if (f.s0 == 0 || page < 0 || !s_any) return;
   for (int g = 0; g < 2 * H; ++g) {
     const int role = g >= H, h = g - role * H, had = s_grown[role][h];
@@ -270,13 +416,15 @@ __global__ void __launch_bounds__(kRopeThreads) append_rope_few_kernel(const Rop
 template <int NU>
 __global__ void __launch_bounds__(kRopeThreads, NU == 4 ? 2 : NU == 2 ? 3 : 4) append_rope_kernel(const RopeArgs a, int heads, int k_groups) {
   extern __shared__ __align__(16) float2 s_cs[];        // [tokens][rot / 2]
-  __shared__ int smax[2][kRopeThreads / 32], sbad[2][kRopeThreads / 32];
+  __shared__ int smax[2][kRopeThreads / 32], smin[2][kRopeThreads / 32], sbad[2][kRopeThreads / 32];
+  __shared__ Doubts s_doubts;
   const AppendArgs& ap = a.ap;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int P = ap.c.page_size, D = ap.c.head_dim, H = ap.c.n_kv_heads;
   const int group = blockIdx.y, role = group < k_groups ? 0 : group < 2 * k_groups ? 1 : 2;
   const int rot = role == 1 ? 0 : a.rot, half = rot / 2;
   const uint64_t F = rot && tid / half < kRopeThreads / half ? turns_of(__ldg(a.inv_freq + tid % half)) : 0;
+  clear_doubts(&s_doubts);             // find_block_cta has barriers
   bool bad = false;
   const Block f = find_block_cta(ap, int(blockIdx.x), &bad);
   if (bad && ap.status) atomicOr(ap.status, MOE_DEV_INDEX_OOB);
@@ -313,6 +461,7 @@ __global__ void __launch_bounds__(kRopeThreads, NU == 4 ? 2 : NU == 2 ? 3 : 4) a
     return;
   }
 
+  const int h0 = h;
   for (int k = 0; h < h1; ++h, k ^= 1) {
     float y[NU][16];
 #pragma unroll
@@ -335,18 +484,27 @@ __global__ void __launch_bounds__(kRopeThreads, NU == 4 ? 2 : NU == 2 ? 3 : 4) a
 #pragma unroll
     for (int i = 0; i < NU; ++i) top = max(top, largest(y[i], &nonfinite));
     nonfinite = __any_sync(0xFFFFFFFFu, nonfinite);
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    uint32_t least = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(largest_least(__uint_as_float(top), kind)));
+    top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(largest_most(__uint_as_float(top), kind)));
     if (lane == 0) {
       smax[k][warp] = int(top);
+      smin[k][warp] = int(least);
       sbad[k][warp] = nonfinite;
     }
     __syncthreads();   // also: everyone has read the old scale
 #pragma unroll
     for (int i = 0; i < kRopeThreads / 32; ++i) {
       top = max(top, uint32_t(smax[k][i]));
+      least = max(least, uint32_t(smin[k][i]));
       nonfinite |= sbad[k][i] != 0;
     }
-    const int byte = max(kv_scale_byte(__uint_as_float(top)), had);
+    int byte = kv_scale_byte(__uint_as_float(top));
+    const bool turned = rot && !nonfinite;
+    if (byte > had && turned && kv_scale_byte(__uint_as_float(least)) != byte) {      // the same for all threads
+      if (tid == 0) note_head(&s_doubts, h);
+      continue;
+    }
+    byte = max(byte, had);
     if (tid == 0) {
       *scale = uint8_t(byte);
       if (nonfinite && ap.status) atomicOr(ap.status, MOE_DEV_NONFINITE_INPUT);
@@ -355,9 +513,13 @@ __global__ void __launch_bounds__(kRopeThreads, NU == 4 ? 2 : NU == 2 ? 3 : 4) a
     for (int i = 0; i < NU; ++i) {
       if (i * kRopeThreads + tid >= n) break;
       store_codes(codes + (f.s0 + row0 + i * rows) * D, c0, c1, y[i], code_factor(byte), nonfinite);
+      if (turned && kind && in_doubt(y[i], code_factor(byte), kind)) note_doubt(&s_doubts, h, row0 + i * rows, u);
     }
     if (byte > had && f.s0 > 0) rescale_codes(codes, f.s0 * D, kv_factor(had, byte));
   }
+  if (!rot || role == 2) return;
+  __syncthreads();
+  if (s_doubts.n || s_doubts.any_head) settle_doubts(a, f, page, h0, h1, &s_doubts);
 }
 
 }  // namespace
@@ -368,7 +530,7 @@ int launch_kv_append_rope(const RopeArgs& a, const DeviceInfo& di, cudaStream_t 
   const int64_t most = (int64_t)a.ap.total / P + 2 * (int64_t)a.ap.n_seq;
   const int nb = int(std::min(most, (int64_t)a.ap.total)) + 1;   // the last one looks at every sequence
   // Heads a CTA: more share one table of angles, while there are CTAs for every SM several times over (12,345 tokens:
-  // one 64.1 us, two 47.9, four 42.9).
+  // one 64.1 us, two 47.9, four 42.9, before keys in doubt were turned again).
   const int H = a.ap.c.n_kv_heads, n_q = a.q ? a.n_heads : 0;
   int heads = 1;
   while (heads < 4 && (int64_t)nb * (2 * H + n_q) >= (int64_t)kRopeCtas * di.sm_count * 2 * heads) heads *= 2;
