@@ -191,8 +191,8 @@ constexpr float kKeyError = 3.4e-7f;    // 1.4143 * 2^-22 = 3.372e-7
 __device__ __noinline__ float2 turn_exact(float a0, float b0, const float* freq, int64_t pos, float f) {
   const double a = a0, b = b0;
   const int64_t at = int64_t(uint64_t(pos) * turns_of(__ldg(freq)));
-  double sn, cs;
-  sincospi(double(at) * 1.0842021724855044e-19, &sn, &cs);      // half turns: 2^-63
+  double sn = 0.0, cs = 1.0;
+  if (at != 0) sincospi(double(at) * 1.0842021724855044e-19, &sn, &cs);      // half turns: 2^-63
   auto odd = [f](double v) {
     v *= f;
     const uint32_t r = __float_as_uint(__double2float_rz(v));
@@ -294,7 +294,7 @@ __device__ __noinline__ void settle_doubts(const RopeArgs& a, const Block& f, in
       return make_float2(__bfloat162float(src[*c0]) * code_factor(byte), __bfloat162float(src[*c1]) * code_factor(byte));
     };
     int c0, c1;
-    float top = 0.0f;                 // of values that are truncated, but not to what a scale holds exactly
+    float top = 0.0f;                 // truncated values, but what they leave out is in their last bit
     for (int i = threadIdx.x; i < tokens * (D / 2); i += kRopeThreads) {
       const float2 v = value(i, 127, &c0, &c1);
       top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
@@ -317,6 +317,7 @@ __device__ __noinline__ void settle_doubts(const RopeArgs& a, const Block& f, in
     if (byte > had && f.s0 > 0) rescale_codes(codes(h), f.s0 * D, kv_factor(had, byte));
   }
 }
+
 // Few new tokens a page, one mostly (a decode step): a CTA takes all heads of a
 // page's tokens, D / 16 neighbouring lanes a head. Right for any number of tokens,
 // which are read once more where there are several. A token of each of 64 sequences:
