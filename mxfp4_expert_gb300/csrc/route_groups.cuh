@@ -396,24 +396,25 @@ __device__ __forceinline__ void route_token(const GroupArgs& a, const float* row
     };
     int n = 0;
     while (n < a.k && next_best(n)) ++n;
-    if (a.bias && n == 32) unsure = true;      // there is no lane for one more
     if (a.bias && !unsure) {
-      // Does the order stand? One more key than are wanted, and more while they may belong before the last.
-      float ml = 0.0f, mb = 0.0f;
-      bool close = false;
-      for (bool more = true; more && n < 32;) {
+      // Does the order stand? Candidates are all keys that may be as large as the last one wanted, of one logit and bias
+      // with it or not, and one more, which shows that there are no others.
+      for (bool more = true; more;) {
+        if (n == 32) {
+          unsure = true;
+          break;
+        }
         more = next_best(n);
         if (more) ++n;
-        const float v = rank_value(my_key), w = __shfl_down_sync(0xFFFFFFFFu, v, 1);
-        if (lane < n) ml = row[my_e], mb = a.bias[my_e];
-        const float wl = __shfl_down_sync(0xFFFFFFFFu, ml, 1), wb = __shfl_down_sync(0xFFFFFFFFu, mb, 1);
-        // keys of one logit and bias are equal, whatever their rounding
-        const bool near = lane + 1 < n && v - w <= doubt(a.softmax, s_max, fabsf(v)) && !(ml == wl && mb == wb);
-        const unsigned nears = __ballot_sync(0xFFFFFFFFu, near);
-        close = nears != 0u;
-        more = more && (nears >> (n - 2)) & 1;       // the last two
-        if (more && n == 32) unsure = true;
+        const float v = rank_value(my_key), last = __shfl_sync(0xFFFFFFFFu, v, a.k - 1);
+        more = more && last - __shfl_sync(0xFFFFFFFFu, v, n - 1) <= doubt(a.softmax, s_max, fabsf(last));
       }
+      const float v = rank_value(my_key), w = __shfl_down_sync(0xFFFFFFFFu, v, 1);
+      const float ml = lane < n ? row[my_e] : 0.0f, mb = lane < n ? a.bias[my_e] : 0.0f;
+      const float wl = __shfl_down_sync(0xFFFFFFFFu, ml, 1), wb = __shfl_down_sync(0xFFFFFFFFu, mb, 1);
+      // keys of one logit and bias are equal, whatever their rounding: their order stands
+      const bool close = __any_sync(
+          0xFFFFFFFFu, lane + 1 < n && v - w <= doubt(a.softmax, s_max, fabsf(v)) && !(ml == wl && mb == wb));
       if (close && !unsure) {       // rank the candidates by their keys as pairs
         const F2 tab{kExpTable.hi[lane], kExpTable.lo[lane]};
         const F2 of_all = a.softmax ? pair_sum(row, a.E, l_max) : F2{1.0f, 0.0f};
