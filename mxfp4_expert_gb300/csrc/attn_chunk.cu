@@ -704,9 +704,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         for (int x = 0; x < D / 8; ++x)
           m2 = __vmaxu2(__vmaxu2(m2, __vmaxu2(w[x].x & 0x7FFF7FFFu, w[x].y & 0x7FFF7FFFu)),
                         __vmaxu2(w[x].z & 0x7FFF7FFFu, w[x].w & 0x7FFF7FFFu));
-        const int ex = min(max(int(max(m2 & 0xFFFFu, m2 >> 16) >> 7) - 127, -112), 127);
+        const uint32_t top = max(m2 & 0xFFFFu, m2 >> 16);
+        const int ex = min(max(int(top >> 7) - 127, -112), 127);
         ce += ex - 14;
-        const float f = P.negate ? -pow2(14 - ex) : pow2(14 - ex);
+        // A row that is not finite becomes NaN as a whole, and so do the scores of what it sees: those of an infinity
+        // may all be -inf, which a mask leaves too.
+        const float f = top >= 0x7F80u ? __int_as_float(0x7FC00000) : P.negate ? -pow2(14 - ex) : pow2(14 - ex);
         const uint32_t dst = row * 128;
         uint8_t* qs = smem + Pl::kQ + j * Pl::kTile;
 #pragma unroll
