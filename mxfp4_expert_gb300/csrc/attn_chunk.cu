@@ -707,9 +707,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         const uint32_t top = max(m2 & 0xFFFFu, m2 >> 16);
         const int ex = min(max(int(top >> 7) - 127, -112), 127);
         ce += ex - 14;
-        // A row that is not finite becomes NaN as a whole, and so do the scores of what it sees: those of an infinity
-        // may all be -inf, which a mask leaves too.
-        const float f = top >= 0x7F80u ? __int_as_float(0x7FC00000) : P.negate ? -pow2(14 - ex) : pow2(14 - ex);
+        // 2^(14 - ex). A row that is not finite becomes NaN as a whole, and so do the scores of what it sees: those of an
+        // infinity may all be -inf, which a mask leaves too.
+        const float f = __uint_as_float((uint32_t(141 - ex) << 23) | (P.negate ? 0x80000000u : 0u) | (top >= 0x7F80u ? 0x7FC00000u : 0u));
         const uint32_t dst = row * 128;
         uint8_t* qs = smem + Pl::kQ + j * Pl::kTile;
 #pragma unroll
