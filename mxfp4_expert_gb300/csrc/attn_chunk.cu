@@ -1099,10 +1099,10 @@ int launch_attn_chunk(const ChunkArgs& a, const DeviceInfo& di, cudaStream_t s) 
   P.a = a;
   P.G = a.n_heads / a.c.n_kv_heads;
   while ((1 << P.log2_page) < a.c.page_size) ++P.log2_page;
-  const float c = fabsf(a.scale) * 1.4426950408889634f;
-  if (c > 0.0f) {
+  const double c = fabs(double(a.scale)) * 1.4426950408889634;      // beyond fp32 for the largest scales
+  if (c > 0.0) {
     int e;
-    P.cm = 2.0f * frexpf(c, &e);
+    P.cm = float(2.0 * frexp(c, &e));
     P.ce = e - 1;
   } else {   // every score counts the same
     P.cm = 1.0f;
