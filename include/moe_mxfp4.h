@@ -214,14 +214,16 @@ int moe_route_topk(const float* logits_dev, int T, int E, int k,
  * one token over E experts in n_groups groups of E / n_groups consecutive ones:
  *   s[e]   = 1 / (1 + exp(-l[e])), or the softmax of l over all E experts
  *   key[e] = s[e] + bias[e]                 the bias only selects
- *   group  = its largest key, or (group_best 2) the sum of its two largest
+ *   group  = its largest key, or (group_best 2) the sum of its two largest (the larger one if that is +inf)
  *   S      = the k largest keys in the top_groups best groups
  *   w[j]   = scale * s[S_j] / (sum_i s[S_i] + 1e-20), or scale * s[S_j]
  * Equal keys go to the lower expert, equal groups to the lower group. Keys are
  * compared as sums of two fp32 numbers, to about 2^-40 of a score, so that rounding
  * decides no selection (scores below 2^-100 lose bits); without a bias the logits
- * rank. A NaN logit has score 0 and ranks behind all others; an infinite one
- * counts as the largest finite number of its sign.
+ * rank. A NaN logit has score 0 and the key -inf; an infinite one counts as the
+ * largest finite number of its sign. A bias of +inf or -inf forces or masks its
+ * expert (masked ones are taken, the lower first, where others do not reach), a NaN
+ * one counts as -inf.
  *   logits_dev   fp32 [T][E]
  *   bias_dev     fp32 [E], NULL for none
  *   rule         host

@@ -203,8 +203,9 @@ __device__ __noinline__ int route_in_pairs(const GroupArgs& a, const float* row,
       take(o0);
       take(o1);
     }
+    // with an infinite key the sum is that, the larger of two
     F2 score = b0;
-    if (a.best > 1) score = fabsf(b0.hi) <= kFmax && fabsf(b1.hi) <= kFmax ? add(b0, b1) : F2{b0.hi + b1.hi, 0.0f};
+    if (a.best > 1 && fabsf(b0.hi) <= kFmax) score = fabsf(b1.hi) <= kFmax ? add(b0, b1) : b1;
     int better = 0;
     for (int i = 0; i < a.n_groups; ++i) {
       const F2 v{__shfl_sync(0xFFFFFFFFu, score.hi, i * L), __shfl_sync(0xFFFFFFFFu, score.lo, i * L)};

@@ -55,7 +55,9 @@ def _keys(l, s, nan, bias, best):
 
 
 def _ranks(member, n_groups, best):
-    return np.array([sum(sorted(m, reverse=True)[:best]) for m in np.asarray(member).reshape(n_groups, -1)])
+    """Sums of each group's best; with an infinite one it is that, the larger of two."""
+    best_of = [sorted(m, reverse=True)[:best] for m in np.asarray(member).reshape(n_groups, -1)]
+    return np.array([m[0] if np.isposinf(m[0]) else sum(m) for m in best_of])
 
 
 def group_ranks(l, bias, kind, n_groups, best=2):
