@@ -203,9 +203,12 @@ __device__ __noinline__ int route_in_pairs(const GroupArgs& a, const float* row,
       take(o0);
       take(o1);
     }
-    // with an infinite key the sum is that, the larger of two
+    // a sum of two keys in halves, so that it does not leave fp32; with an infinite one it is that, the larger of two
     F2 score = b0;
-    if (a.best > 1 && fabsf(b0.hi) <= kFmax) score = fabsf(b1.hi) <= kFmax ? add(b0, b1) : b1;
+    if (a.best > 1) {
+      auto half = [](const F2& v) { return F2{0.5f * v.hi, 0.5f * v.lo}; };
+      if (fabsf(b0.hi) <= kFmax) score = fabsf(b1.hi) <= kFmax ? add(half(b0), half(b1)) : b1;
+    }
     int better = 0;
     for (int i = 0; i < a.n_groups; ++i) {
       const F2 v{__shfl_sync(0xFFFFFFFFu, score.hi, i * L), __shfl_sync(0xFFFFFFFFu, score.lo, i * L)};
@@ -322,7 +325,7 @@ __device__ __forceinline__ void route_token(const GroupArgs& a, const float* row
         const int in = __ffs(__ballot_sync(0xFFFFFFFFu, g < a.n_groups && better == a.top - 1)) - 1;
         const int out = __ffs(__ballot_sync(0xFFFFFFFFu, g < a.n_groups && better == a.top)) - 1;
         const float v = __shfl_sync(0xFFFFFFFFu, score, in), w = __shfl_sync(0xFFFFFFFFu, score, out);
-        if (v - w <= 2.0f * doubt(a.softmax, s_max, fabsf(v) + fabsf(w))) {
+        if (!(v - w > 2.0f * doubt(a.softmax, s_max, fabsf(v) + fabsf(w)))) {     // where sums leave fp32, too
           // Rank the groups by sums of pairs, where it is clear of which experts.
           const float from_key = (a.best > 1 ? b1 : b0) - doubt(a.softmax, s_max, fabsf(b0) + fabsf(b1));
           int n = 0, e0 = -1, e1 = -1;           // this lane's experts that may count
@@ -335,7 +338,7 @@ __device__ __forceinline__ void route_token(const GroupArgs& a, const float* row
             }
           int of_group = n;
           for (int o = 1; o < L; o <<= 1) of_group += __shfl_xor_sync(0xFFFFFFFFu, of_group, o);
-          unsure = __any_sync(0xFFFFFFFFu, g < a.n_groups && of_group != a.best);
+          unsure = __any_sync(0xFFFFFFFFu, g < a.n_groups && (of_group != a.best || !(fabsf(score) <= kFmax)));
           if (!unsure) {
             const F2 tab{kExpTable.hi[lane], kExpTable.lo[lane]};
             const F2 of_all = a.softmax ? pair_sum(row, a.E, l_max) : F2{1.0f, 0.0f};

@@ -55,3 +55,15 @@ def test_groups_that_are_masked_whole(mx, score):
     _check(mx, l, 4, bias, score, 8, 3, 2)
     l[:5, 47] = math.nan
     _check(mx, l, 4, bias, score, 8, 4, 2)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_sums_beyond_fp32(mx, score, sign):
+    """Two keys of a group add up to more than fp32 holds; their order is that of the sums."""
+    l = torch.randn((20, 64), generator=_gen(5), device="cuda")
+    bias = sign * (2.0 + torch.randperm(64, generator=torch.Generator().manual_seed(6)).float().cuda() / 64) * 1e38
+    for top in (1, 3, 5):
+        _check(mx, l, 8, bias, score, 8, top, 2)
+        _check(mx, l, 2, bias, score, 32, 2 * top, 2)      # groups of two
+        bias[::5] = 0.25
