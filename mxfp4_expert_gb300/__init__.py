@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 
 import torch
@@ -248,12 +249,20 @@ _SCORES = {"sigmoid": 0, "softmax": 1}
 
 
 @functools.lru_cache(maxsize=64)
-def _rule(score, n_groups, top_groups, group_best, renormalise, scale):
-    """Reference to the struct of a rule; never written to."""
+def _rule_struct(score, n_groups, top_groups, group_best, renormalise, scale, zero):
+    """Reference to the struct of a rule; never written to. zero: text of a scale of 0, for -0.0 equals 0.0."""
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
-    return ctypes.byref(moe_group_rule(_SCORES[score], n_groups, top_groups, group_best, 1 if renormalise else 0,
-                                       float(scale)))
+    return ctypes.byref(moe_group_rule(_SCORES[score], n_groups, top_groups, group_best, 1 if renormalise else 0, scale))
+
+
+def _rule(score, n_groups, top_groups, group_best, renormalise, scale):
+    # plain numbers before the cache: what a caller's tensors hold may change between two calls
+    if not (type(n_groups) is type(top_groups) is type(group_best) is int and type(renormalise) is bool
+            and type(scale) is float):
+        n_groups, top_groups, group_best = (operator.index(n) for n in (n_groups, top_groups, group_best))
+        renormalise, scale = bool(renormalise), float(scale)
+    return _rule_struct(score, n_groups, top_groups, group_best, renormalise, scale, None if scale else str(scale))
 
 
 def moe_route_groups(logits: torch.Tensor, k: int, bias: torch.Tensor | None = None, score: str = "sigmoid",
