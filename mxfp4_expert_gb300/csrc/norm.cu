@@ -99,25 +99,31 @@ __device__ __forceinline__ void store8(void* row, int c, const Eight& v) {
   }
 }
 
+__device__ __forceinline__ Eight constant(float v) {
+  const uint64_t p = pack2(v, v);
+  return {{p, p, p, p}};
+}
+__device__ __forceinline__ Eight product(const Eight& a, const Eight& b) {
+  return {{mul2(a.p[0], b.p[0]), mul2(a.p[1], b.p[1]), mul2(a.p[2], b.p[2]), mul2(a.p[3], b.p[3])}};
+}
+
 // 1 / sqrt(mean v^2 + eps) of the row. Where the squares' sum leaves what fp32
-// holds well, they are summed once more in units of the row's largest value.
+// holds well, v is brought to other units, in which the result then is: those of its
+// largest value where that is small (of subnormal numbers the result would else be
+// more than fp32 holds), 2^72 where it is large.
 template <int V>
-__device__ __forceinline__ float row_rstd(const Eight (&v)[V], float d, float eps, float* s) {
-  auto squares = [&](float f) {
+__device__ __forceinline__ float row_rstd(Eight (&v)[V], float d, float eps, float* s) {
+  auto squares = [&]() {
     uint64_t q[2] = {0, 0};            // two zeros each
-    const uint64_t f2 = pack2(f, f);
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint64_t z = f == 1.0f ? v[i].p[e] : mul2(v[i].p[e], f2);
-        q[e & 1] = fma2(z, z, q[e & 1]);
-      }
+      for (int e = 0; e < 4; ++e) q[e & 1] = fma2(v[i].p[e], v[i].p[e], q[e & 1]);
     float lo, hi;
     unpack2(add2(q[0], q[1]), lo, hi);
     return lo + hi;
   };
-  float q = cta_sum(squares(1.0f), s);
+  float q = cta_sum(squares(), s);
   if (q >= 1e-30f && q <= 1e37f) return rsqrtf(q / d + eps);
   float m = 0.0f;
 #pragma unroll
@@ -130,12 +136,14 @@ __device__ __forceinline__ float row_rstd(const Eight (&v)[V], float d, float ep
     }
   m = cta_max(m, s);
   if (!(m > 0.0f && m <= 3.4028235e38f) || q != q) return rsqrtf(q / d + eps);
-  const int ex = min(max(int(__float_as_uint(m) >> 23) - 127, -125), 126);
-  const float f = __uint_as_float(uint32_t(127 - ex) << 23);   // 2^-ex
+  const int ex = m < 1.0f ? max(int(__float_as_uint(m) >> 23) - 127, -125) : 72;
+  const float f = __uint_as_float(uint32_t(127 - ex) << 23), e2 = eps * f * f;   // 2^-ex
+  if (e2 > 3.4028235e38f) return rsqrtf(eps);
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = product(v[i], constant(f));
   __syncthreads();
-  q = cta_sum(squares(f), s);
-  const float e2 = eps * f * f;
-  return e2 <= 3.4028235e38f ? f * rsqrtf(q / d + e2) : rsqrtf(eps);
+  q = cta_sum(squares(), s);
+  return rsqrtf(q / d + e2);
 }
 
 // What n (of the half's output) and y are multiplied with, beside their norms:
@@ -144,13 +152,6 @@ template <int V>
 struct Weights {
   Eight a[V], h[V];
 };
-__device__ __forceinline__ Eight constant(float v) {
-  const uint64_t p = pack2(v, v);
-  return {{p, p, p, p}};
-}
-__device__ __forceinline__ Eight product(const Eight& a, const Eight& b) {
-  return {{mul2(a.p[0], b.p[0]), mul2(a.p[1], b.p[1]), mul2(a.p[2], b.p[2]), mul2(a.p[3], b.p[3])}};
-}
 __device__ __forceinline__ Eight plus(const Eight& a, const Eight& b) {
   return {{add2(a.p[0], b.p[0]), add2(a.p[1], b.p[1]), add2(a.p[2], b.p[2]), add2(a.p[3], b.p[3])}};
 }
@@ -279,7 +280,7 @@ int launch_v(const NormArgs& a, const DeviceInfo& di, cudaStream_t s) {
 // better (4,096 rows of 2,560: 320 threads with one 20.5 us, 160 with two 18.0), as many as registers hold where 512
 // threads need more. Three with the next row ahead against four without, 1,000 rows of 12,288: 28.8 to 47.8 us; a row
 // shared by a cluster of two CTAs 47.2. Rows beyond 16,384 channels leave registers (1,000 of 16,384: 42 us, 500 of
-// 32,768 with an fp32 stream 139).
+// 32,768 with an fp32 stream 121).
 int launch_block_norm(const NormArgs& a, const DeviceInfo& di, cudaStream_t s) {
   const int vecs = a.d / 8;
   if (vecs <= 256) return launch_v<1>(a, di, s);
