@@ -1,0 +1,68 @@
+"""Codes and scales of rotated keys are those of the exact values, also inside pages in use.
+
+The oracle turns in fp64 and rounds once; where position times frequency has more than 53 bits, the angle comes from whole
+numbers.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import attention as oa
+from oracle import block as ob
+from test_gpu_attention import _Cache, _bf16, _cu, _gen, _i32, _np, _tables
+
+pytestmark = pytest.mark.gpu
+BEYOND = 2.0 ** 128 - 2.0 ** 103      # from here on fp32 rounds to infinity
+
+
+@pytest.fixture(scope="module")
+def mx():
+    import mxfp4_expert_gb300 as mx
+    return mx
+
+
+def _freq(r):
+    return (10000.0 ** (-torch.arange(0, r, 2, dtype=torch.float64) / r)).float().cuda()
+
+
+def _append(mx, c, k, lens, start, table, f, interleaved, rope_start=None, turned=None):
+    """On the GPU and in the oracle's cache (turned: the exact keys where fp64 products do not give them); the status."""
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    at = start if rope_start is None else rope_start
+    mx.moe_kv_append_rope_fp8(c.gpu, k, k, _cu(lens), _i32(start), table, f, interleaved=interleaved, dev_status=status,
+                              rope_start=None if rope_start is None else _i32(rope_start))
+    if turned is None:
+        pos = np.concatenate([np.arange(n) + p for n, p in zip(lens, at)])
+        assert pos.max(initial=0) < 2 ** 29
+        with np.errstate(invalid="ignore"):
+            turned = ob.rotate(_np(k), pos, _np(f), interleaved)
+    turned = np.where(np.abs(turned) >= BEYOND, np.inf, turned)
+    tab, t0 = table.cpu().numpy(), 0
+    for b, n in enumerate(lens):
+        oa.append(c.codes["k"], c.scales["k"], turned[t0:t0 + n], start[b], tab[b])
+        t0 += n
+    return int(status)
+
+
+def _same(c):
+    assert np.array_equal(c.gpu.k_scales.cpu().numpy(), c.scales["k"])
+    got, want = c.gpu.k_codes.cpu().numpy(), c.codes["k"]
+    got, want = (np.where(x & 0x7F == 0x7F, 0x7F, x) for x in (got, want))       # NaN of either sign
+    same = (got == want) | ((got | want) & 0x7F == 0)
+    assert same.all(), (int((~same).sum()), np.argwhere(~same)[:4].tolist())
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("P,d,r,n_seq", [(16, 64, 32, 600), (64, 128, 128, 120), (128, 128, 64, 60), (32, 64, 64, 300)])
+def test_pages_in_use(mx, P, d, r, n_seq, interleaved):
+    """Tokens behind others of the same page: one and two a sequence, and more; scales that stay and that grow."""
+    g, H = _gen(P + d), 8
+    c, table, f = _Cache(mx, n_seq * 3, P, H, d), _tables(n_seq, 3), _freq(r)
+    at = [0] * n_seq
+    for step, spread in ((lambda b: 3 + b % (P // 2), 1.0), (lambda b: 1, 1.0), (lambda b: 1, 4.0), (lambda b: 2, 0.25),
+                         (lambda b: 5 + b % 9, 16.0), (lambda b: b % 3, 60.0), (lambda b: 1 + b % 7, 1.0)):
+        lens = [step(b) for b in range(n_seq)]
+        _append(mx, c, _bf16(g, sum(lens), H, d, spread=spread), lens, at, table, f, interleaved)
+        _same(c)
+        at = [a + n for a, n in zip(at, lens)]
