@@ -3,9 +3,11 @@
 //
 // Pair j of a head is turned by the angle p f_j, p the token's position. The
 // angle is taken in turns and in integers: F_j = f_j / 2 pi (without its whole
-// part) times 2^64, and p F_j modulo 2^64 is the angle's fraction of a turn, to
-// p 2^-64 whatever p is. Its top 32 bits give quadrant and remainder, cosine and
-// sine of the remainder are their Taylor series.
+// part) times 2^64, and p F_j modulo 2^64 is the angle's fraction of a turn. With F_j
+// rounded to a whole number that errs by p 2^-65, of which the top 32 bits do for fp32:
+// they give quadrant and remainder, cosine and sine of the remainder are their Taylor
+// series. Keys in doubt take what F_j leaves out along, so their angle errs by 2^-64 of
+// a turn.
 //
 // A CTA takes one page's new tokens and a few heads, of keys, values or queries: the
 // cosines and sines of all the tokens into shared memory once, then head after head,
@@ -120,10 +122,20 @@ __device__ __forceinline__ Block find_block_cta(const AppendArgs& a, int x, bool
   }
   return s_blk;
 }
-// Phase of a frequency per position, in 2^-64 turns: 1 / 2 pi in two parts.
-__device__ __forceinline__ uint64_t turns_of(float inv_freq) {
-  const double f = inv_freq, t = f * 0.15915494309189535, rest = fma(f, 0.15915494309189535, -t) + f * -9.839338337591243e-18;
-  return uint64_t((t - floor(t)) * 18446744073709551616.0) + uint64_t(int64_t(rest * 18446744073709551616.0));
+// Phase of a frequency per position, in 2^-64 turns: the nearest whole number, and
+// what that leaves out, which errs by |inv_freq| 2^-44 (1 / 2 pi in two parts).
+struct Phase {
+  uint64_t whole;
+  double rest;
+};
+__device__ __forceinline__ Phase phase_of(float inv_freq) {
+  const double f = fabsf(inv_freq), t = f * 0.15915494309189535;
+  const double low = fma(f, 0.15915494309189535, -t) + f * -9.839338337591243e-18;
+  const double up = (t - floor(t)) * 18446744073709551616.0;       // exact, and so is what its whole part leaves
+  const uint64_t first = uint64_t(up);
+  const double r = (up - double(first)) + low * 18446744073709551616.0, near = rint(r);
+  const uint64_t whole = first + uint64_t(int64_t(near));
+  return inv_freq < 0.0f ? Phase{0 - whole, near - r} : Phase{whole, r - near};
 }
 // Position of a page's first new token.
 __device__ __forceinline__ int64_t first_position(const RopeArgs& a, const Block& f) {
@@ -190,7 +202,8 @@ constexpr float kKeyError = 3.4e-7f;    // 1.4143 * 2^-22 = 3.372e-7
 // that leaves something out, so that a further rounding is right.
 __device__ __noinline__ float2 turn_exact(float a0, float b0, const float* freq, int64_t pos, float f) {
   const double a = a0, b = b0;
-  const int64_t at = int64_t(uint64_t(pos) * turns_of(__ldg(freq)));
+  const Phase step = phase_of(__ldg(freq));
+  const int64_t at = int64_t(uint64_t(pos) * step.whole + uint64_t(llrint(double(pos) * step.rest)));
   double sn = 0.0, cs = 1.0;
   if (at != 0) sincospi(double(at) * 1.0842021724855044e-19, &sn, &cs);      // half turns: 2^-63
   auto odd = [f](double v) {
@@ -333,7 +346,7 @@ __global__ void __launch_bounds__(kRopeThreads) append_rope_few_kernel(const Rop
   const int P = ap.c.page_size, D = ap.c.head_dim, H = ap.c.n_kv_heads, half = a.rot / 2;
   if (tid == 0) s_any = 0;
   clear_doubts(&s_doubts);             // find_block_cta has barriers
-  const uint64_t F = tid / half < kRopeThreads / half ? turns_of(__ldg(a.inv_freq + tid % half)) : 0;
+  const uint64_t F = tid / half < kRopeThreads / half ? phase_of(__ldg(a.inv_freq + tid % half)).whole : 0;
   bool bad = false;
   const Block f = find_block_cta(ap, int(blockIdx.x), &bad);
   if (bad && ap.status) atomicOr(ap.status, MOE_DEV_INDEX_OOB);
@@ -424,7 +437,7 @@ __global__ void __launch_bounds__(kRopeThreads, NU == 4 ? 2 : NU == 2 ? 3 : 4) a
   const int P = ap.c.page_size, D = ap.c.head_dim, H = ap.c.n_kv_heads;
   const int group = blockIdx.y, role = group < k_groups ? 0 : group < 2 * k_groups ? 1 : 2;
   const int rot = role == 1 ? 0 : a.rot, half = rot / 2;
-  const uint64_t F = rot && tid / half < kRopeThreads / half ? turns_of(__ldg(a.inv_freq + tid % half)) : 0;
+  const uint64_t F = rot && tid / half < kRopeThreads / half ? phase_of(__ldg(a.inv_freq + tid % half)).whole : 0;
   clear_doubts(&s_doubts);             // find_block_cta has barriers
   bool bad = false;
   const Block f = find_block_cta(ap, int(blockIdx.x), &bad);

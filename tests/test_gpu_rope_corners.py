@@ -1,8 +1,10 @@
-"""Codes and scales of rotated keys are those of the exact values, also inside pages in use.
+"""Codes and scales of rotated keys are those of the exact values, also inside pages in use, beside values that are not
+finite, at far positions and for frequencies of any sign.
 
 The oracle turns in fp64 and rounds once; where position times frequency has more than 53 bits, the angle comes from whole
 numbers.
 """
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -13,6 +15,7 @@ from oracle import block as ob
 from test_gpu_attention import _Cache, _bf16, _cu, _gen, _i32, _np, _tables
 
 pytestmark = pytest.mark.gpu
+TURN = Fraction(62831853071795864769252867665590057683943, 10 ** 40)
 BEYOND = 2.0 ** 128 - 2.0 ** 103      # from here on fp32 rounds to infinity
 
 
@@ -66,3 +69,47 @@ def test_pages_in_use(mx, P, d, r, n_seq, interleaved):
         _append(mx, c, _bf16(g, sum(lens), H, d, spread=spread), lens, at, table, f, interleaved)
         _same(c)
         at = [a + n for a, n in zip(at, lens)]
+
+
+def _exact(k, pos, f, interleaved):
+    """Keys turned by angles that whole numbers reduce."""
+    x, r = _np(k), 2 * len(f)
+    y = x.copy()
+    i, j = (np.arange(0, r, 2), np.arange(1, r, 2)) if interleaved else (np.arange(r // 2), np.arange(r // 2, r))
+    for t, p in enumerate(pos):
+        z = [Fraction(fj) * int(p) / TURN for fj in f.tolist()]
+        w = np.array([float((v - round(v)) * TURN) for v in z])
+        co, si = np.cos(w), np.sin(w)
+        y[t][:, i] = x[t][:, i] * co - x[t][:, j] * si
+        y[t][:, j] = x[t][:, j] * co + x[t][:, i] * si
+    return y
+
+
+# position, pair (of 32), channels: values that an angle wrong by 2^-31 of a radian puts on the other side of a border
+FAR = [(2138202708, 1, 36.0, -2.046875), (2144234721, 8, 59.0, -3.6875), (2146559153, 3, 39.75, 25.75), (2146559153, 3, 51.5, -79.5)]
+
+
+@pytest.mark.parametrize("p,j,a,b", FAR)
+@pytest.mark.parametrize("tokens", [1, 5])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_far_positions(mx, p, j, a, b, tokens, interleaved):
+    k = torch.zeros((tokens, 1, 128), dtype=torch.bfloat16, device="cuda")
+    k[0, 0, 127] = 448.0                     # the scale: one
+    k[0, 0, 2 * j if interleaved else j], k[0, 0, 2 * j + 1 if interleaved else j + 32] = a, b
+    c, f = _Cache(mx, 1, 16, 1, 128), _freq(64)
+    _append(mx, c, k, [tokens], [0], _i32([[0]]), f, interleaved, rope_start=[p], turned=_exact(k, p + np.arange(tokens), f, interleaved))
+    assert int(c.scales["k"][0, 0]) == 127
+    _same(c)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("lens,factor", [([4000], -1.0), ([1] * 2000, -1.0), ([1500], 1000.0), ([1500], -1234.5), ([700], 1e6), ([700], 1e-6)])
+def test_frequencies_of_any_size_and_sign(mx, lens, factor, interleaved):
+    g, P, n = _gen(7), 64, len(lens)
+    width = lens[0] // P + 1
+    c, table, f = _Cache(mx, n * width, P, 8, 128), _tables(n, width), _freq(128) * factor
+    bits = 2 ** 53 / 2 ** 24
+    assert bits == 2 ** 29
+    at = [2 ** 29 - lens[0] - 64 * b for b in range(n)]
+    _append(mx, c, _bf16(g, sum(lens), 8, 128), lens, [0] * n, table, f, interleaved, rope_start=at)
+    _same(c)
