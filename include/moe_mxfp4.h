@@ -532,7 +532,8 @@ int moe_kv_append_fp8(const moe_kv_cache* cache, const moe_rows* k, const moe_ro
  * The angle is reduced in whole numbers (keys: to 2^-63 of a turn, for inv_freq up
  * to 2^13 at any position), so positions may be as far as an int reaches, and codes
  * and scales are those of the exact turned keys (queries are turned in fp32).
- *   inv_freq_dev    fp32 [rot_dim / 2]
+ *   inv_freq_dev    fp32 [rot_dim / 2]; one that is not finite, or beyond 2^40, turns
+ *                   its pairs to NaN
  *   rot_dim         16, 32, .. head_dim (a multiple of 16)
  *   rope_start_dev  int32 [n_seq]: position that a sequence's first new token is
  *                   turned by, where it is not start (after an eviction the cache

@@ -137,18 +137,26 @@ __device__ __forceinline__ Phase phase_of(float inv_freq) {
   const uint64_t whole = first + uint64_t(int64_t(near));
   return inv_freq < 0.0f ? Phase{0 - whole, near - r} : Phase{whole, r - near};
 }
+// Beyond this, phase_of errs too much; such a frequency, and one that is not finite, turns to NaN.
+constexpr float kMostFreq = 1099511627776.0f;       // 2^40
+__device__ __forceinline__ bool phase_of_pair(const RopeArgs& a, int j, uint64_t* F) {
+  const float inv_freq = __ldg(a.inv_freq + j);
+  *F = phase_of(inv_freq).whole;
+  return fabsf(inv_freq) <= kMostFreq;
+}
 // Position of a page's first new token.
 __device__ __forceinline__ int64_t first_position(const RopeArgs& a, const Block& f) {
   return (int64_t)__ldg(a.rope_start + f.b) + ((int64_t)f.blk * a.ap.c.page_size + f.s0 - __ldg(a.ap.start + f.b));
 }
-// Cosines and sines of a page's new tokens, for the caller's barrier.
-__device__ __forceinline__ void fill_angles(const RopeArgs& a, const Block& f, uint64_t F, float2* cs) {
+// Cosines and sines of a page's new tokens, for the caller's barrier; NaN without an `angle`.
+__device__ __forceinline__ void fill_angles(const RopeArgs& a, const Block& f, uint64_t F, bool angle, float2* cs) {
   const int half = a.rot / 2, j = threadIdx.x % half, first = threadIdx.x / half, step = kRopeThreads / half;
   if (first >= step) return;
   const int64_t p0 = first_position(a, f);
   uint64_t at = uint64_t(p0 + first) * F;
   const uint64_t by = uint64_t(step) * F;
-  for (int t = first; t < f.s1 - f.s0; t += step, at += by) cs[t * half + j] = turn(uint32_t(at >> 32));
+  for (int t = first; t < f.s1 - f.s0; t += step, at += by)
+    cs[t * half + j] = angle ? turn(uint32_t(at >> 32)) : make_float2(__int_as_float(0x7FC00000), __int_as_float(0x7FC00000));
 }
 __device__ __forceinline__ void store_bf16(__nv_bfloat16* o, int c0, int c1, const float (&y)[16]) {
   *reinterpret_cast<uint4*>(o + c0) = make_uint4(bf16x2(y[0], y[1]), bf16x2(y[2], y[3]), bf16x2(y[4], y[5]), bf16x2(y[6], y[7]));
@@ -202,7 +210,9 @@ constexpr float kKeyError = 3.4e-7f;    // 1.4143 * 2^-22 = 3.372e-7
 // that leaves something out, so that a further rounding is right.
 __device__ __noinline__ float2 turn_exact(float a0, float b0, const float* freq, int64_t pos, float f) {
   const double a = a0, b = b0;
-  const Phase step = phase_of(__ldg(freq));
+  const float fr = __ldg(freq), nan = __int_as_float(0x7FC00000);
+  if (!(fabsf(fr) <= kMostFreq)) return make_float2(nan, nan);
+  const Phase step = phase_of(fr);
   const int64_t at = int64_t(uint64_t(pos) * step.whole + uint64_t(llrint(double(pos) * step.rest)));
   double sn = 0.0, cs = 1.0;
   if (at != 0) sincospi(double(at) * 1.0842021724855044e-19, &sn, &cs);      // half turns: 2^-63
@@ -346,14 +356,15 @@ __global__ void __launch_bounds__(kRopeThreads) append_rope_few_kernel(const Rop
   const int P = ap.c.page_size, D = ap.c.head_dim, H = ap.c.n_kv_heads, half = a.rot / 2;
   if (tid == 0) s_any = 0;
   clear_doubts(&s_doubts);             // find_block_cta has barriers
-  const uint64_t F = tid / half < kRopeThreads / half ? phase_of(__ldg(a.inv_freq + tid % half)).whole : 0;
+  uint64_t F = 0;
+  const bool angle = tid / half >= kRopeThreads / half || phase_of_pair(a, tid % half, &F);
   bool bad = false;
   const Block f = find_block_cta(ap, int(blockIdx.x), &bad);
   if (bad && ap.status) atomicOr(ap.status, MOE_DEV_INDEX_OOB);
   if (f.b < 0) return;
   const int tokens = f.s1 - f.s0, upr = D / 16, u = tid % upr, step = kRopeThreads / upr, all = 2 * H + (a.q ? a.n_heads : 0);
   int page = f.blk < ap.width ? __ldg(ap.table + (size_t)f.b * ap.width + f.blk) : -1;
-  fill_angles(a, f, F, s_cs);
+  fill_angles(a, f, F, angle, s_cs);
   __syncthreads();
   if (page < 0 || page >= ap.c.n_pages) {
     if (tid == 0 && ap.status) atomicOr(ap.status, MOE_DEV_INDEX_OOB);
@@ -437,7 +448,8 @@ __global__ void __launch_bounds__(kRopeThreads, NU == 4 ? 2 : NU == 2 ? 3 : 4) a
   const int P = ap.c.page_size, D = ap.c.head_dim, H = ap.c.n_kv_heads;
   const int group = blockIdx.y, role = group < k_groups ? 0 : group < 2 * k_groups ? 1 : 2;
   const int rot = role == 1 ? 0 : a.rot, half = rot / 2;
-  const uint64_t F = rot && tid / half < kRopeThreads / half ? phase_of(__ldg(a.inv_freq + tid % half)).whole : 0;
+  uint64_t F = 0;
+  const bool angle = !rot || tid / half >= kRopeThreads / half || phase_of_pair(a, tid % half, &F);
   clear_doubts(&s_doubts);             // find_block_cta has barriers
   bool bad = false;
   const Block f = find_block_cta(ap, int(blockIdx.x), &bad);
@@ -467,7 +479,7 @@ __global__ void __launch_bounds__(kRopeThreads, NU == 4 ? 2 : NU == 2 ? 3 : 4) a
   fetch(h);
   const int page = role < 2 && f.blk < ap.width ? __ldg(ap.table + (size_t)f.b * ap.width + f.blk) : -1;
   if (rot) {
-    fill_angles(a, f, F, s_cs);
+    fill_angles(a, f, F, angle, s_cs);
     __syncthreads();
   }
   if (role < 2 && (page < 0 || page >= ap.c.n_pages)) {

@@ -4,6 +4,7 @@ finite, at far positions and for frequencies of any sign.
 The oracle turns in fp64 and rounds once; where position times frequency has more than 53 bits, the angle comes from whole
 numbers.
 """
+import math
 from fractions import Fraction
 
 import numpy as np
@@ -113,3 +114,22 @@ def test_frequencies_of_any_size_and_sign(mx, lens, factor, interleaved):
     at = [2 ** 29 - lens[0] - 64 * b for b in range(n)]
     _append(mx, c, _bf16(g, sum(lens), 8, 128), lens, [0] * n, table, f, interleaved, rope_start=at)
     _same(c)
+
+
+@pytest.mark.parametrize("tokens", [1, 5])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan, 2.0 ** 41])
+def test_frequencies_that_are_no_angles(mx, bad, tokens, interleaved):
+    """They give NaN, for keys and queries, and nothing else does."""
+    f = _freq(32)
+    f[3] = bad
+    k, q = _bf16(_gen(8), tokens, 2, 64), _bf16(_gen(9), tokens, 4, 64)
+    c, status = _Cache(mx, 1, 16, 2, 64), torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = mx.moe_kv_append_rope_fp8(c.gpu, k, k, _cu([tokens]), _i32([0]), _i32([[0]]), f, q=q, interleaved=interleaved,
+                                    rope_start=_i32([1000]), dev_status=status)
+    assert int(status) == mx.DEV_NONFINITE_INPUT
+    pair = [6, 7] if interleaved else [3, 19]
+    want = torch.zeros(64, dtype=torch.bool, device="cuda")
+    want[pair] = True
+    assert torch.equal(torch.isnan(out), want.expand_as(out))
+    assert torch.equal(c.gpu.k_codes[0, :, :tokens] & 0x7F == 0x7F, want.expand(2, tokens, 64))
