@@ -205,18 +205,21 @@ __device__ __forceinline__ void store_codes(uint8_t* o, int c0, int c1, const fl
 // a scale, the pair is turned once more in fp64, so that codes and scales are those of
 // the exact values: one value in 2^16, and 10 % of the time for 12,345 tokens.
 constexpr float kKeyError = 3.4e-7f;    // 1.4143 * 2^-22 = 3.372e-7
+constexpr float kLargest = 3.4028235e38f;
 
 // A key's pair turned in fp64, times f; rounded to fp32 by truncation with the last bit set where
-// that leaves something out, so that a further rounding is right.
+// that leaves something out, so that a further rounding is right. What is not finite, or would not be
+// in fp32 before the product with f, is NaN.
 __device__ __noinline__ float2 turn_exact(float a0, float b0, const float* freq, int64_t pos, float f) {
   const double a = a0, b = b0;
   const float fr = __ldg(freq), nan = __int_as_float(0x7FC00000);
-  if (!(fabsf(fr) <= kMostFreq)) return make_float2(nan, nan);
+  if (!(fabsf(fr) <= kMostFreq && fabsf(a0) <= kLargest && fabsf(b0) <= kLargest)) return make_float2(nan, nan);
   const Phase step = phase_of(fr);
   const int64_t at = int64_t(uint64_t(pos) * step.whole + uint64_t(llrint(double(pos) * step.rest)));
   double sn = 0.0, cs = 1.0;
   if (at != 0) sincospi(double(at) * 1.0842021724855044e-19, &sn, &cs);      // half turns: 2^-63
-  auto odd = [f](double v) {
+  auto odd = [f, nan](double v) {
+    if (fabs(v) >= 3.4028235677973366e38) return nan;     // 2^128 - 2^103: half a step above fp32's largest
     v *= f;
     const uint32_t r = __float_as_uint(__double2float_rz(v));
     return __uint_as_float(double(__uint_as_float(r)) != v ? r | 1u : r);
@@ -249,12 +252,13 @@ __device__ __forceinline__ bool in_doubt(const float (&y)[16], float f, int kind
 }
 // Bounds of a largest magnitude: of turned channels on both sides of it, others are exact.
 __device__ __forceinline__ float largest_most(float top, int kind) {
-  return kind ? fminf(fmaf(top, 2.0f * kKeyError, top), 3.4028235e38f) : top;
+  return kind ? fminf(fmaf(top, 2.0f * kKeyError, top), kLargest) : top;
 }
 __device__ __forceinline__ float largest_least(float top, int kind) { return kind ? fmaf(top, -2.0f * kKeyError, top) : top; }
 
 // What a CTA turns exactly when it has stored everything else: groups of eight pairs (head, row of the page's new tokens,
-// group; beyond the list's room all groups), and heads whose scale is in doubt, of which nothing is stored yet.
+// group; beyond the list's room all groups), and heads of which nothing is stored yet: those whose scale is in doubt, and
+// those with values that are not finite or may be beyond fp32.
 constexpr int kDoubts = 256;
 struct Doubts {
   int n, any_head;
@@ -298,7 +302,6 @@ __device__ __noinline__ void settle_doubts(const RopeArgs& a, const Block& f, in
     if (in_heads(h)) continue;
     int c0, c1;
     const float2 v = exact(h, row, 8 * u + (i & 7), scales[h], &c0, &c1);
-    if (!(fabsf(v.x) <= 448.0f && fabsf(v.y) <= 448.0f)) continue;      // not finite in fp32: stored as NaN
     uint8_t* o = codes(h) + (f.s0 + row) * D;
     const uint32_t c = f32x2_to_e4m3x2(v.x, v.y);
     o[c0] = uint8_t(c);
@@ -314,15 +317,19 @@ __device__ __noinline__ void settle_doubts(const RopeArgs& a, const Block& f, in
       *c0 = 2 * pair;
       *c1 = 2 * pair + 1;
       const __nv_bfloat16* src = ap.k + (int64_t)(f.t0 + row) * ap.k_ts + h * ap.k_hs;
-      return make_float2(__bfloat162float(src[*c0]) * code_factor(byte), __bfloat162float(src[*c1]) * code_factor(byte));
+      auto times = [byte](float v) { return fabsf(v) <= kLargest ? v * code_factor(byte) : __int_as_float(0x7FC00000); };
+      return make_float2(times(__bfloat162float(src[*c0])), times(__bfloat162float(src[*c1])));
     };
     int c0, c1;
     float top = 0.0f;                 // truncated values, but what they leave out is in their last bit
+    bool odd = false;
     for (int i = threadIdx.x; i < tokens * (D / 2); i += kRopeThreads) {
       const float2 v = value(i, 127, &c0, &c1);
-      top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+      top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));        // of numbers
+      odd |= isnan(v.x) || isnan(v.y);
     }
-    __syncthreads();
+    odd = __syncthreads_or(odd);
+    if (threadIdx.x == 0 && odd && ap.status) atomicOr(ap.status, MOE_DEV_NONFINITE_INPUT);
     if (threadIdx.x == 0) s_top = 0;
     __syncthreads();
     atomicMax(&s_top, __float_as_uint(top));
@@ -401,8 +408,8 @@ __global__ void __launch_bounds__(kRopeThreads) append_rope_few_kernel(const Rop
     uint8_t* scale = (role ? ap.c.v_scales : ap.c.k_scales) + (size_t)page * H + h;
     const int had = f.s0 > 0 ? int(*scale) : 0;
     int byte = kv_scale_byte(most);
-    const bool turned = role == 0 && !nonfinite;
-    if (byte > had && turned && kv_scale_byte(least) != byte) {
+    const bool turned = role == 0;
+    if (turned && (nonfinite || most >= kLargest || (byte > had && kv_scale_byte(least) != byte))) {
       if (u == 0) {
         note_head(&s_doubts, h);
         s_grown[0][h] = 255;          // nothing below has to be done for it
@@ -525,8 +532,8 @@ __global__ void __launch_bounds__(kRopeThreads, NU == 4 ? 2 : NU == 2 ? 3 : 4) a
       nonfinite |= sbad[k][i] != 0;
     }
     int byte = kv_scale_byte(__uint_as_float(top));
-    const bool turned = rot && !nonfinite;
-    if (byte > had && turned && kv_scale_byte(__uint_as_float(least)) != byte) {      // the same for all threads
+    const bool turned = rot != 0;      // the branch is the same for all threads
+    if (turned && (nonfinite || __uint_as_float(top) >= kLargest || (byte > had && kv_scale_byte(__uint_as_float(least)) != byte))) {
       if (tid == 0) note_head(&s_doubts, h);
       continue;
     }

@@ -72,6 +72,56 @@ def test_pages_in_use(mx, P, d, r, n_seq, interleaved):
         at = [a + n for a, n in zip(at, lens)]
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("lens,start", [([3000, 700], [0, 21]), ([1] * 500, [37] * 500), ([2] * 300, [64] * 300)])
+def test_beside_values_that_are_not_finite(mx, lens, start, interleaved):
+    """One such channel in a fifth of the rows: its pair becomes NaN, the rest of the head keeps exact codes."""
+    g, H, d, P = _gen(len(lens)), 8, 128, 64
+    width = max(n + s for n, s in zip(lens, start)) // P + 1
+    c, table, f = _Cache(mx, len(lens) * width, P, H, d), _tables(len(lens), width), _freq(96)
+    k = _bf16(g, sum(start), H, d, spread=0.5)
+    _append(mx, c, k, start, [0] * len(lens), table, f, interleaved)
+    k = _bf16(g, sum(lens), H, d)
+    for i, bad in enumerate((math.inf, -math.inf, math.nan)):
+        rows = torch.arange(i, sum(lens), 15, device="cuda")
+        k[rows, rows % H, rows * 7 % d] = bad
+    assert _append(mx, c, k, lens, start, table, f, interleaved) == mx.DEV_NONFINITE_INPUT
+    _same(c)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("lens", [[400], [1] * 200])
+def test_keys_next_to_the_largest_number(mx, lens, interleaved):
+    """Pairs whose turned channels lie on both sides of what fp32 holds."""
+    g = _gen(5)
+    k = (torch.rand((sum(lens), 4, 64), generator=g, device="cuda") * 0.6 + 0.4) * 3.38e38
+    k = (k * (torch.randint(0, 2, k.shape, generator=g, device="cuda") * 2 - 1)).to(torch.bfloat16)
+    c, table = _Cache(mx, 16 * len(lens), 32, 4, 64), _tables(len(lens), 16)
+    assert _append(mx, c, k, lens, [0] * len(lens), table, _freq(64), interleaved, rope_start=[1000] * len(lens)) == mx.DEV_NONFINITE_INPUT
+    _same(c)
+
+
+@pytest.mark.parametrize("tokens", [1, 5])
+def test_a_key_within_an_fp32_step_of_infinity(mx, tokens):
+    """Angles that put the larger channel of a pair right below and right above it."""
+    a = float(torch.tensor(3.38e38).to(torch.bfloat16))
+    theta = np.float32(math.pi / 4 - math.acos(BEYOND / (a * math.sqrt(2.0))))     # a (cos t + sin t) = BEYOND
+    seen = set()
+    for step in range(-8, 9):
+        t = theta
+        for _ in range(abs(step)):
+            t = np.nextafter(t, np.float32(9.0 if step > 0 else 0.0))
+        k = torch.zeros((tokens, 2, 64), dtype=torch.bfloat16, device="cuda")
+        k[0, :, 0], k[0, :, 8] = a, a
+        c, f = _Cache(mx, 2, 16, 2, 64), torch.full((8,), float(t), device="cuda")
+        status = _append(mx, c, k, [tokens], [0], _i32([[0, 1]]), f, False, rope_start=[1])
+        big = a * (math.cos(float(t)) + math.sin(float(t)))
+        assert (status != 0) == (big >= BEYOND), step
+        _same(c)
+        seen.add(status)
+    assert len(seen) == 2
+
+
 def _exact(k, pos, f, interleaved):
     """Keys turned by angles that whole numbers reduce."""
     x, r = _np(k), 2 * len(f)
