@@ -530,7 +530,7 @@ int moe_kv_append_fp8(const moe_kv_cache* cache, const moe_rows* k, const moe_ro
  * 2j and 2j + 1) of a token at position p becomes
  *   (a cos t - b sin t, b cos t + a sin t),  t = p * inv_freq[j]
  * The angle is reduced in whole numbers (keys: to 2^-63 of a turn, for inv_freq up
- * to 2^13 at any position), so positions may be as far as an int reaches, and codes
+ * to 2^30 at any position), so positions may be as far as an int reaches, and codes
  * and scales are those of the exact turned keys (queries are turned in fp32).
  *   inv_freq_dev    fp32 [rot_dim / 2]; one that is not finite, or beyond 2^40, turns
  *                   its pairs to NaN

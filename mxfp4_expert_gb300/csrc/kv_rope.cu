@@ -3,19 +3,18 @@
 //
 // Pair j of a head is turned by the angle p f_j, p the token's position. The
 // angle is taken in turns and in integers: F_j = f_j / 2 pi (without its whole
-// part) times 2^64, and p F_j modulo 2^64 is the angle's fraction of a turn. With F_j
-// rounded to a whole number that errs by p 2^-65, of which the top 32 bits do for fp32:
-// they give quadrant and remainder, cosine and sine of the remainder are their Taylor
-// series. Keys in doubt take what F_j leaves out along, so their angle errs by 2^-64 of
-// a turn.
+// part) times 2^64, and p F_j modulo 2^64 is the angle's fraction of a turn. F_j is
+// cut, so that errs by p 2^-64; the top 32 bits, which do for fp32, give quadrant and
+// remainder, cosine and sine of the remainder are their Taylor series. Keys in doubt
+// take the angle from p f_j as a whole, to 2^-63 of a turn.
 //
 // A CTA takes one page's new tokens and a few heads, of keys, values or queries: the
 // cosines and sines of all the tokens into shared memory once, then head after head,
 // the next one's channels on their way meanwhile. A thread holds both halves of its
 // pairs. Of a key or value head the maximum, the page's scale and the codes as
 // append_kernel makes them, which has no rotation. Bound by HBM: 3 bytes a key or
-// value, 4 a query's channel; 12,345 tokens of 16 heads over 8 of 128 take 47 us (3.8
-// TB/s), a token of each of 64 sequences 6.5 to 9 (a key in doubt costs 2).
+// value, 4 a query's channel; 12,345 tokens of 16 heads over 8 of 128 take 45.5 us (3.9
+// TB/s), a token of each of 64 sequences 8.2 where a key is in doubt, which costs about 2.
 #include <algorithm>
 
 #include "attn.h"
@@ -122,26 +121,33 @@ __device__ __forceinline__ Block find_block_cta(const AppendArgs& a, int x, bool
   }
   return s_blk;
 }
-// Phase of a frequency per position, in 2^-64 turns: the nearest whole number, and
-// what that leaves out, which errs by |inv_freq| 2^-44 (1 / 2 pi in two parts).
-struct Phase {
-  uint64_t whole;
-  double rest;
+// n f / 2 pi for a frequency of magnitude f = mantissa 2^e, n times the mantissa below 2^57: its
+// fraction of a turn in units of 2^-64, cut. 1 / 2 pi to 2^-128, and shifts: what the last words
+// leave out is less than 2^-64 of a turn for f up to 2^30.
+struct Frequency {
+  uint32_t mantissa;
+  int e, negative;
 };
-__device__ __forceinline__ Phase phase_of(float inv_freq) {
-  const double f = fabsf(inv_freq), t = f * 0.15915494309189535;
-  const double low = fma(f, 0.15915494309189535, -t) + f * -9.839338337591243e-18;
-  const double up = (t - floor(t)) * 18446744073709551616.0;       // exact, and so is what its whole part leaves
-  const uint64_t first = uint64_t(up);
-  const double r = (up - double(first)) + low * 18446744073709551616.0, near = rint(r);
-  const uint64_t whole = first + uint64_t(int64_t(near));
-  return inv_freq < 0.0f ? Phase{0 - whole, near - r} : Phase{whole, r - near};
+__device__ __forceinline__ Frequency parts_of(float inv_freq) {
+  const uint32_t b = __float_as_uint(inv_freq) & 0x7FFFFFFFu, ex = b >> 23;
+  return {(b & 0x7FFFFFu) | (ex ? 0x800000u : 0u), min(int(ex ? ex : 1u) - 150, 63), inv_freq < 0.0f};
 }
-// Beyond this, phase_of errs too much; such a frequency, and one that is not finite, turns to NaN.
+__device__ __forceinline__ uint64_t turns_of(uint64_t n, const Frequency& f) {
+  constexpr uint64_t kHigh = 0x28BE60DB9391054Aull, kLow = 0x7F09D5F47D4D3770ull;
+  n *= f.mantissa;
+  const uint64_t w0 = n * kLow, c = __umul64hi(n, kLow), w1 = n * kHigh + c, w2 = __umul64hi(n, kHigh) + (w1 < c);
+  if (f.e >= 0) return f.e ? w1 << f.e | w0 >> (64 - f.e) : w1;
+  const int s = -f.e;
+  return s < 64 ? w1 >> s | w2 << (64 - s) : s < 128 ? w2 >> (s - 64) : 0;
+}
+// Beyond this a frequency is no angle per position; it turns to NaN, as does one that is not finite.
 constexpr float kMostFreq = 1099511627776.0f;       // 2^40
+// Phase per position of a pair, in 2^-64 turns; false for NaN.
 __device__ __forceinline__ bool phase_of_pair(const RopeArgs& a, int j, uint64_t* F) {
   const float inv_freq = __ldg(a.inv_freq + j);
-  *F = phase_of(inv_freq).whole;
+  const Frequency f = parts_of(inv_freq);
+  const uint64_t x = turns_of(1, f);
+  *F = f.negative ? 0 - x : x;
   return fabsf(inv_freq) <= kMostFreq;
 }
 // Position of a page's first new token.
@@ -210,12 +216,13 @@ constexpr float kLargest = 3.4028235e38f;
 // A key's pair turned in fp64, times f; rounded to fp32 by truncation with the last bit set where
 // that leaves something out, so that a further rounding is right. What is not finite, or would not be
 // in fp32 before the product with f, is NaN.
-__device__ __noinline__ float2 turn_exact(float a0, float b0, const float* freq, int64_t pos, float f) {
+__device__ __noinline__ float2 turn_exact(float a0, float b0, const float* inv_freq, int64_t pos, float f) {
   const double a = a0, b = b0;
-  const float fr = __ldg(freq), nan = __int_as_float(0x7FC00000);
+  const float fr = __ldg(inv_freq), nan = __int_as_float(0x7FC00000);
   if (!(fabsf(fr) <= kMostFreq && fabsf(a0) <= kLargest && fabsf(b0) <= kLargest)) return make_float2(nan, nan);
-  const Phase step = phase_of(fr);
-  const int64_t at = int64_t(uint64_t(pos) * step.whole + uint64_t(llrint(double(pos) * step.rest)));
+  const Frequency freq = parts_of(fr);
+  const uint64_t x = turns_of(uint64_t(pos < 0 ? -pos : pos), freq);
+  const int64_t at = int64_t((pos < 0) != (freq.negative != 0) ? 0 - x : x);
   double sn = 0.0, cs = 1.0;
   if (at != 0) sincospi(double(at) * 1.0842021724855044e-19, &sn, &cs);      // half turns: 2^-63
   auto odd = [f, nan](double v) {
