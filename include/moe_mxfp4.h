@@ -338,7 +338,8 @@ int moe_forward_w4a8(const moe_layer* L, const void* x_dev, int T, void* y_dev,
 /* The layer with routing by groups (moe_route_groups) of its router's logits in
  * place of moe_route_topk; bias_dev fp32 [E] or NULL. Paths as moe_forward's, but
  * the per-stage kernels for T <= 4 where a group's experts over the lanes that hold
- * them (32 over the power of two not below n_groups) are more than 16 each. Other
+ * them (32 over the power of two not below n_groups) are more than 16 each
+ * (moe_query_path knows of no rule and names the single launch there). Other
  * arguments, workspace and errors as moe_forward, and those of moe_route_groups for
  * the rule. */
 int moe_forward_groups(const moe_layer* L, const moe_group_rule* rule, const void* x_dev, int T, void* y_dev,

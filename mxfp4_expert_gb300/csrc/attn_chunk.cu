@@ -40,18 +40,19 @@
 // second product: in a tile that some row of the item does not see whole the
 // converters put 0 for NaN; the rows that see it get it back at the end.
 //
-// Measured: the last 4,096 tokens of 32,768, 32 heads over 4 of 128, in 1,650 us (1,250
-// TFLOP/s, 0.65 of the GEMM rate), 4 x 256 behind 65,536 each in 860. What bounds it
-// for heads of 128 is shared memory: a key tile costs 256 rows 2,066 wavefronts of
+// Measured: the last 4,096 tokens of 32,768, 32 heads over 4 of 128, in 1,640 us (1,257
+// TFLOP/s, 0.66 of the GEMM rate); chunks of four sequences, 1,024 tokens in all (68 to
+// 555 each) behind 40,413 to 65,536, in 854 (1,145 TFLOP/s). What bounds it for heads of
+// 128 is shared memory: a key tile costs 256 rows 2,066 wavefronts of
 // tensor operands (Q is read once for each half), about 1,120 of the converters and
 // 256 of the copies, of 3,950 cycles. Heads of 64 in short pages are bound by the
-// softmax threads (24 follow-ups of 62 tokens on average: 130 us, 4,600 cycles a tile),
+// softmax threads (24 follow-ups of 63 tokens on average: 130 us, 4,600 cycles a tile),
 // items of few rows by the converters (2,200 cycles a tile), a single short call by its
-// chain (37 tokens behind 5,000: 33 us).
+// chain (37 tokens behind 5,000: 32 us).
 // - Instructions have to be few as well: with long waits in line, the converters' loop
 //   unrolled and every mask in its own pass, the same took 1,122 instead of 888 us.
 // - Scores of 128 keys in one product read Q once, but a tile's chain of products then
-//   stands between two softmax passes: 1,098 instead of 868 us for 4 x 256.
+//   stands between two softmax passes: 1,098 instead of 868 us for the four sequences.
 // - Moving registers between the roles (setmaxnreg) 905 instead of 870, the next half's
 //   scores fetched early 954 to 983 instead of 888, no turns between the MMA warps 880.
 #include <math.h>

@@ -13,8 +13,8 @@
 // the next one's channels on their way meanwhile. A thread holds both halves of its
 // pairs. Of a key or value head the maximum, the page's scale and the codes as
 // append_kernel makes them, which has no rotation. Bound by HBM: 3 bytes a key or
-// value, 4 a query's channel; 12,345 tokens of 16 heads over 8 of 128 take 45.5 us (3.9
-// TB/s), a token of each of 64 sequences 8.2 where a key is in doubt, which costs about 2.
+// value, 4 a query's channel; 12,345 tokens of 16 heads over 8 of 128 take 46 us (3.8
+// TB/s), a token of each of 64 sequences 8.8 where a key is in doubt, which costs about 2.
 #include <algorithm>
 
 #include "attn.h"
@@ -588,7 +588,9 @@ int launch_kv_append_rope(const RopeArgs& a, const DeviceInfo& di, cudaStream_t 
     kernel<<<grid, kRopeThreads, smem, s>>>(a, heads, k_groups);
     return launch_status();
   };
-  // a token or two a sequence: a CTA for all their heads
+  // A token or two a sequence: a CTA for all their heads. The host knows the mean alone: 64 sequences of two tokens take
+  // 9.9 us here, but 64 single tokens beside a chunk of 64 (128 tokens of 65 sequences) take 77, since one CTA has the
+  // chunk's page; with 67 in the chunk the other kernel has them all, 15.0.
   if (a.ap.total <= 2 * (int64_t)a.ap.n_seq) {
     const int st = room(append_rope_few_kernel);
     if (st != MOE_OK) return st;

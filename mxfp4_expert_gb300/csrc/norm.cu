@@ -9,11 +9,13 @@
 // are on their way meanwhile, and the weights stay for all rows. h comes from y
 // before its rounding.
 //
-// Bound by HBM, 8 bytes an element with a bf16 stream: 4,096 rows of 2,560 in 18.0 us
-// (4.7 TB/s; a fill alone writes 4.1), 1,001 of 7,168 with an fp32 stream and a gate
-// per token in 20.8 (4.8 TB/s). A ring of bulk copies in place of the reads into
-// registers took 21.2 to 23.8 and 21.9 us. One row of 2,560: 3.4 us, the launch and a
-// chain of a read and two sums over the CTA.
+// Bound by the reads in flight: 4,096 rows of 2,560 (8 bytes an element with a bf16
+// stream) take 17.8 us, 0.69 of the copy rate, and three CTAs of 160 threads at 128
+// registers are all an SM holds, some 30 KB on their way; DRAM carries 2.6 TB/s where the
+// writes stay in L2, and the time is the same where they do not. 1,001 of 7,168 with an
+// fp32 stream and a gate per token: 20.6 us (0.72). A ring of bulk copies in place of the
+// reads into registers took 21.2 to 23.8 and 21.9 us. One row of 2,560: 3.4 us, the
+// launch and a chain of a read and two sums over the CTA.
 #include "block.h"
 #include "common.cuh"
 #include "f32x2.cuh"
@@ -277,10 +279,11 @@ int launch_v(const NormArgs& a, const DeviceInfo& di, cudaStream_t s) {
 }  // namespace
 
 // Vectors a thread. One up to 256 threads; with more of them a row's sums cost more than its channels, and two are
-// better (4,096 rows of 2,560: 320 threads with one 20.5 us, 160 with two 18.0), as many as registers hold where 512
-// threads need more. Three with the next row ahead against four without, 1,000 rows of 12,288: 28.8 to 47.8 us; a row
-// shared by a cluster of two CTAs 47.2. Rows beyond 16,384 channels leave registers (1,000 of 16,384: 42 us, 500 of
-// 32,768 with an fp32 stream 121).
+// better (4,096 rows of 2,560: 320 threads with one 20.5 us, 160 with two 17.8), more where 512 threads need them. Of
+// those, parts leave registers for local memory: the weights of three vectors (128 and 232 bytes a thread with a bf16 and
+// an fp32 stream), some of four (96, 128), most of eight (880, 928). Three with the next row ahead against four without,
+// 1,000 rows of 12,288: 29 to 47.8 us; a row shared by a cluster of two CTAs 47.2. 1,000 rows of 16,384: 42 us, 500 of
+// 32,768 with an fp32 stream 121.
 int launch_block_norm(const NormArgs& a, const DeviceInfo& di, cudaStream_t s) {
   const int vecs = a.d / 8;
   if (vecs <= 256) return launch_v<1>(a, di, s);

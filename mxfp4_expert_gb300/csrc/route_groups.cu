@@ -1,7 +1,7 @@
 // Routing by groups, a warp per token (route_groups.cuh has the mathematics).
 //
 // Bound by instructions: 4,096 tokens over 512 experts in 8 groups, the 8 best of 4,
-// in 17.8 us (0.47 TB/s of logits; pairs for every key 49), 16,384 over 160 in 19.8. A
+// in 17.8 us (0.47 TB/s of logits; pairs for every key 49), 16,384 over 160 in 19.9. A
 // batch of 64 tokens takes 7.5, one token's chain of k + groups reductions.
 #include "route_groups.cuh"
 
